@@ -88,14 +88,14 @@ def draw(rng):
                     window=_log(rng, 1, 4096) - 1, sinks=rng.choice([0, 1, 4, 16, rng.randrange(129)]),
                     train=rng.random() < 0.5)
     elif op in ("decode", "decode4"):
-        capacity = _log(rng, 16, 32768)
+        capacity = -(-_log(rng, 16, 32768) // 8) * 8
         hi = rng.randint(1, capacity)
         case.update(batch=rng.choice([1, 2, 5, 16, 32]), capacity=capacity, len_lo=rng.randint(1, hi), len_hi=hi,
                     heads=heads, window=_log(rng, 1, 16384) - 1, sinks=rng.choice([0, 1, 4, 16, rng.randrange(129)]))
     else:
         tokens = _log(rng, 1, 8192)
         first = rng.randrange(4096)
-        case.update(batch=rng.choice([1, 2, 5]), tokens=tokens, capacity=first + tokens + rng.randrange(64), first=first)
+        case.update(batch=rng.choice([1, 2, 5]), tokens=tokens, capacity=-(-(first + tokens) // 8) * 8 + 8 * rng.randrange(8), first=first)
     return case
 
 
