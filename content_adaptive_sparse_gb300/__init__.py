@@ -6,7 +6,8 @@ work of the hot path runs in the library's CUDA kernels. There is no CPU fallbac
 if the library is missing or the device is not an sm_103 GPU, calls raise.
 
 Names follow the C ABI: ``sa_build_mask``, ``sa_attn_fwd``, ``sa_attn_fwd_heads``,
-``sa_offset_attn_fwd``, ``sa_offset_attn_fwd_list``, ``sa_fib_offsets``, ``sa_pow2_offsets``, ``sa_layer_alpha``, ``sa_block_ratios``, ``sa_mask_nnz_bound``, ``sa_device_status``.
+``sa_offset_attn_fwd``, ``sa_offset_attn_fwd_list``, ``sa_fib_offsets``, ``sa_pow2_offsets``, ``sa_layer_alpha``, ``sa_block_ratios``, ``sa_mask_nnz_bound``, ``sa_device_status``;
+the streaming-attention calls (norm and rotation, sink window, decoding, 4-bit cache) are in ``streaming.py``.
 """
 from __future__ import annotations
 
@@ -15,7 +16,9 @@ import os
 
 import numpy as np
 
+from . import streaming as _streaming
 from .build import LIB, build as build_library
+from .streaming import *  # noqa: F401,F403
 
 MASK_TOPK, MASK_BIGBIRD, MASK_FULL, MASK_LITERAL_MEAN = 0, 1, 2, 3
 LITERAL_LOCAL, LITERAL_PAIRS = 1, 2          # parts of the LITERAL_MEAN mask (0 = both)
@@ -94,6 +97,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                  "sa_offset_attn_interp_fwd", "sa_fib_offsets", "sa_pow2_offsets", "sa_layer_alpha", "sa_block_ratios",
                  "sa_device_status", "sa_selftest_bounded_wait", "sa_build_mask_from_bytes"):
         getattr(lib, name).restype = ctypes.c_int
+    _streaming.declare(lib)
     _lib = lib
     return lib
 
@@ -435,4 +439,6 @@ __all__ = [
     "build_mask", "attn_fwd", "attn_fwd_heads", "attn_bwd", "attn_bwd_heads", "offset_attn_fwd", "offset_attn_interp_fwd",
     # constants
     "MASK_TOPK", "MASK_BIGBIRD", "MASK_FULL", "MASK_LITERAL_MEAN", "LITERAL_LOCAL", "LITERAL_PAIRS",
+    # streaming attention (norm and rotation, sink-window graph, single tokens over a cache)
+    *_streaming.NAMES,
 ]

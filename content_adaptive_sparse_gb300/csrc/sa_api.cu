@@ -800,6 +800,342 @@ int sa_build_mask_from_bytes(const sa_mask_params* params, const uint8_t* h_byte
   return sa::launch_build_mask(*params, d_ratio, d_row_ptr, d_col_idx, s);
 }
 
+}  // extern "C"
+
+namespace {
+
+void copy3(int64_t (&dst)[3], const int64_t src[3]) {
+  for (int i = 0; i < 3; ++i) dst[i] = src[i];
+}
+
+bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
+
+bool scale_ok(float s) { return s > 0.f && s <= 3.4028234e38f; }
+
+// Arguments that both directions of the norm-and-rotation share; fills `a`.
+int norm_rope_args(const void* q, const void* k, const int64_t qs[3], const int64_t ks[3], int32_t batch,
+                   int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, const float* wq,
+                   const float* wk, float eps, const double* h_inv_freq, int32_t rotary_dim, int32_t interleaved,
+                   const int32_t* positions, void* q_out, void* k_out, const int64_t qos[3], const int64_t kos[3],
+                   sa::NormRopeArgs& a) {
+  if (!q || !k || !qs || !ks || !q_out || !k_out || !qos || !kos) return SA_ERR_INVALID_ARG;
+  if (batch <= 0 || n_tokens <= 0 || heads <= 0 || kv_heads <= 0) return SA_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || (interleaved != 0 && interleaved != 1)) return SA_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > head_dim || (rotary_dim > 0 && !h_inv_freq)) return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || rotary_dim % 16 != 0) return SA_ERR_UNSUPPORTED;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!(h_inv_freq[i] >= 0.0 && h_inv_freq[i] < 6.28)) return SA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return SA_ERR_UNSUPPORTED;
+  if (!strides_ok(qs) || !strides_ok(ks) || !strides_ok(qos) || !strides_ok(kos)) return SA_ERR_UNSUPPORTED;
+  if ((int64_t)heads + kv_heads > 65536) return SA_ERR_UNSUPPORTED;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  copy3(a.q_strides, qs);
+  copy3(a.k_strides, ks);
+  copy3(a.q_out_strides, qos);
+  copy3(a.k_out_strides, kos);
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
+  a.q_weight = wq;
+  a.k_weight = wk;
+  a.eps = eps;
+  a.h_inv_freq = h_inv_freq;
+  a.positions = positions;
+  return SA_OK;
+}
+
+// Graph and size limits of the sink-window calls. The window is cut to the sequence.
+int check_sink(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t& window,
+               int32_t sinks) {
+  if (batch <= 0 || n_tokens <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0) return SA_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || sinks > sa::kMaxSinks || n_tokens > (1 << 24)) return SA_ERR_UNSUPPORTED;
+  // work items are counted in 32 bits, and so are the CTAs of the backward's first launch (one per
+  // 256 threads of head_dim / 8 per row)
+  const int64_t tiles = ((int64_t)n_tokens + 127) / 128;
+  if ((int64_t)batch * heads > (1 << 24) || (int64_t)batch * heads * tiles > (1 << 27)) return SA_ERR_UNSUPPORTED;
+  if (window > n_tokens - 1) window = n_tokens - 1;
+  return SA_OK;
+}
+
+int decode_args(const void* q, const void* k, const void* v, const int64_t qs[3], const int64_t os[3], int32_t batch,
+                int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim, const int32_t* d_lengths,
+                int32_t window, int32_t sinks, float softmax_scale, void* o, float* lse, sa::SinkDecodeArgs& a) {
+  if (!q || !k || !v || !qs || !os || !d_lengths || !o || !lse) return SA_ERR_INVALID_ARG;
+  if (batch <= 0 || capacity <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0) return SA_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0 || !scale_ok(softmax_scale)) return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || sinks > sa::kMaxSinks || capacity > (1 << 30)) return SA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SA_ERR_UNSUPPORTED;
+  if (!strides_ok(qs) || !strides_ok(os)) return SA_ERR_UNSUPPORTED;
+  const int64_t head_groups = (int64_t)kv_heads * ((heads / kv_heads + 15) / 16);
+  if (batch > 65535 || head_groups > 65535) return SA_ERR_UNSUPPORTED;    // grid
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  a.lengths = d_lengths;
+  copy3(a.q_strides, qs);
+  copy3(a.o_strides, os);
+  a.batch = batch;
+  a.capacity = capacity;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.window = window < capacity ? window : capacity - 1;
+  a.sinks = sinks;
+  a.softmax_scale = softmax_scale;
+  return SA_OK;
+}
+
+int cache4_args(const void* k, const void* v, const int64_t kst[3], const int64_t vst[3], int32_t batch,
+                int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity, const int32_t* d_start,
+                const void* kc, const void* ks, const void* vc, const void* vs, sa::Cache4Args& a) {
+  if (!k || !v || !kst || !vst || !kc || !ks || !vc || !vs) return SA_ERR_INVALID_ARG;
+  if (batch <= 0 || n_tokens <= 0 || kv_heads <= 0 || capacity <= 0) return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || capacity % 8 != 0 || capacity > (1 << 30)) return SA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs))
+    return SA_ERR_UNSUPPORTED;
+  if (!strides_ok(kst) || !strides_ok(vst)) return SA_ERR_UNSUPPORTED;
+  // one thread per 8 elements, 256 per CTA of a 31-bit grid
+  if ((double)batch * n_tokens * kv_heads * (head_dim / 8) > 256.0 * 2147483647.0) return SA_ERR_UNSUPPORTED;
+  memset(&a, 0, sizeof(a));
+  a.k = const_cast<void*>(k);
+  a.v = const_cast<void*>(v);
+  a.k_codes = static_cast<uint8_t*>(const_cast<void*>(kc));
+  a.k_scales = const_cast<void*>(ks);
+  a.v_codes = static_cast<uint8_t*>(const_cast<void*>(vc));
+  a.v_scales = const_cast<void*>(vs);
+  a.start = d_start;
+  copy3(a.k_strides, kst);
+  copy3(a.v_strides, vst);
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.capacity = capacity;
+  return SA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sa_qk_norm_rope_fwd(const void* q, const void* k, const int64_t q_strides[3], const int64_t k_strides[3],
+                        int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                        const float* d_q_weight, const float* d_k_weight, float eps, const double* h_inv_freq,
+                        int32_t rotary_dim, int32_t interleaved, const int32_t* d_positions, void* q_out, void* k_out,
+                        const int64_t q_out_strides[3], const int64_t k_out_strides[3], void* stream) {
+  sa::NormRopeArgs a;
+  const int st = norm_rope_args(q, k, q_strides, k_strides, batch, n_tokens, heads, kv_heads, head_dim, d_q_weight,
+                                d_k_weight, eps, h_inv_freq, rotary_dim, interleaved, d_positions, q_out, k_out,
+                                q_out_strides, k_out_strides, a);
+  if (st != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  return sa::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_qk_norm_rope_bwd_workspace_size(int32_t head_dim, size_t* h_bytes) {
+  if (!h_bytes) return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim)) return SA_ERR_UNSUPPORTED;
+  *h_bytes = (size_t)sa::kNormRopeMaxCtas * 2 * head_dim * sizeof(float);
+  return SA_OK;
+}
+
+int sa_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out, const void* d_k_out,
+                        const int64_t q_strides[3], const int64_t k_strides[3], const int64_t d_q_out_strides[3],
+                        const int64_t d_k_out_strides[3], int32_t batch, int32_t n_tokens, int32_t heads,
+                        int32_t kv_heads, int32_t head_dim, const float* d_q_weight, const float* d_k_weight, float eps,
+                        const double* h_inv_freq, int32_t rotary_dim, int32_t interleaved, const int32_t* d_positions,
+                        void* dq, void* dk, const int64_t dq_strides[3], const int64_t dk_strides[3],
+                        float* d_dq_weight, float* d_dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  sa::NormRopeArgs a;
+  const int st = norm_rope_args(q, k, q_strides, k_strides, batch, n_tokens, heads, kv_heads, head_dim, d_q_weight,
+                                d_k_weight, eps, h_inv_freq, rotary_dim, interleaved, d_positions, dq, dk, dq_strides,
+                                dk_strides, a);
+  if (st != SA_OK) return st;
+  if (!d_q_out || !d_k_out || !d_q_out_strides || !d_k_out_strides || !workspace) return SA_ERR_INVALID_ARG;
+  if (!aligned16(d_q_out) || !aligned16(d_k_out) || !strides_ok(d_q_out_strides) || !strides_ok(d_k_out_strides))
+    return SA_ERR_UNSUPPORTED;
+  size_t need = 0;
+  sa_qk_norm_rope_bwd_workspace_size(head_dim, &need);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return SA_ERR_CAPACITY;
+  if (!device_ok()) return SA_ERR_CUDA;
+  a.backward = true;
+  a.d_q_out = d_q_out;
+  a.d_k_out = d_k_out;
+  copy3(a.dy_q_strides, d_q_out_strides);
+  copy3(a.dy_k_strides, d_k_out_strides);
+  a.dq_weight = d_dq_weight;
+  a.dk_weight = d_dk_weight;
+  a.workspace = workspace;
+  return sa::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_sink_attn_fwd(const void* q, const void* k, const void* v, const int64_t q_strides[3],
+                     const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3], int32_t batch,
+                     int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t window,
+                     int32_t sinks, float softmax_scale, void* o, float* lse, void* stream) {
+  int st = check_attn_common(q, k, v, q_strides, k_strides, o_strides, batch, n_tokens, heads, kv_heads, o, lse);
+  if (st != SA_OK) return st;
+  if (!v_strides) return SA_ERR_INVALID_ARG;
+  if (!strides_ok(v_strides)) return SA_ERR_UNSUPPORTED;
+  if (!scale_ok(softmax_scale)) return SA_ERR_INVALID_ARG;
+  if ((st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks)) != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  sa::SinkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  copy3(a.q_strides, q_strides);
+  copy3(a.k_strides, k_strides);
+  copy3(a.v_strides, v_strides);
+  copy3(a.o_strides, o_strides);
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.window = window;
+  a.sinks = sinks;
+  a.softmax_scale = softmax_scale;
+  return sa::launch_sink_attn_fwd(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_sink_attn_bwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                    int32_t window, int32_t sinks, size_t* h_bytes) {
+  if (!h_bytes) return SA_ERR_INVALID_ARG;
+  const int st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks);
+  if (st != SA_OK) return st;
+  *h_bytes = sa::sink_bwd_workspace_layout(batch, n_tokens, heads, kv_heads, head_dim, window, sinks).bytes;
+  return SA_OK;
+}
+
+int sa_sink_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* d_o, const float* lse,
+                     const int64_t q_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
+                     const int64_t o_strides[3], const int64_t d_o_strides[3], int32_t batch, int32_t n_tokens,
+                     int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t window, int32_t sinks,
+                     float softmax_scale, void* dq, void* dk, void* dv, const int64_t dq_strides[3],
+                     const int64_t dk_strides[3], const int64_t dv_strides[3], void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  int st = check_attn_common(q, k, v, q_strides, k_strides, o_strides, batch, n_tokens, heads, kv_heads,
+                             const_cast<void*>(o), const_cast<float*>(lse));
+  if (st != SA_OK) return st;
+  if (!v_strides || !d_o || !d_o_strides || !dq || !dk || !dv || !workspace) return SA_ERR_INVALID_ARG;
+  if (!dq_strides || !dk_strides || !dv_strides) return SA_ERR_INVALID_ARG;
+  if (!scale_ok(softmax_scale)) return SA_ERR_INVALID_ARG;
+  if (!aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv)) return SA_ERR_UNSUPPORTED;
+  if (!strides_ok(v_strides) || !strides_ok(d_o_strides) || !strides_ok(dq_strides) || !strides_ok(dk_strides) ||
+      !strides_ok(dv_strides))
+    return SA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
+  if ((st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks)) != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  sa::SinkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = const_cast<void*>(o);
+  a.lse = const_cast<float*>(lse);
+  a.d_o = d_o;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  copy3(a.q_strides, q_strides);
+  copy3(a.k_strides, k_strides);
+  copy3(a.v_strides, v_strides);
+  copy3(a.o_strides, o_strides);
+  copy3(a.do_strides, d_o_strides);
+  copy3(a.dq_strides, dq_strides);
+  copy3(a.dk_strides, dk_strides);
+  copy3(a.dv_strides, dv_strides);
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.window = window;
+  a.sinks = sinks;
+  a.softmax_scale = softmax_scale;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  return sa::launch_sink_attn_bwd(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_sink_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int64_t q_strides[3],
+                        const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3],
+                        int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                        const int32_t* d_lengths, int32_t window, int32_t sinks, float softmax_scale, void* o,
+                        float* lse, void* stream) {
+  sa::SinkDecodeArgs a;
+  const int st = decode_args(q, k_cache, v_cache, q_strides, o_strides, batch, capacity, heads, kv_heads, head_dim,
+                             d_lengths, window, sinks, softmax_scale, o, lse, a);
+  if (st != SA_OK) return st;
+  if (!k_strides || !v_strides) return SA_ERR_INVALID_ARG;
+  if (!strides_ok(k_strides) || !strides_ok(v_strides)) return SA_ERR_UNSUPPORTED;
+  if (!device_ok()) return SA_ERR_CUDA;
+  copy3(a.k_strides, k_strides);
+  copy3(a.v_strides, v_strides);
+  return sa::launch_sink_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_sink_attn_decode_cache4(const void* q, const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes,
+                               const void* v_scales, const int64_t q_strides[3], const int64_t o_strides[3],
+                               int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                               const int32_t* d_lengths, int32_t window, int32_t sinks, float softmax_scale, void* o,
+                               float* lse, void* stream) {
+  sa::SinkDecodeArgs a;
+  const int st = decode_args(q, k_codes, v_codes, q_strides, o_strides, batch, capacity, heads, kv_heads, head_dim,
+                             d_lengths, window, sinks, softmax_scale, o, lse, a);
+  if (st != SA_OK) return st;
+  if (!k_scales || !v_scales) return SA_ERR_INVALID_ARG;
+  if (!aligned16(k_scales) || !aligned16(v_scales) || capacity % 8 != 0) return SA_ERR_UNSUPPORTED;
+  if (!device_ok()) return SA_ERR_CUDA;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.cache4 = true;
+  return sa::launch_sink_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_cache4_append(const void* k, const void* v, const int64_t k_strides[3], const int64_t v_strides[3],
+                     int32_t batch, int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity,
+                     const int32_t* d_start, uint8_t* k_codes, void* k_scales, uint8_t* v_codes, void* v_scales,
+                     void* stream) {
+  sa::Cache4Args a;
+  const int st = cache4_args(k, v, k_strides, v_strides, batch, n_tokens, kv_heads, head_dim, capacity, d_start,
+                             k_codes, k_scales, v_codes, v_scales, a);
+  if (st != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  return sa::launch_cache4(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_cache4_read(const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes, const void* v_scales,
+                   int32_t batch, int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity,
+                   const int32_t* d_start, void* k, void* v, const int64_t k_strides[3], const int64_t v_strides[3],
+                   void* stream) {
+  sa::Cache4Args a;
+  const int st = cache4_args(k, v, k_strides, v_strides, batch, n_tokens, kv_heads, head_dim, capacity, d_start,
+                             k_codes, k_scales, v_codes, v_scales, a);
+  if (st != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  a.read = true;
+  return sa::launch_cache4(a, static_cast<cudaStream_t>(stream));
+}
+
 int sa_selftest_bounded_wait(void* stream) {
   if (!device_ok()) return SA_ERR_CUDA;
   bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
@@ -813,7 +1149,9 @@ int sa_device_status(void* stream) {
   cudaMemcpyFromSymbolAsync(&self, g_selftest_err, sizeof(self), 0, cudaMemcpyDeviceToHost, s);
   cudaMemcpyToSymbolAsync(g_selftest_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
   const unsigned int e = sa::attn_read_and_clear_error(s) | sa::offset_read_and_clear_error(s) |
-                         sa::interp_read_and_clear_error(s) | sa::bwd_read_and_clear_error(s) | self;
+                         sa::interp_read_and_clear_error(s) | sa::bwd_read_and_clear_error(s) |
+                         sa::sink_fwd_read_and_clear_error(s) | sa::sink_bwd_read_and_clear_error(s) |
+                         sa::decode_read_and_clear_error(s) | sa::cache4_read_and_clear_error(s) | self;
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   if (e & sa::kErrTimeout) return SA_ERR_TIMEOUT;
   if (e & sa::kErrBadIndex) return SA_ERR_DEVICE;

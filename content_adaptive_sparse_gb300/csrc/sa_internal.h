@@ -135,4 +135,92 @@ constexpr size_t kBwdStaticScratchBytes = size_t(16) << 20;
 int bwd_static_scratch(void** ptr);
 unsigned int bwd_read_and_clear_error(cudaStream_t stream);
 
+// norm_rope.cu
+constexpr int kNormRopeMaxCtas = 2048;   // CTAs of a launch at most (partial weight gradients)
+struct NormRopeArgs {
+  bool backward;
+  const void* q;
+  const void* k;
+  const void* d_q_out;                   // backward
+  const void* d_k_out;
+  void* q_out;                           // forward: outputs; backward: dq, dk
+  void* k_out;
+  int64_t q_strides[3], k_strides[3], dy_q_strides[3], dy_k_strides[3], q_out_strides[3], k_out_strides[3];
+  int32_t batch, n_tokens, heads, kv_heads, head_dim, rotary_dim, interleaved;
+  const float* q_weight;                 // [head_dim] or null
+  const float* k_weight;
+  float eps;
+  const double* h_inv_freq;              // host, [rotary_dim / 2]
+  const int32_t* positions;              // [batch][n_tokens] or null
+  float* dq_weight;                      // backward, [head_dim] or null
+  float* dk_weight;
+  void* workspace;                       // backward: [kNormRopeMaxCtas][2][head_dim] floats
+};
+int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+// sink_attn.cu, sink_bwd.cu
+constexpr int kMaxSinks = 128;           // one 128-row key tile
+struct SinkArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;                               // written by the forward, read by the backward
+  float* lse;
+  const void* d_o;
+  void* dq;
+  void* dk;
+  void* dv;
+  int64_t q_strides[3], k_strides[3], v_strides[3], o_strides[3], do_strides[3];
+  int64_t dq_strides[3], dk_strides[3], dv_strides[3];
+  int32_t batch, n_tokens, heads, kv_heads, head_dim, window, sinks;
+  float softmax_scale;
+  void* workspace;
+  size_t workspace_bytes;
+};
+int launch_sink_attn_fwd(const SinkArgs& a, cudaStream_t stream);
+unsigned int sink_fwd_read_and_clear_error(cudaStream_t stream);
+// Workspace of the backward: -LSE log2(e) and D, fp32 [batch][heads][n_tokens rounded up to 128],
+// then the partial sums of the sinks' dK and dV.
+struct SinkBwdWorkspace {
+  size_t nl2_off, dvec_off, partial_off, bytes;
+};
+SinkBwdWorkspace sink_bwd_workspace_layout(int64_t batch, int64_t n_tokens, int64_t heads, int64_t kv_heads, int64_t d,
+                                           int window, int sinks);
+int launch_sink_attn_bwd(const SinkArgs& a, cudaStream_t stream);
+unsigned int sink_bwd_read_and_clear_error(cudaStream_t stream);
+
+// sink_decode.cu
+struct SinkDecodeArgs {
+  const void* q;
+  const void* k;                         // bf16 rows, or codes
+  const void* v;
+  const void* k_scales;                  // 4-bit cache
+  const void* v_scales;
+  void* o;
+  float* lse;
+  const int32_t* lengths;
+  int64_t q_strides[3], k_strides[3], v_strides[3], o_strides[3];
+  int32_t batch, capacity, heads, kv_heads, head_dim, window, sinks;
+  bool cache4;
+  float softmax_scale;
+};
+int launch_sink_decode(const SinkDecodeArgs& a, cudaStream_t stream);
+unsigned int decode_read_and_clear_error(cudaStream_t stream);
+
+// sink_cache4.cu
+struct Cache4Args {
+  bool read;
+  void* k;                               // rows, [batch][n_tokens][kv_heads][head_dim]
+  void* v;
+  uint8_t* k_codes;
+  void* k_scales;
+  uint8_t* v_codes;
+  void* v_scales;
+  const int32_t* start;
+  int64_t k_strides[3], v_strides[3];
+  int32_t batch, n_tokens, kv_heads, head_dim, capacity;
+};
+int launch_cache4(const Cache4Args& a, cudaStream_t stream);
+unsigned int cache4_read_and_clear_error(cudaStream_t stream);
+
 }  // namespace sa

@@ -1,0 +1,804 @@
+// Backward of the sink-window attention (sink_attn.cu) for sm_103a (tcgen05 + TMEM + TMA).
+//
+// Gradients of L = sum(dO * O) over the graph "key j is visible to query i iff j <= i and
+// (i - j <= window or j < sinks)". With P_ij = exp(s_ij - LSE_i), D_i = sum_d dO_id O_id:
+//   dP_ij = <dO_i, v_j>,  dS_ij = P_ij (dP_ij - D_i),
+//   dQ_i = c sum_j dS_ij k_j,  dK_j = c sum_i dS_ij q_i,  dV_j = sum_i P_ij dO_i.
+// Launches: sink_prep_kernel (D and -LSE log2(e), padded to whole tiles), sink_bwd_kernel<D, false>
+// (dQ: query-stationary), sink_bwd_kernel<D, true> (dK and dV: key-stationary, all query heads of
+// the key head), and sink_reduce_kernel when the sinks' rows were summed in parts. S and dP are
+// taken twice, so every gradient row has one owner: no atomics, the same bits every run.
+//
+// Step: 128 stationary rows (A0, A1) against 128 moving rows (B0, B1) of a ring stage,
+//   S = A0 B0^T, dP = A1 B1^T (tcgen05, SS, N = 128), then from the compute warps
+//   acc0 += dS B0 and, key-stationary, acc1 += P B1 (A from TMEM as bf16 pairs, B MN-major).
+//   dQ: A = Q, dO; B = K, V.  dK / dV: A = K, V; B = Q, dO (S and dP come out transposed).
+// A tcgen05.mma costs its issuing thread the same ~67 cycles at N = 64 as at N = 128, hence the
+// 128-row steps. At d <= 64 (and for dQ at any d) P and dS have TMEM columns of their own, so the
+// next step's S runs under this step's exponentials and its dP under this step's dS. Key-stationary
+// at d = 128 the accumulators leave no room: P goes over S and dS over dP, and the next S waits
+// for this step's dV product, the next dP for its dK product; products and exponentials still
+// alternate, dK / dP under one step's exponentials, dV / S under its dS.
+//
+// The sinks are seen by every query: the first key tile's items over the queries past the
+// window are cut into chunks of query tiles as long as an ordinary item, whose fp32 sums of the
+// sinks' rows go to the workspace and are added in a fixed order.
+//
+// One persistent CTA per SM (320 threads), items dealt out in turn:
+//   warp 0      lane 0 loads the stationary tiles and the ring by TMA
+//   warp 1      owns TMEM; lane 0 issues the MMAs
+//   warps 2-9   compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
+//               columns 64 h .. 64 h + 63 of a step, h = (w - 2) / 4; at an item's end they write
+//               its rows. An item's S and dP run under the previous item's output.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "ptx_sm100.cuh"
+#include "sa_internal.h"
+#include "tma_host.h"
+
+namespace sa {
+namespace {
+
+__device__ unsigned int g_sink_bwd_err;
+
+constexpr int kTile = 128;
+constexpr int kThreads = 320;
+constexpr int kComputeWarps = 8;
+constexpr int kMaxStages = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColDP = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, bool KV>
+struct Cfg {
+  static constexpr int CH = D >= 64 ? 64 : 32;         // elements per swizzled row
+  static constexpr int NCH = D / CH;
+  static constexpr int ROWB = CH * 2;
+  static constexpr uint32_t SWZ = ROWB == 128 ? kSwizzle128B : kSwizzle64B;
+  static constexpr CUtensorMapSwizzle TMA_SWZ =
+      ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  static constexpr uint32_t ATOM = 8 * ROWB;
+  static constexpr int CHUNK = kTile * ROWB;           // one d-chunk of a 128-row tile
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int STAGE = 2 * TILE + 1024;        // B0, B1, then -LSE log2(e) [128] and D [128]
+  static constexpr int SMEM_NEED = 1024 + 2 * TILE + STAGES * STAGE;
+  // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
+  static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
+  // P and dS in columns of their own, or over S and dP
+  static constexpr bool OWN = !KV || D <= 64;
+  static constexpr uint32_t COL_P = OWN ? 256 : kColS;
+  static constexpr uint32_t COL_DS = OWN ? (KV ? 320 : 256) : kColDP;
+  static constexpr uint32_t HALF = OWN ? 32 : 64;      // columns between the halves' P (or dS)
+  static constexpr uint32_t COL_ACC0 = KV ? (OWN ? 384 : 256) : 320;      // dQ or dK
+  static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;                      // dV
+  static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
+  static_assert(STAGES <= kMaxStages && SMEM <= 227 * 1024, "shared memory");
+};
+
+struct BParams {
+  int batch, n_tokens, heads, kv_heads, group;   // group: query heads per key head
+  int tiles, pitch;                 // 128-row tiles per sequence; padded tokens = 128 tiles
+  int window, sinks;
+  int n_items, n_main;              // items; the first n_main are ordinary, the rest sink chunks
+  int chunk_tiles, n_chunks;        // query tiles per sink chunk, sink chunks per (sequence, head)
+  int far_tile;                     // first query tile whose window misses key tile 0
+  const float* nl2;                 // [batch][heads][pitch]: -LSE log2(e); -inf past the sequence
+  const float* dvec;                // [batch][heads][pitch]: D
+  __nv_bfloat16* out0;              // dQ or dK
+  __nv_bfloat16* out1;              // dV
+  int64_t os_b[2], os_n[2], os_h[2];   // strides of out0, out1
+  float* partial;                   // [batch][kv_heads][n_chunks + 1][2][sinks][d]
+  float scale, scale_log2;
+};
+
+struct Bars {
+  uint64_t fixed_full, fixed_empty;                     // stationary tiles (phase: item)
+  uint64_t st_full[kMaxStages], st_empty[kMaxStages];   // ring
+  uint64_t s_full, dp_full;         // S / dP written (phase: step)
+  uint64_t s_free, dp_free;         // S / dP loaded by the compute warps
+  uint64_t p_full, ds_full;         // P / dS stored by the compute warps
+  uint64_t dv_done, dk_done;        // products of P (dV) and of dS (dK or dQ) complete
+  uint64_t acc_full;                // an item's accumulators complete (phase: item)
+  uint64_t drain;
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, abort_flag, &g_sink_bwd_err, kErrTimeout);
+}
+__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
+  int never = 0;
+  mbar_wait(bar, parity, &never, &g_sink_bwd_err, kErrTimeout);
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Work item: a stationary tile and its moving tiles. Step j (0 .. steps - 1) of a dQ item is key
+// tile 0 (n_sink = 1, j = 0) or tile0 + j - n_sink; of a dK / dV item query head head0 + j / per and
+// query tile tile0 + j % per.
+struct Item {
+  int s, head, tile;                // stationary rows: head of Q (dQ) or of K / V
+  int steps, per, tile0, n_sink;
+  int slot;                         // dK / dV: partial-sum slot of the sinks' rows (-1: none)
+};
+
+template <bool KV>
+__device__ __forceinline__ Item decode_item(const BParams& p, int k) {
+  Item it;
+  it.slot = -1;
+  if constexpr (!KV) {
+    const int bh = k % (p.batch * p.heads);
+    it.head = bh % p.heads;
+    it.s = bh / p.heads;
+    it.tile = p.tiles - 1 - k / (p.batch * p.heads);   // the last tiles see the most keys
+    it.tile0 = max(0, it.tile * kTile - p.window) / kTile;
+    it.n_sink = p.sinks > 0 && it.tile0 > 0 ? 1 : 0;
+    it.per = it.tile - it.tile0 + 1;
+    it.steps = it.n_sink + it.per;
+  } else {
+    const bool main = k < p.n_main;
+    const int r = main ? k : k - p.n_main;
+    const int bh = r % (p.batch * p.kv_heads);
+    const int rank = r / (p.batch * p.kv_heads);
+    it.head = bh % p.kv_heads;
+    it.s = bh / p.kv_heads;
+    it.n_sink = 0;
+    if (main) {
+      it.tile = rank;
+      it.tile0 = rank;
+      it.per = min(p.tiles - 1, (rank * kTile + kTile - 1 + p.window) / kTile) - rank + 1;
+      if (rank == 0 && p.n_chunks > 0) it.slot = 0;
+    } else {
+      it.tile = 0;
+      it.tile0 = p.far_tile + rank * p.chunk_tiles;
+      it.per = min(p.tiles, it.tile0 + p.chunk_tiles) - it.tile0;
+      it.slot = 1 + rank;
+    }
+    it.steps = it.per * p.group;
+  }
+  return it;
+}
+
+// Moving rows of step j: head and tile.
+template <bool KV>
+__device__ __forceinline__ void step_rows(const BParams& p, const Item& it, int j, int& head, int& tile) {
+  if constexpr (KV) {
+    const int hh = j / it.per;
+    head = it.head * p.group + hh;
+    tile = it.tile0 + j - hh * it.per;
+  } else {
+    head = it.head / p.group;
+    tile = j < it.n_sink ? 0 : it.tile0 + j - it.n_sink;
+  }
+}
+
+// Descriptor offset (bytes >> 4) of k-step ks (16 head-dimension elements) of a K-major tile.
+template <int D, bool KV>
+__device__ __forceinline__ constexpr uint32_t kstep(int ks) {
+  using C = Cfg<D, KV>;
+  return (uint32_t)(((ks * 16) / C::CH) * C::CHUNK + ((ks * 16) % C::CH) * 2) >> 4;
+}
+
+// ------------------------------------------------------------------ loader (warp 0, lane 0)
+
+template <int D, bool KV>
+__device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorMap* ta1, const CUtensorMap* tb0,
+                       const CUtensorMap* tb1, Bars& bars, uint8_t* sFix, uint8_t* sRing, volatile int* abort_flag) {
+  using C = Cfg<D, KV>;
+  int g = 0, n = 0;
+  bool ok = true;
+  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
+    const Item it = decode_item<KV>(p, k);
+    // the previous item's S and dP have read the stationary tiles
+    if (n > 0 && !(ok = wait_bar(&bars.fixed_empty, (uint32_t)(n - 1) & 1u, abort_flag))) break;
+    mbar_arrive_expect_tx(&bars.fixed_full, 2 * C::TILE);
+#pragma unroll
+    for (int c = 0; c < C::NCH; ++c) {
+      tma_load_4d(sFix + c * C::CHUNK, ta0, &bars.fixed_full, c * C::CH, it.head, it.tile * kTile, it.s);
+      tma_load_4d(sFix + C::TILE + c * C::CHUNK, ta1, &bars.fixed_full, c * C::CH, it.head, it.tile * kTile, it.s);
+    }
+    for (int j = 0; j < it.steps; ++j, ++g) {
+      const int st = g % C::STAGES;
+      if (g >= C::STAGES && !(ok = wait_bar(&bars.st_empty[st], (uint32_t)(g / C::STAGES - 1) & 1u, abort_flag))) break;
+      int head, tile;
+      step_rows<KV>(p, it, j, head, tile);
+      uint8_t* stage = sRing + st * C::STAGE;
+      mbar_arrive_expect_tx(&bars.st_full[st], 2 * C::TILE + (KV ? 1024 : 0));
+#pragma unroll
+      for (int c = 0; c < C::NCH; ++c) {
+        tma_load_4d(stage + c * C::CHUNK, tb0, &bars.st_full[st], c * C::CH, head, tile * kTile, it.s);
+        tma_load_4d(stage + C::TILE + c * C::CHUNK, tb1, &bars.st_full[st], c * C::CH, head, tile * kTile, it.s);
+      }
+      if constexpr (KV) {
+        const int64_t at = ((int64_t)it.s * p.heads + head) * p.pitch + (int64_t)tile * kTile;
+        bulk_load(stage + 2 * C::TILE, p.nl2 + at, 512, &bars.st_full[st]);
+        bulk_load(stage + 2 * C::TILE + 512, p.dvec + at, 512, &bars.st_full[st]);
+      }
+    }
+  }
+  // every copy of this CTA has landed before it may exit (n counts the items whose stationary
+  // tiles were requested, a broken-off one too; g the steps requested)
+  if (n > 0) drain_bar(&bars.fixed_full, (uint32_t)(n - 1) & 1u);
+  for (int t = max(0, g - C::STAGES); t < g; ++t)
+    drain_bar(&bars.st_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
+}
+
+// ------------------------------------------------------------------ MMA issuer (warp 1, lane 0)
+
+template <int D, bool KV>
+struct Issuer {
+  using C = Cfg<D, KV>;
+  Bars& bars;
+  uint32_t tmem;
+  volatile int* abort_flag;
+  uint64_t a0, a1, b0, b1, b0mn, b1mn;
+
+  __device__ uint64_t at(int st) const { return (uint64_t)((st * C::STAGE) >> 4); }
+
+  __device__ __forceinline__ void rows_x_rows(uint32_t col, uint64_t a, uint64_t b) const {
+    constexpr uint32_t idesc = make_idesc_bf16(128, kTile, 0, 0);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      mma_bf16_ss(tmem + col, a + kstep<D, KV>(ks), b + kstep<D, KV>(ks), idesc, ks > 0 ? 1u : 0u);
+  }
+  // acc (+)= A[128 x 128, bf16 pairs in TMEM] * B[128 x d], the moving tile read MN-major
+  __device__ __forceinline__ void pairs_x_tile(uint32_t col, uint32_t a, uint64_t b, bool acc) const {
+    constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)
+      mma_bf16_ts(tmem + col, tmem + a + C::HALF * (ks >> 2) + 8u * (ks & 3), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
+                  idesc, (acc || ks > 0) ? 1u : 0u);
+  }
+  // S of step g: its columns are free once step g - 1's are loaded (OWN), or once the product of
+  // the P that lies over them is complete
+  __device__ __forceinline__ bool scores(int g, int st) const {
+    if (g > 0 && !wait_bar(C::OWN ? &bars.s_free : &bars.dv_done, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
+    if (!wait_bar(&bars.st_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag)) return false;
+    tc_fence_after();
+    rows_x_rows(kColS, a0, b0 + at(st));
+    mma_commit(&bars.s_full);
+    return true;
+  }
+  __device__ __forceinline__ bool products(int g, int st) const {
+    if (g > 0 && !wait_bar(C::OWN ? &bars.dp_free : &bars.dk_done, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
+    tc_fence_after();
+    rows_x_rows(kColDP, a1, b1 + at(st));
+    mma_commit(&bars.dp_full);
+    return true;
+  }
+  __device__ __forceinline__ bool acc1(int g, int st, bool acc) const {
+    if (!wait_bar(&bars.p_full, (uint32_t)g & 1u, abort_flag)) return false;
+    tc_fence_after();
+    pairs_x_tile(C::COL_ACC1, C::COL_P, b1mn + at(st), acc);
+    mma_commit(&bars.dv_done);
+    return true;
+  }
+  __device__ __forceinline__ bool acc0(int g, int st, bool acc) const {
+    if (!wait_bar(&bars.ds_full, (uint32_t)g & 1u, abort_flag)) return false;
+    tc_fence_after();
+    pairs_x_tile(C::COL_ACC0, C::COL_DS, b0mn + at(st), acc);
+    mma_commit(&bars.st_empty[st]);
+    mma_commit(&bars.dk_done);
+    return true;
+  }
+  // One item of `steps` steps from step g on
+  __device__ bool item(int g, int steps) const {
+    if (!scores(g, g % C::STAGES) || !products(g, g % C::STAGES)) return false;
+    if (steps == 1) mma_commit(&bars.fixed_empty);
+    for (int j = 0; j < steps; ++j, ++g) {
+      const int st = g % C::STAGES, nx = (g + 1) % C::STAGES;
+      const bool more = j + 1 < steps, last = j + 2 == steps;
+      if (C::OWN && more && !scores(g + 1, nx)) return false;
+      if (KV && !acc1(g, st, j > 0)) return false;
+      if (!C::OWN && more && !scores(g + 1, nx)) return false;
+      if (C::OWN && more && !products(g + 1, nx)) return false;
+      if (!acc0(g, st, j > 0)) return false;
+      if (!C::OWN && more && !products(g + 1, nx)) return false;
+      if (last) mma_commit(&bars.fixed_empty);         // the item's last S and dP are issued
+    }
+    mma_commit(&bars.acc_full);
+    return true;
+  }
+};
+
+template <int D, bool KV>
+__device__ void issuer(const BParams& p, Bars& bars, uint8_t* sFix, uint8_t* sRing, uint32_t tmem,
+                       volatile int* abort_flag) {
+  using C = Cfg<D, KV>;
+  const uint32_t fix = smem_u32(sFix), ring = smem_u32(sRing);
+  const Issuer<D, KV> I{bars, tmem, abort_flag,
+                        make_smem_desc(fix, 16, C::ATOM, C::SWZ),
+                        make_smem_desc(fix + C::TILE, 16, C::ATOM, C::SWZ),
+                        make_smem_desc(ring, 16, C::ATOM, C::SWZ),
+                        make_smem_desc(ring + C::TILE, 16, C::ATOM, C::SWZ),
+                        make_smem_desc(ring, C::CHUNK, C::ATOM, C::SWZ),
+                        make_smem_desc(ring + C::TILE, C::CHUNK, C::ATOM, C::SWZ)};
+  int g = 0, n = 0;
+  for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
+    const Item it = decode_item<KV>(p, k);
+    if (!wait_bar(&bars.fixed_full, (uint32_t)n & 1u, abort_flag)) break;
+    if (!I.item(g, it.steps)) break;
+    g += it.steps;
+  }
+  // no MMA of this thread is still at work when the CTA frees its TMEM
+  mma_commit(&bars.drain);
+  drain_bar(&bars.drain, 0);
+}
+
+// ------------------------------------------------------------------ compute (warps 2-9)
+
+// Bits b in [lo, hi] of 32.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const uint32_t from = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : (0xffffffffu << lo));
+  const uint32_t upto = hi >= 31 ? 0xffffffffu : (hi < 0 ? 0u : ((2u << hi) - 1u));
+  return from & upto;
+}
+
+// Visible columns c0 .. c0 + 31 of the thread's row token r. dQ: r is a query, columns are keys;
+// dK / dV: r is a key, columns are queries.
+template <bool KV>
+__device__ __forceinline__ uint32_t visible(int r, int c0, int window, int sinks) {
+  if constexpr (KV) return bit_range(r - c0, r < sinks ? 31 : r + window - c0);
+  else return bit_range(r - window - c0, r - c0) | (bit_range(0, sinks - 1 - c0) & bit_range(0, r - c0));
+}
+
+template <int D, bool KV>
+__device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<D, KV>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  const int row = quarter * 32 + lane;
+  const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t tS = base + kColS + 64u * half, tDP = base + kColDP + 64u * half;
+  const uint32_t tPout = base + C::COL_P + C::HALF * half, tDSout = base + C::COL_DS + C::HALF * half;
+  const float kNegInf = __int_as_float(0xff800000);
+  const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+  int g = 0, n = 0;
+  for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
+    const Item it = decode_item<KV>(p, k);
+    const int tok = it.tile * kTile + row;
+    float nl2 = 0.f, dval = 0.f;
+    if constexpr (!KV) {
+      const int64_t at = ((int64_t)it.s * p.heads + it.head) * p.pitch + tok;
+      nl2 = p.nl2[at];
+      dval = p.dvec[at];
+    }
+    for (int j = 0; j < it.steps; ++j, ++g) {
+      int head, tile;
+      step_rows<KV>(p, it, j, head, tile);
+      const int c0 = tile * kTile + 64 * half;
+      const uint32_t see0 = visible<KV>(tok, c0, p.window, p.sinks);
+      const uint32_t see1 = visible<KV>(tok, c0 + 32, p.window, p.sinks);
+      const bool any = __any_sync(0xffffffffu, (see0 | see1) != 0u);
+      const bool full = __all_sync(0xffffffffu, (see0 & see1) == 0xffffffffu);
+      const int st = g % C::STAGES;
+      const float* vec = reinterpret_cast<const float*>(sRing + st * C::STAGE + 2 * C::TILE) + 64 * half;
+      if (!__all_sync(0xffffffffu, wait_bar(&bars.s_full, (uint32_t)g & 1u, abort_flag))) return;
+      tc_fence_after();
+      // ---- P
+      float pr[64];
+      if (any) {
+        uint32_t v[64];
+        tmem_ld_x32(tS, v);
+        tmem_ld_x32(tS + 32, v + 32);
+        if (KV) {
+          // the stage's -LSE and D have landed with its tiles
+          if (!__all_sync(0xffffffffu, wait_bar(&bars.st_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) return;
+        }
+        tmem_ld_wait<64>(v);
+        if (C::OWN) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.s_free);
+        }
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          float4 L = make_float4(nl2, nl2, nl2, nl2);
+          if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + e);
+          const uint64_t s01 = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          const uint64_t s23 = f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+          float x[4];
+          f2_unpack(f2_fma(s01, c2, f2_pack(L.x, L.y)), x[0], x[1]);
+          f2_unpack(f2_fma(s23, c2, f2_pack(L.z, L.w)), x[2], x[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pr[e + i] = ex2_approx(x[i]);
+        }
+        if (!full) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) pr[e] = (((e < 32 ? see0 : see1) >> (e & 31)) & 1u) ? pr[e] : 0.f;
+        }
+      } else {
+        if (C::OWN) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.s_free);
+        }
+#pragma unroll
+        for (int e = 0; e < 64; ++e) pr[e] = 0.f;
+      }
+      if constexpr (KV) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) pk[e >> 1] = pack_bf16x2(pr[e], pr[e + 1]);
+        if (C::OWN && g > 0) {
+          // the previous step's dV product has read P
+          if (!__all_sync(0xffffffffu, wait_bar(&bars.dv_done, (uint32_t)(g - 1) & 1u, abort_flag))) return;
+          tc_fence_after();
+        }
+        tmem_st_x32(tPout, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full);
+      }
+      // ---- dS = P (dP - D)
+      if (!__all_sync(0xffffffffu, wait_bar(&bars.dp_full, (uint32_t)g & 1u, abort_flag))) return;
+      tc_fence_after();
+      uint32_t ds[32];
+      if (any) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t v[32];
+          tmem_ld_x32(tDP + 32 * q, v);
+          tmem_ld_wait<32>(v);
+          if (C::OWN && q == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.dp_free);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 L = make_float4(dval, dval, dval, dval);
+            if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + 128 + 32 * q + e);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
+              float y0, y1;
+              f2_unpack(f2_mul(f2_pack(pr[32 * q + e + i], pr[32 * q + e + i + 1]),
+                               f2_sub(f2_pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1])), d2)),
+                        y0, y1);
+              ds[16 * q + ((e + i) >> 1)] = pack_bf16x2(y0, y1);
+            }
+          }
+        }
+      } else {
+        if (C::OWN) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.dp_free);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ds[e] = 0u;
+      }
+      if (C::OWN && g > 0) {
+        // the previous step's product has read dS
+        if (!__all_sync(0xffffffffu, wait_bar(&bars.dk_done, (uint32_t)(g - 1) & 1u, abort_flag))) return;
+        tc_fence_after();
+      }
+      tmem_st_x32(tDSout, ds);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.ds_full);
+    }
+    // ---- the item's rows
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return;
+    tc_fence_after();
+    constexpr int DH = D / 2;
+    const bool part = KV && it.slot >= 0 && tok < p.sinks;          // an fp32 partial sum
+    const bool store = !part && tok < p.n_tokens && it.slot <= 0;   // a sink chunk writes sinks only
+#pragma unroll 1
+    for (int m = 0; m < (KV ? 2 : 1); ++m) {
+      const float f = m ? 1.f : p.scale;
+      __nv_bfloat16* orow =
+          (m ? p.out1 : p.out0) + it.s * p.os_b[m] + tok * p.os_n[m] + it.head * p.os_h[m] + DH * half;
+      float* prow = nullptr;
+      if (part)
+        prow = p.partial + DH * half +
+               (((((int64_t)it.s * p.kv_heads + it.head) * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D;
+#pragma unroll 1
+      for (int c = 0; c < DH / 16; ++c) {
+        uint32_t w[16];
+        tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)(DH * half + 16 * c), w);
+        tmem_ld_wait<16>(w);
+        if (store) {
+          uint32_t pkd[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            pkd[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
+          uint4* dst = reinterpret_cast<uint4*>(orow + 16 * c);
+          dst[0] = make_uint4(pkd[0], pkd[1], pkd[2], pkd[3]);
+          dst[1] = make_uint4(pkd[4], pkd[5], pkd[6], pkd[7]);
+        } else if (part) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(prow + 16 * c + e) =
+                make_float4(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f, __uint_as_float(w[e + 2]) * f,
+                            __uint_as_float(w[e + 3]) * f);
+        }
+      }
+    }
+    // The next item's first product into the accumulators follows these loads: its issuer waits
+    // for the P or dS that this warp stores after them.
+  }
+}
+
+template <int D, bool KV>
+__global__ void __launch_bounds__(kThreads, 1)
+    sink_bwd_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap ta1,
+                    const __grid_constant__ CUtensorMap tb0, const __grid_constant__ CUtensorMap tb1,
+                    const __grid_constant__ BParams p) {
+  using C = Cfg<D, KV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars.fixed_full, 1);
+    mbar_init(&bars.fixed_empty, 1);
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&bars.st_full[i], 1);
+      mbar_init(&bars.st_empty[i], 1);
+    }
+    mbar_init(&bars.s_full, 1);
+    mbar_init(&bars.dp_full, 1);
+    mbar_init(&bars.s_free, kComputeWarps);
+    mbar_init(&bars.dp_free, kComputeWarps);
+    mbar_init(&bars.p_full, kComputeWarps);
+    mbar_init(&bars.ds_full, kComputeWarps);
+    mbar_init(&bars.dv_done, 1);
+    mbar_init(&bars.dk_done, 1);
+    mbar_init(&bars.acc_full, 1);
+    mbar_init(&bars.drain, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&ta0);
+    tma_prefetch_desc(&ta1);
+    tma_prefetch_desc(&tb0);
+    tma_prefetch_desc(&tb1);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  uint8_t* sFix = sbase;
+  uint8_t* sRing = sFix + 2 * C::TILE;
+  if (warp == 0) {
+    if ((threadIdx.x & 31) == 0) loader<D, KV>(p, &ta0, &ta1, &tb0, &tb1, bars, sFix, sRing, &abort_flag);
+    __syncwarp();
+  } else if (warp == 1) {
+    if ((threadIdx.x & 31) == 0) issuer<D, KV>(p, bars, sFix, sRing, tmem, &abort_flag);
+    __syncwarp();
+  } else {
+    compute<D, KV>(p, bars, sRing, tmem, &abort_flag);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ D and -LSE log2(e)
+
+// D / 8 consecutive threads per (sequence, token, head) row, 16 bytes of O and dO each; tokens
+// n .. pitch - 1 get D = 0 and -LSE = -inf, so that their P is 0.
+template <int D>
+__global__ void __launch_bounds__(256)
+    sink_prep_kernel(const __nv_bfloat16* o, const __nv_bfloat16* d_o, const float* lse, int64_t o_sb, int64_t o_sn,
+                     int64_t o_sh, int64_t g_sb, int64_t g_sn, int64_t g_sh, int batch, int n_tokens, int heads,
+                     int pitch, float* nl2, float* dvec) {
+  constexpr int G = D / 8;
+  const float kNegInf = __int_as_float(0xff800000);
+  const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t row = gid / G;
+  const int part = (int)(gid % G);
+  const bool in = row < (int64_t)batch * pitch * heads;
+  const int h = (int)(row % heads);
+  const int i = (int)(row / heads % pitch);
+  const int s = (int)(row / heads / pitch);
+  float acc = 0.f;
+  if (in && i < n_tokens) {
+    const uint4 a = *reinterpret_cast<const uint4*>(o + s * o_sb + i * o_sn + h * o_sh + 8 * part);
+    const uint4 b = *reinterpret_cast<const uint4*>(d_o + s * g_sb + i * g_sn + h * g_sh + 8 * part);
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
+      acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
+    }
+  }
+#pragma unroll
+  for (int w = G / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w, G);
+  if (in && part == 0) {
+    const int64_t at = ((int64_t)s * heads + h) * pitch + i;
+    dvec[at] = acc;
+    nl2[at] = i < n_tokens ? -lse[((int64_t)s * heads + h) * n_tokens + i] * kLog2e : kNegInf;
+  }
+}
+
+// dK, dV of the sinks' rows: the partial sums of the first key tile's items, in slot order.
+__global__ void __launch_bounds__(256) sink_reduce_kernel(const __grid_constant__ BParams p, int d) {
+  const int quads = d / 4;
+  const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int e = (int)(gid % quads) * 4;
+  int64_t r = gid / quads;
+  const int row = (int)(r % p.sinks);
+  r /= p.sinks;
+  const int m = (int)(r % 2);
+  const int64_t bh = r / 2;
+  if (bh >= (int64_t)p.batch * p.kv_heads || row >= p.n_tokens) return;
+  const float* src = p.partial + (bh * (p.n_chunks + 1) * 2 + m) * (int64_t)p.sinks * d + (int64_t)row * d + e;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c <= p.n_chunks; ++c) {
+    const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)c * 2 * p.sinks * d);
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  __nv_bfloat16* out =
+      (m ? p.out1 : p.out0) + (bh / p.kv_heads) * p.os_b[m] + row * p.os_n[m] + (bh % p.kv_heads) * p.os_h[m] + e;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+}
+
+// ------------------------------------------------------------------ launch
+
+// Chunks of the first key tile's queries past the window (none without sinks).
+struct Chunks {
+  int far_tile, tiles_each, count;
+};
+
+Chunks sink_chunks(int tiles, int window, int sinks) {
+  Chunks c;
+  c.far_tile = (int)(((int64_t)kTile - 1 + window) / kTile) + 1;
+  if (c.far_tile > tiles) c.far_tile = tiles;
+  // as long as an ordinary item, and at least 8 tiles, so that their partial sums stay few
+  c.tiles_each = c.far_tile > 8 ? c.far_tile : 8;
+  c.count = sinks > 0 ? (tiles - c.far_tile + c.tiles_each - 1) / c.tiles_each : 0;
+  return c;
+}
+
+template <int D, bool KV>
+int launch(const SinkArgs& a, const BParams& p, cudaStream_t stream) {
+  using C = Cfg<D, KV>;
+  CUtensorMap tq, tk, tv, tdo;
+  auto map = [&](CUtensorMap* m, const void* base, int heads, const int64_t st[3]) {
+    return encode_bhnd_map(m, base, a.batch, a.n_tokens, heads, D, st[0], st[1], st[2], C::CH, kTile, C::TMA_SWZ);
+  };
+  if (!map(&tq, a.q, a.heads, a.q_strides) || !map(&tk, a.k, a.kv_heads, a.k_strides) ||
+      !map(&tv, a.v, a.kv_heads, a.v_strides) || !map(&tdo, a.d_o, a.heads, a.do_strides))
+    return SA_ERR_UNSUPPORTED;
+  const auto kern = sink_bwd_kernel<D, KV>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return SA_ERR_CUDA;
+  const int sm_count = current_sm_count();
+  const int grid = p.n_items < sm_count ? p.n_items : sm_count;
+  if (KV) kern<<<grid, kThreads, C::SMEM, stream>>>(tk, tv, tq, tdo, p);
+  else kern<<<grid, kThreads, C::SMEM, stream>>>(tq, tdo, tk, tv, p);
+  return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+template <int D>
+int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream) {
+  uint8_t* wsb = static_cast<uint8_t*>(a.workspace);
+  BParams p;
+  memset(&p, 0, sizeof(p));
+  p.batch = a.batch;
+  p.n_tokens = a.n_tokens;
+  p.heads = a.heads;
+  p.kv_heads = a.kv_heads;
+  p.group = a.heads / a.kv_heads;
+  p.tiles = (a.n_tokens + kTile - 1) / kTile;
+  p.pitch = p.tiles * kTile;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  float* nl2 = reinterpret_cast<float*>(wsb + ws.nl2_off);
+  float* dvec = reinterpret_cast<float*>(wsb + ws.dvec_off);
+  p.nl2 = nl2;
+  p.dvec = dvec;
+  p.partial = reinterpret_cast<float*>(wsb + ws.partial_off);
+  p.scale = a.softmax_scale;
+  p.scale_log2 = a.softmax_scale * kLog2e;
+  const int64_t threads = (int64_t)a.batch * p.pitch * a.heads * (D / 8);
+  sink_prep_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.d_o), a.lse, a.o_strides[0],
+      a.o_strides[1], a.o_strides[2], a.do_strides[0], a.do_strides[1], a.do_strides[2], a.batch, a.n_tokens, a.heads,
+      p.pitch, nl2, dvec);
+  if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
+  BParams pq = p;
+  pq.n_items = pq.n_main = a.batch * a.heads * p.tiles;
+  pq.out0 = static_cast<__nv_bfloat16*>(a.dq);
+  pq.os_b[0] = a.dq_strides[0];
+  pq.os_n[0] = a.dq_strides[1];
+  pq.os_h[0] = a.dq_strides[2];
+  int st = launch<D, false>(a, pq, stream);
+  if (st != SA_OK) return st;
+  const Chunks c = sink_chunks(p.tiles, a.window, a.sinks);
+  p.far_tile = c.far_tile;
+  p.chunk_tiles = c.tiles_each;
+  p.n_chunks = c.count;
+  p.n_main = a.batch * a.kv_heads * p.tiles;
+  p.n_items = p.n_main + a.batch * a.kv_heads * c.count;
+  p.out0 = static_cast<__nv_bfloat16*>(a.dk);
+  p.out1 = static_cast<__nv_bfloat16*>(a.dv);
+  for (int m = 0; m < 2; ++m) {
+    const int64_t* st = m ? a.dv_strides : a.dk_strides;
+    p.os_b[m] = st[0];
+    p.os_n[m] = st[1];
+    p.os_h[m] = st[2];
+  }
+  st = launch<D, true>(a, p, stream);
+  if (st != SA_OK || c.count == 0) return st;
+  const int64_t quads = (int64_t)a.batch * a.kv_heads * 2 * a.sinks * (D / 4);
+  sink_reduce_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p, D);
+  return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // namespace
+
+SinkBwdWorkspace sink_bwd_workspace_layout(int64_t batch, int64_t n_tokens, int64_t heads, int64_t kv_heads, int64_t d,
+                                           int window, int sinks) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const int tiles = (int)((n_tokens + kTile - 1) / kTile);
+  const Chunks c = sink_chunks(tiles, window, sinks);
+  SinkBwdWorkspace w;
+  w.nl2_off = 0;
+  w.dvec_off = up((size_t)(batch * heads * tiles) * kTile * 4);
+  w.partial_off = 2 * w.dvec_off;
+  w.bytes = w.partial_off + (c.count > 0 ? up((size_t)(batch * kv_heads * (c.count + 1)) * 2 * sinks * d * 4) : 0);
+  return w;
+}
+
+int launch_sink_attn_bwd(const SinkArgs& a, cudaStream_t stream) {
+  const SinkBwdWorkspace ws =
+      sink_bwd_workspace_layout(a.batch, a.n_tokens, a.heads, a.kv_heads, a.head_dim, a.window, a.sinks);
+  if (a.workspace_bytes < ws.bytes) return SA_ERR_CAPACITY;
+  switch (a.head_dim) {
+    case 32: return launch_d<32>(a, ws, stream);
+    case 64: return launch_d<64>(a, ws, stream);
+    case 128: return launch_d<128>(a, ws, stream);
+  }
+  return SA_ERR_UNSUPPORTED;
+}
+
+unsigned int sink_bwd_read_and_clear_error(cudaStream_t stream) {
+  unsigned int v = 0, zero = 0;
+  cudaMemcpyFromSymbolAsync(&v, g_sink_bwd_err, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+  cudaMemcpyToSymbolAsync(g_sink_bwd_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+  cudaStreamSynchronize(stream);
+  return v;
+}
+
+}  // namespace sa

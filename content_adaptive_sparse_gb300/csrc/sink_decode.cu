@@ -1,0 +1,591 @@
+// Single-token form of the sink-window attention over a key / value cache: the query is token
+// length - 1 of its sequence and sees cache rows j < length with length - 1 - j <= window or
+// j < sinks. Cache rows are bf16 (any [batch, capacity, kv_heads, d] strides) or 4-bit codes with
+// one bf16 scale per 32 elements (sink_cache4.cu has the layout). Bandwidth bound: each visible
+// row is read once for all query heads that share it, and 4-bit rows are read as stored.
+//
+// A CTA takes one (sequence, key head, up to 16 query heads) and a share of its rows; the CTAs of a
+// cluster split the rows of one (sequence, key head) and join their partial results over
+// distributed shared memory, so there is one launch, no workspace and no atomics.
+//   warp 4      lane 0 fills a ring of 64-row stages: 16-row TMA boxes (bf16) or bulk copies of the
+//               contiguous 4-bit rows and scales
+//   warps 0-3   16 rows of every stage each, with their own running maximum and sum:
+//               S = Q K^T and O += P V on mma.sync m16n8k16 (the 16 query rows are one m-tile;
+//               a tcgen05 tile would need 64 or 128 rows of queries, and the tensor work is small
+//               beside the reads)
+// 4-bit keys: the codes (-7 .. 7, exact in bf16) go to the tensor cores as they are, one pair of
+// k-steps per scale group, and the group's sum is multiplied by its scale in fp32. 4-bit values:
+// the scale belongs to the summed-over row, so it multiplies P (in fp32, before P's rounding).
+// The products' order of elements within a row is free, so a lane takes the elements that lie
+// together in the stored words, and Q and O use the same order.
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "mma_frag.cuh"
+#include "ptx_sm100.cuh"
+#include "sa_internal.h"
+#include "tma_host.h"
+
+namespace sa {
+namespace {
+
+using frag::lds128;
+using frag::ldsm_x4_t;
+using frag::mma16816;
+using frag::swz;
+
+__device__ unsigned int g_decode_err;
+
+constexpr int kWarps = 4;               // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kRows = 16 * kWarps;      // cache rows per stage
+constexpr int kQ = 16;                  // query heads per CTA (one m-tile)
+constexpr int kMaxStages = 8;
+constexpr int kMaxCluster = 8;
+
+template <int D, bool Q4>
+struct Cfg {
+  static constexpr int CH = D >= 64 ? 64 : 32;         // bf16: elements per swizzled row
+  static constexpr int ROWB = CH * 2;
+  static constexpr CUtensorMapSwizzle TMA_SWZ =
+      ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  static constexpr int NG = D / 32;                    // scale groups
+  static constexpr int CODES = Q4 ? kRows * D / 2 : kRows * D * 2;   // K (or V) bytes of a stage
+  static constexpr int SCALES = Q4 ? kRows * NG * 2 : 0;
+  static constexpr int STAGE = 2 * (CODES + SCALES);
+  static constexpr int STAGES = Q4 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : (D == 64 ? 4 : 8));
+  static constexpr int RING = STAGES * STAGE;
+  // after the last stage the ring's memory holds the warps' partial results
+  static constexpr int MERGE = kWarps * kQ * (D + 2) * 4;
+  static constexpr int SMEM = 1024 + (RING > MERGE ? RING : MERGE);
+  static constexpr int NT = D / 8;                     // output n-tiles
+  static_assert(STAGES <= kMaxStages && SMEM <= 227 * 1024, "shared memory");
+};
+
+struct DParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;                       // [batch][heads]
+  const int32_t* lengths;
+  const uint8_t* kc;                // 4-bit cache, [batch][kv_heads][capacity] rows
+  const __nv_bfloat16* ks;
+  const uint8_t* vc;
+  const __nv_bfloat16* vs;
+  int64_t q_sb, q_sh, o_sb, o_sh;
+  int heads, kv_heads, group, head_groups, capacity, window, sinks;
+  float scale_log2;
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, abort_flag, &g_decode_err, kErrTimeout);
+}
+
+// The rows that a sequence's query sees, cut into stages of 64: first those of the sinks that the
+// window does not hold, then the window's, this CTA's share being [begin, end).
+struct Rows {
+  int len, lo, n_sink;              // tokens; first token of the window; sinks before it
+  int sink_stages, first, begin, end;   // first: token of the window's first stage row
+
+  template <bool Q4>
+  __device__ static Rows of(const DParams& p, int s, int rank, int ranks) {
+    Rows r;
+    r.len = max(0, min(p.lengths[s], p.capacity));
+    r.lo = max(0, r.len - 1 - p.window);
+    r.n_sink = min(p.sinks, r.lo);
+    r.first = Q4 ? (r.lo & ~7) : r.lo;          // bulk copies start at a multiple of 16 bytes
+    r.sink_stages = (r.n_sink + kRows - 1) / kRows;
+    const int total = r.sink_stages + (r.len - r.first + kRows - 1) / kRows;
+    const int per = (total + ranks - 1) / ranks;
+    r.begin = min(total, rank * per);
+    r.end = min(total, r.begin + per);
+    return r;
+  }
+  // stage j: its first row's token, and the tokens [lo, hi) of it that are seen
+  __device__ __forceinline__ void stage(int j, int& tok, int& vlo, int& vhi) const {
+    if (j < sink_stages) {
+      tok = j * kRows;
+      vlo = 0;
+      vhi = n_sink;
+    } else {
+      tok = first + (j - sink_stages) * kRows;
+      vlo = lo;
+      vhi = len;
+    }
+  }
+};
+
+template <int D, bool Q4>
+__device__ void producer(const DParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Bars& bars, uint8_t* ring,
+                         const Rows& r, int s, int hk, volatile int* abort_flag) {
+  using C = Cfg<D, Q4>;
+  int g = 0;
+  for (int j = r.begin; j < r.end; ++j, ++g) {
+    const int st = g % C::STAGES;
+    if (g >= C::STAGES && !wait_bar(&bars.empty[st], (uint32_t)(g / C::STAGES - 1) & 1u, abort_flag)) break;
+    int tok, vlo, vhi;
+    r.stage(j, tok, vlo, vhi);
+    uint8_t* stage = ring + st * C::STAGE;
+    if constexpr (Q4) {
+      const int rows = min(kRows, (vhi - tok + 7) & ~7);          // the capacity is a multiple of 8
+      const int64_t row = ((int64_t)s * p.kv_heads + hk) * p.capacity + tok;
+      mbar_arrive_expect_tx(&bars.full[st], (uint32_t)(rows * (D + 4 * C::NG)));
+      bulk_load(stage, p.kc + row * (D / 2), rows * (D / 2), &bars.full[st]);
+      bulk_load(stage + C::CODES, p.ks + row * C::NG, rows * C::NG * 2, &bars.full[st]);
+      bulk_load(stage + C::CODES + C::SCALES, p.vc + row * (D / 2), rows * (D / 2), &bars.full[st]);
+      bulk_load(stage + 2 * C::CODES + C::SCALES, p.vs + row * C::NG, rows * C::NG * 2, &bars.full[st]);
+    } else {
+      const int boxes = min(kWarps, (vhi - tok + 15) >> 4);       // tok >= vlo: every earlier box is seen
+      mbar_arrive_expect_tx(&bars.full[st], (uint32_t)(boxes * 16 * D * 4));
+      for (int b = 0; b < boxes; ++b)
+#pragma unroll
+        for (int c = 0; c < D / C::CH; ++c) {
+          uint8_t* dst = stage + (c * kRows + 16 * b) * C::ROWB;
+          tma_load_4d(dst, tk, &bars.full[st], c * C::CH, hk, tok + 16 * b, s);
+          tma_load_4d(dst + C::CODES, tv, &bars.full[st], c * C::CH, hk, tok + 16 * b, s);
+        }
+    }
+  }
+  // every copy of this CTA has landed before it goes on
+  int never = 0;
+  for (int t = max(0, g - C::STAGES); t < g; ++t)
+    mbar_wait(&bars.full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u, &never, &g_decode_err, kErrTimeout);
+}
+
+// Shared-memory address of 16-byte unit u of a stage's row (the TMA swizzle undone).
+template <int D>
+__device__ __forceinline__ uint32_t row_unit(uint32_t base, int row, int u) {
+  if constexpr (D == 32) {
+    return base + (uint32_t)(row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
+  } else {
+    return swz(base + (uint32_t)((u >> 3) * kRows * 128), row, u & 7);
+  }
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+
+// Codes c (nibble s of the low and of the high half-word, 1 .. 15) as the bf16 pair (c - 8): 0x43
+// over a zero exponent-and-mantissa byte is 128 + c, exact in bf16, and so is the difference.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int s) {
+  const uint32_t x = ((w >> (4 * s)) & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "words");
+  if constexpr (N == 4) {
+    const uint4 v = lds128(addr);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  }
+}
+
+// Scales of rows `row` and `row + 1` (row even): sc[e][c], zero for a row outside [lo, hi).
+template <int NG>
+__device__ __forceinline__ void load_scales(uint32_t base, int row, bool on0, bool on1, float (&sc)[2][NG]) {
+  uint32_t w[NG];
+  lds_words<NG>(base + (uint32_t)(row * NG * 2), w);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+      const int i = e * NG + c;
+      const float v = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+      sc[e][c] = (e ? on1 : on0) ? v : 0.f;
+    }
+}
+
+template <int D, bool Q4>
+__device__ void consumer(const DParams& p, Bars& bars, uint8_t* ring, const Rows& r, int s, int h0, int n_q,
+                         float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
+  using C = Cfg<D, Q4>;
+  constexpr int NG = C::NG, KS = D / 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const float kNegInf = __int_as_float(0xff800000);
+  const float c = p.scale_log2;
+  // Q as A fragments: rows g and g + 8 (absent heads are zero)
+  uint32_t qa[KS][4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int row = g + 8 * half;
+    const __nv_bfloat16* qr = p.q + (int64_t)s * p.q_sb + (int64_t)(h0 + row) * p.q_sh;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      if constexpr (Q4) {
+        // elements 32 i + 8 t .. + 7: the pairs of code word (t, i)
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (row < n_q) w = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
+        qa[2 * i][half] = w.x;
+        qa[2 * i][half + 2] = w.y;
+        qa[2 * i + 1][half] = w.z;
+        qa[2 * i + 1][half + 2] = w.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const __nv_bfloat16* at = qr + 32 * i + 16 * k + 2 * t;
+          qa[2 * i + k][half] = row < n_q ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+          qa[2 * i + k][half + 2] = row < n_q ? *reinterpret_cast<const uint32_t*>(at + 8) : 0u;
+        }
+      }
+    }
+  }
+  const uint32_t ring0 = smem_u32(ring);
+  for (int j = r.begin, n = 0; j < r.end; ++j, ++n) {
+    const int st = n % C::STAGES;
+    int tok, vlo, vhi;
+    r.stage(j, tok, vlo, vhi);
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.full[st], (uint32_t)(n / C::STAGES) & 1u, abort_flag))) return;
+    const int t0 = tok + 16 * warp;
+    if (t0 < vhi && t0 + 16 > vlo) {
+      const uint32_t kb = ring0 + (uint32_t)(st * C::STAGE);
+      const uint32_t vb = kb + C::CODES + C::SCALES;
+      const int row0 = 16 * warp;
+      // rows of this lane's score columns: 8 nt + 2 t + e
+      bool on[2][2];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = t0 + 8 * nt + 2 * t + e;
+          on[nt][e] = at >= vlo && at < vhi;
+        }
+      float sc[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+      if constexpr (Q4) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          uint32_t w[NG];
+          lds_words<NG>(kb + (uint32_t)((row0 + 8 * nt + g) * (D / 2) + t * (D / 8)), w);
+          float ksc[2][NG];
+          load_scales<NG>(kb + C::CODES, row0 + 8 * nt + 2 * t, true, true, ksc);
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(acc, qa[2 * i], code_pair(w[i], 0), code_pair(w[i], 1));
+            mma16816(acc, qa[2 * i + 1], code_pair(w[i], 2), code_pair(w[i], 3));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nt][e] = fmaf(acc[e], ksc[e & 1][i], sc[nt][e]);
+          }
+        }
+      } else {
+        const int mi = lane >> 3;
+        const int row = row0 + (lane & 7) + ((mi >> 1) << 3);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(row_unit<D>(kb, row, 2 * ks + (mi & 1)), b0, b1, b2, b3);
+          mma16816(sc[0], qa[ks], b0, b1);
+          mma16816(sc[1], qa[ks], b2, b3);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = on[nt][e & 1] ? sc[nt][e] * c : kNegInf;
+      // running maximum of rows g (half 0) and g + 8; O and l follow it only when it grows by 2^8
+      float mx[2];
+      bool grow = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        grow = grow || mx[h] > m[h] + 8.f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (mx[h] > m[h] + 8.f) {
+            const float a = ex2_approx(m[h] - mx[h]);             // 0 from -inf
+            m[h] = mx[h];
+            l[h] *= a;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[i][2 * h] *= a;
+              o[i][2 * h + 1] *= a;
+            }
+          }
+        }
+      }
+      const float ref[2] = {m[0] == kNegInf ? 0.f : m[0], m[1] == kNegInf ? 0.f : m[1]};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[nt][e] = ex2_approx(sc[nt][e] - ref[e >> 1]);
+          l[e >> 1] += sc[nt][e];
+        }
+      if constexpr (Q4) {
+        float vsc[2][2][NG];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+          load_scales<NG>(vb + C::CODES, row0 + 8 * nt + 2 * t, on[nt][0], on[nt][1], vsc[nt]);
+        // words (g / 2, c) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; byte pair g % 2 of each holds
+        // this lane's elements 32 c + 4 g + {0, 2, 1, 3} (nibbles 0 .. 3 after the byte selection)
+        uint32_t w[4][NG];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          lds_words<NG>(vb + (uint32_t)((row0 + 2 * t + (k & 1) + 8 * (k >> 1)) * (D / 2) + (g >> 1) * (D / 8)), w[k]);
+        const uint32_t sel = g & 1 ? 0x7531u : 0x6420u;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const uint32_t pa[4] = {pack_bf16x2(sc[0][0] * vsc[0][0][i], sc[0][1] * vsc[0][1][i]),
+                                  pack_bf16x2(sc[0][2] * vsc[0][0][i], sc[0][3] * vsc[0][1][i]),
+                                  pack_bf16x2(sc[1][0] * vsc[1][0][i], sc[1][1] * vsc[1][1][i]),
+                                  pack_bf16x2(sc[1][2] * vsc[1][0][i], sc[1][3] * vsc[1][1][i])};
+          const uint32_t x0 = __byte_perm(w[0][i], w[1][i], sel), x1 = __byte_perm(w[2][i], w[3][i], sel);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma16816(o[4 * i + k], pa, code_pair(x0, k), code_pair(x1, k));
+        }
+      } else {
+        const uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
+                                pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
+        const int mi = lane >> 3;
+        const int row = row0 + (lane & 7) + ((mi & 1) << 3);
+        // rows that are not seen count as zeros, whatever they hold (0 x NaN is NaN)
+        const bool whole = t0 >= vlo && t0 + 16 <= vhi;
+        const uint32_t k0 = (on[0][0] ? 0xffffu : 0u) | (on[0][1] ? 0xffff0000u : 0u);
+        const uint32_t k1 = (on[1][0] ? 0xffffu : 0u) | (on[1][1] ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(row_unit<D>(vb, row, 2 * i + (mi >> 1)), b0, b1, b2, b3);
+          if (!whole) {
+            b0 &= k0;
+            b1 &= k1;
+            b2 &= k0;
+            b3 &= k1;
+          }
+          mma16816(o[2 * i], pa, b0, b1);
+          mma16816(o[2 * i + 1], pa, b2, b3);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.empty[st]);
+  }
+}
+
+template <int D, bool Q4>
+__global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
+                                                               const __grid_constant__ CUtensorMap tv,
+                                                               const __grid_constant__ DParams p) {
+  using C = Cfg<D, Q4>;
+  namespace cg = cooperative_groups;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars bars;
+  __shared__ int abort_flag;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x, ranks = gridDim.x;          // the cluster spans the grid's x
+  const int s = blockIdx.z, hk = blockIdx.y / p.head_groups, hg = blockIdx.y % p.head_groups;
+  const int h0 = hk * p.group + hg * kQ;
+  const int n_q = min(kQ, p.group - hg * kQ);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float kNegInf = __int_as_float(0xff800000);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], kWarps);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const Rows r = Rows::of<Q4>(p, s, rank, ranks);
+  float o[C::NT][4];
+  float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  if (warp == kWarps) {
+    if (lane == 0) producer<D, Q4>(p, &tk, &tv, bars, ring, r, s, hk, &abort_flag);
+    __syncwarp();
+  } else {
+    consumer<D, Q4>(p, bars, ring, r, s, h0, n_q, o, m, l, &abort_flag);
+  }
+  __syncthreads();                                          // the ring is free
+  // ---- the warps' partial results: O [warp][query][D], maxima and sums
+  float* wo = reinterpret_cast<float*>(ring);
+  float* wm = wo + kWarps * kQ * D;
+  float* wl = wm + kWarps * kQ;
+  if (warp < kWarps) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const int row = g + 8 * h;
+      if (row < n_q) {
+        if (t == 0) {
+          wm[warp * kQ + row] = m[h];
+          wl[warp * kQ + row] = l[h];
+        }
+        float* dst = wo + (warp * kQ + row) * D;
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // column 2 t + e of n-tile i; 4-bit: element 32 (i / 4) + 4 (2 t + e) + {0, 2, 1, 3}[i % 4]
+            const int k = i & 3;
+            const int at = Q4 ? 32 * (i >> 2) + 4 * (2 * t + e) + (k == 1 ? 2 : (k == 2 ? 1 : k)) : 8 * i + 2 * t + e;
+            dst[at] = o[i][2 * h + e];
+          }
+      }
+    }
+  }
+  __syncthreads();
+  // ---- one partial result per CTA, in warp 0's place
+  for (int at = threadIdx.x; at < n_q * D; at += kThreads) {
+    const int row = at / D, col = at % D;
+    float M = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * kQ + row]);
+    float sum = 0.f;
+    if (M != kNegInf) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += wo[(w * kQ + row) * D + col] * ex2_approx(wm[w * kQ + row] - M);
+    }
+    wo[row * D + col] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < n_q) {
+    const int row = threadIdx.x;
+    float M = kNegInf, L = 0.f;
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * kQ + row]);
+    if (M != kNegInf)
+      for (int w = 0; w < kWarps; ++w) L += wl[w * kQ + row] * ex2_approx(wm[w * kQ + row] - M);
+    wm[row] = M;
+    wl[row] = L;
+  }
+  cluster.sync();
+  // ---- the cluster's CTAs join their results: CTA `rank` writes its share of the elements
+  const int pairs = n_q * (D / 2);
+  const int p0 = (int)((int64_t)pairs * rank / ranks), p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
+  for (int at = p0 + threadIdx.x; at < p1; at += kThreads) {
+    const int row = at / (D / 2), col = 2 * (at % (D / 2));
+    float M = kNegInf;
+    for (int k = 0; k < ranks; ++k) M = fmaxf(M, *cluster.map_shared_rank(wm + row, k));
+    float x = 0.f, y = 0.f, L = 0.f;
+    if (M != kNegInf) {
+      for (int k = 0; k < ranks; ++k) {
+        const float a = ex2_approx(*cluster.map_shared_rank(wm + row, k) - M);
+        const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + row * D + col, k));
+        x = fmaf(a, v.x, x);
+        y = fmaf(a, v.y, y);
+        L = fmaf(a, *cluster.map_shared_rank(wl + row, k), L);
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    *reinterpret_cast<uint32_t*>(p.o + (int64_t)s * p.o_sb + (int64_t)(h0 + row) * p.o_sh + col) =
+        pack_bf16x2(x * inv, y * inv);
+    if (col == 0)
+      p.lse[(int64_t)s * p.heads + h0 + row] = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : kNegInf;
+  }
+  cluster.sync();                                           // no CTA leaves while another reads its results
+}
+
+template <int D, bool Q4>
+int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, Q4>;
+  CUtensorMap tk, tv;
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
+  if (!Q4 &&
+      (!encode_bhnd_map(&tk, a.k, a.batch, a.capacity, a.kv_heads, D, a.k_strides[0], a.k_strides[1], a.k_strides[2],
+                        C::CH, 16, C::TMA_SWZ) ||
+       !encode_bhnd_map(&tv, a.v, a.batch, a.capacity, a.kv_heads, D, a.v_strides[0], a.v_strides[1], a.v_strides[2],
+                        C::CH, 16, C::TMA_SWZ)))
+    return SA_ERR_UNSUPPORTED;
+  DParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.lengths = a.lengths;
+  if (Q4) {
+    p.kc = static_cast<const uint8_t*>(a.k);
+    p.ks = static_cast<const __nv_bfloat16*>(a.k_scales);
+    p.vc = static_cast<const uint8_t*>(a.v);
+    p.vs = static_cast<const __nv_bfloat16*>(a.v_scales);
+  }
+  p.q_sb = a.q_strides[0];
+  p.q_sh = a.q_strides[2];
+  p.o_sb = a.o_strides[0];
+  p.o_sh = a.o_strides[2];
+  p.heads = a.heads;
+  p.kv_heads = a.kv_heads;
+  p.group = a.heads / a.kv_heads;
+  p.head_groups = (p.group + kQ - 1) / kQ;
+  p.capacity = a.capacity;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  const auto kern = sink_decode_kernel<D, Q4>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return SA_ERR_CUDA;
+  // CTAs per (sequence, key head): enough for two per SM, while each has two stages of rows or
+  // more when the cache is full
+  const int64_t base = (int64_t)a.batch * a.kv_heads * p.head_groups;
+  const int64_t seen = (int64_t)a.window + 1 + a.sinks < a.capacity ? (int64_t)a.window + 1 + a.sinks : a.capacity;
+  const int sm_count = current_sm_count();
+  int ranks = 1;
+  while (ranks < kMaxCluster && base * ranks < 2 * sm_count && seen >= 4 * kRows * ranks) ranks *= 2;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)ranks, (unsigned)(a.kv_heads * p.head_groups), (unsigned)a.batch);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ranks;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, p) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_sink_decode(const SinkDecodeArgs& a, cudaStream_t stream) {
+  switch (a.head_dim) {
+    case 32: return a.cache4 ? launch<32, true>(a, stream) : launch<32, false>(a, stream);
+    case 64: return a.cache4 ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+    case 128: return a.cache4 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+  }
+  return SA_ERR_UNSUPPORTED;
+}
+
+unsigned int decode_read_and_clear_error(cudaStream_t stream) {
+  unsigned int v = 0, zero = 0;
+  cudaMemcpyFromSymbolAsync(&v, g_decode_err, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+  cudaMemcpyToSymbolAsync(g_decode_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+  cudaStreamSynchronize(stream);
+  return v;
+}
+
+}  // namespace sa

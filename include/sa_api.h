@@ -332,6 +332,124 @@ int sa_build_mask_from_bytes(const sa_mask_params* params, const uint8_t* h_byte
                              int32_t n_threads, float* h_ratio, float* d_ratio, int32_t* d_row_ptr,
                              int32_t* d_col_idx, int64_t col_capacity, void* stream);
 
+/* ---------------------------------------------------------------- streaming attention
+ *
+ * The sink-window graph: query i sees key j iff j <= i and (i - j <= window or j < sinks), a dense
+ * causal window (window >= 0; the diagonal and `window` keys before it, as in the offset calls)
+ * and the first `sinks` tokens (0 .. 128), which stay visible to every later query. A window of
+ * n_tokens - 1 or more is the full causal graph. The calls below prepare queries and keys for it,
+ * train through it, and decode over a cache of bf16 rows or of 4-bit codes.
+ *
+ * q, k, v and d_o are expected to be finite: as in sa_attn_fwd, a non-finite row reaches the
+ * queries whose 128-query tile meets it. (The decoding calls ignore whatever stands in rows that
+ * the query does not see.) None of these calls uses the legacy default stream or memory of its
+ * own; calls on several streams need separate workspaces where a call takes one. */
+
+/* RMS norm of every query and key head and the position rotation, in one pass. Per row x (one
+ * token's head) of q or k: y = x / sqrt(mean(x^2) + eps) * weight, then each pair (a, b) of the first
+ * rotary_dim elements becomes (a cos t - b sin t, b cos t + a sin t), t = position * h_inv_freq[pair].
+ *   q [batch, n_tokens, heads, head_dim], k [batch, n_tokens, kv_heads, head_dim], bf16 with
+ *   q_strides / k_strides; q_out, k_out likewise (a call may write over its own inputs: the same
+ *   pointer and strides). Statistics and rotation in fp32, one rounding to bf16. heads need not be
+ *   a multiple of kv_heads here.
+ *   d_q_weight, d_k_weight : fp32 [head_dim], or NULL for ones.
+ *   eps > 0.
+ *   h_inv_freq : host array of rotary_dim / 2 frequencies, radians per position, 0 <= f < 6.28,
+ *                read before the call returns. rotary_dim: a multiple of 16, 0 .. head_dim (0: no
+ *                rotation, h_inv_freq may be NULL); later elements are normed only.
+ *   interleaved: 0 pairs element p with p + rotary_dim / 2, 1 pairs 2p with 2p + 1.
+ *   d_positions: int32 [batch][n_tokens], any values, or NULL for 0 .. n_tokens - 1. */
+int sa_qk_norm_rope_fwd(const void* q, const void* k, const int64_t q_strides[3], const int64_t k_strides[3],
+                        int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                        const float* d_q_weight, const float* d_k_weight, float eps, const double* h_inv_freq,
+                        int32_t rotary_dim, int32_t interleaved, const int32_t* d_positions, void* q_out, void* k_out,
+                        const int64_t q_out_strides[3], const int64_t k_out_strides[3], void* stream);
+
+/* Workspace bytes of sa_qk_norm_rope_bwd (partial weight gradients). Host only. */
+int sa_qk_norm_rope_bwd_workspace_size(int32_t head_dim, size_t* h_bytes);
+
+/* Gradients of sa_qk_norm_rope_fwd from its inputs q and k and the gradients d_q_out, d_k_out of its
+ * outputs: dq, dk (bf16; may be written over d_q_out, d_k_out) and the weights' gradients
+ * d_dq_weight, d_dk_weight (fp32 [head_dim], summed over all rows of q or k in a fixed order; NULL: not
+ * wanted). Other arguments as in the forward. workspace: device memory, 256-byte aligned, of at
+ * least sa_qk_norm_rope_bwd_workspace_size bytes. */
+int sa_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out, const void* d_k_out,
+                        const int64_t q_strides[3], const int64_t k_strides[3], const int64_t d_q_out_strides[3],
+                        const int64_t d_k_out_strides[3], int32_t batch, int32_t n_tokens, int32_t heads,
+                        int32_t kv_heads, int32_t head_dim, const float* d_q_weight, const float* d_k_weight, float eps,
+                        const double* h_inv_freq, int32_t rotary_dim, int32_t interleaved, const int32_t* d_positions,
+                        void* dq, void* dk, const int64_t dq_strides[3], const int64_t dk_strides[3],
+                        float* d_dq_weight, float* d_dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention over the sink-window graph, forward. Shapes, strides, O and LSE as in sa_attn_fwd
+ * (head_dim 32, 64 or 128), any n_tokens from 1 to 2^24; k and v have strides of
+ * their own. */
+int sa_sink_attn_fwd(const void* q, const void* k, const void* v, const int64_t q_strides[3],
+                     const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3], int32_t batch,
+                     int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t window,
+                     int32_t sinks, float softmax_scale, void* o, float* lse, void* stream);
+
+/* Workspace bytes of sa_sink_attn_bwd. Host only. */
+int sa_sink_attn_bwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                    int32_t window, int32_t sinks, size_t* h_bytes);
+
+/* Gradients dq, dk, dv of sum(d_o * o) of sa_sink_attn_fwd (formulas as in sa_attn_bwd), from its
+ * inputs and its outputs o and lse. Every tensor has strides of its own. The same bits on every run.
+ * workspace: device memory, 256-byte aligned, of at least sa_sink_attn_bwd_workspace_size bytes. */
+int sa_sink_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* d_o, const float* lse,
+                     const int64_t q_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
+                     const int64_t o_strides[3], const int64_t d_o_strides[3], int32_t batch, int32_t n_tokens,
+                     int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t window, int32_t sinks,
+                     float softmax_scale, void* dq, void* dk, void* dv, const int64_t dq_strides[3],
+                     const int64_t dk_strides[3], const int64_t dv_strides[3], void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* The single-token form: one query per sequence, which is token d_lengths[s] - 1 of it, over a cache.
+ *   q, o : bf16 [batch, 1, heads, head_dim] (strides {batch, token, head}; the token stride is not
+ *          used), lse fp32 [batch][heads].
+ *   k_cache, v_cache : bf16 [batch, capacity, kv_heads, head_dim]; rows that the
+ *          query does not see may hold anything.
+ *   d_lengths : int32 [batch] on the device, tokens in each sequence's cache, the query's own key
+ *          among them; values are taken into 0 .. capacity. Length 0: o = 0, lse = -inf.
+ * One launch without workspace. capacity <= 2^30. */
+int sa_sink_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int64_t q_strides[3],
+                        const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3],
+                        int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                        const int32_t* d_lengths, int32_t window, int32_t sinks, float softmax_scale, void* o,
+                        float* lse, void* stream);
+
+/* A cache in 4 bits. For every (sequence, key head, token) a row of codes and scales, contiguous:
+ *   codes  uint8 [batch][kv_heads][capacity][head_dim / 2], scales bf16 [batch][kv_heads][capacity][head_dim / 32]
+ * for keys and for values. Each run of 32 elements has the scale s = bf16(amax / 7) and codes
+ * round(x / s) in -7 .. 7 (ties to even), stored + 8; an element reads back as code * s. In a row the
+ * little-endian 32-bit word t * (head_dim / 32) + c holds elements 32 c + 8 t + u, u = 0 .. 7, element
+ * u = 4 p + i at bit 8 p + 4 (i / 2) + 16 (i % 2). A run that holds an infinity or a NaN reads back as
+ * NaN. capacity is a multiple of 8; the four arrays are 16-byte aligned.
+ *
+ * sa_cache4_append writes rows d_start[s] .. d_start[s] + n_tokens - 1 of every sequence from k and v
+ * (bf16 [batch, n_tokens, kv_heads, head_dim]). d_start: int32 [batch] on the
+ * device, or NULL for 0; a sequence with a negative start is left out. Rows at or past the capacity
+ * are not written and reported as SA_ERR_DEVICE by sa_device_status. Other rows keep their contents. */
+int sa_cache4_append(const void* k, const void* v, const int64_t k_strides[3], const int64_t v_strides[3],
+                     int32_t batch, int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity,
+                     const int32_t* d_start, uint8_t* k_codes, void* k_scales, uint8_t* v_codes, void* v_scales,
+                     void* stream);
+
+/* The rows d_start[s] .. d_start[s] + n_tokens - 1 of the cache as bf16 (code * scale, rounded once) into
+ * k and v, for example for a later chunk of a prompt that attends to them. Rows of a left-out sequence
+ * and rows at or past the capacity (reported as by sa_cache4_append) come back as zeros. */
+int sa_cache4_read(const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes, const void* v_scales,
+                   int32_t batch, int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity,
+                   const int32_t* d_start, void* k, void* v, const int64_t k_strides[3], const int64_t v_strides[3],
+                   void* stream);
+
+/* sa_sink_attn_decode over a 4-bit cache: the same attention over the values the codes stand for. */
+int sa_sink_attn_decode_cache4(const void* q, const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes,
+                               const void* v_scales, const int64_t q_strides[3], const int64_t o_strides[3],
+                               int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                               const int32_t* d_lengths, int32_t window, int32_t sinks, float softmax_scale, void* o,
+                               float* lse, void* stream);
+
 /* Synchronises `stream`, then reads and clears the library's device error words.
  * Returns SA_OK, SA_ERR_TIMEOUT (a bounded wait expired; the kernel unwound and its
  * outputs are undefined), SA_ERR_DEVICE (invalid CSR data was skipped) or

@@ -1,0 +1,463 @@
+"""Streaming attention on the GPU against float64 (oracle/streaming.py): norm and rotation, the
+sink-window graph forward and backward, single tokens over bf16 and 4-bit caches, and a run of
+them together. Tolerances are the oracle's elementwise bounds."""
+import numpy as np
+import pytest
+
+import content_adaptive_sparse_gb300 as sa
+from gpu_helpers import bf16_to_f64, torch_cuda
+from oracle import streaming as ref
+
+pytestmark = pytest.mark.gpu
+
+# LSE in fp32: scores of |s| <= about 20 carry a few 2^-24 of sum |q k|, the exponentials and the
+# logarithm 2^-22 each; 1e-4 is an order of magnitude above their sum
+LSE_TOL = 1e-4
+
+
+def rand(seed, *shape, scale=1.0):
+    """bf16 CUDA tensor and its float64 values."""
+    torch = torch_cuda()
+    x = (torch.from_numpy(np.random.default_rng(seed).standard_normal(shape) * scale)).to(torch.bfloat16).cuda()
+    return x, bf16_to_f64(x)
+
+
+def close(got, want, bound, what):
+    got = got.detach().double().cpu().numpy() if not isinstance(got, np.ndarray) else got
+    assert got.shape == want.shape, what
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    over = np.abs(got - want) - bound
+    at = np.unravel_index(np.argmax(over), over.shape)
+    assert over[at] <= 0, f"{what}: {got[at]} against {want[at]}, bound {np.broadcast_to(bound, want.shape)[at]} at {at}"
+
+
+def status_ok():
+    torch_cuda().cuda.synchronize()
+    assert sa.sa_device_status() == 0
+
+
+# ------------------------------------------------------------------ sink-window attention
+
+SINK_CASES = [
+    # batch, tokens, heads, kv_heads, dim, window, sinks
+    (1, 1, 1, 1, 32, 0, 0), (1, 1, 2, 1, 64, 5, 4), (1, 2, 2, 2, 128, 0, 1),
+    (2, 31, 2, 1, 64, 7, 3), (1, 33, 4, 2, 128, 0, 0), (1, 127, 2, 2, 32, 31, 32), (2, 128, 2, 1, 64, 32, 33),
+    (1, 129, 2, 2, 128, 33, 1), (1, 300, 4, 1, 64, 64, 4), (1, 300, 2, 2, 128, 100, 17), (2, 257, 6, 3, 32, 128, 5),
+    (1, 640, 2, 1, 64, 0, 128), (1, 640, 2, 1, 128, 1, 127), (1, 641, 3, 3, 32, 255, 0), (1, 500, 2, 1, 64, 499, 4),
+    (1, 500, 2, 1, 128, 100000, 4), (1, 1500, 2, 1, 64, 127, 4), (1, 1411, 4, 2, 128, 200, 9), (3, 200, 5, 5, 64, 96, 64),
+    (1, 2900, 1, 1, 32, 3, 100),
+]
+
+
+@pytest.mark.parametrize("b,n,h,hk,d,w,s", SINK_CASES)
+def test_sink_attention_forward_and_backward(b, n, h, hk, d, w, s):
+    (q, qf), (k, kf), (v, vf), (g, gf) = (rand(i, b, n, x, d) for i, x in enumerate((h, hk, hk, h)))
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    status_ok()
+    of, lf, ob = ref.sink_attention(qf, kf, vf, w, s)
+    close(o, of, ob, "o")
+    close(lse, lf, LSE_TOL, "lse")
+    grads = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    want, bounds = ref.sink_attention_backward(qf, kf, vf, gf, w, s)
+    for name, x, y, e in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(x, y, e, name)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sink_attention_large_scores(d):
+    """Scores of hundreds that grow along the sequence: the running maximum is rescaled often."""
+    n, w, s = 400, 90, 6
+    (q, qf), (k, kf), (v, vf) = rand(0, 1, n, 2, d, scale=6.0), rand(1, 1, n, 1, d, scale=6.0), rand(2, 1, n, 1, d)
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    status_ok()
+    of, lf, ob = ref.sink_attention(qf, kf, vf, w, s)
+    # |s| up to 400: fp32 scores are off by up to about 400 x 2^-20, and so is ln P
+    close(o, of, ob + 8e-4 * np.abs(vf).max(), "o")
+    close(lse, lf, 4e-4, "lse")
+
+
+def test_sink_attention_strided_scaled_and_repeated():
+    """Packed Q/K/V views, outputs and gradients with strides of their own, an explicit scale; the
+    backward gives the same bits twice."""
+    torch = torch_cuda()
+    b, n, h, hk, d, w, s = 2, 333, 4, 2, 64, 75, 5
+    packed, pf = rand(3, b, n, h + 2 * hk, d)
+    q, k, v = packed[:, :, :h], packed[:, :, h:h + hk], packed[:, :, h + hk:]
+    qf, kf, vf = pf[:, :, :h], pf[:, :, h:h + hk], pf[:, :, h + hk:]
+    wide_g, wgf = rand(4, b, n, 2 * h, d)
+    g, gf = wide_g[:, :, h:], wgf[:, :, h:]
+    o = torch.empty(b, n, 2, h, d, dtype=torch.bfloat16, device="cuda")[:, :, 1]
+    lse = torch.empty(b, h, n, dtype=torch.float32, device="cuda")
+    sa.sa_sink_attn_fwd(q, k, v, w, s, o, lse, softmax_scale=0.2)
+    of, lf, ob = ref.sink_attention(qf, kf, vf, w, s, scale=0.2)
+    status_ok()
+    close(o, of, ob, "o")
+    close(lse, lf, LSE_TOL, "lse")
+    dpacked = torch.full_like(packed, 7.0)
+    dq, dk, dv = dpacked[:, :, :h], dpacked[:, :, h:h + hk], dpacked[:, :, h + hk:]
+    ws = torch.empty(sa.sa_sink_attn_bwd_workspace_size(b, n, h, hk, d, w, s), dtype=torch.uint8, device="cuda")
+    sa.sa_sink_attn_bwd(q, k, v, o, g, lse, w, s, dq, dk, dv, ws, softmax_scale=0.2)
+    status_ok()
+    want, bounds = ref.sink_attention_backward(qf, kf, vf, gf, w, s, scale=0.2)
+    for name, x, y, e in zip(("dq", "dk", "dv"), (dq, dk, dv), want, bounds):
+        close(x, y, e, name)
+    first = dpacked.clone()
+    ws.fill_(0xff)
+    sa.sa_sink_attn_bwd(q, k, v, o, g, lse, w, s, dq, dk, dv, ws, softmax_scale=0.2)
+    status_ok()
+    assert torch.equal(first.view(torch.int16), dpacked.view(torch.int16))
+
+
+# ------------------------------------------------------------------ single tokens over a cache
+
+DECODE_CASES = [
+    # heads, kv_heads, dim, capacity, window, sinks, lengths
+    (1, 1, 32, 8, 0, 0, [1]), (2, 1, 64, 16, 3, 2, [0, 1, 16]), (4, 4, 128, 64, 100, 4, [64, 63, 1]),
+    (8, 2, 64, 72, 16, 16, [72, 40, 17, 16]), (16, 1, 128, 200, 50, 33, [200, 84, 51, 3]), (20, 1, 64, 136, 65, 1, [136, 5]),
+    (40, 2, 32, 264, 500, 0, [264, 130]), (6, 3, 128, 1000, 700, 128, [1000, 900, 701, 128]),
+    (4, 1, 64, 4096, 4095, 4, [4096, 4001, 2]), (2, 2, 32, 6000, 3000, 70, [5999, 3071, 3001, 10]),
+    (5, 5, 128, 2048, 1, 65, [2000]), (12, 12, 64, 520, 511, 4, [7, 520, 519]),
+]
+
+
+@pytest.mark.parametrize("h,hk,d,cap,w,s,lengths", DECODE_CASES)
+def test_decode_over_a_bf16_cache(h, hk, d, cap, w, s, lengths):
+    """Rows that the query does not see hold NaN and infinities."""
+    torch = torch_cuda()
+    b = len(lengths)
+    q, qf = rand(0, b, 1, h, d)
+    k, kf = rand(1, b, cap, hk, d)
+    v, vf = rand(2, b, cap, hk, d)
+    for i, n in enumerate(lengths):
+        j = torch.arange(cap, device="cuda")
+        unseen = (j >= n) | ((n - 1 - j > w) & (j >= s))
+        k[i, unseen] = float("nan")
+        v[i, unseen] = float("inf")
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    o, lse = sa.sink_attn_decode(q, k, v, n, w, s)
+    status_ok()
+    of, lf, ob = ref.sink_decode(qf, kf, vf, lengths, w, s)
+    close(o, of, ob, "o")
+    lse = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(lse), np.isneginf(lf))
+    some = ~np.isneginf(lf)
+    close(lse[some], lf[some], LSE_TOL, "lse")
+
+
+@pytest.mark.parametrize("h,hk,d,cap,w,s,lengths", DECODE_CASES)
+def test_decode_over_a_4_bit_cache(h, hk, d, cap, w, s, lengths):
+    """The rows are written by the append; rows that are not seen hold random codes and NaN scales."""
+    torch = torch_cuda()
+    b = len(lengths)
+    q, qf = rand(0, b, 1, h, d)
+    k, kf = rand(1, b, cap, hk, d)
+    v, vf = rand(2, b, cap, hk, d, scale=3.0)
+    cache = sa.cache4_alloc(b, cap, hk, d)
+    sa.cache4_append(cache, k, v)
+    j = torch.arange(cap, device="cuda")
+    for i, n in enumerate(lengths):
+        unseen = (j >= n) | ((n - 1 - j > w) & (j >= s))
+        cache.k_codes[i][:, unseen] = 255
+        cache.v_codes[i][:, unseen] = 0
+        cache.k_scales[i][:, unseen] = float("nan")
+        cache.v_scales[i][:, unseen] = float("nan")
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    o, lse = sa.sink_attn_decode_cache4(q, cache, n, w, s)
+    status_ok()
+    kq, vq = (ref.values(*ref.quantise(x)) for x in (kf, vf))
+    of, lf, ob = ref.sink_decode(qf, kq, vq, lengths, w, s)
+    close(o, of, ob, "o")
+    lse = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(lse), np.isneginf(lf))
+    some = ~np.isneginf(lf)
+    close(lse[some], lf[some], LSE_TOL, "lse")
+
+
+def test_decode_lengths_outside_the_cache_are_cut():
+    torch = torch_cuda()
+    q, qf = rand(0, 3, 1, 4, 64)
+    k, kf = rand(1, 3, 40, 2, 64)
+    v, vf = rand(2, 3, 40, 2, 64)
+    n = torch.tensor([-5, 1000, 40], dtype=torch.int32, device="cuda")
+    o, lse = sa.sink_attn_decode(q, k, v, n, 20, 3)
+    status_ok()
+    of, lf, ob = ref.sink_decode(qf, kf, vf, [0, 40, 40], 20, 3)
+    close(o, of, ob, "o")
+    close(lse[1:], lf[1:], LSE_TOL, "lse")
+    assert torch.isneginf(lse[0]).all() and not o[0].any()
+
+
+def test_decode_strided_cache_and_large_scores():
+    """Keys and values interleaved in one buffer, queries from a packed projection."""
+    torch = torch_cuda()
+    b, h, hk, d, cap = 2, 8, 2, 128, 300
+    kv, kvf = rand(1, b, cap, 2 * hk, d, scale=4.0)
+    packed, pf = rand(0, b, 1, h + 2 * hk, d, scale=4.0)
+    q, qf = packed[:, :, :h], pf[:, :, :h]
+    n = torch.tensor([300, 211], dtype=torch.int32, device="cuda")
+    o, lse = sa.sink_attn_decode(q, kv[:, :, :hk], kv[:, :, hk:], n, 150, 4)
+    status_ok()
+    of, lf, ob = ref.sink_decode(qf, kvf[:, :, :hk], kvf[:, :, hk:], [300, 211], 150, 4)
+    close(o, of, ob + 4e-4 * np.abs(kvf).max(), "o")
+    close(lse, lf, 4e-4, "lse")
+
+
+# ------------------------------------------------------------------ 4-bit cache
+
+@pytest.mark.parametrize("b,n,hk,d,cap,start", [(1, 1, 1, 32, 8, [7]), (2, 5, 3, 64, 16, [0, 11]), (3, 70, 2, 128, 96, [3, 26, 9]),
+                                                (1, 333, 4, 32, 1000, [600]), (2, 129, 1, 64, 136, None)])
+def test_cache4_rows(b, n, hk, d, cap, start):
+    """Codes, scales, what they read back as, and the other rows untouched; a run of zeros, one of a
+    single subnormal, one of the largest magnitudes."""
+    torch = torch_cuda()
+    k, _ = rand(1, b, n, hk, d)
+    v, _ = rand(2, b, n, hk, d, scale=100.0)
+    k[0, 0, 0, :32] = 0.0
+    v[0, 0, 0, :32] = torch.tensor([1e-39] + [0.0] * 31)
+    v[0, n - 1, hk - 1, -32:] = 3.0e38 * torch.linspace(-1, 1, 32)
+    kf, vf = bf16_to_f64(k), bf16_to_f64(v)
+    cache = sa.cache4_alloc(b, cap, hk, d)
+    for x in cache:
+        x.view(torch.uint8).fill_(0x5a)
+    at = None if start is None else torch.tensor(start, dtype=torch.int32, device="cuda")
+    sa.cache4_append(cache, k, v, at)
+    k2, v2 = sa.cache4_read(cache, at, n)
+    status_ok()
+    for x, codes, scales, back in ((kf, cache.k_codes, cache.k_scales, k2), (vf, cache.v_codes, cache.v_scales, v2)):
+        c, s = ref.quantise(x)
+        assert np.array_equal(bf16_to_f64(back), ref.bf16_round(ref.values(c, s)))
+        codes, scales = codes.cpu().numpy(), bf16_to_f64(scales)
+        packed = ref.pack(c)
+        for i in range(b):
+            lo = 0 if start is None else start[i]
+            assert np.array_equal(codes[i, :, lo:lo + n], packed[i].transpose(1, 0, 2))
+            assert np.array_equal(scales[i, :, lo:lo + n], s[i].transpose(1, 0, 2))
+            other = np.delete(codes[i], np.arange(lo, lo + n), axis=1)
+            assert np.all(other == 0x5a)
+
+
+def test_cache4_left_out_and_overfull_sequences():
+    torch = torch_cuda()
+    b, n, hk, d, cap = 3, 6, 2, 64, 16
+    (k, kf), (v, vf) = rand(1, b, n, hk, d), rand(2, b, n, hk, d)
+    k[1, 2, 0, 3] = float("inf")
+    k[1, 3, 1, 40] = float("nan")
+    cache = sa.cache4_alloc(b, cap, hk, d)
+    for x in cache:
+        x.zero_()
+    start = torch.tensor([-1, 4, 12], dtype=torch.int32, device="cuda")
+    sa.cache4_append(cache, k, v, start)
+    torch.cuda.synchronize()
+    assert sa.sa_device_status() == -6                    # two rows of the third sequence did not fit
+    assert not cache.k_codes[0].any() and not cache.v_scales[0].any()
+    k2, v2 = sa.cache4_read(cache, start, n)
+    torch.cuda.synchronize()
+    assert sa.sa_device_status() == -6
+    assert not k2[0].any() and not v2[0].any() and not k2[2, 4:].any()
+    assert np.array_equal(bf16_to_f64(k2[2, :4]), ref.bf16_round(ref.values(*ref.quantise(kf[2, :4]))))
+    nan = torch.isnan(k2[1])
+    assert nan[2, 0, :32].all() and nan[3, 1, 32:].all() and int(nan.sum()) == 64
+    assert np.array_equal(bf16_to_f64(v2[1]), ref.bf16_round(ref.values(*ref.quantise(vf[1]))))
+
+
+# ------------------------------------------------------------------ norm and rotation
+
+ROPE_CASES = [
+    # batch, tokens, heads, kv_heads, dim, rotary, interleaved, weights, positions
+    (1, 1, 1, 1, 32, 32, False, True, None), (2, 3, 5, 2, 64, 64, False, True, "far"), (1, 7, 4, 4, 128, 128, True, True, "far"),
+    (1, 40, 3, 1, 128, 64, False, False, None), (2, 33, 12, 12, 64, 32, True, True, "far"), (1, 129, 2, 1, 32, 16, False, True, "negative"),
+    (1, 5, 9, 1, 64, 0, False, True, None), (3, 1, 16, 4, 128, 128, False, True, "far"), (2, 700, 6, 2, 32, 32, True, False, "far"),
+]
+
+
+@pytest.mark.parametrize("b,n,h,hk,d,rotary,inter,weights,where", ROPE_CASES)
+def test_norm_rope_forward_and_backward(b, n, h, hk, d, rotary, inter, weights, where):
+    torch = torch_cuda()
+    rng = np.random.default_rng(5)
+    packed, pf = rand(0, b, n, h + 2 * hk, d)
+    packed[0, 0, 0] = 0.0                                  # a row of zeros
+    pf[0, 0, 0] = 0.0
+    q, k, qf, kf = packed[:, :, :h], packed[:, :, h:h + hk], pf[:, :, :h], pf[:, :, h:h + hk]
+    (gq, gqf), (gk, gkf) = rand(1, b, n, h, d), rand(2, b, n, hk, d)
+    w = [np.float32(1 + 0.2 * rng.standard_normal(d)) if weights else np.ones(d, np.float32) for _ in range(2)]
+    wt = [torch.from_numpy(x).cuda() if weights else None for x in w]
+    freq = 10000.0 ** (-2.0 * np.arange(rotary // 2) / max(rotary, 1))
+    pos = np.broadcast_to(np.arange(n), (b, n))
+    if where:
+        pos = rng.integers(0, 1 << 30, (b, n)) if where == "far" else -rng.integers(0, 100000, (b, n))
+    pt = torch.from_numpy(pos.astype(np.int32)).cuda() if where else None
+    eps = 1e-5
+    outs = sa.qk_norm_rope_fwd(q, k, *wt, freq, pt, eps, inter)
+    status_ok()
+    for name, x, xf, wf in zip("qk", outs, (qf, kf), w):
+        y, bound = ref.norm_rope(xf, wf.astype(np.float64), pos, freq, eps, inter)
+        close(x, y, bound, name + "_out")
+    dq, dk, dqw, dkw = sa.qk_norm_rope_bwd(q, k, gq, gk, *wt, freq, pt, eps, inter)
+    status_ok()
+    for name, x, dw, xf, gf, wf in zip("qk", (dq, dk), (dqw, dkw), (qf, kf), (gqf, gkf), w):
+        (dxf, dwf), (bx, bw) = ref.norm_rope_backward(xf, wf.astype(np.float64), gf, pos, freq, eps, inter)
+        close(x, dxf, bx, "d" + name)
+        if weights:
+            close(dw, dwf, bw, "dw_" + name)
+        else:
+            assert dw is None
+    # in place, and the same bits twice
+    qc, kc = q.clone(memory_format=torch.contiguous_format), k.clone(memory_format=torch.contiguous_format)
+    sa.sa_qk_norm_rope_fwd(qc, kc, *wt, freq, pt, qc, kc, eps, inter)
+    status_ok()
+    assert torch.equal(qc, outs[0]) and torch.equal(kc, outs[1])
+    again = sa.qk_norm_rope_bwd(q, k, gq, gk, *wt, freq, pt, eps, inter)
+    for x, y in zip((dq, dk, dqw, dkw), again):
+        assert (x is None and y is None) or torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ together
+
+def _model(seed, b, n, h, hk, d):
+    packed, pf = rand(seed, b, n, h + 2 * hk, d)
+    rng = np.random.default_rng(9)
+    w = [np.float32(1 + 0.1 * rng.standard_normal(d)) for _ in range(2)]
+    freq = 10000.0 ** (-2.0 * np.arange(d // 2) / d)
+    return packed, pf, w, freq
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_then_tokens_agree_with_one_pass(d):
+    """A prompt through norm, rotation and the window, its rows into both caches, then one token at a
+    time on another stream: every token's output is the row that one pass over all tokens gives."""
+    torch = torch_cuda()
+    b, n, prompt, h, hk, w, s = 2, 90, 83, 4, 2, 40, 3
+    packed, _, wts, freq = _model(0, b, n, h, hk, d)
+    wt = [torch.from_numpy(x).cuda() for x in wts]
+    q, k, v = packed[:, :, :h], packed[:, :, h:h + hk], packed[:, :, h + hk:]
+    qr, kr = sa.qk_norm_rope_fwd(q, k, *wt, freq)
+    o, lse = sa.sink_attn_fwd(qr, kr, v, w, s)
+    status_ok()
+    qf, kf, vf = (bf16_to_f64(x) for x in (qr, kr, v))
+    of, lf, ob = ref.sink_attention(qf, kf, vf, w, s)
+    close(o, of, ob, "one pass")
+    k4, v4 = (ref.values(*ref.quantise(x)) for x in (kf, vf))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cap = 96
+        kcache = torch.full((b, cap, hk, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        vcache = torch.full_like(kcache, float("nan"))
+        kcache[:, :prompt], vcache[:, :prompt] = kr[:, :prompt], v[:, :prompt]
+        cache = sa.cache4_alloc(b, cap, hk, d)
+        sa.cache4_append(cache, kr[:, :prompt], v[:, :prompt])
+        outs, outs4 = [], []
+        for i in range(prompt, n):
+            at = torch.full((b,), i, dtype=torch.int32, device="cuda")
+            qi, ki = sa.qk_norm_rope_fwd(q[:, i:i + 1], k[:, i:i + 1], *wt, freq, at[:, None])
+            kcache[:, i], vcache[:, i] = ki[:, 0], v[:, i]
+            sa.cache4_append(cache, ki, v[:, i:i + 1], at)
+            outs.append(sa.sink_attn_decode(qi, kcache, vcache, at + 1, w, s))
+            outs4.append(sa.sink_attn_decode_cache4(qi, cache, at + 1, w, s))
+    side.synchronize()
+    assert sa.sa_device_status(side) == 0
+    o4, l4, ob4 = ref.sink_attention(qf, k4, v4, w, s)
+    for got, want, bound, lw in ((outs, of, ob, lf), (outs4, o4, ob4, l4)):
+        close(torch.cat([x[0] for x in got], 1), want[:, prompt:], bound[:, prompt:], "tokens")
+        close(torch.cat([x[1] for x in got], 2), lw[:, :, prompt:], LSE_TOL, "tokens' lse")
+
+
+def test_training_chain_against_differences():
+    """Norm, rotation and attention with their gradients chained, against the float64 chain's
+    differences along random directions."""
+    torch = torch_cuda()
+    b, n, h, hk, d, w, s = 1, 150, 4, 2, 64, 30, 3
+    packed, pf, wts, freq = _model(1, b, n, h, hk, d)
+    wt = [torch.from_numpy(x).cuda() for x in wts]
+    g, gf = rand(7, b, n, h, d)
+    q, k, v = packed[:, :, :h], packed[:, :, h:h + hk], packed[:, :, h + hk:]
+    qr, kr = sa.qk_norm_rope_fwd(q, k, *wt, freq)
+    o, lse = sa.sink_attn_fwd(qr, kr, v, w, s)
+    dqr, dkr, dv = sa.sink_attn_bwd(qr, kr, v, o, lse, g, w, s)
+    dq, dk, dqw, dkw = sa.qk_norm_rope_bwd(q, k, dqr, dkr, *wt, freq)
+    status_ok()
+    pos = np.arange(n)[None]
+
+    def loss(x, wq, wk):
+        a, _ = ref.norm_rope(x[:, :, :h], wq, pos, freq, 1e-6, False)
+        c, _ = ref.norm_rope(x[:, :, h:h + hk], wk, pos, freq, 1e-6, False)
+        return (ref.sink_attention(a, c, x[:, :, h + hk:], w, s)[0] * gf).sum()
+
+    grad = np.concatenate([bf16_to_f64(x) for x in (dq, dk, dv)], axis=2)
+    gw = [x.double().cpu().numpy() for x in (dqw, dkw)]
+    rng = np.random.default_rng(11)
+    for trial in range(4):
+        dx, dwq, dwk = rng.standard_normal(pf.shape), rng.standard_normal(d), rng.standard_normal(d)
+        e = 1e-5
+        w64 = [x.astype(np.float64) for x in wts]
+        num = (loss(pf + e * dx, w64[0] + e * dwq, w64[1] + e * dwk) - loss(pf - e * dx, w64[0] - e * dwq, w64[1] - e * dwk)) / (2 * e)
+        got = (grad * dx).sum() + gw[0] @ dwq + gw[1] @ dwk
+        # each gradient element is off by a few independent bf16 roundings (2^-8 at most, about 2^-9
+        # on average) of its size, and the roundings of q_out, k_out, P and O before it add about as
+        # much again: along a random direction their sum is far below 4 x 2^-8 of the gradient's norm
+        size = np.sqrt((grad ** 2).sum() + (gw[0] ** 2).sum() + (gw[1] ** 2).sum())
+        assert abs(num - got) <= 4 * ref.U * size, (trial, num, got, size)
+
+
+def test_captured_and_replayed_on_new_inputs():
+    """One CUDA graph of the whole chain, replayed after its inputs changed."""
+    torch = torch_cuda()
+    b, n, h, hk, d, w, s, cap = 2, 260, 4, 2, 64, 60, 4, 264
+    packed, _, wts, freq = _model(2, b, n, h, hk, d)
+    wt = [torch.from_numpy(x).cuda() for x in wts]
+    g, _ = rand(8, b, n, h, d)
+    cache = sa.cache4_alloc(b, cap, hk, d)
+    lengths = torch.tensor([n, 131], dtype=torch.int32, device="cuda")
+
+    def chain():
+        q, k, v = packed[:, :, :h], packed[:, :, h:h + hk], packed[:, :, h + hk:]
+        qr, kr = sa.qk_norm_rope_fwd(q, k, *wt, freq)
+        o, lse = sa.sink_attn_fwd(qr, kr, v, w, s)
+        grads = sa.sink_attn_bwd(qr, kr, v, o, lse, g, w, s)
+        back = sa.qk_norm_rope_bwd(q, k, grads[0], grads[1], *wt, freq)
+        sa.cache4_append(cache, kr, v)
+        last = qr[:, -1:].contiguous()
+        return (o, lse) + grads + back + sa.sink_attn_decode(last, kr, v, lengths, w, s) + \
+            sa.sink_attn_decode_cache4(last, cache, lengths, w, s) + sa.cache4_read(cache, None, n)
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = chain()
+    for seed in (21, 22):
+        packed.copy_(rand(seed, *packed.shape)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in outs]
+        for x, y in zip(got, chain()):
+            assert torch.equal(x, y)
+    status_ok()
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams with separate outputs and workspaces do not meet."""
+    torch = torch_cuda()
+    b, n, h, hk, d, w, s = 1, 2000, 8, 2, 128, 300, 4
+    sets = []
+    for i in range(2):
+        t = [rand(10 * i + j, b, n, x, d)[0] for j, x in enumerate((h, hk, hk, h))]
+        sets.append(t)
+
+    def both(q, k, v, g):
+        o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+        return (o, lse) + sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+
+    want = [both(*t) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None, None]
+    for rep in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = both(*sets[i])
+    torch.cuda.synchronize()
+    status_ok()
+    for a, c in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, c))
