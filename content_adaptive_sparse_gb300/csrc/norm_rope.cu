@@ -7,8 +7,9 @@
 // Layout: a row is one (token, head); D / 8 lanes share it and each lane owns four (a, b) pairs,
 // so a rotation never leaves its lane. With rotated halves (element p with p + rotary / 2) a
 // lane reads two 8-byte runs, interleaved (2p with 2p + 1) one 16-byte run. A warp stays on one
-// token and walks its heads, queries then keys: the angles depend on (token, pair) only, and a
-// lane's four sines and cosines serve every head of the token.
+// token and walks its heads, queries then keys: the angles depend on (token, pair) only, each lane
+// takes one of them (two at D = 128), and shuffles hand a lane the four that serve it for every
+// head of the token.
 //
 // Angles: position * frequency is taken modulo one turn in integer arithmetic. The host gives
 // frequency / (2 pi) as a 64-bit binary fraction F of a turn; the low 64 bits of position * F
@@ -89,10 +90,78 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// The rows of heads [h0, h1) of q (M = 0) or k (M = 1) of one token, RPW at a time; s and i are
+// the token's sequence and place, c / sn the lane's angles. w_smem: this lane's eight weights.
+template <int D, bool INTER, bool BWD, int M>
+__device__ __forceinline__ void token_rows(const RopeParams& p, int64_t s, int64_t i, int h0, int h1, int slot, int lo,
+                                           int hi, const float (&cs)[4], const float (&sn)[4], const float* w_smem,
+                                           float (&dw)[8]) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  if (h0 >= h1) return;
+  const __nv_bfloat16* xp = p.x[M].ptr + s * p.x[M].sb + i * p.x[M].sn + (h0 + slot) * p.x[M].sh;
+  const __nv_bfloat16* gp = BWD ? p.dy[M].ptr + s * p.dy[M].sb + i * p.dy[M].sn + (h0 + slot) * p.dy[M].sh : nullptr;
+  __nv_bfloat16* op =
+      const_cast<__nv_bfloat16*>(p.out[M].ptr) + s * p.out[M].sb + i * p.out[M].sn + (h0 + slot) * p.out[M].sh;
+  const int64_t xs = RPW * p.x[M].sh, gs = RPW * p.dy[M].sh, os = RPW * p.out[M].sh;
+#pragma unroll(BWD ? 1 : 2)
+  for (int h = h0 + slot; h - slot < h1; h += RPW) {
+    const bool on = h < h1;
+    float x[8], z[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (on) load_pairs<INTER>(xp, lo, hi, x);
+    if constexpr (BWD) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = 0.f;
+      if (on) load_pairs<INTER>(gp, lo, hi, z);
+    }
+    float w[8];
+    *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(w_smem);
+    *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(w_smem + 4);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+    if constexpr (!BWD) {
+      const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = x[e] * rstd * w[e], b = x[e + 4] * rstd * w[e + 4];
+        z[e] = a * cs[e] - b * sn[e];
+        z[e + 4] = b * cs[e] + a * sn[e];
+      }
+    } else {
+      float g[8];
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = z[e] * cs[e] + z[e + 4] * sn[e];
+        g[e + 4] = z[e + 4] * cs[e] - z[e] * sn[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot += g[e] * w[e] * x[e];
+      const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+      const float c = row_sum<LPR>(dot) * rstd * (1.f / D);          // mean(g w xh)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = x[e] * rstd;
+        dw[e] += g[e] * xh;                                           // a row past the last head adds 0
+        z[e] = rstd * (g[e] * w[e] - xh * c);
+      }
+    }
+    if (on) store_pairs<INTER>(op, lo, hi, z);
+    xp += xs;
+    if constexpr (BWD) gp += gs;
+    op += os;
+  }
+}
+
 template <int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, BWD ? 3 : 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPR = D / 8;             // lanes per row
-  constexpr int RPW = 32 / LPR;          // rows (heads) a warp handles at a time
+  constexpr int PAIRS = D / 2;
+  constexpr int PPL = (PAIRS + 31) / 32; // pairs whose angles a lane takes
+  __shared__ __align__(16) float w_smem[2][D];            // weights in the lanes' order
+  __shared__ float red[BWD ? kWarps : 1][2][BWD ? D : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = lane % LPR, slot = lane / LPR;
   // this lane's pairs are 4t .. 4t+3 of the row's D / 2; those past rotary / 2 are not rotated
@@ -100,102 +169,59 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const __grid_con
   const int half = p.rotary >> 1;
   const int lo = INTER ? 8 * t : (4 * t < half ? 4 * t : 4 * t + half);
   const int hi = 4 * t < half ? 4 * t + half : 4 * t + D / 2;
-  uint64_t turn[4];
+  const auto element = [&](int e) { return INTER ? 8 * t + 2 * (e & 3) + (e >> 2) : (e < 4 ? lo + e : hi + e - 4); };
+  if (warp < 2 && slot == 0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) turn[i] = 4 * t + i < half ? p.turn[4 * t + i] : 0ull;
-  float w[2][8];
+    for (int e = 0; e < 8; ++e) w_smem[warp][8 * t + e] = p.w[warp] ? p.w[warp][element(e)] : 1.f;
+  }
+  uint64_t turn[PPL];
+#pragma unroll
+  for (int k = 0; k < PPL; ++k) turn[k] = lane + 32 * k < half ? p.turn[lane + 32 * k] : 0ull;
+  __syncthreads();
   float dw[2][8];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = INTER ? 8 * t + 2 * (i & 3) + (i >> 2) : (i < 4 ? lo + i : hi + i - 4);
-      w[m][i] = p.w[m] ? p.w[m][e] : 1.f;
-      dw[m][i] = 0.f;
-    }
-  const int all = p.heads[0] + p.heads[1];
+    for (int e = 0; e < 8; ++e) dw[m][e] = 0.f;
+  const int hq = p.heads[0], all = hq + p.heads[1];
   for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < p.units; u += (int64_t)gridDim.x * kWarps) {
     const int64_t tok = u / p.chunks;
-    const int h0 = (int)(u % p.chunks) * p.heads_per_unit;
+    const int h0 = (int)(u - tok * p.chunks) * p.heads_per_unit;
     const int h1 = min(all, h0 + p.heads_per_unit);
-    const int64_t s = tok / p.n;
-    const int64_t i0 = tok % p.n;
-    const int64_t pos = p.positions ? (int64_t)p.positions[tok] : i0;
-    float cs[4], sn[4];
+    const int64_t s = tok / p.n, i = tok - s * p.n;
+    const int64_t pos = p.positions ? (int64_t)p.positions[tok] : i;
+    // one angle per lane (two at D = 128), handed to the lanes whose pair it is
+    float my_c[PPL], my_s[PPL], cs[4], sn[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int k = 0; k < PPL; ++k) {
       // phase of a turn in [-2^31, 2^31) / 2^32; sincospif takes half turns
-      const int32_t phase = (int32_t)(((uint64_t)pos * turn[i]) >> 32);
-      sincospif((float)phase * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
+      const int32_t phase = (int32_t)(((uint64_t)pos * turn[k]) >> 32);
+      sincospif((float)phase * 4.656612873077393e-10f, &my_s[k], &my_c[k]);   // 2^-31
     }
-#pragma unroll 2
-    for (int hb = h0; hb < h1; hb += RPW) {
-      const int head = hb + slot;
-      const bool on = head < h1;
-      const int m = head >= p.heads[0] ? 1 : 0;
-      const int64_t h = m ? head - p.heads[0] : head;
-      const Tensor& X = p.x[m];
-      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-      if (on) load_pairs<INTER>(X.ptr + s * X.sb + i0 * X.sn + h * X.sh, lo, hi, x);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-      if constexpr (!BWD) {
-        const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[i] * rstd * (m ? w[1][i] : w[0][i]);
-          const float b = x[i + 4] * rstd * (m ? w[1][i + 4] : w[0][i + 4]);
-          z[i] = a * cs[i] - b * sn[i];
-          z[i + 4] = b * cs[i] + a * sn[i];
-        }
-        const Tensor& O = p.out[m];
-        if (on) store_pairs<INTER>(const_cast<__nv_bfloat16*>(O.ptr) + s * O.sb + i0 * O.sn + h * O.sh, lo, hi, z);
-      } else {
-        const Tensor& G = p.dy[m];
-        float g[8], z[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = 0.f;
-        if (on) load_pairs<INTER>(G.ptr + s * G.sb + i0 * G.sn + h * G.sh, lo, hi, z);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          g[i] = z[i] * cs[i] + z[i + 4] * sn[i];
-          g[i + 4] = z[i + 4] * cs[i] - z[i] * sn[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dot += g[i] * (m ? w[1][i] : w[0][i]) * x[i];
-        const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        const float c = row_sum<LPR>(dot) * rstd * (1.f / D);      // mean(g w xh)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = x[i] * rstd;
-          const float wi = m ? w[1][i] : w[0][i];
-          // a row past the last head adds g xh = 0
-          if (m) dw[1][i] += g[i] * xh;
-          else dw[0][i] += g[i] * xh;
-          z[i] = rstd * (g[i] * wi - xh * c);
-        }
-        const Tensor& O = p.out[m];
-        if (on) store_pairs<INTER>(const_cast<__nv_bfloat16*>(O.ptr) + s * O.sb + i0 * O.sn + h * O.sh, lo, hi, z);
+    for (int e = 0; e < 4; ++e) {
+      const int from = (4 * t + e) & 31;
+      cs[e] = __shfl_sync(0xffffffffu, my_c[0], from);
+      sn[e] = __shfl_sync(0xffffffffu, my_s[0], from);
+      if constexpr (PPL == 2) {
+        const float c1 = __shfl_sync(0xffffffffu, my_c[PPL - 1], from), s1 = __shfl_sync(0xffffffffu, my_s[PPL - 1], from);
+        cs[e] = 4 * t >= 32 ? c1 : cs[e];
+        sn[e] = 4 * t >= 32 ? s1 : sn[e];
       }
     }
+    token_rows<D, INTER, BWD, 0>(p, s, i, h0, min(h1, hq), slot, lo, hi, cs, sn, &w_smem[0][8 * t], dw[0]);
+    token_rows<D, INTER, BWD, 1>(p, s, i, max(h0 - hq, 0), h1 - hq, slot, lo, hi, cs, sn, &w_smem[1][8 * t], dw[1]);
   }
   if constexpr (BWD) {
     // this CTA's sums of g xh: over the warp's row slots, then over its warps, in a fixed order
-    __shared__ float red[kWarps][2][D];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v = dw[m][i];
+      for (int e = 0; e < 8; ++e) {
+        float v = dw[m][e];
 #pragma unroll
         for (int o = 16; o >= LPR; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int e = INTER ? 8 * t + 2 * (i & 3) + (i >> 2) : (i < 4 ? lo + i : hi + i - 4);
-        if (slot == 0) red[warp][m][e] = v;
+        if (slot == 0) red[warp][m][element(e)] = v;
       }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * D; e += 32 * kWarps) {

@@ -906,8 +906,8 @@ int cache4_args(const void* k, const void* v, const int64_t kst[3], const int64_
   if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs))
     return SA_ERR_UNSUPPORTED;
   if (!strides_ok(kst) || !strides_ok(vst)) return SA_ERR_UNSUPPORTED;
-  // one thread per 8 elements, 256 per CTA of a 31-bit grid
-  if ((double)batch * n_tokens * kv_heads * (head_dim / 8) > 256.0 * 2147483647.0) return SA_ERR_UNSUPPORTED;
+  // a sequence's 8-element words are counted in 32 bits; the grid's y holds the sequences twice
+  if ((int64_t)n_tokens * kv_heads > (INT32_MAX / (head_dim / 8)) || batch > 32767) return SA_ERR_UNSUPPORTED;
   memset(&a, 0, sizeof(a));
   a.k = const_cast<void*>(k);
   a.v = const_cast<void*>(v);

@@ -2,11 +2,11 @@
 // rows one way, 4.5 bits an element the other).
 //
 // A row is one (token, key head). Each run of 32 elements has the bf16 scale s = amax / 7, and an
-// element x the code round(x / s) (ties to even) in -7 .. 7, stored + 8 (s = 0: code 0). Both
-// divisions are the correctly rounded ones, and neither quotient can come so near a border of
-// the next rounding that the first one moves it across: x has 8 significant bits, a border times s
-// (or times 7) at most 12, so they are equal or differ by 2^-12 and more. A run with an infinity or
-// a NaN gets that scale, and reads back as NaN.
+// element x the code round(x / s) (ties to even) in -7 .. 7, stored + 8 (s = 0: code 0). The scale is
+// the exact quotient rounded once: amax has 8 significant bits and a border between two bf16
+// numbers times 7 has 12, so amax / 7 is 2^-13 and more away from the border or on it, and its
+// fp32 rounding does not move it across. A run with an infinity or a NaN has the scale NaN and
+// reads back as NaN.
 //   codes  [batch][kv_heads][capacity][d / 2] bytes: little-endian 32-bit word t * (d / 32) + c holds
 //          elements 32 c + 8 t + u, u = 0 .. 7; u = 4 p + i stands at bit 8 p + 4 (i / 2) + 16 (i % 2)
 //   scales [batch][kv_heads][capacity][d / 32] bf16
@@ -14,6 +14,10 @@
 // (t, c) for all c in one load, pairs (2k, 2k + 1) in the two half-words at the same nibble.
 //
 // One thread per word: 16 bytes of the row, the run's maximum over its four threads by shuffles.
+// The rounding takes no division per element: q = x (1 / s) is off by less than 2^-20, while a
+// quotient lies on a border (k + 1/2) or 2^-10 and more away from it, so q is first rounded to a
+// multiple of 2^-15 (adding 384, whose last place that is, and taking it off again), which puts
+// a border's quotient back on the border, and then to the nearest even integer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -32,27 +36,25 @@ struct CParams {
   __nv_bfloat16* scales[2];
   const int32_t* start;
   int64_t sb[2], sn[2], sh[2];
-  int n, kv_heads, capacity;
-  int64_t words;                    // 32-bit words of all rows
+  int kv_heads, capacity;
+  uint32_t words;                   // 32-bit words of one sequence's rows
 };
 
 __host__ __device__ constexpr int bit_of(int u) { return 8 * (u >> 2) + 4 * ((u & 3) >> 1) + 16 * (u & 1); }
 
-// Thread's word: sequence s, token i of the call, head h, run c, word t of the run; the cache row,
-// or -1 (out of range: reported; start < 0: the sequence is left out, not reported).
+// Thread's word of sequence s: token i of the call, head h, run c, word t of the run; the cache
+// row, or -1 (out of range: reported; start < 0: the sequence is left out, not reported).
 template <int D>
 struct Place {
-  int s, i, h, c, t;
+  uint32_t c, t, h, i;
   int64_t row;
-  __device__ Place(const CParams& p, int64_t w) {
-    constexpr int NG = D / 32;
-    t = (int)(w & 3);
-    c = (int)((w >> 2) % NG);
-    const int64_t r = (w >> 2) / NG;
-    h = (int)(r % p.kv_heads);
-    const int64_t si = r / p.kv_heads;
-    i = (int)(si % p.n);
-    s = (int)(si / p.n);
+  __device__ Place(const CParams& p, uint32_t s, uint32_t w) {
+    constexpr uint32_t NG = D / 32;
+    t = w & 3;
+    c = (w >> 2) % NG;
+    const uint32_t r = (w >> 2) / NG;
+    i = r / (uint32_t)p.kv_heads;
+    h = r - i * (uint32_t)p.kv_heads;
     const int start = p.start ? p.start[s] : 0;
     const int64_t slot = (int64_t)start + i;
     row = -1;
@@ -63,42 +65,49 @@ struct Place {
   }
 };
 
+// Largest magnitude of a pair's halves as bf16 bits in each half (the order of the bits of
+// non-negative bf16 numbers is that of the numbers, infinity and NaN last).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
 template <int D>
 __global__ void __launch_bounds__(256) cache4_append_kernel(const __grid_constant__ CParams p) {
   constexpr int NG = D / 32;
-  const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int m = blockIdx.y;
+  const uint32_t w = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t s = blockIdx.y >> 1, m = blockIdx.y & 1;
   const bool in = w < p.words;                       // whole runs: four threads in or out together
-  const Place<D> at(p, in ? w : 0);
+  const Place<D> at(p, s, in ? w : 0u);
   uint32_t v[4] = {0u, 0u, 0u, 0u};
   if (in) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p.x[m] + at.s * p.sb[m] + at.i * p.sn[m] + at.h * p.sh[m] +
+    const uint4 r = *reinterpret_cast<const uint4*>(p.x[m] + s * p.sb[m] + at.i * p.sn[m] + at.h * p.sh[m] +
                                                     32 * at.c + 8 * at.t);
     v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
   }
-  float x[8];
-  float amax = 0.f;
-  int odd = 0;                                       // an infinity or a NaN in the run
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    x[u] = __uint_as_float(u & 1 ? v[u >> 1] & 0xffff0000u : v[u >> 1] << 16);
-    const float a = fabsf(x[u]);
-    odd |= a < __int_as_float(0x7f800000) ? 0 : 1;
-    amax = fmaxf(amax, a);
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  odd |= __shfl_xor_sync(0xffffffffu, odd, 1);
-  odd |= __shfl_xor_sync(0xffffffffu, odd, 2);
-  const __nv_bfloat16 sb = __float2bfloat16_rn(odd ? __int_as_float(0x7fc00000) : __fdiv_rn(amax, 7.f));
-  const float s = __bfloat162float(sb);
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t top = max2(max2(v[0] & kAbs, v[1] & kAbs), max2(v[2] & kAbs, v[3] & kAbs));
+  top = max2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t amax = max(top & 0xffffu, top >> 16);             // bf16 bits
+  // a run with an infinity or a NaN has the scale NaN
+  const __nv_bfloat16 sb =
+      __float2bfloat16_rn(amax >= 0x7f80u ? __int_as_float(0x7fc00000) : __fdiv_rn(__uint_as_float(amax << 16), 7.f));
+  float sc = __bfloat162float(sb);
+  // scales below 2^-64 (the last ones subnormal): 1 / s would overflow, so x and s are taken times
+  // 2^70, exactly; and there s = amax / 7 is so coarse that a code can come out past 7
+  const bool tiny = sc < 5.421010862427522e-20f;
+  const float up = tiny ? 1.1805916207174113e21f : 1.f;
+  sc *= up;
+  const float inv = sc > 0.f ? __fdiv_rn(1.f, sc) * up : 0.f;      // NaN: 0
   uint32_t word = 0u;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const float q = s > 0.f ? rintf(__fdiv_rn(x[u], s)) : 0.f;
-    const int code = (int)fminf(fmaxf(q, -7.f), 7.f) + 8;
-    word |= (uint32_t)code << bit_of(u);
+    const float x = __uint_as_float(u & 1 ? v[u >> 1] & 0xffff0000u : v[u >> 1] << 16);
+    float q = x * inv;
+    if (tiny) q = fminf(fmaxf(x * up * (sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f), -7.f), 7.f);
+    // to a multiple of 2^-15, then to an integer, stored + 8 in the last bits of 1.5 x 2^23 + code
+    const float e = __fadd_rn(__fadd_rn(q, 384.f), -384.f);
+    word |= (__float_as_uint(__fadd_rn(e, 12582920.f)) & 15u) << bit_of(u);
   }
+  if (amax >= 0x7f80u) word = 0x88888888u;
   if (in && at.row >= 0) {
     p.codes[m][at.row * (D / 8) + at.t * NG + at.c] = word;
     if (at.t == 0) p.scales[m][at.row * NG + at.c] = sb;
@@ -108,30 +117,33 @@ __global__ void __launch_bounds__(256) cache4_append_kernel(const __grid_constan
 template <int D>
 __global__ void __launch_bounds__(256) cache4_read_kernel(const __grid_constant__ CParams p) {
   constexpr int NG = D / 32;
-  const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int m = blockIdx.y;
+  const uint32_t w = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t s = blockIdx.y >> 1, m = blockIdx.y & 1;
   if (w >= p.words) return;
-  const Place<D> at(p, w);
+  const Place<D> at(p, s, w);
   uint32_t word = 0x88888888u;                       // rows outside the cache read as zeros
-  float s = 0.f;
+  __nv_bfloat16 sc = __float2bfloat16_rn(0.f);
   if (at.row >= 0) {
     word = p.codes[m][at.row * (D / 8) + at.t * NG + at.c];
-    s = __bfloat162float(p.scales[m][at.row * NG + at.c]);
+    sc = p.scales[m][at.row * NG + at.c];
   }
+  // pair k of the word is elements 2k, 2k + 1: 128 + code over the bits of 128, exact, minus 136,
+  // times the scale with one rounding
+  const __nv_bfloat162 s2 = __halves2bfloat162(sc, sc), off = __floats2bfloat162_rn(136.f, 136.f);
   uint32_t v[4];
 #pragma unroll
-  for (int u = 0; u < 8; u += 2) {
-    const float a = (float)((int)((word >> bit_of(u)) & 15u) - 8) * s;
-    const float b = (float)((int)((word >> bit_of(u + 1)) & 15u) - 8) * s;
-    v[u >> 1] = pack_bf16x2(a, b);
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = ((word >> (4 * k)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), off), s2);
+    v[k] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  *reinterpret_cast<uint4*>(p.x[m] + at.s * p.sb[m] + at.i * p.sn[m] + at.h * p.sh[m] + 32 * at.c + 8 * at.t) =
+  *reinterpret_cast<uint4*>(p.x[m] + s * p.sb[m] + at.i * p.sn[m] + at.h * p.sh[m] + 32 * at.c + 8 * at.t) =
       make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 template <int D>
 int launch(const Cache4Args& a, const CParams& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.words + 255) / 256), 2);
+  const dim3 grid((p.words + 255u) / 256u, 2 * a.batch);
   if (a.read) cache4_read_kernel<D><<<grid, 256, 0, stream>>>(p);
   else cache4_append_kernel<D><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
@@ -154,10 +166,9 @@ int launch_cache4(const Cache4Args& a, cudaStream_t stream) {
     p.sn[m] = st[1];
     p.sh[m] = st[2];
   }
-  p.n = a.n_tokens;
   p.kv_heads = a.kv_heads;
   p.capacity = a.capacity;
-  p.words = (int64_t)a.batch * a.n_tokens * a.kv_heads * (a.head_dim / 8);
+  p.words = (uint32_t)a.n_tokens * a.kv_heads * (a.head_dim / 8);
   switch (a.head_dim) {
     case 32: return launch<32>(a, p, stream);
     case 64: return launch<64>(a, p, stream);

@@ -10,16 +10,19 @@ while the library's own refusals raise ``SAError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import numpy as np
 
 _P, _I32, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
 _S3 = ctypes.c_int64 * 3
+_LIB = None
 
 
 def declare(lib) -> None:
     """Argument types of this module's entry points (called once, when the library is loaded)."""
+    global _LIB
     sizes = [_I32] * 5
     rope = [_P, _P, _F32, _P, _I32, _I32, _P]          # weights, eps, frequencies, rotary, interleaved, positions
     sink = [_I32] * 7 + [_F32]                         # batch, tokens, heads, kv_heads, dim, window, sinks; scale
@@ -40,11 +43,14 @@ def declare(lib) -> None:
         fn = getattr(lib, name)
         fn.argtypes = types
         fn.restype = ctypes.c_int
+    _LIB = lib
 
 
 def _lib():
-    from . import load_library
-    return load_library()
+    if _LIB is None:
+        from . import load_library
+        load_library()
+    return _LIB
 
 
 def _check(name: str, code: int) -> None:
@@ -54,49 +60,68 @@ def _check(name: str, code: int) -> None:
 
 
 # ------------------------------------------------------------------ argument checks
+#
+# A decoding step is a few microseconds of GPU work, so the checks are single comparisons and the
+# stride arrays are kept by their values. Each helper raises with the argument's name.
 
-def _rows(name: str, t, shape=None) -> _S3:
+@functools.lru_cache(maxsize=1024)
+def _s3(strides: tuple) -> _S3:
+    return _S3(*strides[:3])
+
+
+@functools.lru_cache(maxsize=64)
+def _frequencies(raw: bytes):
+    """A host array of the doubles in `raw`: (address, count, the array, which owns the memory)."""
+    n = len(raw) // 8
+    array = (ctypes.c_double * n).from_buffer_copy(raw)
+    return ctypes.addressof(array) if n else 0, n, array
+
+
+def _dense(shape) -> _S3:
+    """Strides of a contiguous [batch, tokens, heads, head_dim] tensor."""
+    _, n, h, d = shape
+    return _s3((n * h * d, h * d, d))
+
+
+def _device() -> int:
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2   # no tensor is there
+
+
+def _rows(name: str, t, device: int, shape=None) -> _S3:
     """Strides of a bf16 [batch, tokens, heads, head_dim] tensor on the current device."""
     import torch
-    if t.dtype is not torch.bfloat16 or t.dim() != 4:
-        raise ValueError(f"{name}: expected a bfloat16 [batch, tokens, heads, head_dim] tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
+    if t.dtype is not torch.bfloat16 or len(st) != 4:
+        raise ValueError(f"{name}: expected a bfloat16 [batch, tokens, heads, head_dim] tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if st[3] != 1:
         raise ValueError(f"{name}: head_dim must be contiguous")
-    _on_device(name, t)
-    return _S3(st[0], st[1], st[2])
+    if t.get_device() != device:
+        _elsewhere(name)
+    return _s3(st)
 
 
-def _sizes(name: str, t):
-    if t.dim() != 4:
-        raise ValueError(f"{name}: expected a bfloat16 [batch, tokens, heads, head_dim] tensor")
-    return t.shape
+def _elsewhere(name: str):
+    raise ValueError(f"{name}: expected a tensor on the current CUDA device")
 
 
-def _on_device(name: str, t) -> None:
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
-
-
-def _flat(name: str, t, dtype, shape) -> int:
-    """Address of a contiguous tensor of this type and shape (0 for None)."""
-    if t is None:              # a null pointer: refused by the library where the argument is needed
+def _flat(name: str, t, dtype, shape, device: int) -> int:
+    """Address of a contiguous tensor of this type and shape (0 for None, which the library refuses
+    where it needs the argument)."""
+    if t is None:
         return 0
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
-    _on_device(name, t)
+    if t.get_device() != device:
+        _elsewhere(name)
     return t.data_ptr()
 
 
-def _kv(k, v, shape=None) -> tuple[_S3, _S3]:
-    return _rows("k", k, shape), _rows("v", v, k.shape)
-
-
 def _same_sequence(q, k) -> None:
-    if k.shape[0] != q.shape[0] or k.shape[1] != q.shape[1] or k.shape[3] != q.shape[3]:
+    a, b = q.shape, k.shape
+    if a[0] != b[0] or a[1] != b[1] or a[3] != b[3]:
         raise ValueError("q and k must agree in batch, tokens and head_dim")
 
 
@@ -104,32 +129,42 @@ def _scale(softmax_scale, d: int) -> float:
     return d ** -0.5 if softmax_scale is None else float(softmax_scale)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)   # current_stream().cuda_stream without its object
 
 
-def _workspace(ws) -> tuple[int, int]:
-    _on_device("workspace", ws)
+def _workspace(ws, device: int) -> tuple[int, int]:
+    if ws.get_device() != device:
+        _elsewhere("workspace")
     if not ws.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _like(t):
+    import torch
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 # ------------------------------------------------------------------ norm and rotation of queries and keys
 
-def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
+def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev):
     import torch
-    qs, ks = _rows("q", q), _rows("k", k)
+    qs, ks = _rows("q", q, dev), _rows("k", k, dev)
     _same_sequence(q, k)
     b, n, h, d = q.shape
-    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    if freq.ndim != 1:
+    if type(inv_freq) is not np.ndarray or inv_freq.dtype != np.float64:
+        inv_freq = np.asarray(inv_freq, dtype=np.float64)
+    if inv_freq.ndim != 1:
         raise ValueError("inv_freq: expected one frequency per rotated pair")
-    tail = (_flat("q_weight", q_weight, torch.float32, (d,)), _flat("k_weight", k_weight, torch.float32, (d,)),
-            float(eps), freq.ctypes.data if freq.size else 0, 2 * freq.size, int(bool(interleaved)),
-            _flat("positions", positions, torch.int32, (b, n)))
-    return qs, ks, (b, n, h, k.shape[2], d) + tail, freq        # freq: kept alive until the call returns
+    freq, pairs, _ = _frequencies(inv_freq.tobytes())
+    f32 = torch.float32
+    return (q.data_ptr(), k.data_ptr()), (qs, ks), (
+        b, n, h, k.shape[2], d, _flat("q_weight", q_weight, f32, (d,), dev), _flat("k_weight", k_weight, f32, (d,), dev),
+        eps, freq, 2 * pairs, 1 if interleaved else 0, _flat("positions", positions, torch.int32, (b, n), dev))
 
 
 def sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps: float = 1e-6,
@@ -137,10 +172,11 @@ def sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_
     """RMS norm and rotation of q and k into q_out and k_out (which may be q and k). ``inv_freq``:
     host sequence of one frequency per rotated pair, radians per position; weights (fp32 [head_dim])
     and ``positions`` (int32 [batch, tokens]) may be None."""
-    qs, ks, args, freq = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    dev = _device()
+    ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev)
     _check("sa_qk_norm_rope_fwd", _lib().sa_qk_norm_rope_fwd(
-        q.data_ptr(), k.data_ptr(), qs, ks, *args, q_out.data_ptr(), k_out.data_ptr(), _rows("q_out", q_out, q.shape),
-        _rows("k_out", k_out, k.shape), _stream(stream)))
+        *ptrs, *strides, *args, q_out.data_ptr(), k_out.data_ptr(), _rows("q_out", q_out, dev, q.shape),
+        _rows("k_out", k_out, dev, k.shape), _stream(stream, dev)))
 
 
 def sa_qk_norm_rope_bwd_workspace_size(head_dim: int) -> int:
@@ -153,22 +189,23 @@ def sa_qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, po
                         workspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """Gradients of sa_qk_norm_rope_fwd; the weights' (fp32 [head_dim]) may be None."""
     import torch
-    qs, ks, args, freq = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
-    d = q.shape[3]
-    ws, ws_bytes = _workspace(workspace)
+    dev = _device()
+    ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev)
+    d = (q.shape[3],)
     _check("sa_qk_norm_rope_bwd", _lib().sa_qk_norm_rope_bwd(
-        q.data_ptr(), k.data_ptr(), d_q_out.data_ptr(), d_k_out.data_ptr(), qs, ks, _rows("d_q_out", d_q_out, q.shape),
-        _rows("d_k_out", d_k_out, k.shape), *args, dq.data_ptr(), dk.data_ptr(), _rows("dq", dq, q.shape),
-        _rows("dk", dk, k.shape), _flat("dq_weight", dq_weight, torch.float32, (d,)),
-        _flat("dk_weight", dk_weight, torch.float32, (d,)), ws, ws_bytes, _stream(stream)))
+        *ptrs, d_q_out.data_ptr(), d_k_out.data_ptr(), *strides, _rows("d_q_out", d_q_out, dev, q.shape),
+        _rows("d_k_out", d_k_out, dev, k.shape), *args, dq.data_ptr(), dk.data_ptr(), _rows("dq", dq, dev, q.shape),
+        _rows("dk", dk, dev, k.shape), _flat("dq_weight", dq_weight, torch.float32, d, dev),
+        _flat("dk_weight", dk_weight, torch.float32, d, dev), *_workspace(workspace, dev), _stream(stream, dev)))
 
 
 def qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions=None, eps: float = 1e-6, interleaved: bool = False):
     """Returns (q_out, k_out), contiguous."""
-    import torch
-    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-    sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, interleaved)
+    dev = _device()
+    ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev)
+    q_out, k_out = _like(q), _like(k)
+    _check("sa_qk_norm_rope_fwd", _lib().sa_qk_norm_rope_fwd(
+        *ptrs, *strides, *args, q_out.data_ptr(), k_out.data_ptr(), _dense(q.shape), _dense(k.shape), _stream(None, dev)))
     return q_out, k_out
 
 
@@ -177,7 +214,7 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, posit
     """Returns (dq, dk, dq_weight, dk_weight); a weight given as None has the gradient None."""
     import torch
     d, dev = q.shape[-1], q.device
-    dq, dk = torch.empty(q.shape, dtype=torch.bfloat16, device=dev), torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    dq, dk = _like(q), _like(k)
     dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
     dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
     ws = torch.empty(sa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dev)
@@ -188,14 +225,20 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, posit
 
 # ------------------------------------------------------------------ sink-window attention
 
+def _sink_inputs(q, k, v, dev):
+    strides = _rows("q", q, dev), _rows("k", k, dev), _rows("v", v, dev, k.shape)
+    _same_sequence(q, k)
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr()), strides
+
+
 def sa_sink_attn_fwd(q, k, v, window: int, sinks: int, o, lse, softmax_scale: float | None = None, stream=None) -> None:
     import torch
-    qs, (ks, vs) = _rows("q", q), _kv(k, v)
-    _same_sequence(q, k)
+    dev = _device()
+    ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
     _check("sa_sink_attn_fwd", _lib().sa_sink_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _rows("o", o, q.shape), b, n, h, k.shape[2], d, window, sinks,
-        _scale(softmax_scale, d), o.data_ptr(), _flat("lse", lse, torch.float32, (b, h, n)), _stream(stream)))
+        *ptrs, *strides, _rows("o", o, dev, q.shape), b, n, h, k.shape[2], d, window, sinks, _scale(softmax_scale, d),
+        o.data_ptr(), _flat("lse", lse, torch.float32, (b, h, n), dev), _stream(stream, dev)))
 
 
 def sa_sink_attn_bwd_workspace_size(batch: int, n_tokens: int, heads: int, kv_heads: int, head_dim: int, window: int,
@@ -209,36 +252,39 @@ def sa_sink_attn_bwd_workspace_size(batch: int, n_tokens: int, heads: int, kv_he
 def sa_sink_attn_bwd(q, k, v, o, d_o, lse, window: int, sinks: int, dq, dk, dv, workspace,
                      softmax_scale: float | None = None, stream=None) -> None:
     import torch
-    qs, (ks, vs) = _rows("q", q), _kv(k, v)
-    _same_sequence(q, k)
+    dev = _device()
+    ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
-    ws, ws_bytes = _workspace(workspace)
     _check("sa_sink_attn_bwd", _lib().sa_sink_attn_bwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d_o.data_ptr(),
-        _flat("lse", lse, torch.float32, (b, h, n)), qs, ks, vs, _rows("o", o, q.shape), _rows("d_o", d_o, q.shape), b, n, h,
-        k.shape[2], d, window, sinks, _scale(softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-        _rows("dq", dq, q.shape), _rows("dk", dk, k.shape), _rows("dv", dv, k.shape), ws, ws_bytes, _stream(stream)))
+        *ptrs, o.data_ptr(), d_o.data_ptr(), _flat("lse", lse, torch.float32, (b, h, n), dev), *strides,
+        _rows("o", o, dev, q.shape), _rows("d_o", d_o, dev, q.shape), b, n, h, k.shape[2], d, window, sinks,
+        _scale(softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _rows("dq", dq, dev, q.shape),
+        _rows("dk", dk, dev, k.shape), _rows("dv", dv, dev, k.shape), *_workspace(workspace, dev), _stream(stream, dev)))
 
 
 def sink_attn_fwd(q, k, v, window: int, sinks: int, softmax_scale: float | None = None):
     """Returns (o, lse): causal attention over the `window` keys before each query, itself and the
     first `sinks` tokens."""
     import torch
-    b, n, h, d = _sizes("q", q)
-    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    dev = _device()
+    ptrs, strides = _sink_inputs(q, k, v, dev)
+    b, n, h, d = q.shape
+    o = _like(q)
     lse = torch.empty((b, h, n), dtype=torch.float32, device=q.device)
-    sa_sink_attn_fwd(q, k, v, window, sinks, o, lse, softmax_scale)
+    _check("sa_sink_attn_fwd", _lib().sa_sink_attn_fwd(
+        *ptrs, *strides, _dense(q.shape), b, n, h, k.shape[2], d, window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        lse.data_ptr(), _stream(None, dev)))
     return o, lse
 
 
 def sink_attn_bwd(q, k, v, o, lse, d_o, window: int, sinks: int, softmax_scale: float | None = None):
     """Returns (dq, dk, dv) from sink_attn_fwd's inputs and outputs."""
     import torch
-    b, n, h, d = _sizes("q", q)
-    dev = q.device
-    dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    dk, dv = torch.empty(k.shape, dtype=torch.bfloat16, device=dev), torch.empty(v.shape, dtype=torch.bfloat16, device=dev)
-    ws = torch.empty(sa_sink_attn_bwd_workspace_size(b, n, h, k.shape[2], d, window, sinks), dtype=torch.uint8, device=dev)
+    _rows("q", q, _device())
+    b, n, h, d = q.shape
+    dq, dk, dv = _like(q), _like(k), _like(v)
+    ws = torch.empty(sa_sink_attn_bwd_workspace_size(b, n, h, k.shape[2], d, window, sinks), dtype=torch.uint8,
+                     device=q.device)
     sa_sink_attn_bwd(q, k, v, o, d_o, lse, window, sinks, dq, dk, dv, ws, softmax_scale)
     return dq, dk, dv
 
@@ -266,38 +312,47 @@ def cache4_alloc(batch: int, capacity: int, kv_heads: int, head_dim: int, device
     return Cache4(*rows(), *rows())
 
 
-def _cache4(cache) -> tuple[tuple[int, int, int, int], tuple[int, int, int, int]]:
-    """Addresses of a cache's four tensors and (batch, kv_heads, capacity, head_dim)."""
+def _cache4(cache, dev):
+    """Addresses of a cache's four tensors, and (batch, kv_heads, capacity, head_dim)."""
     import torch
     kc, ks, vc, vs = cache
-    if kc.dim() != 4:
+    codes = kc.shape
+    if len(codes) != 4:
         raise ValueError("cache: expected codes of shape [batch, kv_heads, capacity, head_dim / 2]")
-    b, hk, cap, half = kc.shape
+    b, hk, cap, half = codes
     scales = (b, hk, cap, half // 16)
-    at = (_flat("k_codes", kc, torch.uint8, kc.shape), _flat("k_scales", ks, torch.bfloat16, scales),
-          _flat("v_codes", vc, torch.uint8, kc.shape), _flat("v_scales", vs, torch.bfloat16, scales))
-    return at, (b, hk, cap, 2 * half)
+    u8, bf16 = torch.uint8, torch.bfloat16
+    return (_flat("k_codes", kc, u8, codes, dev), _flat("k_scales", ks, bf16, scales, dev),
+            _flat("v_codes", vc, u8, codes, dev), _flat("v_scales", vs, bf16, scales, dev)), (b, hk, cap, 2 * half)
 
 
 def sa_cache4_append(cache: Cache4, k, v, start=None, stream=None) -> None:
     """Writes rows start[s] .. start[s] + n - 1 of every sequence (``start``: int32 [batch] on the
     device, None for 0; a negative one leaves its sequence out)."""
     import torch
-    at, (b, hk, cap, d) = _cache4(cache)
-    ks, vs = _kv(k, v, (b, k.shape[1], hk, d))
+    dev = _device()
+    at, (b, hk, cap, d) = _cache4(cache, dev)
+    ks = _rows("k", k, dev)
+    n = k.shape[1]
+    if k.shape != (b, n, hk, d):
+        raise ValueError(f"k: expected rows of the cache's shape {(b, n, hk, d)}, got {tuple(k.shape)}")
     _check("sa_cache4_append", _lib().sa_cache4_append(
-        k.data_ptr(), v.data_ptr(), ks, vs, b, k.shape[1], hk, d, cap, _flat("start", start, torch.int32, (b,)), *at,
-        _stream(stream)))
+        k.data_ptr(), v.data_ptr(), ks, _rows("v", v, dev, k.shape), b, n, hk, d, cap,
+        _flat("start", start, torch.int32, (b,), dev), *at, _stream(stream, dev)))
 
 
 def sa_cache4_read(cache: Cache4, start, k, v, stream=None) -> None:
     """Reads rows start[s] .. start[s] + n - 1 of every sequence into k and v."""
     import torch
-    at, (b, hk, cap, d) = _cache4(cache)
-    ks, vs = _kv(k, v, (b, k.shape[1], hk, d))
+    dev = _device()
+    at, (b, hk, cap, d) = _cache4(cache, dev)
+    ks = _rows("k", k, dev)
+    n = k.shape[1]
+    if k.shape != (b, n, hk, d):
+        raise ValueError(f"k: expected rows of the cache's shape {(b, n, hk, d)}, got {tuple(k.shape)}")
     _check("sa_cache4_read", _lib().sa_cache4_read(
-        *at, b, k.shape[1], hk, d, cap, _flat("start", start, torch.int32, (b,)), k.data_ptr(), v.data_ptr(), ks, vs,
-        _stream(stream)))
+        *at, b, n, hk, d, cap, _flat("start", start, torch.int32, (b,), dev), k.data_ptr(), v.data_ptr(), ks,
+        _rows("v", v, dev, k.shape), _stream(stream, dev)))
 
 
 def cache4_append(cache: Cache4, k, v, start=None) -> None:
@@ -307,64 +362,84 @@ def cache4_append(cache: Cache4, k, v, start=None) -> None:
 def cache4_read(cache: Cache4, start, n_tokens: int):
     """Returns (k, v), bfloat16 [batch, n_tokens, kv_heads, head_dim]."""
     import torch
-    b, hk, _, half = cache[0].shape
-    k = torch.empty((b, n_tokens, hk, 2 * half), dtype=torch.bfloat16, device=cache[0].device)
+    dev = _device()
+    at, (b, hk, cap, d) = _cache4(cache, dev)
+    k = torch.empty((b, n_tokens, hk, d), dtype=torch.bfloat16, device=cache[0].device)
     v = torch.empty_like(k)
-    sa_cache4_read(cache, start, k, v)
+    st = _dense(k.shape)
+    _check("sa_cache4_read", _lib().sa_cache4_read(
+        *at, b, n_tokens, hk, d, cap, _flat("start", start, torch.int32, (b,), dev), k.data_ptr(), v.data_ptr(), st, st,
+        _stream(None, dev)))
     return k, v
 
 
-def _token(q, b: int, d: int) -> _S3:
-    st = _rows("q", q)
-    if q.shape[0] != b or q.shape[1] != 1 or q.shape[3] != d:
+def _token(q, b: int, d: int, dev: int) -> _S3:
+    st = _rows("q", q, dev)
+    shape = q.shape
+    if shape[0] != b or shape[1] != 1 or shape[3] != d:
         raise ValueError("q: expected one token per sequence, [batch, 1, heads, head_dim]")
     return st
+
+
+def _token_outputs(q):
+    import torch
+    return _like(q), torch.empty((q.shape[0], q.shape[2], 1), dtype=torch.float32, device=q.device)
 
 
 def sa_sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, o, lse,
                         softmax_scale: float | None = None, stream=None) -> None:
     """``lengths``: int32 [batch] on the device, tokens in each cache with the query's own key."""
     import torch
-    ks, vs = _kv(k_cache, v_cache)
+    dev = _device()
     b, cap, hk, d = k_cache.shape
-    qs = _token(q, b, d)
-    h = q.shape[2]
+    qs, h = _token(q, b, d, dev), q.shape[2]
     _check("sa_sink_attn_decode", _lib().sa_sink_attn_decode(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qs, ks, vs, _rows("o", o, q.shape), b, cap, h, hk, d,
-        _flat("lengths", lengths, torch.int32, (b,)), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
-        _flat("lse", lse, torch.float32, (b, h, 1)), _stream(stream)))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qs, _rows("k_cache", k_cache, dev),
+        _rows("v_cache", v_cache, dev, k_cache.shape), _rows("o", o, dev, q.shape), b, cap, h, hk, d,
+        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        _flat("lse", lse, torch.float32, (b, h, 1), dev), _stream(stream, dev)))
 
 
 def sa_sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: int, o, lse,
                                softmax_scale: float | None = None, stream=None) -> None:
     import torch
-    at, (b, hk, cap, d) = _cache4(cache)
-    qs = _token(q, b, d)
-    h = q.shape[2]
+    dev = _device()
+    at, (b, hk, cap, d) = _cache4(cache, dev)
+    qs, h = _token(q, b, d, dev), q.shape[2]
     _check("sa_sink_attn_decode_cache4", _lib().sa_sink_attn_decode_cache4(
-        q.data_ptr(), *at, qs, _rows("o", o, q.shape), b, cap, h, hk, d,
-        _flat("lengths", lengths, torch.int32, (b,)), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
-        _flat("lse", lse, torch.float32, (b, h, 1)), _stream(stream)))
-
-
-def _token_outputs(q):
-    import torch
-    b, _, h, d = _sizes("q", q)
-    return (torch.empty((b, 1, h, d), dtype=torch.bfloat16, device=q.device),
-            torch.empty((b, h, 1), dtype=torch.float32, device=q.device))
+        q.data_ptr(), *at, qs, _rows("o", o, dev, q.shape), b, cap, h, hk, d,
+        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        _flat("lse", lse, torch.float32, (b, h, 1), dev), _stream(stream, dev)))
 
 
 def sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, softmax_scale: float | None = None):
     """One token per sequence over a bf16 cache; returns (o [batch, 1, heads, head_dim], lse)."""
+    import torch
+    dev = _device()
+    if len(k_cache.shape) != 4:
+        raise ValueError("k_cache: expected a bfloat16 [batch, capacity, kv_heads, head_dim] tensor")
+    b, cap, hk, d = k_cache.shape
+    qs = _token(q, b, d, dev)
     o, lse = _token_outputs(q)
-    sa_sink_attn_decode(q, k_cache, v_cache, lengths, window, sinks, o, lse, softmax_scale)
+    _check("sa_sink_attn_decode", _lib().sa_sink_attn_decode(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qs, _rows("k_cache", k_cache, dev),
+        _rows("v_cache", v_cache, dev, k_cache.shape), _dense(q.shape), b, cap, q.shape[2], hk, d,
+        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        lse.data_ptr(), _stream(None, dev)))
     return o, lse
 
 
 def sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: int, softmax_scale: float | None = None):
     """One token per sequence over a 4-bit cache; returns (o [batch, 1, heads, head_dim], lse)."""
+    import torch
+    dev = _device()
+    at, (b, hk, cap, d) = _cache4(cache, dev)
+    qs = _token(q, b, d, dev)
     o, lse = _token_outputs(q)
-    sa_sink_attn_decode_cache4(q, cache, lengths, window, sinks, o, lse, softmax_scale)
+    _check("sa_sink_attn_decode_cache4", _lib().sa_sink_attn_decode_cache4(
+        q.data_ptr(), *at, qs, _dense(q.shape), b, cap, q.shape[2], hk, d,
+        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        lse.data_ptr(), _stream(None, dev)))
     return o, lse
 
 
