@@ -52,22 +52,31 @@ __device__ __forceinline__ void unpack2(uint32_t v, float& lo, float& hi) {
   hi = __uint_as_float(v & 0xffff0000u);
 }
 
-// A lane's four pairs of one row: v[0..3] the a elements, v[4..7] the b elements.
+// A lane's 16 bytes of one row, as loaded, and as its four pairs: v[0..3] the a elements, v[4..7]
+// the b elements.
 template <bool INTER>
-__device__ __forceinline__ void load_pairs(const __nv_bfloat16* row, int lo, int hi, float (&v)[8]) {
-  if (INTER) {
-    const uint4 r = *reinterpret_cast<const uint4*>(row + lo);
+__device__ __forceinline__ uint4 load_pairs(const __nv_bfloat16* row, int lo, int hi) {
+  if constexpr (INTER) {
+    return *reinterpret_cast<const uint4*>(row + lo);
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + lo);
+    const uint2 b = *reinterpret_cast<const uint2*>(row + hi);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+}
+
+template <bool INTER>
+__device__ __forceinline__ void unpack_pairs(const uint4& r, float (&v)[8]) {
+  if constexpr (INTER) {
     unpack2(r.x, v[0], v[4]);
     unpack2(r.y, v[1], v[5]);
     unpack2(r.z, v[2], v[6]);
     unpack2(r.w, v[3], v[7]);
   } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(row + lo);
-    const uint2 b = *reinterpret_cast<const uint2*>(row + hi);
-    unpack2(a.x, v[0], v[1]);
-    unpack2(a.y, v[2], v[3]);
-    unpack2(b.x, v[4], v[5]);
-    unpack2(b.y, v[6], v[7]);
+    unpack2(r.x, v[0], v[1]);
+    unpack2(r.y, v[2], v[3]);
+    unpack2(r.z, v[4], v[5]);
+    unpack2(r.w, v[6], v[7]);
   }
 }
 
@@ -90,73 +99,82 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// The rows of heads [h0, h1) of q (M = 0) or k (M = 1) of one token, RPW at a time; s and i are
-// the token's sequence and place, c / sn the lane's angles. w_smem: this lane's eight weights.
+// The rows of heads [h0, h1) of q (M = 0) or k (M = 1) of one token, RPW at a time and U times RPW
+// rows loaded before the first is written (the outputs may be the inputs, so the compiler cannot
+// move a load over a store by itself); s and i are the token's sequence and place, cs / sn the
+// lane's angles, w_smem its eight weights.
 template <int D, bool INTER, bool BWD, int M>
 __device__ __forceinline__ void token_rows(const RopeParams& p, int64_t s, int64_t i, int h0, int h1, int slot, int lo,
                                            int hi, const float (&cs)[4], const float (&sn)[4], const float* w_smem,
                                            float (&dw)[8]) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr int U = 3;
   if (h0 >= h1) return;
   const __nv_bfloat16* xp = p.x[M].ptr + s * p.x[M].sb + i * p.x[M].sn + (h0 + slot) * p.x[M].sh;
   const __nv_bfloat16* gp = BWD ? p.dy[M].ptr + s * p.dy[M].sb + i * p.dy[M].sn + (h0 + slot) * p.dy[M].sh : nullptr;
   __nv_bfloat16* op =
       const_cast<__nv_bfloat16*>(p.out[M].ptr) + s * p.out[M].sb + i * p.out[M].sn + (h0 + slot) * p.out[M].sh;
   const int64_t xs = RPW * p.x[M].sh, gs = RPW * p.dy[M].sh, os = RPW * p.out[M].sh;
-#pragma unroll(BWD ? 1 : 2)
-  for (int h = h0 + slot; h - slot < h1; h += RPW) {
-    const bool on = h < h1;
-    float x[8], z[8];
+#pragma unroll 1
+  for (int hb = h0; hb < h1; hb += U * RPW) {
+    uint4 xr[U], gr[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (on) load_pairs<INTER>(xp, lo, hi, x);
-    if constexpr (BWD) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = 0.f;
-      if (on) load_pairs<INTER>(gp, lo, hi, z);
+    for (int k = 0; k < U; ++k) {
+      xr[k] = make_uint4(0u, 0u, 0u, 0u);            // a row past the last head counts as zeros
+      gr[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (hb + k * RPW + slot < h1) {
+        xr[k] = load_pairs<INTER>(xp, lo, hi);
+        if constexpr (BWD) gr[k] = load_pairs<INTER>(gp, lo, hi);
+      }
+      xp += xs;
+      if constexpr (BWD) gp += gs;
     }
-    float w[8];
-    *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(w_smem);
-    *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(w_smem + 4);
-    float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-    if constexpr (!BWD) {
-      const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+    for (int k = 0; k < U; ++k) {
+      if (hb + k * RPW >= h1) break;                 // the whole warp
+      float x[8], z[8], w[8];
+      unpack_pairs<INTER>(xr[k], x);
+      *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(w_smem);
+      *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(w_smem + 4);
+      float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = x[e] * rstd * w[e], b = x[e + 4] * rstd * w[e + 4];
-        z[e] = a * cs[e] - b * sn[e];
-        z[e + 4] = b * cs[e] + a * sn[e];
+      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+      if constexpr (!BWD) {
+        const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = x[e] * rstd * w[e], b = x[e + 4] * rstd * w[e + 4];
+          z[e] = a * cs[e] - b * sn[e];
+          z[e + 4] = b * cs[e] + a * sn[e];
+        }
+      } else {
+        float g[8];
+        float dot = 0.f;
+        unpack_pairs<INTER>(gr[k], z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          g[e] = z[e] * cs[e] + z[e + 4] * sn[e];
+          g[e + 4] = z[e + 4] * cs[e] - z[e] * sn[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += g[e] * w[e] * x[e];
+        const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+        const float c = row_sum<LPR>(dot) * rstd * (1.f / D);        // mean(g w xh)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float xh = x[e] * rstd;
+          dw[e] += g[e] * xh;
+          z[e] = rstd * (g[e] * w[e] - xh * c);
+        }
       }
-    } else {
-      float g[8];
-      float dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        g[e] = z[e] * cs[e] + z[e + 4] * sn[e];
-        g[e + 4] = z[e + 4] * cs[e] - z[e] * sn[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dot += g[e] * w[e] * x[e];
-      const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-      const float c = row_sum<LPR>(dot) * rstd * (1.f / D);          // mean(g w xh)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = x[e] * rstd;
-        dw[e] += g[e] * xh;                                           // a row past the last head adds 0
-        z[e] = rstd * (g[e] * w[e] - xh * c);
-      }
+      if (hb + k * RPW + slot < h1) store_pairs<INTER>(op, lo, hi, z);
+      op += os;
     }
-    if (on) store_pairs<INTER>(op, lo, hi, z);
-    xp += xs;
-    if constexpr (BWD) gp += gs;
-    op += os;
   }
 }
 
 template <int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps, BWD ? 3 : 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, BWD ? 2 : 4) norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPR = D / 8;             // lanes per row
   constexpr int PAIRS = D / 2;
   constexpr int PPL = (PAIRS + 31) / 32; // pairs whose angles a lane takes

@@ -907,7 +907,7 @@ int cache4_args(const void* k, const void* v, const int64_t kst[3], const int64_
     return SA_ERR_UNSUPPORTED;
   if (!strides_ok(kst) || !strides_ok(vst)) return SA_ERR_UNSUPPORTED;
   // a sequence's 8-element words are counted in 32 bits; the grid's y holds the sequences twice
-  if ((int64_t)n_tokens * kv_heads > (INT32_MAX / (head_dim / 8)) || batch > 32767) return SA_ERR_UNSUPPORTED;
+  if ((int64_t)n_tokens * kv_heads > (1 << 30) / (head_dim / 8) || batch > 32767) return SA_ERR_UNSUPPORTED;
   memset(&a, 0, sizeof(a));
   a.k = const_cast<void*>(k);
   a.v = const_cast<void*>(v);

@@ -2,22 +2,23 @@
 // rows one way, 4.5 bits an element the other).
 //
 // A row is one (token, key head). Each run of 32 elements has the bf16 scale s = amax / 7, and an
-// element x the code round(x / s) (ties to even) in -7 .. 7, stored + 8 (s = 0: code 0). The scale is
-// the exact quotient rounded once: amax has 8 significant bits and a border between two bf16
-// numbers times 7 has 12, so amax / 7 is 2^-13 and more away from the border or on it, and its
-// fp32 rounding does not move it across. A run with an infinity or a NaN has the scale NaN and
-// reads back as NaN.
+// element x the code round(x / s) (ties to even) in -7 .. 7, stored + 8 (s = 0: code 0). A run with an
+// infinity or a NaN has the scale NaN and reads back as NaN. amax has 8 significant bits, and a
+// border between two bf16 numbers, an odd number of 9 bits, is odd and of 11 bits and more when
+// taken 7 times: amax / 7 is never on a border, and 2^-13 of its size or more away from it.
 //   codes  [batch][kv_heads][capacity][d / 2] bytes: little-endian 32-bit word t * (d / 32) + c holds
 //          elements 32 c + 8 t + u, u = 0 .. 7; u = 4 p + i stands at bit 8 p + 4 (i / 2) + 16 (i % 2)
 //   scales [batch][kv_heads][capacity][d / 32] bf16
 // The word order puts what one lane of the decoding kernel's fragments needs side by side: word
 // (t, c) for all c in one load, pairs (2k, 2k + 1) in the two half-words at the same nibble.
 //
-// One thread per word: 16 bytes of the row, the run's maximum over its four threads by shuffles.
-// The rounding takes no division per element: q = x (1 / s) is off by less than 2^-20, while a
+// One thread per word (four words a thread, loaded before the first is worked on): 16 bytes of the
+// row, the run's maximum over its four threads by shuffles.
+// The rounding takes no division: the approximate q = x (1 / s) is off by less than 2^-19, while a
 // quotient lies on a border (k + 1/2) or 2^-10 and more away from it, so q is first rounded to a
 // multiple of 2^-15 (adding 384, whose last place that is, and taking it off again), which puts
-// a border's quotient back on the border, and then to the nearest even integer.
+// a border's quotient back on the border, and then to the nearest even integer. In the same way
+// amax times fp32's 1 / 7 rounds to the bf16 number that amax / 7 does.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,6 +31,8 @@ namespace {
 
 __device__ unsigned int g_cache_err;
 
+constexpr int kWords = 4;           // words per thread, 256 apart
+
 struct CParams {
   __nv_bfloat16* x[2];              // k, v rows (read by the append, written by the read)
   uint32_t* codes[2];
@@ -38,30 +41,43 @@ struct CParams {
   int64_t sb[2], sn[2], sh[2];
   int kv_heads, capacity;
   uint32_t words;                   // 32-bit words of one sequence's rows
+  uint32_t div_m, div_s;            // r / kv_heads = r * div_m >> div_s for r < 2^31
+  uint32_t step_i, step_h;          // 256 words on: step_i tokens and step_h heads
 };
 
 __host__ __device__ constexpr int bit_of(int u) { return 8 * (u >> 2) + 4 * ((u & 3) >> 1) + 16 * (u & 1); }
 
-// Thread's word of sequence s: token i of the call, head h, run c, word t of the run; the cache
-// row, or -1 (out of range: reported; start < 0: the sequence is left out, not reported).
+// A thread's words: run c and word t of it, the same for all its words (256 words are whole
+// rows), and per word token i of the call and head h.
 template <int D>
 struct Place {
+  static constexpr uint32_t NG = D / 32;
   uint32_t c, t, h, i;
-  int64_t row;
-  __device__ Place(const CParams& p, uint32_t s, uint32_t w) {
-    constexpr uint32_t NG = D / 32;
+  __device__ Place(const CParams& p, uint32_t w) {
     t = w & 3;
     c = (w >> 2) % NG;
     const uint32_t r = (w >> 2) / NG;
-    i = r / (uint32_t)p.kv_heads;
+    i = (uint32_t)(((uint64_t)r * p.div_m) >> p.div_s);
     h = r - i * (uint32_t)p.kv_heads;
-    const int start = p.start ? p.start[s] : 0;
-    const int64_t slot = (int64_t)start + i;
-    row = -1;
-    if (start >= 0) {
-      if (slot < p.capacity) row = ((int64_t)s * p.kv_heads + h) * p.capacity + slot;
-      else if (t == 0 && c == 0) atomicOr(&g_cache_err, kErrBadIndex);
+  }
+  __device__ __forceinline__ void next(const CParams& p) {
+    i += p.step_i;
+    h += p.step_h;
+    if (h >= (uint32_t)p.kv_heads) {
+      h -= (uint32_t)p.kv_heads;
+      ++i;
     }
+  }
+  __device__ __forceinline__ __nv_bfloat16* x(const CParams& p, int m, uint32_t s) const {
+    return p.x[m] + s * p.sb[m] + i * p.sn[m] + h * p.sh[m] + 32 * c + 8 * t;
+  }
+  // the cache row, or -1 (out of range: reported; start < 0: the sequence is left out, not reported)
+  __device__ __forceinline__ int64_t row(const CParams& p, uint32_t s, int start) const {
+    if (start < 0) return -1;
+    const uint32_t slot = (uint32_t)start + i;       // below 2^32: start and i are below 2^31
+    if (slot < (uint32_t)p.capacity) return ((int64_t)s * p.kv_heads + h) * p.capacity + slot;
+    if (t == 0 && c == 0) atomicOr(&g_cache_err, kErrBadIndex);
+    return -1;
   }
 };
 
@@ -69,83 +85,136 @@ struct Place {
 // non-negative bf16 numbers is that of the numbers, infinity and NaN last).
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-template <int D>
-__global__ void __launch_bounds__(256) cache4_append_kernel(const __grid_constant__ CParams p) {
-  constexpr int NG = D / 32;
-  const uint32_t w = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t s = blockIdx.y >> 1, m = blockIdx.y & 1;
-  const bool in = w < p.words;                       // whole runs: four threads in or out together
-  const Place<D> at(p, s, in ? w : 0u);
-  uint32_t v[4] = {0u, 0u, 0u, 0u};
-  if (in) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p.x[m] + s * p.sb[m] + at.i * p.sn[m] + at.h * p.sh[m] +
-                                                    32 * at.c + 8 * at.t);
-    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
-  }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The code word of 8 elements (bf16 pairs v), and their run's scale (all 32 lanes call).
+__device__ __forceinline__ uint32_t quantise(const uint4& r, __nv_bfloat16& scale) {
+  const uint32_t v[4] = {r.x, r.y, r.z, r.w};
   constexpr uint32_t kAbs = 0x7fff7fffu;
   uint32_t top = max2(max2(v[0] & kAbs, v[1] & kAbs), max2(v[2] & kAbs, v[3] & kAbs));
   top = max2(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max2(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const uint32_t amax = max(top & 0xffffu, top >> 16);             // bf16 bits
   // a run with an infinity or a NaN has the scale NaN
-  const __nv_bfloat16 sb =
-      __float2bfloat16_rn(amax >= 0x7f80u ? __int_as_float(0x7fc00000) : __fdiv_rn(__uint_as_float(amax << 16), 7.f));
-  float sc = __bfloat162float(sb);
-  // scales below 2^-64 (the last ones subnormal): 1 / s would overflow, so x and s are taken times
-  // 2^70, exactly; and there s = amax / 7 is so coarse that a code can come out past 7
-  const bool tiny = sc < 5.421010862427522e-20f;
-  const float up = tiny ? 1.1805916207174113e21f : 1.f;
-  sc *= up;
-  const float inv = sc > 0.f ? __fdiv_rn(1.f, sc) * up : 0.f;      // NaN: 0
+  scale = __float2bfloat16_rn(amax >= 0x7f80u ? __int_as_float(0x7fc00000)
+                                              : __uint_as_float(amax << 16) * 0.14285714924335480f);
+  const float sc = __bfloat162float(scale);
   uint32_t word = 0u;
+  if (!(sc < 5.421010862427522e-20f)) {
+    const float inv = rcp_approx(sc);                // NaN: the codes are not used
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const float x = __uint_as_float(u & 1 ? v[u >> 1] & 0xffff0000u : v[u >> 1] << 16);
-    float q = x * inv;
-    if (tiny) q = fminf(fmaxf(x * up * (sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f), -7.f), 7.f);
-    // to a multiple of 2^-15, then to an integer, stored + 8 in the last bits of 1.5 x 2^23 + code
-    const float e = __fadd_rn(__fadd_rn(q, 384.f), -384.f);
-    word |= (__float_as_uint(__fadd_rn(e, 12582920.f)) & 15u) << bit_of(u);
+    for (int u = 0; u < 8; ++u) {
+      const float x = __uint_as_float(u & 1 ? v[u >> 1] & 0xffff0000u : v[u >> 1] << 16);
+      // to a multiple of 2^-15, then to an integer, stored + 8 in the last bits of 1.5 x 2^23 + code
+      const float e = __fadd_rn(__fadd_rn(x * inv, 384.f), -384.f);
+      word |= (__float_as_uint(__fadd_rn(e, 12582920.f)) & 15u) << bit_of(u);
+    }
+    if (amax >= 0x7f80u) word = 0x88888888u;
+  } else {
+    // scales below 2^-64, the last ones subnormal: 1 / s could overflow, and s can be so coarse that
+    // a code comes out past 7; the division and the limits then
+#pragma unroll 1
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t pair = u < 4 ? (u < 2 ? v[0] : v[1]) : (u < 6 ? v[2] : v[3]);
+      const float x = __uint_as_float(u & 1 ? pair & 0xffff0000u : pair << 16);
+      const float q = sc > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x, sc)), -7.f), 7.f) : 0.f;
+      word |= (uint32_t)((int)q + 8) << bit_of(u);
+    }
   }
-  if (amax >= 0x7f80u) word = 0x88888888u;
-  if (in && at.row >= 0) {
-    p.codes[m][at.row * (D / 8) + at.t * NG + at.c] = word;
-    if (at.t == 0) p.scales[m][at.row * NG + at.c] = sb;
+  return word;
+}
+
+template <int D, int M>
+__device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint32_t w, int start) {
+  const Place<D> first(p, w);
+  uint4 v[kWords];
+  Place<D> at = first;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {                 // whole runs: four threads in or out together
+    v[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (w + 256u * k < p.words) v[k] = *reinterpret_cast<const uint4*>(at.x(p, M, s));
+    at.next(p);
+  }
+  at = first;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    __nv_bfloat16 scale;
+    const uint32_t word = quantise(v[k], scale);
+    if (w + 256u * k < p.words) {
+      const int64_t row = at.row(p, s, start);
+      if (row >= 0) {
+        p.codes[M][row * (D / 8) + at.t * Place<D>::NG + at.c] = word;
+        if (at.t == 0) p.scales[M][row * Place<D>::NG + at.c] = scale;
+      }
+    }
+    at.next(p);
+  }
+}
+
+template <int D, int M>
+__device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_t w, int start) {
+  const Place<D> first(p, w);
+  uint32_t word[kWords];
+  __nv_bfloat16 scale[kWords];
+  Place<D> at = first;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    word[k] = 0x88888888u;                           // rows outside the cache read as zeros
+    scale[k] = __float2bfloat16_rn(0.f);
+    if (w + 256u * k < p.words) {
+      const int64_t row = at.row(p, s, start);
+      if (row >= 0) {
+        word[k] = p.codes[M][row * (D / 8) + at.t * Place<D>::NG + at.c];
+        scale[k] = p.scales[M][row * Place<D>::NG + at.c];
+      }
+    }
+    at.next(p);
+  }
+  at = first;
+  const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    // pair e of the word is elements 2e, 2e + 1: 128 + code over the bits of 128, exact, minus 136,
+    // times the scale with one rounding
+    const __nv_bfloat162 s2 = __halves2bfloat162(scale[k], scale[k]);
+    uint32_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = ((word[k] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+      const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), off), s2);
+      v[e] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    if (w + 256u * k < p.words) *reinterpret_cast<uint4*>(at.x(p, M, s)) = make_uint4(v[0], v[1], v[2], v[3]);
+    at.next(p);
+  }
+}
+
+// One CTA per 1024 words of a sequence's keys or values (K and V interleaved in y).
+template <int D, bool READ>
+__global__ void __launch_bounds__(256) cache4_kernel(const __grid_constant__ CParams p) {
+  const uint32_t w = blockIdx.x * (256u * kWords) + threadIdx.x, s = blockIdx.y >> 1;
+  const int start = p.start ? p.start[s] : 0;
+  if constexpr (READ) {
+    if (blockIdx.y & 1) read_words<D, 1>(p, s, w, start);
+    else read_words<D, 0>(p, s, w, start);
+  } else {
+    if (blockIdx.y & 1) append_words<D, 1>(p, s, w, start);
+    else append_words<D, 0>(p, s, w, start);
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) cache4_read_kernel(const __grid_constant__ CParams p) {
-  constexpr int NG = D / 32;
-  const uint32_t w = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t s = blockIdx.y >> 1, m = blockIdx.y & 1;
-  if (w >= p.words) return;
-  const Place<D> at(p, s, w);
-  uint32_t word = 0x88888888u;                       // rows outside the cache read as zeros
-  __nv_bfloat16 sc = __float2bfloat16_rn(0.f);
-  if (at.row >= 0) {
-    word = p.codes[m][at.row * (D / 8) + at.t * NG + at.c];
-    sc = p.scales[m][at.row * NG + at.c];
-  }
-  // pair k of the word is elements 2k, 2k + 1: 128 + code over the bits of 128, exact, minus 136,
-  // times the scale with one rounding
-  const __nv_bfloat162 s2 = __halves2bfloat162(sc, sc), off = __floats2bfloat162_rn(136.f, 136.f);
-  uint32_t v[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t x = ((word >> (4 * k)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), off), s2);
-    v[k] = *reinterpret_cast<const uint32_t*>(&y);
-  }
-  *reinterpret_cast<uint4*>(p.x[m] + s * p.sb[m] + at.i * p.sn[m] + at.h * p.sh[m] + 32 * at.c + 8 * at.t) =
-      make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-template <int D>
-int launch(const Cache4Args& a, const CParams& p, cudaStream_t stream) {
-  const dim3 grid((p.words + 255u) / 256u, 2 * a.batch);
-  if (a.read) cache4_read_kernel<D><<<grid, 256, 0, stream>>>(p);
-  else cache4_append_kernel<D><<<grid, 256, 0, stream>>>(p);
+int launch(const Cache4Args& a, CParams& p, cudaStream_t stream) {
+  const uint32_t rows = 256 / (D / 8);               // rows in 256 words
+  p.step_i = rows / (uint32_t)a.kv_heads;
+  p.step_h = rows % (uint32_t)a.kv_heads;
+  const dim3 grid((p.words + 256u * kWords - 1) / (256u * kWords), 2 * a.batch);
+  if (a.read) cache4_kernel<D, true><<<grid, 256, 0, stream>>>(p);
+  else cache4_kernel<D, false><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -168,6 +237,12 @@ int launch_cache4(const Cache4Args& a, cudaStream_t stream) {
   }
   p.kv_heads = a.kv_heads;
   p.capacity = a.capacity;
+  // x / d = x * m >> (31 + k), 2^k >= d, m = ceil(2^(31 + k) / d): m d is off 2^(31 + k) by less than
+  // d <= 2^k, so x < 2^31 times that stays below 2^(31 + k)
+  uint32_t k = 0;
+  while ((1u << k) < (uint32_t)a.kv_heads) ++k;
+  p.div_s = 31 + k;
+  p.div_m = (uint32_t)(((1ull << p.div_s) + a.kv_heads - 1) / a.kv_heads);
   p.words = (uint32_t)a.n_tokens * a.kv_heads * (a.head_dim / 8);
   switch (a.head_dim) {
     case 32: return launch<32>(a, p, stream);

@@ -162,7 +162,7 @@ def test_cache4_refusals(lib, read):
                 dict(n=0), dict(kv_heads=0), dict(capacity=0)):
         assert c.with_(**bad) == INVALID, bad
     for bad in (dict(d=16), dict(capacity=60), dict(capacity=(1 << 30) + 8), dict(k=A + 8), dict(vc=A + 4), dict(vs=A + 2),
-                dict(vst=S3(512, 128, 60)), dict(n=1 << 26, kv_heads=16), dict(batch=40000)):
+                dict(vst=S3(512, 128, 60)), dict(n=1 << 25, kv_heads=16), dict(batch=40000)):
         assert c.with_(**bad) == UNSUPPORTED, bad
 
 
