@@ -24,11 +24,11 @@
 // window are cut into chunks of query tiles as long as an ordinary item, whose fp32 sums of the
 // sinks' rows go to the workspace and are added in a fixed order.
 //
-// One persistent CTA per SM (320 threads), items dealt out in turn:
+// One persistent CTA per SM (18 warps), items dealt out in turn:
 //   warp 0      lane 0 loads the stationary tiles and the ring by TMA
 //   warp 1      owns TMEM; lane 0 issues the MMAs
-//   warps 2-9   compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
-//               columns 64 h .. 64 h + 63 of a step, h = (w - 2) / 4; at an item's end they write
+//   warps 2-17  compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
+//               columns 32 c .. 32 c + 31 of a step, c = (w - 2) / 4; at an item's end they write
 //               its rows. An item's S and dP run under the previous item's output.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -46,8 +46,8 @@ namespace {
 __device__ unsigned int g_sink_bwd_err;
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;
-constexpr int kComputeWarps = 8;
+constexpr int kComputeWarps = 16;     // four per TMEM lane quarter, 32 columns of a step each
+constexpr int kThreads = 32 * (2 + kComputeWarps);
 constexpr int kMaxStages = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128;
@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr bool OWN = !KV || D <= 64;
   static constexpr uint32_t COL_P = OWN ? 256 : kColS;
   static constexpr uint32_t COL_DS = OWN ? (KV ? 320 : 256) : kColDP;
-  static constexpr uint32_t HALF = OWN ? 32 : 64;      // columns between the halves' P (or dS)
+  static constexpr uint32_t PART = OWN ? 16 : 32;      // TMEM columns between two warps' P (or dS)
   static constexpr uint32_t COL_ACC0 = KV ? (OWN ? 384 : 256) : 320;      // dQ or dK
   static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;                      // dV
   static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
@@ -272,7 +272,7 @@ struct Issuer {
     constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks)
-      mma_bf16_ts(tmem + col, tmem + a + C::HALF * (ks >> 2) + 8u * (ks & 3), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
+      mma_bf16_ts(tmem + col, tmem + a + C::PART * (ks >> 1) + 8u * (ks & 1), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
                   idesc, (acc || ks > 0) ? 1u : 0u);
   }
   // S of step g: its columns are free once step g - 1's are loaded (OWN), or once the product of
@@ -351,7 +351,7 @@ __device__ void issuer(const BParams& p, Bars& bars, uint8_t* sFix, uint8_t* sRi
   drain_bar(&bars.drain, 0);
 }
 
-// ------------------------------------------------------------------ compute (warps 2-9)
+// ------------------------------------------------------------------ compute (warps 2-17)
 
 // Bits b in [lo, hi] of 32.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
@@ -372,12 +372,11 @@ template <int D, bool KV>
 __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t tmem, volatile int* abort_flag) {
   using C = Cfg<D, KV>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  const int quarter = warp & 3, part = (warp - 2) >> 2;
   const int row = quarter * 32 + lane;
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
-  const uint32_t tS = base + kColS + 64u * half, tDP = base + kColDP + 64u * half;
-  const uint32_t tPout = base + C::COL_P + C::HALF * half, tDSout = base + C::COL_DS + C::HALF * half;
-  const float kNegInf = __int_as_float(0xff800000);
+  const uint32_t tS = base + kColS + 32u * part, tDP = base + kColDP + 32u * part;
+  const uint32_t tPout = base + C::COL_P + C::PART * part, tDSout = base + C::COL_DS + C::PART * part;
   const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
   int g = 0, n = 0;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
@@ -392,33 +391,30 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
     for (int j = 0; j < it.steps; ++j, ++g) {
       int head, tile;
       step_rows<KV>(p, it, j, head, tile);
-      const int c0 = tile * kTile + 64 * half;
-      const uint32_t see0 = visible<KV>(tok, c0, p.window, p.sinks);
-      const uint32_t see1 = visible<KV>(tok, c0 + 32, p.window, p.sinks);
-      const bool any = __any_sync(0xffffffffu, (see0 | see1) != 0u);
-      const bool full = __all_sync(0xffffffffu, (see0 & see1) == 0xffffffffu);
+      const uint32_t see = visible<KV>(tok, tile * kTile + 32 * part, p.window, p.sinks);
+      const bool any = __any_sync(0xffffffffu, see != 0u);
+      const bool full = __all_sync(0xffffffffu, see == 0xffffffffu);
       const int st = g % C::STAGES;
-      const float* vec = reinterpret_cast<const float*>(sRing + st * C::STAGE + 2 * C::TILE) + 64 * half;
+      const float* vec = reinterpret_cast<const float*>(sRing + st * C::STAGE + 2 * C::TILE) + 32 * part;
       if (!__all_sync(0xffffffffu, wait_bar(&bars.s_full, (uint32_t)g & 1u, abort_flag))) return;
       tc_fence_after();
       // ---- P
-      float pr[64];
+      float pr[32];
       if (any) {
-        uint32_t v[64];
+        uint32_t v[32];
         tmem_ld_x32(tS, v);
-        tmem_ld_x32(tS + 32, v + 32);
         if (KV) {
           // the stage's -LSE and D have landed with its tiles
           if (!__all_sync(0xffffffffu, wait_bar(&bars.st_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) return;
         }
-        tmem_ld_wait<64>(v);
+        tmem_ld_wait<32>(v);
         if (C::OWN) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_free);
         }
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
+        for (int e = 0; e < 32; e += 4) {
           float4 L = make_float4(nl2, nl2, nl2, nl2);
           if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + e);
           const uint64_t s01 = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
@@ -431,7 +427,7 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
         }
         if (!full) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) pr[e] = (((e < 32 ? see0 : see1) >> (e & 31)) & 1u) ? pr[e] : 0.f;
+          for (int e = 0; e < 32; ++e) pr[e] = ((see >> e) & 1u) ? pr[e] : 0.f;
         }
       } else {
         if (C::OWN) {
@@ -439,18 +435,18 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
           if (lane == 0) mbar_arrive(&bars.s_free);
         }
 #pragma unroll
-        for (int e = 0; e < 64; ++e) pr[e] = 0.f;
+        for (int e = 0; e < 32; ++e) pr[e] = 0.f;
       }
       if constexpr (KV) {
-        uint32_t pk[32];
+        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) pk[e >> 1] = pack_bf16x2(pr[e], pr[e + 1]);
+        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack_bf16x2(pr[e], pr[e + 1]);
         if (C::OWN && g > 0) {
           // the previous step's dV product has read P
           if (!__all_sync(0xffffffffu, wait_bar(&bars.dv_done, (uint32_t)(g - 1) & 1u, abort_flag))) return;
           tc_fence_after();
         }
-        tmem_st_x32(tPout, pk);
+        tmem_st_x16(tPout, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -459,31 +455,27 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
       // ---- dS = P (dP - D)
       if (!__all_sync(0xffffffffu, wait_bar(&bars.dp_full, (uint32_t)g & 1u, abort_flag))) return;
       tc_fence_after();
-      uint32_t ds[32];
+      uint32_t ds[16];
       if (any) {
+        uint32_t v[32];
+        tmem_ld_x32(tDP, v);
+        tmem_ld_wait<32>(v);
+        if (C::OWN) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.dp_free);
+        }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-          tmem_ld_x32(tDP + 32 * q, v);
-          tmem_ld_wait<32>(v);
-          if (C::OWN && q == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.dp_free);
-          }
+        for (int e = 0; e < 32; e += 4) {
+          float4 L = make_float4(dval, dval, dval, dval);
+          if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + 128 + e);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 L = make_float4(dval, dval, dval, dval);
-            if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + 128 + 32 * q + e);
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
-              float y0, y1;
-              f2_unpack(f2_mul(f2_pack(pr[32 * q + e + i], pr[32 * q + e + i + 1]),
-                               f2_sub(f2_pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1])), d2)),
-                        y0, y1);
-              ds[16 * q + ((e + i) >> 1)] = pack_bf16x2(y0, y1);
-            }
+          for (int i = 0; i < 4; i += 2) {
+            const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
+            const uint64_t dp = f2_pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1]));
+            float y0, y1;
+            f2_unpack(f2_mul(f2_pack(pr[e + i], pr[e + i + 1]), f2_sub(dp, d2)), y0, y1);
+            ds[(e + i) >> 1] = pack_bf16x2(y0, y1);
           }
         }
       } else {
@@ -492,54 +484,48 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
           if (lane == 0) mbar_arrive(&bars.dp_free);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) ds[e] = 0u;
+        for (int e = 0; e < 16; ++e) ds[e] = 0u;
       }
       if (C::OWN && g > 0) {
         // the previous step's product has read dS
         if (!__all_sync(0xffffffffu, wait_bar(&bars.dk_done, (uint32_t)(g - 1) & 1u, abort_flag))) return;
         tc_fence_after();
       }
-      tmem_st_x32(tDSout, ds);
+      tmem_st_x16(tDSout, ds);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.ds_full);
     }
-    // ---- the item's rows
+    // ---- the item's rows: each warp a share of the columns, 16 at a time
     if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return;
     tc_fence_after();
-    constexpr int DH = D / 2;
-    const bool part = KV && it.slot >= 0 && tok < p.sinks;          // an fp32 partial sum
-    const bool store = !part && tok < p.n_tokens && it.slot <= 0;   // a sink chunk writes sinks only
+    const bool sum = KV && it.slot >= 0 && tok < p.sinks;          // an fp32 partial sum
+    const bool store = !sum && tok < p.n_tokens && it.slot <= 0;   // a sink chunk writes sinks only
 #pragma unroll 1
-    for (int m = 0; m < (KV ? 2 : 1); ++m) {
+    for (int c = part; c < (KV ? 2 : 1) * (D / 16); c += kComputeWarps / 4) {
+      const int m = c / (D / 16), col = 16 * (c % (D / 16));
       const float f = m ? 1.f : p.scale;
-      __nv_bfloat16* orow =
-          (m ? p.out1 : p.out0) + it.s * p.os_b[m] + tok * p.os_n[m] + it.head * p.os_h[m] + DH * half;
-      float* prow = nullptr;
-      if (part)
-        prow = p.partial + DH * half +
-               (((((int64_t)it.s * p.kv_heads + it.head) * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D;
-#pragma unroll 1
-      for (int c = 0; c < DH / 16; ++c) {
-        uint32_t w[16];
-        tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)(DH * half + 16 * c), w);
-        tmem_ld_wait<16>(w);
-        if (store) {
-          uint32_t pkd[8];
+      uint32_t w[16];
+      tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)col, w);
+      tmem_ld_wait<16>(w);
+      if (store) {
+        uint32_t pkd[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            pkd[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
-          uint4* dst = reinterpret_cast<uint4*>(orow + 16 * c);
-          dst[0] = make_uint4(pkd[0], pkd[1], pkd[2], pkd[3]);
-          dst[1] = make_uint4(pkd[4], pkd[5], pkd[6], pkd[7]);
-        } else if (part) {
+        for (int e = 0; e < 16; e += 2)
+          pkd[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
+        uint4* dst = reinterpret_cast<uint4*>((m ? p.out1 : p.out0) + it.s * p.os_b[m] + tok * p.os_n[m] +
+                                              it.head * p.os_h[m] + col);
+        dst[0] = make_uint4(pkd[0], pkd[1], pkd[2], pkd[3]);
+        dst[1] = make_uint4(pkd[4], pkd[5], pkd[6], pkd[7]);
+      } else if (sum) {
+        float* prow = p.partial + col +
+                      (((((int64_t)it.s * p.kv_heads + it.head) * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D;
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(prow + 16 * c + e) =
-                make_float4(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f, __uint_as_float(w[e + 2]) * f,
-                            __uint_as_float(w[e + 3]) * f);
-        }
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(prow + e) =
+              make_float4(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f, __uint_as_float(w[e + 2]) * f,
+                          __uint_as_float(w[e + 3]) * f);
       }
     }
     // The next item's first product into the accumulators follows these loads: its issuer waits

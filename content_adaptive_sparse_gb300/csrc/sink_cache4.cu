@@ -12,8 +12,8 @@
 // The word order puts what one lane of the decoding kernel's fragments needs side by side: word
 // (t, c) for all c in one load, pairs (2k, 2k + 1) in the two half-words at the same nibble.
 //
-// One thread per word (four words a thread, loaded before the first is worked on): 16 bytes of the
-// row, the run's maximum over its four threads by shuffles.
+// One thread per word at a time: 16 bytes of the row, the run's maximum over its four threads by
+// shuffles.
 // The rounding takes no division: the approximate q = x (1 / s) is off by less than 2^-19, while a
 // quotient lies on a border (k + 1/2) or 2^-10 and more away from it, so q is first rounded to a
 // multiple of 2^-15 (adding 384, whose last place that is, and taking it off again), which puts
@@ -31,7 +31,6 @@ namespace {
 
 __device__ unsigned int g_cache_err;
 
-constexpr int kWords = 4;           // words per thread, 256 apart
 
 struct CParams {
   __nv_bfloat16* x[2];              // k, v rows (read by the append, written by the read)
@@ -128,7 +127,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4& r, __nv_bfloat16& scal
   return word;
 }
 
-template <int D, int M>
+template <int D, int M, int kWords>
 __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint32_t w, int start) {
   const Place<D> first(p, w);
   uint4 v[kWords];
@@ -155,7 +154,7 @@ __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint3
   }
 }
 
-template <int D, int M>
+template <int D, int M, int kWords>
 __device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_t w, int start) {
   const Place<D> first(p, w);
   uint32_t word[kWords];
@@ -193,17 +192,17 @@ __device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_
   }
 }
 
-// One CTA per 1024 words of a sequence's keys or values (K and V interleaved in y).
-template <int D, bool READ>
+// One CTA per 256 kWords words of a sequence's keys or values (K and V interleaved in y).
+template <int D, bool READ, int kWords>
 __global__ void __launch_bounds__(256) cache4_kernel(const __grid_constant__ CParams p) {
   const uint32_t w = blockIdx.x * (256u * kWords) + threadIdx.x, s = blockIdx.y >> 1;
   const int start = p.start ? p.start[s] : 0;
   if constexpr (READ) {
-    if (blockIdx.y & 1) read_words<D, 1>(p, s, w, start);
-    else read_words<D, 0>(p, s, w, start);
+    if (blockIdx.y & 1) read_words<D, 1, kWords>(p, s, w, start);
+    else read_words<D, 0, kWords>(p, s, w, start);
   } else {
-    if (blockIdx.y & 1) append_words<D, 1>(p, s, w, start);
-    else append_words<D, 0>(p, s, w, start);
+    if (blockIdx.y & 1) append_words<D, 1, kWords>(p, s, w, start);
+    else append_words<D, 0, kWords>(p, s, w, start);
   }
 }
 
@@ -212,9 +211,20 @@ int launch(const Cache4Args& a, CParams& p, cudaStream_t stream) {
   const uint32_t rows = 256 / (D / 8);               // rows in 256 words
   p.step_i = rows / (uint32_t)a.kv_heads;
   p.step_h = rows % (uint32_t)a.kv_heads;
-  const dim3 grid((p.words + 256u * kWords - 1) / (256u * kWords), 2 * a.batch);
-  if (a.read) cache4_kernel<D, true><<<grid, 256, 0, stream>>>(p);
-  else cache4_kernel<D, false><<<grid, 256, 0, stream>>>(p);
+  // Four words a thread, all loaded before the first is worked on, where that still gives every SM
+  // several CTAs (K and V of 2 x 16384 tokens: append 49 -> 40 us, read 41 -> 28 us); one word a thread
+  // in smaller calls, whose time is one thread's latency (64 sequences of one token: append 3.2 ->
+  // 2.0 us).
+  const bool many = (int64_t)p.words * 2 * a.batch >= (int64_t)1024 * 4 * current_sm_count();
+  const uint32_t per = many ? 1024u : 256u;
+  const dim3 grid((p.words + per - 1) / per, 2 * a.batch);
+  if (many) {
+    if (a.read) cache4_kernel<D, true, 4><<<grid, 256, 0, stream>>>(p);
+    else cache4_kernel<D, false, 4><<<grid, 256, 0, stream>>>(p);
+  } else {
+    if (a.read) cache4_kernel<D, true, 1><<<grid, 256, 0, stream>>>(p);
+    else cache4_kernel<D, false, 1><<<grid, 256, 0, stream>>>(p);
+  }
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
