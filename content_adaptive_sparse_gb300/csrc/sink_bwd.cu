@@ -24,11 +24,11 @@
 // window are cut into chunks of query tiles as long as an ordinary item, whose fp32 sums of the
 // sinks' rows go to the workspace and are added in a fixed order.
 //
-// One persistent CTA per SM (18 warps), items dealt out in turn:
+// One persistent CTA per SM (20 warps), items dealt out in turn:
 //   warp 0      lane 0 loads the stationary tiles and the ring by TMA
-//   warp 1      owns TMEM; lane 0 issues the MMAs
-//   warps 2-17  compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
-//               columns 32 c .. 32 c + 31 of a step, c = (w - 2) / 4; at an item's end they write
+//   warps 1-3   lane 0 issues MMAs (S and dP, dV, dK; or S, dP, dQ); warp 1 owns TMEM
+//   warps 4-19  compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
+//               columns 32 c .. 32 c + 31 of a step, c = w / 4 - 1; at an item's end they write
 //               its rows. An item's S and dP run under the previous item's output.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -46,8 +46,10 @@ namespace {
 __device__ unsigned int g_sink_bwd_err;
 
 constexpr int kTile = 128;
-constexpr int kComputeWarps = 16;     // four per TMEM lane quarter, 32 columns of a step each
-constexpr int kThreads = 32 * (2 + kComputeWarps);
+constexpr int kCols = 32;              // columns of a step per compute warp
+constexpr int kComputeWarps = 4 * kTile / kCols;
+constexpr int kIssuers = 3;           // warps whose lane 0 issues MMAs
+constexpr int kThreads = 32 * (1 + kIssuers + kComputeWarps);
 constexpr int kMaxStages = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128;
@@ -73,7 +75,7 @@ struct Cfg {
   static constexpr bool OWN = !KV || D <= 64;
   static constexpr uint32_t COL_P = OWN ? 256 : kColS;
   static constexpr uint32_t COL_DS = OWN ? (KV ? 320 : 256) : kColDP;
-  static constexpr uint32_t PART = OWN ? 16 : 32;      // TMEM columns between two warps' P (or dS)
+  static constexpr uint32_t PART = OWN ? kCols / 2 : kCols;   // TMEM columns between two warps' P (or dS)
   static constexpr uint32_t COL_ACC0 = KV ? (OWN ? 384 : 256) : 320;      // dQ or dK
   static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;                      // dV
   static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
@@ -104,7 +106,7 @@ struct Bars {
   uint64_t p_full, ds_full;         // P / dS stored by the compute warps
   uint64_t dv_done, dk_done;        // products of P (dV) and of dS (dK or dQ) complete
   uint64_t acc_full;                // an item's accumulators complete (phase: item)
-  uint64_t drain;
+  uint64_t drain[kIssuers];
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -185,18 +187,24 @@ __device__ __forceinline__ Item decode_item(const BParams& p, int k) {
   return it;
 }
 
-// Moving rows of step j: head and tile.
+// Moving rows of an item's steps, in order: head and tile.
 template <bool KV>
-__device__ __forceinline__ void step_rows(const BParams& p, const Item& it, int j, int& head, int& tile) {
-  if constexpr (KV) {
-    const int hh = j / it.per;
-    head = it.head * p.group + hh;
-    tile = it.tile0 + j - hh * it.per;
-  } else {
-    head = it.head / p.group;
-    tile = j < it.n_sink ? 0 : it.tile0 + j - it.n_sink;
+struct Steps {
+  int head, tile, last;
+  __device__ Steps(const BParams& p, const Item& it) {
+    head = KV ? it.head * p.group : it.head / p.group;
+    tile = !KV && it.n_sink ? 0 : it.tile0;
+    last = it.tile0 + it.per - 1;
   }
-}
+  __device__ __forceinline__ void next(const Item& it) {
+    if (KV && tile == last) {
+      tile = it.tile0;
+      ++head;
+    } else {
+      tile = !KV && tile < it.tile0 ? it.tile0 : tile + 1;
+    }
+  }
+};
 
 // Descriptor offset (bytes >> 4) of k-step ks (16 head-dimension elements) of a K-major tile.
 template <int D, bool KV>
@@ -223,11 +231,11 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
       tma_load_4d(sFix + c * C::CHUNK, ta0, &bars.fixed_full, c * C::CH, it.head, it.tile * kTile, it.s);
       tma_load_4d(sFix + C::TILE + c * C::CHUNK, ta1, &bars.fixed_full, c * C::CH, it.head, it.tile * kTile, it.s);
     }
-    for (int j = 0; j < it.steps; ++j, ++g) {
+    Steps<KV> at(p, it);
+    for (int j = 0; j < it.steps; ++j, ++g, at.next(it)) {
       const int st = g % C::STAGES;
       if (g >= C::STAGES && !(ok = wait_bar(&bars.st_empty[st], (uint32_t)(g / C::STAGES - 1) & 1u, abort_flag))) break;
-      int head, tile;
-      step_rows<KV>(p, it, j, head, tile);
+      const int head = at.head, tile = at.tile;
       uint8_t* stage = sRing + st * C::STAGE;
       mbar_arrive_expect_tx(&bars.st_full[st], 2 * C::TILE + (KV ? 1024 : 0));
 #pragma unroll
@@ -236,9 +244,9 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
         tma_load_4d(stage + C::TILE + c * C::CHUNK, tb1, &bars.st_full[st], c * C::CH, head, tile * kTile, it.s);
       }
       if constexpr (KV) {
-        const int64_t at = ((int64_t)it.s * p.heads + head) * p.pitch + (int64_t)tile * kTile;
-        bulk_load(stage + 2 * C::TILE, p.nl2 + at, 512, &bars.st_full[st]);
-        bulk_load(stage + 2 * C::TILE + 512, p.dvec + at, 512, &bars.st_full[st]);
+        const int64_t row = ((int64_t)it.s * p.heads + head) * p.pitch + (int64_t)tile * kTile;
+        bulk_load(stage + 2 * C::TILE, p.nl2 + row, 512, &bars.st_full[st]);
+        bulk_load(stage + 2 * C::TILE + 512, p.dvec + row, 512, &bars.st_full[st]);
       }
     }
   }
@@ -249,8 +257,11 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
     drain_bar(&bars.st_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
 }
 
-// ------------------------------------------------------------------ MMA issuer (warp 1, lane 0)
+// ------------------------------------------------------------------ MMA issuers (warps 1-3, lane 0)
 
+// One thread issues an MMA every ~67 cycles and spends hundreds more in the waits between products
+// (the barriers' shared-memory accesses queue behind the tensor core's operand reads), so the
+// products are dealt out to three threads: S and dP, dV, dK; or S, dP, dQ.
 template <int D, bool KV>
 struct Issuer {
   using C = Cfg<D, KV>;
@@ -260,6 +271,9 @@ struct Issuer {
   uint64_t a0, a1, b0, b1, b0mn, b1mn;
 
   __device__ uint64_t at(int st) const { return (uint64_t)((st * C::STAGE) >> 4); }
+  __device__ __forceinline__ bool landed(int g) const {
+    return wait_bar(&bars.st_full[g % C::STAGES], (uint32_t)(g / C::STAGES) & 1u, abort_flag);
+  }
 
   __device__ __forceinline__ void rows_x_rows(uint32_t col, uint64_t a, uint64_t b) const {
     constexpr uint32_t idesc = make_idesc_bf16(128, kTile, 0, 0);
@@ -272,63 +286,47 @@ struct Issuer {
     constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks)
-      mma_bf16_ts(tmem + col, tmem + a + C::PART * (ks >> 1) + 8u * (ks & 1), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
+      mma_bf16_ts(tmem + col, tmem + a + C::PART * (ks / (kCols / 16)) + 8u * (ks % (kCols / 16)), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
                   idesc, (acc || ks > 0) ? 1u : 0u);
   }
   // S of step g: its columns are free once step g - 1's are loaded (OWN), or once the product of
-  // the P that lies over them is complete
-  __device__ __forceinline__ bool scores(int g, int st) const {
+  // the P that lies over them is complete; dP likewise
+  __device__ __forceinline__ bool scores(int g) const {
     if (g > 0 && !wait_bar(C::OWN ? &bars.s_free : &bars.dv_done, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
-    if (!wait_bar(&bars.st_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag)) return false;
+    if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(kColS, a0, b0 + at(st));
+    rows_x_rows(kColS, a0, b0 + at(g % C::STAGES));
     mma_commit(&bars.s_full);
     return true;
   }
-  __device__ __forceinline__ bool products(int g, int st) const {
+  __device__ __forceinline__ bool products(int g) const {
     if (g > 0 && !wait_bar(C::OWN ? &bars.dp_free : &bars.dk_done, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
+    if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(kColDP, a1, b1 + at(st));
+    rows_x_rows(kColDP, a1, b1 + at(g % C::STAGES));
     mma_commit(&bars.dp_full);
     return true;
   }
-  __device__ __forceinline__ bool acc1(int g, int st, bool acc) const {
-    if (!wait_bar(&bars.p_full, (uint32_t)g & 1u, abort_flag)) return false;
+  __device__ __forceinline__ bool acc1(int g, bool acc) const {
+    if (!landed(g) || !wait_bar(&bars.p_full, (uint32_t)g & 1u, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC1, C::COL_P, b1mn + at(st), acc);
+    pairs_x_tile(C::COL_ACC1, C::COL_P, b1mn + at(g % C::STAGES), acc);
+    mma_commit(&bars.st_empty[g % C::STAGES]);
     mma_commit(&bars.dv_done);
     return true;
   }
-  __device__ __forceinline__ bool acc0(int g, int st, bool acc) const {
-    if (!wait_bar(&bars.ds_full, (uint32_t)g & 1u, abort_flag)) return false;
+  __device__ __forceinline__ bool acc0(int g, bool acc) const {
+    if (!landed(g) || !wait_bar(&bars.ds_full, (uint32_t)g & 1u, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC0, C::COL_DS, b0mn + at(st), acc);
-    mma_commit(&bars.st_empty[st]);
+    pairs_x_tile(C::COL_ACC0, C::COL_DS, b0mn + at(g % C::STAGES), acc);
+    mma_commit(&bars.st_empty[g % C::STAGES]);
     mma_commit(&bars.dk_done);
-    return true;
-  }
-  // One item of `steps` steps from step g on
-  __device__ bool item(int g, int steps) const {
-    if (!scores(g, g % C::STAGES) || !products(g, g % C::STAGES)) return false;
-    if (steps == 1) mma_commit(&bars.fixed_empty);
-    for (int j = 0; j < steps; ++j, ++g) {
-      const int st = g % C::STAGES, nx = (g + 1) % C::STAGES;
-      const bool more = j + 1 < steps, last = j + 2 == steps;
-      if (C::OWN && more && !scores(g + 1, nx)) return false;
-      if (KV && !acc1(g, st, j > 0)) return false;
-      if (!C::OWN && more && !scores(g + 1, nx)) return false;
-      if (C::OWN && more && !products(g + 1, nx)) return false;
-      if (!acc0(g, st, j > 0)) return false;
-      if (!C::OWN && more && !products(g + 1, nx)) return false;
-      if (last) mma_commit(&bars.fixed_empty);         // the item's last S and dP are issued
-    }
-    mma_commit(&bars.acc_full);
     return true;
   }
 };
 
 template <int D, bool KV>
-__device__ void issuer(const BParams& p, Bars& bars, uint8_t* sFix, uint8_t* sRing, uint32_t tmem,
+__device__ void issuer(const BParams& p, int role, Bars& bars, uint8_t* sFix, uint8_t* sRing, uint32_t tmem,
                        volatile int* abort_flag) {
   using C = Cfg<D, KV>;
   const uint32_t fix = smem_u32(sFix), ring = smem_u32(sRing);
@@ -340,18 +338,27 @@ __device__ void issuer(const BParams& p, Bars& bars, uint8_t* sFix, uint8_t* sRi
                         make_smem_desc(ring, C::CHUNK, C::ATOM, C::SWZ),
                         make_smem_desc(ring + C::TILE, C::CHUNK, C::ATOM, C::SWZ)};
   int g = 0, n = 0;
-  for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
-    const Item it = decode_item<KV>(p, k);
-    if (!wait_bar(&bars.fixed_full, (uint32_t)n & 1u, abort_flag)) break;
-    if (!I.item(g, it.steps)) break;
-    g += it.steps;
+  bool ok = true;
+  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
+    const int steps = decode_item<KV>(p, k).steps;
+    if (role == 2 || (KV && role == 1)) {
+      for (int j = 0; ok && j < steps; ++j, ++g) ok = KV && role == 1 ? I.acc1(g, j > 0) : I.acc0(g, j > 0);
+      if (ok) mma_commit(&bars.acc_full);
+    } else {
+      if (!(ok = wait_bar(&bars.fixed_full, (uint32_t)n & 1u, abort_flag))) break;
+      for (int j = 0; ok && j < steps; ++j, ++g) {
+        if (role == 0) ok = I.scores(g);
+        if (ok && role == (KV ? 0 : 1)) ok = I.products(g);
+      }
+      if (ok) mma_commit(&bars.fixed_empty);           // the item's last S (and dP) are issued
+    }
   }
   // no MMA of this thread is still at work when the CTA frees its TMEM
-  mma_commit(&bars.drain);
-  drain_bar(&bars.drain, 0);
+  mma_commit(&bars.drain[role]);
+  drain_bar(&bars.drain[role], 0);
 }
 
-// ------------------------------------------------------------------ compute (warps 2-17)
+// ------------------------------------------------------------------ compute (warps 4-19)
 
 // Bits b in [lo, hi] of 32.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
@@ -368,134 +375,144 @@ __device__ __forceinline__ uint32_t visible(int r, int c0, int window, int sinks
   else return bit_range(r - window - c0, r - c0) | (bit_range(0, sinks - 1 - c0) & bit_range(0, r - c0));
 }
 
+// How a warp's 32 rows see its columns of a step. Each way has a copy of the step's code: joined
+// by selects, the masks' instructions would be issued in every step (measured: 4 ALU
+// instructions for each exponential).
+enum : int { kNone = 0, kAll = 1, kSome = 2 };
+
+// One warp's part of a step.
+template <int D, bool KV>
+struct Compute {
+  using C = Cfg<D, KV>;
+  Bars& bars;
+  volatile int* abort_flag;
+  uint32_t tS, tDP, tP, tDS;        // TMEM: S, dP (read), P, dS (written), this warp's lanes and columns
+  uint64_t c2;
+  float nl2, dval;                  // dQ: the row's -LSE log2(e) and D
+  bool lead;                        // lane 0
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, int phase) const {
+    return __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)phase & 1u, abort_flag));
+  }
+  // This warp's TMEM accesses so far are done: one arrival.
+  __device__ __forceinline__ void arrive(uint64_t* bar) const {
+    tc_fence_before();
+    __syncwarp();
+    if (lead) mbar_arrive(bar);
+  }
+
+  template <int SEE>
+  __device__ __forceinline__ bool step(int g, const float* vec, uint32_t see) const {
+    if (!wait(&bars.s_full, g)) return false;
+    tc_fence_after();
+    // ---- P
+    float pr[kCols];
+    if constexpr (SEE != kNone) {
+      uint32_t v[kCols];
+      tmem_ld_x32(tS, v);
+      // dK / dV: the stage's -LSE and D have landed with its tiles
+      if (KV && !wait(&bars.st_full[g % C::STAGES], g / C::STAGES)) return false;
+      tmem_ld_wait<kCols>(v);
+      if (C::OWN) arrive(&bars.s_free);
+#pragma unroll
+      for (int e = 0; e < kCols; e += 4) {
+        float4 L = make_float4(nl2, nl2, nl2, nl2);
+        if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + e);
+        const uint64_t s01 = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        const uint64_t s23 = f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        float x[4];
+        f2_unpack(f2_fma(s01, c2, f2_pack(L.x, L.y)), x[0], x[1]);
+        f2_unpack(f2_fma(s23, c2, f2_pack(L.z, L.w)), x[2], x[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (SEE == kSome) x[i] = ((see >> (e + i)) & 1u) ? x[i] : __int_as_float(0xff800000);
+          pr[e + i] = ex2_approx(x[i]);
+        }
+      }
+    } else if (C::OWN) {
+      arrive(&bars.s_free);
+    }
+    if constexpr (KV) {
+      uint32_t pk[kCols / 2];
+#pragma unroll
+      for (int e = 0; e < kCols; e += 2) pk[e >> 1] = SEE != kNone ? pack_bf16x2(pr[e], pr[e + 1]) : 0u;
+      if (C::OWN && g > 0) {
+        // the previous step's dV product has read P
+        if (!wait(&bars.dv_done, g - 1)) return false;
+        tc_fence_after();
+      }
+      tmem_st_x16(tP, pk);
+      tmem_st_wait();
+      arrive(&bars.p_full);
+    }
+    // ---- dS = P (dP - D)
+    if (!wait(&bars.dp_full, g)) return false;
+    tc_fence_after();
+    uint32_t ds[kCols / 2];
+    if constexpr (SEE != kNone) {
+      uint32_t v[kCols];
+      tmem_ld_x32(tDP, v);
+      tmem_ld_wait<kCols>(v);
+      if (C::OWN) arrive(&bars.dp_free);
+#pragma unroll
+      for (int e = 0; e < kCols; e += 4) {
+        float4 L = make_float4(dval, dval, dval, dval);
+        if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + 128 + e);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
+          const uint64_t dp = f2_pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1]));
+          float y0, y1;
+          f2_unpack(f2_mul(f2_pack(pr[e + i], pr[e + i + 1]), f2_sub(dp, d2)), y0, y1);
+          ds[(e + i) >> 1] = pack_bf16x2(y0, y1);
+        }
+      }
+    } else {
+      if (C::OWN) arrive(&bars.dp_free);
+#pragma unroll
+      for (int e = 0; e < kCols / 2; ++e) ds[e] = 0u;
+    }
+    if (C::OWN && g > 0) {
+      // the previous step's product has read dS
+      if (!wait(&bars.dk_done, g - 1)) return false;
+      tc_fence_after();
+    }
+    tmem_st_x16(tDS, ds);
+    tmem_st_wait();
+    arrive(&bars.ds_full);
+    return true;
+  }
+};
+
 template <int D, bool KV>
 __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t tmem, volatile int* abort_flag) {
   using C = Cfg<D, KV>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, part = (warp - 2) >> 2;
+  const int quarter = warp & 3, part = (warp - 1 - kIssuers) >> 2;
   const int row = quarter * 32 + lane;
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
-  const uint32_t tS = base + kColS + 32u * part, tDP = base + kColDP + 32u * part;
-  const uint32_t tPout = base + C::COL_P + C::PART * part, tDSout = base + C::COL_DS + C::PART * part;
-  const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+  Compute<D, KV> W{bars, abort_flag,
+                   base + kColS + (uint32_t)(kCols * part), base + kColDP + (uint32_t)(kCols * part),
+                   base + C::COL_P + C::PART * part, base + C::COL_DS + C::PART * part,
+                   f2_pack(p.scale_log2, p.scale_log2), 0.f, 0.f, lane == 0};
   int g = 0, n = 0;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
     const Item it = decode_item<KV>(p, k);
     const int tok = it.tile * kTile + row;
-    float nl2 = 0.f, dval = 0.f;
     if constexpr (!KV) {
       const int64_t at = ((int64_t)it.s * p.heads + it.head) * p.pitch + tok;
-      nl2 = p.nl2[at];
-      dval = p.dvec[at];
+      W.nl2 = p.nl2[at];
+      W.dval = p.dvec[at];
     }
-    for (int j = 0; j < it.steps; ++j, ++g) {
-      int head, tile;
-      step_rows<KV>(p, it, j, head, tile);
-      const uint32_t see = visible<KV>(tok, tile * kTile + 32 * part, p.window, p.sinks);
-      const bool any = __any_sync(0xffffffffu, see != 0u);
-      const bool full = __all_sync(0xffffffffu, see == 0xffffffffu);
-      const int st = g % C::STAGES;
-      const float* vec = reinterpret_cast<const float*>(sRing + st * C::STAGE + 2 * C::TILE) + 32 * part;
-      if (!__all_sync(0xffffffffu, wait_bar(&bars.s_full, (uint32_t)g & 1u, abort_flag))) return;
-      tc_fence_after();
-      // ---- P
-      float pr[32];
-      if (any) {
-        uint32_t v[32];
-        tmem_ld_x32(tS, v);
-        if (KV) {
-          // the stage's -LSE and D have landed with its tiles
-          if (!__all_sync(0xffffffffu, wait_bar(&bars.st_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) return;
-        }
-        tmem_ld_wait<32>(v);
-        if (C::OWN) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.s_free);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float4 L = make_float4(nl2, nl2, nl2, nl2);
-          if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + e);
-          const uint64_t s01 = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-          const uint64_t s23 = f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-          float x[4];
-          f2_unpack(f2_fma(s01, c2, f2_pack(L.x, L.y)), x[0], x[1]);
-          f2_unpack(f2_fma(s23, c2, f2_pack(L.z, L.w)), x[2], x[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pr[e + i] = ex2_approx(x[i]);
-        }
-        if (!full) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) pr[e] = ((see >> e) & 1u) ? pr[e] : 0.f;
-        }
-      } else {
-        if (C::OWN) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.s_free);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pr[e] = 0.f;
-      }
-      if constexpr (KV) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack_bf16x2(pr[e], pr[e + 1]);
-        if (C::OWN && g > 0) {
-          // the previous step's dV product has read P
-          if (!__all_sync(0xffffffffu, wait_bar(&bars.dv_done, (uint32_t)(g - 1) & 1u, abort_flag))) return;
-          tc_fence_after();
-        }
-        tmem_st_x16(tPout, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full);
-      }
-      // ---- dS = P (dP - D)
-      if (!__all_sync(0xffffffffu, wait_bar(&bars.dp_full, (uint32_t)g & 1u, abort_flag))) return;
-      tc_fence_after();
-      uint32_t ds[16];
-      if (any) {
-        uint32_t v[32];
-        tmem_ld_x32(tDP, v);
-        tmem_ld_wait<32>(v);
-        if (C::OWN) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.dp_free);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float4 L = make_float4(dval, dval, dval, dval);
-          if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + 128 + e);
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
-            const uint64_t dp = f2_pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1]));
-            float y0, y1;
-            f2_unpack(f2_mul(f2_pack(pr[e + i], pr[e + i + 1]), f2_sub(dp, d2)), y0, y1);
-            ds[(e + i) >> 1] = pack_bf16x2(y0, y1);
-          }
-        }
-      } else {
-        if (C::OWN) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.dp_free);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ds[e] = 0u;
-      }
-      if (C::OWN && g > 0) {
-        // the previous step's product has read dS
-        if (!__all_sync(0xffffffffu, wait_bar(&bars.dk_done, (uint32_t)(g - 1) & 1u, abort_flag))) return;
-        tc_fence_after();
-      }
-      tmem_st_x16(tDSout, ds);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.ds_full);
+    Steps<KV> moving(p, it);
+    for (int j = 0; j < it.steps; ++j, ++g, moving.next(it)) {
+      const uint32_t see = visible<KV>(tok, moving.tile * kTile + kCols * part, p.window, p.sinks);
+      const float* vec = reinterpret_cast<const float*>(sRing + (g % C::STAGES) * C::STAGE + 2 * C::TILE) + kCols * part;
+      bool ok;
+      if (__all_sync(0xffffffffu, see == 0xffffffffu)) ok = W.template step<kAll>(g, vec, see);
+      else if (__any_sync(0xffffffffu, see != 0u)) ok = W.template step<kSome>(g, vec, see);
+      else ok = W.template step<kNone>(g, vec, see);
+      if (!ok) return;
     }
     // ---- the item's rows: each warp a share of the columns, 16 at a time
     if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return;
@@ -547,10 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&bars.fixed_full, 1);
-    mbar_init(&bars.fixed_empty, 1);
+    mbar_init(&bars.fixed_empty, KV ? 1 : 2);          // S and dP from one thread, or from two
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bars.st_full[i], 1);
-      mbar_init(&bars.st_empty[i], 1);
+      mbar_init(&bars.st_empty[i], KV ? 2 : 1);        // the products into the accumulators
     }
     mbar_init(&bars.s_full, 1);
     mbar_init(&bars.dp_full, 1);
@@ -560,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars.ds_full, kComputeWarps);
     mbar_init(&bars.dv_done, 1);
     mbar_init(&bars.dk_done, 1);
-    mbar_init(&bars.acc_full, 1);
-    mbar_init(&bars.drain, 1);
+    mbar_init(&bars.acc_full, KV ? 2 : 1);
+    for (int i = 0; i < kIssuers; ++i) mbar_init(&bars.drain[i], 1);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&ta0);
@@ -582,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if ((threadIdx.x & 31) == 0) loader<D, KV>(p, &ta0, &ta1, &tb0, &tb1, bars, sFix, sRing, &abort_flag);
     __syncwarp();
-  } else if (warp == 1) {
-    if ((threadIdx.x & 31) == 0) issuer<D, KV>(p, bars, sFix, sRing, tmem, &abort_flag);
+  } else if (warp <= kIssuers) {
+    if ((threadIdx.x & 31) == 0) issuer<D, KV>(p, warp - 1, bars, sFix, sRing, tmem, &abort_flag);
     __syncwarp();
   } else {
     compute<D, KV>(p, bars, sRing, tmem, &abort_flag);
