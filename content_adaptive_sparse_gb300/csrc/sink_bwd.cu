@@ -68,7 +68,8 @@ struct Cfg {
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr int STAGE = 2 * TILE + 1024;        // B0, B1, then -LSE log2(e) [128] and D [128]
-  static constexpr int SMEM_NEED = 1024 + 2 * TILE + STAGES * STAGE;
+  // then 1 KB per compute warp, from which the outputs leave
+  static constexpr int SMEM_NEED = 1024 + 2 * TILE + STAGES * STAGE + kComputeWarps * 1024;
   // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
   static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
   // P and dS in columns of their own, or over S and dP
@@ -79,7 +80,8 @@ struct Cfg {
   static constexpr uint32_t COL_ACC0 = KV ? (OWN ? 384 : 256) : 320;      // dQ or dK
   static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;                      // dV
   static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
-  static_assert(STAGES <= kMaxStages && SMEM <= 227 * 1024, "shared memory");
+  static_assert(kCols == 32, "one visibility word per thread");
+  static_assert(STAGES <= kMaxStages && SMEM <= 226 * 1024, "shared memory");
 };
 
 struct BParams {
@@ -91,7 +93,7 @@ struct BParams {
   int far_tile;                     // first query tile whose window misses key tile 0
   const float* nl2;                 // [batch][heads][pitch]: -LSE log2(e); -inf past the sequence
   const float* dvec;                // [batch][heads][pitch]: D
-  __nv_bfloat16* out0;              // dQ or dK
+  __nv_bfloat16* out0;              // dK (the sinks' rows, sink_reduce_kernel)
   __nv_bfloat16* out1;              // dV
   int64_t os_b[2], os_n[2], os_h[2];   // strides of out0, out1
   float* partial;                   // [batch][kv_heads][n_chunks + 1][2][sinks][d]
@@ -110,7 +112,7 @@ struct Bars {
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return mbar_wait(bar, parity, abort_flag, &g_sink_bwd_err, kErrTimeout);
+  return mbar_wait_suspend(bar, parity, abort_flag, &g_sink_bwd_err, kErrTimeout);
 }
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
   int never = 0;
@@ -375,11 +377,18 @@ __device__ __forceinline__ uint32_t visible(int r, int c0, int window, int sinks
   else return bit_range(r - window - c0, r - c0) | (bit_range(0, sinks - 1 - c0) & bit_range(0, r - c0));
 }
 
-// How a warp's 32 rows see its columns of a step. Each way has a copy of the step's code: joined
-// by selects, the masks' instructions would be issued in every step (measured: 4 ALU
-// instructions for each exponential).
 enum : int { kNone = 0, kAll = 1, kSome = 2 };
 
+// How rows r0 .. r0 + 31 see columns c0 .. c0 + 31 (see `visible`).
+template <bool KV>
+__device__ __forceinline__ int visibility(int r0, int c0, int window, int sinks) {
+  const int q = KV ? c0 : r0, k = KV ? r0 : c0;        // first query, first key
+  if (q + 31 < k || (q - (k + 31) > window && k >= sinks)) return kNone;
+  return q >= k + 31 && (q + 31 - k <= window || k + 31 < sinks) ? kAll : kSome;
+}
+
+// Each of the three ways of seeing has a copy of the step's code: joined by selects, the mask's
+// instructions would be issued in every step.
 // One warp's part of a step.
 template <int D, bool KV>
 struct Compute {
@@ -402,7 +411,7 @@ struct Compute {
   }
 
   template <int SEE>
-  __device__ __forceinline__ bool step(int g, const float* vec, uint32_t see) const {
+  __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see) const {
     if (!wait(&bars.s_full, g)) return false;
     tc_fence_after();
     // ---- P
@@ -417,7 +426,7 @@ struct Compute {
 #pragma unroll
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(nl2, nl2, nl2, nl2);
-        if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + e);
+        if constexpr (KV) L = ld_shared_f4(vec + 4 * e);
         const uint64_t s01 = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
         const uint64_t s23 = f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
         float x[4];
@@ -457,7 +466,7 @@ struct Compute {
 #pragma unroll
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(dval, dval, dval, dval);
-        if constexpr (KV) L = *reinterpret_cast<const float4*>(vec + 128 + e);
+        if constexpr (KV) L = ld_shared_f4(vec + 512 + 4 * e);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
@@ -485,12 +494,16 @@ struct Compute {
 };
 
 template <int D, bool KV>
-__device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t tmem, volatile int* abort_flag) {
+__device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensorMap* to1, Bars& bars, uint8_t* sRing,
+                        uint32_t tmem, volatile int* abort_flag) {
   using C = Cfg<D, KV>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, part = (warp - 1 - kIssuers) >> 2;
   const int row = quarter * 32 + lane;
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t ring = smem_u32(sRing);
+  uint8_t* out = sRing + C::STAGES * C::STAGE + 1024 * (4 * part + quarter);
+  const uint32_t srow = smem_u32(out) + 32u * lane;
   Compute<D, KV> W{bars, abort_flag,
                    base + kColS + (uint32_t)(kCols * part), base + kColDP + (uint32_t)(kCols * part),
                    base + C::COL_P + C::PART * part, base + C::COL_DS + C::PART * part,
@@ -506,19 +519,23 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
     }
     Steps<KV> moving(p, it);
     for (int j = 0; j < it.steps; ++j, ++g, moving.next(it)) {
-      const uint32_t see = visible<KV>(tok, moving.tile * kTile + kCols * part, p.window, p.sinks);
-      const float* vec = reinterpret_cast<const float*>(sRing + (g % C::STAGES) * C::STAGE + 2 * C::TILE) + kCols * part;
+      const int c0 = moving.tile * kTile + kCols * part;
+      const uint32_t vec = ring + (uint32_t)((g % C::STAGES) * C::STAGE + 2 * C::TILE + 4 * kCols * part);
       bool ok;
-      if (__all_sync(0xffffffffu, see == 0xffffffffu)) ok = W.template step<kAll>(g, vec, see);
-      else if (__any_sync(0xffffffffu, see != 0u)) ok = W.template step<kSome>(g, vec, see);
-      else ok = W.template step<kNone>(g, vec, see);
+      const int see = visibility<KV>(it.tile * kTile + 32 * quarter, c0, p.window, p.sinks);
+      if (see == kAll) ok = W.template step<kAll>(g, vec, 0u);
+      else if (see == kSome) ok = W.template step<kSome>(g, vec, visible<KV>(tok, c0, p.window, p.sinks));
+      else ok = W.template step<kNone>(g, vec, 0u);
       if (!ok) return;
     }
-    // ---- the item's rows: each warp a share of the columns, 16 at a time
-    if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return;
+    // ---- the item's rows: each warp a share of the columns, 16 at a time, through 1 KB of shared
+    // memory (32-byte rows, 32B swizzle) and a TMA store, which drops rows past the sequence. (Stored
+    // straight from the registers, 32 rows in 32 lines per instruction, an item's output took as
+    // long as two steps.)
+    if (!W.wait(&bars.acc_full, n)) return;
     tc_fence_after();
-    const bool sum = KV && it.slot >= 0 && tok < p.sinks;          // an fp32 partial sum
-    const bool store = !sum && tok < p.n_tokens && it.slot <= 0;   // a sink chunk writes sinks only
+    const int tok0 = it.tile * kTile + 32 * quarter;
+    const bool sum = KV && it.slot >= 0 && tok < p.sinks;   // an fp32 partial sum (its bf16 row is written after)
 #pragma unroll 1
     for (int c = part; c < (KV ? 2 : 1) * (D / 16); c += kComputeWarps / 4) {
       const int m = c / (D / 16), col = 16 * (c % (D / 16));
@@ -526,16 +543,24 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
       uint32_t w[16];
       tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)col, w);
       tmem_ld_wait<16>(w);
-      if (store) {
-        uint32_t pkd[8];
+      if (it.slot <= 0) {                                    // a sink chunk has sums only
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        uint32_t pk[8];
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
-          pkd[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
-        uint4* dst = reinterpret_cast<uint4*>((m ? p.out1 : p.out0) + it.s * p.os_b[m] + tok * p.os_n[m] +
-                                              it.head * p.os_h[m] + col);
-        dst[0] = make_uint4(pkd[0], pkd[1], pkd[2], pkd[3]);
-        dst[1] = make_uint4(pkd[4], pkd[5], pkd[6], pkd[7]);
-      } else if (sum) {
+          pk[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
+        const uint32_t swz = (uint32_t)((lane >> 2) & 1) << 4;
+        st_shared_v4(srow + swz, pk[0], pk[1], pk[2], pk[3]);
+        st_shared_v4(srow + (swz ^ 16u), pk[4], pk[5], pk[6], pk[7]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && tok0 < p.n_tokens) {
+          tma_store_4d(m ? to1 : to0, out, col, it.head, tok0, it.s);
+          bulk_commit_group();
+        }
+      }
+      if (sum) {
         float* prow = p.partial + col +
                       (((((int64_t)it.s * p.kv_heads + it.head) * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D;
 #pragma unroll
@@ -548,12 +573,16 @@ __device__ void compute(const BParams& p, Bars& bars, uint8_t* sRing, uint32_t t
     // The next item's first product into the accumulators follows these loads: its issuer waits
     // for the P or dS that this warp stores after them.
   }
+  // this warp's stores are complete before the CTA may exit
+  if (lane == 0) bulk_wait_group<0>();
+  __syncwarp();
 }
 
 template <int D, bool KV>
 __global__ void __launch_bounds__(kThreads, 1)
     sink_bwd_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap ta1,
                     const __grid_constant__ CUtensorMap tb0, const __grid_constant__ CUtensorMap tb1,
+                    const __grid_constant__ CUtensorMap to0, const __grid_constant__ CUtensorMap to1,
                     const __grid_constant__ BParams p) {
   using C = Cfg<D, KV>;
   extern __shared__ uint8_t smem_raw[];
@@ -603,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((threadIdx.x & 31) == 0) issuer<D, KV>(p, warp - 1, bars, sFix, sRing, tmem, &abort_flag);
     __syncwarp();
   } else {
-    compute<D, KV>(p, bars, sRing, tmem, &abort_flag);
+    compute<D, KV>(p, &to0, &to1, bars, sRing, tmem, &abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -703,13 +732,22 @@ int launch(const SinkArgs& a, const BParams& p, cudaStream_t stream) {
   if (!map(&tq, a.q, a.heads, a.q_strides) || !map(&tk, a.k, a.kv_heads, a.k_strides) ||
       !map(&tv, a.v, a.kv_heads, a.v_strides) || !map(&tdo, a.d_o, a.heads, a.do_strides))
     return SA_ERR_UNSUPPORTED;
+  // outputs: boxes of 32 rows by 16 elements
+  CUtensorMap to0, to1;
+  auto omap = [&](CUtensorMap* m, const void* base, int heads, const int64_t st[3]) {
+    return encode_bhnd_map(m, base, a.batch, a.n_tokens, heads, D, st[0], st[1], st[2], 16, 32,
+                           CU_TENSOR_MAP_SWIZZLE_32B);
+  };
+  if (KV ? !omap(&to0, a.dk, a.kv_heads, a.dk_strides) || !omap(&to1, a.dv, a.kv_heads, a.dv_strides)
+         : !omap(&to0, a.dq, a.heads, a.dq_strides) || !omap(&to1, a.dq, a.heads, a.dq_strides))
+    return SA_ERR_UNSUPPORTED;
   const auto kern = sink_bwd_kernel<D, KV>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
   const int sm_count = current_sm_count();
   const int grid = p.n_items < sm_count ? p.n_items : sm_count;
-  if (KV) kern<<<grid, kThreads, C::SMEM, stream>>>(tk, tv, tq, tdo, p);
-  else kern<<<grid, kThreads, C::SMEM, stream>>>(tq, tdo, tk, tv, p);
+  if (KV) kern<<<grid, kThreads, C::SMEM, stream>>>(tk, tv, tq, tdo, to0, to1, p);
+  else kern<<<grid, kThreads, C::SMEM, stream>>>(tq, tdo, tk, tv, to0, to1, p);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -742,10 +780,6 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   BParams pq = p;
   pq.n_items = pq.n_main = a.batch * a.heads * p.tiles;
-  pq.out0 = static_cast<__nv_bfloat16*>(a.dq);
-  pq.os_b[0] = a.dq_strides[0];
-  pq.os_n[0] = a.dq_strides[1];
-  pq.os_h[0] = a.dq_strides[2];
   int st = launch<D, false>(a, pq, stream);
   if (st != SA_OK) return st;
   const Chunks c = sink_chunks(p.tiles, a.window, a.sinks);
