@@ -14,11 +14,13 @@
 //   acc0 += dS B0 and, key-stationary, acc1 += P B1 (A from TMEM as bf16 pairs, B MN-major).
 //   dQ: A = Q, dO; B = K, V.  dK / dV: A = K, V; B = Q, dO (S and dP come out transposed).
 // A tcgen05.mma costs its issuing thread the same ~67 cycles at N = 64 as at N = 128, hence the
-// 128-row steps. At d <= 64 (and for dQ at any d) P and dS have TMEM columns of their own, so the
-// next step's S runs under this step's exponentials and its dP under this step's dS. Key-stationary
-// at d = 128 the accumulators leave no room: P goes over S and dS over dP, and the next S waits
-// for this step's dV product, the next dP for its dK product; products and exponentials still
-// alternate, dK / dP under one step's exponentials, dV / S under its dS.
+// 128-row steps. P (key-stationary) and dS are stored over the S that they come from, each warp over
+// the columns that it alone has read, so that what the issuing threads wait for anyway (P, dS
+// stored; products complete) frees the columns: the compute warps neither announce nor wait for
+// free columns. S has two buffers (steps alternate), and the next step's S runs under this step's
+// exponentials; dP has one, and the next dP runs once this step's dS is stored. Key-stationary at
+// d = 128 the accumulators leave room for one S; there dS goes over dP, the next S waits for this
+// step's dV product and the next dP for its dK product.
 //
 // The sinks are seen by every query: the first key tile's items over the queries past the
 // window are cut into chunks of query tiles as long as an ordinary item, whose fp32 sums of the
@@ -52,7 +54,6 @@ constexpr int kIssuers = 3;           // warps whose lane 0 issues MMAs
 constexpr int kThreads = 32 * (1 + kIssuers + kComputeWarps);
 constexpr int kMaxStages = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColDP = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, bool KV>
@@ -68,17 +69,17 @@ struct Cfg {
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr int STAGE = 2 * TILE + 1024;        // B0, B1, then -LSE log2(e) [128] and D [128]
-  // then 1 KB per compute warp, from which the outputs leave
-  static constexpr int SMEM_NEED = 1024 + 2 * TILE + STAGES * STAGE + kComputeWarps * 1024;
+  // then 1 KB or 2 per compute warp, from which the outputs leave
+  static constexpr int OUT = KV && D <= 64 ? 2 : 1;
+  static constexpr int SMEM_NEED = 1024 + 2 * TILE + STAGES * STAGE + kComputeWarps * 1024 * OUT;
   // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
   static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
-  // P and dS in columns of their own, or over S and dP
-  static constexpr bool OWN = !KV || D <= 64;
-  static constexpr uint32_t COL_P = OWN ? 256 : kColS;
-  static constexpr uint32_t COL_DS = OWN ? (KV ? 320 : 256) : kColDP;
-  static constexpr uint32_t PART = OWN ? kCols / 2 : kCols;   // TMEM columns between two warps' P (or dS)
-  static constexpr uint32_t COL_ACC0 = KV ? (OWN ? 384 : 256) : 320;      // dQ or dK
-  static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;                      // dV
+  // TMEM columns: S (one buffer or two), dP, accumulators. P is stored over the first half of the
+  // kCols columns of S that a warp reads, dS over the second half, or over the first half of its dP.
+  static constexpr int SB = KV && D == 128 ? 1 : 2;
+  static constexpr uint32_t COL_DP = 128 * SB;
+  static constexpr uint32_t COL_ACC0 = COL_DP + 128;   // dQ or dK
+  static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;   // dV
   static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
   static_assert(kCols == 32, "one visibility word per thread");
   static_assert(STAGES <= kMaxStages && SMEM <= 226 * 1024, "shared memory");
@@ -103,16 +104,21 @@ struct BParams {
 struct Bars {
   uint64_t fixed_full, fixed_empty;                     // stationary tiles (phase: item)
   uint64_t st_full[kMaxStages], st_empty[kMaxStages];   // ring
-  uint64_t s_full, dp_full;         // S / dP written (phase: step)
-  uint64_t s_free, dp_free;         // S / dP loaded by the compute warps
-  uint64_t p_full, ds_full;         // P / dS stored by the compute warps
-  uint64_t dv_done, dk_done;        // products of P (dV) and of dS (dK or dQ) complete
+  // Steps alternate between two barriers (phase: step / 2) where a wait for one step could meet the
+  // next one's completion
+  uint64_t s_full[2], dp_full;      // S / dP written
+  uint64_t p_full[2], ds_full[2];   // P / dS stored by the compute warps
+  uint64_t dv_done[2], dk_done[2];  // products of P (dV) and of dS (dK or dQ) complete
   uint64_t acc_full;                // an item's accumulators complete (phase: item)
   uint64_t drain[kIssuers];
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return mbar_wait_suspend(bar, parity, abort_flag, &g_sink_bwd_err, kErrTimeout);
+}
+// The barrier of step g of a pair.
+__device__ __forceinline__ bool wait_pair(uint64_t (&bar)[2], int g, volatile int* abort_flag) {
+  return wait_bar(&bar[g & 1], (uint32_t)(g >> 1) & 1u, abort_flag);
 }
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
   int never = 0;
@@ -288,41 +294,45 @@ struct Issuer {
     constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks)
-      mma_bf16_ts(tmem + col, tmem + a + C::PART * (ks / (kCols / 16)) + 8u * (ks % (kCols / 16)), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
+      mma_bf16_ts(tmem + col, tmem + a + (uint32_t)(kCols * (ks / (kCols / 16)) + 8 * (ks % (kCols / 16))), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
                   idesc, (acc || ks > 0) ? 1u : 0u);
   }
-  // S of step g: its columns are free once step g - 1's are loaded (OWN), or once the product of
-  // the P that lies over them is complete; dP likewise
+  static __device__ constexpr uint32_t col_s(int g) { return C::SB == 2 ? 128u * (g & 1) : 0u; }
+  static __device__ constexpr uint32_t col_ds(int g) { return C::SB == 2 ? col_s(g) + kCols / 2 : C::COL_DP; }
+  // S of step g, once the P and dS that lay over its columns are used; dP once step g - 1's is used
   __device__ __forceinline__ bool scores(int g) const {
-    if (g > 0 && !wait_bar(C::OWN ? &bars.s_free : &bars.dv_done, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
+    if (g >= C::SB) {
+      if (KV && !wait_pair(bars.dv_done, g - C::SB, abort_flag)) return false;
+      if (C::SB == 2 && !wait_pair(bars.dk_done, g - 2, abort_flag)) return false;
+    }
     if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(kColS, a0, b0 + at(g % C::STAGES));
-    mma_commit(&bars.s_full);
+    rows_x_rows(col_s(g), a0, b0 + at(g % C::STAGES));
+    mma_commit(&bars.s_full[g & 1]);
     return true;
   }
   __device__ __forceinline__ bool products(int g) const {
-    if (g > 0 && !wait_bar(C::OWN ? &bars.dp_free : &bars.dk_done, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
+    if (g > 0 && !wait_pair(C::SB == 2 ? bars.ds_full : bars.dk_done, g - 1, abort_flag)) return false;
     if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(kColDP, a1, b1 + at(g % C::STAGES));
+    rows_x_rows(C::COL_DP, a1, b1 + at(g % C::STAGES));
     mma_commit(&bars.dp_full);
     return true;
   }
   __device__ __forceinline__ bool acc1(int g, bool acc) const {
-    if (!landed(g) || !wait_bar(&bars.p_full, (uint32_t)g & 1u, abort_flag)) return false;
+    if (!landed(g) || !wait_pair(bars.p_full, g, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC1, C::COL_P, b1mn + at(g % C::STAGES), acc);
+    pairs_x_tile(C::COL_ACC1, col_s(g), b1mn + at(g % C::STAGES), acc);
     mma_commit(&bars.st_empty[g % C::STAGES]);
-    mma_commit(&bars.dv_done);
+    mma_commit(&bars.dv_done[g & 1]);
     return true;
   }
   __device__ __forceinline__ bool acc0(int g, bool acc) const {
-    if (!landed(g) || !wait_bar(&bars.ds_full, (uint32_t)g & 1u, abort_flag)) return false;
+    if (!landed(g) || !wait_pair(bars.ds_full, g, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC0, C::COL_DS, b0mn + at(g % C::STAGES), acc);
+    pairs_x_tile(C::COL_ACC0, col_ds(g), b0mn + at(g % C::STAGES), acc);
     mma_commit(&bars.st_empty[g % C::STAGES]);
-    mma_commit(&bars.dk_done);
+    mma_commit(&bars.dk_done[g & 1]);
     return true;
   }
 };
@@ -395,16 +405,14 @@ struct Compute {
   using C = Cfg<D, KV>;
   Bars& bars;
   volatile int* abort_flag;
-  uint32_t tS, tDP, tP, tDS;        // TMEM: S, dP (read), P, dS (written), this warp's lanes and columns
+  uint32_t tS, tDP;                 // TMEM: S (first buffer) and dP, this warp's lanes and columns
   uint64_t c2;
   float nl2, dval;                  // dQ: the row's -LSE log2(e) and D
   bool lead;                        // lane 0
 
-  __device__ __forceinline__ bool wait(uint64_t* bar, int phase) const {
-    return __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)phase & 1u, abort_flag));
-  }
-  // This warp's TMEM accesses so far are done: one arrival.
+  // This warp's TMEM stores are done: one arrival.
   __device__ __forceinline__ void arrive(uint64_t* bar) const {
+    tmem_st_wait();
     tc_fence_before();
     __syncwarp();
     if (lead) mbar_arrive(bar);
@@ -412,17 +420,18 @@ struct Compute {
 
   template <int SEE>
   __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see) const {
-    if (!wait(&bars.s_full, g)) return false;
+    const uint32_t tSg = tS + (C::SB == 2 ? 128u * (g & 1) : 0u);
+    if (!__all_sync(0xffffffffu, wait_pair(bars.s_full, g, abort_flag))) return false;
     tc_fence_after();
     // ---- P
     float pr[kCols];
     if constexpr (SEE != kNone) {
       uint32_t v[kCols];
-      tmem_ld_x32(tS, v);
+      tmem_ld_x32(tSg, v);
       // dK / dV: the stage's -LSE and D have landed with its tiles
-      if (KV && !wait(&bars.st_full[g % C::STAGES], g / C::STAGES)) return false;
+      if (KV && !__all_sync(0xffffffffu, wait_bar(&bars.st_full[g % C::STAGES], (uint32_t)(g / C::STAGES) & 1u, abort_flag)))
+        return false;
       tmem_ld_wait<kCols>(v);
-      if (C::OWN) arrive(&bars.s_free);
 #pragma unroll
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(nl2, nl2, nl2, nl2);
@@ -438,31 +447,22 @@ struct Compute {
           pr[e + i] = ex2_approx(x[i]);
         }
       }
-    } else if (C::OWN) {
-      arrive(&bars.s_free);
     }
     if constexpr (KV) {
       uint32_t pk[kCols / 2];
 #pragma unroll
       for (int e = 0; e < kCols; e += 2) pk[e >> 1] = SEE != kNone ? pack_bf16x2(pr[e], pr[e + 1]) : 0u;
-      if (C::OWN && g > 0) {
-        // the previous step's dV product has read P
-        if (!wait(&bars.dv_done, g - 1)) return false;
-        tc_fence_after();
-      }
-      tmem_st_x16(tP, pk);
-      tmem_st_wait();
-      arrive(&bars.p_full);
+      tmem_st_x16(tSg, pk);
+      arrive(&bars.p_full[g & 1]);
     }
     // ---- dS = P (dP - D)
-    if (!wait(&bars.dp_full, g)) return false;
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.dp_full, (uint32_t)g & 1u, abort_flag))) return false;
     tc_fence_after();
     uint32_t ds[kCols / 2];
     if constexpr (SEE != kNone) {
       uint32_t v[kCols];
       tmem_ld_x32(tDP, v);
       tmem_ld_wait<kCols>(v);
-      if (C::OWN) arrive(&bars.dp_free);
 #pragma unroll
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(dval, dval, dval, dval);
@@ -477,18 +477,11 @@ struct Compute {
         }
       }
     } else {
-      if (C::OWN) arrive(&bars.dp_free);
 #pragma unroll
       for (int e = 0; e < kCols / 2; ++e) ds[e] = 0u;
     }
-    if (C::OWN && g > 0) {
-      // the previous step's product has read dS
-      if (!wait(&bars.dk_done, g - 1)) return false;
-      tc_fence_after();
-    }
-    tmem_st_x16(tDS, ds);
-    tmem_st_wait();
-    arrive(&bars.ds_full);
+    tmem_st_x16(C::SB == 2 ? tSg + kCols / 2 : tDP, ds);
+    arrive(&bars.ds_full[g & 1]);
     return true;
   }
 };
@@ -497,16 +490,15 @@ template <int D, bool KV>
 __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensorMap* to1, Bars& bars, uint8_t* sRing,
                         uint32_t tmem, volatile int* abort_flag) {
   using C = Cfg<D, KV>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp: uniform
   const int quarter = warp & 3, part = (warp - 1 - kIssuers) >> 2;
   const int row = quarter * 32 + lane;
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
   const uint32_t ring = smem_u32(sRing);
-  uint8_t* out = sRing + C::STAGES * C::STAGE + 1024 * (4 * part + quarter);
+  uint8_t* out = sRing + C::STAGES * C::STAGE + 1024 * C::OUT * (4 * part + quarter);
   const uint32_t srow = smem_u32(out) + 32u * lane;
   Compute<D, KV> W{bars, abort_flag,
-                   base + kColS + (uint32_t)(kCols * part), base + kColDP + (uint32_t)(kCols * part),
-                   base + C::COL_P + C::PART * part, base + C::COL_DS + C::PART * part,
+                   base + (uint32_t)(kCols * part), base + C::COL_DP + (uint32_t)(kCols * part),
                    f2_pack(p.scale_log2, p.scale_log2), 0.f, 0.f, lane == 0};
   int g = 0, n = 0;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
@@ -532,42 +524,60 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
     // memory (32-byte rows, 32B swizzle) and a TMA store, which drops rows past the sequence. (Stored
     // straight from the registers, 32 rows in 32 lines per instruction, an item's output took as
     // long as two steps.)
-    if (!W.wait(&bars.acc_full, n)) return;
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return;
     tc_fence_after();
     const int tok0 = it.tile * kTile + 32 * quarter;
     const bool sum = KV && it.slot >= 0 && tok < p.sinks;   // an fp32 partial sum (its bf16 row is written after)
+    constexpr int N = (KV ? 2 : 1) * (D / 16);               // chunks of 16 columns of the accumulators
 #pragma unroll 1
-    for (int c = part; c < (KV ? 2 : 1) * (D / 16); c += kComputeWarps / 4) {
-      const int m = c / (D / 16), col = 16 * (c % (D / 16));
-      const float f = m ? 1.f : p.scale;
-      uint32_t w[16];
-      tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)col, w);
-      tmem_ld_wait<16>(w);
+    for (int c0 = part; c0 < N; c0 += C::OUT * (kComputeWarps / 4)) {
+      uint32_t w[C::OUT][16];
+#pragma unroll
+      for (int o = 0; o < C::OUT; ++o) {
+        const int c = c0 + o * (kComputeWarps / 4);
+        if (c < N) tmem_ld_x16(base + (c < D / 16 ? C::COL_ACC0 : C::COL_ACC1) + (uint32_t)(16 * (c % (D / 16))), w[o]);
+      }
       if (it.slot <= 0) {                                    // a sink chunk has sums only
         if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
-        uint32_t pk[8];
+      }
 #pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          pk[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
-        const uint32_t swz = (uint32_t)((lane >> 2) & 1) << 4;
-        st_shared_v4(srow + swz, pk[0], pk[1], pk[2], pk[3]);
-        st_shared_v4(srow + (swz ^ 16u), pk[4], pk[5], pk[6], pk[7]);
+      for (int o = 0; o < C::OUT; ++o) {
+        tmem_ld_wait<16>(w[o]);
+        const int c = c0 + o * (kComputeWarps / 4);
+        if (c >= N) continue;
+        const int m = c / (D / 16), col = 16 * (c % (D / 16));
+        const float f = m ? 1.f : p.scale;
+        if (it.slot <= 0) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            pk[e >> 1] = pack_bf16x2(__uint_as_float(w[o][e]) * f, __uint_as_float(w[o][e + 1]) * f);
+          const uint32_t swz = (uint32_t)((lane >> 2) & 1) << 4;
+          st_shared_v4(srow + 1024u * o + swz, pk[0], pk[1], pk[2], pk[3]);
+          st_shared_v4(srow + 1024u * o + (swz ^ 16u), pk[4], pk[5], pk[6], pk[7]);
+        }
+        if (sum) {
+          const int64_t bh = (int64_t)it.s * p.kv_heads + it.head;
+          float* prow = p.partial + (((bh * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D + col;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(prow + e) =
+                make_float4(__uint_as_float(w[o][e]) * f, __uint_as_float(w[o][e + 1]) * f,
+                            __uint_as_float(w[o][e + 2]) * f, __uint_as_float(w[o][e + 3]) * f);
+        }
+      }
+      if (it.slot <= 0) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && tok0 < p.n_tokens) {
-          tma_store_4d(m ? to1 : to0, out, col, it.head, tok0, it.s);
+#pragma unroll
+          for (int o = 0; o < C::OUT; ++o) {
+            const int c = c0 + o * (kComputeWarps / 4);
+            if (c < N) tma_store_4d(c < D / 16 ? to0 : to1, out + 1024 * o, 16 * (c % (D / 16)), it.head, tok0, it.s);
+          }
           bulk_commit_group();
         }
-      }
-      if (sum) {
-        float* prow = p.partial + col +
-                      (((((int64_t)it.s * p.kv_heads + it.head) * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D;
-#pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(prow + e) =
-              make_float4(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f, __uint_as_float(w[e + 2]) * f,
-                          __uint_as_float(w[e + 3]) * f);
       }
     }
     // The next item's first product into the accumulators follows these loads: its issuer waits
@@ -598,14 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.st_full[i], 1);
       mbar_init(&bars.st_empty[i], KV ? 2 : 1);        // the products into the accumulators
     }
-    mbar_init(&bars.s_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], kComputeWarps);
+      mbar_init(&bars.ds_full[i], kComputeWarps);
+      mbar_init(&bars.dv_done[i], 1);
+      mbar_init(&bars.dk_done[i], 1);
+    }
     mbar_init(&bars.dp_full, 1);
-    mbar_init(&bars.s_free, kComputeWarps);
-    mbar_init(&bars.dp_free, kComputeWarps);
-    mbar_init(&bars.p_full, kComputeWarps);
-    mbar_init(&bars.ds_full, kComputeWarps);
-    mbar_init(&bars.dv_done, 1);
-    mbar_init(&bars.dk_done, 1);
     mbar_init(&bars.acc_full, KV ? 2 : 1);
     for (int i = 0; i < kIssuers; ++i) mbar_init(&bars.drain[i], 1);
     abort_flag = 0;
