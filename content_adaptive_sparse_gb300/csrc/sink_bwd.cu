@@ -67,11 +67,12 @@ struct Cfg {
   static constexpr uint32_t ATOM = 8 * ROWB;
   static constexpr int CHUNK = kTile * ROWB;           // one d-chunk of a 128-row tile
   static constexpr int TILE = NCH * CHUNK;
-  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int FIX = D == 128 ? 1 : 2;         // buffers of the stationary tiles
+  static constexpr int STAGES = D == 128 ? 2 : 3;
   static constexpr int STAGE = 2 * TILE + 1024;        // B0, B1, then -LSE log2(e) [128] and D [128]
-  // then 1 KB or 2 per compute warp, from which the outputs leave
-  static constexpr int OUT = KV && D <= 64 ? 2 : 1;
-  static constexpr int SMEM_NEED = 1024 + 2 * TILE + STAGES * STAGE + kComputeWarps * 1024 * OUT;
+  // then OUT KB per compute warp, from which the outputs leave
+  static constexpr int OUT = KV && D == 64 ? 2 : 1;
+  static constexpr int SMEM_NEED = 1024 + FIX * 2 * TILE + STAGES * STAGE + kComputeWarps * 1024 * OUT;
   // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
   static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
   // TMEM columns: S (one buffer or two), dP, accumulators. P is stored over the first half of the
@@ -102,7 +103,7 @@ struct BParams {
 };
 
 struct Bars {
-  uint64_t fixed_full, fixed_empty;                     // stationary tiles (phase: item)
+  uint64_t fixed_full[2], fixed_empty[2];               // stationary tiles (items alternate where FIX is 2)
   uint64_t st_full[kMaxStages], st_empty[kMaxStages];   // ring
   // Steps alternate between two barriers (phase: step / 2) where a wait for one step could meet the
   // next one's completion
@@ -231,13 +232,15 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
   bool ok = true;
   for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
     const Item it = decode_item<KV>(p, k);
-    // the previous item's S and dP have read the stationary tiles
-    if (n > 0 && !(ok = wait_bar(&bars.fixed_empty, (uint32_t)(n - 1) & 1u, abort_flag))) break;
-    mbar_arrive_expect_tx(&bars.fixed_full, 2 * C::TILE);
+    // the S and dP of the item before in this buffer have read its stationary tiles
+    const int fb = n % C::FIX;
+    if (n >= C::FIX && !(ok = wait_bar(&bars.fixed_empty[fb], (uint32_t)(n / C::FIX - 1) & 1u, abort_flag))) break;
+    mbar_arrive_expect_tx(&bars.fixed_full[fb], 2 * C::TILE);
+    uint8_t* fix = sFix + fb * 2 * C::TILE;
 #pragma unroll
     for (int c = 0; c < C::NCH; ++c) {
-      tma_load_4d(sFix + c * C::CHUNK, ta0, &bars.fixed_full, c * C::CH, it.head, it.tile * kTile, it.s);
-      tma_load_4d(sFix + C::TILE + c * C::CHUNK, ta1, &bars.fixed_full, c * C::CH, it.head, it.tile * kTile, it.s);
+      tma_load_4d(fix + c * C::CHUNK, ta0, &bars.fixed_full[fb], c * C::CH, it.head, it.tile * kTile, it.s);
+      tma_load_4d(fix + C::TILE + c * C::CHUNK, ta1, &bars.fixed_full[fb], c * C::CH, it.head, it.tile * kTile, it.s);
     }
     Steps<KV> at(p, it);
     for (int j = 0; j < it.steps; ++j, ++g, at.next(it)) {
@@ -260,7 +263,7 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
   }
   // every copy of this CTA has landed before it may exit (n counts the items whose stationary
   // tiles were requested, a broken-off one too; g the steps requested)
-  if (n > 0) drain_bar(&bars.fixed_full, (uint32_t)(n - 1) & 1u);
+  for (int i = max(0, n - C::FIX); i < n; ++i) drain_bar(&bars.fixed_full[i % C::FIX], (uint32_t)(i / C::FIX) & 1u);
   for (int t = max(0, g - C::STAGES); t < g; ++t)
     drain_bar(&bars.st_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
 }
@@ -300,22 +303,22 @@ struct Issuer {
   static __device__ constexpr uint32_t col_s(int g) { return C::SB == 2 ? 128u * (g & 1) : 0u; }
   static __device__ constexpr uint32_t col_ds(int g) { return C::SB == 2 ? col_s(g) + kCols / 2 : C::COL_DP; }
   // S of step g, once the P and dS that lay over its columns are used; dP once step g - 1's is used
-  __device__ __forceinline__ bool scores(int g) const {
+  __device__ __forceinline__ bool scores(int g, uint64_t fix) const {
     if (g >= C::SB) {
       if (KV && !wait_pair(bars.dv_done, g - C::SB, abort_flag)) return false;
       if (C::SB == 2 && !wait_pair(bars.dk_done, g - 2, abort_flag)) return false;
     }
     if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(col_s(g), a0, b0 + at(g % C::STAGES));
+    rows_x_rows(col_s(g), a0 + fix, b0 + at(g % C::STAGES));
     mma_commit(&bars.s_full[g & 1]);
     return true;
   }
-  __device__ __forceinline__ bool products(int g) const {
+  __device__ __forceinline__ bool products(int g, uint64_t fix) const {
     if (g > 0 && !wait_pair(C::SB == 2 ? bars.ds_full : bars.dk_done, g - 1, abort_flag)) return false;
     if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(C::COL_DP, a1, b1 + at(g % C::STAGES));
+    rows_x_rows(C::COL_DP, a1 + fix, b1 + at(g % C::STAGES));
     mma_commit(&bars.dp_full);
     return true;
   }
@@ -357,12 +360,14 @@ __device__ void issuer(const BParams& p, int role, Bars& bars, uint8_t* sFix, ui
       for (int j = 0; ok && j < steps; ++j, ++g) ok = KV && role == 1 ? I.acc1(g, j > 0) : I.acc0(g, j > 0);
       if (ok) mma_commit(&bars.acc_full);
     } else {
-      if (!(ok = wait_bar(&bars.fixed_full, (uint32_t)n & 1u, abort_flag))) break;
+      const int fb = n % C::FIX;
+      const uint64_t fix = (uint64_t)((fb * 2 * C::TILE) >> 4);
+      if (!(ok = wait_bar(&bars.fixed_full[fb], (uint32_t)(n / C::FIX) & 1u, abort_flag))) break;
       for (int j = 0; ok && j < steps; ++j, ++g) {
-        if (role == 0) ok = I.scores(g);
-        if (ok && role == (KV ? 0 : 1)) ok = I.products(g);
+        if (role == 0) ok = I.scores(g, fix);
+        if (ok && role == (KV ? 0 : 1)) ok = I.products(g, fix);
       }
-      if (ok) mma_commit(&bars.fixed_empty);           // the item's last S (and dP) are issued
+      if (ok) mma_commit(&bars.fixed_empty[fb]);       // the item's last S (and dP) are issued
     }
   }
   // no MMA of this thread is still at work when the CTA frees its TMEM
@@ -397,39 +402,102 @@ __device__ __forceinline__ int visibility(int r0, int c0, int window, int sinks)
   return q >= k + 31 && (q + 31 - k <= window || k + 31 < sinks) ? kAll : kSome;
 }
 
-// Each of the three ways of seeing has a copy of the step's code: joined by selects, the mask's
-// instructions would be issued in every step.
-// One warp's part of a step.
+// A compute warp.
 template <int D, bool KV>
 struct Compute {
   using C = Cfg<D, KV>;
+  const BParams& p;
+  const CUtensorMap* to0;
+  const CUtensorMap* to1;
   Bars& bars;
   volatile int* abort_flag;
-  uint32_t tS, tDP;                 // TMEM: S (first buffer) and dP, this warp's lanes and columns
+  uint32_t base;                    // TMEM of this warp's lanes
+  int quarter, part, lane;
+  uint8_t* out;                     // this warp's staging memory
   uint64_t c2;
-  float nl2, dval;                  // dQ: the row's -LSE log2(e) and D
-  bool lead;                        // lane 0
 
   // This warp's TMEM stores are done: one arrival.
   __device__ __forceinline__ void arrive(uint64_t* bar) const {
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
-    if (lead) mbar_arrive(bar);
+    if (lane == 0) mbar_arrive(bar);
   }
 
+  // An item's rows, this warp's share of the columns: 16 at a time, through 1 KB of shared memory
+  // (32-byte rows, 32B swizzle) and a TMA store, which drops rows past the sequence. (Stored straight
+  // from the registers, 32 rows in 32 lines per instruction, an item's output took as long as two
+  // steps.)
+  __device__ __forceinline__ bool write(const Item& it, int n) const {
+    const int tok0 = it.tile * kTile + 32 * quarter, tok = tok0 + lane;
+    const bool sum = KV && it.slot >= 0 && tok < p.sinks;   // an fp32 partial sum (its bf16 row is written after)
+    const bool rows = it.slot <= 0;                          // a sink chunk has sums only
+    const uint32_t srow = smem_u32(out) + 32u * lane;
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return false;
+    tc_fence_after();
+    constexpr int N = (KV ? 2 : 1) * (D / 16), W = kComputeWarps / 4;   // chunks; warps that share them
+#pragma unroll 1
+    for (int c0 = part; c0 < N; c0 += C::OUT * W) {
+      if (rows) {
+        if (lane < C::OUT) bulk_wait_group_read<0>();
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int o = 0; o < C::OUT && c0 + o * W < N; ++o) {
+        const int c = c0 + o * W, m = c / (D / 16), col = 16 * (c % (D / 16));
+        const float f = m ? 1.f : p.scale;
+        uint32_t w[16];
+        tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)col, w);
+        tmem_ld_wait<16>(w);
+        if (sum) {
+          const int64_t bh = (int64_t)it.s * p.kv_heads + it.head;
+          float* prow = p.partial + (((bh * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D + col;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(prow + e) =
+                make_float4(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f, __uint_as_float(w[e + 2]) * f,
+                            __uint_as_float(w[e + 3]) * f);
+        }
+        if (rows) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            pk[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
+          const uint32_t swz = (uint32_t)((lane >> 2) & 1) << 4;
+          st_shared_v4(srow + 1024u * o + swz, pk[0], pk[1], pk[2], pk[3]);
+          st_shared_v4(srow + 1024u * o + (swz ^ 16u), pk[4], pk[5], pk[6], pk[7]);
+        }
+      }
+      if (rows) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        // lane o sends chunk o
+        const int c = c0 + lane * W, m = c / (D / 16);
+        if (lane < C::OUT && c < N && tok0 < p.n_tokens)
+          tma_store_4d(m ? to1 : to0, out + 1024 * lane, 16 * (c % (D / 16)), it.head, tok0, it.s);
+        if (lane < C::OUT) bulk_commit_group();
+      }
+    }
+    return true;
+  }
+
+  // A step. Each way of seeing (SEE) has a copy of the code: joined by selects, the mask's
+  // instructions would be issued in every step. `prev`: the item before, at an item's first step.
   template <int SEE>
-  __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see) const {
-    const uint32_t tSg = tS + (C::SB == 2 ? 128u * (g & 1) : 0u);
+  __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see, float nl2, float dval, const Item* prev,
+                                       int n) const {
+    const uint32_t tS = base + (uint32_t)(kCols * part) + (C::SB == 2 ? 128u * (g & 1) : 0u);
+    const uint32_t tDP = base + C::COL_DP + (uint32_t)(kCols * part);
     if (!__all_sync(0xffffffffu, wait_pair(bars.s_full, g, abort_flag))) return false;
     tc_fence_after();
     // ---- P
     float pr[kCols];
     if constexpr (SEE != kNone) {
       uint32_t v[kCols];
-      tmem_ld_x32(tSg, v);
+      tmem_ld_x32(tS, v);
       // dK / dV: the stage's -LSE and D have landed with its tiles
-      if (KV && !__all_sync(0xffffffffu, wait_bar(&bars.st_full[g % C::STAGES], (uint32_t)(g / C::STAGES) & 1u, abort_flag)))
+      if (KV && !__all_sync(0xffffffffu,
+                            wait_bar(&bars.st_full[g % C::STAGES], (uint32_t)(g / C::STAGES) & 1u, abort_flag)))
         return false;
       tmem_ld_wait<kCols>(v);
 #pragma unroll
@@ -452,9 +520,14 @@ struct Compute {
       uint32_t pk[kCols / 2];
 #pragma unroll
       for (int e = 0; e < kCols; e += 2) pk[e >> 1] = SEE != kNone ? pack_bf16x2(pr[e], pr[e + 1]) : 0u;
-      tmem_st_x16(tSg, pk);
-      arrive(&bars.p_full[g & 1]);
+      tmem_st_x16(tS, pk);
     }
+    // dQ: the previous item's rows leave after the first exponentials of this one, under which its last
+    // product completes (8K training: 132 -> 121 us; for dK / dV, whose registers are full, leaving
+    // before them is faster: 163 against 190 us). This item's first product into the accumulators
+    // waits for the P or dS that is announced after them.
+    if (!KV && prev != nullptr && !write(*prev, n - 1)) return false;
+    if constexpr (KV) arrive(&bars.p_full[g & 1]);
     // ---- dS = P (dP - D)
     if (!__all_sync(0xffffffffu, wait_bar(&bars.dp_full, (uint32_t)g & 1u, abort_flag))) return false;
     tc_fence_after();
@@ -480,7 +553,7 @@ struct Compute {
 #pragma unroll
       for (int e = 0; e < kCols / 2; ++e) ds[e] = 0u;
     }
-    tmem_st_x16(C::SB == 2 ? tSg + kCols / 2 : tDP, ds);
+    tmem_st_x16(C::SB == 2 ? tS + kCols / 2 : tDP, ds);
     arrive(&bars.ds_full[g & 1]);
     return true;
   }
@@ -493,98 +566,39 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp: uniform
   const int quarter = warp & 3, part = (warp - 1 - kIssuers) >> 2;
   const int row = quarter * 32 + lane;
-  const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
   const uint32_t ring = smem_u32(sRing);
-  uint8_t* out = sRing + C::STAGES * C::STAGE + 1024 * C::OUT * (4 * part + quarter);
-  const uint32_t srow = smem_u32(out) + 32u * lane;
-  Compute<D, KV> W{bars, abort_flag,
-                   base + (uint32_t)(kCols * part), base + C::COL_DP + (uint32_t)(kCols * part),
-                   f2_pack(p.scale_log2, p.scale_log2), 0.f, 0.f, lane == 0};
+  const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+  const Compute<D, KV> W{p, to0, to1, bars, abort_flag, base, quarter, part, lane,
+                         sRing + C::STAGES * C::STAGE + 1024 * C::OUT * (4 * part + quarter), f2_pack(p.scale_log2, p.scale_log2)};
   int g = 0, n = 0;
+  Item it, prev;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
-    const Item it = decode_item<KV>(p, k);
+    prev = it;
+    it = decode_item<KV>(p, k);
     const int tok = it.tile * kTile + row;
+    float nl2 = 0.f, dval = 0.f;
     if constexpr (!KV) {
       const int64_t at = ((int64_t)it.s * p.heads + it.head) * p.pitch + tok;
-      W.nl2 = p.nl2[at];
-      W.dval = p.dvec[at];
+      nl2 = p.nl2[at];
+      dval = p.dvec[at];
     }
     Steps<KV> moving(p, it);
+    if (KV && n > 0 && !W.write(prev, n - 1)) return;
     for (int j = 0; j < it.steps; ++j, ++g, moving.next(it)) {
       const int c0 = moving.tile * kTile + kCols * part;
       const uint32_t vec = ring + (uint32_t)((g % C::STAGES) * C::STAGE + 2 * C::TILE + 4 * kCols * part);
-      bool ok;
       const int see = visibility<KV>(it.tile * kTile + 32 * quarter, c0, p.window, p.sinks);
-      if (see == kAll) ok = W.template step<kAll>(g, vec, 0u);
-      else if (see == kSome) ok = W.template step<kSome>(g, vec, visible<KV>(tok, c0, p.window, p.sinks));
-      else ok = W.template step<kNone>(g, vec, 0u);
+      const Item* before = !KV && j == 0 && n > 0 ? &prev : nullptr;
+      bool ok;
+      if (see == kAll) ok = W.template step<kAll>(g, vec, 0u, nl2, dval, before, n);
+      else if (see == kSome) ok = W.template step<kSome>(g, vec, visible<KV>(tok, c0, p.window, p.sinks), nl2, dval, before, n);
+      else ok = W.template step<kNone>(g, vec, 0u, nl2, dval, before, n);
       if (!ok) return;
     }
-    // ---- the item's rows: each warp a share of the columns, 16 at a time, through 1 KB of shared
-    // memory (32-byte rows, 32B swizzle) and a TMA store, which drops rows past the sequence. (Stored
-    // straight from the registers, 32 rows in 32 lines per instruction, an item's output took as
-    // long as two steps.)
-    if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return;
-    tc_fence_after();
-    const int tok0 = it.tile * kTile + 32 * quarter;
-    const bool sum = KV && it.slot >= 0 && tok < p.sinks;   // an fp32 partial sum (its bf16 row is written after)
-    constexpr int N = (KV ? 2 : 1) * (D / 16);               // chunks of 16 columns of the accumulators
-#pragma unroll 1
-    for (int c0 = part; c0 < N; c0 += C::OUT * (kComputeWarps / 4)) {
-      uint32_t w[C::OUT][16];
-#pragma unroll
-      for (int o = 0; o < C::OUT; ++o) {
-        const int c = c0 + o * (kComputeWarps / 4);
-        if (c < N) tmem_ld_x16(base + (c < D / 16 ? C::COL_ACC0 : C::COL_ACC1) + (uint32_t)(16 * (c % (D / 16))), w[o]);
-      }
-      if (it.slot <= 0) {                                    // a sink chunk has sums only
-        if (lane == 0) bulk_wait_group_read<0>();
-        __syncwarp();
-      }
-#pragma unroll
-      for (int o = 0; o < C::OUT; ++o) {
-        tmem_ld_wait<16>(w[o]);
-        const int c = c0 + o * (kComputeWarps / 4);
-        if (c >= N) continue;
-        const int m = c / (D / 16), col = 16 * (c % (D / 16));
-        const float f = m ? 1.f : p.scale;
-        if (it.slot <= 0) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            pk[e >> 1] = pack_bf16x2(__uint_as_float(w[o][e]) * f, __uint_as_float(w[o][e + 1]) * f);
-          const uint32_t swz = (uint32_t)((lane >> 2) & 1) << 4;
-          st_shared_v4(srow + 1024u * o + swz, pk[0], pk[1], pk[2], pk[3]);
-          st_shared_v4(srow + 1024u * o + (swz ^ 16u), pk[4], pk[5], pk[6], pk[7]);
-        }
-        if (sum) {
-          const int64_t bh = (int64_t)it.s * p.kv_heads + it.head;
-          float* prow = p.partial + (((bh * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D + col;
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(prow + e) =
-                make_float4(__uint_as_float(w[o][e]) * f, __uint_as_float(w[o][e + 1]) * f,
-                            __uint_as_float(w[o][e + 2]) * f, __uint_as_float(w[o][e + 3]) * f);
-        }
-      }
-      if (it.slot <= 0) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && tok0 < p.n_tokens) {
-#pragma unroll
-          for (int o = 0; o < C::OUT; ++o) {
-            const int c = c0 + o * (kComputeWarps / 4);
-            if (c < N) tma_store_4d(c < D / 16 ? to0 : to1, out + 1024 * o, 16 * (c % (D / 16)), it.head, tok0, it.s);
-          }
-          bulk_commit_group();
-        }
-      }
-    }
-    // The next item's first product into the accumulators follows these loads: its issuer waits
-    // for the P or dS that this warp stores after them.
   }
+  if (n > 0) W.write(it, n - 1);
   // this warp's stores are complete before the CTA may exit
-  if (lane == 0) bulk_wait_group<0>();
+  if (lane < C::OUT) bulk_wait_group<0>();
   __syncwarp();
 }
 
@@ -602,8 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    mbar_init(&bars.fixed_full, 1);
-    mbar_init(&bars.fixed_empty, KV ? 1 : 2);          // S and dP from one thread, or from two
+    for (int i = 0; i < C::FIX; ++i) {
+      mbar_init(&bars.fixed_full[i], 1);
+      mbar_init(&bars.fixed_empty[i], KV ? 1 : 2);     // S and dP from one thread, or from two
+    }
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&bars.st_full[i], 1);
       mbar_init(&bars.st_empty[i], KV ? 2 : 1);        // the products into the accumulators
@@ -624,6 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&ta1);
     tma_prefetch_desc(&tb0);
     tma_prefetch_desc(&tb1);
+    tma_prefetch_desc(&to0);
+    tma_prefetch_desc(&to1);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, kTmemCols);
@@ -634,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   uint8_t* sFix = sbase;
-  uint8_t* sRing = sFix + 2 * C::TILE;
+  uint8_t* sRing = sFix + C::FIX * 2 * C::TILE;
   if (warp == 0) {
     if ((threadIdx.x & 31) == 0) loader<D, KV>(p, &ta0, &ta1, &tb0, &tb1, bars, sFix, sRing, &abort_flag);
     __syncwarp();
