@@ -7,12 +7,7 @@
 // per query block. The list is cut into 32-key chunks and four consecutive chunks form one
 // key tile (128 keys; the last tile of an item may be shorter).
 //
-// The same kernels also run the sink-window graph (sink_attn.cu; the WIN template argument): key
-// j is visible to query i iff j <= i and (i - j <= window or j < sinks). Its items need no CSR:
-// an item's chunks are the sinks' and then the window's, by arithmetic, and each softmax thread
-// masks the chunks that its warp's rows see in part.
-//
-// Token rule of the block graphs: key j of block J is visible to query i of block I iff J is in row(I) and
+// Token rule: key j of block J is visible to query i of block I iff J is in row(I) and
 // (not causal or j <= i) ("Parameter-free Adaptive Sparse Attention via Compression-Based
 // Content Selection", section 3.4 block-to-token expansion). No token mask is materialised.
 #pragma once
@@ -99,8 +94,7 @@ struct __align__(16) Batch {
   uint8_t nch[kBatch];        // per key tile: 32-key chunks (1 .. 4); 16-byte aligned
   uint8_t vq[4][kBatch];      // per TMEM lane quarter and key tile: bits 0-3, chunk c visible
                               // to some row of the quarter; bits 4-6, 1 + the causal-diagonal
-                              // chunk (0: none). Sink-window graph: bits 4-7, chunk c hidden
-                              // from some row of the quarter
+                              // chunk (0: none)
 };
 
 // Visibility byte of one key tile for the 32 query rows of lane quarter q (rows 32q ..
@@ -122,30 +116,6 @@ __device__ __forceinline__ int quarter_vis(const int (&tm)[4], int nch, int sub,
     }
   }
   return vis | ((dch + 1) << 4);
-}
-
-// Visibility byte of the sink-window graph for the 32 query rows q_warp .. q_warp + 31 (bits 0-3:
-// some pair of the chunk is visible; bits 4-7: some is visible and some is not).
-__device__ __forceinline__ int quarter_vis_window(const int (&tm)[4], int nch, int q_warp, int window, int sinks) {
-  int vis = 0, part = 0;
-#pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
-    const int c = tm[ch] >> 4;                     // first key of the chunk, a multiple of 32
-    if (ch >= nch || c > q_warp + 31) continue;
-    if (q_warp - (c + 31) > window && c >= sinks) continue;
-    vis |= 1 << ch;
-    if (c + 31 > q_warp || (q_warp + 31 - c > window && c + 31 >= sinks)) part |= 1 << ch;
-  }
-  return vis | (part << 4);
-}
-
-// The 32 keys c .. c + 31 that query i sees in the sink-window graph (bit b: key c + b).
-__device__ __forceinline__ uint32_t window_bits(int i, int c, int window, int sinks) {
-  const int lim = i - c, low = lim - window, sk = sinks - c;
-  const uint32_t upto = lim >= 31 ? 0xffffffffu : (lim < 0 ? 0u : ((2u << lim) - 1u));
-  const uint32_t from = low <= 0 ? 0xffffffffu : (low >= 32 ? 0u : (0xffffffffu << low));
-  const uint32_t sink = sk >= 32 ? 0xffffffffu : (sk <= 0 ? 0u : ((1u << sk) - 1u));
-  return upto & (from | sink);
 }
 
 __device__ __forceinline__ uint4 ld_shared_u4(const void* ptr) {
@@ -198,7 +168,6 @@ struct Params {
   float* lse;
   int64_t o_sb, o_sn, o_sh;
   float scale_log2;
-  int window, sinks;                   // sink-window graph (WIN)
 };
 struct Item {
   int s, h, tile;
@@ -301,12 +270,9 @@ __device__ __forceinline__ bool load_tile(const TileLoad& L, const CUtensorMap* 
 // Claims work items from the launch-wide counter, builds each item's key-block union and
 // publishes the item's key tiles in batches. With two ring entries the next item's union is
 // built while the consumers still work on the current one, and no more than about two items
-// are claimed ahead of them. The sink-window graph (WIN) has items of nearly equal length and
-// deals them out in turn instead: stream `stream` of `n_streams` takes every n_streams-th item,
-// and the launch needs no counter.
-template <int D, bool WIN, class Bars>
-__device__ void planner(const Params& p, Bars& bars, Batch* ring, UnionSmem& u, int stream, int n_streams,
-                        volatile int* abort_flag) {
+// are claimed ahead of them.
+template <int D, class Bars>
+__device__ void planner(const Params& p, Bars& bars, Batch* ring, UnionSmem& u, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
   const int b = p.block;
   const int cpb = b >> 5;                            // 32-key chunks per key block
@@ -317,14 +283,10 @@ __device__ void planner(const Params& p, Bars& bars, Batch* ring, UnionSmem& u, 
   const int list_len = split_mode ? p.list_hdr[0] : p.n_items;
   const int n_split = split_mode ? p.list_hdr[1] : 0;
   const int part_tiles = split_mode ? p.list_hdr[2] : 0;
-  for (int next = stream;; next += n_streams) {
+  for (;;) {
     int idx = 0;
-    if constexpr (WIN) {
-      idx = next;
-    } else {
-      if (lane == 0) idx = (int)atomicAdd(p.work_counter, 1u);
-      idx = __shfl_sync(0xffffffffu, idx, 0);
-    }
+    if (lane == 0) idx = (int)atomicAdd(p.work_counter, 1u);
+    idx = __shfl_sync(0xffffffffu, idx, 0);
     const bool done = idx >= list_len;
     int k = idx, part = 0;
     if (split_mode && !done) {
@@ -334,14 +296,7 @@ __device__ void planner(const Params& p, Bars& bars, Batch* ring, UnionSmem& u, 
     }
     const int slot = (split_mode && idx < n_split) ? idx : -1;
     int n_chunks = 0;
-    int n_sink = 0, win0 = 0;                        // WIN: sink chunks, first chunk of the window
-    if (WIN && !done) {
-      const int q0 = decode_item(p, k).tile * kTile;
-      win0 = max(0, q0 - p.window) >> 5;
-      n_sink = min((p.sinks + 31) >> 5, win0);
-      n_chunks = n_sink + (min(q0 + kTile, p.n_tokens) - 1) / 32 - win0 + 1;
-    }
-    if (!WIN && !done) {
+    if (!done) {
       const Item it = decode_item(p, k);
       const int I0 = (it.tile * kTile) >> p.log2b;
       const int nq = min(qb_per_tile, p.nb - I0);
@@ -366,12 +321,8 @@ __device__ void planner(const Params& p, Bars& bars, Batch* ring, UnionSmem& u, 
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int q = 4 * (t0 + lane) + c;         // chunk index within the item
-          if constexpr (WIN) {
-            tm[c] = q < n_chunks ? (((q < n_sink ? q : win0 + q - n_sink) << 9) | 15) : 0;
-          } else {
-            const uint32_t e = q < n_chunks ? u.list[q / cpb] : 0u;
-            tm[c] = q < n_chunks ? ((((int)(e & 0xfffu) * b + (q % cpb) * 32) << 4) | (int)(e >> 12)) : 0;
-          }
+          const uint32_t e = q < n_chunks ? u.list[q / cpb] : 0u;
+          tm[c] = q < n_chunks ? ((((int)(e & 0xfffu) * b + (q % cpb) * 32) << 4) | (int)(e >> 12)) : 0;
         }
         ring[ms].tile[lane] = make_int4(tm[0], tm[1], tm[2], tm[3]);
         const int nch = min(4, n_chunks - 4 * (t0 + lane));
@@ -379,9 +330,7 @@ __device__ void planner(const Params& p, Bars& bars, Batch* ring, UnionSmem& u, 
         const int tile0 = decode_item(p, k).tile * kTile;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          ring[ms].vq[q][lane] =
-              (uint8_t)(WIN ? quarter_vis_window(tm, nch, tile0 + 32 * q, p.window, p.sinks)
-                            : quarter_vis(tm, nch, (32 * q) >> p.log2b, tile0 + 32 * q, p.causal));
+          ring[ms].vq[q][lane] = (uint8_t)quarter_vis(tm, nch, (32 * q) >> p.log2b, tile0 + 32 * q, p.causal);
       }
       if (lane == 0) {
         *reinterpret_cast<int4*>(&ring[ms]) = make_int4(done ? kKindDone : kKindItem, nt, k,

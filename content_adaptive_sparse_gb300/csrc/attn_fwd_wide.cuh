@@ -276,7 +276,7 @@ __device__ __forceinline__ void store_row(const Params& p, uint32_t tO, const It
 // TMEM lane quarter) and key columns 64 half .. 64 half + 63 of every key tile (32-key chunks
 // 2 half and 2 half + 1). At the end of an item it hands the rows' max and its half's sums to
 // the epilogue warps and goes on with the next item.
-template <int D, bool WIN>
+template <int D>
 __device__ void softmax_halves(const Params& p, StreamBars& bars, const Batch* ring, EpiEntry* epi, uint32_t tmem,
                                float* xch, volatile int* abort_flag) {
   using C = Cfg<D>;
@@ -319,7 +319,7 @@ __device__ void softmax_halves(const Params& p, StreamBars& bars, const Batch* r
         const int nch = (int)((word_of(ncw, i >> 2) >> sh) & 0xffu);
         // this warp's two chunks: visibility bits and the causal-diagonal chunk among them
         const int vis = (vb >> (2 * half)) & 3;
-        const int dch_all = WIN ? -1 : (vb >> 4) - 1;
+        const int dch_all = (vb >> 4) - 1;
         const int dch = (dch_all >= 2 * half && dch_all < 2 * half + 2) ? dch_all - 2 * half : -1;
         const int b = g & 1;
 
@@ -343,15 +343,6 @@ __device__ void softmax_halves(const Params& p, StreamBars& bars, const Batch* r
           if (dch == 0) mask_chunk(v, kp);
           else mask_chunk(v + 32, kp);
         }
-        if (WIN && ((vb >> (4 + 2 * half)) & 3) != 0) {
-          // chunks that some of this warp's rows see in part
-          const int4 tm = ld_shared_v4(&e.tile[i]);
-          const int qtok = decode_item(p, hdr.z).tile * kTile + row;
-          if ((vb >> (4 + 2 * half)) & 1)
-            mask_chunk(v, window_bits(qtok, (half ? tm.z : tm.x) >> 4, p.window, p.sinks));
-          if ((vb >> (5 + 2 * half)) & 1)
-            mask_chunk(v + 32, window_bits(qtok, (half ? tm.w : tm.y) >> 4, p.window, p.sinks));
-        }
         float cm = kNegInf;
         if (vis & 1) cm = chunk_max(v, cm);
         if (vis & 2) cm = chunk_max(v + 32, cm);
@@ -370,9 +361,7 @@ __device__ void softmax_halves(const Params& p, StreamBars& bars, const Batch* r
           l *= alpha;
           if (need) m_use = mx;
         }
-        // a row of the sink-window graph may have seen no key yet: its scores are all -inf
-        const float m_ref = WIN && m_use == kNegInf ? 0.f : m_use;
-        const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+        const uint64_t negm2 = f2_pack(-m_use, -m_use);
         uint64_t rs[2] = {0ull, 0ull};
         uint32_t pk[32];
 #pragma unroll
@@ -484,7 +473,7 @@ __device__ void epilogue(const Params& p, StreamBars& bars, const EpiEntry* epi,
 
 // ------------------------------------------------------------------ kernel
 
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_wide_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
@@ -556,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
-    softmax_halves<D, WIN>(p, bars, ring, epi, tmem, xch, &abort_flag);
+    softmax_halves<D>(p, bars, ring, epi, tmem, xch, &abort_flag);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 8) {
@@ -569,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((threadIdx.x & 31) == 0) pv_issuer<D>(bars, ring, sV, tmem, &abort_flag);
       __syncwarp();
     } else if (warp == 11) {
-      planner<D, WIN>(p, bars, ring, un, blockIdx.x, gridDim.x, &abort_flag);
+      planner<D>(p, bars, ring, un, &abort_flag);
     } else {
       epilogue<D>(p, bars, epi, tmem, &abort_flag);
     }

@@ -1,68 +1,613 @@
-// Causal attention over a token window and a few first tokens ("sinks"), forward: key j is
-// visible to query i iff j <= i and (i - j <= window or j < sinks). The kernels are those of the
-// block-sparse forward (attn_fwd_pipes.cuh at d = 32 and 64, attn_fwd_wide.cuh at d = 128) on the
-// sink-window graph: a 128-query tile's key list is the sinks' 32-key chunks and then the
-// window's, so no CSR and no workspace are read, and an item's list is about as long as every
-// other's, so items are dealt out in turn.
+// Causal attention over a token window and a few first tokens ("sinks"), forward, for sm_103a
+// (tcgen05 + TMEM + TMA): key j is visible to query i iff j <= i and (i - j <= window or j < sinks).
+//
+// Work item: 128 queries of one (sequence, head). Its key tiles (128 keys) are those that the window
+// meets and, where it does not reach back to it, the first one for the sinks; every role derives
+// them from the item's number, so there is no list, no counter and no workspace, and items, of
+// nearly equal length, are dealt out in turn to one persistent CTA per SM.
+//
+// The two 64-key halves of every tile are softmaxes of their own: half h has its running maximum,
+// sum and output accumulator O_h = sum P v over its keys, and an item's end joins them:
+//   m = max(m_0, m_1),  L = sum_h l_h 2^(m_h - m),  O = sum_h O_h 2^(m_h - m) / L,  LSE = m ln 2 + ln L.
+// So no warp waits for another one's row maximum inside a tile (the exchange of half-row maxima was
+// the longest wait of a softmax step), and the halves drift apart, one in the exponentials while the
+// other is in its loads and stores. The running maximum is followed only when it grows by more than
+// 2^8; probabilities are then at most 2^8, rounded to bf16 for the tensor core, and summed in fp32.
+//
+// TMEM (512 columns): S_b [128 b, +128) for tiles b = g % 2; P of half h over the first 32 of its own 64
+// columns of S_b (bf16 pairs), so the second PV's completion frees S_b for the tile after next;
+// O_h from column 256 on, at d <= 64 in two sets that items alternate between.
+//
+// Warp roles (512 threads; warp w runs on SM sub-partition w % 4):
+//   warps 0-7   softmax: query rows 32 (w % 4) .. of the tile, key half w / 4
+//   warp 8      lane 0 loads Q, K and V by TMA (V one tile behind K)
+//   warp 9      lane 0 issues S_b = Q K^T
+//   warps 10, 11  lane 0 issues O_h += P_h V_h (A = P from TMEM, B = V MN-major), h = 0, 1
+//   warps 12-15 epilogue: an item's rows through shared memory and TMA stores, under the next item
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
 #include <string.h>
 
-#include "attn_fwd_common.cuh"
-#include "attn_fwd_pipes.cuh"
-#include "attn_fwd_wide.cuh"
+#include "ptx_sm100.cuh"
+#include "sa_internal.h"
+#include "tma_host.h"
 
 namespace sa {
 namespace {
+
+__device__ unsigned int g_sink_fwd_err;
+
+constexpr int kTile = 128;            // queries of an item; keys of a tile
+constexpr int kHalf = 64;             // keys of a half
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarps = 8, kHalfWarps = 4, kEpilogueWarps = 4;
+constexpr int kMaxStages = 4;
+constexpr uint32_t kTmemCols = 512;
+// Register split (setmaxnreg): softmax warpgroups 184, the others 72, of 128 per thread at launch
+constexpr int kLaunchRegs = 128;
+static_assert(8 * 184 + 8 * 72 == 16 * kLaunchRegs, "register split");
+
+template <int D>
+struct Cfg {
+  static constexpr int CH = D >= 64 ? 64 : 32;         // elements per swizzled row
+  static constexpr int NCH = D / CH;
+  static constexpr int ROWB = CH * 2;
+  static constexpr uint32_t SWZ = ROWB == 128 ? kSwizzle128B : kSwizzle64B;
+  static constexpr CUtensorMapSwizzle TMA_SWZ =
+      ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  static constexpr uint32_t ATOM = 8 * ROWB;
+  static constexpr int CHUNK = kTile * ROWB;           // one d-chunk of a 128-row tile
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int STAGES = D == 128 ? 2 : 4;      // of K and of V
+  static constexpr int OB = D == 128 ? 1 : 2;          // sets of output accumulators
+  static constexpr int OUT = 2048;                     // staging per epilogue warp: 32 rows of 32 elements
+  static constexpr int SMEM = 1024 + (2 + 2 * STAGES) * TILE + kEpilogueWarps * OUT;
+  static_assert(STAGES <= kMaxStages && SMEM <= 222 * 1024, "shared memory");
+};
+
+struct FParams {
+  int batch, n_tokens, heads, heads_per_kv;
+  int tiles, n_items;               // 128-row tiles per sequence; items
+  int window, sinks;
+  float* lse;
+  float scale_log2;
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];                                 // phase: item / 2
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+  // per tile g, alternating (phase: g / 2)
+  uint64_t s_full[2];               // S written
+  uint64_t p_full[2][2];            // [half]: P stored
+  uint64_t pv_done[2][2];           // [half]: the PV is complete
+  uint64_t o_full[2], o_free[2];    // per accumulator set: an item's output complete; read
+  uint64_t epi_full[2], epi_empty[2];   // maxima and sums handed to the epilogue
+  uint64_t drain[3];
+};
+
+struct Handoff {
+  float m[2][kTile], l[2][kTile];   // per half and row: running maximum (log2 units), sum
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait_suspend(bar, parity, abort_flag, &g_sink_fwd_err, kErrTimeout);
+}
+__device__ __forceinline__ bool wait_pair(uint64_t (&bar)[2], int g, volatile int* abort_flag) {
+  return wait_bar(&bar[g & 1], (uint32_t)(g >> 1) & 1u, abort_flag);
+}
+__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
+  int never = 0;
+  mbar_wait(bar, parity, &never, &g_sink_fwd_err, kErrTimeout);
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Item k: all (sequence, head) pairs of one query tile before the next, from the last tile (which
+// sees the most keys). Step j is key tile 0 (n_sink = 1, j = 0) or t0 + j - n_sink.
+struct Item {
+  int s, h, tile, t0, n_sink, steps;
+  __device__ Item() {}
+  __device__ Item(const FParams& p, int k) {
+    const int pairs = p.batch * p.heads;
+    const int bh = k % pairs;
+    h = bh % p.heads;
+    s = bh / p.heads;
+    tile = p.tiles - 1 - k / pairs;
+    t0 = max(0, tile * kTile - p.window) / kTile;
+    n_sink = p.sinks > 0 && t0 > 0 ? 1 : 0;
+    steps = n_sink + tile - t0 + 1;
+  }
+  __device__ __forceinline__ int key_tile(int j) const { return j < n_sink ? 0 : t0 + j - n_sink; }
+  // The sink tile's second half is left out when the first holds every sink.
+  __device__ __forceinline__ bool one_half(const FParams& p, int j) const { return j < n_sink && p.sinks <= kHalf; }
+};
+
+// ------------------------------------------------------------------ loader (warp 8, lane 0)
+
+template <int D>
+__device__ void loader(const FParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, Bars& bars,
+                       uint8_t* sQ, uint8_t* sK, uint8_t* sV, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  int g = 0, gv = 0, n = 0;          // K tiles, V tiles and Q tiles requested
+  bool ok = true;
+  const auto load = [&](int t, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, const Item& it, int j) {
+    const int st = t % C::STAGES;
+    if (t >= C::STAGES && !wait_bar(&empty[st], (uint32_t)(t / C::STAGES - 1) & 1u, abort_flag)) return false;
+    const int halves = it.one_half(p, j) ? 1 : 2, tok = it.key_tile(j) * kTile;
+    mbar_arrive_expect_tx(&full[st], (uint32_t)(halves * kHalf * D * 2));
+    for (int h = 0; h < halves; ++h)
+#pragma unroll
+      for (int c = 0; c < C::NCH; ++c)
+        tma_load_4d(ring + st * C::TILE + c * C::CHUNK + h * kHalf * C::ROWB, map, &full[st], c * C::CH,
+                    it.h / p.heads_per_kv, tok + h * kHalf, it.s);
+    return true;
+  };
+  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x) {
+    const Item it(p, k);
+    const int qb = n & 1;
+    if (n >= 2 && !(ok = wait_bar(&bars.q_empty[qb], (uint32_t)(n / 2 - 1) & 1u, abort_flag))) break;
+    mbar_arrive_expect_tx(&bars.q_full[qb], C::TILE);
+#pragma unroll
+    for (int c = 0; c < C::NCH; ++c)
+      tma_load_4d(sQ + qb * C::TILE + c * C::CHUNK, tq, &bars.q_full[qb], c * C::CH, it.h, it.tile * kTile, it.s);
+    ++n;
+    for (int j = 0; j <= it.steps; ++j) {              // V one tile behind K
+      if (j < it.steps) {
+        if (!(ok = load(g, tk, sK, bars.k_full, bars.k_empty, it, j))) break;
+        ++g;
+      }
+      if (j > 0) {
+        if (!(ok = load(gv, tv, sV, bars.v_full, bars.v_empty, it, j - 1))) break;
+        ++gv;
+      }
+    }
+  }
+  // every copy of this CTA has landed before it may exit
+  for (int i = max(0, n - 2); i < n; ++i) drain_bar(&bars.q_full[i & 1], (uint32_t)(i >> 1) & 1u);
+  for (int t = max(0, g - C::STAGES); t < g; ++t) drain_bar(&bars.k_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
+  for (int t = max(0, gv - C::STAGES); t < gv; ++t) drain_bar(&bars.v_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
+}
+
+// ------------------------------------------------------------------ MMA issuers (warps 9-11, lane 0)
+
+template <int D>
+__device__ __forceinline__ constexpr uint64_t kstep(int ks) {
+  using C = Cfg<D>;
+  return (uint64_t)((((ks * 16) / C::CH) * C::CHUNK + ((ks * 16) % C::CH) * 2) >> 4);
+}
+
+template <int D>
+__device__ void qk_issuer(const FParams& p, Bars& bars, uint8_t* sQ, uint8_t* sK, uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  const uint64_t q0 = make_smem_desc(smem_u32(sQ), 16, C::ATOM, C::SWZ);
+  const uint64_t k0 = make_smem_desc(smem_u32(sK), 16, C::ATOM, C::SWZ);
+  int g = 0, n = 0;
+  bool ok = true;
+  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
+    const Item it(p, k);
+    if (!(ok = wait_pair(bars.q_full, n, abort_flag))) break;
+    const uint64_t a = q0 + (uint64_t)(((n & 1) * C::TILE) >> 4);
+    for (int j = 0; j < it.steps; ++j, ++g) {
+      const int st = g % C::STAGES;
+      // the P of tile g - 2 lay over this S
+      if (g >= 2 && !(ok = wait_pair(bars.pv_done[0], g - 2, abort_flag) && wait_pair(bars.pv_done[1], g - 2, abort_flag))) break;
+      if (!(ok = wait_bar(&bars.k_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) break;
+      tc_fence_after();
+      const uint64_t b = k0 + (uint64_t)((st * C::TILE) >> 4);
+      const uint32_t idesc = make_idesc_bf16(128, it.one_half(p, j) ? kHalf : kTile, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        mma_bf16_ss(tmem + 128u * (g & 1), a + kstep<D>(ks), b + kstep<D>(ks), idesc, ks > 0 ? 1u : 0u);
+      mma_commit(&bars.k_empty[st]);
+      mma_commit(&bars.s_full[g & 1]);
+    }
+    if (ok) mma_commit(&bars.q_empty[n & 1]);
+  }
+  // no MMA of this thread is still at work when the CTA frees its TMEM
+  mma_commit(&bars.drain[0]);
+  drain_bar(&bars.drain[0], 0);
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t col_o(int n, int half) {
+  return Cfg<D>::OB == 2 ? 256u + 128u * (n & 1) + 64u * half : 256u + 128u * half;
+}
+
+template <int D>
+__device__ void pv_issuer(const FParams& p, int half, Bars& bars, uint8_t* sV, uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  const uint64_t v0 = make_smem_desc(smem_u32(sV), C::CHUNK, C::ATOM, C::SWZ);   // MN-major
+  constexpr uint32_t idesc = make_idesc_bf16(128, D, 0, 1);
+  int g = 0, n = 0;
+  bool ok = true;
+  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
+    const Item it(p, k);
+    const int ob = n % C::OB;
+    // the output of the item before in this accumulator has been read
+    if (n >= C::OB && !(ok = wait_bar(&bars.o_free[ob], (uint32_t)(n / C::OB - 1) & 1u, abort_flag))) break;
+    bool acc = false;
+    for (int j = 0; j < it.steps; ++j, ++g) {
+      const int st = g % C::STAGES;
+      if (!(ok = wait_bar(&bars.v_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) break;
+      if (!(ok = wait_pair(bars.p_full[half], g, abort_flag))) break;
+      if (half == 0 || !it.one_half(p, j)) {
+        tc_fence_after();
+        const uint32_t a = tmem + 128u * (g & 1) + 64u * half;
+        const uint64_t b = v0 + (uint64_t)((st * C::TILE + half * kHalf * C::ROWB) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kHalf / 16; ++ks)
+          mma_bf16_ts(tmem + col_o<D>(n, half), a + 8u * ks, b + (uint64_t)((16 * ks * C::ROWB) >> 4), idesc,
+                      (acc || ks > 0) ? 1u : 0u);
+        acc = true;
+      }
+      mma_commit(&bars.v_empty[st]);
+      mma_commit(&bars.pv_done[half][g & 1]);
+    }
+    if (ok) mma_commit(&bars.o_full[ob]);
+  }
+  mma_commit(&bars.drain[1 + half]);
+  drain_bar(&bars.drain[1 + half], 0);
+}
+
+// ------------------------------------------------------------------ softmax (warps 0-7)
+
+// Keys c .. c + 31 that query i sees (bit b: key c + b).
+__device__ __forceinline__ uint32_t visible(int i, int c, int window, int sinks) {
+  const int lim = i - c, low = lim - window, sk = sinks - c;
+  const uint32_t upto = lim >= 31 ? 0xffffffffu : (lim < 0 ? 0u : ((2u << lim) - 1u));
+  const uint32_t from = low <= 0 ? 0xffffffffu : (low >= 32 ? 0u : (0xffffffffu << low));
+  const uint32_t sink = sk >= 32 ? 0xffffffffu : (sk <= 0 ? 0u : ((1u << sk) - 1u));
+  return upto & (from | sink);
+}
+
+// How queries q .. q + 31 see keys k .. k + 63.
+enum : int { kNone = 0, kAll = 1, kSome = 2 };
+__device__ __forceinline__ int visibility(int q, int k, int window, int sinks) {
+  if (q + 31 < k || (q - (k + 63) > window && k >= sinks)) return kNone;
+  return q >= k + 63 && (q + 31 - k <= window || k + 63 < sinks) ? kAll : kSome;
+}
+
+template <int D>
+struct Softmax {
+  using C = Cfg<D>;
+  Bars& bars;
+  volatile int* abort_flag;
+  uint32_t tS, tO;                  // TMEM of this warp's rows: S_0 (this half's columns); O_h of the item's set
+  int half, lane;
+  float c;                          // softmax scale in log2 units
+  float m, l;                       // running maximum (log2 units) and sum of this thread's row
+
+  __device__ __forceinline__ bool done(uint64_t (&bar)[2], int g) const {
+    return __all_sync(0xffffffffu, wait_pair(bar, g, abort_flag));
+  }
+
+  // One tile. Each way of seeing has a copy of the code. `later`: O_h holds a sum of this item.
+  template <int SEE>
+  __device__ __forceinline__ bool tile(int g, uint32_t see0, uint32_t see1, bool later) {
+    const float kNegInf = __int_as_float(0xff800000);
+    const uint32_t t = tS + 128u * (g & 1);
+    uint32_t pk[32];
+    if constexpr (SEE == kNone) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) pk[j] = 0u;
+    } else {
+      uint32_t v[64];
+      tmem_ld_x32(t, v);
+      tmem_ld_x32(t + 32, v + 32);
+      tmem_ld_wait<64>(v);
+      if constexpr (SEE == kSome) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          v[j] = ((see0 >> j) & 1u) ? v[j] : 0xff800000u;
+          v[32 + j] = ((see1 >> j) & 1u) ? v[32 + j] : 0xff800000u;
+        }
+      }
+      float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+      for (int j = 0; j < 64; j += 2)
+        a[(j >> 1) & 3] = max3(a[(j >> 1) & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+      const float mx = fmaxf(max3(a[0], a[1], a[2]), a[3]) * c;          // -inf stays -inf
+      const bool need = mx > m + 8.f;
+      if (__any_sync(0xffffffffu, need)) {
+        // the running maximum grows by more than 2^8: l and O_h follow
+        const float alpha = need ? ex2_approx(m - mx) : 1.f;              // 0 from -inf
+        l *= alpha;
+        if (need) m = mx;
+        if (later) {
+          if (!done(bars.pv_done[half], g - 1)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint32_t o[16];
+            tmem_ld_x16(tO + 16 * ch, o);
+            tmem_ld_wait<16>(o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st_x16(tO + 16 * ch, o);
+          }
+        }
+      }
+      const float ref = SEE == kSome && m == kNegInf ? 0.f : m;           // no key seen yet: all scores are -inf
+      const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
+      uint64_t rs[2] = {0ull, 0ull};
+#pragma unroll
+      for (int j = 0; j < 64; j += 2) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, r2), x0, x1);
+        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        rs[(j >> 1) & 1] = f2_add(rs[(j >> 1) & 1], f2_pack(p0, p1));
+        pk[j >> 1] = pack_bf16x2(p0, p1);
+      }
+      float lo, hi;
+      f2_unpack(f2_add(rs[0], rs[1]), lo, hi);
+      l += lo + hi;
+    }
+    tmem_st_x32(t, pk);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.p_full[half][g & 1]);
+    return true;
+  }
+};
+
+template <int D>
+__device__ void softmax(const FParams& p, Bars& bars, Handoff* hand, uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp: uniform
+  const int quarter = warp & 3, half = warp >> 2;
+  const int row = quarter * 32 + lane;
+  const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+  Softmax<D> W{bars, abort_flag, base + 64u * half, 0u, half, lane, p.scale_log2, 0.f, 0.f};
+  int g = 0, n = 0;
+  for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
+    const Item it(p, k);
+    const int q0 = it.tile * kTile + 32 * quarter;
+    W.tO = base + col_o<D>(n, half);
+    W.m = __int_as_float(0xff800000);
+    W.l = 0.f;
+    bool later = false;
+    for (int j = 0; j < it.steps; ++j, ++g) {
+      const int k0 = it.key_tile(j) * kTile + kHalf * half;
+      const int see = visibility(q0, k0, p.window, p.sinks);
+      if (!W.done(bars.s_full, g)) return;
+      if (half == 1 && it.one_half(p, j)) {            // left out: nothing to store
+        if (lane == 0) mbar_arrive(&bars.p_full[1][g & 1]);
+        continue;
+      }
+      tc_fence_after();
+      bool ok;
+      if (see == kAll) ok = W.template tile<kAll>(g, 0u, 0u, later);
+      else if (see == kSome)
+        ok = W.template tile<kSome>(g, visible(q0 + lane, k0, p.window, p.sinks),
+                                    visible(q0 + lane, k0 + 32, p.window, p.sinks), later);
+      else ok = W.template tile<kNone>(g, 0u, 0u, later);
+      if (!ok) return;
+      later = true;
+    }
+    // the rows' maxima and sums go to the epilogue
+    const int e = n & 1;
+    if (n >= 2 && !__all_sync(0xffffffffu, wait_bar(&bars.epi_empty[e], (uint32_t)(n / 2 - 1) & 1u, abort_flag))) return;
+    hand[e].m[half][row] = W.m;
+    hand[e].l[half][row] = W.l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.epi_full[e]);
+  }
+}
+
+// ------------------------------------------------------------------ epilogue (warps 12-15)
+
+template <int D>
+__device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, const Handoff* hand, uint8_t* out,
+                         uint32_t tmem, volatile int* abort_flag) {
+  using C = Cfg<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const float kNegInf = __int_as_float(0xff800000);
+  const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+  uint8_t* stage = out + quarter * C::OUT;
+  const uint32_t srow = smem_u32(stage) + 64u * lane;
+  int n = 0;
+  for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
+    const Item it(p, k);
+    const int e = n & 1, ob = n % C::OB;
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.epi_full[e], (uint32_t)(n >> 1) & 1u, abort_flag))) break;
+    const float m0 = hand[e].m[0][row], m1 = hand[e].m[1][row], l0 = hand[e].l[0][row], l1 = hand[e].l[1][row];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.epi_empty[e]);
+    const float m = fmaxf(m0, m1);
+    float f0 = m0 == kNegInf ? 0.f : ex2_approx(m0 - m), f1 = m1 == kNegInf ? 0.f : ex2_approx(m1 - m);
+    const float L = l0 * f0 + l1 * f1;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    f0 *= inv;
+    f1 *= inv;
+    const int q0 = it.tile * kTile + 32 * quarter, tok = q0 + lane;
+    if (tok < p.n_tokens)
+      p.lse[((int64_t)it.s * p.heads + it.h) * p.n_tokens + tok] =
+          L > 0.f ? (m + __log2f(L)) * 0.69314718055994531f : kNegInf;
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.o_full[ob], (uint32_t)(n / C::OB) & 1u, abort_flag))) break;
+    tc_fence_after();
+    const uint32_t t0 = base + col_o<D>(n, 0), t1 = base + col_o<D>(n, 1);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      if (lane == 0) bulk_wait_group_read<0>();          // the staging memory has been read
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t a[16], b[16];
+        tmem_ld_x16(t0 + c + 16 * q, a);
+        tmem_ld_x16(t1 + c + 16 * q, b);
+        tmem_ld_wait<16>(a);
+        tmem_ld_wait<16>(b);
+        uint32_t pk[8];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2)
+          pk[j >> 1] = pack_bf16x2(__uint_as_float(a[j]) * f0 + __uint_as_float(b[j]) * f1,
+                                   __uint_as_float(a[j + 1]) * f0 + __uint_as_float(b[j + 1]) * f1);
+        // 64-byte rows, 64B swizzle: unit u of row r at u ^ (r / 2) % 4
+        const uint32_t x = (uint32_t)(lane >> 1) & 3u;
+        st_shared_v4(srow + (((2u * q) ^ x) << 4), pk[0], pk[1], pk[2], pk[3]);
+        st_shared_v4(srow + (((2u * q + 1u) ^ x) << 4), pk[4], pk[5], pk[6], pk[7]);
+      }
+      if (c + 32 == D) {
+        // the accumulators have been read: the next item that uses them may start
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.o_free[ob]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && q0 < p.n_tokens) {                // rows past the sequence are dropped by the store
+        tma_store_4d(to, stage, c, it.h, q0, it.s);
+        bulk_commit_group();
+      }
+    }
+  }
+  // this warp's stores are complete before the CTA may exit
+  if (lane == 0) bulk_wait_group<0>();
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    sink_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                    const __grid_constant__ FParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Bars bars;
+  __shared__ Handoff hand[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], 1);
+      mbar_init(&bars.q_empty[i], 1);
+      mbar_init(&bars.s_full[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bars.p_full[h][i], kHalfWarps);
+        mbar_init(&bars.pv_done[h][i], 1);
+      }
+      mbar_init(&bars.o_full[i], 2);                     // both halves' issuers
+      mbar_init(&bars.o_free[i], kEpilogueWarps);
+      mbar_init(&bars.epi_full[i], kSoftmaxWarps);
+      mbar_init(&bars.epi_empty[i], kEpilogueWarps);
+    }
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], 1);
+      mbar_init(&bars.v_empty[i], 2);                    // both halves' issuers
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&bars.drain[i], 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+    tma_prefetch_desc(&to);
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  uint8_t* sQ = sbase;
+  uint8_t* sK = sQ + 2 * C::TILE;
+  uint8_t* sV = sK + C::STAGES * C::TILE;
+  uint8_t* sOut = sV + C::STAGES * C::TILE;
+  // The register split's sum is the launch's allocation (checked on the host), so the growth
+  // always completes.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
+    softmax<D>(p, bars, hand, tmem, &abort_flag);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    if (warp == 8) {
+      if ((threadIdx.x & 31) == 0) loader<D>(p, &tq, &tk, &tv, bars, sQ, sK, sV, &abort_flag);
+      __syncwarp();
+    } else if (warp == 9) {
+      if ((threadIdx.x & 31) == 0) qk_issuer<D>(p, bars, sQ, sK, tmem, &abort_flag);
+      __syncwarp();
+    } else if (warp < 12) {
+      if ((threadIdx.x & 31) == 0) pv_issuer<D>(p, warp - 10, bars, sV, tmem, &abort_flag);
+      __syncwarp();
+    } else {
+      epilogue<D>(p, &to, bars, hand, sOut, tmem, &abort_flag);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
 
 template <int D>
 int launch_d(const SinkArgs& a, cudaStream_t stream) {
   using C = Cfg<D>;
   CUtensorMap tq, tk, tv, to;
-  if (!encode_bhnd_map(&tq, a.q, a.batch, a.n_tokens, a.heads, D, a.q_strides[0], a.q_strides[1], a.q_strides[2],
-                       C::CH, kTile, C::TMA_SWZ) ||
-      !encode_bhnd_map(&tk, a.k, a.batch, a.n_tokens, a.kv_heads, D, a.k_strides[0], a.k_strides[1], a.k_strides[2],
-                       C::CH, 32, C::TMA_SWZ) ||
-      !encode_bhnd_map(&tv, a.v, a.batch, a.n_tokens, a.kv_heads, D, a.v_strides[0], a.v_strides[1], a.v_strides[2],
-                       C::CH, 32, C::TMA_SWZ))
+  const auto map = [&](CUtensorMap* m, const void* base, int heads, const int64_t st[3], int cols, int rows,
+                       CUtensorMapSwizzle swz) {
+    return encode_bhnd_map(m, base, a.batch, a.n_tokens, heads, D, st[0], st[1], st[2], cols, rows, swz);
+  };
+  if (!map(&tq, a.q, a.heads, a.q_strides, C::CH, kTile, C::TMA_SWZ) ||
+      !map(&tk, a.k, a.kv_heads, a.k_strides, C::CH, kHalf, C::TMA_SWZ) ||
+      !map(&tv, a.v, a.kv_heads, a.v_strides, C::CH, kHalf, C::TMA_SWZ) ||
+      !map(&to, a.o, a.heads, a.o_strides, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SA_ERR_UNSUPPORTED;
-  Params p;
-  memset(&p, 0, sizeof(p));
+  FParams p;
   p.batch = a.batch;
   p.n_tokens = a.n_tokens;
   p.heads = a.heads;
   p.heads_per_kv = a.heads / a.kv_heads;
-  p.block = 32;                        // K / V boxes of one 32-key chunk
-  p.log2b = 5;
-  p.causal = 1;
-  p.tiles_per_seq = (a.n_tokens + kTile - 1) / kTile;
-  p.n_items = a.batch * a.heads * p.tiles_per_seq;
-  p.n_masks = 1;
-  p.o = static_cast<__nv_bfloat16*>(a.o);
-  memset(&to, 0, sizeof(to));
-  p.o_tma = D == 64 && encode_bhnd_map(&to, a.o, a.batch, a.n_tokens, a.heads, D, a.o_strides[0], a.o_strides[1],
-                                       a.o_strides[2], C::CH, 32, C::TMA_SWZ)
-                ? 1
-                : 0;
-  p.lse = a.lse;
-  p.o_sb = a.o_strides[0];
-  p.o_sn = a.o_strides[1];
-  p.o_sh = a.o_strides[2];
-  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  p.tiles = (a.n_tokens + kTile - 1) / kTile;
+  p.n_items = a.batch * a.heads * p.tiles;
   p.window = a.window;
   p.sinks = a.sinks;
-  const auto kern = [] {
-    if constexpr (C::WIDE) return attn_fwd_wide_kernel<D, true>;
-    else return attn_fwd_kernel<D, true>;
-  }();
-  // the kernels' register split hands out exactly the launch allocation
+  p.lse = a.lse;
+  p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  const auto kern = sink_fwd_kernel<D>;
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return SA_ERR_CUDA;
   if (fa.numRegs != kLaunchRegs) return SA_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
-  const int per_cta = C::WIDE ? 1 : 2;
   const int sm_count = current_sm_count();
-  const int need = (p.n_items + per_cta - 1) / per_cta;
-  kern<<<need < sm_count ? need : sm_count, kThreads, C::SMEM, stream>>>(tq, tk, tv, to, p);
+  kern<<<p.n_items < sm_count ? p.n_items : sm_count, kThreads, C::SMEM, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -79,8 +624,8 @@ int launch_sink_attn_fwd(const SinkArgs& a, cudaStream_t stream) {
 
 unsigned int sink_fwd_read_and_clear_error(cudaStream_t stream) {
   unsigned int v = 0, zero = 0;
-  cudaMemcpyFromSymbolAsync(&v, g_attn_err, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
-  cudaMemcpyToSymbolAsync(g_attn_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+  cudaMemcpyFromSymbolAsync(&v, g_sink_fwd_err, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+  cudaMemcpyToSymbolAsync(g_sink_fwd_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
   cudaStreamSynchronize(stream);
   return v;
 }
