@@ -14,9 +14,8 @@
 // other is in its loads and stores. The running maximum is followed only when it grows by more than
 // 2^8; probabilities are then at most 2^8, rounded to bf16 for the tensor core, and summed in fp32.
 //
-// TMEM (512 columns): S_b [128 b, +128) for tiles b = g % 2; P of half h over the first 32 of its own 64
-// columns of S_b (bf16 pairs), so the second PV's completion frees S_b for the tile after next;
-// O_h from column 256 on, at d <= 64 in two sets that items alternate between.
+// TMEM (512 columns): S_b [128 b, +128), b = g % SB, SB = 2 (d = 128) or 3; P of half h over the first 32
+// of its own 64 columns of S_b (bf16 pairs), so the PVs' completion frees S_b; then O_0 and O_1.
 //
 // Warp roles (512 threads; warp w runs on SM sub-partition w % 4):
 //   warps 0-7   softmax: query rows 32 (w % 4) .. of the tile, key half w / 4
@@ -43,7 +42,7 @@ constexpr int kTile = 128;            // queries of an item; keys of a tile
 constexpr int kHalf = 64;             // keys of a half
 constexpr int kThreads = 512;
 constexpr int kSoftmaxWarps = 8, kHalfWarps = 4, kEpilogueWarps = 4;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 4, kMaxS = 3;
 constexpr uint32_t kTmemCols = 512;
 // Register split (setmaxnreg): softmax warpgroups 184, the others 72, of 128 per thread at launch
 constexpr int kLaunchRegs = 128;
@@ -61,7 +60,9 @@ struct Cfg {
   static constexpr int CHUNK = kTile * ROWB;           // one d-chunk of a 128-row tile
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int STAGES = D == 128 ? 2 : 4;      // of K and of V
-  static constexpr int OB = D == 128 ? 1 : 2;          // sets of output accumulators
+  static constexpr int SB = D == 128 ? 2 : 3;          // S buffers
+  static constexpr uint32_t COL_O = 128 * SB;          // O_0; O_1 follows
+  static_assert(COL_O + 2 * D <= kTmemCols, "TMEM columns");
   static constexpr int OUT = 2048;                     // staging per epilogue warp: 32 rows of 32 elements
   static constexpr int SMEM = 1024 + (2 + 2 * STAGES) * TILE + kEpilogueWarps * OUT;
   static_assert(STAGES <= kMaxStages && SMEM <= 222 * 1024, "shared memory");
@@ -78,11 +79,11 @@ struct FParams {
 struct Bars {
   uint64_t q_full[2], q_empty[2];                                 // phase: item / 2
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-  // per tile g, alternating (phase: g / 2)
-  uint64_t s_full[2];               // S written
-  uint64_t p_full[2][2];            // [half]: P stored
-  uint64_t pv_done[2][2];           // [half]: the PV is complete
-  uint64_t o_full[2], o_free[2];    // per accumulator set: an item's output complete; read
+  // per S buffer (tile g: barrier g % SB, phase g / SB)
+  uint64_t s_full[kMaxS];           // S written
+  uint64_t p_full[2][kMaxS];        // [half]: P stored
+  uint64_t pv_done[kMaxS];          // both halves' PVs complete
+  uint64_t o_full, o_free;          // an item's output complete; read
   uint64_t epi_full[2], epi_empty[2];   // maxima and sums handed to the epilogue
   uint64_t drain[3];
 };
@@ -94,8 +95,10 @@ struct Handoff {
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return mbar_wait_suspend(bar, parity, abort_flag, &g_sink_fwd_err, kErrTimeout);
 }
-__device__ __forceinline__ bool wait_pair(uint64_t (&bar)[2], int g, volatile int* abort_flag) {
-  return wait_bar(&bar[g & 1], (uint32_t)(g >> 1) & 1u, abort_flag);
+// Use n of a ring of N barriers.
+template <int N>
+__device__ __forceinline__ bool wait_ring(uint64_t* bar, int n, volatile int* abort_flag) {
+  return wait_bar(&bar[n % N], (uint32_t)(n / N) & 1u, abort_flag);
 }
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
   int never = 0;
@@ -209,32 +212,27 @@ __device__ void qk_issuer(const FParams& p, Bars& bars, uint8_t* sQ, uint8_t* sK
   bool ok = true;
   for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
     const Item it(p, k);
-    if (!(ok = wait_pair(bars.q_full, n, abort_flag))) break;
+    if (!(ok = wait_ring<2>(bars.q_full, n, abort_flag))) break;
     const uint64_t a = q0 + (uint64_t)(((n & 1) * C::TILE) >> 4);
     for (int j = 0; j < it.steps; ++j, ++g) {
       const int st = g % C::STAGES;
-      // the P of tile g - 2 lay over this S
-      if (g >= 2 && !(ok = wait_pair(bars.pv_done[0], g - 2, abort_flag) && wait_pair(bars.pv_done[1], g - 2, abort_flag))) break;
-      if (!(ok = wait_bar(&bars.k_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) break;
+      if (!(ok = wait_ring<C::STAGES>(bars.k_full, g, abort_flag))) break;
+      // the P of tile g - SB lay over this S
+      if (g >= C::SB && !(ok = wait_ring<C::SB>(bars.pv_done, g - C::SB, abort_flag))) break;
       tc_fence_after();
       const uint64_t b = k0 + (uint64_t)((st * C::TILE) >> 4);
       const uint32_t idesc = make_idesc_bf16(128, it.one_half(p, j) ? kHalf : kTile, 0, 0);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
-        mma_bf16_ss(tmem + 128u * (g & 1), a + kstep<D>(ks), b + kstep<D>(ks), idesc, ks > 0 ? 1u : 0u);
+        mma_bf16_ss(tmem + 128u * (g % C::SB), a + kstep<D>(ks), b + kstep<D>(ks), idesc, ks > 0 ? 1u : 0u);
       mma_commit(&bars.k_empty[st]);
-      mma_commit(&bars.s_full[g & 1]);
+      mma_commit(&bars.s_full[g % C::SB]);
     }
     if (ok) mma_commit(&bars.q_empty[n & 1]);
   }
   // no MMA of this thread is still at work when the CTA frees its TMEM
   mma_commit(&bars.drain[0]);
   drain_bar(&bars.drain[0], 0);
-}
-
-template <int D>
-__device__ __forceinline__ uint32_t col_o(int n, int half) {
-  return Cfg<D>::OB == 2 ? 256u + 128u * (n & 1) + 64u * half : 256u + 128u * half;
 }
 
 template <int D>
@@ -246,28 +244,27 @@ __device__ void pv_issuer(const FParams& p, int half, Bars& bars, uint8_t* sV, u
   bool ok = true;
   for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
     const Item it(p, k);
-    const int ob = n % C::OB;
-    // the output of the item before in this accumulator has been read
-    if (n >= C::OB && !(ok = wait_bar(&bars.o_free[ob], (uint32_t)(n / C::OB - 1) & 1u, abort_flag))) break;
     bool acc = false;
     for (int j = 0; j < it.steps; ++j, ++g) {
       const int st = g % C::STAGES;
-      if (!(ok = wait_bar(&bars.v_full[st], (uint32_t)(g / C::STAGES) & 1u, abort_flag))) break;
-      if (!(ok = wait_pair(bars.p_full[half], g, abort_flag))) break;
+      if (!(ok = wait_ring<C::STAGES>(bars.v_full, g, abort_flag))) break;
+      // the item before has been read
+      if (j == 0 && n > 0 && !(ok = wait_bar(&bars.o_free, (uint32_t)(n - 1) & 1u, abort_flag))) break;
+      if (!(ok = wait_ring<C::SB>(bars.p_full[half], g, abort_flag))) break;
       if (half == 0 || !it.one_half(p, j)) {
         tc_fence_after();
-        const uint32_t a = tmem + 128u * (g & 1) + 64u * half;
+        const uint32_t a = tmem + 128u * (g % C::SB) + 64u * half;
         const uint64_t b = v0 + (uint64_t)((st * C::TILE + half * kHalf * C::ROWB) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kHalf / 16; ++ks)
-          mma_bf16_ts(tmem + col_o<D>(n, half), a + 8u * ks, b + (uint64_t)((16 * ks * C::ROWB) >> 4), idesc,
+          mma_bf16_ts(tmem + C::COL_O + (uint32_t)(D * half), a + 8u * ks, b + (uint64_t)((16 * ks * C::ROWB) >> 4), idesc,
                       (acc || ks > 0) ? 1u : 0u);
         acc = true;
       }
       mma_commit(&bars.v_empty[st]);
-      mma_commit(&bars.pv_done[half][g & 1]);
+      mma_commit(&bars.pv_done[g % C::SB]);
     }
-    if (ok) mma_commit(&bars.o_full[ob]);
+    if (ok) mma_commit(&bars.o_full);
   }
   mma_commit(&bars.drain[1 + half]);
   drain_bar(&bars.drain[1 + half], 0);
@@ -286,9 +283,34 @@ __device__ __forceinline__ uint32_t visible(int i, int c, int window, int sinks)
 
 // How queries q .. q + 31 see keys k .. k + 63.
 enum : int { kNone = 0, kAll = 1, kSome = 2 };
+// Whether some of queries q .. q + 31 sees some of keys k .. k + 31.
+__device__ __forceinline__ bool some(int q, int k, int window, int sinks) {
+  return q + 31 >= k && (q - (k + 31) <= window || k < sinks);
+}
 __device__ __forceinline__ int visibility(int q, int k, int window, int sinks) {
   if (q + 31 < k || (q - (k + 63) > window && k >= sinks)) return kNone;
   return q >= k + 63 && (q + 31 - k <= window || k + 63 < sinks) ? kAll : kSome;
+}
+
+__device__ __forceinline__ void mask_chunk(uint32_t* v, uint32_t see) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = ((see >> j) & 1u) ? v[j] : 0xff800000u;
+}
+__device__ __forceinline__ void max_chunk(const uint32_t* v, float (&a)[4]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2)
+    a[(j >> 1) & 3] = max3(a[(j >> 1) & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+}
+// p = 2^(s c - r) as bf16 pairs; sums into rs
+__device__ __forceinline__ void exp_chunk(const uint32_t* v, uint64_t c2, uint64_t r2, uint32_t* pk, uint64_t (&rs)[2]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, r2), x0, x1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    rs[(j >> 1) & 1] = f2_add(rs[(j >> 1) & 1], f2_pack(p0, p1));
+    pk[j >> 1] = pack_bf16x2(p0, p1);
+  }
 }
 
 template <int D>
@@ -296,40 +318,42 @@ struct Softmax {
   using C = Cfg<D>;
   Bars& bars;
   volatile int* abort_flag;
-  uint32_t tS, tO;                  // TMEM of this warp's rows: S_0 (this half's columns); O_h of the item's set
+  uint32_t tS, tO;                  // TMEM of this warp's rows: S_0 (this half's columns), O_h
   int half, lane;
   float c;                          // softmax scale in log2 units
   float m, l;                       // running maximum (log2 units) and sum of this thread's row
 
-  __device__ __forceinline__ bool done(uint64_t (&bar)[2], int g) const {
-    return __all_sync(0xffffffffu, wait_pair(bar, g, abort_flag));
+  __device__ __forceinline__ bool done(uint64_t* bar, int g) const {
+    return __all_sync(0xffffffffu, wait_ring<C::SB>(bar, g, abort_flag));
   }
 
-  // One tile. Each way of seeing has a copy of the code. `later`: O_h holds a sum of this item.
+  // One tile. Each way of seeing has a copy of the code. kSome: see0 / see1 are the keys that the
+  // row sees of the two 32-key chunks, any0 / any1 whether some row of the warp sees any (uniform).
+  // `later`: O_h holds a sum of this item.
   template <int SEE>
-  __device__ __forceinline__ bool tile(int g, uint32_t see0, uint32_t see1, bool later) {
+  __device__ __forceinline__ bool tile(int g, bool any0, bool any1, uint32_t see0, uint32_t see1, bool later) {
     const float kNegInf = __int_as_float(0xff800000);
-    const uint32_t t = tS + 128u * (g & 1);
+    const uint32_t t = tS + 128u * (g % C::SB);
     uint32_t pk[32];
     if constexpr (SEE == kNone) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) pk[j] = 0u;
     } else {
       uint32_t v[64];
-      tmem_ld_x32(t, v);
-      tmem_ld_x32(t + 32, v + 32);
+      // kSome: a 32-key chunk that no row of the warp sees is not loaded
+      const bool on0 = SEE == kAll || any0, on1 = SEE == kAll || any1;
+      if (on0) tmem_ld_x32(t, v);
+      if (on1) tmem_ld_x32(t + 32, v + 32);
       tmem_ld_wait<64>(v);
-      if constexpr (SEE == kSome) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          v[j] = ((see0 >> j) & 1u) ? v[j] : 0xff800000u;
-          v[32 + j] = ((see1 >> j) & 1u) ? v[32 + j] : 0xff800000u;
-        }
-      }
       float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-      for (int j = 0; j < 64; j += 2)
-        a[(j >> 1) & 3] = max3(a[(j >> 1) & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+      if (on0) {
+        if constexpr (SEE == kSome) mask_chunk(v, see0);
+        max_chunk(v, a);
+      }
+      if (on1) {
+        if constexpr (SEE == kSome) mask_chunk(v + 32, see1);
+        max_chunk(v + 32, a);
+      }
       const float mx = fmaxf(max3(a[0], a[1], a[2]), a[3]) * c;          // -inf stays -inf
       const bool need = mx > m + 8.f;
       if (__any_sync(0xffffffffu, need)) {
@@ -338,7 +362,7 @@ struct Softmax {
         l *= alpha;
         if (need) m = mx;
         if (later) {
-          if (!done(bars.pv_done[half], g - 1)) return false;
+          if (!done(bars.pv_done, g - 1)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int ch = 0; ch < D / 16; ++ch) {
@@ -354,13 +378,17 @@ struct Softmax {
       const float ref = SEE == kSome && m == kNegInf ? 0.f : m;           // no key seen yet: all scores are -inf
       const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
       uint64_t rs[2] = {0ull, 0ull};
+      if (on0) {
+        exp_chunk(v, c2, r2, pk, rs);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        float x0, x1;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, r2), x0, x1);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        rs[(j >> 1) & 1] = f2_add(rs[(j >> 1) & 1], f2_pack(p0, p1));
-        pk[j >> 1] = pack_bf16x2(p0, p1);
+        for (int j = 0; j < 16; ++j) pk[j] = 0u;
+      }
+      if (on1) {
+        exp_chunk(v + 32, c2, r2, pk + 16, rs);
+      } else {
+#pragma unroll
+        for (int j = 16; j < 32; ++j) pk[j] = 0u;
       }
       float lo, hi;
       f2_unpack(f2_add(rs[0], rs[1]), lo, hi);
@@ -370,7 +398,7 @@ struct Softmax {
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.p_full[half][g & 1]);
+    if (lane == 0) mbar_arrive(&bars.p_full[half][g % C::SB]);
     return true;
   }
 };
@@ -382,12 +410,12 @@ __device__ void softmax(const FParams& p, Bars& bars, Handoff* hand, uint32_t tm
   const int quarter = warp & 3, half = warp >> 2;
   const int row = quarter * 32 + lane;
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
-  Softmax<D> W{bars, abort_flag, base + 64u * half, 0u, half, lane, p.scale_log2, 0.f, 0.f};
+  Softmax<D> W{bars, abort_flag, base + 64u * half, base + C::COL_O + (uint32_t)(D * half), half, lane, p.scale_log2,
+               0.f, 0.f};
   int g = 0, n = 0;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
     const Item it(p, k);
     const int q0 = it.tile * kTile + 32 * quarter;
-    W.tO = base + col_o<D>(n, half);
     W.m = __int_as_float(0xff800000);
     W.l = 0.f;
     bool later = false;
@@ -396,16 +424,17 @@ __device__ void softmax(const FParams& p, Bars& bars, Handoff* hand, uint32_t tm
       const int see = visibility(q0, k0, p.window, p.sinks);
       if (!W.done(bars.s_full, g)) return;
       if (half == 1 && it.one_half(p, j)) {            // left out: nothing to store
-        if (lane == 0) mbar_arrive(&bars.p_full[1][g & 1]);
+        if (lane == 0) mbar_arrive(&bars.p_full[1][g % C::SB]);
         continue;
       }
       tc_fence_after();
       bool ok;
-      if (see == kAll) ok = W.template tile<kAll>(g, 0u, 0u, later);
+      if (see == kAll) ok = W.template tile<kAll>(g, true, true, 0u, 0u, later);
       else if (see == kSome)
-        ok = W.template tile<kSome>(g, visible(q0 + lane, k0, p.window, p.sinks),
+        ok = W.template tile<kSome>(g, some(q0, k0, p.window, p.sinks), some(q0, k0 + 32, p.window, p.sinks),
+                                    visible(q0 + lane, k0, p.window, p.sinks),
                                     visible(q0 + lane, k0 + 32, p.window, p.sinks), later);
-      else ok = W.template tile<kNone>(g, 0u, 0u, later);
+      else ok = W.template tile<kNone>(g, false, false, 0u, 0u, later);
       if (!ok) return;
       later = true;
     }
@@ -435,7 +464,7 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
   int n = 0;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
     const Item it(p, k);
-    const int e = n & 1, ob = n % C::OB;
+    const int e = n & 1;
     if (!__all_sync(0xffffffffu, wait_bar(&bars.epi_full[e], (uint32_t)(n >> 1) & 1u, abort_flag))) break;
     const float m0 = hand[e].m[0][row], m1 = hand[e].m[1][row], l0 = hand[e].l[0][row], l1 = hand[e].l[1][row];
     __syncwarp();
@@ -450,9 +479,9 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
     if (tok < p.n_tokens)
       p.lse[((int64_t)it.s * p.heads + it.h) * p.n_tokens + tok] =
           L > 0.f ? (m + __log2f(L)) * 0.69314718055994531f : kNegInf;
-    if (!__all_sync(0xffffffffu, wait_bar(&bars.o_full[ob], (uint32_t)(n / C::OB) & 1u, abort_flag))) break;
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.o_full, (uint32_t)n & 1u, abort_flag))) break;
     tc_fence_after();
-    const uint32_t t0 = base + col_o<D>(n, 0), t1 = base + col_o<D>(n, 1);
+    const uint32_t t0 = base + C::COL_O, t1 = t0 + D;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       if (lane == 0) bulk_wait_group_read<0>();          // the staging memory has been read
@@ -478,7 +507,7 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
         // the accumulators have been read: the next item that uses them may start
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.o_free[ob]);
+        if (lane == 0) mbar_arrive(&bars.o_free);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -512,13 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
-      mbar_init(&bars.s_full[i], 1);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&bars.p_full[h][i], kHalfWarps);
-        mbar_init(&bars.pv_done[h][i], 1);
-      }
-      mbar_init(&bars.o_full[i], 2);                     // both halves' issuers
-      mbar_init(&bars.o_free[i], kEpilogueWarps);
       mbar_init(&bars.epi_full[i], kSoftmaxWarps);
       mbar_init(&bars.epi_empty[i], kEpilogueWarps);
     }
@@ -528,6 +550,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.v_full[i], 1);
       mbar_init(&bars.v_empty[i], 2);                    // both halves' issuers
     }
+    for (int i = 0; i < C::SB; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.pv_done[i], 2);                    // both halves' issuers
+      for (int h = 0; h < 2; ++h) mbar_init(&bars.p_full[h][i], kHalfWarps);
+    }
+    mbar_init(&bars.o_full, 2);                          // both halves' issuers
+    mbar_init(&bars.o_free, kEpilogueWarps);
     for (int i = 0; i < 3; ++i) mbar_init(&bars.drain[i], 1);
     abort_flag = 0;
     fence_mbar_init();
