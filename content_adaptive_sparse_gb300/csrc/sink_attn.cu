@@ -151,26 +151,35 @@ struct Item {
 
 // ------------------------------------------------------------------ loader (warp 8, lane 0)
 
+// One K or V tile into its ring stage: a box of 128 rows, or of 64 (`half`).
 template <int D>
-__device__ void loader(const FParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, Bars& bars,
-                       uint8_t* sQ, uint8_t* sK, uint8_t* sV, volatile int* abort_flag) {
+__device__ __forceinline__ bool load_tile(int t, const CUtensorMap* whole, const CUtensorMap* part, bool half,
+                                          uint8_t* ring, uint64_t* full, uint64_t* empty, int hk, int tok, int s,
+                                          volatile int* abort_flag) {
+  using C = Cfg<D>;
+  const int st = t % C::STAGES;
+  if (t >= C::STAGES && !wait_bar(&empty[st], (uint32_t)(t / C::STAGES - 1) & 1u, abort_flag)) return false;
+  mbar_arrive_expect_tx(&full[st], half ? C::TILE / 2 : C::TILE);
+  const CUtensorMap* map = half ? part : whole;
+#pragma unroll
+  for (int c = 0; c < C::NCH; ++c)
+    tma_load_4d(ring + st * C::TILE + c * C::CHUNK, map, &full[st], c * C::CH, hk, tok, s);
+  return true;
+}
+
+// The loader is one thread between the softmax warps' instructions; at d = 64 its instructions per
+// tile decide how far ahead it gets, so a tile is one box and nothing is divided inside an item.
+template <int D>
+__device__ void loader(const FParams& p, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
+                       const CUtensorMap* tkh, const CUtensorMap* tvh, Bars& bars, uint8_t* sQ, uint8_t* sK, uint8_t* sV,
+                       volatile int* abort_flag) {
   using C = Cfg<D>;
   int g = 0, gv = 0, n = 0;          // K tiles, V tiles and Q tiles requested
   bool ok = true;
-  const auto load = [&](int t, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, const Item& it, int j) {
-    const int st = t % C::STAGES;
-    if (t >= C::STAGES && !wait_bar(&empty[st], (uint32_t)(t / C::STAGES - 1) & 1u, abort_flag)) return false;
-    const int halves = it.one_half(p, j) ? 1 : 2, tok = it.key_tile(j) * kTile;
-    mbar_arrive_expect_tx(&full[st], (uint32_t)(halves * kHalf * D * 2));
-    for (int h = 0; h < halves; ++h)
-#pragma unroll
-      for (int c = 0; c < C::NCH; ++c)
-        tma_load_4d(ring + st * C::TILE + c * C::CHUNK + h * kHalf * C::ROWB, map, &full[st], c * C::CH,
-                    it.h / p.heads_per_kv, tok + h * kHalf, it.s);
-    return true;
-  };
+  const bool halved = p.sinks <= kHalf;
   for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x) {
     const Item it(p, k);
+    const int hk = it.h / p.heads_per_kv;
     const int qb = n & 1;
     if (n >= 2 && !(ok = wait_bar(&bars.q_empty[qb], (uint32_t)(n / 2 - 1) & 1u, abort_flag))) break;
     mbar_arrive_expect_tx(&bars.q_full[qb], C::TILE);
@@ -178,15 +187,22 @@ __device__ void loader(const FParams& p, const CUtensorMap* tq, const CUtensorMa
     for (int c = 0; c < C::NCH; ++c)
       tma_load_4d(sQ + qb * C::TILE + c * C::CHUNK, tq, &bars.q_full[qb], c * C::CH, it.h, it.tile * kTile, it.s);
     ++n;
+    int tok = it.n_sink ? 0 : it.t0 * kTile, before = 0;
+    bool half = it.n_sink != 0 && halved, half_before = false;
     for (int j = 0; j <= it.steps; ++j) {              // V one tile behind K
       if (j < it.steps) {
-        if (!(ok = load(g, tk, sK, bars.k_full, bars.k_empty, it, j))) break;
+        if (!(ok = load_tile<D>(g, tk, tkh, half, sK, bars.k_full, bars.k_empty, hk, tok, it.s, abort_flag))) break;
         ++g;
       }
       if (j > 0) {
-        if (!(ok = load(gv, tv, sV, bars.v_full, bars.v_empty, it, j - 1))) break;
+        if (!(ok = load_tile<D>(gv, tv, tvh, half_before, sV, bars.v_full, bars.v_empty, hk, before, it.s, abort_flag)))
+          break;
         ++gv;
       }
+      before = tok;
+      half_before = half;
+      tok = j < it.n_sink ? it.t0 * kTile : tok + kTile;
+      half = false;
     }
   }
   // every copy of this CTA has landed before it may exit
@@ -527,7 +543,8 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     sink_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tkh,
+                    const __grid_constant__ CUtensorMap tvh, const __grid_constant__ CUtensorMap to,
                     const __grid_constant__ FParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -585,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 8) {
-      if ((threadIdx.x & 31) == 0) loader<D>(p, &tq, &tk, &tv, bars, sQ, sK, sV, &abort_flag);
+      if ((threadIdx.x & 31) == 0) loader<D>(p, &tq, &tk, &tv, &tkh, &tvh, bars, sQ, sK, sV, &abort_flag);
       __syncwarp();
     } else if (warp == 9) {
       if ((threadIdx.x & 31) == 0) qk_issuer<D>(p, bars, sQ, sK, tmem, &abort_flag);
@@ -608,14 +625,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 int launch_d(const SinkArgs& a, cudaStream_t stream) {
   using C = Cfg<D>;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv, tkh, tvh, to;
   const auto map = [&](CUtensorMap* m, const void* base, int heads, const int64_t st[3], int cols, int rows,
                        CUtensorMapSwizzle swz) {
     return encode_bhnd_map(m, base, a.batch, a.n_tokens, heads, D, st[0], st[1], st[2], cols, rows, swz);
   };
   if (!map(&tq, a.q, a.heads, a.q_strides, C::CH, kTile, C::TMA_SWZ) ||
-      !map(&tk, a.k, a.kv_heads, a.k_strides, C::CH, kHalf, C::TMA_SWZ) ||
-      !map(&tv, a.v, a.kv_heads, a.v_strides, C::CH, kHalf, C::TMA_SWZ) ||
+      !map(&tk, a.k, a.kv_heads, a.k_strides, C::CH, kTile, C::TMA_SWZ) ||
+      !map(&tv, a.v, a.kv_heads, a.v_strides, C::CH, kTile, C::TMA_SWZ) ||
+      !map(&tkh, a.k, a.kv_heads, a.k_strides, C::CH, kHalf, C::TMA_SWZ) ||
+      !map(&tvh, a.v, a.kv_heads, a.v_strides, C::CH, kHalf, C::TMA_SWZ) ||
       !map(&to, a.o, a.heads, a.o_strides, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SA_ERR_UNSUPPORTED;
   FParams p;
@@ -636,7 +655,8 @@ int launch_d(const SinkArgs& a, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
   const int sm_count = current_sm_count();
-  kern<<<p.n_items < sm_count ? p.n_items : sm_count, kThreads, C::SMEM, stream>>>(tq, tk, tv, to, p);
+  kern<<<p.n_items < sm_count ? p.n_items : sm_count, kThreads, C::SMEM, stream>>>(tq, tk, tv, tkh, tvh, to,
+                                                                                        p);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
