@@ -63,7 +63,10 @@ struct Cfg {
   static constexpr int SB = D == 128 ? 2 : 3;          // S buffers
   static constexpr uint32_t COL_O = 128 * SB;          // O_0; O_1 follows
   static_assert(COL_O + 2 * D <= kTmemCols, "TMEM columns");
-  static constexpr int OUT = 2048;                     // staging per epilogue warp: 32 rows of 32 elements
+  // Staging per epilogue warp, boxes of 32 rows by 32 elements: a whole row at d <= 64, so that the
+  // accumulators are free as soon as they are read; a quarter of one at d = 128
+  static constexpr int BOXES = D == 128 ? 1 : D / 32;
+  static constexpr int OUT = 2048 * BOXES;
   static constexpr int SMEM = 1024 + (2 + 2 * STAGES) * TILE + kEpilogueWarps * OUT;
   static_assert(STAGES <= kMaxStages && SMEM <= 222 * 1024, "shared memory");
 };
@@ -499,14 +502,14 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
     tc_fence_after();
     const uint32_t t0 = base + C::COL_O, t1 = t0 + D;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c0 = 0; c0 < D; c0 += 32 * C::BOXES) {
       if (lane == 0) bulk_wait_group_read<0>();          // the staging memory has been read
       __syncwarp();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < 2 * C::BOXES; ++q) {
         uint32_t a[16], b[16];
-        tmem_ld_x16(t0 + c + 16 * q, a);
-        tmem_ld_x16(t1 + c + 16 * q, b);
+        tmem_ld_x16(t0 + c0 + 16 * q, a);
+        tmem_ld_x16(t1 + c0 + 16 * q, b);
         tmem_ld_wait<16>(a);
         tmem_ld_wait<16>(b);
         uint32_t pk[8];
@@ -515,12 +518,12 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
           pk[j >> 1] = pack_bf16x2(__uint_as_float(a[j]) * f0 + __uint_as_float(b[j]) * f1,
                                    __uint_as_float(a[j + 1]) * f0 + __uint_as_float(b[j + 1]) * f1);
         // 64-byte rows, 64B swizzle: unit u of row r at u ^ (r / 2) % 4
-        const uint32_t x = (uint32_t)(lane >> 1) & 3u;
-        st_shared_v4(srow + (((2u * q) ^ x) << 4), pk[0], pk[1], pk[2], pk[3]);
-        st_shared_v4(srow + (((2u * q + 1u) ^ x) << 4), pk[4], pk[5], pk[6], pk[7]);
+        const uint32_t x = (uint32_t)(lane >> 1) & 3u, u = 2u * (q & 1), box = srow + 2048u * (q >> 1);
+        st_shared_v4(box + ((u ^ x) << 4), pk[0], pk[1], pk[2], pk[3]);
+        st_shared_v4(box + (((u + 1u) ^ x) << 4), pk[4], pk[5], pk[6], pk[7]);
       }
-      if (c + 32 == D) {
-        // the accumulators have been read: the next item that uses them may start
+      if (c0 + 32 * C::BOXES == D) {
+        // the accumulators have been read: the next item's PVs may start
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.o_free);
@@ -528,7 +531,8 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && q0 < p.n_tokens) {                // rows past the sequence are dropped by the store
-        tma_store_4d(to, stage, c, it.h, q0, it.s);
+#pragma unroll
+        for (int x = 0; x < C::BOXES; ++x) tma_store_4d(to, stage + 2048 * x, c0 + 32 * x, it.h, q0, it.s);
         bulk_commit_group();
       }
     }
