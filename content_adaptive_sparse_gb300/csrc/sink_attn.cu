@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Handoff hand[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // uniform
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
@@ -606,13 +606,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 8) {
-      if ((threadIdx.x & 31) == 0) loader<D>(p, &tq, &tk, &tv, &tkh, &tvh, bars, sQ, sK, sV, &abort_flag);
+      if (elect_one()) loader<D>(p, &tq, &tk, &tv, &tkh, &tvh, bars, sQ, sK, sV, &abort_flag);
       __syncwarp();
     } else if (warp == 9) {
-      if ((threadIdx.x & 31) == 0) qk_issuer<D>(p, bars, sQ, sK, tmem, &abort_flag);
+      if (elect_one()) qk_issuer<D>(p, bars, sQ, sK, tmem, &abort_flag);
       __syncwarp();
     } else if (warp < 12) {
-      if ((threadIdx.x & 31) == 0) pv_issuer<D>(p, warp - 10, bars, sV, tmem, &abort_flag);
+      if (elect_one()) pv_issuer<D>(p, warp - 10, bars, sV, tmem, &abort_flag);
       __syncwarp();
     } else {
       epilogue<D>(p, &to, bars, hand, sOut, tmem, &abort_flag);
