@@ -9,15 +9,20 @@
 // distributed shared memory, so there is one launch, no workspace and no atomics.
 //   warp 4      lane 0 fills a ring of 64-row stages: 16-row TMA boxes (bf16) or bulk copies of the
 //               contiguous 4-bit rows and scales
-//   warps 0-3   16 rows of every stage each, with their own running maximum and sum:
-//               S = Q K^T and O += P V on mma.sync m16n8k16 (the 16 query rows are one m-tile;
-//               a tcgen05 tile would need 64 or 128 rows of queries, and the tensor work is small
-//               beside the reads)
-// 4-bit keys: the codes (-7 .. 7, exact in bf16) go to the tensor cores as they are, one pair of
-// k-steps per scale group, and the group's sum is multiplied by its scale in fp32. 4-bit values:
-// the scale belongs to the summed-over row, so it multiplies P (in fp32, before P's rounding).
-// The products' order of elements within a row is free, so a lane takes the elements that lie
-// together in the stored words, and Q and O use the same order.
+//   warps 0-3   16 rows of every stage each, with their own running maximum and sum, on mma.sync
+//               m16n8k16 (a tcgen05 tile would need 64 or 128 rows of queries, and the tensor
+//               work is small beside the reads)
+// bf16: S = Q K^T and O += P V with the query heads as the 16 rows.
+// 4 bits: S^T = K Q^T and O^T += V^T P^T with the cache rows (the output elements) as the 16 rows and 8
+// query heads as the columns, NQ times: what counts here is the instructions spent on unpacking and
+// on P, and few heads leave no half-empty tiles this way. Keys: a code n + 8 over the mantissa of 16
+// is the bf16 number 24 + n; the products with Q start from -24 times the sum of Q's elements, which
+// leaves q n, and a scale group's sum is multiplied by its scale in fp32. Values: codes n, exact in
+// bf16; the scale belongs to the summed-over row, so it multiplies P (in fp32, before P's rounding), and
+// P's 8 x 8 blocks are transposed between the two products (movmatrix). The products' order of
+// elements within a row is free, so a lane takes the elements that lie together in the stored
+// words, and Q and O use the same order. The running maximum is followed only when a score exceeds
+// it by 2^8, which one vote shows.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,12 +48,13 @@ __device__ unsigned int g_decode_err;
 constexpr int kWarps = 4;               // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kRows = 16 * kWarps;      // cache rows per stage
-constexpr int kQ = 16;                  // query heads per CTA (one m-tile)
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
 
-template <int D, bool Q4>
+// NQ: groups of 8 query heads of a CTA (2 in the bf16 form: one m-tile)
+template <int D, bool Q4, int NQ>
 struct Cfg {
+  static constexpr int Q = 8 * NQ;                     // query heads
   static constexpr int CH = D >= 64 ? 64 : 32;         // bf16: elements per swizzled row
   static constexpr int ROWB = CH * 2;
   static constexpr CUtensorMapSwizzle TMA_SWZ =
@@ -60,9 +66,10 @@ struct Cfg {
   static constexpr int STAGES = Q4 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : (D == 64 ? 4 : 8));
   static constexpr int RING = STAGES * STAGE;
   // after the last stage the ring's memory holds the warps' partial results
-  static constexpr int MERGE = kWarps * kQ * (D + 2) * 4;
+  static constexpr int MERGE = kWarps * Q * (D + 2) * 4;
   static constexpr int SMEM = 1024 + (RING > MERGE ? RING : MERGE);
-  static constexpr int NT = D / 8;                     // output n-tiles
+  // accumulators of a thread: [D / 8][4], n-tiles of the 16 heads, or [NQ * D / 16][4], m-tiles
+  static constexpr int NT = Q4 ? NQ * D / 16 : D / 8;
   static_assert(STAGES <= kMaxStages && SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -122,10 +129,10 @@ struct Rows {
   }
 };
 
-template <int D, bool Q4>
+template <int D, bool Q4, int NQ>
 __device__ void producer(const DParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Bars& bars, uint8_t* ring,
                          const Rows& r, int s, int hk, volatile int* abort_flag) {
-  using C = Cfg<D, Q4>;
+  using C = Cfg<D, Q4, NQ>;
   int g = 0;
   for (int j = r.begin; j < r.end; ++j, ++g) {
     const int st = g % C::STAGES;
@@ -175,12 +182,33 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r
                : "r"(addr));
 }
 
-// Codes c (nibble s of the low and of the high half-word, 1 .. 15) as the bf16 pair (c - 8): 0x43
-// over a zero exponent-and-mantissa byte is 128 + c, exact in bf16, and so is the difference.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int s) {
-  const uint32_t x = ((w >> (4 * s)) & 0x000f000fu) | 0x43004300u;
+// Codes n + 8 (nibble s of the low and of the high half-word, 1 .. 15) as a bf16 pair: over the
+// mantissa of 16 as 24 + n; over that of 128 as 136 + n and from it n. All exact in bf16.
+template <int S>
+__device__ __forceinline__ uint32_t code_pair_24(uint32_t w) {
+  return ((S == 0 ? w << 3 : w >> (4 * S - 3)) & 0x00780078u) | 0x41804180u;
+}
+template <int S>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  const uint32_t x = ((w >> (4 * S)) & 0x000f000fu) | 0x43004300u;
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// D = A B + C with C of its own.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2], float c0,
+                                              float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements, row lane / 4, columns 2 (lane % 4) and + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 template <int N>
@@ -196,26 +224,172 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   }
 }
 
-// Scales of rows `row` and `row + 1` (row even): sc[e][c], zero for a row outside [lo, hi).
+// A row's scales.
 template <int NG>
-__device__ __forceinline__ void load_scales(uint32_t base, int row, bool on0, bool on1, float (&sc)[2][NG]) {
-  uint32_t w[NG];
-  lds_words<NG>(base + (uint32_t)(row * NG * 2), w);
+__device__ __forceinline__ void load_scales(uint32_t base, int row, float (&sc)[NG]) {
+  uint32_t w[(NG + 1) / 2];
+  if constexpr (NG == 1) {
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w[0]) : "r"(base + (uint32_t)(row * 2)));
+  } else {
+    lds_words<NG / 2>(base + (uint32_t)(row * NG * 2), w);
+  }
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      const int i = e * NG + c;
-      const float v = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-      sc[e][c] = (e ? on1 : on0) ? v : 0.f;
-    }
+  for (int c = 0; c < NG; ++c) sc[c] = __uint_as_float(c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16);
 }
 
-template <int D, bool Q4>
-__device__ void consumer(const DParams& p, Bars& bars, uint8_t* ring, const Rows& r, int s, int h0, int n_q,
-                         float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
-  using C = Cfg<D, Q4>;
-  constexpr int NG = C::NG, KS = D / 16;
+// 4-bit form. m, l: per query head 8 q + 2 t + e of lane (g, t), m the same in all g, l this lane's rows.
+template <int D, int NQ>
+__device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Rows& r, int s, int h0, int n_q,
+                          float (&o)[NQ * D / 16][4], float (&m)[2 * NQ], float (&l)[2 * NQ], volatile int* abort_flag) {
+  using C = Cfg<D, true, NQ>;
+  constexpr int NG = C::NG;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const float kNegInf = __int_as_float(0xff800000);
+  const float c = p.scale_log2;
+  // Q^T as B fragments (absent heads are zero), and -24 times the sums over each scale group
+  uint32_t qb[NQ][2 * NG][2];
+  float start[NQ][NG][2];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const __nv_bfloat16* qr = p.q + (int64_t)s * p.q_sb + (int64_t)(h0 + 8 * q + g) * p.q_sh;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (8 * q + g < n_q) w = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
+      qb[q][2 * i][0] = w.x;
+      qb[q][2 * i][1] = w.y;
+      qb[q][2 * i + 1][0] = w.z;
+      qb[q][2 * i + 1][1] = w.w;
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += __uint_as_float(v[e] << 16) + __uint_as_float(v[e] & 0xffff0000u);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);          // head g
+      start[q][i][0] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t);
+      start[q][i][1] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+    }
+  }
+  const uint32_t ring0 = smem_u32(ring);
+  const uint32_t sel = g & 1 ? 0x7531u : 0x6420u;
+  for (int j = r.begin, n = 0; j < r.end; ++j, ++n) {
+    const int st = n % C::STAGES;
+    int tok, vlo, vhi;
+    r.stage(j, tok, vlo, vhi);
+    if (!__all_sync(0xffffffffu, wait_bar(&bars.full[st], (uint32_t)(n / C::STAGES) & 1u, abort_flag))) return;
+    const int t0 = tok + 16 * warp;
+    if (t0 < vhi && t0 + 16 > vlo) {
+      const uint32_t kb = ring0 + (uint32_t)(st * C::STAGE);
+      const uint32_t vb = kb + C::CODES + C::SCALES;
+      const int row0 = 16 * warp;
+      const bool whole = t0 >= vlo && t0 + 16 <= vhi;
+      // ---- scores of rows g and g + 8
+      uint32_t w0[NG], w1[NG];
+      lds_words<NG>(kb + (uint32_t)((row0 + g) * (D / 2) + t * (D / 8)), w0);
+      lds_words<NG>(kb + (uint32_t)((row0 + 8 + g) * (D / 2) + t * (D / 8)), w1);
+      float k0[NG], k1[NG];
+      load_scales<NG>(kb + C::CODES, row0 + g, k0);
+      load_scales<NG>(kb + C::CODES, row0 + 8 + g, k1);
+      float sc[NQ][4];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const uint32_t a0[4] = {code_pair_24<0>(w0[i]), code_pair_24<0>(w1[i]), code_pair_24<1>(w0[i]), code_pair_24<1>(w1[i])};
+        const uint32_t a1[4] = {code_pair_24<2>(w0[i]), code_pair_24<2>(w1[i]), code_pair_24<3>(w0[i]), code_pair_24<3>(w1[i])};
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          float acc[4];
+          mma16816_from(acc, a0, qb[q][2 * i], start[q][i][0], start[q][i][1]);
+          mma16816(acc, a1, qb[q][2 * i + 1][0], qb[q][2 * i + 1][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float k = e < 2 ? k0[i] : k1[i];
+            sc[q][e] = i == 0 ? acc[e] * k : fmaf(acc[e], k, sc[q][e]);
+          }
+        }
+      }
+      float v0[NG], v1[NG];
+      load_scales<NG>(vb + C::CODES, row0 + g, v0);
+      load_scales<NG>(vb + C::CODES, row0 + 8 + g, v1);
+      if (!whole) {
+        // rows that are not seen: no score, and zeros for whatever their scales hold
+        const bool on0 = t0 + g >= vlo && t0 + g < vhi, on1 = t0 + 8 + g >= vlo && t0 + 8 + g < vhi;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[q][e] = (e < 2 ? on0 : on1) ? sc[q][e] : kNegInf;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          v0[i] = on0 ? v0[i] : 0.f;
+          v1[i] = on1 ? v1[i] : 0.f;
+        }
+      }
+      // ---- the running maximum
+      bool grow = false;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) grow = grow || fmaxf(sc[q][e], sc[q][e + 2]) * c > m[2 * q + e] + 8.f;
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(sc[q][e], sc[q][e + 2]) * c;
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            float a = 1.f;
+            if (mx > m[2 * q + e] + 8.f) {
+              a = ex2_approx(m[2 * q + e] - mx);                 // 0 from -inf
+              m[2 * q + e] = mx;
+            }
+            l[2 * q + e] *= a;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              o[q * (D / 16) + x][e] *= a;
+              o[q * (D / 16) + x][e + 2] *= a;
+            }
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[2 * q + (e & 1)] == kNegInf ? 0.f : m[2 * q + (e & 1)];
+          sc[q][e] = ex2_approx(fmaf(sc[q][e], c, -ref));
+          l[2 * q + (e & 1)] += sc[q][e];
+        }
+      // ---- values: words (g / 2, i) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; byte pair g % 2 of each holds
+      // this lane's elements 32 i + 4 g + {0, 2, 1, 3} (nibbles 0 .. 3 after the byte selection)
+      uint32_t w[4][NG];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        lds_words<NG>(vb + (uint32_t)((row0 + 2 * t + (k & 1) + 8 * (k >> 1)) * (D / 2) + (g >> 1) * (D / 8)), w[k]);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const uint32_t x0 = __byte_perm(w[0][i], w[1][i], sel), x1 = __byte_perm(w[2][i], w[3][i], sel);
+        const uint32_t a0[4] = {code_pair<0>(x0), code_pair<1>(x0), code_pair<0>(x1), code_pair<1>(x1)};
+        const uint32_t a1[4] = {code_pair<2>(x0), code_pair<3>(x0), code_pair<2>(x1), code_pair<3>(x1)};
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const uint32_t b0 = transpose8(pack_bf16x2(sc[q][0] * v0[i], sc[q][1] * v0[i]));
+          const uint32_t b1 = transpose8(pack_bf16x2(sc[q][2] * v1[i], sc[q][3] * v1[i]));
+          mma16816(o[q * (D / 16) + 2 * i], a0, b0, b1);
+          mma16816(o[q * (D / 16) + 2 * i + 1], a1, b0, b1);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.empty[st]);
+  }
+}
+
+// bf16 form. m, l: per query head g + 8 h of lane (g, t), l this lane's columns.
+template <int D>
+__device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Rows& r, int s, int h0, int n_q,
+                           float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
+  using C = Cfg<D, false, 2>;
+  constexpr int KS = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const float kNegInf = __int_as_float(0xff800000);
@@ -227,23 +401,10 @@ __device__ void consumer(const DParams& p, Bars& bars, uint8_t* ring, const Rows
     const int row = g + 8 * half;
     const __nv_bfloat16* qr = p.q + (int64_t)s * p.q_sb + (int64_t)(h0 + row) * p.q_sh;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      if constexpr (Q4) {
-        // elements 32 i + 8 t .. + 7: the pairs of code word (t, i)
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (row < n_q) w = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
-        qa[2 * i][half] = w.x;
-        qa[2 * i][half + 2] = w.y;
-        qa[2 * i + 1][half] = w.z;
-        qa[2 * i + 1][half + 2] = w.w;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const __nv_bfloat16* at = qr + 32 * i + 16 * k + 2 * t;
-          qa[2 * i + k][half] = row < n_q ? *reinterpret_cast<const uint32_t*>(at) : 0u;
-          qa[2 * i + k][half + 2] = row < n_q ? *reinterpret_cast<const uint32_t*>(at + 8) : 0u;
-        }
-      }
+    for (int k = 0; k < KS; ++k) {
+      const __nv_bfloat16* at = qr + 16 * k + 2 * t;
+      qa[k][half] = row < n_q ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+      qa[k][half + 2] = row < n_q ? *reinterpret_cast<const uint32_t*>(at + 8) : 0u;
     }
   }
   const uint32_t ring0 = smem_u32(ring);
@@ -271,23 +432,7 @@ __device__ void consumer(const DParams& p, Bars& bars, uint8_t* ring, const Rows
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-      if constexpr (Q4) {
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          uint32_t w[NG];
-          lds_words<NG>(kb + (uint32_t)((row0 + 8 * nt + g) * (D / 2) + t * (D / 8)), w);
-          float ksc[2][NG];
-          load_scales<NG>(kb + C::CODES, row0 + 8 * nt + 2 * t, true, true, ksc);
-#pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(acc, qa[2 * i], code_pair(w[i], 0), code_pair(w[i], 1));
-            mma16816(acc, qa[2 * i + 1], code_pair(w[i], 2), code_pair(w[i], 3));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = fmaf(acc[e], ksc[e & 1][i], sc[nt][e]);
-          }
-        }
-      } else {
+      {
         const int mi = lane >> 3;
         const int row = row0 + (lane & 7) + ((mi >> 1) << 3);
 #pragma unroll
@@ -335,29 +480,7 @@ __device__ void consumer(const DParams& p, Bars& bars, uint8_t* ring, const Rows
           sc[nt][e] = ex2_approx(sc[nt][e] - ref[e >> 1]);
           l[e >> 1] += sc[nt][e];
         }
-      if constexpr (Q4) {
-        float vsc[2][2][NG];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-          load_scales<NG>(vb + C::CODES, row0 + 8 * nt + 2 * t, on[nt][0], on[nt][1], vsc[nt]);
-        // words (g / 2, c) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; byte pair g % 2 of each holds
-        // this lane's elements 32 c + 4 g + {0, 2, 1, 3} (nibbles 0 .. 3 after the byte selection)
-        uint32_t w[4][NG];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          lds_words<NG>(vb + (uint32_t)((row0 + 2 * t + (k & 1) + 8 * (k >> 1)) * (D / 2) + (g >> 1) * (D / 8)), w[k]);
-        const uint32_t sel = g & 1 ? 0x7531u : 0x6420u;
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          const uint32_t pa[4] = {pack_bf16x2(sc[0][0] * vsc[0][0][i], sc[0][1] * vsc[0][1][i]),
-                                  pack_bf16x2(sc[0][2] * vsc[0][0][i], sc[0][3] * vsc[0][1][i]),
-                                  pack_bf16x2(sc[1][0] * vsc[1][0][i], sc[1][1] * vsc[1][1][i]),
-                                  pack_bf16x2(sc[1][2] * vsc[1][0][i], sc[1][3] * vsc[1][1][i])};
-          const uint32_t x0 = __byte_perm(w[0][i], w[1][i], sel), x1 = __byte_perm(w[2][i], w[3][i], sel);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma16816(o[4 * i + k], pa, code_pair(x0, k), code_pair(x1, k));
-        }
-      } else {
+      {
         const uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
                                 pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
         const int mi = lane >> 3;
@@ -386,11 +509,11 @@ __device__ void consumer(const DParams& p, Bars& bars, uint8_t* ring, const Rows
   }
 }
 
-template <int D, bool Q4>
+template <int D, bool Q4, int NQ>
 __global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv,
                                                                const __grid_constant__ DParams p) {
-  using C = Cfg<D, Q4>;
+  using C = Cfg<D, Q4, NQ>;
   namespace cg = cooperative_groups;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -399,6 +522,7 @@ __global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_cons
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = blockIdx.x, ranks = gridDim.x;          // the cluster spans the grid's x
   const int s = blockIdx.z, hk = blockIdx.y / p.head_groups, hg = blockIdx.y % p.head_groups;
+  constexpr int kQ = C::Q;
   const int h0 = hk * p.group + hg * kQ;
   const int n_q = min(kQ, p.group - hg * kQ);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -414,16 +538,23 @@ __global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_cons
   __syncthreads();
   const Rows r = Rows::of<Q4>(p, s, rank, ranks);
   float o[C::NT][4];
-  float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+  constexpr int NM = Q4 ? 2 * NQ : 2;                       // query heads of a lane
+  float m[NM], l[NM];
+#pragma unroll
+  for (int i = 0; i < NM; ++i) {
+    m[i] = kNegInf;
+    l[i] = 0.f;
+  }
 #pragma unroll
   for (int i = 0; i < C::NT; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
   if (warp == kWarps) {
-    if (lane == 0) producer<D, Q4>(p, &tk, &tv, bars, ring, r, s, hk, &abort_flag);
+    if (lane == 0) producer<D, Q4, NQ>(p, &tk, &tv, bars, ring, r, s, hk, &abort_flag);
     __syncwarp();
   } else {
-    consumer<D, Q4>(p, bars, ring, r, s, h0, n_q, o, m, l, &abort_flag);
+    if constexpr (Q4) consumer4<D, NQ>(p, bars, ring, r, s, h0, n_q, o, m, l, &abort_flag);
+    else consumer16<D>(p, bars, ring, r, s, h0, n_q, o, m, l, &abort_flag);
   }
   __syncthreads();                                          // the ring is free
   // ---- the warps' partial results: O [warp][query][D], maxima and sums
@@ -433,25 +564,28 @@ __global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_cons
   if (warp < kWarps) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const int row = g + 8 * h;
+    for (int h = 0; h < NM; ++h) {
+      // the sums over the lanes that share the head; one of them writes
+#pragma unroll
+      for (int x = Q4 ? 4 : 1; x < (Q4 ? 32 : 4); x *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+      const int row = Q4 ? 8 * (h >> 1) + 2 * t + (h & 1) : g + 8 * h;
       if (row < n_q) {
-        if (t == 0) {
+        if ((Q4 ? g : t) == 0) {
           wm[warp * kQ + row] = m[h];
           wl[warp * kQ + row] = l[h];
         }
         float* dst = wo + (warp * kQ + row) * D;
+        if constexpr (Q4) {
+          // rows g and g + 8 of m-tile x: elements 32 (x / 2) + 4 g + {0, 2} or {1, 3}
 #pragma unroll
-        for (int i = 0; i < C::NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // column 2 t + e of n-tile i; 4-bit: element 32 (i / 4) + 4 (2 t + e) + {0, 2, 1, 3}[i % 4]
-            const int k = i & 3;
-            const int at = Q4 ? 32 * (i >> 2) + 4 * (2 * t + e) + (k == 1 ? 2 : (k == 2 ? 1 : k)) : 8 * i + 2 * t + e;
-            dst[at] = o[i][2 * h + e];
+          for (int x = 0; x < D / 16; ++x) {
+            dst[32 * (x >> 1) + 4 * g + (x & 1)] = o[(h >> 1) * (D / 16) + x][h & 1];
+            dst[32 * (x >> 1) + 4 * g + 2 + (x & 1)] = o[(h >> 1) * (D / 16) + x][2 + (h & 1)];
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < C::NT; ++i) *reinterpret_cast<float2*>(dst + 8 * i + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        }
       }
     }
   }
@@ -506,9 +640,9 @@ __global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_cons
   cluster.sync();                                           // no CTA leaves while another reads its results
 }
 
-template <int D, bool Q4>
+template <int D, bool Q4, int NQ>
 int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, Q4>;
+  using C = Cfg<D, Q4, NQ>;
   CUtensorMap tk, tv;
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));
@@ -537,12 +671,12 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   p.heads = a.heads;
   p.kv_heads = a.kv_heads;
   p.group = a.heads / a.kv_heads;
-  p.head_groups = (p.group + kQ - 1) / kQ;
+  p.head_groups = (p.group + C::Q - 1) / C::Q;
   p.capacity = a.capacity;
   p.window = a.window;
   p.sinks = a.sinks;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
-  const auto kern = sink_decode_kernel<D, Q4>;
+  const auto kern = sink_decode_kernel<D, Q4, NQ>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
   // CTAs per (sequence, key head): enough for two per SM, while each has two stages of rows or
@@ -571,11 +705,17 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+template <int D>
+int launch_d(const SinkDecodeArgs& a, cudaStream_t stream) {
+  if (!a.cache4) return launch<D, false, 2>(a, stream);
+  return a.heads / a.kv_heads > 8 ? launch<D, true, 2>(a, stream) : launch<D, true, 1>(a, stream);
+}
+
 int launch_sink_decode(const SinkDecodeArgs& a, cudaStream_t stream) {
   switch (a.head_dim) {
-    case 32: return a.cache4 ? launch<32, true>(a, stream) : launch<32, false>(a, stream);
-    case 64: return a.cache4 ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
-    case 128: return a.cache4 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+    case 32: return launch_d<32>(a, stream);
+    case 64: return launch_d<64>(a, stream);
+    case 128: return launch_d<128>(a, stream);
   }
   return SA_ERR_UNSUPPORTED;
 }
