@@ -510,7 +510,7 @@ __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Ro
 }
 
 template <int D, bool Q4, int NQ>
-__global__ void __launch_bounds__(kThreads) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
+__global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv,
                                                                const __grid_constant__ DParams p) {
   using C = Cfg<D, Q4, NQ>;
@@ -679,13 +679,15 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   const auto kern = sink_decode_kernel<D, Q4, NQ>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
-  // CTAs per (sequence, key head): enough for two per SM, while each has two stages of rows or
-  // more when the cache is full
+  // CTAs per (sequence, key head), while each has a stage of rows when the cache is full: bf16 until
+  // there are 1.5 per SM (its loads then saturate the memory; 64 sequences of 4 key heads: 73.8 us
+  // with one, 79.6 with two, 88 with four), 4 bits, bound by its instructions, until there are 6 (32
+  // sequences of 4 key heads: 120 us with three, 116 with four, 107 with eight).
   const int64_t base = (int64_t)a.batch * a.kv_heads * p.head_groups;
   const int64_t seen = (int64_t)a.window + 1 + a.sinks < a.capacity ? (int64_t)a.window + 1 + a.sinks : a.capacity;
   const int sm_count = current_sm_count();
   int ranks = 1;
-  while (ranks < kMaxCluster && base * ranks < 2 * sm_count && seen >= 4 * kRows * ranks) ranks *= 2;
+  while (ranks < kMaxCluster && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * kRows * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)ranks, (unsigned)(a.kv_heads * p.head_groups), (unsigned)a.batch);
