@@ -15,10 +15,9 @@
 // bf16: S = Q K^T and O += P V with the query heads as the 16 rows.
 // 4 bits: S^T = K Q^T and O^T += V^T P^T with the cache rows (the output elements) as the 16 rows and 8
 // query heads as the columns, NQ times: what counts here is the instructions spent on unpacking and
-// on P, and few heads leave no half-empty tiles this way. Keys: a code n + 8 over the mantissa of 16
-// is the bf16 number 24 + n; the products with Q start from -24 times the sum of Q's elements, which
-// leaves q n, and a scale group's sum is multiplied by its scale in fp32. Values: codes n, exact in
-// bf16; the scale belongs to the summed-over row, so it multiplies P (in fp32, before P's rounding), and
+// on P, and few heads leave no half-empty tiles this way. Keys: codes n, exact in f16, with Q in f16
+// scaled by a power of two; a scale group's sum is multiplied by its scale in fp32. Values: codes n,
+// exact in bf16 (P needs its range); the scale belongs to the summed-over row, so it multiplies P (in fp32, before P's rounding), and
 // P's 8 x 8 blocks are transposed between the two products (movmatrix). The products' order of
 // elements within a row is free, so a lane takes the elements that lie together in the stored
 // words, and Q and O use the same order. The running maximum is followed only when a score exceeds
@@ -26,6 +25,7 @@
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -47,7 +47,6 @@ __device__ unsigned int g_decode_err;
 
 constexpr int kWarps = 4;               // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kRows = 16 * kWarps;      // cache rows per stage
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
 
@@ -55,15 +54,17 @@ constexpr int kMaxCluster = 8;
 template <int D, bool Q4, int NQ>
 struct Cfg {
   static constexpr int Q = 8 * NQ;                     // query heads
+  static constexpr int TILES = Q4 ? 2 : 1;             // 16-row tiles of a consumer warp per stage
+  static constexpr int ROWS = 16 * kWarps * TILES;     // cache rows per stage
   static constexpr int CH = D >= 64 ? 64 : 32;         // bf16: elements per swizzled row
   static constexpr int ROWB = CH * 2;
   static constexpr CUtensorMapSwizzle TMA_SWZ =
       ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   static constexpr int NG = D / 32;                    // scale groups
-  static constexpr int CODES = Q4 ? kRows * D / 2 : kRows * D * 2;   // K (or V) bytes of a stage
-  static constexpr int SCALES = Q4 ? kRows * NG * 2 : 0;
+  static constexpr int CODES = Q4 ? ROWS * D / 2 : ROWS * D * 2;   // K (or V) bytes of a stage
+  static constexpr int SCALES = Q4 ? ROWS * NG * 2 : 0;
   static constexpr int STAGE = 2 * (CODES + SCALES);
-  static constexpr int STAGES = Q4 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : (D == 64 ? 4 : 8));
+  static constexpr int STAGES = Q4 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : (D == 64 ? 4 : 8));
   static constexpr int RING = STAGES * STAGE;
   // after the last stage the ring's memory holds the warps' partial results
   static constexpr int MERGE = kWarps * Q * (D + 2) * 4;
@@ -95,21 +96,21 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   return mbar_wait(bar, parity, abort_flag, &g_decode_err, kErrTimeout);
 }
 
-// The rows that a sequence's query sees, cut into stages of 64: first those of the sinks that the
+// The rows that a sequence's query sees, cut into stages of R: first those of the sinks that the
 // window does not hold, then the window's, this CTA's share being [begin, end).
+template <int R, bool Q4>
 struct Rows {
   int len, lo, n_sink;              // tokens; first token of the window; sinks before it
   int sink_stages, first, begin, end;   // first: token of the window's first stage row
 
-  template <bool Q4>
   __device__ static Rows of(const DParams& p, int s, int rank, int ranks) {
     Rows r;
     r.len = max(0, min(p.lengths[s], p.capacity));
     r.lo = max(0, r.len - 1 - p.window);
     r.n_sink = min(p.sinks, r.lo);
     r.first = Q4 ? (r.lo & ~7) : r.lo;          // bulk copies start at a multiple of 16 bytes
-    r.sink_stages = (r.n_sink + kRows - 1) / kRows;
-    const int total = r.sink_stages + (r.len - r.first + kRows - 1) / kRows;
+    r.sink_stages = (r.n_sink + R - 1) / R;
+    const int total = r.sink_stages + (r.len - r.first + R - 1) / R;
     const int per = (total + ranks - 1) / ranks;
     r.begin = min(total, rank * per);
     r.end = min(total, r.begin + per);
@@ -118,11 +119,11 @@ struct Rows {
   // stage j: its first row's token, and the tokens [lo, hi) of it that are seen
   __device__ __forceinline__ void stage(int j, int& tok, int& vlo, int& vhi) const {
     if (j < sink_stages) {
-      tok = j * kRows;
+      tok = j * R;
       vlo = 0;
       vhi = n_sink;
     } else {
-      tok = first + (j - sink_stages) * kRows;
+      tok = first + (j - sink_stages) * R;
       vlo = lo;
       vhi = len;
     }
@@ -131,7 +132,7 @@ struct Rows {
 
 template <int D, bool Q4, int NQ>
 __device__ void producer(const DParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Bars& bars, uint8_t* ring,
-                         const Rows& r, int s, int hk, volatile int* abort_flag) {
+                         const Rows<Cfg<D, Q4, NQ>::ROWS, Q4>& r, int s, int hk, volatile int* abort_flag) {
   using C = Cfg<D, Q4, NQ>;
   int g = 0;
   for (int j = r.begin; j < r.end; ++j, ++g) {
@@ -141,7 +142,7 @@ __device__ void producer(const DParams& p, const CUtensorMap* tk, const CUtensor
     r.stage(j, tok, vlo, vhi);
     uint8_t* stage = ring + st * C::STAGE;
     if constexpr (Q4) {
-      const int rows = min(kRows, (vhi - tok + 7) & ~7);          // the capacity is a multiple of 8
+      const int rows = min(C::ROWS, (vhi - tok + 7) & ~7);          // the capacity is a multiple of 8
       const int64_t row = ((int64_t)s * p.kv_heads + hk) * p.capacity + tok;
       mbar_arrive_expect_tx(&bars.full[st], (uint32_t)(rows * (D + 4 * C::NG)));
       bulk_load(stage, p.kc + row * (D / 2), rows * (D / 2), &bars.full[st]);
@@ -154,7 +155,7 @@ __device__ void producer(const DParams& p, const CUtensorMap* tk, const CUtensor
       for (int b = 0; b < boxes; ++b)
 #pragma unroll
         for (int c = 0; c < D / C::CH; ++c) {
-          uint8_t* dst = stage + (c * kRows + 16 * b) * C::ROWB;
+          uint8_t* dst = stage + (c * C::ROWS + 16 * b) * C::ROWB;
           tma_load_4d(dst, tk, &bars.full[st], c * C::CH, hk, tok + 16 * b, s);
           tma_load_4d(dst + C::CODES, tv, &bars.full[st], c * C::CH, hk, tok + 16 * b, s);
         }
@@ -172,7 +173,7 @@ __device__ __forceinline__ uint32_t row_unit(uint32_t base, int row, int u) {
   if constexpr (D == 32) {
     return base + (uint32_t)(row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
   } else {
-    return swz(base + (uint32_t)((u >> 3) * kRows * 128), row, u & 7);
+    return swz(base + (uint32_t)((u >> 3) * Cfg<D, false, 2>::ROWS * 128), row, u & 7);
   }
 }
 
@@ -182,12 +183,8 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r
                : "r"(addr));
 }
 
-// Codes n + 8 (nibble s of the low and of the high half-word, 1 .. 15) as a bf16 pair: over the
-// mantissa of 16 as 24 + n; over that of 128 as 136 + n and from it n. All exact in bf16.
-template <int S>
-__device__ __forceinline__ uint32_t code_pair_24(uint32_t w) {
-  return ((S == 0 ? w << 3 : w >> (4 * S - 3)) & 0x00780078u) | 0x41804180u;
-}
+// Codes n + 8 (nibble S of the low and of the high half-word, 1 .. 15) as a bf16 pair of n: over
+// the mantissa of 128 they are 136 + n. All exact.
 template <int S>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   const uint32_t x = ((w >> (4 * S)) & 0x000f000fu) | 0x43004300u;
@@ -195,13 +192,36 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// D = A B + C with C of its own.
-__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2], float c0,
-                                              float c1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1));
+// The four pairs of a code word as f16 pairs of n: its ten bits of mantissa take two of the four
+// nibbles where they stand, as 1032 + n and 1024 + 16 (n + 8), which one fma turns into n. All exact.
+__device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[4]) {
+  const __half2 one = __floats2half2_rn(-1032.f, -1032.f), off = __floats2half2_rn(-72.f, -72.f);
+  const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t x = ((k ? w >> 8 : w) & 0x000f000fu) | 0x64006400u, y = ((k ? w >> 8 : w) & 0x00f000f0u) | 0x64006400u;
+    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&x), one);
+    const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&y), sixteenth, off);
+    h[2 * k] = *reinterpret_cast<const uint32_t*>(&a);
+    h[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+
+// D += A B in f16 with fp32 sums; FIRST: D = A B.
+template <bool FIRST>
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             const uint32_t (&b)[2]) {
+  if constexpr (FIRST) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(0.f));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+  }
 }
 
 // Transpose of an 8 x 8 matrix of 16-bit elements, row lane / 4, columns 2 (lane % 4) and + 1.
@@ -226,12 +246,12 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 
 // A row's scales.
 template <int NG>
-__device__ __forceinline__ void load_scales(uint32_t base, int row, float (&sc)[NG]) {
+__device__ __forceinline__ void load_scales(uint32_t addr, float (&sc)[NG]) {
   uint32_t w[(NG + 1) / 2];
   if constexpr (NG == 1) {
-    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w[0]) : "r"(base + (uint32_t)(row * 2)));
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w[0]) : "r"(addr));
   } else {
-    lds_words<NG / 2>(base + (uint32_t)(row * NG * 2), w);
+    lds_words<NG / 2>(addr, w);
   }
 #pragma unroll
   for (int c = 0; c < NG; ++c) sc[c] = __uint_as_float(c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16);
@@ -239,68 +259,86 @@ __device__ __forceinline__ void load_scales(uint32_t base, int row, float (&sc)[
 
 // 4-bit form. m, l: per query head 8 q + 2 t + e of lane (g, t), m the same in all g, l this lane's rows.
 template <int D, int NQ>
-__device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Rows& r, int s, int h0, int n_q,
-                          float (&o)[NQ * D / 16][4], float (&m)[2 * NQ], float (&l)[2 * NQ], volatile int* abort_flag) {
+__device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Rows<Cfg<D, true, NQ>::ROWS, true>& r, int s,
+                          int h0, int n_q, float (&o)[NQ * D / 16][4], float (&m)[2 * NQ], float (&l)[2 * NQ],
+                          volatile int* abort_flag) {
   using C = Cfg<D, true, NQ>;
   constexpr int NG = C::NG;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const float kNegInf = __int_as_float(0xff800000);
-  const float c = p.scale_log2;
-  // Q^T as B fragments (absent heads are zero), and -24 times the sums over each scale group
+  // Q^T as f16 B fragments (absent heads are zero). A head's elements are first taken times the power of
+  // two that brings the largest to [2^9, 2^10): bf16's 8 bits fit f16's 11, and what falls below
+  // f16's last place is 2^-34 of the largest. The power comes back with the softmax scale.
   uint32_t qb[NQ][2 * NG][2];
-  float start[NQ][NG][2];
+  float c[2 * NQ], thr[2 * NQ];      // softmax scale of the lane's heads; score beyond which m follows
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const __nv_bfloat16* qr = p.q + (int64_t)s * p.q_sb + (int64_t)(h0 + 8 * q + g) * p.q_sh;
+    uint4 w[NG];
+    uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (8 * q + g < n_q) w = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
-      qb[q][2 * i][0] = w.x;
-      qb[q][2 * i][1] = w.y;
-      qb[q][2 * i + 1][0] = w.z;
-      qb[q][2 * i + 1][1] = w.w;
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum += __uint_as_float(v[e] << 16) + __uint_as_float(v[e] & 0xffff0000u);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);          // head g
-      start[q][i][0] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t);
-      start[q][i][1] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (8 * q + g < n_q) w[i] = *reinterpret_cast<const uint4*>(qr + 32 * i + 8 * t);
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & kAbs, w[i].y & kAbs), __vmaxu2(w[i].z & kAbs, w[i].w & kAbs)));
     }
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));           // head g
+    // exponent field of the largest magnitude (at least that of 2^-90, so that the powers are numbers)
+    const int e = max((int)(max(top & 0xffffu, top >> 16) >> 7), 37);
+    const float up = __int_as_float((127 + 9 + 127 - e) << 23), back = __int_as_float((e - 9) << 23);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
+        qb[q][2 * i + (k >> 1)][k & 1] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    c[2 * q] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
+    c[2 * q + 1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    thr[2 * q] = thr[2 * q + 1] = kNegInf;
   }
+  // this lane's places in a stage: key words, scales of rows g, value words
   const uint32_t ring0 = smem_u32(ring);
+  const uint32_t at_k = (uint32_t)((16 * C::TILES * warp + g) * (D / 2) + t * (D / 8));
+  const uint32_t at_s = (uint32_t)(C::CODES + (16 * C::TILES * warp + g) * NG * 2);
+  const uint32_t at_v = (uint32_t)(C::CODES + C::SCALES + (16 * C::TILES * warp + 2 * t) * (D / 2) + (g >> 1) * (D / 8));
   const uint32_t sel = g & 1 ? 0x7531u : 0x6420u;
   for (int j = r.begin, n = 0; j < r.end; ++j, ++n) {
     const int st = n % C::STAGES;
     int tok, vlo, vhi;
     r.stage(j, tok, vlo, vhi);
     if (!__all_sync(0xffffffffu, wait_bar(&bars.full[st], (uint32_t)(n / C::STAGES) & 1u, abort_flag))) return;
-    const int t0 = tok + 16 * warp;
-    if (t0 < vhi && t0 + 16 > vlo) {
-      const uint32_t kb = ring0 + (uint32_t)(st * C::STAGE);
-      const uint32_t vb = kb + C::CODES + C::SCALES;
-      const int row0 = 16 * warp;
-      const bool whole = t0 >= vlo && t0 + 16 <= vhi;
+    const uint32_t stage = ring0 + (uint32_t)(st * C::STAGE);
+#pragma unroll 1
+    for (int x = 0; x < C::TILES; ++x) {
+      const int t0 = tok + 16 * (C::TILES * warp + x);
+      if (t0 >= vhi || t0 + 16 <= vlo) continue;
+      const uint32_t kb = stage + at_k + (uint32_t)(x * 16 * (D / 2));
+      const uint32_t sb = stage + at_s + (uint32_t)(x * 16 * NG * 2);
+      const uint32_t vb = stage + at_v + (uint32_t)(x * 16 * (D / 2));
       // ---- scores of rows g and g + 8
       uint32_t w0[NG], w1[NG];
-      lds_words<NG>(kb + (uint32_t)((row0 + g) * (D / 2) + t * (D / 8)), w0);
-      lds_words<NG>(kb + (uint32_t)((row0 + 8 + g) * (D / 2) + t * (D / 8)), w1);
+      lds_words<NG>(kb, w0);
+      lds_words<NG>(kb + 8 * (D / 2), w1);
       float k0[NG], k1[NG];
-      load_scales<NG>(kb + C::CODES, row0 + g, k0);
-      load_scales<NG>(kb + C::CODES, row0 + 8 + g, k1);
+      load_scales<NG>(sb, k0);
+      load_scales<NG>(sb + 16 * NG, k1);
       float sc[NQ][4];
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        const uint32_t a0[4] = {code_pair_24<0>(w0[i]), code_pair_24<0>(w1[i]), code_pair_24<1>(w0[i]), code_pair_24<1>(w1[i])};
-        const uint32_t a1[4] = {code_pair_24<2>(w0[i]), code_pair_24<2>(w1[i]), code_pair_24<3>(w0[i]), code_pair_24<3>(w1[i])};
+        uint32_t a[4], b[4];
+        code_halves(w0[i], a);
+        code_halves(w1[i], b);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           float acc[4];
-          mma16816_from(acc, a0, qb[q][2 * i], start[q][i][0], start[q][i][1]);
-          mma16816(acc, a1, qb[q][2 * i + 1][0], qb[q][2 * i + 1][1]);
+          mma16816_f16<true>(acc, a[0], b[0], a[1], b[1], qb[q][2 * i]);
+          mma16816_f16<false>(acc, a[2], b[2], a[3], b[3], qb[q][2 * i + 1]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float k = e < 2 ? k0[i] : k1[i];
@@ -309,9 +347,9 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
         }
       }
       float v0[NG], v1[NG];
-      load_scales<NG>(vb + C::CODES, row0 + g, v0);
-      load_scales<NG>(vb + C::CODES, row0 + 8 + g, v1);
-      if (!whole) {
+      load_scales<NG>(sb + C::CODES + C::SCALES, v0);
+      load_scales<NG>(sb + C::CODES + C::SCALES + 16 * NG, v1);
+      if (t0 < vlo || t0 + 16 > vhi) {
         // rows that are not seen: no score, and zeros for whatever their scales hold
         const bool on0 = t0 + g >= vlo && t0 + g < vhi, on1 = t0 + 8 + g >= vlo && t0 + 8 + g < vhi;
 #pragma unroll
@@ -324,30 +362,31 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
           v1[i] = on1 ? v1[i] : 0.f;
         }
       }
-      // ---- the running maximum
+      // ---- the running maximum: a tile has a row that is seen, so m is a number afterwards
       bool grow = false;
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) grow = grow || fmaxf(sc[q][e], sc[q][e + 2]) * c > m[2 * q + e] + 8.f;
+        for (int e = 0; e < 4; ++e) grow = grow || sc[q][e] > thr[2 * q + (e & 1)];
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(sc[q][e], sc[q][e + 2]) * c;
+            const int h = 2 * q + e;
+            float mx = fmaxf(sc[q][e], sc[q][e + 2]);
 #pragma unroll
-            for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-            float a = 1.f;
-            if (mx > m[2 * q + e] + 8.f) {
-              a = ex2_approx(m[2 * q + e] - mx);                 // 0 from -inf
-              m[2 * q + e] = mx;
-            }
-            l[2 * q + e] *= a;
+            for (int y = 4; y < 32; y *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+            if (mx > thr[h]) {
+              const float a = ex2_approx(m[h] - mx * c[h]);           // 0 from -inf
+              m[h] = mx * c[h];
+              thr[h] = mx + 8.f / c[h];
+              l[h] *= a;
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              o[q * (D / 16) + x][e] *= a;
-              o[q * (D / 16) + x][e + 2] *= a;
+              for (int y = 0; y < D / 16; ++y) {
+                o[q * (D / 16) + y][e] *= a;
+                o[q * (D / 16) + y][e + 2] *= a;
+              }
             }
           }
       }
@@ -355,16 +394,14 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float ref = m[2 * q + (e & 1)] == kNegInf ? 0.f : m[2 * q + (e & 1)];
-          sc[q][e] = ex2_approx(fmaf(sc[q][e], c, -ref));
+          sc[q][e] = ex2_approx(fmaf(sc[q][e], c[2 * q + (e & 1)], -m[2 * q + (e & 1)]));
           l[2 * q + (e & 1)] += sc[q][e];
         }
       // ---- values: words (g / 2, i) of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; byte pair g % 2 of each holds
       // this lane's elements 32 i + 4 g + {0, 2, 1, 3} (nibbles 0 .. 3 after the byte selection)
       uint32_t w[4][NG];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        lds_words<NG>(vb + (uint32_t)((row0 + 2 * t + (k & 1) + 8 * (k >> 1)) * (D / 2) + (g >> 1) * (D / 8)), w[k]);
+      for (int k = 0; k < 4; ++k) lds_words<NG>(vb + (uint32_t)(((k & 1) + 8 * (k >> 1)) * (D / 2)), w[k]);
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         const uint32_t x0 = __byte_perm(w[0][i], w[1][i], sel), x1 = __byte_perm(w[2][i], w[3][i], sel);
@@ -386,7 +423,7 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
 
 // bf16 form. m, l: per query head g + 8 h of lane (g, t), l this lane's columns.
 template <int D>
-__device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Rows& r, int s, int h0, int n_q,
+__device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Rows<64, false>& r, int s, int h0, int n_q,
                            float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
   using C = Cfg<D, false, 2>;
   constexpr int KS = D / 16;
@@ -536,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     fence_mbar_init();
   }
   __syncthreads();
-  const Rows r = Rows::of<Q4>(p, s, rank, ranks);
+  const auto r = Rows<C::ROWS, Q4>::of(p, s, rank, ranks);
   float o[C::NT][4];
   constexpr int NM = Q4 ? 2 * NQ : 2;                       // query heads of a lane
   float m[NM], l[NM];
@@ -687,7 +724,7 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   const int64_t seen = (int64_t)a.window + 1 + a.sinks < a.capacity ? (int64_t)a.window + 1 + a.sinks : a.capacity;
   const int sm_count = current_sm_count();
   int ranks = 1;
-  while (ranks < kMaxCluster && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * kRows * ranks) ranks *= 2;
+  while (ranks < kMaxCluster && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * 64 * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)ranks, (unsigned)(a.kv_heads * p.head_groups), (unsigned)a.batch);
