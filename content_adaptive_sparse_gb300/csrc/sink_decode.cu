@@ -66,8 +66,8 @@ struct Cfg {
   static constexpr int STAGE = 2 * (CODES + SCALES);
   static constexpr int STAGES = Q4 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : (D == 64 ? 4 : 8));
   static constexpr int RING = STAGES * STAGE;
-  // after the last stage the ring's memory holds the warps' partial results
-  static constexpr int MERGE = kWarps * Q * (D + 2) * 4;
+  // after the last stage the ring's memory holds the warps' partial results and the CTA's statistics
+  static constexpr int MERGE = (kWarps * (D + 2) + 2) * Q * 4;
   static constexpr int SMEM = 1024 + (RING > MERGE ? RING : MERGE);
   // accumulators of a thread: [D / 8][4], n-tiles of the 16 heads, or [NQ * D / 16][4], m-tiles
   static constexpr int NT = Q4 ? NQ * D / 16 : D / 8;
@@ -630,45 +630,65 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     }
   }
   __syncthreads();
-  // ---- one partial result per CTA, in warp 0's place
-  for (int at = threadIdx.x; at < n_q * D; at += kThreads) {
-    const int row = at / D, col = at % D;
-    float M = kNegInf;
+  // ---- one partial result per CTA: O in warp 0's place, its maxima and sums behind the warps'
+  float* cm = wl + kWarps * kQ;
+  float* cl = cm + kQ;
+  for (int at = threadIdx.x; at < n_q * (D / 4); at += kThreads) {
+    const int row = at / (D / 4), col = 4 * (at % (D / 4));
+    float a[kWarps], M = kNegInf, L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * kQ + row]);
-    float sum = 0.f;
-    if (M != kNegInf) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += wo[(w * kQ + row) * D + col] * ex2_approx(wm[w * kQ + row] - M);
+    for (int w = 0; w < kWarps; ++w) {
+      a[w] = wm[w * kQ + row];
+      M = fmaxf(M, a[w]);
     }
-    wo[row * D + col] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x < n_q) {
-    const int row = threadIdx.x;
-    float M = kNegInf, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * kQ + row]);
-    if (M != kNegInf)
-      for (int w = 0; w < kWarps; ++w) L += wl[w * kQ + row] * ex2_approx(wm[w * kQ + row] - M);
-    wm[row] = M;
-    wl[row] = L;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      a[w] = M != kNegInf ? ex2_approx(a[w] - M) : 0.f;
+      const float4 v = *reinterpret_cast<const float4*>(wo + (w * kQ + row) * D + col);
+      sum.x = fmaf(a[w], v.x, sum.x);
+      sum.y = fmaf(a[w], v.y, sum.y);
+      sum.z = fmaf(a[w], v.z, sum.z);
+      sum.w = fmaf(a[w], v.w, sum.w);
+      L = fmaf(a[w], wl[w * kQ + row], L);
+    }
+    *reinterpret_cast<float4*>(wo + row * D + col) = sum;
+    if (col == 0) {
+      cm[row] = M;
+      cl[row] = L;
+    }
   }
   cluster.sync();
-  // ---- the cluster's CTAs join their results: CTA `rank` writes its share of the elements
+  // ---- the cluster's CTAs join their results: CTA `rank` writes its share of the elements. All the
+  // remote loads go out together: one trip's latency, not one per CTA.
   const int pairs = n_q * (D / 2);
   const int p0 = (int)((int64_t)pairs * rank / ranks), p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
   for (int at = p0 + threadIdx.x; at < p1; at += kThreads) {
     const int row = at / (D / 2), col = 2 * (at % (D / 2));
+    float mk[kMaxCluster], lk[kMaxCluster];
+    float2 v[kMaxCluster];
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      mk[k] = kNegInf;
+      lk[k] = 0.f;
+      v[k] = make_float2(0.f, 0.f);
+      if (k < ranks) {
+        mk[k] = *cluster.map_shared_rank(cm + row, k);
+        lk[k] = *cluster.map_shared_rank(cl + row, k);
+        v[k] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + row * D + col, k));
+      }
+    }
     float M = kNegInf;
-    for (int k = 0; k < ranks; ++k) M = fmaxf(M, *cluster.map_shared_rank(wm + row, k));
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mk[k]);
     float x = 0.f, y = 0.f, L = 0.f;
     if (M != kNegInf) {
-      for (int k = 0; k < ranks; ++k) {
-        const float a = ex2_approx(*cluster.map_shared_rank(wm + row, k) - M);
-        const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + row * D + col, k));
-        x = fmaf(a, v.x, x);
-        y = fmaf(a, v.y, y);
-        L = fmaf(a, *cluster.map_shared_rank(wl + row, k), L);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        const float a = ex2_approx(mk[k] - M);
+        x = fmaf(a, v[k].x, x);
+        y = fmaf(a, v[k].y, y);
+        L = fmaf(a, lk[k], L);
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
