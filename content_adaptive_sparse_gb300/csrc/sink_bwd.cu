@@ -19,8 +19,8 @@
 // stored; products complete) frees the columns: the compute warps neither announce nor wait for
 // free columns. S has two buffers (steps alternate), and the next step's S runs under this step's
 // exponentials; dP has one, and the next dP runs once this step's dS is stored. Key-stationary at
-// d = 128 the accumulators leave room for one S; there dS goes over dP, the next S waits for this
-// step's dV product and the next dP for its dK product.
+// d = 128 the accumulators leave room for two buffers in all, which S and dP exchange every step: the
+// next S goes where dP lay, once that is read, and the next dP over P and dS, once they are used.
 //
 // The sinks are seen by every query: the first key tile's items over the queries past the
 // window are cut into chunks of query tiles as long as an ordinary item, whose fp32 sums of the
@@ -75,11 +75,10 @@ struct Cfg {
   static constexpr int SMEM_NEED = 1024 + FIX * 2 * TILE + STAGES * STAGE + kComputeWarps * 1024 * OUT;
   // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
   static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
-  // TMEM columns: S (one buffer or two), dP, accumulators. P is stored over the first half of the
-  // kCols columns of S that a warp reads, dS over the second half, or over the first half of its dP.
-  static constexpr int SB = KV && D == 128 ? 1 : 2;
-  static constexpr uint32_t COL_DP = 128 * SB;
-  static constexpr uint32_t COL_ACC0 = COL_DP + 128;   // dQ or dK
+  // TMEM columns: two buffers of S, dP (SWAP: in the buffer that S leaves free), accumulators. P is
+  // stored over the first half of the kCols columns of S that a warp reads, dS over the second half.
+  static constexpr bool SWAP = KV && D == 128;
+  static constexpr uint32_t COL_ACC0 = SWAP ? 256 : 384;   // dQ or dK
   static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;   // dV
   static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
   static_assert(kCols == 32, "one visibility word per thread");
@@ -108,6 +107,7 @@ struct Bars {
   // Steps alternate between two barriers (phase: step / 2) where a wait for one step could meet the
   // next one's completion
   uint64_t s_full[2], dp_full;      // S / dP written
+  uint64_t dp_read;                 // SWAP: dP read by the compute warps
   uint64_t p_full[2], ds_full[2];   // P / dS stored by the compute warps
   uint64_t dv_done[2], dk_done[2];  // products of P (dV) and of dS (dK or dQ) complete
   uint64_t acc_full;                // an item's accumulators complete (phase: item)
@@ -268,6 +268,13 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
     drain_bar(&bars.st_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
 }
 
+// TMEM columns of S and dP of step g.
+__device__ __forceinline__ constexpr uint32_t col_s(int g) { return 128u * (uint32_t)(g & 1); }
+template <bool SWAP>
+__device__ __forceinline__ constexpr uint32_t col_dp(int g) {
+  return SWAP ? 128u - col_s(g) : 256u;
+}
+
 // ------------------------------------------------------------------ MMA issuers (warps 1-3, lane 0)
 
 // One thread issues an MMA every ~67 cycles and spends hundreds more in the waits between products
@@ -300,13 +307,13 @@ struct Issuer {
       mma_bf16_ts(tmem + col, tmem + a + (uint32_t)(kCols * (ks / (kCols / 16)) + 8 * (ks % (kCols / 16))), b + (uint64_t)((16 * ks * C::ROWB) >> 4),
                   idesc, (acc || ks > 0) ? 1u : 0u);
   }
-  static __device__ constexpr uint32_t col_s(int g) { return C::SB == 2 ? 128u * (g & 1) : 0u; }
-  static __device__ constexpr uint32_t col_ds(int g) { return C::SB == 2 ? col_s(g) + kCols / 2 : C::COL_DP; }
-  // S of step g, once the P and dS that lay over its columns are used; dP once step g - 1's is used
+  // S of step g, once what lay in its buffer is used: P and dS of two steps before, or the last dP
   __device__ __forceinline__ bool scores(int g, uint64_t fix) const {
-    if (g >= C::SB) {
-      if (KV && !wait_pair(bars.dv_done, g - C::SB, abort_flag)) return false;
-      if (C::SB == 2 && !wait_pair(bars.dk_done, g - 2, abort_flag)) return false;
+    if constexpr (C::SWAP) {
+      if (g > 0 && !wait_bar(&bars.dp_read, (uint32_t)(g - 1) & 1u, abort_flag)) return false;
+    } else if (g >= 2) {
+      if (KV && !wait_pair(bars.dv_done, g - 2, abort_flag)) return false;
+      if (!wait_pair(bars.dk_done, g - 2, abort_flag)) return false;
     }
     if (!landed(g)) return false;
     tc_fence_after();
@@ -314,11 +321,18 @@ struct Issuer {
     mma_commit(&bars.s_full[g & 1]);
     return true;
   }
+  // dP, once step g - 1's is read, or its P and dS are used
   __device__ __forceinline__ bool products(int g, uint64_t fix) const {
-    if (g > 0 && !wait_pair(C::SB == 2 ? bars.ds_full : bars.dk_done, g - 1, abort_flag)) return false;
+    if (g > 0) {
+      if constexpr (C::SWAP) {
+        if (!wait_pair(bars.dv_done, g - 1, abort_flag) || !wait_pair(bars.dk_done, g - 1, abort_flag)) return false;
+      } else if (!wait_pair(bars.ds_full, g - 1, abort_flag)) {
+        return false;
+      }
+    }
     if (!landed(g)) return false;
     tc_fence_after();
-    rows_x_rows(C::COL_DP, a1 + fix, b1 + at(g % C::STAGES));
+    rows_x_rows(col_dp<C::SWAP>(g), a1 + fix, b1 + at(g % C::STAGES));
     mma_commit(&bars.dp_full);
     return true;
   }
@@ -333,7 +347,7 @@ struct Issuer {
   __device__ __forceinline__ bool acc0(int g, bool acc) const {
     if (!landed(g) || !wait_pair(bars.ds_full, g, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC0, col_ds(g), b0mn + at(g % C::STAGES), acc);
+    pairs_x_tile(C::COL_ACC0, col_s(g) + kCols / 2, b0mn + at(g % C::STAGES), acc);
     mma_commit(&bars.st_empty[g % C::STAGES]);
     mma_commit(&bars.dk_done[g & 1]);
     return true;
@@ -419,6 +433,10 @@ struct Compute {
   // This warp's TMEM stores are done: one arrival.
   __device__ __forceinline__ void arrive(uint64_t* bar) const {
     tmem_st_wait();
+    announce(bar);
+  }
+  // Its TMEM loads are.
+  __device__ __forceinline__ void announce(uint64_t* bar) const {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -486,8 +504,8 @@ struct Compute {
   template <int SEE>
   __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see, float nl2, float dval, const Item* prev,
                                        int n) const {
-    const uint32_t tS = base + (uint32_t)(kCols * part) + (C::SB == 2 ? 128u * (g & 1) : 0u);
-    const uint32_t tDP = base + C::COL_DP + (uint32_t)(kCols * part);
+    const uint32_t tS = base + (uint32_t)(kCols * part) + col_s(g);
+    const uint32_t tDP = base + (uint32_t)(kCols * part) + col_dp<C::SWAP>(g);
     if (!__all_sync(0xffffffffu, wait_pair(bars.s_full, g, abort_flag))) return false;
     tc_fence_after();
     // ---- P
@@ -536,6 +554,7 @@ struct Compute {
       uint32_t v[kCols];
       tmem_ld_x32(tDP, v);
       tmem_ld_wait<kCols>(v);
+      if constexpr (C::SWAP) announce(&bars.dp_read);
 #pragma unroll
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(dval, dval, dval, dval);
@@ -550,10 +569,11 @@ struct Compute {
         }
       }
     } else {
+      if constexpr (C::SWAP) announce(&bars.dp_read);
 #pragma unroll
       for (int e = 0; e < kCols / 2; ++e) ds[e] = 0u;
     }
-    tmem_st_x16(C::SB == 2 ? tS + kCols / 2 : tDP, ds);
+    tmem_st_x16(tS + kCols / 2, ds);
     arrive(&bars.ds_full[g & 1]);
     return true;
   }
@@ -632,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.dk_done[i], 1);
     }
     mbar_init(&bars.dp_full, 1);
+    mbar_init(&bars.dp_read, kComputeWarps);
     mbar_init(&bars.acc_full, KV ? 2 : 1);
     for (int i = 0; i < kIssuers; ++i) mbar_init(&bars.drain[i], 1);
     abort_flag = 0;
