@@ -27,7 +27,7 @@
 // sinks' rows go to the workspace and are added in a fixed order.
 //
 // One persistent CTA per SM (20 warps), items dealt out in turn:
-//   warp 0      lane 0 loads the stationary tiles and the ring by TMA
+//   warp 0      loads the stationary tiles and the rings by TMA
 //   warps 1-3   lane 0 issues MMAs (S and dP, dV, dK; or S, dP, dQ); warp 1 owns TMEM
 //   warps 4-19  compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
 //               columns 32 c .. 32 c + 31 of a step, c = w / 4 - 1; at an item's end they write
@@ -52,7 +52,7 @@ constexpr int kCols = 32;              // columns of a step per compute warp
 constexpr int kComputeWarps = 4 * kTile / kCols;
 constexpr int kIssuers = 3;           // warps whose lane 0 issues MMAs
 constexpr int kThreads = 32 * (1 + kIssuers + kComputeWarps);
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -68,11 +68,14 @@ struct Cfg {
   static constexpr int CHUNK = kTile * ROWB;           // one d-chunk of a 128-row tile
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int FIX = D == 128 ? 1 : 2;         // buffers of the stationary tiles
-  static constexpr int STAGES = D == 128 ? 2 : 3;
-  static constexpr int STAGE = 2 * TILE + 1024;        // B0, B1, then -LSE log2(e) [128] and D [128]
+  // slots of B0 and of B1
+  static constexpr int N0 = D < 128 || !KV ? 3 : 2;
+  static constexpr int N1 = D < 128 ? 3 : (KV ? 2 : 1);
+  static constexpr int SLOT0 = TILE + (KV ? 1024 : 0);   // B0, then -LSE log2(e) [128] and D [128]
+  static constexpr int RING = N0 * SLOT0 + N1 * TILE;
   // then OUT KB per compute warp, from which the outputs leave
   static constexpr int OUT = KV && D == 64 ? 2 : 1;
-  static constexpr int SMEM_NEED = 1024 + FIX * 2 * TILE + STAGES * STAGE + kComputeWarps * 1024 * OUT;
+  static constexpr int SMEM_NEED = 1024 + FIX * 2 * TILE + RING + kComputeWarps * 1024 * OUT;
   // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
   static constexpr int SMEM = SMEM_NEED > 120 * 1024 ? SMEM_NEED : 120 * 1024;
   // TMEM columns: two buffers of S, dP (SWAP: in the buffer that S leaves free), accumulators. P is
@@ -82,7 +85,7 @@ struct Cfg {
   static constexpr uint32_t COL_ACC1 = COL_ACC0 + D;   // dV
   static_assert(COL_ACC0 + (KV ? 2 : 1) * D <= kTmemCols, "TMEM columns");
   static_assert(kCols == 32, "one visibility word per thread");
-  static_assert(STAGES <= kMaxStages && SMEM <= 226 * 1024, "shared memory");
+  static_assert(N0 <= kMaxStages && N1 <= kMaxStages && SMEM <= 226 * 1024, "shared memory");
 };
 
 struct BParams {
@@ -103,7 +106,8 @@ struct BParams {
 
 struct Bars {
   uint64_t fixed_full[2], fixed_empty[2];               // stationary tiles (items alternate where FIX is 2)
-  uint64_t st_full[kMaxStages], st_empty[kMaxStages];   // ring
+  // ring; [0]: B0 with -LSE and D, for S and the dS product, [1]: B1, for dP and the P product
+  uint64_t st_full[2][kMaxStages], st_empty[2][kMaxStages];
   // Steps alternate between two barriers (phase: step / 2) where a wait for one step could meet the
   // next one's completion
   uint64_t s_full[2], dp_full;      // S / dP written
@@ -222,50 +226,66 @@ __device__ __forceinline__ constexpr uint32_t kstep(int ks) {
   return (uint32_t)(((ks * 16) / C::CH) * C::CHUNK + ((ks * 16) % C::CH) * 2) >> 4;
 }
 
-// ------------------------------------------------------------------ loader (warp 0, lane 0)
+// ------------------------------------------------------------------ loader (warp 0)
 
-template <int D, bool KV>
+// Requests the moving tile of a ring's g-th step, when the slot is free.
+template <int D, bool KV, int B>
+__device__ __forceinline__ bool load_slot(const BParams& p, const CUtensorMap* tb, Bars& bars, uint8_t* sRing, int g,
+                                          int head, int tile, int s, volatile int* abort_flag) {
+  using C = Cfg<D, KV>;
+  constexpr int N = B ? C::N1 : C::N0;
+  const int st = g % N;
+  uint64_t* bar = &bars.st_full[B][st];
+  if (g >= N && !wait_bar(&bars.st_empty[B][st], (uint32_t)(g / N - 1) & 1u, abort_flag)) return false;
+  uint8_t* slot = sRing + (B ? C::N0 * C::SLOT0 + st * C::TILE : st * C::SLOT0);
+  mbar_arrive_expect_tx(bar, B ? C::TILE : C::SLOT0);
+#pragma unroll
+  for (int c = 0; c < C::NCH; ++c) tma_load_4d(slot + c * C::CHUNK, tb, bar, c * C::CH, head, tile * kTile, s);
+  if constexpr (KV && B == 0) {
+    const int64_t row = ((int64_t)s * p.heads + head) * p.pitch + (int64_t)tile * kTile;
+    bulk_load(slot + C::TILE, p.nl2 + row, 512, bar);
+    bulk_load(slot + C::TILE + 512, p.dvec + row, 512, bar);
+  }
+  return true;
+}
+
+// B0: load the stationary tiles and B0's ring; B1: B1's. Where the rings are of one length one lane
+// loads both; where they are not, B0 runs ahead, so each has a lane (d = 128, dQ: 339 -> 297 us). Lanes
+// cost issue slots (d = 64: 165 -> 169 us), a further warp the compute warps' registers (-> 168 us).
+template <int D, bool KV, bool B0, bool B1>
 __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorMap* ta1, const CUtensorMap* tb0,
                        const CUtensorMap* tb1, Bars& bars, uint8_t* sFix, uint8_t* sRing, volatile int* abort_flag) {
   using C = Cfg<D, KV>;
-  int g = 0, n = 0;
+  int g0 = 0, g1 = 0, n = 0;
   bool ok = true;
   for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
     const Item it = decode_item<KV>(p, k);
-    // the S and dP of the item before in this buffer have read its stationary tiles
-    const int fb = n % C::FIX;
-    if (n >= C::FIX && !(ok = wait_bar(&bars.fixed_empty[fb], (uint32_t)(n / C::FIX - 1) & 1u, abort_flag))) break;
-    mbar_arrive_expect_tx(&bars.fixed_full[fb], 2 * C::TILE);
-    uint8_t* fix = sFix + fb * 2 * C::TILE;
-#pragma unroll
-    for (int c = 0; c < C::NCH; ++c) {
-      tma_load_4d(fix + c * C::CHUNK, ta0, &bars.fixed_full[fb], c * C::CH, it.head, it.tile * kTile, it.s);
-      tma_load_4d(fix + C::TILE + c * C::CHUNK, ta1, &bars.fixed_full[fb], c * C::CH, it.head, it.tile * kTile, it.s);
-    }
-    Steps<KV> at(p, it);
-    for (int j = 0; j < it.steps; ++j, ++g, at.next(it)) {
-      const int st = g % C::STAGES;
-      if (g >= C::STAGES && !(ok = wait_bar(&bars.st_empty[st], (uint32_t)(g / C::STAGES - 1) & 1u, abort_flag))) break;
-      const int head = at.head, tile = at.tile;
-      uint8_t* stage = sRing + st * C::STAGE;
-      mbar_arrive_expect_tx(&bars.st_full[st], 2 * C::TILE + (KV ? 1024 : 0));
+    if constexpr (B0) {
+      // the S and dP of the item before in this buffer have read its stationary tiles
+      const int fb = n % C::FIX;
+      if (n >= C::FIX && !(ok = wait_bar(&bars.fixed_empty[fb], (uint32_t)(n / C::FIX - 1) & 1u, abort_flag))) break;
+      mbar_arrive_expect_tx(&bars.fixed_full[fb], 2 * C::TILE);
+      uint8_t* fix = sFix + fb * 2 * C::TILE;
 #pragma unroll
       for (int c = 0; c < C::NCH; ++c) {
-        tma_load_4d(stage + c * C::CHUNK, tb0, &bars.st_full[st], c * C::CH, head, tile * kTile, it.s);
-        tma_load_4d(stage + C::TILE + c * C::CHUNK, tb1, &bars.st_full[st], c * C::CH, head, tile * kTile, it.s);
-      }
-      if constexpr (KV) {
-        const int64_t row = ((int64_t)it.s * p.heads + head) * p.pitch + (int64_t)tile * kTile;
-        bulk_load(stage + 2 * C::TILE, p.nl2 + row, 512, &bars.st_full[st]);
-        bulk_load(stage + 2 * C::TILE + 512, p.dvec + row, 512, &bars.st_full[st]);
+        tma_load_4d(fix + c * C::CHUNK, ta0, &bars.fixed_full[fb], c * C::CH, it.head, it.tile * kTile, it.s);
+        tma_load_4d(fix + C::TILE + c * C::CHUNK, ta1, &bars.fixed_full[fb], c * C::CH, it.head, it.tile * kTile, it.s);
       }
     }
+    Steps<KV> at(p, it);
+    for (int j = 0; j < it.steps; ++j, at.next(it)) {
+      if (B1 && !(ok = load_slot<D, KV, 1>(p, tb1, bars, sRing, g1, at.head, at.tile, it.s, abort_flag))) break;
+      g1 += B1;
+      if (B0 && !(ok = load_slot<D, KV, 0>(p, tb0, bars, sRing, g0, at.head, at.tile, it.s, abort_flag))) break;
+      g0 += B0;
+    }
   }
-  // every copy of this CTA has landed before it may exit (n counts the items whose stationary
-  // tiles were requested, a broken-off one too; g the steps requested)
-  for (int i = max(0, n - C::FIX); i < n; ++i) drain_bar(&bars.fixed_full[i % C::FIX], (uint32_t)(i / C::FIX) & 1u);
-  for (int t = max(0, g - C::STAGES); t < g; ++t)
-    drain_bar(&bars.st_full[t % C::STAGES], (uint32_t)(t / C::STAGES) & 1u);
+  // every copy of this lane has landed before the CTA may exit (n counts the items whose stationary
+  // tiles were requested, a broken-off one too; g0, g1 the steps requested)
+  if constexpr (B0)
+    for (int i = max(0, n - C::FIX); i < n; ++i) drain_bar(&bars.fixed_full[i % C::FIX], (uint32_t)(i / C::FIX) & 1u);
+  for (int t = max(0, g0 - C::N0); t < g0; ++t) drain_bar(&bars.st_full[0][t % C::N0], (uint32_t)(t / C::N0) & 1u);
+  for (int t = max(0, g1 - C::N1); t < g1; ++t) drain_bar(&bars.st_full[1][t % C::N1], (uint32_t)(t / C::N1) & 1u);
 }
 
 // TMEM columns of S and dP of step g.
@@ -288,9 +308,14 @@ struct Issuer {
   volatile int* abort_flag;
   uint64_t a0, a1, b0, b1, b0mn, b1mn;
 
-  __device__ uint64_t at(int st) const { return (uint64_t)((st * C::STAGE) >> 4); }
-  __device__ __forceinline__ bool landed(int g) const {
-    return wait_bar(&bars.st_full[g % C::STAGES], (uint32_t)(g / C::STAGES) & 1u, abort_flag);
+  // descriptor offsets of step g's slots
+  __device__ static uint64_t at0(int g) { return (uint64_t)((g % C::N0 * C::SLOT0) >> 4); }
+  __device__ static uint64_t at1(int g) { return (uint64_t)((g % C::N1 * C::TILE) >> 4); }
+  __device__ __forceinline__ bool landed0(int g) const {
+    return wait_bar(&bars.st_full[0][g % C::N0], (uint32_t)(g / C::N0) & 1u, abort_flag);
+  }
+  __device__ __forceinline__ bool landed1(int g) const {
+    return wait_bar(&bars.st_full[1][g % C::N1], (uint32_t)(g / C::N1) & 1u, abort_flag);
   }
 
   __device__ __forceinline__ void rows_x_rows(uint32_t col, uint64_t a, uint64_t b) const {
@@ -315,9 +340,9 @@ struct Issuer {
       if (KV && !wait_pair(bars.dv_done, g - 2, abort_flag)) return false;
       if (!wait_pair(bars.dk_done, g - 2, abort_flag)) return false;
     }
-    if (!landed(g)) return false;
+    if (!landed0(g)) return false;
     tc_fence_after();
-    rows_x_rows(col_s(g), a0 + fix, b0 + at(g % C::STAGES));
+    rows_x_rows(col_s(g), a0 + fix, b0 + at0(g));
     mma_commit(&bars.s_full[g & 1]);
     return true;
   }
@@ -330,25 +355,26 @@ struct Issuer {
         return false;
       }
     }
-    if (!landed(g)) return false;
+    if (!landed1(g)) return false;
     tc_fence_after();
-    rows_x_rows(col_dp<C::SWAP>(g), a1 + fix, b1 + at(g % C::STAGES));
+    rows_x_rows(col_dp<C::SWAP>(g), a1 + fix, b1 + at1(g));
+    mma_commit(&bars.st_empty[1][g % C::N1]);
     mma_commit(&bars.dp_full);
     return true;
   }
   __device__ __forceinline__ bool acc1(int g, bool acc) const {
-    if (!landed(g) || !wait_pair(bars.p_full, g, abort_flag)) return false;
+    if (!landed1(g) || !wait_pair(bars.p_full, g, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC1, col_s(g), b1mn + at(g % C::STAGES), acc);
-    mma_commit(&bars.st_empty[g % C::STAGES]);
+    pairs_x_tile(C::COL_ACC1, col_s(g), b1mn + at1(g), acc);
+    mma_commit(&bars.st_empty[1][g % C::N1]);
     mma_commit(&bars.dv_done[g & 1]);
     return true;
   }
   __device__ __forceinline__ bool acc0(int g, bool acc) const {
-    if (!landed(g) || !wait_pair(bars.ds_full, g, abort_flag)) return false;
+    if (!landed0(g) || !wait_pair(bars.ds_full, g, abort_flag)) return false;
     tc_fence_after();
-    pairs_x_tile(C::COL_ACC0, col_s(g) + kCols / 2, b0mn + at(g % C::STAGES), acc);
-    mma_commit(&bars.st_empty[g % C::STAGES]);
+    pairs_x_tile(C::COL_ACC0, col_s(g) + kCols / 2, b0mn + at0(g), acc);
+    mma_commit(&bars.st_empty[0][g % C::N0]);
     mma_commit(&bars.dk_done[g & 1]);
     return true;
   }
@@ -358,14 +384,14 @@ template <int D, bool KV>
 __device__ void issuer(const BParams& p, int role, Bars& bars, uint8_t* sFix, uint8_t* sRing, uint32_t tmem,
                        volatile int* abort_flag) {
   using C = Cfg<D, KV>;
-  const uint32_t fix = smem_u32(sFix), ring = smem_u32(sRing);
+  const uint32_t fix = smem_u32(sFix), ring = smem_u32(sRing), ring1 = ring + C::N0 * C::SLOT0;
   const Issuer<D, KV> I{bars, tmem, abort_flag,
                         make_smem_desc(fix, 16, C::ATOM, C::SWZ),
                         make_smem_desc(fix + C::TILE, 16, C::ATOM, C::SWZ),
                         make_smem_desc(ring, 16, C::ATOM, C::SWZ),
-                        make_smem_desc(ring + C::TILE, 16, C::ATOM, C::SWZ),
+                        make_smem_desc(ring1, 16, C::ATOM, C::SWZ),
                         make_smem_desc(ring, C::CHUNK, C::ATOM, C::SWZ),
-                        make_smem_desc(ring + C::TILE, C::CHUNK, C::ATOM, C::SWZ)};
+                        make_smem_desc(ring1, C::CHUNK, C::ATOM, C::SWZ)};
   int g = 0, n = 0;
   bool ok = true;
   for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
@@ -515,7 +541,7 @@ struct Compute {
       tmem_ld_x32(tS, v);
       // dK / dV: the stage's -LSE and D have landed with its tiles
       if (KV && !__all_sync(0xffffffffu,
-                            wait_bar(&bars.st_full[g % C::STAGES], (uint32_t)(g / C::STAGES) & 1u, abort_flag)))
+                            wait_bar(&bars.st_full[0][g % C::N0], (uint32_t)(g / C::N0) & 1u, abort_flag)))
         return false;
       tmem_ld_wait<kCols>(v);
 #pragma unroll
@@ -589,7 +615,7 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
   const uint32_t ring = smem_u32(sRing);
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
   const Compute<D, KV> W{p, to0, to1, bars, abort_flag, base, quarter, part, lane,
-                         sRing + C::STAGES * C::STAGE + 1024 * C::OUT * (4 * part + quarter), f2_pack(p.scale_log2, p.scale_log2)};
+                         sRing + C::RING + 1024 * C::OUT * (4 * part + quarter), f2_pack(p.scale_log2, p.scale_log2)};
   int g = 0, n = 0;
   Item it, prev;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
@@ -606,7 +632,7 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
     if (KV && n > 0 && !W.write(prev, n - 1)) return;
     for (int j = 0; j < it.steps; ++j, ++g, moving.next(it)) {
       const int c0 = moving.tile * kTile + kCols * part;
-      const uint32_t vec = ring + (uint32_t)((g % C::STAGES) * C::STAGE + 2 * C::TILE + 4 * kCols * part);
+      const uint32_t vec = ring + (uint32_t)((g % C::N0) * C::SLOT0 + C::TILE + 4 * kCols * part);
       const int see = visibility<KV>(it.tile * kTile + 32 * quarter, c0, p.window, p.sinks);
       const Item* before = !KV && j == 0 && n > 0 ? &prev : nullptr;
       bool ok;
@@ -640,9 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.fixed_full[i], 1);
       mbar_init(&bars.fixed_empty[i], KV ? 1 : 2);     // S and dP from one thread, or from two
     }
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&bars.st_full[i], 1);
-      mbar_init(&bars.st_empty[i], KV ? 2 : 1);        // the products into the accumulators
+    for (int i = 0; i < kMaxStages; ++i) {
+      for (int b = 0; b < 2; ++b) mbar_init(&bars.st_full[b][i], 1);
+      mbar_init(&bars.st_empty[0][i], 1);              // the dS product (S is complete before)
+      mbar_init(&bars.st_empty[1][i], KV ? 2 : 1);     // dP, and the P product
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
@@ -675,7 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sFix = sbase;
   uint8_t* sRing = sFix + C::FIX * 2 * C::TILE;
   if (warp == 0) {
-    if ((threadIdx.x & 31) == 0) loader<D, KV>(p, &ta0, &ta1, &tb0, &tb1, bars, sFix, sRing, &abort_flag);
+    const int lane = threadIdx.x & 31;
+    constexpr bool kOne = C::N0 == C::N1;
+    if (lane == 0) loader<D, KV, true, kOne>(p, &ta0, &ta1, &tb0, &tb1, bars, sFix, sRing, &abort_flag);
+    if constexpr (!kOne)
+      if (lane == 1) loader<D, KV, false, true>(p, &ta0, &ta1, &tb0, &tb1, bars, sFix, sRing, &abort_flag);
     __syncwarp();
   } else if (warp <= kIssuers) {
     if ((threadIdx.x & 31) == 0) issuer<D, KV>(p, warp - 1, bars, sFix, sRing, tmem, &abort_flag);
