@@ -724,8 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ D and -LSE log2(e)
 
-// D / 8 consecutive threads per (sequence, token, head) row, 16 bytes of O and dO each; tokens
-// n .. pitch - 1 get D = 0 and -LSE = -inf, so that their P is 0.
+// D / 8 consecutive threads per kPrepRows (token, head) rows of a sequence, 16 bytes of O and dO each;
+// tokens n .. pitch - 1 get D = 0 and -LSE = -inf, so that their P is 0.
+constexpr int kPrepRows = 2;
 template <int D>
 __global__ void __launch_bounds__(256)
     sink_prep_kernel(const __nv_bfloat16* o, const __nv_bfloat16* d_o, const float* lse, int64_t o_sb, int64_t o_sn,
@@ -733,30 +734,38 @@ __global__ void __launch_bounds__(256)
                      int pitch, float* nl2, float* dvec) {
   constexpr int G = D / 8;
   const float kNegInf = __int_as_float(0xff800000);
-  const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t row = gid / G;
-  const int part = (int)(gid % G);
-  const bool in = row < (int64_t)batch * pitch * heads;
-  const int h = (int)(row % heads);
-  const int i = (int)(row / heads % pitch);
-  const int s = (int)(row / heads / pitch);
-  float acc = 0.f;
-  if (in && i < n_tokens) {
-    const uint4 a = *reinterpret_cast<const uint4*>(o + s * o_sb + i * o_sn + h * o_sh + 8 * part);
-    const uint4 b = *reinterpret_cast<const uint4*>(d_o + s * g_sb + i * g_sn + h * g_sh + 8 * part);
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+  const int part = threadIdx.x % G;
+  const uint32_t rows = (uint32_t)pitch * (uint32_t)heads;   // below 2^31 (the host's check)
+  for (int s = blockIdx.y; s < batch; s += gridDim.y) {
+    const uint32_t r0 = (blockIdx.x * (blockDim.x / G) + threadIdx.x / G) * kPrepRows;
+    uint4 a[kPrepRows], b[kPrepRows];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
-      acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
+    for (int u = 0; u < kPrepRows; ++u) {
+      const uint32_t i = (r0 + u) / (uint32_t)heads, h = (r0 + u) % (uint32_t)heads;
+      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < (uint32_t)n_tokens) {
+        a[u] = *reinterpret_cast<const uint4*>(o + s * o_sb + i * o_sn + h * o_sh + 8 * part);
+        b[u] = *reinterpret_cast<const uint4*>(d_o + s * g_sb + i * g_sn + h * g_sh + 8 * part);
+      }
     }
-  }
 #pragma unroll
-  for (int w = G / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w, G);
-  if (in && part == 0) {
-    const int64_t at = ((int64_t)s * heads + h) * pitch + i;
-    dvec[at] = acc;
-    nl2[at] = i < n_tokens ? -lse[((int64_t)s * heads + h) * n_tokens + i] * kLog2e : kNegInf;
+    for (int u = 0; u < kPrepRows; ++u) {
+      const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bv[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+      float acc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
+        acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
+      }
+#pragma unroll
+      for (int w = G / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w, G);
+      const uint32_t i = (r0 + u) / (uint32_t)heads, h = (r0 + u) % (uint32_t)heads;
+      if (part == 0 && r0 + u < rows) {
+        const int64_t bh = (int64_t)s * heads + h;
+        dvec[bh * pitch + i] = acc;
+        nl2[bh * pitch + i] = i < (uint32_t)n_tokens ? -lse[bh * n_tokens + i] * kLog2e : kNegInf;
+      }
+    }
   }
 }
 
@@ -852,8 +861,10 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
   p.partial = reinterpret_cast<float*>(wsb + ws.partial_off);
   p.scale = a.softmax_scale;
   p.scale_log2 = a.softmax_scale * kLog2e;
-  const int64_t threads = (int64_t)a.batch * p.pitch * a.heads * (D / 8);
-  sink_prep_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(
+  const int64_t groups = ((int64_t)p.pitch * a.heads + kPrepRows - 1) / kPrepRows;   // of D / 8 threads
+  if (groups * kPrepRows >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
+  const dim3 prep_grid((unsigned)((groups * (D / 8) + 255) / 256), (unsigned)(a.batch < 65535 ? a.batch : 65535));
+  sink_prep_kernel<D><<<prep_grid, 256, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.d_o), a.lse, a.o_strides[0],
       a.o_strides[1], a.o_strides[2], a.do_strides[0], a.do_strides[1], a.do_strides[2], a.batch, a.n_tokens, a.heads,
       p.pitch, nl2, dvec);
