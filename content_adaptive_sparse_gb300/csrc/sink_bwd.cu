@@ -643,9 +643,6 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
     }
   }
   if (n > 0) W.write(it, n - 1);
-  // this warp's stores are complete before the CTA may exit
-  if (lane < C::OUT) bulk_wait_group<0>();
-  __syncwarp();
 }
 
 template <int D, bool KV>
@@ -713,6 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     compute<D, KV>(p, &to0, &to1, bars, sRing, tmem, &abort_flag);
+    // this warp's stores are complete before the CTA may exit
+    if ((threadIdx.x & 31) < C::OUT) bulk_wait_group<0>();
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
