@@ -29,6 +29,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "f32x2.cuh"
 #include "ptx_sm100.cuh"
 #include "sa_internal.h"
 #include "tma_host.h"
@@ -108,24 +109,6 @@ __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
   mbar_wait(bar, parity, &never, &g_sink_fwd_err, kErrTimeout);
 }
 
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -325,9 +308,9 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* v, uint64_t c2, uint64
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, r2), x0, x1);
+    f2::unpack(f2::fma(f2::pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, r2), x0, x1);
     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-    rs[(j >> 1) & 1] = f2_add(rs[(j >> 1) & 1], f2_pack(p0, p1));
+    rs[(j >> 1) & 1] = f2::add(rs[(j >> 1) & 1], f2::pack(p0, p1));
     pk[j >> 1] = pack_bf16x2(p0, p1);
   }
 }
@@ -395,7 +378,7 @@ struct Softmax {
         }
       }
       const float ref = SEE == kSome && m == kNegInf ? 0.f : m;           // no key seen yet: all scores are -inf
-      const uint64_t c2 = f2_pack(c, c), r2 = f2_pack(-ref, -ref);
+      const uint64_t c2 = f2::pack(c, c), r2 = f2::pack(-ref, -ref);
       uint64_t rs[2] = {0ull, 0ull};
       if (on0) {
         exp_chunk(v, c2, r2, pk, rs);
@@ -410,7 +393,7 @@ struct Softmax {
         for (int j = 16; j < 32; ++j) pk[j] = 0u;
       }
       float lo, hi;
-      f2_unpack(f2_add(rs[0], rs[1]), lo, hi);
+      f2::unpack(f2::add(rs[0], rs[1]), lo, hi);
       l += lo + hi;
     }
     tmem_st_x32(t, pk);

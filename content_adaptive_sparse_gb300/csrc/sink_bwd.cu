@@ -38,6 +38,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "f32x2.cuh"
 #include "ptx_sm100.cuh"
 #include "sa_internal.h"
 #include "tma_host.h"
@@ -128,30 +129,6 @@ __device__ __forceinline__ bool wait_pair(uint64_t (&bar)[2], int g, volatile in
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
   int never = 0;
   mbar_wait(bar, parity, &never, &g_sink_bwd_err, kErrTimeout);
-}
-
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 // Work item: a stationary tile and its moving tiles. Step j (0 .. steps - 1) of a dQ item is key
@@ -548,11 +525,11 @@ struct Compute {
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(nl2, nl2, nl2, nl2);
         if constexpr (KV) L = ld_shared_f4(vec + 4 * e);
-        const uint64_t s01 = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        const uint64_t s23 = f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        const uint64_t s01 = f2::pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        const uint64_t s23 = f2::pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
         float x[4];
-        f2_unpack(f2_fma(s01, c2, f2_pack(L.x, L.y)), x[0], x[1]);
-        f2_unpack(f2_fma(s23, c2, f2_pack(L.z, L.w)), x[2], x[3]);
+        f2::unpack(f2::fma(s01, c2, f2::pack(L.x, L.y)), x[0], x[1]);
+        f2::unpack(f2::fma(s23, c2, f2::pack(L.z, L.w)), x[2], x[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (SEE == kSome) x[i] = ((see >> (e + i)) & 1u) ? x[i] : __int_as_float(0xff800000);
@@ -587,10 +564,10 @@ struct Compute {
         if constexpr (KV) L = ld_shared_f4(vec + 512 + 4 * e);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const uint64_t d2 = i ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y);
-          const uint64_t dp = f2_pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1]));
+          const uint64_t d2 = i ? f2::pack(L.z, L.w) : f2::pack(L.x, L.y);
+          const uint64_t dp = f2::pack(__uint_as_float(v[e + i]), __uint_as_float(v[e + i + 1]));
           float y0, y1;
-          f2_unpack(f2_mul(f2_pack(pr[e + i], pr[e + i + 1]), f2_sub(dp, d2)), y0, y1);
+          f2::unpack(f2::mul(f2::pack(pr[e + i], pr[e + i + 1]), f2::sub(dp, d2)), y0, y1);
           ds[(e + i) >> 1] = pack_bf16x2(y0, y1);
         }
       }
@@ -615,7 +592,7 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
   const uint32_t ring = smem_u32(sRing);
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
   const Compute<D, KV> W{p, to0, to1, bars, abort_flag, base, quarter, part, lane,
-                         sRing + C::RING + 1024 * C::OUT * (4 * part + quarter), f2_pack(p.scale_log2, p.scale_log2)};
+                         sRing + C::RING + 1024 * C::OUT * (4 * part + quarter), f2::pack(p.scale_log2, p.scale_log2)};
   int g = 0, n = 0;
   Item it, prev;
   for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
