@@ -4,10 +4,11 @@
 // (i - j <= window or j < sinks)". With P_ij = exp(s_ij - LSE_i), D_i = sum_d dO_id O_id:
 //   dP_ij = <dO_i, v_j>,  dS_ij = P_ij (dP_ij - D_i),
 //   dQ_i = c sum_j dS_ij k_j,  dK_j = c sum_i dS_ij q_i,  dV_j = sum_i P_ij dO_i.
-// Launches: sink_prep_kernel (D and -LSE log2(e), padded to whole tiles), sink_bwd_kernel<D, false>
-// (dQ: query-stationary), sink_bwd_kernel<D, true> (dK and dV: key-stationary, all query heads of
-// the key head), and sink_reduce_kernel when the sinks' rows were summed in parts. S and dP are
-// taken twice, so every gradient row has one owner: no atomics, the same bits every run.
+// Launches: sink_prep_kernel and, where few keys are seen, sink_few_kernel (D and -LSE log2(e), padded
+// to whole tiles), sink_bwd_kernel<D, false> (dQ: query-stationary), sink_bwd_kernel<D, true> (dK and
+// dV: key-stationary, all query heads of the key head), and sink_reduce_kernel when the sinks' rows
+// were summed in parts. S and dP are taken twice, so every gradient row has one owner: no atomics,
+// the same bits every run.
 //
 // Step: 128 stationary rows (A0, A1) against 128 moving rows (B0, B1) of a ring stage,
 //   S = A0 B0^T, dP = A1 B1^T (tcgen05, SS, N = 128), then from the compute warps
@@ -102,7 +103,7 @@ struct BParams {
   __nv_bfloat16* out1;              // dV
   int64_t os_b[2], os_n[2], os_h[2];   // strides of out0, out1
   float* partial;                   // [batch][kv_heads][n_chunks + 1][2][sinks][d]
-  float scale, scale_log2;
+  float scale, scale_log2;          // of dQ and dK; of the scores
 };
 
 struct Bars {
@@ -701,47 +702,121 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ D and -LSE log2(e)
 
+struct PrepTensor {
+  const __nv_bfloat16* ptr;
+  int64_t sb, sn, sh;
+};
+
+struct PrepParams {
+  PrepTensor q, k, v, o, d_o;
+  const float* lse;
+  float* nl2;
+  float* dvec;
+  int batch, n_tokens, heads, group, pitch, window, sinks;
+  float scale_log2;
+};
+
+// This lane's share of a dot product: 8 elements.
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+  const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+  float acc = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
+    acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
+  }
+  return acc;
+}
+
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int w = G / 2; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w, G);
+  return v;
+}
+
+// The row `part` of D / 8 threads reads 16 bytes of.
+__device__ __forceinline__ uint4 prep_row(const PrepTensor& t, int s, uint32_t i, uint32_t h, int part) {
+  return *reinterpret_cast<const uint4*>(t.ptr + s * t.sb + i * t.sn + h * t.sh + 8 * part);
+}
+
 // D / 8 consecutive threads per kPrepRows (token, head) rows of a sequence, 16 bytes of O and dO each;
-// tokens n .. pitch - 1 get D = 0 and -LSE = -inf, so that their P is 0.
+// tokens n .. pitch - 1 get D = 0 and -LSE = -inf, so that their P is 0. (16321 tokens of 16 heads of
+// 128: 28 us, 4.8 TB/s; one row a thread 32.)
 constexpr int kPrepRows = 2;
 template <int D>
-__global__ void __launch_bounds__(256)
-    sink_prep_kernel(const __nv_bfloat16* o, const __nv_bfloat16* d_o, const float* lse, int64_t o_sb, int64_t o_sn,
-                     int64_t o_sh, int64_t g_sb, int64_t g_sn, int64_t g_sh, int batch, int n_tokens, int heads,
-                     int pitch, float* nl2, float* dvec) {
+__global__ void __launch_bounds__(256) sink_prep_kernel(const __grid_constant__ PrepParams p) {
   constexpr int G = D / 8;
-  const float kNegInf = __int_as_float(0xff800000);
   const int part = threadIdx.x % G;
-  const uint32_t rows = (uint32_t)pitch * (uint32_t)heads;   // below 2^31 (the host's check)
-  for (int s = blockIdx.y; s < batch; s += gridDim.y) {
-    const uint32_t r0 = (blockIdx.x * (blockDim.x / G) + threadIdx.x / G) * kPrepRows;
+  const uint32_t heads = (uint32_t)p.heads, n = (uint32_t)p.n_tokens;
+  const uint32_t rows = (uint32_t)p.pitch * heads;           // below 2^31 (the host's check)
+  const uint32_t r0 = (blockIdx.x * (blockDim.x / G) + threadIdx.x / G) * kPrepRows;
+  for (int s = blockIdx.y; s < p.batch; s += gridDim.y) {
     uint4 a[kPrepRows], b[kPrepRows];
 #pragma unroll
     for (int u = 0; u < kPrepRows; ++u) {
-      const uint32_t i = (r0 + u) / (uint32_t)heads, h = (r0 + u) % (uint32_t)heads;
+      const uint32_t i = (r0 + u) / heads, h = (r0 + u) % heads;
       a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < (uint32_t)n_tokens) {
-        a[u] = *reinterpret_cast<const uint4*>(o + s * o_sb + i * o_sn + h * o_sh + 8 * part);
-        b[u] = *reinterpret_cast<const uint4*>(d_o + s * g_sb + i * g_sn + h * g_sh + 8 * part);
+      if (i < n) {
+        a[u] = prep_row(p.o, s, i, h, part);
+        b[u] = prep_row(p.d_o, s, i, h, part);
       }
     }
 #pragma unroll
     for (int u = 0; u < kPrepRows; ++u) {
-      const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bv[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
-      float acc = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc = fmaf(__uint_as_float(av[e] << 16), __uint_as_float(bv[e] << 16), acc);
-        acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), __uint_as_float(bv[e] & 0xffff0000u), acc);
-      }
-#pragma unroll
-      for (int w = G / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w, G);
-      const uint32_t i = (r0 + u) / (uint32_t)heads, h = (r0 + u) % (uint32_t)heads;
+      const uint32_t i = (r0 + u) / heads, h = (r0 + u) % heads;
+      const float d = lanes_sum<G>(dot8(a[u], b[u]));
       if (part == 0 && r0 + u < rows) {
         const int64_t bh = (int64_t)s * heads + h;
-        dvec[bh * pitch + i] = acc;
-        nl2[bh * pitch + i] = i < (uint32_t)n_tokens ? -lse[bh * n_tokens + i] * kLog2e : kNegInf;
+        p.dvec[bh * p.pitch + i] = d;
+        p.nl2[bh * p.pitch + i] = i < n ? -p.lse[bh * n + i] * kLog2e : __int_as_float(0xff800000);
       }
+    }
+  }
+}
+
+// The same for tokens below `tokens`, which see at most kFewKeys keys, with D = sum of P dP. O is stored
+// in bf16, and in <dO, O> its rounding, 2^-9 of |dO| |O|, goes into every dS of the row alike: into dQ
+// times the mean of the visible keys. That is little where many keys are seen (their mean is short,
+// and dS has a rounding of its own); at two keys it took dQ's error from 0.0024 to 0.0046 of its size.
+constexpr int kFewKeys = 8, kFewStep = 4;
+template <int D>
+__global__ void __launch_bounds__(256) sink_few_kernel(const __grid_constant__ PrepParams p, int tokens) {
+  constexpr int G = D / 8;
+  const int part = threadIdx.x % G;
+  const uint32_t heads = (uint32_t)p.heads, n = (uint32_t)p.n_tokens;
+  const uint32_t r = blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
+  const uint32_t i = r / heads, h = r % heads, hk = h / (uint32_t)p.group;
+  const bool in = i < (uint32_t)tokens;
+  const int lo = max(0, (int)i - p.window), n_sink = min(p.sinks, lo);
+  const int keys = in && i < n ? n_sink + (int)i - lo + 1 : 0;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int s = blockIdx.y; s < p.batch; s += gridDim.y) {
+    const int64_t bh = (int64_t)s * heads + h;
+    const uint4 q = keys > 0 ? prep_row(p.q, s, i, h, part) : zero;
+    const uint4 g = keys > 0 ? prep_row(p.d_o, s, i, h, part) : zero;
+    const float nl2 = keys > 0 ? -p.lse[bh * n + i] * kLog2e : __int_as_float(0xff800000);
+    float d = 0.f;
+#pragma unroll 1
+    for (int e0 = 0; __any_sync(0xffffffffu, e0 < keys); e0 += kFewStep) {
+      float sc[kFewStep], dp[kFewStep];
+#pragma unroll
+      for (int x = 0; x < kFewStep; ++x) {
+        const int e = e0 + x;
+        const uint32_t j = (uint32_t)(e < n_sink ? e : lo + e - n_sink);
+        sc[x] = dot8(q, e < keys ? prep_row(p.k, s, j, hk, part) : zero);
+        dp[x] = dot8(g, e < keys ? prep_row(p.v, s, j, hk, part) : zero);
+      }
+#pragma unroll
+      for (int x = 0; x < kFewStep; ++x) {
+        sc[x] = lanes_sum<G>(sc[x]);
+        dp[x] = lanes_sum<G>(dp[x]);
+        if (e0 + x < keys) d = fmaf(ex2_approx(fmaf(sc[x], p.scale_log2, nl2)), dp[x], d);
+      }
+    }
+    if (part == 0 && in) {
+      p.dvec[bh * p.pitch + i] = d;
+      p.nl2[bh * p.pitch + i] = nl2;
     }
   }
 }
@@ -836,15 +911,28 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
   p.nl2 = nl2;
   p.dvec = dvec;
   p.partial = reinterpret_cast<float*>(wsb + ws.partial_off);
-  p.scale = a.softmax_scale;
+  // Where every query sees one key, P is 1 whatever the scores are: dQ and dK are zero, and dP - D would
+  // leave them the rounding of two sums.
+  const bool one_key = a.n_tokens == 1 || (a.window == 0 && a.sinks == 0);
+  p.scale = one_key ? 0.f : a.softmax_scale;
   p.scale_log2 = a.softmax_scale * kLog2e;
-  const int64_t groups = ((int64_t)p.pitch * a.heads + kPrepRows - 1) / kPrepRows;   // of D / 8 threads
-  if (groups * kPrepRows >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
-  const dim3 prep_grid((unsigned)((groups * (D / 8) + 255) / 256), (unsigned)(a.batch < 65535 ? a.batch : 65535));
-  sink_prep_kernel<D><<<prep_grid, 256, 0, stream>>>(
-      static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.d_o), a.lse, a.o_strides[0],
-      a.o_strides[1], a.o_strides[2], a.do_strides[0], a.do_strides[1], a.do_strides[2], a.batch, a.n_tokens, a.heads,
-      p.pitch, nl2, dvec);
+  const auto tensor = [](const void* ptr, const int64_t st[3]) {
+    return PrepTensor{static_cast<const __nv_bfloat16*>(ptr), st[0], st[1], st[2]};
+  };
+  const PrepParams pp{tensor(a.q, a.q_strides), tensor(a.k, a.k_strides), tensor(a.v, a.v_strides),
+                      tensor(a.o, a.o_strides), tensor(a.d_o, a.do_strides), a.lse, nl2, dvec,
+                      a.batch, a.n_tokens, a.heads, p.group, p.pitch, a.window, a.sinks, p.scale_log2};
+  const auto grid = [&](int64_t rows) {                      // of groups of D / 8 threads
+    return dim3((unsigned)((rows * (D / 8) + 255) / 256), (unsigned)(a.batch < 65535 ? a.batch : 65535));
+  };
+  const int64_t rows = (int64_t)p.pitch * a.heads;
+  if (rows >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
+  // token i sees min(i, window + sinks) + 1 keys
+  const bool all_few = a.n_tokens <= kFewKeys || (int64_t)a.window + a.sinks < kFewKeys;
+  if (!all_few) sink_prep_kernel<D><<<grid((rows + kPrepRows - 1) / kPrepRows), 256, 0, stream>>>(pp);
+  // a long sequence's first rows keep <dO, O>: the launch would cost 7 us for one row in hundreds
+  const int few = all_few ? p.pitch : (a.n_tokens <= 8 * kFewKeys ? kFewKeys : 0);
+  if (few > 0) sink_few_kernel<D><<<grid((int64_t)few * a.heads), 256, 0, stream>>>(pp, few);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   BParams pq = p;
   pq.n_items = pq.n_main = a.batch * a.heads * p.tiles;

@@ -109,6 +109,22 @@ def test_sink_attention_strided_scaled_and_repeated():
     assert torch.equal(first.view(torch.int16), dpacked.view(torch.int16))
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("n,w,s", [(1, 0, 0), (1, 9, 4), (131, 0, 0)])
+def test_sink_attention_backward_of_one_visible_key(n, w, s, d):
+    """P is 1 whatever the scores are: the gradients of queries and keys are zero, not the rounding of
+    two equal sums."""
+    torch = torch_cuda()
+    q, k, v, g = (rand(i, 2, n, 2 if i in (1, 2) else 6, d)[0] for i in range(4))
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    dq, dk, dv = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    assert not dq.any() and not dk.any()
+    want = g.double().unflatten(2, (2, 3)).sum(3)
+    # three bf16 numbers summed in 32 bits, and one rounding
+    assert ((dv.double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-20 * g.double().abs().max()).all()
+
+
 # ------------------------------------------------------------------ single tokens over a cache
 
 DECODE_CASES = [
