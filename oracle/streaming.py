@@ -45,8 +45,8 @@ def sink_attention(q, k, v, window, sinks, scale=None):
     return o, lse, 1.02 * U * (np.abs(o) + mag) + 1e-6
 
 
-def sink_attention_backward(q, k, v, d_o, window, sinks, scale=None):
-    """(dq, dk, dv) and their bounds."""
+def sink_attention_backward(q, k, v, d_o, window, sinks, scale=None, rounded_o=True):
+    """(dq, dk, dv) and their bounds; rounded_o: D may be formed from the rounded O."""
     b, n, h, d = q.shape
     hk = k.shape[2]
     g = h // hk
@@ -65,7 +65,7 @@ def sink_attention_backward(q, k, v, d_o, window, sinks, scale=None):
             dv[s, :, e // g] += p.T @ gg
             # D is formed from the rounded O (off by U (|o| + p |v|)); dS and P are rounded
             off = (np.abs(gg) * (np.abs(o) + p @ np.abs(vv))).sum(-1, keepdims=True)
-            worst = np.abs(ds) + p * off
+            worst = np.abs(ds) + (p * off if rounded_o else 0.0)
             bq[s, :, e] = c * worst @ np.abs(kk)
             bk[s, :, e // g] += c * worst.T @ np.abs(qq)
             bv[s, :, e // g] += p.T @ np.abs(gg)

@@ -125,6 +125,22 @@ def test_sink_attention_backward_of_one_visible_key(n, w, s, d):
     assert ((dv.double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-20 * g.double().abs().max()).all()
 
 
+@pytest.mark.parametrize("n,h,hk,d,w,s", [(2, 4, 1, 64, 9, 0), (8, 4, 4, 32, 50, 3), (300, 6, 2, 128, 1, 0), (150, 4, 2, 64, 4, 3),
+                                          (131, 2, 1, 32, 2, 5)])
+def test_sink_attention_backward_of_few_visible_keys(n, h, hk, d, w, s):
+    """Up to eight keys a query: the rounding of O leaves the gradients alone."""
+    q, qf = rand(0, 2, n, h, d)
+    k, kf = rand(1, 2, n, hk, d)
+    v, vf = rand(2, 2, n, hk, d)
+    g, gf = rand(3, 2, n, h, d)
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    got = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    want, bounds = ref.sink_attention_backward(qf, kf, vf, gf, w, s, rounded_o=False)
+    for name, x, y, e in zip(("dq", "dk", "dv"), got, want, bounds):
+        close(x, y, e, name)
+
+
 # ------------------------------------------------------------------ single tokens over a cache
 
 DECODE_CASES = [
