@@ -858,8 +858,7 @@ int check_sink(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads,
   if (batch <= 0 || n_tokens <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0) return SA_ERR_INVALID_ARG;
   if (window < 0 || sinks < 0) return SA_ERR_INVALID_ARG;
   if (!head_dim_ok(head_dim) || sinks > sa::kMaxSinks || n_tokens > (1 << 24)) return SA_ERR_UNSUPPORTED;
-  // work items are counted in 32 bits, and so are the CTAs of the backward's first launch (one per
-  // 256 threads of head_dim / 8 per row)
+  // work items are counted in 32 bits
   const int64_t tiles = ((int64_t)n_tokens + 127) / 128;
   if ((int64_t)batch * heads > (1 << 24) || (int64_t)batch * heads * tiles > (1 << 27)) return SA_ERR_UNSUPPORTED;
   if (window > n_tokens - 1) window = n_tokens - 1;

@@ -213,7 +213,9 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, posit
                      interleaved: bool = False):
     """Returns (dq, dk, dq_weight, dk_weight); a weight given as None has the gradient None."""
     import torch
-    d, dev = q.shape[-1], q.device
+    _rows("q", q, _device())
+    _rows("k", k, _device())
+    d, dev = q.shape[3], q.device
     dq, dk = _like(q), _like(k)
     dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
     dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
@@ -280,7 +282,7 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int, softmax_scale: float | None 
 def sink_attn_bwd(q, k, v, o, lse, d_o, window: int, sinks: int, softmax_scale: float | None = None):
     """Returns (dq, dk, dv) from sink_attn_fwd's inputs and outputs."""
     import torch
-    _rows("q", q, _device())
+    _sink_inputs(q, k, v, _device())
     b, n, h, d = q.shape
     dq, dk, dv = _like(q), _like(k), _like(v)
     ws = torch.empty(sa_sink_attn_bwd_workspace_size(b, n, h, k.shape[2], d, window, sinks), dtype=torch.uint8,
@@ -391,6 +393,8 @@ def sa_sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, o
     """``lengths``: int32 [batch] on the device, tokens in each cache with the query's own key."""
     import torch
     dev = _device()
+    if len(k_cache.shape) != 4:
+        raise ValueError("k_cache: expected a bfloat16 [batch, capacity, kv_heads, head_dim] tensor")
     b, cap, hk, d = k_cache.shape
     qs, h = _token(q, b, d, dev), q.shape[2]
     _check("sa_sink_attn_decode", _lib().sa_sink_attn_decode(

@@ -432,6 +432,66 @@ def test_training_chain_against_differences():
         assert abs(num - got) <= 4 * ref.U * size, (trial, num, got, size)
 
 
+class Guard:
+    """bf16, fp32 or byte tensors inside poisoned buffers; `check` finds any byte changed around them."""
+
+    def __init__(self):
+        self.kept = []
+
+    def __call__(self, *shape, dtype=None, every_other_head=False):
+        torch = torch_cuda()
+        dtype = dtype or torch.bfloat16
+        full = list(shape)
+        if every_other_head:
+            full[2] *= 2
+        size = int(np.prod(full)) * torch.empty(0, dtype=dtype).element_size()
+        raw = torch.full((size + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+        t = raw[4096:4096 + size].view(dtype).view(full)
+        self.kept += [raw[:4096], raw[-4096:]] + ([t[:, :, 1::2]] if every_other_head else [])
+        return t[:, :, ::2] if every_other_head else t
+
+    def check(self):
+        torch = torch_cuda()
+        assert all(bool((x.contiguous().view(torch.uint8) == 0x5A).all()) for x in self.kept)
+
+
+@pytest.mark.parametrize("n,d", [(1, 128), (333, 64), (130, 32)])
+def test_nothing_is_written_around_the_outputs(n, d):
+    torch = torch_cuda()
+    b, h, hk, w, s = 2, 4, 2, 70, 9
+    f32 = torch.float32
+    x = {i: rand(i, b, n, h if i in (0, 3) else hk, d)[0] for i in range(5)}
+    q, k, v, g = x[0], x[1], x[2], x[3]
+    weight = torch.ones(d, dtype=f32, device="cuda")
+    freq = 100.0 ** -np.arange(d // 2)
+    guard = Guard()
+    qo, ko = guard(b, n, h, d, every_other_head=True), guard(b, n, hk, d, every_other_head=True)
+    sa.sa_qk_norm_rope_fwd(q, k, weight, weight, freq, None, qo, ko)
+    dqw, dkw = guard(d, dtype=f32), guard(d, dtype=f32)
+    dq, dk = guard(b, n, h, d, every_other_head=True), guard(b, n, hk, d, every_other_head=True)
+    ws = guard(sa.sa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8)
+    sa.sa_qk_norm_rope_bwd(q, k, g, x[4], weight, weight, freq, None, dq, dk, dqw, dkw, ws)
+    o, lse = guard(b, n, h, d, every_other_head=True), guard(b, h, n, dtype=f32)
+    sa.sa_sink_attn_fwd(q, k, v, w, s, o, lse)
+    dq, dk, dv = (guard(b, n, e, d, every_other_head=True) for e in (h, hk, hk))
+    ws = guard(sa.sa_sink_attn_bwd_workspace_size(b, n, h, hk, d, w, s), dtype=torch.uint8)
+    sa.sa_sink_attn_bwd(q, k, v, o, g, lse, w, s, dq, dk, dv, ws)
+    lengths = torch.tensor([n, max(0, n - 3)], dtype=torch.int32, device="cuda")
+    o, lse = guard(b, 1, h, d, every_other_head=True), guard(b, h, 1, dtype=f32)
+    sa.sa_sink_attn_decode(q[:, :1], k, v, lengths, w, s, o, lse)
+    cap = -(-n // 8) * 8
+    u8, bf16 = torch.uint8, torch.bfloat16
+    cache = sa.Cache4(guard(b, hk, cap, d // 2, dtype=u8), guard(b, hk, cap, d // 32, dtype=bf16),
+                      guard(b, hk, cap, d // 2, dtype=u8), guard(b, hk, cap, d // 32, dtype=bf16))
+    sa.sa_cache4_append(cache, k, v)
+    ko, vo = (guard(b, n, hk, d, every_other_head=True) for _ in range(2))
+    sa.sa_cache4_read(cache, None, ko, vo)
+    o, lse = guard(b, 1, h, d, every_other_head=True), guard(b, h, 1, dtype=f32)
+    sa.sa_sink_attn_decode_cache4(q[:, :1], cache, lengths, w, s, o, lse)
+    status_ok()
+    guard.check()
+
+
 def test_captured_and_replayed_on_new_inputs():
     """One CUDA graph of the whole chain, replayed after its inputs changed."""
     torch = torch_cuda()
