@@ -251,6 +251,9 @@ def sa_sink_attn_bwd_workspace_size(batch: int, n_tokens: int, heads: int, kv_he
     return int(out.value)
 
 
+_sink_bwd_bytes = functools.lru_cache(maxsize=64)(sa_sink_attn_bwd_workspace_size)
+
+
 def sa_sink_attn_bwd(q, k, v, o, d_o, lse, window: int, sinks: int, dq, dk, dv, workspace,
                      softmax_scale: float | None = None, stream=None) -> None:
     import torch
@@ -282,12 +285,20 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int, softmax_scale: float | None 
 def sink_attn_bwd(q, k, v, o, lse, d_o, window: int, sinks: int, softmax_scale: float | None = None):
     """Returns (dq, dk, dv) from sink_attn_fwd's inputs and outputs."""
     import torch
-    _sink_inputs(q, k, v, _device())
+    dev = _device()
+    ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
+    hk = k.shape[2]
+    os, gs = _rows("o", o, dev, q.shape), _rows("d_o", d_o, dev, q.shape)
+    lse_at = _flat("lse", lse, torch.float32, (b, h, n), dev)
     dq, dk, dv = _like(q), _like(k), _like(v)
-    ws = torch.empty(sa_sink_attn_bwd_workspace_size(b, n, h, k.shape[2], d, window, sinks), dtype=torch.uint8,
-                     device=q.device)
-    sa_sink_attn_bwd(q, k, v, o, d_o, lse, window, sinks, dq, dk, dv, ws, softmax_scale)
+    size = _sink_bwd_bytes(b, n, h, hk, d, window, sinks)
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
+    kv = _dense(k.shape)
+    _check("sa_sink_attn_bwd", _lib().sa_sink_attn_bwd(
+        *ptrs, o.data_ptr(), d_o.data_ptr(), lse_at, *strides, os, gs, b, n, h, hk, d, window, sinks,
+        _scale(softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dense(q.shape), kv, kv, ws.data_ptr(),
+        size, _stream(None, dev)))
     return dq, dk, dv
 
 
