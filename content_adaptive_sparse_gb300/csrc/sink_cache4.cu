@@ -16,13 +16,18 @@
 // shuffles.
 // The rounding takes no division: the approximate q = x (1 / s) is off by less than 2^-19, while a
 // quotient lies on a border (k + 1/2) or 2^-10 and more away from it, so q is first rounded to a
-// multiple of 2^-15 (adding 384, whose last place that is, and taking it off again), which puts
-// a border's quotient back on the border, and then to the nearest even integer. In the same way
+// multiple of 2^-15 (by adding 384, whose last place that is), which puts a border's quotient back on
+// the border, and then to the nearest even integer. In the same way
 // amax times fp32's 1 / 7 rounds to the bf16 number that amax / 7 does.
+//
+// Measured, K and V of 2 x 16384 tokens, 8 heads of 128 (172 MB): append 32.8 us (5.2 TB/s; 40 with one
+// element an instruction and a multiplication per address; bound by its instructions, ~115 a word),
+// read 28.0 us (6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
 #include "ptx_sm100.cuh"
 #include "sa_internal.h"
 
@@ -30,7 +35,6 @@ namespace sa {
 namespace {
 
 __device__ unsigned int g_cache_err;
-
 
 struct CParams {
   __nv_bfloat16* x[2];              // k, v rows (read by the append, written by the read)
@@ -41,42 +45,50 @@ struct CParams {
   int kv_heads, capacity;
   uint32_t words;                   // 32-bit words of one sequence's rows
   uint32_t div_m, div_s;            // r / kv_heads = r * div_m >> div_s for r < 2^31
-  uint32_t step_i, step_h;          // 256 words on: step_i tokens and step_h heads
+  // 256 words on: step_i tokens and step_h heads, and one token on where that passes the last head;
+  // the same in elements of x and in cache rows
+  uint32_t step_i, step_h;
+  int64_t x_step[2], x_wrap[2], row_step, row_wrap;
 };
 
 __host__ __device__ constexpr int bit_of(int u) { return 8 * (u >> 2) + 4 * ((u & 3) >> 1) + 16 * (u & 1); }
 
 // A thread's words: run c and word t of it, the same for all its words (256 words are whole
-// rows), and per word token i of the call and head h.
-template <int D>
+// rows), and per word token i of the call and head h. Addresses are found by additions.
+template <int D, int M>
 struct Place {
   static constexpr uint32_t NG = D / 32;
   uint32_t c, t, h, i;
-  __device__ Place(const CParams& p, uint32_t w) {
+  __nv_bfloat16* x;                 // the word's elements
+  int64_t row;                      // the cache row of slot `start` 0
+  __device__ Place(const CParams& p, uint32_t s, uint32_t w) {
     t = w & 3;
     c = (w >> 2) % NG;
     const uint32_t r = (w >> 2) / NG;
     i = (uint32_t)(((uint64_t)r * p.div_m) >> p.div_s);
     h = r - i * (uint32_t)p.kv_heads;
+    x = p.x[M] + s * p.sb[M] + i * p.sn[M] + h * p.sh[M] + 32 * c + 8 * t;
+    row = ((int64_t)s * p.kv_heads + h) * p.capacity + i;
   }
   __device__ __forceinline__ void next(const CParams& p) {
     i += p.step_i;
     h += p.step_h;
+    x += p.x_step[M];
+    row += p.row_step;
     if (h >= (uint32_t)p.kv_heads) {
       h -= (uint32_t)p.kv_heads;
       ++i;
+      x += p.x_wrap[M];
+      row += p.row_wrap;
     }
   }
-  __device__ __forceinline__ __nv_bfloat16* x(const CParams& p, int m, uint32_t s) const {
-    return p.x[m] + s * p.sb[m] + i * p.sn[m] + h * p.sh[m] + 32 * c + 8 * t;
-  }
-  // the cache row, or -1 (out of range: reported; start < 0: the sequence is left out, not reported)
-  __device__ __forceinline__ int64_t row(const CParams& p, uint32_t s, int start) const {
-    if (start < 0) return -1;
-    const uint32_t slot = (uint32_t)start + i;       // below 2^32: start and i are below 2^31
-    if (slot < (uint32_t)p.capacity) return ((int64_t)s * p.kv_heads + h) * p.capacity + slot;
+  // whether the word's row is in the cache (past it: reported; start < 0: the sequence is left out, not
+  // reported)
+  __device__ __forceinline__ bool in(const CParams& p, int start) const {
+    if (start < 0) return false;
+    if ((uint32_t)start + i < (uint32_t)p.capacity) return true;   // the sum is below 2^32
     if (t == 0 && c == 0) atomicOr(&g_cache_err, kErrBadIndex);
-    return -1;
+    return false;
   }
 };
 
@@ -105,13 +117,18 @@ __device__ __forceinline__ uint32_t quantise(const uint4& r, __nv_bfloat16& scal
   uint32_t word = 0u;
   if (!(sc < 5.421010862427522e-20f)) {
     const float inv = rcp_approx(sc);                // NaN: the codes are not used
+    // x / s + 384 to a multiple of 2^-15, then, with 8 more, to an integer in the last bits of 1.5 x 2^23;
+    // the numbers' low halves are the codes, pair e's at nibble e
+    const uint64_t inv2 = f2::pack(inv, inv), grid = f2::pack(384.f, 384.f), last = f2::pack(12582536.f, 12582536.f);
+    uint32_t pair[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float x = __uint_as_float(u & 1 ? v[u >> 1] & 0xffff0000u : v[u >> 1] << 16);
-      // to a multiple of 2^-15, then to an integer, stored + 8 in the last bits of 1.5 x 2^23 + code
-      const float e = __fadd_rn(__fadd_rn(x * inv, 384.f), -384.f);
-      word |= (__float_as_uint(__fadd_rn(e, 12582920.f)) & 15u) << bit_of(u);
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t x = f2::pack(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
+      float lo, hi;
+      f2::unpack(f2::add(f2::fma(x, inv2, grid), last), lo, hi);
+      pair[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
     }
+    word = ((pair[3] * 16u + pair[2]) * 16u + pair[1]) * 16u + pair[0];
     if (amax >= 0x7f80u) word = 0x88888888u;
   } else {
     // scales below 2^-64, the last ones subnormal: 1 / s could overflow, and s can be so coarse that
@@ -129,13 +146,14 @@ __device__ __forceinline__ uint32_t quantise(const uint4& r, __nv_bfloat16& scal
 
 template <int D, int M, int kWords>
 __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint32_t w, int start) {
-  const Place<D> first(p, w);
+  constexpr uint32_t NG = D / 32;
+  const Place<D, M> first(p, s, w);
   uint4 v[kWords];
-  Place<D> at = first;
+  Place<D, M> at = first;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {                 // whole runs: four threads in or out together
     v[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (w + 256u * k < p.words) v[k] = *reinterpret_cast<const uint4*>(at.x(p, M, s));
+    if (w + 256u * k < p.words) v[k] = *reinterpret_cast<const uint4*>(at.x);
     at.next(p);
   }
   at = first;
@@ -143,12 +161,10 @@ __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint3
   for (int k = 0; k < kWords; ++k) {
     __nv_bfloat16 scale;
     const uint32_t word = quantise(v[k], scale);
-    if (w + 256u * k < p.words) {
-      const int64_t row = at.row(p, s, start);
-      if (row >= 0) {
-        p.codes[M][row * (D / 8) + at.t * Place<D>::NG + at.c] = word;
-        if (at.t == 0) p.scales[M][row * Place<D>::NG + at.c] = scale;
-      }
+    if (w + 256u * k < p.words && at.in(p, start)) {
+      const int64_t row = at.row + start;
+      p.codes[M][row * (D / 8) + at.t * NG + at.c] = word;
+      if (at.t == 0) p.scales[M][row * NG + at.c] = scale;
     }
     at.next(p);
   }
@@ -156,20 +172,19 @@ __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint3
 
 template <int D, int M, int kWords>
 __device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_t w, int start) {
-  const Place<D> first(p, w);
+  constexpr uint32_t NG = D / 32;
+  const Place<D, M> first(p, s, w);
   uint32_t word[kWords];
   __nv_bfloat16 scale[kWords];
-  Place<D> at = first;
+  Place<D, M> at = first;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {
     word[k] = 0x88888888u;                           // rows outside the cache read as zeros
     scale[k] = __float2bfloat16_rn(0.f);
-    if (w + 256u * k < p.words) {
-      const int64_t row = at.row(p, s, start);
-      if (row >= 0) {
-        word[k] = p.codes[M][row * (D / 8) + at.t * Place<D>::NG + at.c];
-        scale[k] = p.scales[M][row * Place<D>::NG + at.c];
-      }
+    if (w + 256u * k < p.words && at.in(p, start)) {
+      const int64_t row = at.row + start;
+      word[k] = p.codes[M][row * (D / 8) + at.t * NG + at.c];
+      scale[k] = p.scales[M][row * NG + at.c];
     }
     at.next(p);
   }
@@ -187,14 +202,15 @@ __device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_
       const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), off), s2);
       v[e] = *reinterpret_cast<const uint32_t*>(&y);
     }
-    if (w + 256u * k < p.words) *reinterpret_cast<uint4*>(at.x(p, M, s)) = make_uint4(v[0], v[1], v[2], v[3]);
+    if (w + 256u * k < p.words) *reinterpret_cast<uint4*>(at.x) = make_uint4(v[0], v[1], v[2], v[3]);
     at.next(p);
   }
 }
 
-// One CTA per 256 kWords words of a sequence's keys or values (K and V interleaved in y).
+// One CTA per 256 kWords words of a sequence's keys or values (K and V interleaved in y). The append's
+// registers are held to five CTAs an SM (35.0 -> 32.8 us below).
 template <int D, bool READ, int kWords>
-__global__ void __launch_bounds__(256) cache4_kernel(const __grid_constant__ CParams p) {
+__global__ void __launch_bounds__(256, !READ && kWords > 1 ? 5 : 1) cache4_kernel(const __grid_constant__ CParams p) {
   const uint32_t w = blockIdx.x * (256u * kWords) + threadIdx.x, s = blockIdx.y >> 1;
   const int start = p.start ? p.start[s] : 0;
   if constexpr (READ) {
@@ -211,6 +227,12 @@ int launch(const Cache4Args& a, CParams& p, cudaStream_t stream) {
   const uint32_t rows = 256 / (D / 8);               // rows in 256 words
   p.step_i = rows / (uint32_t)a.kv_heads;
   p.step_h = rows % (uint32_t)a.kv_heads;
+  for (int m = 0; m < 2; ++m) {
+    p.x_step[m] = p.step_i * p.sn[m] + p.step_h * p.sh[m];
+    p.x_wrap[m] = p.sn[m] - a.kv_heads * p.sh[m];
+  }
+  p.row_step = (int64_t)p.step_h * p.capacity + p.step_i;
+  p.row_wrap = 1 - (int64_t)a.kv_heads * p.capacity;
   // Four words a thread, all loaded before the first is worked on, where that still gives every SM
   // several CTAs (K and V of 2 x 16384 tokens: append 49 -> 40 us, read 41 -> 28 us); one word a thread
   // in smaller calls, whose time is one thread's latency (64 sequences of one token: append 3.2 ->
