@@ -75,7 +75,7 @@ struct Cfg {
   static constexpr int N1 = D < 128 ? 3 : (KV ? 2 : 1);
   static constexpr int SLOT0 = TILE + (KV ? 1024 : 0);   // B0, then -LSE log2(e) [128] and D [128]
   static constexpr int RING = N0 * SLOT0 + N1 * TILE;
-  // then OUT KB per compute warp, from which the outputs leave
+  // then OUT KB per compute warp, from which the outputs leave, 16 OUT columns at a time
   static constexpr int OUT = KV && D == 64 ? 2 : 1;
   static constexpr int SMEM_NEED = 1024 + FIX * 2 * TILE + RING + kComputeWarps * 1024 * OUT;
   // more than half an SM's shared memory: one CTA (and its 512 TMEM columns) per SM
@@ -446,58 +446,59 @@ struct Compute {
     if (lane == 0) mbar_arrive(bar);
   }
 
-  // An item's rows, this warp's share of the columns: 16 at a time, through 1 KB of shared memory
-  // (32-byte rows, 32B swizzle) and a TMA store, which drops rows past the sequence. (Stored straight
-  // from the registers, 32 rows in 32 lines per instruction, an item's output took as long as two
-  // steps.)
+  // An item's rows, this warp's share of the columns: 16 OUT at a time, through OUT KB of shared
+  // memory (rows of 32 OUT bytes, swizzled over them) and a TMA store, which drops rows past the
+  // sequence. (Stored straight from the registers, 32 rows in 32 lines per instruction, an item's
+  // output took as long as two steps; TMA takes a cycle per row whatever its width.)
   __device__ __forceinline__ bool write(const Item& it, int n) const {
     const int tok0 = it.tile * kTile + 32 * quarter, tok = tok0 + lane;
     const bool sum = KV && it.slot >= 0 && tok < p.sinks;   // an fp32 partial sum (its bf16 row is written after)
     const bool rows = it.slot <= 0;                          // a sink chunk has sums only
-    const uint32_t srow = smem_u32(out) + 32u * lane;
+    const uint32_t srow = smem_u32(out) + 32u * C::OUT * lane;
+    const uint32_t turn = C::OUT == 2 ? (uint32_t)(lane >> 1) & 3u : (uint32_t)(lane >> 2) & 1u;
     if (!__all_sync(0xffffffffu, wait_bar(&bars.acc_full, (uint32_t)n & 1u, abort_flag))) return false;
     tc_fence_after();
     constexpr int N = (KV ? 2 : 1) * (D / 16), W = kComputeWarps / 4;   // chunks; warps that share them
 #pragma unroll 1
-    for (int c0 = part; c0 < N; c0 += C::OUT * W) {
+    for (int c0 = C::OUT * part; c0 < N; c0 += C::OUT * W) {
       if (rows) {
-        if (lane < C::OUT) bulk_wait_group_read<0>();
+        if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
       }
-#pragma unroll 1
-      for (int o = 0; o < C::OUT && c0 + o * W < N; ++o) {
-        const int c = c0 + o * W, m = c / (D / 16), col = 16 * (c % (D / 16));
-        const float f = m ? 1.f : p.scale;
-        uint32_t w[16];
-        tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)col, w);
-        tmem_ld_wait<16>(w);
+      const int m = c0 / (D / 16), col = 16 * (c0 % (D / 16));   // OUT pieces of one tensor
+      const float f = m ? 1.f : p.scale;
+      uint32_t w[C::OUT][16];
+#pragma unroll
+      for (int o = 0; o < C::OUT; ++o)
+        tmem_ld_x16(base + (m ? C::COL_ACC1 : C::COL_ACC0) + (uint32_t)(col + 16 * o), w[o]);
+#pragma unroll
+      for (int o = 0; o < C::OUT; ++o) {
+        tmem_ld_wait<16>(w[o]);
         if (sum) {
           const int64_t bh = (int64_t)it.s * p.kv_heads + it.head;
-          float* prow = p.partial + (((bh * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D + col;
+          float* prow = p.partial + (((bh * (p.n_chunks + 1) + it.slot) * 2 + m) * p.sinks + tok) * D + col + 16 * o;
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
             *reinterpret_cast<float4*>(prow + e) =
-                make_float4(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f, __uint_as_float(w[e + 2]) * f,
-                            __uint_as_float(w[e + 3]) * f);
+                make_float4(__uint_as_float(w[o][e]) * f, __uint_as_float(w[o][e + 1]) * f,
+                            __uint_as_float(w[o][e + 2]) * f, __uint_as_float(w[o][e + 3]) * f);
         }
         if (rows) {
           uint32_t pk[8];
 #pragma unroll
           for (int e = 0; e < 16; e += 2)
-            pk[e >> 1] = pack_bf16x2(__uint_as_float(w[e]) * f, __uint_as_float(w[e + 1]) * f);
-          const uint32_t swz = (uint32_t)((lane >> 2) & 1) << 4;
-          st_shared_v4(srow + 1024u * o + swz, pk[0], pk[1], pk[2], pk[3]);
-          st_shared_v4(srow + 1024u * o + (swz ^ 16u), pk[4], pk[5], pk[6], pk[7]);
+            pk[e >> 1] = pack_bf16x2(__uint_as_float(w[o][e]) * f, __uint_as_float(w[o][e + 1]) * f);
+          st_shared_v4(srow + (((2u * o) ^ turn) << 4), pk[0], pk[1], pk[2], pk[3]);
+          st_shared_v4(srow + (((2u * o + 1u) ^ turn) << 4), pk[4], pk[5], pk[6], pk[7]);
         }
       }
       if (rows) {
         fence_proxy_async_smem();
         __syncwarp();
-        // lane o sends chunk o
-        const int c = c0 + lane * W, m = c / (D / 16);
-        if (lane < C::OUT && c < N && tok0 < p.n_tokens)
-          tma_store_4d(m ? to1 : to0, out + 1024 * lane, 16 * (c % (D / 16)), it.head, tok0, it.s);
-        if (lane < C::OUT) bulk_commit_group();
+        if (lane == 0 && tok0 < p.n_tokens) {
+          tma_store_4d(m ? to1 : to0, out, col, it.head, tok0, it.s);
+          bulk_commit_group();
+        }
       }
     }
     return true;
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     compute<D, KV>(p, &to0, &to1, bars, sRing, tmem, &abort_flag);
     // this warp's stores are complete before the CTA may exit
-    if ((threadIdx.x & 31) < C::OUT) bulk_wait_group<0>();
+    if ((threadIdx.x & 31) == 0) bulk_wait_group<0>();
     __syncwarp();
   }
   tc_fence_before();
@@ -873,11 +874,11 @@ int launch(const SinkArgs& a, const BParams& p, cudaStream_t stream) {
   if (!map(&tq, a.q, a.heads, a.q_strides) || !map(&tk, a.k, a.kv_heads, a.k_strides) ||
       !map(&tv, a.v, a.kv_heads, a.v_strides) || !map(&tdo, a.d_o, a.heads, a.do_strides))
     return SA_ERR_UNSUPPORTED;
-  // outputs: boxes of 32 rows by 16 elements
+  // outputs: boxes of 32 rows by 16 OUT elements
   CUtensorMap to0, to1;
   auto omap = [&](CUtensorMap* m, const void* base, int heads, const int64_t st[3]) {
-    return encode_bhnd_map(m, base, a.batch, a.n_tokens, heads, D, st[0], st[1], st[2], 16, 32,
-                           CU_TENSOR_MAP_SWIZZLE_32B);
+    return encode_bhnd_map(m, base, a.batch, a.n_tokens, heads, D, st[0], st[1], st[2], 16 * C::OUT, 32,
+                           C::OUT == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
   };
   if (KV ? !omap(&to0, a.dk, a.kv_heads, a.dk_strides) || !omap(&to1, a.dv, a.kv_heads, a.dv_strides)
          : !omap(&to0, a.dq, a.heads, a.dq_strides) || !omap(&to1, a.dq, a.heads, a.dq_strides))

@@ -210,7 +210,7 @@ __device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_
 // One CTA per 256 kWords words of a sequence's keys or values (K and V interleaved in y). The append's
 // registers are held to five CTAs an SM (35.0 -> 32.8 us below).
 template <int D, bool READ, int kWords>
-__global__ void __launch_bounds__(256, !READ && kWords > 1 ? 5 : 1) cache4_kernel(const __grid_constant__ CParams p) {
+__global__ void __launch_bounds__(256, READ ? 8 : (kWords > 1 ? 5 : 1)) cache4_kernel(const __grid_constant__ CParams p) {
   const uint32_t w = blockIdx.x * (256u * kWords) + threadIdx.x, s = blockIdx.y >> 1;
   const int start = p.start ? p.start[s] : 0;
   if constexpr (READ) {
