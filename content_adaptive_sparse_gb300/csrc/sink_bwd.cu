@@ -94,7 +94,9 @@ struct BParams {
   int batch, n_tokens, heads, kv_heads, group;   // group: query heads per key head
   int tiles, pitch;                 // 128-row tiles per sequence; padded tokens = 128 tiles
   int window, sinks;
-  int n_items, n_main;              // items; the first n_main are ordinary, the rest sink chunks
+  // items: (rank, sequence, head of the stationary rows); dK / dV: ranks from `tiles` on are sink chunks
+  int ranks;
+  int step_head, step_s, step_rank; // one item of every CTA, in these digits
   int chunk_tiles, n_chunks;        // query tiles per sink chunk, sink chunks per (sequence, head)
   int far_tile;                     // first query tile whose window misses key tile 0
   const float* nl2;                 // [batch][heads][pitch]: -LSE log2(e); -inf past the sequence
@@ -141,42 +143,61 @@ struct Item {
   int slot;                         // dK / dV: partial-sum slot of the sinks' rows (-1: none)
 };
 
+// A CTA's items in turn, found by additions (the divisions of an item's number took every role some
+// hundred cycles between items).
 template <bool KV>
-__device__ __forceinline__ Item decode_item(const BParams& p, int k) {
-  Item it;
-  it.slot = -1;
-  if constexpr (!KV) {
-    const int bh = k % (p.batch * p.heads);
-    it.head = bh % p.heads;
-    it.s = bh / p.heads;
-    it.tile = p.tiles - 1 - k / (p.batch * p.heads);   // the last tiles see the most keys
-    it.tile0 = max(0, it.tile * kTile - p.window) / kTile;
-    it.n_sink = p.sinks > 0 && it.tile0 > 0 ? 1 : 0;
-    it.per = it.tile - it.tile0 + 1;
-    it.steps = it.n_sink + it.per;
-  } else {
-    const bool main = k < p.n_main;
-    const int r = main ? k : k - p.n_main;
-    const int bh = r % (p.batch * p.kv_heads);
-    const int rank = r / (p.batch * p.kv_heads);
-    it.head = bh % p.kv_heads;
-    it.s = bh / p.kv_heads;
-    it.n_sink = 0;
-    if (main) {
-      it.tile = rank;
-      it.tile0 = rank;
-      it.per = min(p.tiles - 1, (rank * kTile + kTile - 1 + p.window) / kTile) - rank + 1;
-      if (rank == 0 && p.n_chunks > 0) it.slot = 0;
-    } else {
-      it.tile = 0;
-      it.tile0 = p.far_tile + rank * p.chunk_tiles;
-      it.per = min(p.tiles, it.tile0 + p.chunk_tiles) - it.tile0;
-      it.slot = 1 + rank;
-    }
-    it.steps = it.per * p.group;
+struct Walk {
+  int head, s, rank;
+  __device__ explicit Walk(const BParams& p) {
+    const int heads = KV ? p.kv_heads : p.heads, k = blockIdx.x;
+    head = k % heads;
+    s = k / heads % p.batch;
+    rank = k / heads / p.batch;
   }
-  return it;
-}
+  __device__ __forceinline__ bool more(const BParams& p) const { return rank < p.ranks; }
+  __device__ __forceinline__ void next(const BParams& p) {
+    head += p.step_head;
+    s += p.step_s;
+    rank += p.step_rank;
+    if (head >= (KV ? p.kv_heads : p.heads)) {
+      head -= KV ? p.kv_heads : p.heads;
+      ++s;
+    }
+    if (s >= p.batch) {
+      s -= p.batch;
+      ++rank;
+    }
+  }
+  __device__ __forceinline__ Item item(const BParams& p) const {
+    Item it;
+    it.slot = -1;
+    it.head = head;
+    it.s = s;
+    it.n_sink = 0;
+    if constexpr (!KV) {
+      it.tile = p.tiles - 1 - rank;                      // the last tiles see the most keys
+      it.tile0 = max(0, it.tile * kTile - p.window) / kTile;
+      it.n_sink = p.sinks > 0 && it.tile0 > 0 ? 1 : 0;
+      it.per = it.tile - it.tile0 + 1;
+      it.steps = it.n_sink + it.per;
+    } else {
+      if (rank < p.tiles) {
+        it.tile = rank;
+        it.tile0 = rank;
+        it.per = min(p.tiles - 1, (rank * kTile + kTile - 1 + p.window) / kTile) - rank + 1;
+        if (rank == 0 && p.n_chunks > 0) it.slot = 0;
+      } else {
+        const int chunk = rank - p.tiles;
+        it.tile = 0;
+        it.tile0 = p.far_tile + chunk * p.chunk_tiles;
+        it.per = min(p.tiles, it.tile0 + p.chunk_tiles) - it.tile0;
+        it.slot = 1 + chunk;
+      }
+      it.steps = it.per * p.group;
+    }
+    return it;
+  }
+};
 
 // Moving rows of an item's steps, in order: head and tile.
 template <bool KV>
@@ -236,8 +257,8 @@ __device__ void loader(const BParams& p, const CUtensorMap* ta0, const CUtensorM
   using C = Cfg<D, KV>;
   int g0 = 0, g1 = 0, n = 0;
   bool ok = true;
-  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
-    const Item it = decode_item<KV>(p, k);
+  for (Walk<KV> walk(p); ok && walk.more(p); walk.next(p), ++n) {
+    const Item it = walk.item(p);
     if constexpr (B0) {
       // the S and dP of the item before in this buffer have read its stationary tiles
       const int fb = n % C::FIX;
@@ -372,8 +393,8 @@ __device__ void issuer(const BParams& p, int role, Bars& bars, uint8_t* sFix, ui
                         make_smem_desc(ring1, C::CHUNK, C::ATOM, C::SWZ)};
   int g = 0, n = 0;
   bool ok = true;
-  for (int k = blockIdx.x; ok && k < p.n_items; k += gridDim.x, ++n) {
-    const int steps = decode_item<KV>(p, k).steps;
+  for (Walk<KV> walk(p); ok && walk.more(p); walk.next(p), ++n) {
+    const int steps = walk.item(p).steps;
     if (role == 2 || (KV && role == 1)) {
       for (int j = 0; ok && j < steps; ++j, ++g) ok = KV && role == 1 ? I.acc1(g, j > 0) : I.acc0(g, j > 0);
       if (ok) mma_commit(&bars.acc_full);
@@ -597,9 +618,9 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
                          sRing + C::RING + 1024 * C::OUT * (4 * part + quarter), f2::pack(p.scale_log2, p.scale_log2)};
   int g = 0, n = 0;
   Item it, prev;
-  for (int k = blockIdx.x; k < p.n_items; k += gridDim.x, ++n) {
+  for (Walk<KV> walk(p); walk.more(p); walk.next(p), ++n) {
     prev = it;
-    it = decode_item<KV>(p, k);
+    it = walk.item(p);
     const int tok = it.tile * kTile + row;
     float nl2 = 0.f, dval = 0.f;
     if constexpr (!KV) {
@@ -865,7 +886,7 @@ Chunks sink_chunks(int tiles, int window, int sinks) {
 }
 
 template <int D, bool KV>
-int launch(const SinkArgs& a, const BParams& p, cudaStream_t stream) {
+int launch(const SinkArgs& a, BParams p, int ranks, cudaStream_t stream) {
   using C = Cfg<D, KV>;
   CUtensorMap tq, tk, tv, tdo;
   auto map = [&](CUtensorMap* m, const void* base, int heads, const int64_t st[3]) {
@@ -887,7 +908,13 @@ int launch(const SinkArgs& a, const BParams& p, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
   const int sm_count = current_sm_count();
-  const int grid = p.n_items < sm_count ? p.n_items : sm_count;
+  const int heads = KV ? a.kv_heads : a.heads;
+  const int64_t items = (int64_t)ranks * a.batch * heads;
+  const int grid = items < sm_count ? (int)items : sm_count;
+  p.ranks = ranks;
+  p.step_head = grid % heads;
+  p.step_s = grid / heads % a.batch;
+  p.step_rank = grid / heads / a.batch;
   if (KV) kern<<<grid, kThreads, C::SMEM, stream>>>(tk, tv, tq, tdo, to0, to1, p);
   else kern<<<grid, kThreads, C::SMEM, stream>>>(tq, tdo, tk, tv, to0, to1, p);
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
@@ -935,16 +962,12 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
   const int few = all_few ? p.pitch : (a.n_tokens <= 8 * kFewKeys ? kFewKeys : 0);
   if (few > 0) sink_few_kernel<D><<<grid((int64_t)few * a.heads), 256, 0, stream>>>(pp, few);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
-  BParams pq = p;
-  pq.n_items = pq.n_main = a.batch * a.heads * p.tiles;
-  int st = launch<D, false>(a, pq, stream);
+  int st = launch<D, false>(a, p, p.tiles, stream);
   if (st != SA_OK) return st;
   const Chunks c = sink_chunks(p.tiles, a.window, a.sinks);
   p.far_tile = c.far_tile;
   p.chunk_tiles = c.tiles_each;
   p.n_chunks = c.count;
-  p.n_main = a.batch * a.kv_heads * p.tiles;
-  p.n_items = p.n_main + a.batch * a.kv_heads * c.count;
   p.out0 = static_cast<__nv_bfloat16*>(a.dk);
   p.out1 = static_cast<__nv_bfloat16*>(a.dv);
   for (int m = 0; m < 2; ++m) {
@@ -953,7 +976,7 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
     p.os_n[m] = st[1];
     p.os_h[m] = st[2];
   }
-  st = launch<D, true>(a, p, stream);
+  st = launch<D, true>(a, p, p.tiles + c.count, stream);
   if (st != SA_OK || c.count == 0) return st;
   const int64_t quads = (int64_t)a.batch * a.kv_heads * 2 * a.sinks * (D / 4);
   sink_reduce_kernel<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p, D);
