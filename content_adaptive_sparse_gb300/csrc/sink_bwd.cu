@@ -33,6 +33,11 @@
 //   warps 4-19  compute: warp w reads TMEM lane quarter w % 4 (one stationary row per thread) and
 //               columns 32 c .. 32 c + 31 of a step, c = w / 4 - 1; at an item's end they write
 //               its rows. An item's S and dP run under the previous item's output.
+//
+// Measured: 16321 tokens, 16 / 4 heads of 128, window 2047: 762 us (28 + 295 + 445: 1.06 PFLOP/s over the
+// edges, 1.48 with S and dP counted twice; tensor pipe 65 % busy, the rest the chain S, P, dS, product).
+// 4 x 8192 tokens, 12 heads of 64, window 511: 290 us (23 + 117 + 160); an item is five steps, and about
+// 3000 cycles, of 13000, pass between two items' steps.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -797,11 +802,14 @@ __global__ void __launch_bounds__(256) sink_prep_kernel(const __grid_constant__ 
   }
 }
 
-// The same for tokens below `tokens`, which see at most kFewKeys keys, with D = sum of P dP. O is stored
-// in bf16, and in <dO, O> its rounding, 2^-9 of |dO| |O|, goes into every dS of the row alike: into dQ
-// times the mean of the visible keys. That is little where many keys are seen (their mean is short,
-// and dS has a rounding of its own); at two keys it took dQ's error from 0.0024 to 0.0046 of its size.
-constexpr int kFewKeys = 8, kFewStep = 4;
+// The same for tokens below `tokens` with D = sum of P dP. O is stored in bf16, and in <dO, O> its
+// rounding, 2^-9 of |dO| |O|, goes into every dS of the row alike: into dQ times the mean of the visible
+// keys. That is little where many keys are seen (their mean is short, and dS has a rounding of its
+// own); at two keys it took dQ's error from 0.0024 to 0.0046 of its size, at nine to 0.0027. So it is
+// done where no query sees more than kFewKeys keys (16K tokens of 16 heads of 128 at eight: 210 -> 322
+// us), and for the first kFewTokens of sequences of up to 8 kFewTokens, where the launch is short
+// beside the others; in longer ones it would cost 7 us for one row in hundreds.
+constexpr int kFewKeys = 8, kFewTokens = 32, kFewStep = 4;
 template <int D>
 __global__ void __launch_bounds__(256) sink_few_kernel(const __grid_constant__ PrepParams p, int tokens) {
   constexpr int G = D / 8;
@@ -956,10 +964,9 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
   const int64_t rows = (int64_t)p.pitch * a.heads;
   if (rows >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
   // token i sees min(i, window + sinks) + 1 keys
-  const bool all_few = a.n_tokens <= kFewKeys || (int64_t)a.window + a.sinks < kFewKeys;
+  const bool all_few = a.n_tokens <= kFewTokens || (int64_t)a.window + a.sinks < kFewKeys;
   if (!all_few) sink_prep_kernel<D><<<grid((rows + kPrepRows - 1) / kPrepRows), 256, 0, stream>>>(pp);
-  // a long sequence's first rows keep <dO, O>: the launch would cost 7 us for one row in hundreds
-  const int few = all_few ? p.pitch : (a.n_tokens <= 8 * kFewKeys ? kFewKeys : 0);
+  const int few = all_few ? p.pitch : (a.n_tokens <= 8 * kFewTokens ? kFewTokens : 0);
   if (few > 0) sink_few_kernel<D><<<grid((int64_t)few * a.heads), 256, 0, stream>>>(pp, few);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   int st = launch<D, false>(a, p, p.tiles, stream);

@@ -126,9 +126,9 @@ def test_sink_attention_backward_of_one_visible_key(n, w, s, d):
 
 
 @pytest.mark.parametrize("n,h,hk,d,w,s", [(2, 4, 1, 64, 9, 0), (8, 4, 4, 32, 50, 3), (300, 6, 2, 128, 1, 0), (150, 4, 2, 64, 4, 3),
-                                          (131, 2, 1, 32, 2, 5)])
+                                          (131, 2, 1, 32, 2, 5), (32, 3, 3, 64, 31, 0), (23, 4, 2, 128, 6, 9)])
 def test_sink_attention_backward_of_few_visible_keys(n, h, hk, d, w, s):
-    """Up to eight keys a query: the rounding of O leaves the gradients alone."""
+    """Up to eight keys a query, or 32 tokens: the rounding of O leaves the gradients alone."""
     q, qf = rand(0, 2, n, h, d)
     k, kf = rand(1, 2, n, hk, d)
     v, vf = rand(2, 2, n, hk, d)
@@ -430,6 +430,73 @@ def test_training_chain_against_differences():
         # much again: along a random direction their sum is far below 4 x 2^-8 of the gradient's norm
         size = np.sqrt((grad ** 2).sum() + (gw[0] ** 2).sum() + (gw[1] ** 2).sum())
         assert abs(num - got) <= 4 * ref.U * size, (trial, num, got, size)
+
+
+def _ends(x, head, tail):
+    """The first `head` and last `tail` tokens of a tensor, as one short sequence."""
+    torch = torch_cuda()
+    return torch.cat((x[:, :head], x[:, -tail:]), 1).contiguous()
+
+
+def test_attention_over_more_than_2_31_elements():
+    """The last queries and keys of a sequence whose tensors pass 32-bit offsets see what those of a
+    short one with the same ends see."""
+    torch = torch_cuda()
+    n, h, d, w, s, tail = (1 << 20) + 77, 17, 128, 100, 4, 500
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v, g = (torch.randn(1, n, h, d, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    freq = 1000.0 ** -np.arange(d // 2)
+    positions = torch.arange(n, device="cuda", dtype=torch.int32)[None]
+    qr, kr = sa.qk_norm_rope_fwd(q, k, None, None, freq, positions)
+    small = [_ends(x, s, tail) for x in (q, k, v, g)]
+    want_q, want_k = sa.qk_norm_rope_fwd(small[0], small[1], None, None, freq, _ends(positions, s, tail))
+    assert torch.equal(_ends(qr, s, tail), want_q) and torch.equal(_ends(kr, s, tail), want_k)
+    o, lse = sa.sink_attn_fwd(qr, kr, v, w, s)
+    grads = sa.sink_attn_bwd(qr, kr, v, o, lse, g, w, s)
+    status_ok()
+    qf, kf, vf, gf = (bf16_to_f64(x) for x in (want_q, want_k, small[2], small[3]))
+    of, lf, ob = ref.sink_attention(qf, kf, vf, w, s)
+    rows = slice(-tail + 2 * w, None)                 # past the seam and its queries' windows
+    close(o[:, -tail + 2 * w:], of[:, rows], ob[:, rows], "o")
+    close(lse[:, :, -tail + 2 * w:], lf[:, :, rows], LSE_TOL, "lse")
+    want, bounds = ref.sink_attention_backward(qf, kf, vf, gf, w, s)
+    for name, x, y, e in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(x[:, -tail + 2 * w:], y[:, rows], e[:, rows], name)
+
+
+def test_caches_of_more_than_2_31_elements():
+    torch = torch_cuda()
+    b, hk, h, d, w, s, tail = 3, 4, 8, 128, 40, 4, 64
+    cap = 1 << 22
+    ends = [rand(i, b, s + tail, hk, d)[0] for i in (1, 2)]
+    q, qf = rand(3, b, 1, h, d)
+    lengths = torch.full((b,), cap, dtype=torch.int32, device="cuda")
+    first = torch.zeros(b, dtype=torch.int32, device="cuda")
+    kf, vf = (bf16_to_f64(x) for x in ends)
+    cache = sa.cache4_alloc(b, cap, hk, d)
+    assert cache.k_codes.numel() > 1 << 31
+    sa.cache4_append(cache, *(x[:, :s] for x in ends), first)
+    sa.cache4_append(cache, *(x[:, s:] for x in ends), first + (cap - tail))
+    back = sa.cache4_read(cache, first + (cap - tail), tail)
+    o, lse = sa.sink_attn_decode_cache4(q, cache, lengths, w, s)
+    status_ok()
+    k4, v4 = (ref.values(*ref.quantise(x)) for x in (kf, vf))
+    for x, y in zip(back, (k4, v4)):
+        assert np.array_equal(bf16_to_f64(x), ref.bf16_round(y[:, s:]))
+    of, lf, ob = ref.sink_decode(qf, k4, v4, [s + tail] * b, w, s)
+    close(o, of, ob, "o")
+    close(lse, lf, LSE_TOL, "lse")
+    del cache, back
+    k, v = (torch.empty(b, cap, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 1 << 32
+    for x, e in ((k, ends[0]), (v, ends[1])):
+        x[:, :s] = e[:, :s]
+        x[:, -tail:] = e[:, s:]
+    o, lse = sa.sink_attn_decode(q, k, v, lengths, w, s)
+    status_ok()
+    of, lf, ob = ref.sink_decode(qf, kf, vf, [s + tail] * b, w, s)
+    close(o, of, ob, "o")
+    close(lse, lf, LSE_TOL, "lse")
 
 
 class Guard:
