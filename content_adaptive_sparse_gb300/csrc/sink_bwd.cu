@@ -34,8 +34,8 @@
 //               columns 32 c .. 32 c + 31 of a step, c = w / 4 - 1; at an item's end they write
 //               its rows. An item's S and dP run under the previous item's output.
 //
-// Measured: 16321 tokens, 16 / 4 heads of 128, window 2047: 762 us (28 + 295 + 445: 1.06 PFLOP/s over the
-// edges, 1.48 with S and dP counted twice; tensor pipe 65 % busy, the rest the chain S, P, dS, product).
+// Measured: 16321 tokens, 16 / 4 heads of 128, window 2047: 762 us (28 + 295 + 445: 0.84 PFLOP/s over the
+// edges, 1.18 with S and dP counted twice; tensor pipe 65 % busy, the rest the chain S, P, dS, product).
 // 4 x 8192 tokens, 12 heads of 64, window 511: 290 us (23 + 117 + 160); an item is five steps, and about
 // 3000 cycles, of 13000, pass between two items' steps.
 #include <cuda.h>
