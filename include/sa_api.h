@@ -358,7 +358,8 @@ int sa_build_mask_from_bytes(const sa_mask_params* params, const uint8_t* h_byte
  *                read before the call returns. rotary_dim: a multiple of 16, 0 .. head_dim (0: no
  *                rotation, h_inv_freq may be NULL); later elements are normed only.
  *   interleaved: 0 pairs element p with p + rotary_dim / 2, 1 pairs 2p with 2p + 1.
- *   d_positions: int32 [batch][n_tokens], any values, or NULL for 0 .. n_tokens - 1. */
+ *   d_positions: int32 [batch][n_tokens], any values, or NULL for 0 .. n_tokens - 1.
+ * SA_ERR_UNSUPPORTED from 2^30 tokens on (of all sequences together). */
 int sa_qk_norm_rope_fwd(const void* q, const void* k, const int64_t q_strides[3], const int64_t k_strides[3],
                         int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
                         const float* d_q_weight, const float* d_k_weight, float eps, const double* h_inv_freq,
@@ -394,7 +395,9 @@ int sa_sink_attn_bwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t hea
                                     int32_t window, int32_t sinks, size_t* h_bytes);
 
 /* Gradients dq, dk, dv of sum(d_o * o) of sa_sink_attn_fwd (formulas as in sa_attn_bwd), from its
- * inputs and its outputs o and lse. Every tensor has strides of its own. The same bits on every run.
+ * inputs and its outputs o and lse. Every tensor has strides of its own. The same bits on every run;
+ * dq and dk are exact zeros where every query sees one key (one token, or window 0 without sinks).
+ * SA_ERR_UNSUPPORTED if heads times n_tokens (rounded up to 128) reaches 2^31.
  * workspace: device memory, 256-byte aligned, of at least sa_sink_attn_bwd_workspace_size bytes. */
 int sa_sink_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* d_o, const float* lse,
                      const int64_t q_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
