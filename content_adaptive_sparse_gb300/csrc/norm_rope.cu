@@ -413,8 +413,8 @@ int launch(RopeParams& p, const NormRopeArgs& a, cudaStream_t stream) {
   per = per < groups ? per : groups;
   p.heads_per_unit = per * RPW;
   p.chunks = (groups + per - 1) / per;
-  const int64_t units = tokens * p.chunks;
-  if (units >= (int64_t)1 << 30) return SA_ERR_UNSUPPORTED;
+  const int64_t units = tokens * p.chunks;             // below 2^31: tokens are below 2^30, and where there are
+                                                       // several chunks a token, units are at most warps + tokens
   int64_t grid = (units + kWarps - 1) / kWarps;
   if (grid > ctas) grid = ctas;
   if (grid > kNormRopeMaxCtas) grid = kNormRopeMaxCtas;

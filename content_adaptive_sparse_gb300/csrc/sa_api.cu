@@ -827,7 +827,7 @@ int norm_rope_args(const void* q, const void* k, const int64_t qs[3], const int6
     if (!(h_inv_freq[i] >= 0.0 && h_inv_freq[i] < 6.28)) return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return SA_ERR_UNSUPPORTED;
   if (!strides_ok(qs) || !strides_ok(ks) || !strides_ok(qos) || !strides_ok(kos)) return SA_ERR_UNSUPPORTED;
-  if ((int64_t)heads + kv_heads > 65536) return SA_ERR_UNSUPPORTED;
+  if ((int64_t)heads + kv_heads > 65536 || (int64_t)batch * n_tokens >= 1 << 30) return SA_ERR_UNSUPPORTED;
   memset(&a, 0, sizeof(a));
   a.q = q;
   a.k = k;
@@ -1042,6 +1042,8 @@ int sa_sink_attn_bwd(const void* q, const void* k, const void* v, const void* o,
     return SA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
   if ((st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks)) != SA_OK) return st;
+  // a sequence's rows, padded to whole tiles, are counted in 32 bits
+  if (((int64_t)n_tokens + 127) / 128 * 128 * heads >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
   if (!device_ok()) return SA_ERR_CUDA;
   sa::SinkArgs a;
   memset(&a, 0, sizeof(a));

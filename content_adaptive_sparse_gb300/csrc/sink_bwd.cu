@@ -962,7 +962,6 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
     return dim3((unsigned)((rows * (D / 8) + 255) / 256), (unsigned)(a.batch < 65535 ? a.batch : 65535));
   };
   const int64_t rows = (int64_t)p.pitch * a.heads;
-  if (rows >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
   // token i sees min(i, window + sinks) + 1 keys
   const bool all_few = a.n_tokens <= kFewTokens || (int64_t)a.window + a.sinks < kFewKeys;
   if (!all_few) sink_prep_kernel<D><<<grid((rows + kPrepRows - 1) / kPrepRows), 256, 0, stream>>>(pp);

@@ -68,7 +68,7 @@ def test_norm_rope_refusals(lib, backward):
         assert c.with_() == INVALID, f
     c.keep[31] = 0.5
     for bad in (dict(d=48, rotary=32), dict(d=256), dict(rotary=24), dict(q=A + 8), dict(ko=A + 2), dict(qs=S3(2048, 256, 60)),
-                dict(kos=S3(1024, 0, 64))):
+                dict(kos=S3(1024, 0, 64)), dict(batch=1 << 15, n=1 << 15), dict(heads=65536)):
         assert c.with_(**bad) == UNSUPPORTED, bad
     if backward:
         assert c.with_() == CAPACITY
@@ -109,7 +109,8 @@ def test_sink_attention_refusals(lib, backward):
     if backward:
         for bad in (dict(d_o=0), dict(dq=0), dict(dk=0), dict(dv=0),                     dict(ws=0), dict(lse=0)):
             assert c.with_(**bad) == INVALID, bad
-        for bad in (dict(d_o=A + 8), dict(dq=A + 8), dict(dk=A + 8), dict(dv=A + 8), dict(ws=A + 128), dict(dvs=S3(1, 1, 1))):
+        for bad in (dict(d_o=A + 8), dict(dq=A + 8), dict(dk=A + 8), dict(dv=A + 8), dict(ws=A + 128), dict(dvs=S3(1, 1, 1)),
+                    dict(batch=1, heads=2048, n=(1 << 20) - 127)):
             assert c.with_(**bad) == UNSUPPORTED, bad
 
 
