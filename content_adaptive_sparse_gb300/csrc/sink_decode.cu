@@ -24,7 +24,7 @@
 // it by 2^8, which one vote shows.
 //
 // Measured: 64 sequences of up to 16000 tokens, 16 / 4 heads of 128, window 4095, bf16: 73 us, 6.7 TB/s,
-// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 89 us, 3.1 TB/s: the
+// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 86 us, 3.3 TB/s: the
 // instructions that unpack codes (57 % of the ALU pipe) and 1.7 waves of CTAs. One sequence of 700
 // tokens, 12 heads of 64, window 511: 4.4 us, a launch, one load and the join.
 #include <cooperative_groups.h>
@@ -102,12 +102,15 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   return mbar_wait(bar, parity, abort_flag, &g_decode_err, kErrTimeout);
 }
 
-// The rows that a sequence's query sees, cut into stages of R: first those of the sinks that the
-// window does not hold, then the window's, this CTA's share being [begin, end).
-template <int R, bool Q4>
+// The rows that a sequence's query sees, cut into units of 16 rows a warp: first those of the sinks that
+// the window does not hold, then the window's, this CTA's share being [begin, end). A stage is up to
+// TILES units.
+constexpr int kUnit = 16 * kWarps;
+
+template <int TILES, bool Q4>
 struct Rows {
   int len, lo, n_sink;              // tokens; first token of the window; sinks before it
-  int sink_stages, first, begin, end;   // first: token of the window's first stage row
+  int sink_units, first, begin, end;    // first: token of the window's first unit
 
   __device__ static Rows of(const DParams& p, int s, int rank, int ranks) {
     Rows r;
@@ -115,37 +118,42 @@ struct Rows {
     r.lo = max(0, r.len - 1 - p.window);
     r.n_sink = min(p.sinks, r.lo);
     r.first = Q4 ? (r.lo & ~7) : r.lo;          // bulk copies start at a multiple of 16 bytes
-    r.sink_stages = (r.n_sink + R - 1) / R;
-    const int total = r.sink_stages + (r.len - r.first + R - 1) / R;
-    const int per = (total + ranks - 1) / ranks;
-    r.begin = min(total, rank * per);
-    r.end = min(total, r.begin + per);
+    r.sink_units = (r.n_sink + kUnit - 1) / kUnit;
+    const int total = r.sink_units + (r.len - r.first + kUnit - 1) / kUnit;
+    // shares that differ by one unit at most (whole stages of two: 89 us where these take 86)
+    r.begin = (int)((int64_t)total * rank / ranks);
+    r.end = (int)((int64_t)total * (rank + 1) / ranks);
     return r;
   }
-  // stage j: its first row's token, and the tokens [lo, hi) of it that are seen
-  __device__ __forceinline__ void stage(int j, int& tok, int& vlo, int& vhi) const {
-    if (j < sink_stages) {
-      tok = j * R;
+  // The stage that starts at unit j: its first row's token and the tokens [vlo, vhi) of it that are
+  // seen; returns the next stage's unit.
+  __device__ __forceinline__ int stage(int j, int& tok, int& vlo, int& vhi) const {
+    const bool sinks = j < sink_units;
+    const int next = TILES == 1 ? j + 1 : min(j + TILES, sinks ? min(sink_units, end) : end);
+    if (sinks) {
+      tok = j * kUnit;
       vlo = 0;
       vhi = n_sink;
     } else {
-      tok = first + (j - sink_stages) * R;
+      tok = first + (j - sink_units) * kUnit;
       vlo = lo;
       vhi = len;
     }
+    vhi = min(vhi, tok + (next - j) * kUnit);
+    return next;
   }
 };
 
 template <int D, bool Q4, int NQ>
 __device__ void producer(const DParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Bars& bars, uint8_t* ring,
-                         const Rows<Cfg<D, Q4, NQ>::ROWS, Q4>& r, int s, int hk, volatile int* abort_flag) {
+                         const Rows<Cfg<D, Q4, NQ>::TILES, Q4>& r, int s, int hk, volatile int* abort_flag) {
   using C = Cfg<D, Q4, NQ>;
   int g = 0;
-  for (int j = r.begin; j < r.end; ++j, ++g) {
+  for (int j = r.begin; j < r.end; ++g) {
     const int st = g % C::STAGES;
     if (g >= C::STAGES && !wait_bar(&bars.empty[st], (uint32_t)(g / C::STAGES - 1) & 1u, abort_flag)) break;
     int tok, vlo, vhi;
-    r.stage(j, tok, vlo, vhi);
+    j = r.stage(j, tok, vlo, vhi);
     uint8_t* stage = ring + st * C::STAGE;
     if constexpr (Q4) {
       const int rows = min(C::ROWS, (vhi - tok + 7) & ~7);          // the capacity is a multiple of 8
@@ -265,7 +273,7 @@ __device__ __forceinline__ void load_scales(uint32_t addr, float (&sc)[NG]) {
 
 // 4-bit form. m, l: per query head 8 q + 2 t + e of lane (g, t), m the same in all g, l this lane's rows.
 template <int D, int NQ>
-__device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Rows<Cfg<D, true, NQ>::ROWS, true>& r, int s,
+__device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Rows<Cfg<D, true, NQ>::TILES, true>& r, int s,
                           int h0, int n_q, float (&o)[NQ * D / 16][4], float (&m)[2 * NQ], float (&l)[2 * NQ],
                           volatile int* abort_flag) {
   using C = Cfg<D, true, NQ>;
@@ -313,23 +321,23 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
   const int gr = (g >> 1) + 4 * (g & 1);
   // this lane's places in a stage: key words, scales of rows g, value words
   const uint32_t ring0 = smem_u32(ring);
-  const uint32_t at_k = (uint32_t)((16 * C::TILES * warp + gr) * (D / 2) + t * (D / 8));
-  const uint32_t at_s = (uint32_t)(C::CODES + (16 * C::TILES * warp + gr) * NG * 2);
-  const uint32_t at_v = (uint32_t)(C::CODES + C::SCALES + (16 * C::TILES * warp + t) * (D / 2) + (g >> 1) * (D / 8));
+  const uint32_t at_k = (uint32_t)((16 * warp + gr) * (D / 2) + t * (D / 8));
+  const uint32_t at_s = (uint32_t)(C::CODES + (16 * warp + gr) * NG * 2);
+  const uint32_t at_v = (uint32_t)(C::CODES + C::SCALES + (16 * warp + t) * (D / 2) + (g >> 1) * (D / 8));
   const uint32_t sel = g & 1 ? 0x7531u : 0x6420u;
-  for (int j = r.begin, n = 0; j < r.end; ++j, ++n) {
+  for (int j = r.begin, n = 0; j < r.end; ++n) {
     const int st = n % C::STAGES;
     int tok, vlo, vhi;
-    r.stage(j, tok, vlo, vhi);
+    j = r.stage(j, tok, vlo, vhi);
     if (!__all_sync(0xffffffffu, wait_bar(&bars.full[st], (uint32_t)(n / C::STAGES) & 1u, abort_flag))) return;
     const uint32_t stage = ring0 + (uint32_t)(st * C::STAGE);
 #pragma unroll 1
     for (int x = 0; x < C::TILES; ++x) {
-      const int t0 = tok + 16 * (C::TILES * warp + x);
+      const int t0 = tok + kUnit * x + 16 * warp;
       if (t0 >= vhi || t0 + 16 <= vlo) continue;
-      const uint32_t kb = stage + at_k + (uint32_t)(x * 16 * (D / 2));
-      const uint32_t sb = stage + at_s + (uint32_t)(x * 16 * NG * 2);
-      const uint32_t vb = stage + at_v + (uint32_t)(x * 16 * (D / 2));
+      const uint32_t kb = stage + at_k + (uint32_t)(x * kUnit * (D / 2));
+      const uint32_t sb = stage + at_s + (uint32_t)(x * kUnit * NG * 2);
+      const uint32_t vb = stage + at_v + (uint32_t)(x * kUnit * (D / 2));
       // ---- scores of rows g and g + 8
       uint32_t w0[NG], w1[NG];
       lds_words<NG>(kb, w0);
@@ -432,7 +440,7 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
 
 // bf16 form. m, l: per query head g + 8 h of lane (g, t), l this lane's columns.
 template <int D>
-__device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Rows<64, false>& r, int s, int h0, int n_q,
+__device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Rows<1, false>& r, int s, int h0, int n_q,
                            float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
   using C = Cfg<D, false, 2>;
   constexpr int KS = D / 16;
@@ -454,10 +462,10 @@ __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Ro
     }
   }
   const uint32_t ring0 = smem_u32(ring);
-  for (int j = r.begin, n = 0; j < r.end; ++j, ++n) {
+  for (int j = r.begin, n = 0; j < r.end; ++n) {
     const int st = n % C::STAGES;
     int tok, vlo, vhi;
-    r.stage(j, tok, vlo, vhi);
+    j = r.stage(j, tok, vlo, vhi);
     if (!__all_sync(0xffffffffu, wait_bar(&bars.full[st], (uint32_t)(n / C::STAGES) & 1u, abort_flag))) return;
     const int t0 = tok + 16 * warp;
     if (t0 < vhi && t0 + 16 > vlo) {
@@ -583,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     fence_mbar_init();
   }
   __syncthreads();
-  const auto r = Rows<C::ROWS, Q4>::of(p, s, rank, ranks);
+  const auto r = Rows<C::TILES, Q4>::of(p, s, rank, ranks);
   float o[C::NT][4];
   constexpr int NM = Q4 ? 2 * NQ : 2;                       // query heads of a lane
   float m[NM], l[NM];
@@ -755,7 +763,7 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   const int64_t seen = (int64_t)a.window + 1 + a.sinks < a.capacity ? (int64_t)a.window + 1 + a.sinks : a.capacity;
   const int sm_count = current_sm_count();
   int ranks = 1;
-  while (ranks < kMaxCluster && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * 64 * ranks) ranks *= 2;
+  while (ranks < kMaxCluster && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * kUnit * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)ranks, (unsigned)(a.kv_heads * p.head_groups), (unsigned)a.batch);
