@@ -7,9 +7,9 @@
 // A CTA takes one (sequence, key head, up to 16 query heads) and a share of its rows; the CTAs of a
 // cluster split the rows of one (sequence, key head) and join their partial results over
 // distributed shared memory, so there is one launch, no workspace and no atomics.
-//   warp 4      lane 0 fills a ring of 64-row stages: 16-row TMA boxes (bf16) or bulk copies of the
-//               contiguous 4-bit rows and scales
-//   warps 0-3   16 rows of every stage each, with their own running maximum and sum, on mma.sync
+//   warp 4      lane 0 fills a ring of stages: 64 rows in 16-row TMA boxes (bf16), or bulk copies of 128
+//               contiguous 4-bit rows and their scales
+//   warps 0-3   16 rows of every 64 of a stage each, with their own running maximum and sum, on mma.sync
 //               m16n8k16 (a tcgen05 tile would need 64 or 128 rows of queries, and the tensor
 //               work is small beside the reads)
 // bf16: S = Q K^T and O += P V with the query heads as the 16 rows.
