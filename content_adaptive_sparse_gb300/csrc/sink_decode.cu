@@ -757,7 +757,7 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   // CTAs per (sequence, key head), while each has a stage of rows when the cache is full: bf16 until
   // there are 1.5 per SM (its loads then saturate the memory; 64 sequences of 4 key heads: 73.8 us
   // with one, 79.6 with two, 88 with four), 4 bits, bound by its instructions, until there are 6 (32
-  // sequences of 4 key heads: 113 us with two, 99.7 with four, 94.4 with eight; the last two are 3.4
+  // sequences of 4 key heads: 107 us with two, 95 with four, 86 with eight; the last two are 3.4
   // and 6.7 per SM).
   const int64_t base = (int64_t)a.batch * a.kv_heads * p.head_groups;
   const int64_t seen = (int64_t)a.window + 1 + a.sinks < a.capacity ? (int64_t)a.window + 1 + a.sinks : a.capacity;
