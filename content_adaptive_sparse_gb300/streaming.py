@@ -18,6 +18,7 @@ import numpy as np
 _P, _I32, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
 _S3 = ctypes.c_int64 * 3
 _LIB = None
+torch = None                  # imported by the first call (`_bind`): a tensor has come with it by then
 
 
 def declare(lib) -> None:
@@ -83,16 +84,27 @@ def _dense(shape) -> _S3:
     return _s3((n * h * d, h * d, d))
 
 
+def _bind() -> None:
+    """Looks up once what every call needs: a lookup is as long as a check."""
+    global torch, _BF16, _initialized, _current_device, _current_stream
+    import torch as module
+    _BF16 = module.bfloat16
+    _initialized = module.cuda.is_initialized
+    # torch.cuda.current_device() and current_stream().cuda_stream without their Python objects
+    _current_device, _current_stream = module._C._cuda_getDevice, module._C._cuda_getCurrentRawStream
+    torch = module                # last: another thread may be looking
+
+
 def _device() -> int:
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2   # no tensor is there
+    if torch is None:
+        _bind()
+    return _current_device() if _initialized() else -2   # no tensor is there
 
 
 def _rows(name: str, t, device: int, shape=None) -> _S3:
     """Strides of a bf16 [batch, tokens, heads, head_dim] tensor on the current device."""
-    import torch
     st = t.stride()
-    if t.dtype is not torch.bfloat16 or len(st) != 4:
+    if t.dtype is not _BF16 or len(st) != 4:
         raise ValueError(f"{name}: expected a bfloat16 [batch, tokens, heads, head_dim] tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -132,8 +144,7 @@ def _scale(softmax_scale, d: int) -> float:
 def _stream(stream, device: int) -> int:
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device)   # current_stream().cuda_stream without its object
+    return _current_stream(device)
 
 
 def _workspace(ws, device: int) -> tuple[int, int]:
@@ -145,14 +156,12 @@ def _workspace(ws, device: int) -> tuple[int, int]:
 
 
 def _like(t):
-    import torch
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 # ------------------------------------------------------------------ norm and rotation of queries and keys
 
 def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev):
-    import torch
     qs, ks = _rows("q", q, dev), _rows("k", k, dev)
     _same_sequence(q, k)
     b, n, h, d = q.shape
@@ -188,7 +197,6 @@ def sa_qk_norm_rope_bwd_workspace_size(head_dim: int) -> int:
 def sa_qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, positions, dq, dk, dq_weight, dk_weight,
                         workspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """Gradients of sa_qk_norm_rope_fwd; the weights' (fp32 [head_dim]) may be None."""
-    import torch
     dev = _device()
     ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev)
     d = (q.shape[3],)
@@ -212,9 +220,9 @@ def qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions=None, eps: fl
 def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, positions=None, eps: float = 1e-6,
                      interleaved: bool = False):
     """Returns (dq, dk, dq_weight, dk_weight); a weight given as None has the gradient None."""
-    import torch
-    _rows("q", q, _device())
-    _rows("k", k, _device())
+    at = _device()
+    _rows("q", q, at)
+    _rows("k", k, at)
     d, dev = q.shape[3], q.device
     dq, dk = _like(q), _like(k)
     dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
@@ -234,7 +242,6 @@ def _sink_inputs(q, k, v, dev):
 
 
 def sa_sink_attn_fwd(q, k, v, window: int, sinks: int, o, lse, softmax_scale: float | None = None, stream=None) -> None:
-    import torch
     dev = _device()
     ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
@@ -256,7 +263,6 @@ _sink_bwd_bytes = functools.lru_cache(maxsize=64)(sa_sink_attn_bwd_workspace_siz
 
 def sa_sink_attn_bwd(q, k, v, o, d_o, lse, window: int, sinks: int, dq, dk, dv, workspace,
                      softmax_scale: float | None = None, stream=None) -> None:
-    import torch
     dev = _device()
     ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
@@ -270,7 +276,6 @@ def sa_sink_attn_bwd(q, k, v, o, d_o, lse, window: int, sinks: int, dq, dk, dv, 
 def sink_attn_fwd(q, k, v, window: int, sinks: int, softmax_scale: float | None = None):
     """Returns (o, lse): causal attention over the `window` keys before each query, itself and the
     first `sinks` tokens."""
-    import torch
     dev = _device()
     ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
@@ -284,7 +289,6 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int, softmax_scale: float | None 
 
 def sink_attn_bwd(q, k, v, o, lse, d_o, window: int, sinks: int, softmax_scale: float | None = None):
     """Returns (dq, dk, dv) from sink_attn_fwd's inputs and outputs."""
-    import torch
     dev = _device()
     ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
@@ -327,22 +331,20 @@ def cache4_alloc(batch: int, capacity: int, kv_heads: int, head_dim: int, device
 
 def _cache4(cache, dev):
     """Addresses of a cache's four tensors, and (batch, kv_heads, capacity, head_dim)."""
-    import torch
     kc, ks, vc, vs = cache
     codes = kc.shape
     if len(codes) != 4:
         raise ValueError("cache: expected codes of shape [batch, kv_heads, capacity, head_dim / 2]")
     b, hk, cap, half = codes
     scales = (b, hk, cap, half // 16)
-    u8, bf16 = torch.uint8, torch.bfloat16
-    return (_flat("k_codes", kc, u8, codes, dev), _flat("k_scales", ks, bf16, scales, dev),
-            _flat("v_codes", vc, u8, codes, dev), _flat("v_scales", vs, bf16, scales, dev)), (b, hk, cap, 2 * half)
+    u8 = torch.uint8
+    return (_flat("k_codes", kc, u8, codes, dev), _flat("k_scales", ks, _BF16, scales, dev),
+            _flat("v_codes", vc, u8, codes, dev), _flat("v_scales", vs, _BF16, scales, dev)), (b, hk, cap, 2 * half)
 
 
 def sa_cache4_append(cache: Cache4, k, v, start=None, stream=None) -> None:
     """Writes rows start[s] .. start[s] + n - 1 of every sequence (``start``: int32 [batch] on the
     device, None for 0; a negative one leaves its sequence out)."""
-    import torch
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
     ks = _rows("k", k, dev)
@@ -356,7 +358,6 @@ def sa_cache4_append(cache: Cache4, k, v, start=None, stream=None) -> None:
 
 def sa_cache4_read(cache: Cache4, start, k, v, stream=None) -> None:
     """Reads rows start[s] .. start[s] + n - 1 of every sequence into k and v."""
-    import torch
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
     ks = _rows("k", k, dev)
@@ -374,7 +375,6 @@ def cache4_append(cache: Cache4, k, v, start=None) -> None:
 
 def cache4_read(cache: Cache4, start, n_tokens: int):
     """Returns (k, v), bfloat16 [batch, n_tokens, kv_heads, head_dim]."""
-    import torch
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
     k = torch.empty((b, n_tokens, hk, d), dtype=torch.bfloat16, device=cache[0].device)
@@ -395,14 +395,12 @@ def _token(q, b: int, d: int, dev: int) -> _S3:
 
 
 def _token_outputs(q):
-    import torch
     return _like(q), torch.empty((q.shape[0], q.shape[2], 1), dtype=torch.float32, device=q.device)
 
 
 def sa_sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, o, lse,
                         softmax_scale: float | None = None, stream=None) -> None:
     """``lengths``: int32 [batch] on the device, tokens in each cache with the query's own key."""
-    import torch
     dev = _device()
     if len(k_cache.shape) != 4:
         raise ValueError("k_cache: expected a bfloat16 [batch, capacity, kv_heads, head_dim] tensor")
@@ -417,7 +415,6 @@ def sa_sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, o
 
 def sa_sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: int, o, lse,
                                softmax_scale: float | None = None, stream=None) -> None:
-    import torch
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
     qs, h = _token(q, b, d, dev), q.shape[2]
@@ -429,7 +426,6 @@ def sa_sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: in
 
 def sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, softmax_scale: float | None = None):
     """One token per sequence over a bf16 cache; returns (o [batch, 1, heads, head_dim], lse)."""
-    import torch
     dev = _device()
     if len(k_cache.shape) != 4:
         raise ValueError("k_cache: expected a bfloat16 [batch, capacity, kv_heads, head_dim] tensor")
@@ -446,7 +442,6 @@ def sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, soft
 
 def sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: int, softmax_scale: float | None = None):
     """One token per sequence over a 4-bit cache; returns (o [batch, 1, heads, head_dim], lse)."""
-    import torch
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
     qs = _token(q, b, d, dev)
