@@ -24,8 +24,8 @@
 // it by 2^8, which one vote shows.
 //
 // Measured: 64 sequences of up to 16000 tokens, 16 / 4 heads of 128, window 4095, bf16: 73 us, 6.7 TB/s,
-// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 86 us, 3.3 TB/s: the
-// instructions that unpack codes (57 % of the ALU pipe) and 1.7 waves of CTAs. One sequence of 700
+// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 77 us, 3.6 TB/s: the
+// instructions that unpack codes (372 per 16 rows) and 1.7 waves of CTAs. One sequence of 700
 // tokens, 12 heads of 64, window 511: 4.4 us, a launch, one load and the join.
 #include <cooperative_groups.h>
 #include <cuda.h>
@@ -92,6 +92,9 @@ struct DParams {
   int64_t q_sb, q_sh, o_sb, o_sh;
   int heads, kv_heads, group, head_groups, capacity, window, sinks;
   float scale_log2;
+  // 0x000f000f, not known to the compiler: (w & mask) | bits is one instruction, but only with one constant
+  // in it (4 bits: 220 -> 158 ALU instructions per 16 rows, 86 -> 77 us)
+  uint32_t code_mask;
 };
 
 struct Bars {
@@ -198,22 +201,23 @@ __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r
 }
 
 // Codes n + 8 (nibble S of the low and of the high half-word, 1 .. 15) as a bf16 pair of n: over
-// the mantissa of 128 they are 136 + n. All exact.
+// the mantissa of 128 they are 136 + n. All exact. low: 0x000f000f.
 template <int S>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  const uint32_t x = ((w >> (4 * S)) & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t low) {
+  const uint32_t x = ((w >> (4 * S)) & low) | 0x43004300u;
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The four pairs of a code word as f16 pairs of n: its ten bits of mantissa take two of the four
 // nibbles where they stand, as 1032 + n and 1024 + 16 (n + 8), which one fma turns into n. All exact.
-__device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[4]) {
+// high: 0x00f000f0.
+__device__ __forceinline__ void code_halves(uint32_t w, uint32_t low, uint32_t high, uint32_t (&h)[4]) {
   const __half2 one = __floats2half2_rn(-1032.f, -1032.f), off = __floats2half2_rn(-72.f, -72.f);
   const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t x = ((k ? w >> 8 : w) & 0x000f000fu) | 0x64006400u, y = ((k ? w >> 8 : w) & 0x00f000f0u) | 0x64006400u;
+    const uint32_t x = ((k ? w >> 8 : w) & low) | 0x64006400u, y = ((k ? w >> 8 : w) & high) | 0x64006400u;
     const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&x), one);
     const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&y), sixteenth, off);
     h[2 * k] = *reinterpret_cast<const uint32_t*>(&a);
@@ -325,6 +329,7 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
   const uint32_t at_s = (uint32_t)(C::CODES + (16 * warp + gr) * NG * 2);
   const uint32_t at_v = (uint32_t)(C::CODES + C::SCALES + (16 * warp + t) * (D / 2) + (g >> 1) * (D / 8));
   const uint32_t sel = g & 1 ? 0x7531u : 0x6420u;
+  const uint32_t low = p.code_mask, high = p.code_mask << 4;
   for (int j = r.begin, n = 0; j < r.end; ++n) {
     const int st = n % C::STAGES;
     int tok, vlo, vhi;
@@ -349,8 +354,8 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         uint32_t a[4], b[4];
-        code_halves(w0[i], a);
-        code_halves(w1[i], b);
+        code_halves(w0[i], low, high, a);
+        code_halves(w1[i], low, high, b);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           float acc[4];
@@ -422,8 +427,8 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         const uint32_t x0 = __byte_perm(w[0][i], w[1][i], sel), x1 = __byte_perm(w[2][i], w[3][i], sel);
-        const uint32_t a0[4] = {code_pair<0>(x0), code_pair<1>(x0), code_pair<0>(x1), code_pair<1>(x1)};
-        const uint32_t a1[4] = {code_pair<2>(x0), code_pair<3>(x0), code_pair<2>(x1), code_pair<3>(x1)};
+        const uint32_t a0[4] = {code_pair<0>(x0, low), code_pair<1>(x0, low), code_pair<0>(x1, low), code_pair<1>(x1, low)};
+        const uint32_t a1[4] = {code_pair<2>(x0, low), code_pair<3>(x0, low), code_pair<2>(x1, low), code_pair<3>(x1, low)};
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           const uint32_t b0 = transpose8(pack_bf16x2(sc[q][0] * v0[i], sc[q][1] * v0[i]));
@@ -751,6 +756,7 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.sinks = a.sinks;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+  p.code_mask = 0x000f000fu;
   const auto kern = sink_decode_kernel<D, Q4, NQ>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
