@@ -24,7 +24,7 @@
 // it by 2^8, which one vote shows.
 //
 // Measured: 64 sequences of up to 16000 tokens, 16 / 4 heads of 128, window 4095, bf16: 73 us, 6.7 TB/s,
-// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 77 us, 3.6 TB/s: the
+// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 74 us, 3.8 TB/s: the
 // instructions that unpack codes (372 per 16 rows) and 1.7 waves of CTAs. One sequence of 700
 // tokens, 12 heads of 64, window 511: 4.4 us, a launch, one load and the join.
 #include <cooperative_groups.h>
@@ -59,7 +59,8 @@ constexpr int kMaxCluster = 8;
 template <int D, bool Q4, int NQ>
 struct Cfg {
   static constexpr int Q = 8 * NQ;                     // query heads
-  // 16-row tiles of a consumer warp per stage (4 bits: 89 us with two in three stages, 94.9 with one in six)
+  // 16-row tiles of a consumer warp per stage (4 bits: 77 us with two in three stages, 84 with
+  // one in six; 74 with the two unrolled)
   static constexpr int TILES = Q4 ? 2 : 1;
   static constexpr int ROWS = 16 * kWarps * TILES;     // cache rows per stage
   static constexpr int CH = D >= 64 ? 64 : 32;         // bf16: elements per swizzled row
@@ -336,7 +337,7 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
     j = r.stage(j, tok, vlo, vhi);
     if (!__all_sync(0xffffffffu, wait_bar(&bars.full[st], (uint32_t)(n / C::STAGES) & 1u, abort_flag))) return;
     const uint32_t stage = ring0 + (uint32_t)(st * C::STAGE);
-#pragma unroll 1
+#pragma unroll
     for (int x = 0; x < C::TILES; ++x) {
       const int t0 = tok + kUnit * x + 16 * warp;
       if (t0 >= vhi || t0 + 16 <= vlo) continue;
@@ -568,7 +569,8 @@ __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Ro
   }
 }
 
-// 4 bits, up to 8 query heads: four CTAs an SM (89 us; five with shorter rings and 80 registers 113 us).
+// 4 bits, up to 8 query heads: four CTAs an SM (74 us; three with longer rings 80, five with shorter ones
+// and 80 registers 90 to 109).
 template <int D, bool Q4, int NQ>
 __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv,
