@@ -20,12 +20,14 @@
 // the border, and then to the nearest even integer. In the same way
 // amax times fp32's 1 / 7 rounds to the bf16 number that amax / 7 does.
 //
-// Measured, K and V of 2 x 16384 tokens, 8 heads of 128 (172 MB): append 32.8 us (5.2 TB/s; 40 with one
-// element an instruction and a multiplication per address; bound by its instructions, ~115 a word),
+// Measured, K and V of 2 x 16384 tokens, 8 heads of 128 (172 MB): append 30.9 us (5.6 TB/s; 40 with one
+// element an instruction and a multiplication per address; bound by its instructions, ~100 a word),
 // read 28.0 us (6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "ptx_sm100.cuh"
@@ -55,7 +57,7 @@ __host__ __device__ constexpr int bit_of(int u) { return 8 * (u >> 2) + 4 * ((u 
 
 // A thread's words: run c and word t of it, the same for all its words (256 words are whole
 // rows), and per word token i of the call and head h. Addresses are found by additions.
-template <int D, int M>
+template <int D, int M, bool WRAP>
 struct Place {
   static constexpr uint32_t NG = D / 32;
   uint32_t c, t, h, i;
@@ -75,7 +77,7 @@ struct Place {
     h += p.step_h;
     x += p.x_step[M];
     row += p.row_step;
-    if (h >= (uint32_t)p.kv_heads) {
+    if (WRAP && h >= (uint32_t)p.kv_heads) {
       h -= (uint32_t)p.kv_heads;
       ++i;
       x += p.x_wrap[M];
@@ -144,12 +146,12 @@ __device__ __forceinline__ uint32_t quantise(const uint4& r, __nv_bfloat16& scal
   return word;
 }
 
-template <int D, int M, int kWords>
+template <int D, int M, int kWords, bool WRAP>
 __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint32_t w, int start) {
   constexpr uint32_t NG = D / 32;
-  const Place<D, M> first(p, s, w);
+  const Place<D, M, WRAP> first(p, s, w);
   uint4 v[kWords];
-  Place<D, M> at = first;
+  Place<D, M, WRAP> at = first;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {                 // whole runs: four threads in or out together
     v[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -170,13 +172,13 @@ __device__ __forceinline__ void append_words(const CParams& p, uint32_t s, uint3
   }
 }
 
-template <int D, int M, int kWords>
+template <int D, int M, int kWords, bool WRAP>
 __device__ __forceinline__ void read_words(const CParams& p, uint32_t s, uint32_t w, int start) {
   constexpr uint32_t NG = D / 32;
-  const Place<D, M> first(p, s, w);
+  const Place<D, M, WRAP> first(p, s, w);
   uint32_t word[kWords];
   __nv_bfloat16 scale[kWords];
-  Place<D, M> at = first;
+  Place<D, M, WRAP> at = first;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {
     word[k] = 0x88888888u;                           // rows outside the cache read as zeros
@@ -213,12 +215,20 @@ template <int D, bool READ, int kWords>
 __global__ void __launch_bounds__(256, READ ? 8 : (kWords > 1 ? 5 : 1)) cache4_kernel(const __grid_constant__ CParams p) {
   const uint32_t w = blockIdx.x * (256u * kWords) + threadIdx.x, s = blockIdx.y >> 1;
   const int start = p.start ? p.start[s] : 0;
-  if constexpr (READ) {
-    if (blockIdx.y & 1) read_words<D, 1, kWords>(p, s, w, start);
-    else read_words<D, 0, kWords>(p, s, w, start);
+  const auto words = [&](auto m, auto wrap) {
+    if constexpr (READ) read_words<D, decltype(m)::value, kWords, decltype(wrap)::value>(p, s, w, start);
+    else append_words<D, decltype(m)::value, kWords, decltype(wrap)::value>(p, s, w, start);
+  };
+  using K = std::integral_constant<int, 0>;
+  using V = std::integral_constant<int, 1>;
+  // where kv_heads divides the rows of 256 words, a thread's words are all of one head (append 33.0 ->
+  // 30.9 us)
+  if (kWords > 1 && p.step_h == 0) {
+    if (blockIdx.y & 1) words(V(), std::false_type());
+    else words(K(), std::false_type());
   } else {
-    if (blockIdx.y & 1) append_words<D, 1, kWords>(p, s, w, start);
-    else append_words<D, 0, kWords>(p, s, w, start);
+    if (blockIdx.y & 1) words(V(), std::true_type());
+    else words(K(), std::true_type());
   }
 }
 

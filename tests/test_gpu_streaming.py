@@ -269,6 +269,29 @@ def test_cache4_rows(b, n, hk, d, cap, start):
             assert np.all(other == 0x5a)
 
 
+@pytest.mark.parametrize("hk,d", [(4, 128), (3, 128), (16, 64), (5, 32)])
+def test_cache4_long_and_short_calls_agree(hk, d):
+    """A long prompt in one call and in pieces: the same codes and scales, read back alike."""
+    torch = torch_cuda()
+    b, n = 2, 6007 * 512 // (hk * d)
+    n += 1 - n % 2
+    cap = -(-n // 8) * 8 + 16
+    start = torch.tensor([3, 0], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(b, n, hk, d, device="cuda").bfloat16() for _ in range(2))
+    whole, parts = sa.cache4_alloc(b, cap, hk, d), sa.cache4_alloc(b, cap, hk, d)
+    for x in whole + parts:
+        x.zero_()
+    sa.cache4_append(whole, k, v, start)
+    step = n // 16 + 1
+    for i in range(0, n, step):
+        sa.cache4_append(parts, k[:, i:i + step], v[:, i:i + step], start + i)
+    rk, rv = sa.cache4_read(whole, start, n)
+    pieces = [sa.cache4_read(whole, start + i, min(step, n - i)) for i in range(0, n, step)]
+    status_ok()
+    assert all(torch.equal(x, y) for x, y in zip(whole, parts))
+    assert torch.equal(rk, torch.cat([x for x, _ in pieces], 1)) and torch.equal(rv, torch.cat([x for _, x in pieces], 1))
+
+
 def test_cache4_left_out_and_overfull_sequences():
     torch = torch_cuda()
     b, n, hk, d, cap = 3, 6, 2, 64, 16
