@@ -643,3 +643,186 @@ def test_two_streams_at_once():
     status_ok()
     for a, c in zip(want, got):
         assert all(torch.equal(x, y) for x, y in zip(a, c))
+
+
+# ------------------------------------------------------------------ several rounds of every loop
+
+def several_per_sm(items):
+    count = torch_cuda().cuda.get_device_properties(0).multi_processor_count
+    assert items >= 3 * count, (items, count)
+
+
+@pytest.mark.parametrize("b,n,h,hk,d,w,s", [(14, 517, 14, 7, 32, 150, 5), (14, 520, 14, 7, 64, 100, 70),
+                                            (14, 515, 14, 7, 128, 60, 9), (14, 530, 14, 7, 64, 600, 0)])
+def test_sink_attention_with_several_items_a_cta(b, n, h, hk, d, w, s):
+    """Persistent CTAs that take three work items and more, forward, dQ and dK / dV, every row checked."""
+    several_per_sm(b * hk * -(-n // 128))
+    (q, qf), (k, kf), (v, vf), (g, gf) = (rand(i, b, n, x, d) for i, x in enumerate((h, hk, hk, h)))
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    grads = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    of, lf, ob = ref.sink_attention(qf, kf, vf, w, s)
+    close(o, of, ob, "o")
+    close(lse, lf, LSE_TOL, "lse")
+    want, bounds = ref.sink_attention_backward(qf, kf, vf, gf, w, s)
+    for name, x, y, e in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(x, y, e, name)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sinks_gradients_over_many_chunks(d):
+    """The sinks' keys and values gather from every query of a long sequence, in some 50 partial sums; P and
+    D in float64 from the forward's outputs."""
+    torch = torch_cuda()
+    n, h, hk, w, s = 50021, 4, 2, 60, 6
+    q, k, v, g = (rand(i, 1, n, x, d)[0] for i, x in enumerate((h, hk, hk, h)))
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    _, dk, dv = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    i, j = torch.arange(n, device="cuda")[:, None], torch.arange(s, device="cuda")[None]
+    for hd in range(hk):
+        want_k, want_v, size_k, size_v = (torch.zeros(s, d, dtype=torch.float64, device="cuda") for _ in range(4))
+        for e in range(hd * h // hk, (hd + 1) * h // hk):
+            qd, gd, od = (x[0, :, e].double() for x in (q, g, o))
+            kd, vd = (x[0, :s, hd].double() for x in (k, v))
+            p = torch.where(j <= i, torch.exp(qd @ kd.T * d ** -0.5 - lse[0, e].double()[:, None]), 0.0)
+            ds = p * (gd @ vd.T - (gd * od).sum(-1, keepdim=True)) * d ** -0.5
+            want_k += ds.T @ qd
+            want_v += p.T @ gd
+            size_k += ds.abs().T @ qd.abs()
+            size_v += p.T @ gd.abs()
+        # P and dS once rounded, and the result; P itself is off by 2 LSE_TOL; fp32 sums of some 130 rows a step,
+        # 400 steps and 50 parts lose less than 2^-12 of the magnitudes
+        for name, got, want, size in (("dk", dk, want_k, size_k), ("dv", dv, want_v, size_v)):
+            bound = 1.02 * ref.U * (want.abs() + size) + (2 * LSE_TOL + 2.0 ** -12) * size + 1e-6
+            close(got[0, :s, hd], want.cpu().numpy(), bound.cpu().numpy(), name)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sink_attention_backward_of_large_scores(d):
+    n, w, s = 400, 90, 6
+    (q, qf), (k, kf) = rand(0, 1, n, 2, d, scale=6.0), rand(1, 1, n, 1, d, scale=6.0)
+    (v, vf), (g, gf) = rand(2, 1, n, 1, d), rand(3, 1, n, 2, d)
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    grads = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    want, bounds = ref.sink_attention_backward(qf, kf, vf, gf, w, s)
+    # |s| up to 400: scores and LSE are each off by up to 400 x 2^-20, so P by 8e-4 of itself and O by
+    # twice that of P |v|. dS then gains 8e-4 |dS| + 16e-4 P |dO| P |v| and P 8e-4 P, at most 16e-4 / U = 0.41 of what
+    # the bounds hold for the roundings of P, dS and O
+    for name, x, y, e in zip(("dq", "dk", "dv"), grads, want, bounds):
+        close(x, y, 1.41 * e, name)
+
+
+@pytest.mark.parametrize("b,n,h,hk,d,rotary,inter", [(3, 3001, 29, 5, 32, 32, False), (3, 3001, 13, 5, 64, 64, True),
+                                                     (3, 3001, 13, 5, 128, 128, False), (3, 3001, 13, 5, 128, 64, True),
+                                                     (2, 501, 40, 5, 128, 128, False), (7, 700, 31, 2, 64, 32, False)])
+def test_norm_rope_with_several_tokens_a_warp(b, n, h, hk, d, rotary, inter):
+    """Warps that take several tokens (or ranges of a token's heads) in several batches; the backward also
+    over its own inputs."""
+    torch = torch_cuda()
+    several_per_sm(b * n / 8 if h < 40 else b * n * 9 / 8 / 2)
+    rng = np.random.default_rng(6)
+    (q, qf), (k, kf), (gq, gqf), (gk, gkf) = (rand(i, b, n, x, d) for i, x in enumerate((h, hk, h, hk)))
+    w = [np.float32(1 + 0.2 * rng.standard_normal(d)) for _ in range(2)]
+    wt = [torch.from_numpy(x).cuda() for x in w]
+    freq = 10000.0 ** (-2.0 * np.arange(rotary // 2) / rotary)
+    pos = rng.integers(0, 1 << 20, (b, n))
+    pt = torch.from_numpy(pos.astype(np.int32)).cuda()
+    outs = sa.qk_norm_rope_fwd(q, k, *wt, freq, pt, 1e-5, inter)
+    grads = sa.qk_norm_rope_bwd(q, k, gq, gk, *wt, freq, pt, 1e-5, inter)
+    status_ok()
+    for name, y, dx, dw, xf, gf, wf in zip("qk", outs, grads[:2], grads[2:], (qf, kf), (gqf, gkf), w):
+        want, bound = ref.norm_rope(xf, wf.astype(np.float64), pos, freq, 1e-5, inter)
+        close(y, want, bound, name + "_out")
+        (dxf, dwf), (bx, bw) = ref.norm_rope_backward(xf, wf.astype(np.float64), gf, pos, freq, 1e-5, inter)
+        close(dx, dxf, bx, "d" + name)
+        close(dw, dwf, bw, "dw_" + name)
+    dqw, dkw = torch.empty_like(wt[0]), torch.empty_like(wt[1])
+    ws = torch.empty(sa.sa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    sa.sa_qk_norm_rope_bwd(q, k, gq, gk, *wt, freq, pt, gq, gk, dqw, dkw, ws, 1e-5, inter)
+    sa.sa_qk_norm_rope_fwd(q, k, *wt, freq, pt, q, k, 1e-5, inter)
+    status_ok()
+    assert all(torch.equal(x, y) for x, y in zip((q, k, gq, gk, dqw, dkw), outs + grads))
+
+
+@pytest.mark.parametrize("cache4", [False, True])
+@pytest.mark.parametrize("h,hk,d", [(4, 2, 32), (24, 2, 32), (4, 2, 64), (24, 2, 64), (4, 2, 128), (24, 2, 128)])
+def test_decode_with_several_rounds_of_the_ring(h, hk, d, cache4):
+    """Long sequences: every CTA fills its ring three times and more; the scores grow along the sequence, so
+    that the running maximum is followed again and again."""
+    torch = torch_cuda()
+    cap, w, s, lengths = 16384, 16100, 70, [16384, 16201, 13007]
+    b = len(lengths)
+    q, qf = rand(0, b, 1, h, d)
+    v, vf = rand(2, b, cap, hk, d)
+    k = torch.randn(b, cap, hk, d, generator=torch.Generator().manual_seed(1))
+    k = (k * torch.linspace(0.1, 4.0, cap)[:, None, None]).to(torch.bfloat16).cuda()
+    kf = bf16_to_f64(k)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    if cache4:
+        cache = sa.cache4_alloc(b, cap, hk, d)
+        sa.cache4_append(cache, k, v)
+        o, lse = sa.sink_attn_decode_cache4(q, cache, n, w, s)
+        kf, vf = (ref.values(*ref.quantise(x)) for x in (kf, vf))
+    else:
+        o, lse = sa.sink_attn_decode(q, k, v, n, w, s)
+    status_ok()
+    of, lf, ob = ref.sink_decode(qf, kf, vf, lengths, w, s)
+    close(o, of, ob, "o")
+    close(lse, lf, LSE_TOL, "lse")
+
+
+FRESH = '''
+import threading
+import numpy as np, torch
+import content_adaptive_sparse_gb300 as sa
+
+b, n, h, hk, d, w, s, threads, calls = 1, 200, 4, 2, 64, 30, 3, 8, 24
+gen = torch.Generator(device="cuda").manual_seed(1)
+q, k, v, g = (torch.randn(b, n, x, d, generator=gen, device="cuda").bfloat16() for x in (h, hk, hk, h))
+length = torch.tensor([n], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+
+def chain(i):
+    freq = (100.0 + i) ** (-np.arange(d // 2) / 32.0)
+    qr, kr = sa.qk_norm_rope_fwd(q, k, None, None, freq)
+    o, lse = sa.sink_attn_fwd(qr, kr, v, w, s)
+    cache = sa.cache4_alloc(b, n, hk, d)
+    sa.cache4_append(cache, kr, v)
+    return (qr, kr, o, lse) + sa.sink_attn_bwd(qr, kr, v, o, lse, g, w, s) + sa.sink_attn_decode_cache4(qr[:, -1:], cache, length, w, s)
+
+start = threading.Barrier(threads)
+got, errors = {}, []
+
+def work(t):
+    try:
+        start.wait()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for c in range(calls):
+                got[t, c] = chain(t * calls + c)
+            torch.cuda.current_stream().synchronize()
+    except Exception as e:
+        errors.append(repr(e))
+
+pool = [threading.Thread(target=work, args=(t,)) for t in range(threads)]
+for t in pool: t.start()
+for t in pool: t.join()
+assert not errors, errors
+for (t, c), x in got.items():
+    assert all(torch.equal(a, e) for a, e in zip(x, chain(t * calls + c))), (t, c)
+torch.cuda.synchronize()
+assert sa.sa_device_status() == 0
+'''
+
+
+def test_first_calls_from_several_host_threads():
+    """A process whose first calls come from eight threads at once, each on a stream and with frequency
+    tables of its own (192 in all)."""
+    import os
+    import subprocess
+    import sys
+    torch_cuda()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FRESH], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-3000:]
