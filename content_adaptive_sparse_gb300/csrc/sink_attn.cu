@@ -493,13 +493,13 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
     const float m = fmaxf(m0, m1);
     float f0 = m0 == kNegInf ? 0.f : ex2_approx(m0 - m), f1 = m1 == kNegInf ? 0.f : ex2_approx(m1 - m);
     const float L = l0 * f0 + l1 * f1;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = 1.f / L;                         // every query sees itself: L > 0, or NaN as its scores
     f0 *= inv;
     f1 *= inv;
     const int q0 = it.tile * kTile + 32 * quarter, tok = q0 + lane;
     if (tok < p.n_tokens)
       p.lse[((int64_t)it.s * p.heads + it.h) * p.n_tokens + tok] =
-          L > 0.f ? (m + __log2f(L)) * 0.69314718055994531f : kNegInf;
+          (m + __log2f(L)) * 0.69314718055994531f;
     if (!__all_sync(0xffffffffu, wait_bar(&bars.o_full, (uint32_t)n & 1u, abort_flag))) break;
     tc_fence_after();
     const uint32_t t0 = base + C::COL_O, t1 = t0 + D;

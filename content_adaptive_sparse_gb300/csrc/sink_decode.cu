@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      a[w] = M != kNegInf ? ex2_approx(a[w] - M) : 0.f;
+      a[w] = M != kNegInf ? ex2_approx(a[w] - M) : 1.f;     // without a maximum the sums are zero, or NaN
       const float4 v = *reinterpret_cast<const float4*>(wo + (w * kQ + row) * D + col);
       sum.x = fmaf(a[w], v.x, sum.x);
       sum.y = fmaf(a[w], v.y, sum.y);
@@ -704,20 +704,19 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mk[k]);
     float x = 0.f, y = 0.f, L = 0.f;
-    if (M != kNegInf) {
 #pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k) {
-        const float a = ex2_approx(mk[k] - M);
-        x = fmaf(a, v[k].x, x);
-        y = fmaf(a, v[k].y, y);
-        L = fmaf(a, lk[k], L);
-      }
+    for (int k = 0; k < kMaxCluster; ++k) {
+      const float a = M != kNegInf ? ex2_approx(mk[k] - M) : 1.f;
+      x = fmaf(a, v[k].x, x);
+      y = fmaf(a, v[k].y, y);
+      L = fmaf(a, lk[k], L);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    // L is 0 where no key is seen, and NaN where a score that is seen is (no maximum follows a NaN)
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<uint32_t*>(p.o + (int64_t)s * p.o_sb + (int64_t)(h0 + row) * p.o_sh + col) =
         pack_bf16x2(x * inv, y * inv);
     if (col == 0)
-      p.lse[(int64_t)s * p.heads + h0 + row] = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : kNegInf;
+      p.lse[(int64_t)s * p.heads + h0 + row] = L == 0.f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
   }
   cluster.sync();                                           // no CTA leaves while another reads its results
 }

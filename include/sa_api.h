@@ -342,7 +342,7 @@ int sa_build_mask_from_bytes(const sa_mask_params* params, const uint8_t* h_byte
  *
  * q, k, v and d_o are expected to be finite: as in sa_attn_fwd, a non-finite row reaches the
  * queries whose 128-query tile meets it. (The decoding calls ignore whatever stands in rows that
- * the query does not see.) None of these calls uses the legacy default stream or memory of its
+ * the query does not see.) Where a score that a query sees is NaN, its o and lse are NaN. None of these calls uses the legacy default stream or memory of its
  * own; calls on several streams need separate workspaces where a call takes one. */
 
 /* RMS norm of every query and key head and the position rotation, in one pass. Per row x (one

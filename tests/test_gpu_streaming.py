@@ -235,6 +235,52 @@ def test_decode_strided_cache_and_large_scores():
     close(lse, lf, 4e-4, "lse")
 
 
+# ------------------------------------------------------------------ numbers that are not numbers
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("h", [4, 24])
+def test_decode_keeps_nan_of_what_is_seen(h, d):
+    """A NaN in a query, in the only key and in one key of many: o and lse are NaN for the heads that see it,
+    not the zeros of an empty sequence, and the others are as without it."""
+    torch = torch_cuda()
+    b, hk, cap, w, s = 4, 2, 512, 511, 0
+    lengths = [1, 400, 400, 0]
+    q, k, v = (rand(i, b, x, y, d)[0] for i, (x, y) in enumerate(((1, h), (cap, hk), (cap, hk))))
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+
+    def both():
+        cache = sa.cache4_alloc(b, cap, hk, d)
+        sa.cache4_append(cache, k, v)
+        out = sa.sink_attn_decode(q, k, v, n, w, s), sa.sink_attn_decode_cache4(q, cache, n, w, s)
+        status_ok()
+        return out
+
+    clean = both()
+    group = h // hk
+    hit = torch.zeros(b, h, dtype=torch.bool, device="cuda")
+    hit[0, :group] = hit[1, group:] = hit[2, 1] = True
+    k[0, 0, 0, 5] = float("nan")                          # the only key of key head 0
+    k[1, 371, 1, d - 1] = float("nan")                    # one of 400 of key head 1
+    q[2, 0, 1, 3] = float("nan")
+    for (o, lse), (o1, lse1) in zip(both(), clean):
+        assert torch.isnan(o[:, 0][hit]).all() and torch.isnan(lse[..., 0][hit]).all()
+        assert torch.equal(o[:, 0][~hit], o1[:, 0][~hit]) and torch.equal(lse[..., 0][~hit], lse1[..., 0][~hit])
+        assert torch.isneginf(lse[3]).all() and not o[3].any()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sink_attention_keeps_nan_queries(d):
+    torch = torch_cuda()
+    b, n, h, w, s = 1, 300, 2, 40, 3
+    q, k, v = (rand(i, b, n, h, d)[0] for i in range(3))
+    q[0, 7, 1, 2] = q[0, 290, 0, 0] = float("nan")
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    status_ok()
+    for i, e in ((7, 1), (290, 0)):
+        assert torch.isnan(o[0, i, e]).all() and torch.isnan(lse[0, e, i])
+    assert int(torch.isnan(lse).sum()) == 2 and not torch.isneginf(lse).any()
+
+
 # ------------------------------------------------------------------ 4-bit cache
 
 @pytest.mark.parametrize("b,n,hk,d,cap,start", [(1, 1, 1, 32, 8, [7]), (2, 5, 3, 64, 16, [0, 11]), (3, 70, 2, 128, 96, [3, 26, 9]),
