@@ -65,9 +65,28 @@ def _check(name: str, code: int) -> None:
 # A decoding step is a few microseconds of GPU work, so the checks are single comparisons and the
 # stride arrays are kept by their values. Each helper raises with the argument's name.
 
+_MAX = 2**31 - 1
+
+
+def _int(v: int) -> int:
+    """`v` for a 32-bit argument, of which ctypes would drop the upper bits: past 32 bits the nearest number
+    that fits, which the library takes or refuses as it would have taken `v` (its limits lie inside)."""
+    return v if -_MAX <= v <= _MAX else _MAX if v > 0 else -_MAX
+
+
 @functools.lru_cache(maxsize=1024)
 def _s3(strides: tuple) -> _S3:
     return _S3(*strides[:3])
+
+
+@functools.lru_cache(maxsize=1024)
+def _layout(strides: tuple, shape: tuple):
+    """Strides of a tensor whose sizes fit in 32 bits, or None."""
+    return _S3(*strides[:3]) if max(shape) <= _MAX else None
+
+
+def _too_large(name: str):
+    raise ValueError(f"{name}: sizes of 2^31 and more are not supported")
 
 
 @functools.lru_cache(maxsize=64)
@@ -112,7 +131,10 @@ def _rows(name: str, t, device: int, shape=None) -> _S3:
         raise ValueError(f"{name}: head_dim must be contiguous")
     if t.get_device() != device:
         _elsewhere(name)
-    return _s3(st)
+    layout = _layout(st, t.shape)
+    if layout is None:
+        _too_large(name)
+    return layout
 
 
 def _elsewhere(name: str):
@@ -137,8 +159,8 @@ def _same_sequence(q, k) -> None:
         raise ValueError("q and k must agree in batch, tokens and head_dim")
 
 
-def _scale(softmax_scale, d: int) -> float:
-    return d ** -0.5 if softmax_scale is None else float(softmax_scale)
+def _graph(window: int, sinks: int, softmax_scale, d: int) -> tuple[int, int, float]:
+    return _int(window), _int(sinks), d ** -0.5 if softmax_scale is None else float(softmax_scale)
 
 
 def _stream(stream, device: int) -> int:
@@ -173,7 +195,7 @@ def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, 
     f32 = torch.float32
     return (q.data_ptr(), k.data_ptr()), (qs, ks), (
         b, n, h, k.shape[2], d, _flat("q_weight", q_weight, f32, (d,), dev), _flat("k_weight", k_weight, f32, (d,), dev),
-        eps, freq, 2 * pairs, 1 if interleaved else 0, _flat("positions", positions, torch.int32, (b, n), dev))
+        eps, freq, _int(2 * pairs), 1 if interleaved else 0, _flat("positions", positions, torch.int32, (b, n), dev))
 
 
 def sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps: float = 1e-6,
@@ -190,7 +212,8 @@ def sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_
 
 def sa_qk_norm_rope_bwd_workspace_size(head_dim: int) -> int:
     out = ctypes.c_size_t(0)
-    _check("sa_qk_norm_rope_bwd_workspace_size", _lib().sa_qk_norm_rope_bwd_workspace_size(head_dim, ctypes.byref(out)))
+    _check("sa_qk_norm_rope_bwd_workspace_size",
+           _lib().sa_qk_norm_rope_bwd_workspace_size(_int(head_dim), ctypes.byref(out)))
     return int(out.value)
 
 
@@ -246,15 +269,15 @@ def sa_sink_attn_fwd(q, k, v, window: int, sinks: int, o, lse, softmax_scale: fl
     ptrs, strides = _sink_inputs(q, k, v, dev)
     b, n, h, d = q.shape
     _check("sa_sink_attn_fwd", _lib().sa_sink_attn_fwd(
-        *ptrs, *strides, _rows("o", o, dev, q.shape), b, n, h, k.shape[2], d, window, sinks, _scale(softmax_scale, d),
+        *ptrs, *strides, _rows("o", o, dev, q.shape), b, n, h, k.shape[2], d, *_graph(window, sinks, softmax_scale, d),
         o.data_ptr(), _flat("lse", lse, torch.float32, (b, h, n), dev), _stream(stream, dev)))
 
 
 def sa_sink_attn_bwd_workspace_size(batch: int, n_tokens: int, heads: int, kv_heads: int, head_dim: int, window: int,
                                     sinks: int) -> int:
     out = ctypes.c_size_t(0)
-    _check("sa_sink_attn_bwd_workspace_size", _lib().sa_sink_attn_bwd_workspace_size(
-        batch, n_tokens, heads, kv_heads, head_dim, window, sinks, ctypes.byref(out)))
+    sizes = map(_int, (batch, n_tokens, heads, kv_heads, head_dim, window, sinks))
+    _check("sa_sink_attn_bwd_workspace_size", _lib().sa_sink_attn_bwd_workspace_size(*sizes, ctypes.byref(out)))
     return int(out.value)
 
 
@@ -268,8 +291,8 @@ def sa_sink_attn_bwd(q, k, v, o, d_o, lse, window: int, sinks: int, dq, dk, dv, 
     b, n, h, d = q.shape
     _check("sa_sink_attn_bwd", _lib().sa_sink_attn_bwd(
         *ptrs, o.data_ptr(), d_o.data_ptr(), _flat("lse", lse, torch.float32, (b, h, n), dev), *strides,
-        _rows("o", o, dev, q.shape), _rows("d_o", d_o, dev, q.shape), b, n, h, k.shape[2], d, window, sinks,
-        _scale(softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _rows("dq", dq, dev, q.shape),
+        _rows("o", o, dev, q.shape), _rows("d_o", d_o, dev, q.shape), b, n, h, k.shape[2], d,
+        *_graph(window, sinks, softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _rows("dq", dq, dev, q.shape),
         _rows("dk", dk, dev, k.shape), _rows("dv", dv, dev, k.shape), *_workspace(workspace, dev), _stream(stream, dev)))
 
 
@@ -282,8 +305,8 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int, softmax_scale: float | None 
     o = _like(q)
     lse = torch.empty((b, h, n), dtype=torch.float32, device=q.device)
     _check("sa_sink_attn_fwd", _lib().sa_sink_attn_fwd(
-        *ptrs, *strides, _dense(q.shape), b, n, h, k.shape[2], d, window, sinks, _scale(softmax_scale, d), o.data_ptr(),
-        lse.data_ptr(), _stream(None, dev)))
+        *ptrs, *strides, _dense(q.shape), b, n, h, k.shape[2], d, *_graph(window, sinks, softmax_scale, d),
+        o.data_ptr(), lse.data_ptr(), _stream(None, dev)))
     return o, lse
 
 
@@ -300,9 +323,9 @@ def sink_attn_bwd(q, k, v, o, lse, d_o, window: int, sinks: int, softmax_scale: 
     ws = torch.empty(size, dtype=torch.uint8, device=q.device)
     kv = _dense(k.shape)
     _check("sa_sink_attn_bwd", _lib().sa_sink_attn_bwd(
-        *ptrs, o.data_ptr(), d_o.data_ptr(), lse_at, *strides, os, gs, b, n, h, hk, d, window, sinks,
-        _scale(softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dense(q.shape), kv, kv, ws.data_ptr(),
-        size, _stream(None, dev)))
+        *ptrs, o.data_ptr(), d_o.data_ptr(), lse_at, *strides, os, gs, b, n, h, hk, d,
+        *_graph(window, sinks, softmax_scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dense(q.shape), kv, kv,
+        ws.data_ptr(), size, _stream(None, dev)))
     return dq, dk, dv
 
 
@@ -335,6 +358,8 @@ def _cache4(cache, dev):
     codes = kc.shape
     if len(codes) != 4:
         raise ValueError("cache: expected codes of shape [batch, kv_heads, capacity, head_dim / 2]")
+    if max(codes) > _MAX:
+        _too_large("cache")
     b, hk, cap, half = codes
     scales = (b, hk, cap, half // 16)
     u8 = torch.uint8
@@ -377,6 +402,8 @@ def cache4_read(cache: Cache4, start, n_tokens: int):
     """Returns (k, v), bfloat16 [batch, n_tokens, kv_heads, head_dim]."""
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
+    if n_tokens > _MAX:
+        _too_large("n_tokens")
     k = torch.empty((b, n_tokens, hk, d), dtype=torch.bfloat16, device=cache[0].device)
     v = torch.empty_like(k)
     st = _dense(k.shape)
@@ -409,7 +436,7 @@ def sa_sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, o
     _check("sa_sink_attn_decode", _lib().sa_sink_attn_decode(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qs, _rows("k_cache", k_cache, dev),
         _rows("v_cache", v_cache, dev, k_cache.shape), _rows("o", o, dev, q.shape), b, cap, h, hk, d,
-        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        _flat("lengths", lengths, torch.int32, (b,), dev), *_graph(window, sinks, softmax_scale, d), o.data_ptr(),
         _flat("lse", lse, torch.float32, (b, h, 1), dev), _stream(stream, dev)))
 
 
@@ -420,7 +447,7 @@ def sa_sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: in
     qs, h = _token(q, b, d, dev), q.shape[2]
     _check("sa_sink_attn_decode_cache4", _lib().sa_sink_attn_decode_cache4(
         q.data_ptr(), *at, qs, _rows("o", o, dev, q.shape), b, cap, h, hk, d,
-        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        _flat("lengths", lengths, torch.int32, (b,), dev), *_graph(window, sinks, softmax_scale, d), o.data_ptr(),
         _flat("lse", lse, torch.float32, (b, h, 1), dev), _stream(stream, dev)))
 
 
@@ -435,7 +462,7 @@ def sink_attn_decode(q, k_cache, v_cache, lengths, window: int, sinks: int, soft
     _check("sa_sink_attn_decode", _lib().sa_sink_attn_decode(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qs, _rows("k_cache", k_cache, dev),
         _rows("v_cache", v_cache, dev, k_cache.shape), _dense(q.shape), b, cap, q.shape[2], hk, d,
-        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        _flat("lengths", lengths, torch.int32, (b,), dev), *_graph(window, sinks, softmax_scale, d), o.data_ptr(),
         lse.data_ptr(), _stream(None, dev)))
     return o, lse
 
@@ -448,7 +475,7 @@ def sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: int, 
     o, lse = _token_outputs(q)
     _check("sa_sink_attn_decode_cache4", _lib().sa_sink_attn_decode_cache4(
         q.data_ptr(), *at, qs, _dense(q.shape), b, cap, q.shape[2], hk, d,
-        _flat("lengths", lengths, torch.int32, (b,), dev), window, sinks, _scale(softmax_scale, d), o.data_ptr(),
+        _flat("lengths", lengths, torch.int32, (b,), dev), *_graph(window, sinks, softmax_scale, d), o.data_ptr(),
         lse.data_ptr(), _stream(None, dev)))
     return o, lse
 

@@ -109,6 +109,25 @@ def test_sink_attention_strided_scaled_and_repeated():
     assert torch.equal(first.view(torch.int16), dpacked.view(torch.int16))
 
 
+def test_windows_past_32_bits_are_the_whole_sequence():
+    torch = torch_cuda()
+    b, n, h, hk, d = 1, 200, 4, 2, 64
+    q, k, v, g = (rand(i, b, n, x, d)[0] for i, x in enumerate((h, hk, hk, h)))
+    length = torch.tensor([n], dtype=torch.int32, device="cuda")
+    cache = sa.cache4_alloc(b, n, hk, d)
+    sa.cache4_append(cache, k, v)
+
+    def calls(w):
+        o, lse = sa.sink_attn_fwd(q, k, v, w, 0)
+        return (o, lse) + sa.sink_attn_bwd(q, k, v, o, lse, g, w, 0) + sa.sink_attn_decode(q[:, -1:], k, v, length, w, 0) + \
+            sa.sink_attn_decode_cache4(q[:, -1:], cache, length, w, 0)
+
+    want = calls(n - 1)
+    for w in (1 << 32, 2**32 + 5, 1 << 63):
+        assert all(torch.equal(x, y) for x, y in zip(calls(w), want))
+    status_ok()
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("n,w,s", [(1, 0, 0), (1, 9, 4), (131, 0, 0)])
 def test_sink_attention_backward_of_one_visible_key(n, w, s, d):

@@ -186,6 +186,87 @@ def test_binding_refuses_wrong_tensors():
         sa.cache4_append(cache, q, q)
 
 
+class Recorder:
+    """In the library's place: keeps each call's arguments and succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    """The binding over CPU tensors and a library that only records."""
+    pytest.importorskip("torch")
+    from content_adaptive_sparse_gb300 import streaming
+    streaming._device()
+    rec = Recorder()
+    monkeypatch.setattr(streaming, "_LIB", rec)
+    monkeypatch.setattr(streaming, "_device", lambda: -1)
+    monkeypatch.setattr(streaming, "_stream", lambda stream, device: 0)
+    streaming._sink_bwd_bytes.cache_clear()
+    yield rec
+    streaming._sink_bwd_bytes.cache_clear()
+
+
+BIG = 2**31 - 1
+
+
+@pytest.mark.parametrize("window,sinks,want", [(5, 4, (5, 4)), (1 << 32, 0, (BIG, 0)), (2**32 + 5, 2**32 + 4, (BIG, BIG)),
+                                               (2**31, 2**40, (BIG, BIG)), (-2**32 + 5, 2**31, (-BIG, BIG)),
+                                               (3, -2**32 + 1, (3, -BIG))])
+def test_windows_and_sinks_past_32_bits(recorder, window, sinks, want):
+    """What does not fit a 32-bit argument is not cut to its low bits: a huge window is the whole sequence,
+    a huge or negative number of sinks a refusal."""
+    torch = pytest.importorskip("torch")
+    q, k = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 8, 2, 64, dtype=torch.bfloat16)
+    n = torch.ones(2, dtype=torch.int32)
+    o, lse = sa.sink_attn_fwd(q, k, k, window, sinks)
+    sa.sa_sink_attn_fwd(q, k, k, window, sinks, o, lse)
+    sa.sink_attn_bwd(q, k, k, o, lse, o, window, sinks)
+    sa.sa_sink_attn_bwd(q, k, k, o, o, lse, window, sinks, o, k, k, torch.zeros(8))
+    sa.sa_sink_attn_bwd_workspace_size(2, 8, 4, 2, 64, window, sinks)
+    o, lse = sa.sink_attn_decode(q[:, :1], k, k, n, window, sinks)
+    sa.sa_sink_attn_decode(q[:, :1], k, k, n, window, sinks, o, lse)
+    cache = sa.cache4_alloc(2, 8, 2, 64, device="cpu")
+    sa.sink_attn_decode_cache4(q[:, :1], cache, n, window, sinks)
+    sa.sa_sink_attn_decode_cache4(q[:, :1], cache, n, window, sinks, o, lse)
+    assert len(recorder.calls) == 10
+    for name, args in recorder.calls:
+        after = args.index(64) + 1                       # head_dim; the decoding calls have the lengths' address next
+        if "decode" in name:
+            after += 1
+        assert args[after:after + 2] == want, name
+
+
+def test_sizes_past_32_bits(recorder, lib):
+    torch = pytest.importorskip("torch")
+    from content_adaptive_sparse_gb300 import streaming
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    for shape in ((2**32 + 1, 1, 1, 64), (1, 2**32 + 5, 1, 64), (1, 1, 2**31, 64)):
+        with pytest.raises(ValueError, match="x: sizes"):
+            streaming._rows("x", x.expand(shape), -1)
+    assert streaming._rows("x", x.expand(1, BIG, 1, 64), -1)[2] == 64
+    cache = sa.cache4_alloc(1, 8, 1, 64, device="cpu")
+    with pytest.raises(ValueError, match="cache: sizes"):
+        streaming._cache4([t[:, :, :1].expand(1, 1, 2**32 + 8, -1) for t in cache], -1)
+    with pytest.raises(ValueError, match="n_tokens: sizes"):
+        sa.cache4_read(cache, None, 2**32 + 1)
+    streaming._LIB = lib
+    for bad in ((2**32 + 1, 8, 4, 2, 64, 1, 1), (1, 2**32 + 8, 4, 2, 64, 1, 1), (1, 8, 4, 2, 2**32 + 64, 1, 1)):
+        with pytest.raises(sa.SAError):
+            sa.sa_sink_attn_bwd_workspace_size(*bad)
+    with pytest.raises(sa.SAError):
+        sa.sa_qk_norm_rope_bwd_workspace_size(2**32 + 64)
+    whole = sa.sa_sink_attn_bwd_workspace_size(1, 4096, 4, 2, 64, 4095, 4)
+    assert sa.sa_sink_attn_bwd_workspace_size(1, 4096, 4, 2, 64, 2**32 + 5, 4) == whole
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_sink_mask_is_the_definition():
