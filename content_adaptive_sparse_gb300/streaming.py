@@ -91,10 +91,9 @@ def _too_large(name: str):
 
 @functools.lru_cache(maxsize=64)
 def _frequencies(raw: bytes):
-    """A host array of the doubles in `raw`: (address, count, the array, which owns the memory)."""
-    n = len(raw) // 8
-    array = (ctypes.c_double * n).from_buffer_copy(raw)
-    return ctypes.addressof(array) if n else 0, n, array
+    """A host array of the doubles in `raw` (None for none). The caller passes the array itself, not its
+    address, and so keeps it until its call is over: this cache may drop it meanwhile."""
+    return (ctypes.c_double * (len(raw) // 8)).from_buffer_copy(raw) if raw else None
 
 
 def _dense(shape) -> _S3:
@@ -191,11 +190,11 @@ def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, 
         inv_freq = np.asarray(inv_freq, dtype=np.float64)
     if inv_freq.ndim != 1:
         raise ValueError("inv_freq: expected one frequency per rotated pair")
-    freq, pairs, _ = _frequencies(inv_freq.tobytes())
+    freq = _frequencies(inv_freq.tobytes())
     f32 = torch.float32
     return (q.data_ptr(), k.data_ptr()), (qs, ks), (
         b, n, h, k.shape[2], d, _flat("q_weight", q_weight, f32, (d,), dev), _flat("k_weight", k_weight, f32, (d,), dev),
-        eps, freq, _int(2 * pairs), 1 if interleaved else 0, _flat("positions", positions, torch.int32, (b, n), dev))
+        eps, freq, _int(2 * inv_freq.size), 1 if interleaved else 0, _flat("positions", positions, torch.int32, (b, n), dev))
 
 
 def sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps: float = 1e-6,

@@ -1,6 +1,7 @@
 """Streaming attention without a GPU: refusals of the C entry points and of the binding, and pins of
 the float64 oracle."""
 import ctypes
+import functools
 
 import numpy as np
 import pytest
@@ -265,6 +266,41 @@ def test_sizes_past_32_bits(recorder, lib):
         sa.sa_qk_norm_rope_bwd_workspace_size(2**32 + 64)
     whole = sa.sa_sink_attn_bwd_workspace_size(1, 4096, 4, 2, 64, 4095, 4)
     assert sa.sa_sink_attn_bwd_workspace_size(1, 4096, 4, 2, 64, 2**32 + 5, 4) == whole
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_frequencies_live_until_the_call_is_over(recorder, monkeypatch, backward):
+    """Other threads rotate with tables of their own meanwhile: the call's table stays where it is."""
+    import gc
+    import weakref
+    torch = pytest.importorskip("torch")
+    from content_adaptive_sparse_gb300 import streaming
+    made, seen = {}, []
+    array = ctypes.c_double * 32
+    freq = np.linspace(0.1, 1.0, 32)
+    plain = streaming._frequencies.__wrapped__
+
+    @functools.lru_cache(maxsize=64)
+    def frequencies(raw):
+        out = plain(raw)
+        made[raw], = (weakref.ref(x) for x in (out if type(out) is tuple else (out,)) if isinstance(x, array))
+        return out
+
+    def call(*args):
+        for i in range(100):
+            frequencies(np.full(32, 2.0 + i).tobytes())
+        gc.collect()
+        seen.append(made[freq.tobytes()]() is not None)
+        return 0
+    monkeypatch.setattr(streaming, "_frequencies", frequencies)
+    monkeypatch.setattr(recorder, "sa_qk_norm_rope_bwd" if backward else "sa_qk_norm_rope_fwd", call, raising=False)
+    q = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
+    if backward:
+        sa.qk_norm_rope_bwd(q, q, q, q, None, None, freq)
+    else:
+        sa.qk_norm_rope_fwd(q, q, None, None, freq)
+        sa.sa_qk_norm_rope_fwd(q, q, None, None, freq, None, q, q)
+    assert seen and all(seen)
 
 
 # ------------------------------------------------------------------ the oracle
