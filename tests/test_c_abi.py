@@ -26,6 +26,20 @@ def test_c_client_links_and_runs(tmp_path):
     assert "c abi ok" in out.stdout
 
 
+def test_first_tensor_maps_from_several_threads(tmp_path):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    cuda_home = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    exe = tmp_path / "first_encode"
+    subprocess.run([cxx, "-std=c++17", "-O1", "-pthread", "-I", os.path.join(cuda_home, "include"), "-I",
+                    os.path.join(ROOT, "content_adaptive_sparse_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "c", "first_encode.cpp"), "-o", str(exe)],
+                   check=True, capture_output=True, text=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0, out.stdout
+
+
 @pytest.mark.gpu
 def test_c_client_runs_the_hot_path_on_the_gpu(tmp_path):
     """A C program (tests/c/abi_gpu.c) runs sa_build_mask and sa_attn_fwd on the tiny
