@@ -4,8 +4,8 @@
 // (i - j <= window or j < sinks)". With P_ij = exp(s_ij - LSE_i), D_i = sum_d dO_id O_id:
 //   dP_ij = <dO_i, v_j>,  dS_ij = P_ij (dP_ij - D_i),
 //   dQ_i = c sum_j dS_ij k_j,  dK_j = c sum_i dS_ij q_i,  dV_j = sum_i P_ij dO_i.
-// Launches: sink_prep_kernel and, where few keys are seen, sink_few_kernel (D and -LSE log2(e), padded
-// to whole tiles), sink_bwd_kernel<D, false> (dQ: query-stationary), sink_bwd_kernel<D, true> (dK and
+// Launches: sink_prep_kernel or, where few keys are seen, sink_few_kernel (D and -LSE log2(e), padded to
+// whole tiles), sink_bwd_kernel<D, false> (dQ: query-stationary), sink_bwd_kernel<D, true> (dK and
 // dV: key-stationary, all query heads of the key head), and sink_reduce_kernel when the sinks' rows
 // were summed in parts. S and dP are taken twice, so every gradient row has one owner: no atomics,
 // the same bits every run.
@@ -105,7 +105,7 @@ struct BParams {
   int chunk_tiles, n_chunks;        // query tiles per sink chunk, sink chunks per (sequence, head)
   int far_tile;                     // first query tile whose window misses key tile 0
   const float* nl2;                 // [batch][heads][pitch]: -LSE log2(e); -inf past the sequence
-  const float* dvec;                // [batch][heads][pitch]: D
+  float* dvec;                      // [batch][heads][pitch]: D
   __nv_bfloat16* out0;              // dK (the sinks' rows, sink_reduce_kernel)
   __nv_bfloat16* out1;              // dV
   int64_t os_b[2], os_n[2], os_h[2];   // strides of out0, out1
@@ -532,9 +532,11 @@ struct Compute {
 
   // A step. Each way of seeing (SEE) has a copy of the code: joined by selects, the mask's
   // instructions would be issued in every step. `prev`: the item before, at an item's first step.
+  // `first`: the columns hold every key that the thread's row sees (the first tokens' rows, dQ only), and
+  // D goes to *first for dK / dV.
   template <int SEE>
-  __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see, float nl2, float dval, const Item* prev,
-                                       int n) const {
+  __device__ __forceinline__ bool step(int g, uint32_t vec, uint32_t see, float nl2, float dval, float* first,
+                                       const Item* prev, int n) const {
     const uint32_t tS = base + (uint32_t)(kCols * part) + col_s(g);
     const uint32_t tDP = base + (uint32_t)(kCols * part) + col_dp<C::SWAP>(g);
     if (!__all_sync(0xffffffffu, wait_pair(bars.s_full, g, abort_flag))) return false;
@@ -586,6 +588,14 @@ struct Compute {
       tmem_ld_x32(tDP, v);
       tmem_ld_wait<kCols>(v);
       if constexpr (C::SWAP) announce(&bars.dp_read);
+      if constexpr (!KV && SEE == kSome) {
+        if (first != nullptr) {
+          dval = 0.f;
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) dval = fmaf(pr[e], __uint_as_float(v[e]), dval);
+          *first = dval;
+        }
+      }
 #pragma unroll
       for (int e = 0; e < kCols; e += 4) {
         float4 L = make_float4(dval, dval, dval, dval);
@@ -628,10 +638,18 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
     it = walk.item(p);
     const int tok = it.tile * kTile + row;
     float nl2 = 0.f, dval = 0.f;
+    float* first = nullptr;
     if constexpr (!KV) {
       const int64_t at = ((int64_t)it.s * p.heads + it.head) * p.pitch + tok;
       nl2 = p.nl2[at];
       dval = p.dvec[at];
+      // O is stored in bf16, and in <dO, O> its rounding, 2^-9 of |dO| |O|, goes into every dS of the row
+      // alike: into dQ times the mean of the visible keys. That is little where many keys are seen (their
+      // mean is short, and dS has a rounding of its own); at two keys it took dQ's error from 0.0024 to
+      // 0.0046 of its size, at nine to 0.0027. The first kCols tokens see no other keys than one another, so
+      // this warp holds all of their P and dP, and their D is sum P dP. (The time is the same with and
+      // without: 4 x 8192 training 384 us; a launch of its own took 11 us in 2 x 200 tokens, 27 against 15.)
+      if (it.tile == 0 && quarter == 0 && part == 0) first = p.dvec + at;
     }
     Steps<KV> moving(p, it);
     if (KV && n > 0 && !W.write(prev, n - 1)) return;
@@ -641,9 +659,10 @@ __device__ void compute(const BParams& p, const CUtensorMap* to0, const CUtensor
       const int see = visibility<KV>(it.tile * kTile + 32 * quarter, c0, p.window, p.sinks);
       const Item* before = !KV && j == 0 && n > 0 ? &prev : nullptr;
       bool ok;
-      if (see == kAll) ok = W.template step<kAll>(g, vec, 0u, nl2, dval, before, n);
-      else if (see == kSome) ok = W.template step<kSome>(g, vec, visible<KV>(tok, c0, p.window, p.sinks), nl2, dval, before, n);
-      else ok = W.template step<kNone>(g, vec, 0u, nl2, dval, before, n);
+      if (see == kAll) ok = W.template step<kAll>(g, vec, 0u, nl2, dval, nullptr, before, n);
+      else if (see == kSome)
+        ok = W.template step<kSome>(g, vec, visible<KV>(tok, c0, p.window, p.sinks), nl2, dval, first, before, n);
+      else ok = W.template step<kNone>(g, vec, 0u, nl2, dval, nullptr, before, n);
       if (!ok) return;
     }
   }
@@ -802,22 +821,18 @@ __global__ void __launch_bounds__(256) sink_prep_kernel(const __grid_constant__ 
   }
 }
 
-// The same for tokens below `tokens` with D = sum of P dP. O is stored in bf16, and in <dO, O> its
-// rounding, 2^-9 of |dO| |O|, goes into every dS of the row alike: into dQ times the mean of the visible
-// keys. That is little where many keys are seen (their mean is short, and dS has a rounding of its
-// own); at two keys it took dQ's error from 0.0024 to 0.0046 of its size, at nine to 0.0027. So it is
-// done where no query sees more than kFewKeys keys (16K tokens of 16 heads of 128 at eight: 210 -> 322
-// us), and for the first kFewTokens of sequences of up to 8 kFewTokens, where the launch is short
-// beside the others; in longer ones it would cost 7 us for one row in hundreds.
-constexpr int kFewKeys = 8, kFewTokens = 32, kFewStep = 4;
+// The same with D = sum of P dP (the reason: Compute's `first`) for windows and sinks of which no query sees
+// more than kFewKeys keys. (16K tokens of 16 heads of 128 at eight: backward 210 -> 322 us; more would cost more
+// than the accuracy that is left to gain.)
+constexpr int kFewKeys = 8, kFewStep = 4;
 template <int D>
-__global__ void __launch_bounds__(256) sink_few_kernel(const __grid_constant__ PrepParams p, int tokens) {
+__global__ void __launch_bounds__(256) sink_few_kernel(const __grid_constant__ PrepParams p) {
   constexpr int G = D / 8;
   const int part = threadIdx.x % G;
   const uint32_t heads = (uint32_t)p.heads, n = (uint32_t)p.n_tokens;
   const uint32_t r = blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
   const uint32_t i = r / heads, h = r % heads, hk = h / (uint32_t)p.group;
-  const bool in = i < (uint32_t)tokens;
+  const bool in = i < (uint32_t)p.pitch;
   const int lo = max(0, (int)i - p.window), n_sink = min(p.sinks, lo);
   const int keys = in && i < n ? n_sink + (int)i - lo + 1 : 0;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -963,10 +978,8 @@ int launch_d(const SinkArgs& a, const SinkBwdWorkspace& ws, cudaStream_t stream)
   };
   const int64_t rows = (int64_t)p.pitch * a.heads;
   // token i sees min(i, window + sinks) + 1 keys
-  const bool all_few = a.n_tokens <= kFewTokens || (int64_t)a.window + a.sinks < kFewKeys;
-  if (!all_few) sink_prep_kernel<D><<<grid((rows + kPrepRows - 1) / kPrepRows), 256, 0, stream>>>(pp);
-  const int few = all_few ? p.pitch : (a.n_tokens <= 8 * kFewTokens ? kFewTokens : 0);
-  if (few > 0) sink_few_kernel<D><<<grid((int64_t)few * a.heads), 256, 0, stream>>>(pp, few);
+  if ((int64_t)a.window + a.sinks < kFewKeys) sink_few_kernel<D><<<grid(rows), 256, 0, stream>>>(pp);
+  else sink_prep_kernel<D><<<grid((rows + kPrepRows - 1) / kPrepRows), 256, 0, stream>>>(pp);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   int st = launch<D, false>(a, p, p.tiles, stream);
   if (st != SA_OK) return st;
