@@ -865,6 +865,14 @@ int check_sink(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads,
   return SA_OK;
 }
 
+// The backward counts a sequence's rows, padded to whole tiles, in 32 bits.
+int check_sink_bwd(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t& window,
+                   int32_t sinks) {
+  const int st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks);
+  if (st != SA_OK) return st;
+  return ((int64_t)n_tokens + 127) / 128 * 128 * heads >= (int64_t)1 << 31 ? SA_ERR_UNSUPPORTED : SA_OK;
+}
+
 int decode_args(const void* q, const void* k, const void* v, const int64_t qs[3], const int64_t os[3], int32_t batch,
                 int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim, const int32_t* d_lengths,
                 int32_t window, int32_t sinks, float softmax_scale, void* o, float* lse, sa::SinkDecodeArgs& a) {
@@ -1017,7 +1025,7 @@ int sa_sink_attn_fwd(const void* q, const void* k, const void* v, const int64_t 
 int sa_sink_attn_bwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t window, int32_t sinks, size_t* h_bytes) {
   if (!h_bytes) return SA_ERR_INVALID_ARG;
-  const int st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks);
+  const int st = check_sink_bwd(batch, n_tokens, heads, kv_heads, head_dim, window, sinks);
   if (st != SA_OK) return st;
   *h_bytes = sa::sink_bwd_workspace_layout(batch, n_tokens, heads, kv_heads, head_dim, window, sinks).bytes;
   return SA_OK;
@@ -1041,9 +1049,7 @@ int sa_sink_attn_bwd(const void* q, const void* k, const void* v, const void* o,
       !strides_ok(dv_strides))
     return SA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
-  if ((st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks)) != SA_OK) return st;
-  // a sequence's rows, padded to whole tiles, are counted in 32 bits
-  if (((int64_t)n_tokens + 127) / 128 * 128 * heads >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
+  if ((st = check_sink_bwd(batch, n_tokens, heads, kv_heads, head_dim, window, sinks)) != SA_OK) return st;
   if (!device_ok()) return SA_ERR_CUDA;
   sa::SinkArgs a;
   memset(&a, 0, sizeof(a));

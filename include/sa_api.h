@@ -390,7 +390,7 @@ int sa_sink_attn_fwd(const void* q, const void* k, const void* v, const int64_t 
                      int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t window,
                      int32_t sinks, float softmax_scale, void* o, float* lse, void* stream);
 
-/* Workspace bytes of sa_sink_attn_bwd. Host only. */
+/* Workspace bytes of sa_sink_attn_bwd; refuses the sizes that it refuses. Host only. */
 int sa_sink_attn_bwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t window, int32_t sinks, size_t* h_bytes);
 

@@ -129,6 +129,19 @@ def test_sink_workspace_size(lib):
             sa.sa_sink_attn_bwd_workspace_size(*bad)
 
 
+def test_sink_workspace_size_refuses_what_the_backward_refuses(lib):
+    c = sink(lib, True)
+    for batch, n, heads, kv_heads, d, s in ((1, (1 << 20) - 127, 2048, 2, 64, 4), (1, 1 << 24, 128, 128, 32, 0),
+                                            (1, (1 << 24) + 1, 4, 2, 64, 4), (1, 8, 4, 2, 96, 4), (1, 8, 4, 2, 64, 129)):
+        assert c.with_(batch=batch, n=n, heads=heads, kv_heads=kv_heads, d=d, sinks=s) == UNSUPPORTED
+        with pytest.raises(sa.SAError) as e:
+            sa.sa_sink_attn_bwd_workspace_size(batch, n, heads, kv_heads, d, 10, s)
+        assert e.value.code == UNSUPPORTED
+    # one tile less is taken (and then misses a device, or its workspace)
+    assert c.with_(batch=1, n=(1 << 24) - 128, heads=128, kv_heads=128, d=32) in (CAPACITY, -4)
+    assert sa.sa_sink_attn_bwd_workspace_size(1, (1 << 24) - 128, 128, 128, 32, 10, 0) == 2 * 4 * 128 * ((1 << 24) - 128)
+
+
 @pytest.mark.parametrize("cache4", [False, True])
 def test_decode_refusals(lib, cache4):
     a = dict(q=A, k=A, ks=A, v=A, vs=A) if cache4 else dict(q=A, k=A, v=A)
