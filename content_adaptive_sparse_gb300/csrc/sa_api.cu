@@ -810,7 +810,8 @@ void copy3(int64_t (&dst)[3], const int64_t src[3]) {
 
 bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
 
-bool scale_ok(float s) { return s > 0.f && s <= 3.4028234e38f; }
+// The kernels take the scale times log2(e), which has to be a number too.
+bool scale_ok(float s) { return s > 0.f && s * 1.4426950408889634f <= 3.4028234e38f; }
 
 // Arguments that both directions of the norm-and-rotation share; fills `a`.
 int norm_rope_args(const void* q, const void* k, const int64_t qs[3], const int64_t ks[3], int32_t batch,

@@ -384,7 +384,7 @@ int sa_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out, const
 
 /* Attention over the sink-window graph, forward. Shapes, strides, O and LSE as in sa_attn_fwd
  * (head_dim 32, 64 or 128), any n_tokens from 1 to 2^24; k and v have strides of
- * their own. */
+ * their own. softmax_scale (here and below): positive, and a number when taken times log2(e). */
 int sa_sink_attn_fwd(const void* q, const void* k, const void* v, const int64_t q_strides[3],
                      const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3], int32_t batch,
                      int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t window,

@@ -129,6 +129,18 @@ def test_sink_workspace_size(lib):
             sa.sa_sink_attn_bwd_workspace_size(*bad)
 
 
+def test_scales_that_overflow_in_log2_units(lib):
+    """2.4e38 log2(e) is no fp32 number; 2.3e38 log2(e) is, and the next check refuses the call."""
+    for backward in (False, True):
+        c = sink(lib, backward)
+        more = {"d": 96} if backward else {"d": 96, "lse": A}
+        assert c.with_(scale=2.4e38, **more) == INVALID and c.with_(scale=2.3e38, **more) == UNSUPPORTED
+    a = dict(q=A, k=A, v=A, qs=st(4, 64, 1), kst=st(2, 64, 64), vst=st(2, 64, 64), os=st(4, 64, 1), batch=2, capacity=64, heads=4,
+             kv_heads=2, d=80, lengths=A, window=10, sinks=4, scale=0.125, o=A, lse=A, stream=0)
+    c = Call(lib, "sa_sink_attn_decode", **a)
+    assert c.with_(scale=2.4e38) == INVALID and c.with_(scale=2.3e38) == UNSUPPORTED
+
+
 def test_sink_workspace_size_refuses_what_the_backward_refuses(lib):
     c = sink(lib, True)
     for batch, n, heads, kv_heads, d, s in ((1, (1 << 20) - 127, 2048, 2, 64, 4), (1, 1 << 24, 128, 128, 32, 0),
