@@ -317,8 +317,10 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
         qb[q][2 * i + (k >> 1)][k & 1] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    c[2 * q] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
-    c[2 * q + 1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    // (at least the smallest number: a key that is not seen has the score -inf, and -inf times 0 is NaN)
+    const float tiny = __int_as_float(1);
+    c[2 * q] = fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t), tiny);
+    c[2 * q + 1] = fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4), tiny);
     thr[2 * q] = thr[2 * q + 1] = kNegInf;
   }
   // The tile's row x (of both products) is cache row x / 2 + 4 (x % 2) of its half: the value rows of the

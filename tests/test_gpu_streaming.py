@@ -268,6 +268,29 @@ def test_decode_strided_cache_and_large_scores():
 
 # ------------------------------------------------------------------ numbers that are not numbers
 
+@pytest.mark.parametrize("scale", [1e-44, 1e-20, None])
+@pytest.mark.parametrize("h,hk,d", [(4, 2, 32), (24, 2, 64), (4, 2, 128)])
+def test_decode_of_zero_queries(h, hk, d, scale):
+    """A query of zeros sees every key alike, however small the scale: the mean of the values."""
+    torch = torch_cuda()
+    b, cap, w, s, lengths = 3, 72, 40, 3, [1, 13, 71]
+    q, qf = rand(0, b, 1, h, d)
+    q[:, :, 1] = 0.0
+    qf[:, :, 1] = 0.0
+    k, kf = rand(1, b, cap, hk, d)
+    v, vf = rand(2, b, cap, hk, d)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    cache = sa.cache4_alloc(b, cap, hk, d)
+    sa.cache4_append(cache, k, v)
+    got = sa.sink_attn_decode(q, k, v, n, w, s, scale), sa.sink_attn_decode_cache4(q, cache, n, w, s, scale)
+    status_ok()
+    quant = [ref.values(*ref.quantise(x)) for x in (kf, vf)]
+    for (o, lse), (kx, vx) in zip(got, ((kf, vf), quant)):
+        of, lf, ob = ref.sink_decode(qf, kx, vx, lengths, w, s, scale)
+        close(o, of, ob, "o")
+        close(lse, lf, LSE_TOL, "lse")
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("h", [4, 24])
 def test_decode_keeps_nan_of_what_is_seen(h, d):
