@@ -4,8 +4,8 @@
 Query i sees key j iff j <= i and (i - j <= window or j < sinks). ``sa_*`` functions carry the
 C ABI's names and write into tensors that the caller gives; the others allocate their outputs
 (and workspace) and make one call. Like the rest of the package this only marshals arguments: it
-checks what the C side cannot see (types, shapes and devices of tensors) and raises ``ValueError``,
-while the library's own refusals raise ``SAError``.
+checks what the C side cannot see (types, shapes and devices of tensors) or could not name (strides)
+and raises ``ValueError``, while the library's own refusals raise ``SAError``.
 """
 from __future__ import annotations
 
@@ -66,6 +66,7 @@ def _check(name: str, code: int) -> None:
 # stride arrays are kept by their values. Each helper raises with the argument's name.
 
 _MAX = 2**31 - 1
+_TOO_LARGE = "sizes of 2^31 and more are not supported"
 
 
 def _int(v: int) -> int:
@@ -81,12 +82,12 @@ def _s3(strides: tuple) -> _S3:
 
 @functools.lru_cache(maxsize=1024)
 def _layout(strides: tuple, shape: tuple):
-    """Strides of a tensor whose sizes fit in 32 bits, or None."""
-    return _S3(*strides[:3]) if max(shape) <= _MAX else None
-
-
-def _too_large(name: str):
-    raise ValueError(f"{name}: sizes of 2^31 and more are not supported")
+    """Strides of a tensor, or what the library would refuse in it without naming the tensor."""
+    if max(shape) > _MAX:
+        return _TOO_LARGE
+    if any(s <= 0 or s % 8 for s in strides[:3]):
+        return "strides must be positive multiples of 8 elements (an expanded tensor needs .contiguous())"
+    return _S3(*strides[:3])
 
 
 @functools.lru_cache(maxsize=64)
@@ -131,8 +132,8 @@ def _rows(name: str, t, device: int, shape=None) -> _S3:
     if t.get_device() != device:
         _elsewhere(name)
     layout = _layout(st, t.shape)
-    if layout is None:
-        _too_large(name)
+    if type(layout) is str:
+        raise ValueError(f"{name}: {layout}")
     return layout
 
 
@@ -358,7 +359,7 @@ def _cache4(cache, dev):
     if len(codes) != 4:
         raise ValueError("cache: expected codes of shape [batch, kv_heads, capacity, head_dim / 2]")
     if max(codes) > _MAX:
-        _too_large("cache")
+        raise ValueError(f"cache: {_TOO_LARGE}")
     b, hk, cap, half = codes
     scales = (b, hk, cap, half // 16)
     u8 = torch.uint8
@@ -402,7 +403,7 @@ def cache4_read(cache: Cache4, start, n_tokens: int):
     dev = _device()
     at, (b, hk, cap, d) = _cache4(cache, dev)
     if n_tokens > _MAX:
-        _too_large("n_tokens")
+        raise ValueError(f"n_tokens: {_TOO_LARGE}")
     k = torch.empty((b, n_tokens, hk, d), dtype=torch.bfloat16, device=cache[0].device)
     v = torch.empty_like(k)
     st = _dense(k.shape)

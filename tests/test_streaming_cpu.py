@@ -212,6 +212,19 @@ def test_binding_refuses_wrong_tensors():
         sa.cache4_append(cache, q, q)
 
 
+def test_expanded_and_misaligned_tensors_are_named():
+    """An expanded gradient, as a sum's backward gives it, and an odd stride."""
+    torch = pytest.importorskip("torch")
+    from content_adaptive_sparse_gb300 import streaming
+    streaming._device()
+    g = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    assert list(streaming._rows("d_o", g, -1)) == [512, 128, 64]
+    for bad in (g.expand(3, 4, 2, 64), g[:, :1].expand(1, 9, 2, 64), g[:, :, :1].expand(1, 4, 5, 64),
+                torch.zeros(1, 4, 2, 68, dtype=torch.bfloat16)[..., :64]):
+        with pytest.raises(ValueError, match="d_o: strides .*contiguous"):
+            streaming._rows("d_o", bad, -1)
+
+
 class Recorder:
     """In the library's place: keeps each call's arguments and succeeds."""
 
@@ -277,7 +290,8 @@ def test_sizes_past_32_bits(recorder, lib):
     for shape in ((2**32 + 1, 1, 1, 64), (1, 2**32 + 5, 1, 64), (1, 1, 2**31, 64)):
         with pytest.raises(ValueError, match="x: sizes"):
             streaming._rows("x", x.expand(shape), -1)
-    assert streaming._rows("x", x.expand(1, BIG, 1, 64), -1)[2] == 64
+    assert "sizes" in streaming._layout((64, 64, 64, 1), (1, BIG + 1, 1, 64))
+    assert streaming._layout((64, 64, 64, 1), (1, BIG, 1, 64))[1] == 64
     cache = sa.cache4_alloc(1, 8, 1, 64, device="cpu")
     with pytest.raises(ValueError, match="cache: sizes"):
         streaming._cache4([t[:, :, :1].expand(1, 1, 2**32 + 8, -1) for t in cache], -1)
