@@ -587,6 +587,41 @@ def test_attention_over_more_than_2_31_elements():
         close(x[:, -tail + 2 * w:], y[:, rows], e[:, rows], name)
 
 
+def test_first_tokens_of_more_than_2_31_elements():
+    """The first tokens' outputs and dQ (a persistent CTA's last items) are those of a short sequence, and the
+    sinks' dK and dV are the sums over all of a million queries."""
+    torch = torch_cuda()
+    n, h, d, w, s, head = (1 << 20) + 77, 17, 128, 100, 4, 300
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v, g = (torch.randn(1, n, h, d, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    assert q.numel() > 1 << 31
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    dq, dk, dv = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    first = [bf16_to_f64(x[:, :head]) for x in (q, k, v, g)]
+    of, lf, ob = ref.sink_attention(*first[:3], w, s)
+    close(o[:, :head], of, ob, "o")
+    close(lse[:, :, :head], lf, LSE_TOL, "lse")
+    want, bounds = ref.sink_attention_backward(*first, w, s)
+    close(dq[:, :head], want[0], bounds[0], "dq")
+    for e in (0, 9, h - 1):
+        kd, vd = k[0, :s, e].double(), v[0, :s, e].double()
+        sums = [torch.zeros(s, d, dtype=torch.float64, device="cuda") for _ in range(4)]
+        for i0 in range(0, n, 1 << 17):
+            rows = slice(i0, min(n, i0 + (1 << 17)))
+            qd, gd, od = (x[0, rows, e].double() for x in (q, g, o))
+            seen = torch.arange(s, device="cuda") <= torch.arange(rows.start, rows.stop, device="cuda")[:, None]
+            p = torch.where(seen, torch.exp(qd @ kd.T * d ** -0.5 - lse[0, e, rows].double()[:, None]), 0.0)
+            ds = p * (gd @ vd.T - (gd * od).sum(-1, keepdim=True)) * d ** -0.5
+            for x, y in zip(sums, (ds.T @ qd, p.T @ gd, ds.abs().T @ qd.abs(), p.T @ gd.abs())):
+                x += y
+        # as over many chunks: P and dS once rounded, and the result; P off by 2 LSE_TOL; fp32 sums of 1024
+        # rows in the tensor core and 1025 parts lose less than 2^-12 of the magnitudes
+        for name, got, total, size in (("dk", dk, sums[0], sums[2]), ("dv", dv, sums[1], sums[3])):
+            bound = 1.02 * ref.U * (total.abs() + size) + (2 * LSE_TOL + 2.0 ** -12) * size + 1e-6
+            close(got[0, :s, e], total.cpu().numpy(), bound.cpu().numpy(), name)
+
+
 def test_caches_of_more_than_2_31_elements():
     torch = torch_cuda()
     b, hk, h, d, w, s, tail = 3, 4, 8, 128, 40, 4, 64
