@@ -27,8 +27,10 @@
 // Measured: 64K tokens, 16 heads of 128, window 4095: 1432 us, 1489 TFLOP/s over the graph's edges, 0.80
 // of the library product's rate; what is lost is in whole tiles at the window's two edges (32 of 33 key
 // tiles' worth is visible) and in the handshakes of S, P and O between the issuing threads and the
-// softmax warps. 4 x 8192 tokens, 12 heads of 64, window 511: 97-100 us, bound by the exponentials (five
-// tiles of 128 keys for 512 visible ones, 55 us of them at 16 a clock and SM) and by the short items.
+// softmax warps (in a long loop, power-capped, 1570 us). 4 x 8192 tokens, 12 heads of 64, window 511: 92-100
+// us, of which the exponentials take 45 at 16 a clock and SM (557 keys a row on average, hidden 32-key chunks
+// left out). No pipe is full (issue 51 %, tensor 32 %): an item is 5.8 steps, and at its end both halves'
+// warps wait for its last products, the epilogue and the next Q.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -24,9 +24,10 @@
 // it by 2^8, which one vote shows.
 //
 // Measured: 64 sequences of up to 16000 tokens, 16 / 4 heads of 128, window 4095, bf16: 73 us, 6.7 TB/s,
-// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 74 us, 3.8 TB/s: the
-// instructions that unpack codes (372 per 16 rows) and 1.7 waves of CTAs. One sequence of 700
-// tokens, 12 heads of 64, window 511: 4.4 us, a launch, one load and the join.
+// a plain copy's rate. 32 sequences of 9001 to 32768 tokens, window 16383, 4 bits: 74 us, 3.8 TB/s:
+// 46.5 M instructions, mostly to unpack codes (372 per 16 rows), that would take some 40 us at full issue;
+// the issue slots are 59 % busy, since the CTAs are unequal and come in 1.7 waves, each with its fill and
+// join. One sequence of 700 tokens, 12 heads of 64, window 511: 4.4 us, a launch, one load and the join.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>

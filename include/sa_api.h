@@ -412,8 +412,10 @@ int sa_sink_attn_bwd(const void* q, const void* k, const void* v, const void* o,
  *          used), lse fp32 [batch][heads].
  *   k_cache, v_cache : bf16 [batch, capacity, kv_heads, head_dim]; rows that the
  *          query does not see may hold anything.
+ *          The cache is indexed by token: it holds the whole sequence, not the sinks and window alone.
  *   d_lengths : int32 [batch] on the device, tokens in each sequence's cache, the query's own key
- *          among them; values are taken into 0 .. capacity. Length 0: o = 0, lse = -inf.
+ *          among them; values are taken into 0 .. capacity, without a report (a longer sequence's query
+ *          would count as token capacity - 1). Length 0: o = 0, lse = -inf.
  * One launch without workspace. capacity <= 2^30. */
 int sa_sink_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int64_t q_strides[3],
                         const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3],
@@ -439,8 +441,9 @@ int sa_cache4_append(const void* k, const void* v, const int64_t k_strides[3], c
                      void* stream);
 
 /* The rows d_start[s] .. d_start[s] + n_tokens - 1 of the cache as bf16 (code * scale, rounded once) into
- * k and v, for example for a later chunk of a prompt that attends to them. Rows of a left-out sequence
- * and rows at or past the capacity (reported as by sa_cache4_append) come back as zeros. */
+ * k and v. (sa_sink_attn_fwd takes as many keys as queries: a later chunk of a prompt attends to these
+ * rows only in a call over the whole prompt.) Rows of a left-out sequence and rows at or past the
+ * capacity (reported as by sa_cache4_append) come back as zeros. */
 int sa_cache4_read(const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes, const void* v_scales,
                    int32_t batch, int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity,
                    const int32_t* d_start, void* k, void* v, const int64_t k_strides[3], const int64_t v_strides[3],
