@@ -951,13 +951,50 @@ assert sa.sa_device_status() == 0
 '''
 
 
-def test_first_calls_from_several_host_threads():
-    """A process whose first calls come from eight threads at once, each on a stream and with frequency
-    tables of its own (192 in all)."""
+def in_a_fresh_process(script):
     import os
     import subprocess
     import sys
     torch_cuda()
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    run = subprocess.run([sys.executable, "-c", FRESH], cwd=root, capture_output=True, text=True, timeout=300)
+    run = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-3000:]
+
+
+def test_first_calls_from_several_host_threads():
+    """A process whose first calls come from eight threads at once, each on a stream and with frequency
+    tables of its own (192 in all)."""
+    in_a_fresh_process(FRESH)
+
+
+CAPTURED = '''
+import numpy as np, torch
+import content_adaptive_sparse_gb300 as sa
+b, n, h, hk, d, w, s = 2, 300, 4, 2, 64, 30, 3
+torch.manual_seed(0)
+q, k, v, g = (torch.randn(b, n, x, d, device="cuda").bfloat16() for x in (h, hk, hk, h))
+length = torch.tensor([n, 100], dtype=torch.int32, device="cuda")
+freq = 100.0 ** (-np.arange(d // 2) / 32.0)
+cache = sa.cache4_alloc(b, 304, hk, d)
+wt = torch.ones(d, device="cuda")
+def chain():
+    qr, kr = sa.qk_norm_rope_fwd(q, k, wt, wt, freq)
+    o, lse = sa.sink_attn_fwd(qr, kr, v, w, s)
+    gr = sa.sink_attn_bwd(qr, kr, v, o, lse, g, w, s)
+    back = sa.qk_norm_rope_bwd(q, k, gr[0], gr[1], wt, wt, freq)
+    sa.cache4_append(cache, kr, v)
+    return (o, lse) + gr + back + sa.sink_attn_decode(qr[:, -1:], kr, v, length, w, s) + sa.sink_attn_decode_cache4(qr[:, -1:], cache, length, w, s) + sa.cache4_read(cache, None, n)
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    outs = chain()
+gr.replay(); torch.cuda.synchronize()
+got = [x.clone() for x in outs]
+assert all(torch.equal(x, y) for x, y in zip(got, chain()))
+torch.cuda.synchronize(); assert sa.sa_device_status() == 0
+'''
+
+
+def test_first_calls_inside_a_capture():
+    """A process that captures every call into a graph before it has made it once."""
+    in_a_fresh_process(CAPTURED)
