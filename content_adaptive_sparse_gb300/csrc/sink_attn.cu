@@ -24,7 +24,7 @@
 //   warps 10, 11  lane 0 issues O_h += P_h V_h (A = P from TMEM, B = V MN-major), h = 0, 1
 //   warps 12-15 epilogue: an item's rows through shared memory and TMA stores, under the next item
 //
-// Measured: 64K tokens, 16 heads of 128, window 4095: 1409-1450 us, 1489 TFLOP/s over the graph's edges, 0.80
+// Measured: 64K tokens, 16 heads of 128, window 4095: 1409-1450 us, 1470-1513 TFLOP/s over the graph's edges, 0.8
 // of the library product's rate; what is lost is in whole tiles at the window's two edges (32 of 33 key
 // tiles' worth is visible) and in the handshakes of S, P and O between the issuing threads and the
 // softmax warps (in a long loop, power-capped, 1570 us). 4 x 8192 tokens, 12 heads of 64, window 511: 92-100

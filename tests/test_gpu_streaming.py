@@ -335,6 +335,23 @@ def test_sink_attention_keeps_nan_queries(d):
     assert int(torch.isnan(lse).sum()) == 2 and not torch.isneginf(lse).any()
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("j", [2, 150])
+def test_sink_attention_keeps_nan_keys(j, d):
+    """A sink, or a key of the middle, with a NaN: NaN for the queries that see it and for no other."""
+    torch = torch_cuda()
+    b, n, h, w, s = 1, 300, 2, 40, 3
+    q, k, v = (rand(i, b, n, h, d)[0] for i in range(3))
+    o1, lse1 = sa.sink_attn_fwd(q, k, v, w, s)
+    k[0, j, 0, d // 2] = float("nan")
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    status_ok()
+    hit = torch.zeros(n, h, dtype=torch.bool, device="cuda")
+    hit[:, 0] = torch.from_numpy(ref.sink_mask(n, w, s)[:, j]).cuda()
+    assert torch.isnan(o[0][hit]).all() and torch.isnan(lse[0].T[hit]).all()
+    assert torch.equal(o[0][~hit], o1[0][~hit]) and torch.equal(lse[0].T[~hit], lse1[0].T[~hit])
+
+
 # ------------------------------------------------------------------ 4-bit cache
 
 @pytest.mark.parametrize("b,n,hk,d,cap,start", [(1, 1, 1, 32, 8, [7]), (2, 5, 3, 64, 16, [0, 11]), (3, 70, 2, 128, 96, [3, 26, 9]),
