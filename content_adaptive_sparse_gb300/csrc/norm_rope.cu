@@ -22,6 +22,10 @@
 // phase's top 32 bits (less than 2^-32 of a turn off) go to sincospif as fp32, half a turn at most, which
 // rounds them by 2^-26 of a turn at most.
 //
+// Several axes (time, height, width): the pair of a lane's angle takes the position of its own axis, one
+// load per lane and angle in place of one per token; everything else is the same. The one-axis form
+// is a kernel of its own (it may count the tokens itself).
+//
 // Measured, 4 x 8192 tokens, 12 + 12 heads of 64: forward 35.2 us (201 MB: 5.7 TB/s), backward with
 // the weights' gradients 55.9 us (302 MB: 5.4 TB/s), 0.84 and 0.80 of a plain copy's rate.
 #include <cuda_bf16.h>
@@ -48,13 +52,15 @@ struct RopeParams {
   Tensor out[2];            // forward: rotated q, k; backward: dq, dk
   const float* w[2];        // [D], or null: ones
   float* partial;           // backward: [grid][2][D] sums of g xh
-  const int32_t* positions; // [batch][n], or null: 0 .. n-1
+  const int32_t* positions; // [batch][n][n_axes], or null: 0 .. n-1
   int batch, n, heads[2];
   int heads_per_unit, chunks;           // a unit of work: a token and one of `chunks` ranges of its heads
   int step_c, step_i, step_s;           // units of one round of the grid's warps, as (chunk, token, sequence)
   int rotary;
   float eps;
   uint64_t turn[64];        // per pair: frequency / (2 pi) as a fraction of 2^64
+  int n_axes;
+  uint8_t axis[64];         // per pair: the axis whose position turns it
 };
 
 __device__ __forceinline__ void unpack2(uint32_t v, float& lo, float& hi) {
@@ -264,16 +270,16 @@ __device__ __forceinline__ void batch_rows(const RopeParams& p, const Cursor<STE
   }
 }
 
-// cos, sin and -sin of a lane's four pairs at `pos`: one angle per lane (two at D = 128), handed to the
-// lanes whose pair it is.
+// cos, sin and -sin of a lane's four pairs at `pos`: one angle per lane (two at D = 128), each with the
+// position of its pair's axis, handed to the lanes whose pair it is.
 template <int PPL>
-__device__ __forceinline__ void angles(int64_t pos, const uint64_t (&turn)[PPL], int t, uint64_t (&cs)[2],
+__device__ __forceinline__ void angles(const int64_t (&pos)[PPL], const uint64_t (&turn)[PPL], int t, uint64_t (&cs)[2],
                                        uint64_t (&sn)[2], uint64_t (&ns)[2]) {
   float my_c[PPL], my_s[PPL];
 #pragma unroll
   for (int k = 0; k < PPL; ++k) {
     // phase of a turn in [-2^31, 2^31) / 2^32; sincospif takes half turns
-    const int32_t phase = (int32_t)(((uint64_t)pos * turn[k]) >> 32);
+    const int32_t phase = (int32_t)(((uint64_t)pos[k] * turn[k]) >> 32);
     sincospif((float)phase * 4.656612873077393e-10f, &my_s[k], &my_c[k]);   // 2^-31
   }
   float c[4], s[4];
@@ -296,7 +302,7 @@ __device__ __forceinline__ void angles(int64_t pos, const uint64_t (&turn)[PPL],
   }
 }
 
-template <int D, bool INTER, bool BWD>
+template <int D, bool INTER, bool BWD, bool AXES>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<D, BWD>::CTAS) norm_rope_kernel(const __grid_constant__ RopeParams p) {
   using C = Cfg<D, BWD>;
   constexpr int LPR = C::LPR;
@@ -319,8 +325,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, BWD>::CTAS) norm_rope_kern
           p.w[warp] ? f2::pack(p.w[warp][element(e)], p.w[warp][element(e + 1)]) : f2::pack(1.f, 1.f);
   }
   uint64_t turn[PPL];
+  int axis[PPL];
 #pragma unroll
-  for (int k = 0; k < PPL; ++k) turn[k] = lane + 32 * k < half ? p.turn[lane + 32 * k] : 0ull;
+  for (int k = 0; k < PPL; ++k) {
+    turn[k] = lane + 32 * k < half ? p.turn[lane + 32 * k] : 0ull;
+    axis[k] = AXES && lane + 32 * k < half ? p.axis[lane + 32 * k] : 0;
+  }
   __syncthreads();
   uint64_t dw[2][4];
 #pragma unroll
@@ -343,7 +353,15 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, BWD>::CTAS) norm_rope_kern
     const int64_t tok = at.token(p);
     if (tok != angles_of) {
       angles_of = tok;
-      angles<PPL>(p.positions ? (int64_t)p.positions[tok] : at.i, turn, t, cs, sn, ns);
+      int64_t pos[PPL];
+      if constexpr (AXES) {
+#pragma unroll
+        for (int k = 0; k < PPL; ++k) pos[k] = p.positions[tok * p.n_axes + axis[k]];
+      } else {
+        pos[0] = p.positions ? (int64_t)p.positions[tok] : at.i;
+        pos[PPL - 1] = pos[0];
+      }
+      angles<PPL>(pos, turn, t, cs, sn, ns);
     }
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     const uint8_t* src = mine + stage * C::BATCH;
@@ -400,7 +418,7 @@ Tensor tensor(const void* ptr, const int64_t s[3]) {
   return Tensor{static_cast<const __nv_bfloat16*>(ptr), s[0], s[1], s[2]};
 }
 
-template <int D, bool INTER, bool BWD>
+template <int D, bool INTER, bool BWD, bool AXES>
 int launch(RopeParams& p, const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int RPW = 32 / (D / 8);
   const int all = a.heads + a.kv_heads;
@@ -423,7 +441,7 @@ int launch(RopeParams& p, const NormRopeArgs& a, cudaStream_t stream) {
   p.step_c = (int)(round % p.chunks);
   p.step_i = (int)(round / p.chunks % a.n_tokens);
   p.step_s = (int)(round / p.chunks / a.n_tokens);
-  const auto kern = norm_rope_kernel<D, INTER, BWD>;
+  const auto kern = norm_rope_kernel<D, INTER, BWD, AXES>;
   constexpr int kSmem = Cfg<D, BWD>::SMEM;
   if (kSmem > 48 * 1024 - 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
@@ -434,10 +452,16 @@ int launch(RopeParams& p, const NormRopeArgs& a, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
+template <int D, bool AXES>
+int launch_axes(RopeParams& p, const NormRopeArgs& a, cudaStream_t stream) {
+  if (a.backward)
+    return a.interleaved ? launch<D, true, true, AXES>(p, a, stream) : launch<D, false, true, AXES>(p, a, stream);
+  return a.interleaved ? launch<D, true, false, AXES>(p, a, stream) : launch<D, false, false, AXES>(p, a, stream);
+}
+
 template <int D>
 int launch_d(RopeParams& p, const NormRopeArgs& a, cudaStream_t stream) {
-  if (a.backward) return a.interleaved ? launch<D, true, true>(p, a, stream) : launch<D, false, true>(p, a, stream);
-  return a.interleaved ? launch<D, true, false>(p, a, stream) : launch<D, false, false>(p, a, stream);
+  return a.n_axes > 0 ? launch_axes<D, true>(p, a, stream) : launch_axes<D, false>(p, a, stream);
 }
 
 }  // namespace
@@ -465,7 +489,9 @@ int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
     // 2^64 is exact
     const double f = i < a.rotary_dim / 2 ? a.h_inv_freq[i] * 0.15915494309189533576888 : 0.0;
     p.turn[i] = (uint64_t)(f * 18446744073709551616.0);
+    p.axis[i] = a.n_axes > 0 && i < a.rotary_dim / 2 ? (uint8_t)a.h_pair_axis[i] : 0;
   }
+  p.n_axes = a.n_axes;
   switch (a.head_dim) {
     case 32: return launch_d<32>(p, a, stream);
     case 64: return launch_d<64>(p, a, stream);

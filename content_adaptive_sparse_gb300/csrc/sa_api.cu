@@ -853,6 +853,38 @@ int norm_rope_args(const void* q, const void* k, const int64_t qs[3], const int6
   return SA_OK;
 }
 
+// The positions of several axes, for arguments that norm_rope_args has taken.
+int axes_args(int32_t n_axes, const int32_t* h_pair_axis, sa::NormRopeArgs& a) {
+  if (n_axes <= 0 || !a.positions || (a.rotary_dim > 0 && !h_pair_axis)) return SA_ERR_INVALID_ARG;
+  if (n_axes > sa::kMaxAxes) return SA_ERR_UNSUPPORTED;
+  for (int i = 0; i < a.rotary_dim / 2; ++i)
+    if (h_pair_axis[i] < 0 || h_pair_axis[i] >= n_axes) return SA_ERR_INVALID_ARG;
+  a.n_axes = n_axes;
+  a.h_pair_axis = h_pair_axis;
+  return SA_OK;
+}
+
+size_t norm_rope_bwd_bytes(int32_t head_dim) { return (size_t)sa::kNormRopeMaxCtas * 2 * head_dim * sizeof(float); }
+
+// The rest of a backward call whose other arguments `a` holds.
+int norm_rope_bwd(sa::NormRopeArgs& a, const void* d_q_out, const void* d_k_out, const int64_t gqs[3], const int64_t gks[3],
+                  float* d_dq_weight, float* d_dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!d_q_out || !d_k_out || !gqs || !gks || !workspace) return SA_ERR_INVALID_ARG;
+  if (!aligned16(d_q_out) || !aligned16(d_k_out) || !strides_ok(gqs) || !strides_ok(gks)) return SA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
+  if (workspace_bytes < norm_rope_bwd_bytes(a.head_dim)) return SA_ERR_CAPACITY;
+  if (!device_ok()) return SA_ERR_CUDA;
+  a.backward = true;
+  a.d_q_out = d_q_out;
+  a.d_k_out = d_k_out;
+  copy3(a.dy_q_strides, gqs);
+  copy3(a.dy_k_strides, gks);
+  a.dq_weight = d_dq_weight;
+  a.dk_weight = d_dk_weight;
+  a.workspace = workspace;
+  return sa::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
 // Graph and size limits of the sink-window calls. The window is cut to the sequence.
 int check_sink(int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t& window,
                int32_t sinks) {
@@ -955,7 +987,7 @@ int sa_qk_norm_rope_fwd(const void* q, const void* k, const int64_t q_strides[3]
 int sa_qk_norm_rope_bwd_workspace_size(int32_t head_dim, size_t* h_bytes) {
   if (!h_bytes) return SA_ERR_INVALID_ARG;
   if (!head_dim_ok(head_dim)) return SA_ERR_UNSUPPORTED;
-  *h_bytes = (size_t)sa::kNormRopeMaxCtas * 2 * head_dim * sizeof(float);
+  *h_bytes = norm_rope_bwd_bytes(head_dim);
   return SA_OK;
 }
 
@@ -971,23 +1003,42 @@ int sa_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out, const
                                 d_k_weight, eps, h_inv_freq, rotary_dim, interleaved, d_positions, dq, dk, dq_strides,
                                 dk_strides, a);
   if (st != SA_OK) return st;
-  if (!d_q_out || !d_k_out || !d_q_out_strides || !d_k_out_strides || !workspace) return SA_ERR_INVALID_ARG;
-  if (!aligned16(d_q_out) || !aligned16(d_k_out) || !strides_ok(d_q_out_strides) || !strides_ok(d_k_out_strides))
-    return SA_ERR_UNSUPPORTED;
-  size_t need = 0;
-  sa_qk_norm_rope_bwd_workspace_size(head_dim, &need);
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
-  if (workspace_bytes < need) return SA_ERR_CAPACITY;
+  return norm_rope_bwd(a, d_q_out, d_k_out, d_q_out_strides, d_k_out_strides, d_dq_weight, d_dk_weight, workspace,
+                       workspace_bytes, stream);
+}
+
+int sa_qk_norm_rope_axes_fwd(const void* q, const void* k, const int64_t q_strides[3], const int64_t k_strides[3],
+                             int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                             const float* d_q_weight, const float* d_k_weight, float eps, const double* h_inv_freq,
+                             int32_t rotary_dim, int32_t interleaved, int32_t n_axes, const int32_t* h_pair_axis,
+                             const int32_t* d_positions, void* q_out, void* k_out, const int64_t q_out_strides[3],
+                             const int64_t k_out_strides[3], void* stream) {
+  sa::NormRopeArgs a;
+  int st = norm_rope_args(q, k, q_strides, k_strides, batch, n_tokens, heads, kv_heads, head_dim, d_q_weight,
+                          d_k_weight, eps, h_inv_freq, rotary_dim, interleaved, d_positions, q_out, k_out,
+                          q_out_strides, k_out_strides, a);
+  if (st == SA_OK) st = axes_args(n_axes, h_pair_axis, a);
+  if (st != SA_OK) return st;
   if (!device_ok()) return SA_ERR_CUDA;
-  a.backward = true;
-  a.d_q_out = d_q_out;
-  a.d_k_out = d_k_out;
-  copy3(a.dy_q_strides, d_q_out_strides);
-  copy3(a.dy_k_strides, d_k_out_strides);
-  a.dq_weight = d_dq_weight;
-  a.dk_weight = d_dk_weight;
-  a.workspace = workspace;
   return sa::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_qk_norm_rope_axes_bwd(const void* q, const void* k, const void* d_q_out, const void* d_k_out,
+                             const int64_t q_strides[3], const int64_t k_strides[3], const int64_t d_q_out_strides[3],
+                             const int64_t d_k_out_strides[3], int32_t batch, int32_t n_tokens, int32_t heads,
+                             int32_t kv_heads, int32_t head_dim, const float* d_q_weight, const float* d_k_weight,
+                             float eps, const double* h_inv_freq, int32_t rotary_dim, int32_t interleaved,
+                             int32_t n_axes, const int32_t* h_pair_axis, const int32_t* d_positions, void* dq, void* dk,
+                             const int64_t dq_strides[3], const int64_t dk_strides[3], float* d_dq_weight,
+                             float* d_dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  sa::NormRopeArgs a;
+  int st = norm_rope_args(q, k, q_strides, k_strides, batch, n_tokens, heads, kv_heads, head_dim, d_q_weight,
+                          d_k_weight, eps, h_inv_freq, rotary_dim, interleaved, d_positions, dq, dk, dq_strides,
+                          dk_strides, a);
+  if (st == SA_OK) st = axes_args(n_axes, h_pair_axis, a);
+  if (st != SA_OK) return st;
+  return norm_rope_bwd(a, d_q_out, d_k_out, d_q_out_strides, d_k_out_strides, d_dq_weight, d_dk_weight, workspace,
+                       workspace_bytes, stream);
 }
 
 int sa_sink_attn_fwd(const void* q, const void* k, const void* v, const int64_t q_strides[3],

@@ -137,6 +137,7 @@ unsigned int bwd_read_and_clear_error(cudaStream_t stream);
 
 // norm_rope.cu
 constexpr int kNormRopeMaxCtas = 2048;   // CTAs of a launch at most (partial weight gradients)
+constexpr int kMaxAxes = 8;
 struct NormRopeArgs {
   bool backward;
   const void* q;
@@ -151,7 +152,9 @@ struct NormRopeArgs {
   const float* k_weight;
   float eps;
   const double* h_inv_freq;              // host, [rotary_dim / 2]
-  const int32_t* positions;              // [batch][n_tokens] or null
+  int32_t n_axes;                        // 0: one position per token
+  const int32_t* h_pair_axis;            // host, [rotary_dim / 2], where n_axes > 0
+  const int32_t* positions;              // [batch][n_tokens] or null; n_axes > 0: [batch][n_tokens][n_axes]
   float* dq_weight;                      // backward, [head_dim] or null
   float* dk_weight;
   void* workspace;                       // backward: [kNormRopeMaxCtas][2][head_dim] floats

@@ -26,12 +26,16 @@ def declare(lib) -> None:
     global _LIB
     sizes = [_I32] * 5
     rope = [_P, _P, _F32, _P, _I32, _I32, _P]          # weights, eps, frequencies, rotary, interleaved, positions
+    axes = rope[:-1] + [_I32, _P, _P]                  # ..., interleaved, axes, axis of each pair, positions
     sink = [_I32] * 7 + [_F32]                         # batch, tokens, heads, kv_heads, dim, window, sinks; scale
     decode = [_I32] * 5 + [_P, _I32, _I32, _F32, _P, _P, _P]
     signatures = {
         "sa_qk_norm_rope_fwd": [_P, _P, _S3, _S3] + sizes + rope + [_P, _P, _S3, _S3, _P],
         "sa_qk_norm_rope_bwd_workspace_size": [_I32, _P],
         "sa_qk_norm_rope_bwd": [_P] * 4 + [_S3] * 4 + sizes + rope + [_P, _P, _S3, _S3, _P, _P, _P, ctypes.c_size_t, _P],
+        "sa_qk_norm_rope_axes_fwd": [_P, _P, _S3, _S3] + sizes + axes + [_P, _P, _S3, _S3, _P],
+        "sa_qk_norm_rope_axes_bwd": [_P] * 4 + [_S3] * 4 + sizes + axes + [_P, _P, _S3, _S3, _P, _P, _P, ctypes.c_size_t,
+                                                                          _P],
         "sa_sink_attn_fwd": [_P] * 3 + [_S3] * 4 + sink + [_P, _P, _P],
         "sa_sink_attn_bwd_workspace_size": [_I32] * 7 + [_P],
         "sa_sink_attn_bwd": [_P] * 6 + [_S3] * 5 + sink + [_P] * 3 + [_S3] * 3 + [_P, ctypes.c_size_t, _P],
@@ -183,7 +187,15 @@ def _like(t):
 
 # ------------------------------------------------------------------ norm and rotation of queries and keys
 
-def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev):
+@functools.lru_cache(maxsize=64)
+def _axes(pair_axes: tuple):
+    """A host array of the pairs' axes (kept by the caller, as `_frequencies`)."""
+    if any(not -_MAX <= a <= _MAX for a in pair_axes):
+        raise ValueError("pair_axes: expected axes of the positions")
+    return (ctypes.c_int32 * len(pair_axes))(*pair_axes) if pair_axes else None
+
+
+def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev, pair_axes=None):
     qs, ks = _rows("q", q, dev), _rows("k", k, dev)
     _same_sequence(q, k)
     b, n, h, d = q.shape
@@ -193,9 +205,19 @@ def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, 
         raise ValueError("inv_freq: expected one frequency per rotated pair")
     freq = _frequencies(inv_freq.tobytes())
     f32 = torch.float32
+    if pair_axes is None:
+        places = (_flat("positions", positions, torch.int32, (b, n), dev),)
+    else:
+        axes = tuple(map(int, pair_axes))
+        if len(axes) != inv_freq.size:
+            raise ValueError("pair_axes: expected one axis per frequency")
+        if positions is None or len(positions.shape) != 3:
+            raise ValueError("positions: expected an int32 [batch, tokens, axes] tensor")
+        a = positions.shape[2]
+        places = (_int(a), _axes(axes), _flat("positions", positions, torch.int32, (b, n, a), dev))
     return (q.data_ptr(), k.data_ptr()), (qs, ks), (
         b, n, h, k.shape[2], d, _flat("q_weight", q_weight, f32, (d,), dev), _flat("k_weight", k_weight, f32, (d,), dev),
-        eps, freq, _int(2 * inv_freq.size), 1 if interleaved else 0, _flat("positions", positions, torch.int32, (b, n), dev))
+        eps, freq, _int(2 * inv_freq.size), 1 if interleaved else 0, *places)
 
 
 def sa_qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps: float = 1e-6,
@@ -253,6 +275,59 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, posit
     ws = torch.empty(sa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dev)
     sa_qk_norm_rope_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, positions, dq, dk, dqw, dkw, ws, eps,
                         interleaved)
+    return dq, dk, dqw, dkw
+
+
+# with a position per axis (time, height, width): `pair_axes` is a host sequence of one axis per rotated
+# pair, `positions` int32 [batch, tokens, axes]
+
+def sa_qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, inv_freq, pair_axes, positions, q_out, k_out, eps: float = 1e-6,
+                             interleaved: bool = False, stream=None) -> None:
+    """sa_qk_norm_rope_fwd with pair p turned by positions[..., pair_axes[p]] * inv_freq[p]."""
+    dev = _device()
+    ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev, pair_axes)
+    _check("sa_qk_norm_rope_axes_fwd", _lib().sa_qk_norm_rope_axes_fwd(
+        *ptrs, *strides, *args, q_out.data_ptr(), k_out.data_ptr(), _rows("q_out", q_out, dev, q.shape),
+        _rows("k_out", k_out, dev, k.shape), _stream(stream, dev)))
+
+
+def sa_qk_norm_rope_axes_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, pair_axes, positions, dq, dk, dq_weight,
+                             dk_weight, workspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Gradients of sa_qk_norm_rope_axes_fwd; the weights' (fp32 [head_dim]) may be None."""
+    dev = _device()
+    ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev, pair_axes)
+    d = (q.shape[3],)
+    _check("sa_qk_norm_rope_axes_bwd", _lib().sa_qk_norm_rope_axes_bwd(
+        *ptrs, d_q_out.data_ptr(), d_k_out.data_ptr(), *strides, _rows("d_q_out", d_q_out, dev, q.shape),
+        _rows("d_k_out", d_k_out, dev, k.shape), *args, dq.data_ptr(), dk.data_ptr(), _rows("dq", dq, dev, q.shape),
+        _rows("dk", dk, dev, k.shape), _flat("dq_weight", dq_weight, torch.float32, d, dev),
+        _flat("dk_weight", dk_weight, torch.float32, d, dev), *_workspace(workspace, dev), _stream(stream, dev)))
+
+
+def qk_norm_rope_axes_fwd(q, k, q_weight, k_weight, inv_freq, pair_axes, positions, eps: float = 1e-6,
+                          interleaved: bool = False):
+    """Returns (q_out, k_out), contiguous."""
+    dev = _device()
+    ptrs, strides, args = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev, pair_axes)
+    q_out, k_out = _like(q), _like(k)
+    _check("sa_qk_norm_rope_axes_fwd", _lib().sa_qk_norm_rope_axes_fwd(
+        *ptrs, *strides, *args, q_out.data_ptr(), k_out.data_ptr(), _dense(q.shape), _dense(k.shape), _stream(None, dev)))
+    return q_out, k_out
+
+
+def qk_norm_rope_axes_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, pair_axes, positions, eps: float = 1e-6,
+                          interleaved: bool = False):
+    """Returns (dq, dk, dq_weight, dk_weight); a weight given as None has the gradient None."""
+    at = _device()
+    _rows("q", q, at)
+    _rows("k", k, at)
+    d, dev = q.shape[3], q.device
+    dq, dk = _like(q), _like(k)
+    dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    ws = torch.empty(sa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dev)
+    sa_qk_norm_rope_axes_bwd(q, k, d_q_out, d_k_out, q_weight, k_weight, inv_freq, pair_axes, positions, dq, dk, dqw, dkw,
+                             ws, eps, interleaved)
     return dq, dk, dqw, dkw
 
 
@@ -482,6 +557,7 @@ def sink_attn_decode_cache4(q, cache: Cache4, lengths, window: int, sinks: int, 
 
 NAMES = [
     "sa_qk_norm_rope_fwd", "sa_qk_norm_rope_bwd", "sa_qk_norm_rope_bwd_workspace_size", "sa_sink_attn_fwd",
+    "sa_qk_norm_rope_axes_fwd", "sa_qk_norm_rope_axes_bwd", "qk_norm_rope_axes_fwd", "qk_norm_rope_axes_bwd",
     "sa_sink_attn_bwd", "sa_sink_attn_bwd_workspace_size", "sa_sink_attn_decode", "sa_sink_attn_decode_cache4",
     "sa_cache4_append", "sa_cache4_read",
     "qk_norm_rope_fwd", "qk_norm_rope_bwd", "sink_attn_fwd", "sink_attn_bwd", "sink_attn_decode",

@@ -382,6 +382,29 @@ int sa_qk_norm_rope_bwd(const void* q, const void* k, const void* d_q_out, const
                         void* dq, void* dk, const int64_t dq_strides[3], const int64_t dk_strides[3],
                         float* d_dq_weight, float* d_dk_weight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* sa_qk_norm_rope_fwd / _bwd with positions on several axes (time, height and width of a video's
+ * patches): pair p of the first rotary_dim elements is turned by position[h_pair_axis[p]] * h_inv_freq[p].
+ *   n_axes       : 1 .. 8.
+ *   h_pair_axis  : host int32 [rotary_dim / 2], each in [0, n_axes); read before the call returns (may be
+ *                  NULL where rotary_dim is 0).
+ *   d_positions  : int32 [batch][n_tokens][n_axes], any values; not NULL.
+ * Every other argument, limit and error as there; the backward's workspace is
+ * sa_qk_norm_rope_bwd_workspace_size bytes. */
+int sa_qk_norm_rope_axes_fwd(const void* q, const void* k, const int64_t q_strides[3], const int64_t k_strides[3],
+                             int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                             const float* d_q_weight, const float* d_k_weight, float eps, const double* h_inv_freq,
+                             int32_t rotary_dim, int32_t interleaved, int32_t n_axes, const int32_t* h_pair_axis,
+                             const int32_t* d_positions, void* q_out, void* k_out, const int64_t q_out_strides[3],
+                             const int64_t k_out_strides[3], void* stream);
+int sa_qk_norm_rope_axes_bwd(const void* q, const void* k, const void* d_q_out, const void* d_k_out,
+                             const int64_t q_strides[3], const int64_t k_strides[3], const int64_t d_q_out_strides[3],
+                             const int64_t d_k_out_strides[3], int32_t batch, int32_t n_tokens, int32_t heads,
+                             int32_t kv_heads, int32_t head_dim, const float* d_q_weight, const float* d_k_weight,
+                             float eps, const double* h_inv_freq, int32_t rotary_dim, int32_t interleaved,
+                             int32_t n_axes, const int32_t* h_pair_axis, const int32_t* d_positions, void* dq, void* dk,
+                             const int64_t dq_strides[3], const int64_t dk_strides[3], float* d_dq_weight,
+                             float* d_dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Attention over the sink-window graph, forward. Shapes, strides, O and LSE as in sa_attn_fwd
  * (head_dim 32, 64 or 128), any n_tokens from 1 to 2^24; k and v have strides of
  * their own. softmax_scale (here and below): positive, and a number when taken times log2(e). */

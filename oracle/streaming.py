@@ -97,13 +97,19 @@ def _pairs(rotary, interleaved):
     return (2 * p, 2 * p + 1) if interleaved else (p, p + rotary // 2)
 
 
+def _turns(positions, inv_freq):
+    """Angles [b, n, 1, pairs] of positions [b, n], or [b, n, pairs] where each pair has its own."""
+    own = positions[:, :, None, None] if positions.ndim == 2 else positions[:, :, None, :]
+    return own.astype(np.float64) * np.asarray(inv_freq)
+
+
 def norm_rope(x, w, positions, inv_freq, eps, interleaved):
-    """x [b, n, h, d], positions [b, n]; y and the bound of the kernel's error (one bf16 rounding; fp32
+    """x [b, n, h, d], positions [b, n] (or [b, n, pairs]); y and the bound of the kernel's error (one bf16 rounding; fp32
     sums, products and angles below 4e-6 of the magnitudes that they combine)."""
     y = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w
     out, mag = y.copy(), np.abs(y)
     a, c = _pairs(2 * len(inv_freq), interleaved)
-    t = positions[:, :, None, None].astype(np.float64) * np.asarray(inv_freq)
+    t = _turns(positions, inv_freq)
     out[..., a] = y[..., a] * np.cos(t) - y[..., c] * np.sin(t)
     out[..., c] = y[..., c] * np.cos(t) + y[..., a] * np.sin(t)
     both = mag[..., a] + mag[..., c]
@@ -117,7 +123,7 @@ def norm_rope_backward(x, w, dy, positions, inv_freq, eps, interleaved):
     d = x.shape[-1]
     g = dy.copy()
     a, c = _pairs(2 * len(inv_freq), interleaved)
-    t = positions[:, :, None, None].astype(np.float64) * np.asarray(inv_freq)
+    t = _turns(positions, inv_freq)
     g[..., a] = dy[..., a] * np.cos(t) + dy[..., c] * np.sin(t)
     g[..., c] = dy[..., c] * np.cos(t) - dy[..., a] * np.sin(t)
     rstd = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
