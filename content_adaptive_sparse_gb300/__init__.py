@@ -7,7 +7,8 @@ if the library is missing or the device is not an sm_103 GPU, calls raise.
 
 Names follow the C ABI: ``sa_build_mask``, ``sa_attn_fwd``, ``sa_attn_fwd_heads``,
 ``sa_offset_attn_fwd``, ``sa_offset_attn_fwd_list``, ``sa_fib_offsets``, ``sa_pow2_offsets``, ``sa_layer_alpha``, ``sa_block_ratios``, ``sa_mask_nnz_bound``, ``sa_device_status``;
-the streaming-attention calls (norm and rotation, sink window, decoding, 4-bit cache) are in ``streaming.py``.
+the streaming-attention calls (norm and rotation, sink window, decoding, 4-bit cache) are in ``streaming.py``, those of
+shared prefixes and of caches with accumulated weights in ``context.py``.
 """
 from __future__ import annotations
 
@@ -16,8 +17,10 @@ import os
 
 import numpy as np
 
+from . import context as _context
 from . import streaming as _streaming
 from .build import LIB, build as build_library
+from .context import *  # noqa: F401,F403
 from .streaming import *  # noqa: F401,F403
 
 MASK_TOPK, MASK_BIGBIRD, MASK_FULL, MASK_LITERAL_MEAN = 0, 1, 2, 3
@@ -98,6 +101,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                  "sa_device_status", "sa_selftest_bounded_wait", "sa_build_mask_from_bytes"):
         getattr(lib, name).restype = ctypes.c_int
     _streaming.declare(lib)
+    _context.declare(lib)
     _lib = lib
     return lib
 
@@ -441,4 +445,6 @@ __all__ = [
     "MASK_TOPK", "MASK_BIGBIRD", "MASK_FULL", "MASK_LITERAL_MEAN", "LITERAL_LOCAL", "LITERAL_PAIRS",
     # streaming attention (norm and rotation, sink-window graph, single tokens over a cache)
     *_streaming.NAMES,
+    # shared prefixes, caches with accumulated weights
+    *_context.NAMES,
 ]

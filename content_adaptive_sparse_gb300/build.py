@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsa.so")
 SOURCES = ["sa_api.cu", "mask_build.cu", "attn_fwd.cu", "attn_bwd.cu", "offset_attn.cu", "offset_interp.cu",
-           "norm_rope.cu", "sink_attn.cu", "sink_bwd.cu", "sink_decode.cu", "sink_cache4.cu"]
+           "norm_rope.cu", "sink_attn.cu", "sink_bwd.cu", "sink_decode.cu", "sink_cache4.cu",
+           "prefix_attn.cu", "scored_cache.cu", "sink_weights.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

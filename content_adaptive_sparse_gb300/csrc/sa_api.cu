@@ -937,6 +937,73 @@ int decode_args(const void* q, const void* k, const void* v, const int64_t qs[3]
   return SA_OK;
 }
 
+// Sizes and graph of the calls behind a shared prefix. The window is cut to the own tokens.
+int check_prefix(int32_t batch, int32_t n_tokens, int32_t prefix, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                 int32_t& window) {
+  if (batch <= 0 || n_tokens <= 0 || prefix < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || window < 0)
+    return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || n_tokens > (1 << 24) || prefix > (1 << 30)) return SA_ERR_UNSUPPORTED;
+  // rows and work items are counted in 32 bits
+  const int64_t tiles = ((int64_t)n_tokens * (heads / kv_heads) + 127) / 128;
+  if ((int64_t)batch * heads > (1 << 24) || (int64_t)batch * kv_heads * tiles > (1 << 24)) return SA_ERR_UNSUPPORTED;
+  if (window > n_tokens - 1) window = n_tokens - 1;
+  return SA_OK;
+}
+
+int prefix_rows(const void* kp, const void* vp, const int64_t kps[3], const int64_t vps[3], int32_t prefix) {
+  if (prefix == 0) return SA_OK;
+  if (!kp || !vp || !kps || !vps) return SA_ERR_INVALID_ARG;
+  if (!aligned16(kp) || !aligned16(vp)) return SA_ERR_UNSUPPORTED;
+  for (int i = 1; i < 3; ++i)
+    if (kps[i] <= 0 || kps[i] % 8 != 0 || vps[i] <= 0 || vps[i] % 8 != 0) return SA_ERR_UNSUPPORTED;
+  return SA_OK;
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!workspace) return SA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SA_ERR_UNSUPPORTED;
+  return bytes < need ? SA_ERR_CAPACITY : SA_OK;
+}
+
+// The prefix's part of both calls; its tensors have no batch.
+void prefix_args(const void* q, const void* kp, const void* vp, const int64_t qs[3], const int64_t kps[3],
+                 const int64_t vps[3], const int64_t os[3], int32_t batch, int32_t n_tokens, int32_t prefix, int32_t heads,
+                 int32_t kv_heads, int32_t head_dim, int32_t window, float scale, void* o, float* lse, void* workspace,
+                 sa::PrefixArgs& a) {
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k_prefix = kp;
+  a.v_prefix = vp;
+  a.o = o;
+  a.lse = lse;
+  copy3(a.q_strides, qs);
+  copy3(a.o_strides, os);
+  for (int i = 0; i < 3 && prefix > 0; ++i) {
+    a.k_prefix_strides[i] = kps[i > 0 ? i : 1];
+    a.v_prefix_strides[i] = vps[i > 0 ? i : 1];
+  }
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.prefix = prefix;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.window = window;
+  a.softmax_scale = scale;
+  a.workspace = workspace;
+}
+
+size_t scored_bytes(int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads) {
+  const size_t head_groups = (size_t)(heads / kv_heads + 15) / 16;
+  return (size_t)batch * kv_heads * head_groups * capacity * sa::scored_stride(heads, kv_heads) * sizeof(float);
+}
+
+int check_scored(int32_t batch, int32_t capacity, int32_t kv_heads, int32_t head_dim) {
+  if (batch <= 0 || capacity <= 0 || kv_heads <= 0) return SA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || capacity > sa::kMaxScoredCapacity) return SA_ERR_UNSUPPORTED;
+  return batch > 32767 || kv_heads > 65535 ? SA_ERR_UNSUPPORTED : SA_OK;   // grids
+}
+
 int cache4_args(const void* k, const void* v, const int64_t kst[3], const int64_t vst[3], int32_t batch,
                 int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity, const int32_t* d_start,
                 const void* kc, const void* ks, const void* vc, const void* vs, sa::Cache4Args& a) {
@@ -1195,6 +1262,232 @@ int sa_cache4_read(const uint8_t* k_codes, const void* k_scales, const uint8_t* 
   return sa::launch_cache4(a, static_cast<cudaStream_t>(stream));
 }
 
+int sa_prefix_attn_fwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t prefix_tokens, int32_t heads,
+                                      int32_t kv_heads, int32_t head_dim, int32_t window, size_t* h_bytes) {
+  if (!h_bytes) return SA_ERR_INVALID_ARG;
+  const int st = check_prefix(batch, n_tokens, prefix_tokens, heads, kv_heads, head_dim, window);
+  if (st != SA_OK) return st;
+  *h_bytes = sa::prefix_workspace(batch, n_tokens, prefix_tokens, heads, kv_heads, head_dim, window, false).bytes;
+  return SA_OK;
+}
+
+int sa_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                       const int64_t q_strides[3], const int64_t k_prefix_strides[3], const int64_t v_prefix_strides[3],
+                       const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3], int32_t batch,
+                       int32_t n_tokens, int32_t prefix_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                       int32_t window, float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  int st = check_attn_common(q, k, v, q_strides, k_strides, o_strides, batch, n_tokens, heads, kv_heads, o, lse);
+  if (st != SA_OK) return st;
+  if (!v_strides) return SA_ERR_INVALID_ARG;
+  if (!strides_ok(v_strides)) return SA_ERR_UNSUPPORTED;
+  if (!scale_ok(softmax_scale)) return SA_ERR_INVALID_ARG;
+  if ((st = check_prefix(batch, n_tokens, prefix_tokens, heads, kv_heads, head_dim, window)) != SA_OK) return st;
+  if ((st = prefix_rows(k_prefix, v_prefix, k_prefix_strides, v_prefix_strides, prefix_tokens)) != SA_OK) return st;
+  const sa::PrefixWorkspace w =
+      sa::prefix_workspace(batch, n_tokens, prefix_tokens, heads, kv_heads, head_dim, window, false);
+  if ((st = check_workspace(workspace, workspace_bytes, w.bytes)) != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  sa::PrefixArgs a;
+  prefix_args(q, k_prefix, v_prefix, q_strides, k_prefix_strides, v_prefix_strides, o_strides, batch, n_tokens,
+              prefix_tokens, heads, kv_heads, head_dim, window, softmax_scale, o, lse, workspace, a);
+  a.k = k;
+  a.v = v;
+  copy3(a.k_strides, k_strides);
+  copy3(a.v_strides, v_strides);
+  return sa::launch_prefix_attn(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_prefix_attn_decode_workspace_size(int32_t batch, int32_t prefix_tokens, int32_t heads, int32_t kv_heads,
+                                         int32_t head_dim, size_t* h_bytes) {
+  int32_t window = 0;
+  if (!h_bytes) return SA_ERR_INVALID_ARG;
+  const int st = check_prefix(batch, 1, prefix_tokens, heads, kv_heads, head_dim, window);
+  if (st != SA_OK) return st;
+  *h_bytes = sa::prefix_workspace(batch, 1, prefix_tokens, heads, kv_heads, head_dim, 0, true).bytes;
+  return SA_OK;
+}
+
+int sa_prefix_attn_decode(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
+                          const void* v_cache, const int64_t q_strides[3], const int64_t k_prefix_strides[3],
+                          const int64_t v_prefix_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
+                          const int64_t o_strides[3], int32_t batch, int32_t prefix_tokens, int32_t capacity,
+                          int32_t heads, int32_t kv_heads, int32_t head_dim, const int32_t* d_lengths, int32_t window,
+                          float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  sa::SinkDecodeArgs d;
+  int st = decode_args(q, k_cache, v_cache, q_strides, o_strides, batch, capacity, heads, kv_heads, head_dim, d_lengths,
+                       window, 0, softmax_scale, o, lse, d);
+  if (st != SA_OK) return st;
+  if (!k_strides || !v_strides) return SA_ERR_INVALID_ARG;
+  if (!strides_ok(k_strides) || !strides_ok(v_strides)) return SA_ERR_UNSUPPORTED;
+  int32_t none = 0;
+  if ((st = check_prefix(batch, 1, prefix_tokens, heads, kv_heads, head_dim, none)) != SA_OK) return st;
+  if ((st = prefix_rows(k_prefix, v_prefix, k_prefix_strides, v_prefix_strides, prefix_tokens)) != SA_OK) return st;
+  const sa::PrefixWorkspace w = sa::prefix_workspace(batch, 1, prefix_tokens, heads, kv_heads, head_dim, 0, true);
+  if ((st = check_workspace(workspace, workspace_bytes, w.bytes)) != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  copy3(d.k_strides, k_strides);
+  copy3(d.v_strides, v_strides);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (prefix_tokens > 0) {
+    sa::PrefixArgs a;
+    prefix_args(q, k_prefix, v_prefix, q_strides, k_prefix_strides, v_prefix_strides, o_strides, batch, 1, prefix_tokens,
+                heads, kv_heads, head_dim, 0, softmax_scale, o, lse, workspace, a);
+    a.decode = true;
+    if ((st = sa::launch_prefix_attn(a, s)) != SA_OK) return st;
+    d.n_parts = w.slots;
+    d.part_ml = workspace;
+    d.part_o = reinterpret_cast<const float*>(static_cast<const uint8_t*>(workspace) + w.part_o_off);
+  }
+  return sa::launch_sink_decode(d, s);
+}
+
+int sa_scored_append(const void* k, const void* v, const int64_t k_strides[3], const int64_t v_strides[3], int32_t batch,
+                     int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity, const int32_t* d_start,
+                     const int32_t* d_tokens, void* k_cache, void* v_cache, const int64_t k_cache_strides[3],
+                     const int64_t v_cache_strides[3], float* d_weights, int32_t* d_positions, void* stream) {
+  if (!k || !v || !k_strides || !v_strides || !k_cache || !v_cache || !k_cache_strides || !v_cache_strides || !d_weights ||
+      !d_positions || n_tokens <= 0)
+    return SA_ERR_INVALID_ARG;
+  const int st = check_scored(batch, capacity, kv_heads, head_dim);
+  if (st != SA_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return SA_ERR_UNSUPPORTED;
+  if (!strides_ok(k_strides) || !strides_ok(v_strides) || !strides_ok(k_cache_strides) || !strides_ok(v_cache_strides))
+    return SA_ERR_UNSUPPORTED;
+  // a sequence's 16-byte words are counted in 32 bits
+  if ((int64_t)n_tokens * kv_heads > (1 << 30) / (head_dim / 8)) return SA_ERR_UNSUPPORTED;
+  if (!device_ok()) return SA_ERR_CUDA;
+  sa::ScoredArgs a;
+  memset(&a, 0, sizeof(a));
+  a.k = k;
+  a.v = v;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  copy3(a.k_strides, k_strides);
+  copy3(a.v_strides, v_strides);
+  copy3(a.k_cache_strides, k_cache_strides);
+  copy3(a.v_cache_strides, v_cache_strides);
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.capacity = capacity;
+  a.start = d_start;
+  a.tokens = d_tokens;
+  a.weights_out = d_weights;
+  a.positions_out = d_positions;
+  return sa::launch_scored_append(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_scored_attn_decode_workspace_size(int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads,
+                                         size_t* h_bytes) {
+  if (!h_bytes || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0) return SA_ERR_INVALID_ARG;
+  const int st = check_scored(batch, capacity, kv_heads, 32);
+  if (st != SA_OK) return st;
+  if (heads / kv_heads > sa::kMaxScoredHeads) return SA_ERR_UNSUPPORTED;
+  *h_bytes = scored_bytes(batch, capacity, heads, kv_heads);
+  return SA_OK;
+}
+
+int sa_scored_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int64_t q_strides[3],
+                          const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3],
+                          int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                          const int32_t* d_lengths, float softmax_scale, float decay, const float* d_weights_in,
+                          float* d_weights_out, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  sa::SinkDecodeArgs a;
+  int st = decode_args(q, k_cache, v_cache, q_strides, o_strides, batch, capacity, heads, kv_heads, head_dim, d_lengths,
+                       capacity, 0, softmax_scale, o, lse, a);
+  if (st != SA_OK) return st;
+  if (!k_strides || !v_strides || !d_weights_in || !d_weights_out || !(decay >= 0.f && decay <= 1.f))
+    return SA_ERR_INVALID_ARG;
+  if (!strides_ok(k_strides) || !strides_ok(v_strides) || heads / kv_heads > sa::kMaxScoredHeads) return SA_ERR_UNSUPPORTED;
+  if ((st = check_scored(batch, capacity, kv_heads, head_dim)) != SA_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, scored_bytes(batch, capacity, heads, kv_heads))) != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  copy3(a.k_strides, k_strides);
+  copy3(a.v_strides, v_strides);
+  a.scores = static_cast<float*>(workspace);
+  a.weights_in = d_weights_in;
+  a.weights_out = d_weights_out;
+  a.decay = decay;
+  return sa::launch_sink_decode(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_scored_evict(void* k_cache, void* v_cache, const int64_t k_strides[3], const int64_t v_strides[3], int32_t batch,
+                    int32_t kv_heads, int32_t head_dim, int32_t capacity, int32_t keep, int32_t sinks, int32_t recent,
+                    const float* d_weights_in, const int32_t* d_positions_in, const int32_t* d_lengths_in,
+                    float* d_weights_out, int32_t* d_positions_out, int32_t* d_lengths_out, void* stream) {
+  if (!k_cache || !v_cache || !k_strides || !v_strides || !d_weights_in || !d_positions_in || !d_lengths_in ||
+      !d_weights_out || !d_positions_out || !d_lengths_out)
+    return SA_ERR_INVALID_ARG;
+  if (keep <= 0 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return SA_ERR_INVALID_ARG;
+  const int st = check_scored(batch, capacity, kv_heads, head_dim);
+  if (st != SA_OK) return st;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !strides_ok(k_strides) || !strides_ok(v_strides))
+    return SA_ERR_UNSUPPORTED;
+  if (!device_ok()) return SA_ERR_CUDA;
+  sa::ScoredArgs a;
+  memset(&a, 0, sizeof(a));
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  copy3(a.k_cache_strides, k_strides);
+  copy3(a.v_cache_strides, v_strides);
+  a.batch = batch;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.capacity = capacity;
+  a.keep = keep < capacity ? keep : capacity;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.weights_in = d_weights_in;
+  a.positions_in = d_positions_in;
+  a.lengths_in = d_lengths_in;
+  a.weights_out = d_weights_out;
+  a.positions_out = d_positions_out;
+  a.lengths_out = d_lengths_out;
+  return sa::launch_scored_evict(a, static_cast<cudaStream_t>(stream));
+}
+
+int sa_sink_attn_weights_workspace_size(size_t* h_bytes) {
+  if (!h_bytes) return SA_ERR_INVALID_ARG;
+  *h_bytes = sa::kWeightsWorkspace;
+  return SA_OK;
+}
+
+int sa_sink_attn_weights(const void* q, const void* k, const float* lse, const int64_t q_strides[3],
+                         const int64_t k_strides[3], int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads,
+                         int32_t head_dim, int32_t window, int32_t sinks, int32_t first_query, float softmax_scale,
+                         float* d_weights, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k || !lse || !q_strides || !k_strides || !d_weights || !scale_ok(softmax_scale)) return SA_ERR_INVALID_ARG;
+  int st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks);
+  if (st != SA_OK) return st;
+  if (first_query < 0 || first_query >= n_tokens) return SA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !strides_ok(q_strides) || !strides_ok(k_strides)) return SA_ERR_UNSUPPORTED;
+  if ((st = check_workspace(workspace, workspace_bytes, sa::kWeightsWorkspace)) != SA_OK) return st;
+  if (!device_ok()) return SA_ERR_CUDA;
+  sa::WeightsArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.lse = lse;
+  copy3(a.q_strides, q_strides);
+  copy3(a.k_strides, k_strides);
+  a.batch = batch;
+  a.n_tokens = n_tokens;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.window = window;
+  a.sinks = sinks;
+  a.first_query = first_query;
+  a.softmax_scale = softmax_scale;
+  a.weights = d_weights;
+  a.workspace = workspace;
+  return sa::launch_sink_attn_weights(a, static_cast<cudaStream_t>(stream));
+}
+
 int sa_selftest_bounded_wait(void* stream) {
   if (!device_ok()) return SA_ERR_CUDA;
   bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
@@ -1210,7 +1503,9 @@ int sa_device_status(void* stream) {
   const unsigned int e = sa::attn_read_and_clear_error(s) | sa::offset_read_and_clear_error(s) |
                          sa::interp_read_and_clear_error(s) | sa::bwd_read_and_clear_error(s) |
                          sa::sink_fwd_read_and_clear_error(s) | sa::sink_bwd_read_and_clear_error(s) |
-                         sa::decode_read_and_clear_error(s) | sa::cache4_read_and_clear_error(s) | self;
+                         sa::decode_read_and_clear_error(s) | sa::cache4_read_and_clear_error(s) |
+                         sa::prefix_read_and_clear_error(s) | sa::scored_read_and_clear_error(s) |
+                         sa::weights_read_and_clear_error(s) | self;
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   if (e & sa::kErrTimeout) return SA_ERR_TIMEOUT;
   if (e & sa::kErrBadIndex) return SA_ERR_DEVICE;

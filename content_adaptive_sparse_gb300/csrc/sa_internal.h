@@ -206,9 +206,88 @@ struct SinkDecodeArgs {
   int32_t batch, capacity, heads, kv_heads, head_dim, window, sinks;
   bool cache4;
   float softmax_scale;
+  int32_t n_parts;                       // > 0: join these partial results of a shared prefix
+  const float* part_o;
+  const void* part_ml;
+  float* scores;                         // not null: add up the rows' weights (workspace of scored_bytes)
+  const float* weights_in;
+  float* weights_out;
+  float decay;
 };
+// Floats of a row's scores of up to 16 query heads: a power of two.
+inline int scored_stride(int heads, int kv_heads) {
+  const int group = heads / kv_heads < 16 ? heads / kv_heads : 16;
+  int n = 1;
+  while (n < group) n *= 2;
+  return n;
+}
+constexpr int kMaxScoredHeads = 128;     // query heads of a key head
 int launch_sink_decode(const SinkDecodeArgs& a, cudaStream_t stream);
 unsigned int decode_read_and_clear_error(cudaStream_t stream);
+
+// prefix_attn.cu
+struct PrefixArgs {
+  const void* q;
+  const void* k_prefix;
+  const void* v_prefix;
+  const void* k;                         // own tokens (decode: left to sink_decode.cu)
+  const void* v;
+  void* o;
+  float* lse;
+  int64_t q_strides[3], k_prefix_strides[3], v_prefix_strides[3], k_strides[3], v_strides[3], o_strides[3];
+  int32_t batch, n_tokens, prefix, heads, kv_heads, head_dim, window;
+  bool decode;                           // write the prefix's partial results alone
+  float softmax_scale;
+  void* workspace;
+};
+// Workspace: maxima and sums of the partial results, then their O.
+struct PrefixWorkspace {
+  int slots;
+  size_t part_o_off, bytes;
+};
+PrefixWorkspace prefix_workspace(int batch, int n_tokens, int prefix, int heads, int kv_heads, int head_dim, int window,
+                                 bool decode);
+int launch_prefix_attn(const PrefixArgs& a, cudaStream_t stream);
+unsigned int prefix_read_and_clear_error(cudaStream_t stream);
+
+// scored_cache.cu
+constexpr int kMaxScoredCapacity = 1 << 20;
+struct ScoredArgs {
+  const void* k;                         // append: new rows
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  int64_t k_strides[3], v_strides[3], k_cache_strides[3], v_cache_strides[3];
+  int32_t batch, n_tokens, kv_heads, head_dim, capacity;
+  const int32_t* start;                  // append
+  const int32_t* tokens;
+  int32_t keep, sinks, recent;           // evict
+  const float* weights_in;
+  const int32_t* positions_in;
+  const int32_t* lengths_in;
+  float* weights_out;
+  int32_t* positions_out;
+  int32_t* lengths_out;
+};
+int launch_scored_append(const ScoredArgs& a, cudaStream_t stream);
+int launch_scored_evict(const ScoredArgs& a, cudaStream_t stream);
+unsigned int scored_read_and_clear_error(cudaStream_t stream);
+
+// sink_weights.cu
+struct WeightsArgs {
+  const void* q;
+  const void* k;
+  const float* lse;
+  int64_t q_strides[3], k_strides[3];
+  int32_t batch, n_tokens, heads, kv_heads, head_dim, window, sinks, first_query;
+  float softmax_scale;
+  float* weights;
+  void* workspace;
+};
+constexpr int kWeightsMaxCtas = 256;     // CTAs of a launch at most
+constexpr size_t kWeightsWorkspace = (size_t)kWeightsMaxCtas * 2 * 256 * sizeof(float);
+int launch_sink_attn_weights(const WeightsArgs& a, cudaStream_t stream);
+unsigned int weights_read_and_clear_error(cudaStream_t stream);
 
 // sink_cache4.cu
 struct Cache4Args {

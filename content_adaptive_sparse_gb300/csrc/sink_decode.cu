@@ -12,6 +12,11 @@
 //   warps 0-3   16 rows of every 64 of a stage each, with their own running maximum and sum, on mma.sync
 //               m16n8k16 (a tcgen05 tile would need 64 or 128 rows of queries, and the tensor
 //               work is small beside the reads)
+// Two more forms over bf16 rows: behind a shared prefix, whose partial results (prefix_attn.cu) the join takes
+// in beside the cluster's; and with the rows' attention weights added up: a score goes to a workspace as
+// it is computed, and after the join, when the heads' maxima and sums are known, each CTA takes its rows'
+// probabilities from it (4 bytes per row and query head each way, mostly within L2, where recomputing
+// them would read the keys again).
 // bf16: S = Q K^T and O += P V with the query heads as the 16 rows.
 // 4 bits: S^T = K Q^T and O^T += V^T P^T with the cache rows (the output elements) as the 16 rows and 8
 // query heads as the columns, NQ times: what counts here is the instructions spent on unpacking and
@@ -55,6 +60,7 @@ constexpr int kWarps = 4;               // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxScoredGroup = kMaxScoredHeads;
 
 // NQ: groups of 8 query heads of a CTA (2 in the bf16 form: one m-tile)
 template <int D, bool Q4, int NQ>
@@ -82,6 +88,10 @@ struct Cfg {
   static_assert(STAGES <= kMaxStages && SMEM <= 227 * 1024, "shared memory");
 };
 
+// What a launch does besides: join the partial results of a shared prefix (prefix_attn.cu), or add up the
+// attention weights of the rows.
+enum : int { kPlain = 0, kBehindPrefix = 1, kScored = 2 };
+
 struct DParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
@@ -97,6 +107,16 @@ struct DParams {
   // 0x000f000f, not known to the compiler: (w & mask) | bits is one instruction, but only with one constant
   // in it (4 bits: 220 -> 158 ALU instructions per 16 rows, 86 -> 77 us)
   uint32_t code_mask;
+  // kBehindPrefix: partial results of row (hk, s, query head of the group), n_parts of them
+  const float* part_o;              // [n_parts][kv_heads * batch * group][D]
+  const float2* part_ml;            // m (log2 units), l
+  int n_parts, part_rows;           // part_rows: kv_heads * batch * group
+  // kScored
+  float* scores;                    // [batch][kv_heads][head_groups][capacity][score_stride], log2 units
+  const float* w_in;                // [batch][kv_heads][capacity]
+  float* w_out;
+  float decay;
+  int score_stride;
 };
 
 struct Bars {
@@ -448,9 +468,10 @@ __device__ void consumer4(const DParams& p, Bars& bars, uint8_t* ring, const Row
 }
 
 // bf16 form. m, l: per query head g + 8 h of lane (g, t), l this lane's columns.
-template <int D>
+// kScored: `scores` takes the scores of the CTA's heads, [capacity][score_stride].
+template <int D, int MODE>
 __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Rows<1, false>& r, int s, int h0, int n_q,
-                           float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
+                           float* scores, float (&o)[D / 8][4], float (&m)[2], float (&l)[2], volatile int* abort_flag) {
   using C = Cfg<D, false, 2>;
   constexpr int KS = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -510,6 +531,16 @@ __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Ro
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[nt][e] = on[nt][e & 1] ? sc[nt][e] * c : kNegInf;
+      if constexpr (MODE == kScored) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int head = g + 8 * (e >> 1);
+            if (head < n_q && on[nt][e & 1])
+              scores[(int64_t)(t0 + 8 * nt + 2 * t + (e & 1)) * p.score_stride + head] = sc[nt][e];
+          }
+      }
       // running maximum of rows g (half 0) and g + 8; O and l follow it only when it grows by 2^8
       float mx[2];
       bool grow = false;
@@ -574,7 +605,7 @@ __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Ro
 
 // 4 bits, up to 8 query heads: four CTAs an SM (74 us; three with longer rings 80, five with shorter ones
 // and 80 registers 90 to 109).
-template <int D, bool Q4, int NQ>
+template <int D, bool Q4, int NQ, int MODE>
 __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv,
                                                                const __grid_constant__ DParams p) {
@@ -585,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
   __shared__ Bars bars;
   __shared__ int abort_flag;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = blockIdx.x, ranks = gridDim.x;          // the cluster spans the grid's x
+  const int rank = blockIdx.x, ranks = gridDim.x;          // the cluster spans the grid's x (and the head groups: kScored)
   const int s = blockIdx.z, hk = blockIdx.y / p.head_groups, hg = blockIdx.y % p.head_groups;
   constexpr int kQ = C::Q;
   const int h0 = hk * p.group + hg * kQ;
@@ -619,7 +650,12 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     __syncwarp();
   } else {
     if constexpr (Q4) consumer4<D, NQ>(p, bars, ring, r, s, h0, n_q, o, m, l, &abort_flag);
-    else consumer16<D>(p, bars, ring, r, s, h0, n_q, o, m, l, &abort_flag);
+    else {
+      float* scores = nullptr;
+      if constexpr (MODE == kScored)
+        scores = p.scores + (((int64_t)s * p.kv_heads + hk) * p.head_groups + hg) * p.capacity * p.score_stride;
+      consumer16<D, MODE>(p, bars, ring, r, s, h0, n_q, scores, o, m, l, &abort_flag);
+    }
   }
   __syncthreads();                                          // the ring is free
   // ---- the warps' partial results: O [warp][query][D], maxima and sums
@@ -686,6 +722,8 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
   cluster.sync();
   // ---- the cluster's CTAs join their results: CTA `rank` writes its share of the elements. All the
   // remote loads go out together: one trip's latency, not one per CTA.
+  if constexpr (MODE == kBehindPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");   // the prefix's results
+  const int first = MODE == kScored ? hg * ranks : 0;       // this head group's first CTA
   const int pairs = n_q * (D / 2);
   const int p0 = (int)((int64_t)pairs * rank / ranks), p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
   for (int at = p0 + threadIdx.x; at < p1; at += kThreads) {
@@ -698,15 +736,30 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
       lk[k] = 0.f;
       v[k] = make_float2(0.f, 0.f);
       if (k < ranks) {
-        mk[k] = *cluster.map_shared_rank(cm + row, k);
-        lk[k] = *cluster.map_shared_rank(cl + row, k);
-        v[k] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + row * D + col, k));
+        mk[k] = *cluster.map_shared_rank(cm + row, first + k);
+        lk[k] = *cluster.map_shared_rank(cl + row, first + k);
+        v[k] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(wo + row * D + col, first + k));
       }
     }
     float M = kNegInf;
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mk[k]);
     float x = 0.f, y = 0.f, L = 0.f;
+    if constexpr (MODE == kBehindPrefix) {
+      const int64_t at_row = ((int64_t)hk * gridDim.z + s) * p.group + hg * kQ + row;
+      const float2* ml = p.part_ml + at_row;
+#pragma unroll 8
+      for (int k = 0; k < p.n_parts; ++k) M = fmaxf(M, ml[(int64_t)k * p.part_rows].x);
+#pragma unroll 4
+      for (int k = 0; k < p.n_parts; ++k) {
+        const float2 e = ml[(int64_t)k * p.part_rows];
+        const float2 z = *reinterpret_cast<const float2*>(p.part_o + ((int64_t)k * p.part_rows + at_row) * D + col);
+        const float a = M != kNegInf ? ex2_approx(e.x - M) : 1.f;
+        x = fmaf(a, z.x, x);
+        y = fmaf(a, z.y, y);
+        L = fmaf(a, e.y, L);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) {
       const float a = M != kNegInf ? ex2_approx(mk[k] - M) : 1.f;
@@ -721,10 +774,38 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     if (col == 0)
       p.lse[(int64_t)s * p.heads + h0 + row] = L == 0.f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
   }
+  if constexpr (MODE == kScored) {
+    // ---- the weights of this CTA's rows: maxima and sums of all of the key head's query heads, then a row a
+    // thread. The head groups' CTAs of one rank have the same rows and share them out.
+    __shared__ float hm[kMaxScoredGroup], hi[kMaxScoredGroup];
+    for (int q = threadIdx.x; q < p.group; q += kThreads) {
+      float M = kNegInf, L = 0.f;
+      for (int k = 0; k < ranks; ++k) M = fmaxf(M, *cluster.map_shared_rank(cm + q % kQ, q / kQ * ranks + k));
+      for (int k = 0; k < ranks; ++k) {
+        const float mk = *cluster.map_shared_rank(cm + q % kQ, q / kQ * ranks + k);
+        L = fmaf(M != kNegInf ? ex2_approx(mk - M) : 1.f, *cluster.map_shared_rank(cl + q % kQ, q / kQ * ranks + k), L);
+      }
+      hm[q] = M;
+      hi[q] = 1.f / L;
+    }
+    __syncthreads();
+    const int64_t list = (int64_t)s * p.kv_heads + hk;
+    const int end = min(r.len, r.end * kUnit);
+    for (int j = r.begin * kUnit + hg * kThreads + threadIdx.x; j < end; j += p.head_groups * kThreads) {
+      float w = 0.f;
+      for (int g0 = 0; g0 < p.head_groups; ++g0) {
+        const float* sc = p.scores + ((list * p.head_groups + g0) * p.capacity + j) * p.score_stride;
+        const int n = min(kQ, p.group - g0 * kQ);
+        for (int q = 0; q < n; ++q) w = fmaf(ex2_approx(sc[q] - hm[g0 * kQ + q]), hi[g0 * kQ + q], w);
+      }
+      const int64_t at = list * p.capacity + j;
+      p.w_out[at] = p.decay != 0.f ? fmaf(p.decay, p.w_in[at], w) : w;
+    }
+  }
   cluster.sync();                                           // no CTA leaves while another reads its results
 }
 
-template <int D, bool Q4, int NQ>
+template <int D, bool Q4, int NQ, int MODE>
 int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   using C = Cfg<D, Q4, NQ>;
   CUtensorMap tk, tv;
@@ -761,7 +842,20 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   p.sinks = a.sinks;
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.code_mask = 0x000f000fu;
-  const auto kern = sink_decode_kernel<D, Q4, NQ>;
+  if (MODE == kBehindPrefix) {
+    p.part_o = a.part_o;
+    p.part_ml = static_cast<const float2*>(a.part_ml);
+    p.n_parts = a.n_parts;
+    p.part_rows = a.batch * a.heads;
+  }
+  if (MODE == kScored) {
+    p.scores = a.scores;
+    p.w_in = a.weights_in;
+    p.w_out = a.weights_out;
+    p.decay = a.decay;
+    p.score_stride = scored_stride(a.heads, a.kv_heads);
+  }
+  const auto kern = sink_decode_kernel<D, Q4, NQ, MODE>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return SA_ERR_CUDA;
   // CTAs per (sequence, key head), while each has a stage of rows when the cache is full: bf16 until
@@ -773,21 +867,28 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   const int64_t seen = (int64_t)a.window + 1 + a.sinks < a.capacity ? (int64_t)a.window + 1 + a.sinks : a.capacity;
   const int sm_count = current_sm_count();
   int ranks = 1;
-  while (ranks < kMaxCluster && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * kUnit * ranks) ranks *= 2;
+  const int most = MODE == kScored ? kMaxCluster / p.head_groups : kMaxCluster;
+  while (2 * ranks <= most && 2 * base * ranks < (Q4 ? 12 : 3) * sm_count && seen >= 2 * kUnit * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)ranks, (unsigned)(a.kv_heads * p.head_groups), (unsigned)a.batch);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  memset(&attr, 0, sizeof(attr));
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)ranks;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
+  cudaLaunchAttribute attr[2];
+  memset(attr, 0, sizeof(attr));
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = MODE == kScored ? (unsigned)p.head_groups : 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (MODE == kBehindPrefix) {
+    // its CTAs may start as the prefix's leave; they read its results after griddepcontrol.wait
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
   return cudaLaunchKernelEx(&cfg, kern, tk, tv, p) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -795,8 +896,10 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
 
 template <int D>
 int launch_d(const SinkDecodeArgs& a, cudaStream_t stream) {
-  if (!a.cache4) return launch<D, false, 2>(a, stream);
-  return a.heads / a.kv_heads > 8 ? launch<D, true, 2>(a, stream) : launch<D, true, 1>(a, stream);
+  if (a.n_parts > 0) return launch<D, false, 2, kBehindPrefix>(a, stream);
+  if (a.scores) return launch<D, false, 2, kScored>(a, stream);
+  if (!a.cache4) return launch<D, false, 2, kPlain>(a, stream);
+  return a.heads / a.kv_heads > 8 ? launch<D, true, 2, kPlain>(a, stream) : launch<D, true, 1, kPlain>(a, stream);
 }
 
 int launch_sink_decode(const SinkDecodeArgs& a, cudaStream_t stream) {

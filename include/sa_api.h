@@ -479,6 +479,103 @@ int sa_sink_attn_decode_cache4(const void* q, const uint8_t* k_codes, const void
                                const int32_t* d_lengths, int32_t window, int32_t sinks, float softmax_scale, void* o,
                                float* lse, void* stream);
 
+/* ---------------------------------------------------------------- shared prefixes and bounded caches
+ *
+ * Attention of a batch whose sequences share a prefix: a query sees every row of the prefix and, of its
+ * own sequence's tokens, itself and the `window` (>= 0) before it. The prefix's rows are read once for
+ * the whole batch. Conventions, shapes, strides, O, LSE, NaN scores and softmax_scale as in the
+ * sink-window calls, with
+ *   k_prefix, v_prefix : bf16 [1, prefix_tokens, kv_heads, head_dim] with k_prefix_strides / v_prefix_strides
+ *              (the batch stride is not used); prefix_tokens 0 .. 2^30, with 0 the pointers may be NULL.
+ *   workspace : device memory, 256-byte aligned, of at least the bytes that the call's size query gives
+ *              (partial results); its contents on entry do not matter.
+ *
+ * sa_prefix_attn_fwd: n_tokens own tokens of every sequence, 1 .. 2^24, whose keys and values k, v are
+ * [batch, n_tokens, kv_heads, head_dim]. (With one sequence it is the later part of a prompt, over the rows
+ * that its first part left.) SA_ERR_UNSUPPORTED from 2^24 heads of all sequences on, and from 2^24 tiles
+ * of 128 queries of a key head on. */
+int sa_prefix_attn_fwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t prefix_tokens, int32_t heads,
+                                      int32_t kv_heads, int32_t head_dim, int32_t window, size_t* h_bytes);
+int sa_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                       const int64_t q_strides[3], const int64_t k_prefix_strides[3], const int64_t v_prefix_strides[3],
+                       const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3], int32_t batch,
+                       int32_t n_tokens, int32_t prefix_tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                       int32_t window, float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Its single-token form: one query per sequence, token d_lengths[s] - 1 of its own tokens, over caches of them
+ * (q, o, k_cache, v_cache, capacity, d_lengths as in sa_sink_attn_decode; the caches do not hold the
+ * prefix). With length 0 a query sees the prefix alone. */
+int sa_prefix_attn_decode_workspace_size(int32_t batch, int32_t prefix_tokens, int32_t heads, int32_t kv_heads,
+                                         int32_t head_dim, size_t* h_bytes);
+int sa_prefix_attn_decode(const void* q, const void* k_prefix, const void* v_prefix, const void* k_cache,
+                          const void* v_cache, const int64_t q_strides[3], const int64_t k_prefix_strides[3],
+                          const int64_t v_prefix_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
+                          const int64_t o_strides[3], int32_t batch, int32_t prefix_tokens, int32_t capacity,
+                          int32_t heads, int32_t kv_heads, int32_t head_dim, const int32_t* d_lengths, int32_t window,
+                          float softmax_scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* A cache that is kept below a number of rows by the attention weight that they gather. A sequence's rows
+ * stand in slots, in no particular order (attention does not depend on it):
+ *   k_cache, v_cache : bf16 [batch, capacity, kv_heads, head_dim], any strides
+ *   weights   : fp32 [batch][kv_heads][capacity], the weight that each row has gathered
+ *   positions : int32 [batch][kv_heads][capacity], the token that each row belongs to
+ *   lengths   : int32 [batch], slots in use, the same for all key heads of a sequence (taken into 0 .. capacity)
+ * capacity 1 .. 2^20, batch <= 32767. Slots from the length on are neither read nor written by the calls
+ * that do not name them.
+ *
+ * sa_scored_append writes rows d_start[s] .. d_start[s] + n_tokens - 1 of every sequence from k and v
+ * (bf16 [batch, n_tokens, kv_heads, head_dim]), their weights to 0 and their positions to d_tokens[s] ..
+ * d_start, d_tokens: int32 [batch] on the device, or NULL for 0 and for the slots' own numbers; a sequence
+ * with a negative start is left out. Slots at or past the capacity are not written and reported as
+ * SA_ERR_DEVICE by sa_device_status. The lengths are the caller's to raise. */
+int sa_scored_append(const void* k, const void* v, const int64_t k_strides[3], const int64_t v_strides[3], int32_t batch,
+                     int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity, const int32_t* d_start,
+                     const int32_t* d_tokens, void* k_cache, void* v_cache, const int64_t k_cache_strides[3],
+                     const int64_t v_cache_strides[3], float* d_weights, int32_t* d_positions, void* stream);
+
+/* One query per sequence over the first d_lengths[s] slots (all of them are seen), as sa_sink_attn_decode, and
+ * for each of these slots w_out = decay * w_in + the sum of its probabilities over the query heads of its
+ * key head, in a fixed order.
+ *   decay : 0 .. 1; 0 does not read w_in.
+ *   d_weights_out may be d_weights_in.
+ *   workspace : device memory, 256-byte aligned, of sa_scored_attn_decode_workspace_size bytes (scores).
+ * At most 128 query heads per key head. A score that is NaN makes its key head's weights NaN. */
+int sa_scored_attn_decode_workspace_size(int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads,
+                                         size_t* h_bytes);
+int sa_scored_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int64_t q_strides[3],
+                          const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3],
+                          int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                          const int32_t* d_lengths, float softmax_scale, float decay, const float* d_weights_in,
+                          float* d_weights_out, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Leaves at most `keep` slots of every sequence and key head: first those with position < sinks or
+ * position > newest - recent (newest: the list's largest position), then the ones of most weight; ties go to
+ * the lower slot, NaN counts as the largest weight. sinks + recent <= keep (positions of one list are
+ * expected to differ; where more are protected than `keep`, the lowest slots stay). The e-th kept slot at or past
+ * `keep` moves into the e-th freed slot below it, both counted upwards, with its rows of k_cache and v_cache,
+ * weight and position. d_weights_out and d_positions_out receive the slots that remain, d_lengths_out
+ * min(length, keep); each may be its input. Slots from there on stay as they were. Lists that are not
+ * longer than `keep` do not change. */
+int sa_scored_evict(void* k_cache, void* v_cache, const int64_t k_strides[3], const int64_t v_strides[3], int32_t batch,
+                    int32_t kv_heads, int32_t head_dim, int32_t capacity, int32_t keep, int32_t sinks, int32_t recent,
+                    const float* d_weights_in, const int32_t* d_positions_in, const int32_t* d_lengths_in,
+                    float* d_weights_out, int32_t* d_positions_out, int32_t* d_lengths_out, void* stream);
+
+/* The weights that a prompt's rows begin with: for each key j and key head the sum of exp(s_ij - LSE_i) over the
+ * query heads of the key head and the queries i >= first_query (0 .. n_tokens - 1) that see j in the
+ * sink-window graph, from the inputs and the LSE of sa_sink_attn_fwd (LSE of earlier queries is not used).
+ *   d_weights : fp32 [batch][kv_heads][n_tokens], all written; the same bits on every run on one GPU.
+ *   workspace : device memory, 256-byte aligned, of sa_sink_attn_weights_workspace_size bytes.
+ * Limits as in sa_sink_attn_fwd. */
+int sa_sink_attn_weights_workspace_size(size_t* h_bytes);
+int sa_sink_attn_weights(const void* q, const void* k, const float* lse, const int64_t q_strides[3],
+                         const int64_t k_strides[3], int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads,
+                         int32_t head_dim, int32_t window, int32_t sinks, int32_t first_query, float softmax_scale,
+                         float* d_weights, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the library's device error words.
  * Returns SA_OK, SA_ERR_TIMEOUT (a bounded wait expired; the kernel unwound and its
  * outputs are undefined), SA_ERR_DEVICE (invalid CSR data was skipped) or
