@@ -46,6 +46,12 @@ struct Layout {
   int tiles0, parts0, items0;       // class 0: row tiles of a key head, parts of their lists, items in all
   int tiles1, parts1, items1;       // class 1: row tiles of a sequence and key head, ...
   int slots;                        // partial results of a row; 0: the items write O and LSE
+  // Item of part k of the list of row r of all sequences (class 0), or of row r of sequence s (class 1), of key head
+  // hk; the row's place in it is r % 128.
+  __host__ __device__ int item0(int hk, int r, int k) const { return (hk * tiles0 + r / kTile) * parts0 + k; }
+  __host__ __device__ int item1(int hk, int s, int r, int k) const {
+    return items0 + ((hk * batch + s) * tiles1 + r / kTile) * parts1 + k;
+  }
 };
 
 struct PParams {
@@ -53,8 +59,10 @@ struct PParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;                       // [batch][heads][n]
-  float* part_o;                    // [slots][kv_heads * rows][D]
-  float2* part_ml;                  // [slots][kv_heads * rows]: m (log2 units), l
+  // Partial results by item, row tiles as the threads hold them: O [item][D / 4][128] of four columns each, m (log2
+  // units) and l [item][128]. A warp's 32 rows are neighbours: written row by row they took 2 us.
+  float4* part_o;
+  float2* part_ml;
   int64_t q_sb, q_sn, q_sh, o_sb, o_sn, o_sh;
   float scale_log2;
 };
@@ -66,7 +74,6 @@ struct Item {
   bool common;                      // class 0
   int s, hk, row0, rows;            // rows row0 .. row0 + rows - 1 of all sequences' (class 0) or of s's
   int pre, begin, steps, own;       // prefix tiles of the whole list; this part of it; first own tile
-  int slot;
   __device__ explicit Item(const PParams& p) : Item(p, (int)blockIdx.x) {}
   __host__ __device__ Item(const PParams& p, int first) : at(first) { set(p); }
   __device__ __forceinline__ bool more() const { return on; }
@@ -102,7 +109,6 @@ struct Item {
     }
     begin = (int)((int64_t)all * part / parts);
     steps = (int)((int64_t)all * (part + 1) / parts) - begin;
-    slot = common ? part : (l.items0 > 0 ? l.parts0 : part);
   }
   __host__ __device__ bool is_prefix(int j) const { return begin + j < pre; }
   __host__ __device__ int key_tile(int j) const { return begin + j < pre ? begin + j : own + begin + j - pre; }
@@ -223,22 +229,25 @@ __device__ void softmax(const PParams& p, Bars& bars, Handoff* hand, uint32_t tm
 
 // ------------------------------------------------------------------ Q and the results (warps 12-15)
 
-// Copies this thread's row of the item's Q into buffer `dst` in the layout of the swizzled TMA boxes (zeros for
-// a row past the last one).
+// Copies this warp's 32 rows of the item's Q into buffer `dst` in the layout of the swizzled TMA boxes (zeros for
+// rows past the last one). D / 8 lanes take a row together (a row a lane: 3.5 us, of a cold Q).
 template <int D>
-__device__ __forceinline__ void load_q(const PParams& p, const Item& it, int row, uint8_t* dst) {
+__device__ __forceinline__ void load_q(const PParams& p, const Item& it, int quarter, int lane, uint8_t* dst) {
   using C = Cfg<D>;
-  const bool on = row < it.rows;
-  const int r = it.row(p, on ? row : 0);
+  constexpr int kLanes = D / 8;
+  const bool mine = 32 * quarter + lane < it.rows;
+  const int r = it.row(p, mine ? 32 * quarter + lane : 0);
   const int tok = r / p.l.group, e = r - tok * p.l.group, s = tok / p.l.n, t = tok - s * p.l.n;
-  const __nv_bfloat16* src = p.q + s * p.q_sb + t * p.q_sn + (int64_t)(it.hk * p.l.group + e) * p.q_sh;
-  const uint32_t at = smem_u32(dst) + (uint32_t)(row * C::ROWB);
-  const uint32_t x = C::ROWB == 128 ? (uint32_t)(row & 7) : (uint32_t)((row >> 1) & 3);
+  const int64_t at = s * p.q_sb + t * p.q_sn + (int64_t)(it.hk * p.l.group + e) * p.q_sh;
+  const int u = lane % kLanes, c = u / (C::CH / 8), v = u % (C::CH / 8);
+  const uint32_t to = smem_u32(dst) + (uint32_t)(c * C::CHUNK);
 #pragma unroll
-  for (int u = 0; u < D / 8; ++u) {
-    const int c = u / (C::CH / 8), v = u % (C::CH / 8);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + (uint32_t)(c * C::CHUNK) + (((uint32_t)v ^ x) << 4)),
-                 "l"(src + 8 * u), "r"(on ? 16 : 0)
+  for (int k = 0; k < kLanes; ++k) {
+    const int from = k * (32 / kLanes) + lane / kLanes, row = 32 * quarter + from;
+    const int64_t off = __shfl_sync(0xffffffffu, at, from);
+    const uint32_t x = C::ROWB == 128 ? (uint32_t)(row & 7) : (uint32_t)((row >> 1) & 3);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (uint32_t)(row * C::ROWB) + (((uint32_t)v ^ x) << 4)),
+                 "l"(p.q + off + 8 * u), "r"(row < it.rows ? 16 : 0)
                  : "memory");
   }
 }
@@ -255,7 +264,7 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
   const auto queries = [&](const Item& it, int n) {
     if (!it.more()) return true;
     if (n >= 2 && !__all_sync(0xffffffffu, wait_bar(&bars.q_empty[n & 1], (uint32_t)(n / 2 - 1) & 1u, abort_flag))) return false;
-    load_q<D>(p, it, row, sQ + (n & 1) * C::TILE);
+    load_q<D>(p, it, quarter, lane, sQ + (n & 1) * C::TILE);
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     fence_proxy_async_smem();
     __syncwarp();
@@ -279,7 +288,6 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
     const float L = l0 * f0 + l1 * f1;
     const bool on = row < it.rows;
     const int r = it.row(p, on ? row : 0);
-    const int64_t slot_row = ((int64_t)it.slot * p.l.kv_heads + it.hk) * p.l.rows + r;
     __nv_bfloat16* o = nullptr;
     if (p.l.slots == 0) {
       const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -289,13 +297,13 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
       o = p.o + s * p.o_sb + t * p.o_sn + (int64_t)h * p.o_sh;
       if (on)
         p.lse[((int64_t)s * p.l.heads + h) * p.l.n + t] = L == 0.f ? kNegInf : (m + __log2f(L)) * 0.69314718055994531f;
-    } else if (on) {
-      p.part_ml[slot_row] = make_float2(m, L);
+    } else {
+      p.part_ml[(int64_t)it.at * kTile + row] = make_float2(m, L);
     }
     if (!__all_sync(0xffffffffu, wait_bar(&bars.o_full, (uint32_t)n & 1u, abort_flag))) return;
     tc_fence_after();
     const uint32_t t0 = base + C::COL_O, t1 = t0 + D;
-    float* part = p.part_o + slot_row * D;
+    float4* part = p.part_o + (int64_t)it.at * (D / 4) * kTile + row;
 #pragma unroll 1
     for (int c = 0; c < D; c += 16) {
       uint32_t a[16], b[16];
@@ -306,7 +314,7 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(a[j]) * f0 + __uint_as_float(b[j]) * f1;
-      if (!on) continue;
+      if (!on) continue;                               // (the places of rows past the last one are not read)
       if (p.l.slots == 0) {
 #pragma unroll
         for (int j = 0; j < 16; j += 8)
@@ -315,7 +323,7 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
                          pack_bf16x2(v[j + 6], v[j + 7]));
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(part + c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        for (int j = 0; j < 16; j += 4) part[(c + j) / 4 * kTile] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       }
     }
     // the accumulators have been read: the next item's PVs may start
@@ -405,36 +413,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins a row's partial results: D / 4 threads a row, four elements each.
+// Joins the partial results of 32 rows of a key head: a lane has a row, a warp every eighth four columns. Rows leave
+// through shared memory, so that they are written in runs.
 template <int D>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PParams p) {
+  constexpr int kWarps = 8, kCols = D / 4 / kWarps;        // groups of four columns of a warp
+  __shared__ uint2 out[32][D / 4 + 1];
+  __shared__ int64_t place[32];
   const float kNegInf = __int_as_float(0xff800000);
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t all = (int64_t)p.l.kv_heads * p.l.rows, row = at / (D / 4);
-  const int col = 4 * (int)(at % (D / 4));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hk = blockIdx.y;
+  const int r = min((int)blockIdx.x * 32 + lane, p.l.rows - 1);
+  const int tok = r / p.l.group, h = hk * p.l.group + r - tok * p.l.group, s = tok / p.l.n, t = tok - s * p.l.n;
+  const int seq_row = r - s * p.l.seq_rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= all) return;
+  // part k: of class 0 first, then of class 1
+  const auto place_of = [&](int k) {
+    const bool common = p.l.items0 > 0 && k < p.l.parts0;
+    const int item = common ? p.l.item0(hk, r, k) : p.l.item1(hk, s, seq_row, p.l.items0 > 0 ? k - p.l.parts0 : k);
+    return (int64_t)item * kTile + (common ? r : seq_row) % kTile;
+  };
+  const int parts = p.l.slots;
   float M = kNegInf, L = 0.f;
-  for (int k = 0; k < p.l.slots; ++k) M = fmaxf(M, p.part_ml[k * all + row].x);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < p.l.slots; ++k) {
-    const float2 ml = p.part_ml[k * all + row];
-    const float4 x = *reinterpret_cast<const float4*>(p.part_o + (k * all + row) * D + col);
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, p.part_ml[place_of(k)].x);
+  float4 v[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const int64_t at = place_of(k);
+    const float2 ml = p.part_ml[at];
     const float a = M != kNegInf ? ex2_approx(ml.x - M) : 1.f;     // without a maximum the sums are zero, or NaN
-    v.x = fmaf(a, x.x, v.x);
-    v.y = fmaf(a, x.y, v.y);
-    v.z = fmaf(a, x.z, v.z);
-    v.w = fmaf(a, x.w, v.w);
     L = fmaf(a, ml.y, L);
+    const float4* part = p.part_o + at / kTile * (D / 4) * kTile + at % kTile;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const float4 x = part[(warp + kWarps * c) * kTile];
+      v[c].x = fmaf(a, x.x, v[c].x);
+      v[c].y = fmaf(a, x.y, v[c].y);
+      v[c].z = fmaf(a, x.z, v[c].z);
+      v[c].w = fmaf(a, x.w, v[c].w);
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int hk = (int)(row / p.l.rows), r = (int)(row % p.l.rows);
-  const int tok = r / p.l.group, h = hk * p.l.group + r - tok * p.l.group, s = tok / p.l.n, t = tok - s * p.l.n;
-  *reinterpret_cast<uint2*>(p.o + s * p.o_sb + t * p.o_sn + (int64_t)h * p.o_sh + col) =
-      make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-  if (col == 0)
-    p.lse[((int64_t)s * p.l.heads + h) * p.l.n + t] = L == 0.f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+    out[lane][warp + kWarps * c] = make_uint2(pack_bf16x2(v[c].x * inv, v[c].y * inv), pack_bf16x2(v[c].z * inv, v[c].w * inv));
+  if (warp == 0) {
+    place[lane] = s * p.o_sb + t * p.o_sn + (int64_t)h * p.o_sh;
+    if ((int)blockIdx.x * 32 + lane < p.l.rows)
+      p.lse[((int64_t)s * p.l.heads + h) * p.l.n + t] = L == 0.f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * (D / 4); i += 256) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    if ((int)blockIdx.x * 32 + row < p.l.rows) *reinterpret_cast<uint2*>(p.o + place[row] + 4 * c) = out[row][c];
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -507,7 +541,7 @@ Layout plan(int batch, int n, int prefix, int heads, int kv_heads, int window, b
   return l;
 }
 
-size_t ml_bytes(const Layout& l) { return ((size_t)l.slots * l.kv_heads * l.rows * sizeof(float2) + 255) / 256 * 256; }
+size_t partial_rows(const Layout& l) { return l.slots > 0 ? (size_t)(l.items0 + l.items1) * kTile : 0; }
 
 template <int D>
 int launch_d(const PrefixArgs& a, const Layout& l, cudaStream_t stream) {
@@ -533,7 +567,7 @@ int launch_d(const PrefixArgs& a, const Layout& l, cudaStream_t stream) {
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
   p.part_ml = static_cast<float2*>(a.workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + ml_bytes(l));
+  p.part_o = reinterpret_cast<float4*>(static_cast<uint8_t*>(a.workspace) + partial_rows(l) * sizeof(float2));
   p.q_sb = a.q_strides[0];
   p.q_sn = a.q_strides[1];
   p.q_sh = a.q_strides[2];
@@ -552,7 +586,7 @@ int launch_d(const PrefixArgs& a, const Layout& l, cudaStream_t stream) {
   if (l.slots == 0 || a.decode) return SA_OK;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(((int64_t)l.kv_heads * l.rows * (D / 4) + 255) / 256));
+  cfg.gridDim = dim3((unsigned)((l.rows + 31) / 32), (unsigned)l.kv_heads);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -570,9 +604,10 @@ PrefixWorkspace prefix_workspace(int batch, int n_tokens, int prefix, int heads,
                                  bool decode) {
   const Layout l = plan(batch, n_tokens, prefix, heads, kv_heads, window, decode);
   PrefixWorkspace w;
-  w.slots = l.slots;
-  w.part_o_off = ml_bytes(l);
-  w.bytes = w.part_o_off + (size_t)l.slots * l.kv_heads * l.rows * head_dim * sizeof(float);
+  w.parts = l.parts0;
+  w.tiles = l.tiles0;
+  w.part_o_off = partial_rows(l) * sizeof(float2);
+  w.bytes = w.part_o_off + partial_rows(l) * head_dim * sizeof(float);
   if (w.bytes < 256) w.bytes = 256;
   return w;
 }

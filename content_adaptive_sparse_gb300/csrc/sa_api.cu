@@ -945,7 +945,8 @@ int check_prefix(int32_t batch, int32_t n_tokens, int32_t prefix, int32_t heads,
   if (!head_dim_ok(head_dim) || n_tokens > (1 << 24) || prefix > (1 << 30)) return SA_ERR_UNSUPPORTED;
   // rows and work items are counted in 32 bits
   const int64_t tiles = ((int64_t)n_tokens * (heads / kv_heads) + 127) / 128;
-  if ((int64_t)batch * heads > (1 << 24) || (int64_t)batch * kv_heads * tiles > (1 << 24)) return SA_ERR_UNSUPPORTED;
+  if ((int64_t)batch * heads > (1 << 24) || (int64_t)batch * kv_heads * tiles > (1 << 24) || kv_heads > 65535)
+    return SA_ERR_UNSUPPORTED;
   if (window > n_tokens - 1) window = n_tokens - 1;
   return SA_OK;
 }
@@ -1336,9 +1337,10 @@ int sa_prefix_attn_decode(const void* q, const void* k_prefix, const void* v_pre
                 heads, kv_heads, head_dim, 0, softmax_scale, o, lse, workspace, a);
     a.decode = true;
     if ((st = sa::launch_prefix_attn(a, s)) != SA_OK) return st;
-    d.n_parts = w.slots;
+    d.n_parts = w.parts;
+    d.part_tiles = w.tiles;
     d.part_ml = workspace;
-    d.part_o = reinterpret_cast<const float*>(static_cast<const uint8_t*>(workspace) + w.part_o_off);
+    d.part_o = static_cast<const uint8_t*>(workspace) + w.part_o_off;
   }
   return sa::launch_sink_decode(d, s);
 }

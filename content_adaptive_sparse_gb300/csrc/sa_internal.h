@@ -206,8 +206,8 @@ struct SinkDecodeArgs {
   int32_t batch, capacity, heads, kv_heads, head_dim, window, sinks;
   bool cache4;
   float softmax_scale;
-  int32_t n_parts;                       // > 0: join these partial results of a shared prefix
-  const float* part_o;
+  int32_t n_parts, part_tiles;           // n_parts > 0: join these partial results of a shared prefix
+  const void* part_o;
   const void* part_ml;
   float* scores;                         // not null: add up the rows' weights (workspace of scored_bytes)
   const float* weights_in;
@@ -240,9 +240,10 @@ struct PrefixArgs {
   float softmax_scale;
   void* workspace;
 };
-// Workspace: maxima and sums of the partial results, then their O.
+// Workspace: maxima and sums of the partial results, then their O. Decoding: `parts` partial results of every row
+// s * group + e of a key head, in items (hk * tiles + row / 128) * parts + part (prefix_attn.cu has their layout).
 struct PrefixWorkspace {
-  int slots;
+  int parts, tiles;
   size_t part_o_off, bytes;
 };
 PrefixWorkspace prefix_workspace(int batch, int n_tokens, int prefix, int heads, int kv_heads, int head_dim, int window,

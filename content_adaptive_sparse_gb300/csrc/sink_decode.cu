@@ -107,10 +107,11 @@ struct DParams {
   // 0x000f000f, not known to the compiler: (w & mask) | bits is one instruction, but only with one constant
   // in it (4 bits: 220 -> 158 ALU instructions per 16 rows, 86 -> 77 us)
   uint32_t code_mask;
-  // kBehindPrefix: partial results of row (hk, s, query head of the group), n_parts of them
-  const float* part_o;              // [n_parts][kv_heads * batch * group][D]
-  const float2* part_ml;            // m (log2 units), l
-  int n_parts, part_rows;           // part_rows: kv_heads * batch * group
+  // kBehindPrefix: n_parts partial results of row s group + e of a key head, in items (hk part_tiles + row / 128)
+  // n_parts + part
+  const float4* part_o;             // [item][D / 4][128]
+  const float2* part_ml;            // [item][128]: m (log2 units), l
+  int n_parts, part_tiles;
   // kScored
   float* scores;                    // [batch][kv_heads][head_groups][capacity][score_stride], log2 units
   const float* w_in;                // [batch][kv_heads][capacity]
@@ -603,6 +604,173 @@ __device__ void consumer16(const DParams& p, Bars& bars, uint8_t* ring, const Ro
   }
 }
 
+// The cluster's partial results (cm, cl, wo of every rank) and the prefix's, for this rank's share of the elements. The
+// factors 2^(m_k - M) of all parts come first, a (query head, part) a thread, so that the parts' elements are then
+// loaded without a wait between them (64 sequences, 19 parts: 31 us for the launch with a thread walking the parts
+// alone).
+template <int D>
+__device__ __forceinline__ void join_prefix(const DParams& p, cooperative_groups::cluster_group& cluster, float* cm, float* cl,
+                                            float* wo, int rank, int ranks, int s, int hk, int hg, int h0, int n_q) {
+  constexpr int kQ = 16, kFactors = 32;                    // parts at a time
+  const float kNegInf = __int_as_float(0xff800000);
+  __shared__ float fm[kQ][kMaxCluster + kFactors];         // maxima, then factors: the ranks', then the parts'
+  __shared__ float fl[kQ][kMaxCluster + kFactors];
+  __shared__ float top[kQ], sum[kQ];
+  const auto item_of = [&](int q, int k) {                 // and the row's place in it
+    const int row = s * p.group + hg * kQ + q;
+    return make_int2((hk * p.part_tiles + row / 128) * p.n_parts + k, row % 128);
+  };
+  const int c0 = rank * (D / 4) / ranks, c1 = (rank + 1) * (D / 4) / ranks;    // this rank's columns, four at a time
+  const int share = n_q * (c1 - c0);
+  constexpr int kEach = (kQ * (D / 4) + kThreads - 1) / kThreads;
+  float4 acc[kEach];
+#pragma unroll
+  for (int x = 0; x < kEach; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (threadIdx.x < kQ) {
+    top[threadIdx.x] = kNegInf;
+    sum[threadIdx.x] = 0.f;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the prefix's results
+  // several rounds where there are more parts than factors; the ranks' own come with the first
+#pragma unroll 1
+  for (int k0 = 0; k0 < p.n_parts; k0 += kFactors) {
+    const int n = min(kFactors, p.n_parts - k0), own = k0 == 0 ? ranks : 0, all = own + n;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_q * all; i += kThreads) {
+      const int q = i / all, k = i % all;
+      if (k < own) {
+        fm[q][k] = *cluster.map_shared_rank(cm + q, k);
+        fl[q][k] = *cluster.map_shared_rank(cl + q, k);
+      } else {
+        const int2 at = item_of(q, k0 + k - own);
+        const float2 ml = p.part_ml[(int64_t)at.x * 128 + at.y];
+        fm[q][k] = ml.x;
+        fl[q][k] = ml.y;
+      }
+    }
+    __syncthreads();
+    float back[kEach];                                     // of what has been added up so far
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int q = (threadIdx.x + x * kThreads) % n_q;
+      back[x] = 1.f;
+      if (k0 > 0) {
+        float M = top[q];
+        for (int k = 0; k < all; ++k) M = fmaxf(M, fm[q][k]);
+        back[x] = M != kNegInf ? ex2_approx(top[q] - M) : 1.f;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < n_q) {
+      const int q = threadIdx.x;
+      float M = top[q];
+      for (int k = 0; k < all; ++k) M = fmaxf(M, fm[q][k]);
+      // without a maximum the sums are zero, or NaN
+      float L = sum[q] * (M != kNegInf ? ex2_approx(top[q] - M) : 1.f);
+      for (int k = 0; k < all; ++k) {
+        const float a = M != kNegInf ? ex2_approx(fm[q][k] - M) : 1.f;
+        fm[q][k] = a;
+        L = fmaf(a, fl[q][k], L);
+      }
+      top[q] = M;
+      sum[q] = L;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int i = threadIdx.x + x * kThreads;
+      if (i >= share) continue;
+      const int q = i % n_q, col = 4 * (c0 + i / n_q);     // neighbouring rows lie together
+      float4 v = acc[x];
+      v.x *= back[x];
+      v.y *= back[x];
+      v.z *= back[x];
+      v.w *= back[x];
+      const auto add = [&](float a, const float4& y) {
+        v.x = fmaf(a, y.x, v.x);
+        v.y = fmaf(a, y.y, v.y);
+        v.z = fmaf(a, y.z, v.z);
+        v.w = fmaf(a, y.w, v.w);
+      };
+      for (int k = 0; k < own; ++k)
+        add(fm[q][k], *reinterpret_cast<const float4*>(cluster.map_shared_rank(wo + q * D + col, k)));
+      const int2 it = item_of(q, k0);
+      const float4* at = p.part_o + ((int64_t)it.x * (D / 4) + col / 4) * 128 + it.y;
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) add(fm[q][own + k], at[(int64_t)k * (D / 4) * 128]);
+      acc[x] = v;
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kEach; ++x) {
+    const int i = threadIdx.x + x * kThreads;
+    if (i >= share) continue;
+    const int q = i % n_q, col = 4 * (c0 + i / n_q);
+    const float L = sum[q], inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2*>(p.o + (int64_t)s * p.o_sb + (int64_t)(h0 + q) * p.o_sh + col) =
+        make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+    if (col == 0)
+      p.lse[(int64_t)s * p.heads + h0 + q] = L == 0.f ? kNegInf : (top[q] + __log2f(L)) * 0.69314718055994531f;
+  }
+}
+
+// Weights of rows begin, begin + step, .. below end of a (sequence, key head), whose query heads have maxima hm and inverse
+// sums hi. Several rows' scores are loaded at once: one after the other they took a third of the call (64
+// sequences of 2049 to 4096 slots).
+template <int STRIDE>
+__device__ __forceinline__ void add_weights(const DParams& p, int64_t list, int begin, int end, int step, const float* hm,
+                                            const float* hi) {
+  constexpr int kRows = STRIDE >= 8 ? 32 / STRIDE : 8, kLoad = STRIDE < 4 ? STRIDE : 4;
+#pragma unroll 1
+  for (int j0 = begin; j0 < end; j0 += kRows * step) {
+    float w[kRows], old[kRows];
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) {
+      const int j = j0 + x * step;
+      w[x] = 0.f;
+      old[x] = p.decay != 0.f && j < end ? p.w_in[list * p.capacity + j] : 0.f;
+    }
+#pragma unroll 1
+    for (int g0 = 0; g0 < p.head_groups; ++g0) {
+      const float* sc = p.scores + (list * p.head_groups + g0) * p.capacity * STRIDE;
+      const int n = min(16, p.group - g0 * 16);
+      float v[kRows][STRIDE];
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        const int j = j0 + x * step;
+#pragma unroll
+        for (int q = 0; q < STRIDE; q += kLoad) {
+          const float* at = sc + (int64_t)j * STRIDE + q;
+          if (j >= end) continue;
+          if constexpr (kLoad == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(at);
+            v[x][q] = y.x;
+            v[x][q + 1] = y.y;
+            v[x][q + 2] = y.z;
+            v[x][q + 3] = y.w;
+          } else if constexpr (kLoad == 2) {
+            const float2 y = *reinterpret_cast<const float2*>(at);
+            v[x][q] = y.x;
+            v[x][q + 1] = y.y;
+          } else {
+            v[x][q] = *at;
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kRows; ++x)
+#pragma unroll
+        for (int q = 0; q < STRIDE; ++q)               // places past the last head were never written
+          if (q < n) w[x] = fmaf(ex2_approx(v[x][q] - hm[g0 * 16 + q]), hi[g0 * 16 + q], w[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) {
+      const int j = j0 + x * step;
+      if (j < end) p.w_out[list * p.capacity + j] = fmaf(p.decay, old[x], w[x]);
+    }
+  }
+}
+
 // 4 bits, up to 8 query heads: four CTAs an SM (74 us; three with longer rings 80, five with shorter ones
 // and 80 registers 90 to 109).
 template <int D, bool Q4, int NQ, int MODE>
@@ -722,7 +890,11 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
   cluster.sync();
   // ---- the cluster's CTAs join their results: CTA `rank` writes its share of the elements. All the
   // remote loads go out together: one trip's latency, not one per CTA.
-  if constexpr (MODE == kBehindPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");   // the prefix's results
+  if constexpr (MODE == kBehindPrefix) {
+    join_prefix<D>(p, cluster, cm, cl, wo, rank, ranks, s, hk, hg, h0, n_q);
+    cluster.sync();                                         // no CTA leaves while another reads its results
+    return;
+  }
   const int first = MODE == kScored ? hg * ranks : 0;       // this head group's first CTA
   const int pairs = n_q * (D / 2);
   const int p0 = (int)((int64_t)pairs * rank / ranks), p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
@@ -745,21 +917,6 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mk[k]);
     float x = 0.f, y = 0.f, L = 0.f;
-    if constexpr (MODE == kBehindPrefix) {
-      const int64_t at_row = ((int64_t)hk * gridDim.z + s) * p.group + hg * kQ + row;
-      const float2* ml = p.part_ml + at_row;
-#pragma unroll 8
-      for (int k = 0; k < p.n_parts; ++k) M = fmaxf(M, ml[(int64_t)k * p.part_rows].x);
-#pragma unroll 4
-      for (int k = 0; k < p.n_parts; ++k) {
-        const float2 e = ml[(int64_t)k * p.part_rows];
-        const float2 z = *reinterpret_cast<const float2*>(p.part_o + ((int64_t)k * p.part_rows + at_row) * D + col);
-        const float a = M != kNegInf ? ex2_approx(e.x - M) : 1.f;
-        x = fmaf(a, z.x, x);
-        y = fmaf(a, z.y, y);
-        L = fmaf(a, e.y, L);
-      }
-    }
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) {
       const float a = M != kNegInf ? ex2_approx(mk[k] - M) : 1.f;
@@ -790,16 +947,14 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_k
     }
     __syncthreads();
     const int64_t list = (int64_t)s * p.kv_heads + hk;
-    const int end = min(r.len, r.end * kUnit);
-    for (int j = r.begin * kUnit + hg * kThreads + threadIdx.x; j < end; j += p.head_groups * kThreads) {
-      float w = 0.f;
-      for (int g0 = 0; g0 < p.head_groups; ++g0) {
-        const float* sc = p.scores + ((list * p.head_groups + g0) * p.capacity + j) * p.score_stride;
-        const int n = min(kQ, p.group - g0 * kQ);
-        for (int q = 0; q < n; ++q) w = fmaf(ex2_approx(sc[q] - hm[g0 * kQ + q]), hi[g0 * kQ + q], w);
-      }
-      const int64_t at = list * p.capacity + j;
-      p.w_out[at] = p.decay != 0.f ? fmaf(p.decay, p.w_in[at], w) : w;
+    const int begin = r.begin * kUnit + hg * kThreads + (int)threadIdx.x, end = min(r.len, r.end * kUnit);
+    const int step = p.head_groups * kThreads;
+    switch (p.score_stride) {
+      case 1: add_weights<1>(p, list, begin, end, step, hm, hi); break;
+      case 2: add_weights<2>(p, list, begin, end, step, hm, hi); break;
+      case 4: add_weights<4>(p, list, begin, end, step, hm, hi); break;
+      case 8: add_weights<8>(p, list, begin, end, step, hm, hi); break;
+      default: add_weights<16>(p, list, begin, end, step, hm, hi);
     }
   }
   cluster.sync();                                           // no CTA leaves while another reads its results
@@ -843,10 +998,10 @@ int launch(const SinkDecodeArgs& a, cudaStream_t stream) {
   p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
   p.code_mask = 0x000f000fu;
   if (MODE == kBehindPrefix) {
-    p.part_o = a.part_o;
+    p.part_o = static_cast<const float4*>(a.part_o);
     p.part_ml = static_cast<const float2*>(a.part_ml);
     p.n_parts = a.n_parts;
-    p.part_rows = a.batch * a.heads;
+    p.part_tiles = a.part_tiles;
   }
   if (MODE == kScored) {
     p.scores = a.scores;

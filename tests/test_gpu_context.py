@@ -216,6 +216,7 @@ EVICT_CASES = [
     (4, 700, 2, 64, [700, 699, 513, 20], 512, 4, 100), (2, 700, 2, 128, [700, 400], 30, 4, 0), (1, 5000, 3, 32, [5000], 4999, 0, 0),
     (2, 4104, 4, 128, [4097, 4104], 4096, 4, 512), (1, 9000, 2, 64, [9000], 1, 0, 1), (3, 3000, 2, 32, [3000, 2999, 1501], 1500, 16, 700),
     (1, 20000, 2, 32, [20000], 9000, 4, 1000), (2, 17001, 1, 64, [17001, 16999], 16998, 1, 1), (2, 50, 2, 64, [50, 49], 60, 0, 0),
+    (1, 33000, 2, 32, [33000], 20000, 4, 1000), (2, 8192, 1, 32, [8192, 8191], 4096, 0, 4096), (2, 8193, 1, 64, [8193, 100], 4000, 100, 0),
 ]
 
 
