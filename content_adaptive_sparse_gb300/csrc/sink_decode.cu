@@ -774,7 +774,7 @@ __device__ __forceinline__ void add_weights(const DParams& p, int64_t list, int 
 // 4 bits, up to 8 query heads: four CTAs an SM (74 us; three with longer rings 80, five with shorter ones
 // and 80 registers 90 to 109).
 template <int D, bool Q4, int NQ, int MODE>
-__global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : 1) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
+__global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : (MODE != kPlain ? 2 : 1)) sink_decode_kernel(const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv,
                                                                const __grid_constant__ DParams p) {
   using C = Cfg<D, Q4, NQ>;
