@@ -16,7 +16,7 @@
 // (two-term sums), since a key of a long prompt gathers from some 10^5 queries.
 //
 // Warp roles (640 threads): 0-15 exponentials and sums (key tile w / 4 % 2, queries 64 (w / 8) .. of the step's); 16 loads K and
-// Q; 17 issues the products; 18 brings LSE. The two key tiles have barriers of their own, so that a scheduler's four
+// Q; 17 issues the products; 18 and 19 bring LSE. The two key tiles have barriers of their own, so that a scheduler's four
 // warps are at different places of a step.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -36,7 +36,10 @@ __device__ unsigned int g_weights_err;
 
 constexpr int kTile = 128, kPair = 256;
 constexpr int kThreads = 640, kSumWarps = 16;
-constexpr uint32_t kTmemCols = 512;      // S^T of key tile w in buffer b: 128 columns at 256 b + 128 w
+// TMEM: three buffers of S^T, 128 columns each, for the products in turn (step g, key tile x: product 2 g + x); then the list's
+// two key tiles.
+constexpr uint32_t kTmemCols = 512, kColK = 384;
+constexpr int kStages = 4;               // query tiles, and numbers -LSE / scale, in shared memory
 
 // The products' last step: tiles of 128 rows of 64 bytes (64-byte swizzle). Ones in the first 32 bytes of one, and -LSE / scale
 // of four steps in both halves of two.
@@ -53,9 +56,7 @@ struct Cfg {
   static constexpr uint32_t ATOM = 8 * ROWB;
   static constexpr int CHUNK = kTile * ROWB;
   static constexpr int TILE = NCH * CHUNK;
-  static constexpr int QS = D == 128 ? 3 : 4;          // query tiles in shared memory
-  static constexpr int KS = D == 128 ? 3 : 4;          // key tiles: a list's two, and one or two of the next list
-  static constexpr int SMEM = 1024 + (KS + QS) * TILE + 3 * kSide;
+  static constexpr int SMEM = 1024 + (2 + kStages) * TILE + 3 * kSide;   // two key tiles on their way to TMEM
   static_assert(SMEM <= 222 * 1024, "shared memory");
 };
 
@@ -64,16 +65,19 @@ struct WParams {
   int tiles, pairs;                 // query tiles, lists of a (sequence, key head)
   int first_tile, reach;            // the first query's tile; query tiles past 2 t that keys of list t reach
   int skip;                         // lists below it have no steps, but for the sinks'
+  int small;                        // all steps are fewer than 2^31
   int window, sinks, first;
   int64_t all;                      // steps of one query head of a (sequence, key head)
-  int64_t total;                    // steps
+  int64_t total;                    // steps: `quota` a CTA, and one more for the first `rest`
+  int64_t quota;
+  int rest;
   const float* lse;
   float* weights;
   float* partial;                   // [CTA][2][256]
   float scale_log2, inv_scale;
 };
 
-__host__ __device__ inline int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
+__host__ __device__ inline int clamp(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // Query tiles of list t: first and last (none: last < first).
 __host__ __device__ inline void span(const WParams& p, int t, int& i0, int& i1) {
@@ -83,20 +87,26 @@ __host__ __device__ inline void span(const WParams& p, int t, int& i0, int& i1) 
 }
 
 // Query tiles of the lists before list t, were it not for the sinks: for t' >= a, where the spans begin to hold
-// tiles, the sum of min(tiles - 1, 2 t' + reach) - max(first_tile, 2 t') + 1.
-__host__ __device__ inline int64_t before_without_sinks(const WParams& p, int64_t t) {
-  const int64_t f = p.first_tile, r = p.reach, last = p.tiles - 1;
-  int64_t a = f > r ? (f - r + 1) / 2 : 0;
-  if (a > t) a = t;
-  const int64_t x = clamp64(last >= r ? (last - r) / 2 + 1 : 0, a, t);      // min is 2 t' + r below x
-  const int64_t y = clamp64(f / 2 + 1, a, t);                               // max is f below y
-  return x * (x - 1) - a * (a - 1) + (x - a) * r + (t - x) * last - (y - a) * f - (t * (t - 1) - y * (y - 1)) + (t - a);
+// tiles, the sum of min(tiles - 1, 2 t' + reach) - max(first_tile, 2 t') + 1. Modulo 2^32 with N = uint32_t, which is enough
+// where the steps of all lists are fewer (64-bit products are long chains, and every CTA begins with them).
+template <class N>
+__host__ __device__ inline N before_without_sinks(const WParams& p, int t) {
+  const int f = p.first_tile, r = p.reach, last = p.tiles - 1;
+  const int a = p.skip < t ? p.skip : t;
+  const int x = clamp(last >= r ? (last - r) / 2 + 1 : 0, a, t);      // min is 2 t' + r below x
+  const int y = clamp(f / 2 + 1, a, t);                               // max is f below y
+  const N A = a, X = x, Y = y, T = t;
+  return X * (X - 1) - A * (A - 1) + (X - A) * (N)r + (T - X) * (N)last - (Y - A) * (N)f - (T * (T - 1) - Y * (Y - 1)) + (T - A);
 }
-__host__ __device__ inline int64_t before(const WParams& p, int64_t t) {
-  if (t == 0 || p.sinks == 0) return before_without_sinks(p, t);
+template <class N>
+__host__ __device__ inline N before_of(const WParams& p, int t) {
+  if (t == 0 || p.sinks == 0) return before_without_sinks<N>(p, t);
   int i0, i1;
   span(p, 0, i0, i1);
-  return before_without_sinks(p, t) - before_without_sinks(p, 1) + (i1 - i0 + 1);
+  return before_without_sinks<N>(p, t) - before_without_sinks<N>(p, 1) + (N)(i1 - i0 + 1);
+}
+__host__ __device__ inline int64_t before(const WParams& p, int t) {
+  return p.small ? (int64_t)before_of<uint32_t>(p, t) : before_of<int64_t>(p, t);
 }
 
 // The last list that begins at r or before, found by all lanes of a warp (one comparison after the other took 5 us of
@@ -126,16 +136,22 @@ struct Walk {
   int sh, t, i0, count;             // the list's first query tile and number of them
   int64_t list;                     // where it begins
   int jb, je;
-  __host__ __device__ static int64_t bound(const WParams& p, int c, int ctas) { return p.total * c / ctas; }
+  __host__ __device__ static int64_t bound(const WParams& p, int c) { return p.quota * c + (c < p.rest ? c : p.rest); }
   // (by all lanes of a warp)
-  __host__ __device__ Walk(const WParams& p, int c, int ctas) : Walk(p, bound(p, c, ctas), bound(p, c + 1, ctas)) {}
+  __host__ __device__ Walk(const WParams& p, int c) : Walk(p, bound(p, c), bound(p, c + 1)) {}
   __host__ __device__ Walk(const WParams& p, int64_t from, int64_t to) : at(from), end(to) {
     sh = t = i0 = count = jb = je = 0;
     list = 0;
     if (at >= end) return;
     const int64_t per = p.all * p.group;
-    sh = (int)(at / per);
-    const int64_t r = (at - sh * per) / p.group;
+    int64_t r;
+    if (p.small) {                  // divisions of 64 bits are long
+      sh = (int)((uint32_t)at / (uint32_t)per);
+      r = (uint32_t)(at - sh * per) / (uint32_t)p.group;
+    } else {
+      sh = (int)(at / per);
+      r = (at - sh * per) / p.group;
+    }
     t = Search()(p, r);
     list = sh * per + before(p, t) * p.group;
     set(p);
@@ -175,16 +191,12 @@ struct Step {
   }
 };
 
-// Whether some query of tile i sees some key of tile k.
-__host__ __device__ inline bool tile_seen(const WParams& p, int i, int k) {
-  return k * kTile < p.n && i >= k && (i * kTile - (k * kTile + kTile - 1) <= p.window || k * kTile < p.sinks);
-}
-
 struct Bars {
-  uint64_t k_full[4], k_empty[4];        // key tile x of the CTA's list n: use 2 n + x of the ring
-  uint64_t q_full[4], q_empty[4];
-  uint64_t s_full[2][2], s_empty[2][2];  // [key tile][buffer]
-  uint64_t lse_full[4], lse_empty[4];
+  uint64_t k_full[2], k_empty[2];        // key tile x of the CTA's list n, phase n: in shared memory; copied from there
+  uint64_t kt_full[2];                   // in TMEM
+  uint64_t q_full[kStages], q_empty[kStages];   // step g: stage g % 4, phase g / 4
+  uint64_t s_full[2][3];                 // key tile x, step g: [x][g % 3], phase g / 3
+  uint64_t s_empty[3];                   // product u: buffer u % 3, phase u / 3
   uint64_t drain;
 };
 
@@ -198,46 +210,48 @@ __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
 
 // ------------------------------------------------------------------ loader (warp 16, one lane)
 
+// Waits for the last copies: of the keys of list n and of the query tiles before g. (A copy that was never asked for ends
+// the wait by its limit; that is after a wait that has already run out.)
+__device__ void drain(Bars& bars, int n, int g) {
+  if (n >= 0)
+    for (int x = 0; x < 2; ++x) drain_bar(&bars.k_full[x], (uint32_t)n & 1u);
+  for (int i = max(0, g - kStages); i < g; ++i) drain_bar(&bars.q_full[i % kStages], (uint32_t)(i / kStages) & 1u);
+}
+
 template <int D>
 __device__ void loader(const WParams& p, Walk w, const CUtensorMap* tq, const CUtensorMap* tk, Bars& bars, uint8_t* sK,
                        uint8_t* sQ, volatile int* abort_flag) {
   using C = Cfg<D>;
-  int n = 0, g = 0;                  // key and query tiles asked for
+  int n = 0, g = 0;                  // lists and query tiles asked for
   bool ok = true;
-  for (; ok && w.more(); w.next(p)) {
+  for (; ok && w.more(); w.next(p), ++n) {
     const int s = w.sh / p.kv_heads, hk = w.sh - s * p.kv_heads;
-    const auto keys = [&](int x) {
-      const int kb = n % C::KS, tok = w.t * kPair + x * kTile;
-      if (n >= C::KS && !wait_bar(&bars.k_empty[kb], (uint32_t)(n / C::KS - 1) & 1u, abort_flag)) return false;
+    for (int x = 0; ok && x < 2; ++x) {
+      const int tok = w.t * kPair + x * kTile;
+      if (n > 0 && !(ok = wait_bar(&bars.k_empty[x], (uint32_t)(n - 1) & 1u, abort_flag))) break;
       if (tok < p.n) {
-        mbar_arrive_expect_tx(&bars.k_full[kb], C::TILE);
+        mbar_arrive_expect_tx(&bars.k_full[x], C::TILE);
 #pragma unroll
         for (int c = 0; c < C::NCH; ++c)
-          tma_load_4d(sK + kb * C::TILE + c * C::CHUNK, tk, &bars.k_full[kb], c * C::CH, hk, tok, s);
+          tma_load_4d(sK + x * C::TILE + c * C::CHUNK, tk, &bars.k_full[x], c * C::CH, hk, tok, s);
       } else {
-        mbar_arrive(&bars.k_full[kb]);                 // no such tile
+        mbar_arrive(&bars.k_full[x]);                  // no such tile
       }
-      ++n;
-      return true;
-    };
-    if (!(ok = keys(0))) break;
+    }
+    if (!ok) break;
     Step st(w);
     for (int j = w.jb; j < w.je; ++j, ++g, st.next(w)) {
-      const int qb = g % C::QS;
-      if (g >= C::QS && !(ok = wait_bar(&bars.q_empty[qb], (uint32_t)(g / C::QS - 1) & 1u, abort_flag))) break;
+      const int qb = g % kStages;
+      if (g >= kStages && !(ok = wait_bar(&bars.q_empty[qb], (uint32_t)(g / kStages - 1) & 1u, abort_flag))) break;
       mbar_arrive_expect_tx(&bars.q_full[qb], C::TILE);
 #pragma unroll
       for (int c = 0; c < C::NCH; ++c)
         tma_load_4d(sQ + qb * C::TILE + c * C::CHUNK, tq, &bars.q_full[qb], c * C::CH, hk * p.group + st.e, st.i * kTile, s);
-      if (j == w.jb && !(ok = keys(1))) {
-        ++g;
-        break;
-      }
     }
   }
   // every copy of this CTA has landed before it may exit
-  for (int i = max(0, n - C::KS); i < n; ++i) drain_bar(&bars.k_full[i % C::KS], (uint32_t)(i / C::KS) & 1u);
-  for (int i = max(0, g - C::QS); i < g; ++i) drain_bar(&bars.q_full[i % C::QS], (uint32_t)(i / C::QS) & 1u);
+  drain(bars, n - 1, g);
+  if (!ok) drain(bars, n, 0);
 }
 
 // Tile of step g's -LSE / scale; it is in its 32-byte half g % 2.
@@ -245,47 +259,59 @@ __device__ __forceinline__ int side_slot(int g) { return (1 + (g >> 1 & 1)) * kS
 
 // ------------------------------------------------------------------ products (warp 17, one lane)
 
+// One thread for both tiles, so that their products, and with them the summing warps, stay half a step apart (with
+// a thread for each: 189 -> 212 us). Its instructions are the longest chain of a step, so counters take the
+// place of divisions and what a list fixes is worked out once.
 template <int D>
-__device__ void issuer(const WParams& p, Walk w, Bars& bars, uint8_t* sK, uint8_t* sQ, uint8_t* sSide, uint32_t tmem,
+__device__ void issuer(const WParams& p, Walk w, Bars& bars, uint8_t* sQ, uint8_t* sSide, uint32_t tmem,
                        volatile int* abort_flag) {
   using C = Cfg<D>;
-  const uint64_t side = make_smem_desc(smem_u32(sSide), 16, 512, kSwizzle64B);     // ones; then -LSE / scale
-  const uint64_t k0 = make_smem_desc(smem_u32(sK), 16, C::ATOM, C::SWZ);
+  const uint64_t ones = make_smem_desc(smem_u32(sSide), 16, 512, kSwizzle64B);
   const uint64_t q0 = make_smem_desc(smem_u32(sQ), 16, C::ATOM, C::SWZ);
   constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
-  int n = 0, g = 0;
+  uint32_t g = 0;                    // step
+  uint32_t r = 0, buf = 0, used = 0; // g % 3; of the next product: its buffer, and whether that was in use, with the phase
   bool ok = true;
-  for (; ok && w.more(); w.next(p), n += 2) {
-    Step st(w);
-    for (int j = w.jb; ok && j < w.je; ++j, ++g, st.next(w)) {
-      const int qb = g % C::QS, b = g & 1;
-      if (!(ok = wait_bar(&bars.q_full[qb], (uint32_t)(g / C::QS) & 1u, abort_flag))) break;
-      if (!(ok = wait_bar(&bars.lse_full[g & 3], (uint32_t)(g >> 2) & 1u, abort_flag))) break;
+  for (int n = 0; ok && w.more(); w.next(p), ++n) {
+    int i0[2], i1[2];                // query tiles that see some of a tile's keys
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int k = 2 * w.t + x;
+      i0[x] = k;
+      i1[x] = k * kTile < p.sinks ? p.tiles - 1 : (int)(((int64_t)k * kTile + kTile - 1 + p.window) / kTile);
+      if (k * kTile >= p.n) i1[x] = -1;
+      ok = ok && wait_bar(&bars.kt_full[x], (uint32_t)n & 1u, abort_flag);
+    }
+    int i = w.i0 + w.jb % w.count;
+    const int i_end = w.i0 + w.count;
+    for (int j = w.jb; ok && j < w.je; ++j, ++g) {
+      const uint32_t qb = g % kStages;
+      if (!(ok = wait_bar(&bars.q_full[qb], g / kStages & 1u, abort_flag))) break;
+      const uint64_t q = q0 + (uint64_t)(qb * (uint32_t)(C::TILE >> 4));
+      const uint64_t side = ones + (uint64_t)((side_slot(g) + 32 * (g & 1)) >> 4);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int kb = (n + x) % C::KS;
-        if (j == w.jb && !(ok = wait_bar(&bars.k_full[kb], (uint32_t)((n + x) / C::KS) & 1u, abort_flag))) break;
-        if (g >= 2 && !(ok = wait_bar(&bars.s_empty[x][b], (uint32_t)(g / 2 - 1) & 1u, abort_flag))) break;
+        if (used > 0 && !(ok = wait_bar(&bars.s_empty[buf], (used - 1) & 1u, abort_flag))) break;
         tc_fence_after();
-        if (tile_seen(p, st.i, 2 * w.t + x)) {
+        if (i >= i0[x] && i <= i1[x]) {
+          const uint32_t s = tmem + 128u * buf, keys = tmem + kColK + (uint32_t)(D / 2) * x;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t at = (uint64_t)((((ks * 16) / C::CH) * C::CHUNK + ((ks * 16) % C::CH) * 2) >> 4);
-            mma_bf16_ss(tmem + 256u * b + 128u * x, k0 + (uint64_t)((kb * C::TILE) >> 4) + at,
-                        q0 + (uint64_t)((qb * C::TILE) >> 4) + at, idesc, ks > 0 ? 1u : 0u);
+            constexpr int kPer = C::CH / 16;
+            mma_bf16_ts(s, keys + 8u * ks, q + (uint64_t)(((ks / kPer) * C::CHUNK + (ks % kPer) * 32) >> 4), idesc,
+                        ks > 0 ? 1u : 0u);
           }
-          mma_bf16_ss(tmem + 256u * b + 128u * x, side, side + (uint64_t)((side_slot(g) + 32 * (g & 1)) >> 4), idesc, 1u);
+          mma_bf16_ss(s, ones, side, idesc, 1u);
         }
-        mma_commit(&bars.s_full[x][b]);
+        mma_commit(&bars.s_full[x][r]);
+        if (++buf == 3) {
+          buf = 0;
+          ++used;
+        }
       }
-      if (ok) {
-        mma_commit(&bars.q_empty[qb]);
-        mma_commit(&bars.lse_empty[g & 3]);
-      }
-    }
-    if (ok) {
-      mma_commit(&bars.k_empty[n % C::KS]);
-      mma_commit(&bars.k_empty[(n + 1) % C::KS]);
+      if (ok) mma_commit(&bars.q_empty[qb]);
+      r = r == 2 ? 0 : r + 1;
+      if (++i == i_end) i = w.i0;
     }
   }
   // no MMA of this thread is still at work when the CTA frees its TMEM
@@ -293,57 +319,59 @@ __device__ void issuer(const WParams& p, Walk w, Bars& bars, uint8_t* sK, uint8_
   drain_bar(&bars.drain, 0);
 }
 
-// ------------------------------------------------------------------ -LSE / scale (warp 18)
+// ------------------------------------------------------------------ -LSE / scale (warps 18, 19)
 
 // Eight bf16 elements of a row of a tile.
 __device__ __forceinline__ uint32_t side_unit(uint8_t* side, int row, int unit) {
   return smem_u32(side) + (uint32_t)(64 * row + ((unit ^ ((row >> 1) & 3)) << 4));
 }
 
-// A step's 128 numbers are asked for two steps ahead of their use.
-__device__ void lse_rows(const WParams& p, Walk w, Bars& bars, uint8_t* sSide, volatile int* abort_flag) {
+// Every second step from `which` on (one warp for all was the longest chain of a step). A step's 128 numbers are asked
+// for while those of the warp's step before are split.
+__device__ void lse_rows(const WParams& p, Walk w, int which, Bars& bars, uint8_t* sSide, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
-  const auto ask = [&](const Walk& at, const Step& st, float (&v)[4]) {
-    const int s = at.sh / p.kv_heads, hk = at.sh - s * p.kv_heads;
-    const float* row = p.lse + ((int64_t)s * p.heads + hk * p.group + st.e) * p.n;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int i = st.i * kTile + 32 * x + lane;
-      v[x] = i < p.n ? row[i] * -p.inv_scale : 0.f;
-    }
-  };
   // the place of the step that is asked for next
-  Step st(w);
-  int j = w.jb;
-  const auto advance = [&] {
-    st.next(w);
-    if (++j == w.je) {
-      w.next(p);
-      if (w.more()) {
-        st = Step(w);
-        j = w.jb;
-      }
-    }
+  int j = w.jb, i = w.i0 + w.jb % w.count;
+  const float* row = nullptr;
+  const auto head = [&] {
+    const int s = w.sh / p.kv_heads, hk = w.sh - s * p.kv_heads;
+    row = p.lse + ((int64_t)s * p.heads + hk * p.group + j / w.count) * p.n;
   };
-  float v[3][4];
-  int asked = 0;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (w.more()) {
-      ask(w, st, v[k]);
-      advance();
-      ++asked;
+  const auto advance = [&] {
+    if (++i == w.i0 + w.count) {
+      i = w.i0;
+      row += p.n;
     }
-  for (int g = 0; g < asked; ++g) {
-    if (w.more()) {
-      ask(w, st, v[2]);
-      advance();
-      ++asked;
-    }
-    if (g >= 4 && !__all_sync(0xffffffffu, wait_bar(&bars.lse_empty[g & 3], (uint32_t)(g / 4 - 1) & 1u, abort_flag))) return;
+    if (++j < w.je) return;
+    w.next(p);
+    if (!w.more()) return;
+    j = w.jb;
+    i = w.i0 + w.jb % w.count;
+    head();
+  };
+  const auto ask = [&](float (&v)[4]) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const float y = v[0][x];
+      const int q = i * kTile + 32 * x + lane;
+      v[x] = q < p.n ? row[q] : 0.f;
+    }
+    advance();
+    if (w.more()) advance();
+  };
+  head();
+  if (which == 1) advance();
+  float v[4], ahead[4];
+  bool on = w.more();
+  if (on) ask(v);
+  for (int g = which; on; g += 2) {
+    const bool more = w.more();
+    if (more) ask(ahead);
+    if (g >= kStages && !__all_sync(0xffffffffu, wait_bar(&bars.q_empty[g % kStages], (uint32_t)(g / kStages - 1) & 1u, abort_flag)))
+      return;
+    uint8_t* tile = sSide + side_slot(g);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float y = v[x] * -p.inv_scale;
       float part[3] = {y, 0.f, 0.f};
       const uint32_t top = __float_as_uint(y) & 0x7f800000u;
       if (top != 0x7f800000u) {                        // numbers: y = part 0 + part 1 + part 2
@@ -351,14 +379,13 @@ __device__ void lse_rows(const WParams& p, Walk w, Bars& bars, uint8_t* sSide, v
         part[1] = __bfloat162float(__float2bfloat16_rn(y - part[0]));
         part[2] = y - part[0] - part[1];
       }
-      st_shared_v4(side_unit(sSide + side_slot(g), 32 * x + lane, 2 * (g & 1)), pack_bf16x2(part[0], part[1]),
-                   pack_bf16x2(part[2], 0.f), 0u, 0u);
-      v[0][x] = v[1][x];
-      v[1][x] = v[2][x];
+      st_shared_v4(side_unit(tile, 32 * x + lane, 2 * (g & 1)), pack_bf16x2(part[0], part[1]), pack_bf16x2(part[2], 0.f), 0u, 0u);
+      v[x] = ahead[x];
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.lse_full[g & 3]);
+    if (lane == 0) mbar_arrive(&bars.q_full[g % kStages]);
+    on = more;
   }
 }
 
@@ -379,13 +406,51 @@ __device__ __forceinline__ void add_chunk(const uint32_t* v, uint64_t c2, uint32
   }
 }
 
-__device__ void sums(const WParams& p, Walk w, Bars& bars, float (*joint)[kPair], uint32_t tmem, volatile int* abort_flag) {
+// This warp's 32 rows of a key tile in shared memory, half of their elements, into TMEM as the products' A operand.
+template <int D>
+__device__ __forceinline__ void keys_to_tmem(const uint8_t* tile, int quarter, int half, int lane, uint32_t to) {
+  using C = Cfg<D>;
+  constexpr int kUnits = D / 16;       // 16-byte units of half a row
+  const int row = 32 * quarter + lane;
+  uint32_t v[4 * kUnits];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int unit = kUnits * half + k, c = unit / (C::CH / 8), u = unit % (C::CH / 8);
+    const int x = C::ROWB == 128 ? row & 7 : (row >> 1) & 3;
+    const uint32_t at = smem_u32(tile) + (uint32_t)(c * C::CHUNK + row * C::ROWB + ((u ^ x) << 4));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[4 * k]), "=r"(v[4 * k + 1]), "=r"(v[4 * k + 2]), "=r"(v[4 * k + 3])
+                 : "r"(at));
+  }
+  if constexpr (D == 128) tmem_st_x32(to + 32 * half, v);
+  else if constexpr (D == 64) tmem_st_x16(to + 16 * half, v);
+  else tmem_st_x8(to + 8 * half, v);
+  tmem_st_wait();
+}
+
+template <int D>
+__device__ void sums(const WParams& p, Walk w, Bars& bars, const uint8_t* sK, float (*joint)[kPair], uint32_t tmem,
+                     volatile int* abort_flag) {
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // warp: uniform
   const int quarter = warp & 3, x = warp >> 2 & 1, half = warp >> 3;
-  const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + 128u * x + 64u * half;
+  const uint32_t rows = tmem + ((uint32_t)(quarter * 32) << 16), ts = rows + 64u * half;
   const uint64_t c2 = f2::pack(p.scale_log2, p.scale_log2);
-  int g = 0;
+  const auto done = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, wait_bar(bar, parity & 1u, abort_flag))) return true;
+    asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 7)) : "memory");    // the other half may wait for this one
+    return false;
+  };
+  uint32_t r = 0, turn = 0, buf = x;     // step g: g % 3, g / 3; buffer of product 2 g + x
   for (int n = 0; w.more(); w.next(p), ++n) {
+    // the products of the list before have all been seen: its keys may go
+    if (!done(&bars.k_full[x], (uint32_t)n)) return;
+    keys_to_tmem<D>(sK + x * Cfg<D>::TILE, quarter, half, lane, rows + kColK + (uint32_t)(D / 2) * x);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bars.k_empty[x]);
+      mbar_arrive(&bars.kt_full[x]);
+    }
     const int tile = 2 * w.t + x, k0 = tile * kTile + 32 * quarter, key = k0 + lane;
     // queries that see this thread's key, some key of the warp, every key of the warp (keys past the sequence
     // are not written and count with none)
@@ -395,40 +460,34 @@ __device__ void sums(const WParams& p, Walk w, Bars& bars, float (*joint)[kPair]
     const int any_lo = max(k0, p.first), any_hi = k0 < p.sinks ? end : last(min(k0 + 31, end));
     const int all_lo = max(k0 + 31, p.first), all_hi = k0 < p.sinks && k0 + 31 >= p.sinks ? last(p.sinks) : last(k0);
     float total = 0.f, lost = 0.f;
-    Step st(w);
-    for (int j = w.jb; j < w.je; ++j, ++g, st.next(w)) {
-      const int b = g & 1;
-      const uint32_t parity = (uint32_t)(g >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, wait_bar(&bars.s_full[x][b], parity, abort_flag))) {
-        asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 7)) : "memory");    // the other half may wait for this one
-        return;
-      }
-      const int qa = st.i * kTile + 64 * half, qb = qa + 32;
-      const bool on0 = qa + 31 >= any_lo && qa <= any_hi, on1 = qb + 31 >= any_lo && qb <= any_hi;
-      if ((on0 || on1) && tile_seen(p, st.i, tile)) {
+    int i = w.i0 + w.jb % w.count;
+    const int i_end = w.i0 + w.count;
+    for (int j = w.jb; j < w.je; ++j) {
+      if (!done(&bars.s_full[x][r], turn)) return;
+      const int q = i * kTile + 64 * half;
+      if (k0 < p.n && q + 63 >= any_lo && q <= any_hi) {
         tc_fence_after();
-        const uint32_t at = ts + 256u * b;
+        const uint32_t at = ts + 128u * buf;
         uint64_t sum[2] = {0ull, 0ull};
-        const auto chunk = [&](int q, const uint32_t* y) {
-          if (q >= all_lo && q + 31 <= all_hi) {
-            add_chunk<false>(y, c2, 0u, sum);
-          } else {
-            const int a = lo - q, z = hi - q;
+        uint32_t v[32], u[32];
+        if (q >= all_lo && q + 63 <= all_hi) {
+          tmem_ld_x32(at, v);
+          tmem_ld_wait<32>(v);
+          tmem_ld_x32(at + 32, u);                     // arrives under the first 32
+          add_chunk<false>(v, c2, 0u, sum);
+          tmem_ld_wait<32>(u);
+          add_chunk<false>(u, c2, 0u, sum);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            if (q + c + 31 < any_lo || q + c > any_hi) continue;
+            tmem_ld_x32(at + c, v);
+            tmem_ld_wait<32>(v);
+            const int a = lo - q - c, z = hi - q - c;
             const uint32_t upto = z >= 31 ? 0xffffffffu : (z < 0 ? 0u : ((2u << z) - 1u));
             const uint32_t from = a <= 0 ? 0xffffffffu : (a >= 32 ? 0u : (0xffffffffu << a));
-            add_chunk<true>(y, c2, upto & from, sum);
+            add_chunk<true>(v, c2, upto & from, sum);
           }
-        };
-        uint32_t v[32], u[32];
-        tmem_ld_x32(on0 ? at : at + 32, v);
-        tmem_ld_wait<32>(v);
-        if (on0 && on1) {                              // the second 32 arrive under the first
-          tmem_ld_x32(at + 32, u);
-          chunk(qa, v);
-          tmem_ld_wait<32>(u);
-          chunk(qb, u);
-        } else {
-          chunk(on0 ? qa : qb, v);
         }
         float a, z;
         f2::unpack(f2::add(sum[0], sum[1]), a, z);
@@ -439,7 +498,13 @@ __device__ void sums(const WParams& p, Walk w, Bars& bars, float (*joint)[kPair]
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
+      if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
+      if (++r == 3) {
+        r = 0;
+        ++turn;
+      }
+      buf = buf == 0 ? 2 : buf - 1;                    // two products on
+      if (++i == i_end) i = w.i0;
     }
     // the two halves of the queries: warps w and w + 8
     const int mine = x * kTile + 32 * quarter + lane;
@@ -471,25 +536,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // uniform
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&bars.s_full[x][i], 1);
-        mbar_init(&bars.s_empty[x][i], kSumWarps / 2);
-      }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars.k_full[x], 1);
+      mbar_init(&bars.k_empty[x], kSumWarps / 2);
+      mbar_init(&bars.kt_full[x], kSumWarps / 2);
+      for (int i = 0; i < 3; ++i) mbar_init(&bars.s_full[x][i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars.lse_full[i], 1);
-      mbar_init(&bars.lse_empty[i], 1);
-    }
-    for (int i = 0; i < C::KS; ++i) {
-      mbar_init(&bars.k_full[i], 1);
-      mbar_init(&bars.k_empty[i], 1);
-    }
-    for (int i = 0; i < C::QS; ++i) {
-      mbar_init(&bars.q_full[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&bars.s_empty[i], kSumWarps / 2);
+    mbar_init(&bars.drain, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars.q_full[i], 2);                   // the tile, and -LSE / scale
       mbar_init(&bars.q_empty[i], 1);
     }
-    mbar_init(&bars.drain, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -498,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   uint8_t* sK = sbase;
-  uint8_t* sQ = sK + C::KS * C::TILE;
-  uint8_t* sSide = sQ + C::QS * C::TILE;
+  uint8_t* sQ = sK + 2 * C::TILE;
+  uint8_t* sSide = sQ + kStages * C::TILE;
   if (threadIdx.x < 3 * kTile) {
     // ones in the first three columns; zeros everywhere else
     const int m = threadIdx.x / kTile, row = threadIdx.x % kTile;
@@ -512,17 +570,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const Walk w(p, (int)blockIdx.x, (int)gridDim.x);
+  const Walk w(p, (int)blockIdx.x);
   if (warp < kSumWarps) {
-    sums(p, w, bars, joint, tmem, &abort_flag);
+    sums<D>(p, w, bars, sK, joint, tmem, &abort_flag);
   } else if (warp == 16) {
     if (elect_one()) loader<D>(p, w, &tq, &tk, bars, sK, sQ, &abort_flag);
     __syncwarp();
   } else if (warp == 17) {
-    if (elect_one()) issuer<D>(p, w, bars, sK, sQ, sSide, tmem, &abort_flag);
+    if (elect_one()) issuer<D>(p, w, bars, sQ, sSide, tmem, &abort_flag);
     __syncwarp();
-  } else if (warp == 18) {
-    lse_rows(p, w, bars, sSide, &abort_flag);
+  } else {
+    lse_rows(p, w, warp - 18, bars, sSide, &abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -539,12 +597,12 @@ __global__ void __launch_bounds__(kPair) sink_weights_join_kernel(const __grid_c
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   if (c > 0 && c < ctas) {
-    const int64_t x = Walk::bound(p, c, ctas);
+    const int64_t x = Walk::bound(p, c);
     const Walk w(p, x, x + 1);
-    if (w.list < x && Walk::bound(p, c - 1, ctas) <= w.list) {
+    if (w.list < x && Walk::bound(p, c - 1) <= w.list) {
       const int64_t end = w.list + w.length(p);
       float sum = p.partial[((int64_t)(c - 1) * 2 + 1) * kPair + threadIdx.x];
-      for (int k = c; Walk::bound(p, k, ctas) < end; ++k) sum += p.partial[(int64_t)k * 2 * kPair + threadIdx.x];
+      for (int k = c; Walk::bound(p, k) < end; ++k) sum += p.partial[(int64_t)k * 2 * kPair + threadIdx.x];
       const int key = w.t * kPair + threadIdx.x;
       if (key < p.n) p.weights[(int64_t)w.sh * p.n + key] = sum;
     }
@@ -568,6 +626,8 @@ int launch(const WeightsArgs& a, WParams& p, cudaStream_t stream) {
   int64_t ctas = current_sm_count();
   if (ctas > kWeightsMaxCtas) ctas = kWeightsMaxCtas;
   if (ctas > p.total) ctas = p.total;
+  p.quota = p.total / ctas;
+  p.rest = (int)(p.total % ctas);
   kern<<<(unsigned)ctas, kThreads, C::SMEM, stream>>>(tq, tk, p);
   if (cudaGetLastError() != cudaSuccess) return SA_ERR_CUDA;
   // lists without a step: those whose window ends before the first query, but for the sinks'
@@ -607,8 +667,9 @@ static WParams params(const WeightsArgs& a) {
   p.sinks = a.sinks;
   p.first = a.first_query;
   p.skip = p.first_tile > p.reach ? (p.first_tile - p.reach + 1) / 2 : 0;
-  p.all = before(p, p.pairs);
+  p.all = before(p, p.pairs);        // small is 0 as yet
   p.total = p.all * p.group * a.kv_heads * a.batch;
+  p.small = p.total < INT32_MAX;
   p.lse = a.lse;
   p.weights = a.weights;
   p.partial = static_cast<float*>(a.workspace);
