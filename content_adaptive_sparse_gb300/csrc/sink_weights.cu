@@ -63,6 +63,9 @@ struct Cfg {
 struct WParams {
   int n, heads, kv_heads, group;
   int tiles, pairs;                 // query tiles, lists of a (sequence, key head)
+  // Query tile i is queries 128 i + shift .., -128 < shift <= 0, so that the first one begins with the first query (the
+  // last 64 queries of a prompt are half a tile, not two halves).
+  int shift;
   int first_tile, reach;            // the first query's tile; query tiles past 2 t that keys of list t reach
   int skip;                         // lists below it have no steps, but for the sinks'
   int small;                        // all steps are fewer than 2^31
@@ -246,7 +249,7 @@ __device__ void loader(const WParams& p, Walk w, const CUtensorMap* tq, const CU
       mbar_arrive_expect_tx(&bars.q_full[qb], C::TILE);
 #pragma unroll
       for (int c = 0; c < C::NCH; ++c)
-        tma_load_4d(sQ + qb * C::TILE + c * C::CHUNK, tq, &bars.q_full[qb], c * C::CH, hk * p.group + st.e, st.i * kTile, s);
+        tma_load_4d(sQ + qb * C::TILE + c * C::CHUNK, tq, &bars.q_full[qb], c * C::CH, hk * p.group + st.e, st.i * kTile + p.shift, s);
     }
   }
   // every copy of this CTA has landed before it may exit
@@ -268,7 +271,6 @@ __device__ void issuer(const WParams& p, Walk w, Bars& bars, uint8_t* sQ, uint8_
   using C = Cfg<D>;
   const uint64_t ones = make_smem_desc(smem_u32(sSide), 16, 512, kSwizzle64B);
   const uint64_t q0 = make_smem_desc(smem_u32(sQ), 16, C::ATOM, C::SWZ);
-  constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
   uint32_t g = 0;                    // step
   uint32_t r = 0, buf = 0, used = 0; // g % 3; of the next product: its buffer, and whether that was in use, with the phase
   bool ok = true;
@@ -278,7 +280,7 @@ __device__ void issuer(const WParams& p, Walk w, Bars& bars, uint8_t* sQ, uint8_
     for (int x = 0; x < 2; ++x) {
       const int k = 2 * w.t + x;
       i0[x] = k;
-      i1[x] = k * kTile < p.sinks ? p.tiles - 1 : (int)(((int64_t)k * kTile + kTile - 1 + p.window) / kTile);
+      i1[x] = k * kTile < p.sinks ? p.tiles - 1 : (int)(((int64_t)k * kTile + kTile - 1 + p.window - p.shift) / kTile);
       if (k * kTile >= p.n) i1[x] = -1;
       ok = ok && wait_bar(&bars.kt_full[x], (uint32_t)n & 1u, abort_flag);
     }
@@ -288,6 +290,8 @@ __device__ void issuer(const WParams& p, Walk w, Bars& bars, uint8_t* sQ, uint8_
       const uint32_t qb = g % kStages;
       if (!(ok = wait_bar(&bars.q_full[qb], g / kStages & 1u, abort_flag))) break;
       const uint64_t q = q0 + (uint64_t)(qb * (uint32_t)(C::TILE >> 4));
+      // the last tile may hold no more than half its queries
+      const uint32_t idesc = make_idesc_bf16(128, p.n - i * kTile - p.shift > kTile / 2 ? kTile : kTile / 2, 0, 0);
       const uint64_t side = ones + (uint64_t)((side_slot(g) + 32 * (g & 1)) >> 4);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -352,7 +356,7 @@ __device__ void lse_rows(const WParams& p, Walk w, int which, Bars& bars, uint8_
   const auto ask = [&](float (&v)[4]) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int q = i * kTile + 32 * x + lane;
+      const int q = i * kTile + p.shift + 32 * x + lane;
       v[x] = q < p.n ? row[q] : 0.f;
     }
     advance();
@@ -464,7 +468,7 @@ __device__ void sums(const WParams& p, Walk w, Bars& bars, const uint8_t* sK, fl
     const int i_end = w.i0 + w.count;
     for (int j = w.jb; j < w.je; ++j) {
       if (!done(&bars.s_full[x][r], turn)) return;
-      const int q = i * kTile + 64 * half;
+      const int q = i * kTile + p.shift + 64 * half;
       if (k0 < p.n && q + 63 >= any_lo && q <= any_hi) {
         tc_fence_after();
         const uint32_t at = ts + 128u * buf;
@@ -659,10 +663,11 @@ static WParams params(const WeightsArgs& a) {
   p.heads = a.heads;
   p.kv_heads = a.kv_heads;
   p.group = a.heads / a.kv_heads;
-  p.tiles = (a.n_tokens + kTile - 1) / kTile;
+  p.first_tile = (a.first_query + kTile - 1) / kTile;
+  p.shift = a.first_query - p.first_tile * kTile;
+  p.tiles = p.first_tile + (a.n_tokens - a.first_query + kTile - 1) / kTile;
   p.pairs = (a.n_tokens + kPair - 1) / kPair;
-  p.first_tile = a.first_query / kTile;
-  p.reach = (int)(((int64_t)a.window + kPair - 1) / kTile);
+  p.reach = (int)(((int64_t)a.window + kPair - 1 - p.shift) / kTile);
   p.window = a.window;
   p.sinks = a.sinks;
   p.first = a.first_query;
