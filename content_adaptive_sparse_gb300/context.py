@@ -54,6 +54,45 @@ def _bytes(size: int, like):
     return _s.torch.empty(size, dtype=_s.torch.uint8, device=like.device)
 
 
+# A decoding step is a few microseconds of GPU work, so what the checks of its tensors' shapes and strides come to
+# (sizes, stride arrays, workspace) is kept by these, in the `_plan` functions below; each call looks at types and
+# devices.
+
+def _layouts(**tensors) -> list:
+    """Stride arrays of bf16 rows given as name=(shape, strides), or the ValueError that names one of them."""
+    out = []
+    for name, (shape, strides) in tensors.items():
+        if len(shape) != 4:
+            raise ValueError(f"{name}: expected a bfloat16 [batch, tokens, heads, head_dim] tensor")
+        if strides[3] != 1:
+            raise ValueError(f"{name}: head_dim must be contiguous")
+        layout = _s._layout(strides, shape)
+        if type(layout) is str:
+            raise ValueError(f"{name}: {layout}")
+        out.append(layout)
+    return out
+
+
+def _blame(dev: int, **tensors):
+    """Raises for the tensor that is not bf16 rows on the current device."""
+    for name, t in tensors.items():
+        if t.dtype is not _s._BF16:
+            raise ValueError(f"{name}: expected a bfloat16 [batch, tokens, heads, head_dim] tensor")
+        if t.get_device() != dev:
+            _s._elsewhere(name)
+
+
+def _expect(name: str, shape, want):
+    if shape != want:
+        raise ValueError(f"{name}: expected shape {tuple(want)}, got {tuple(shape)}")
+
+
+def _cache_dims(name: str, shape):
+    if len(shape) != 4:
+        raise ValueError(f"{name}: expected a bfloat16 [batch, capacity, kv_heads, head_dim] tensor")
+    return shape
+
+
 # ------------------------------------------------------------------ attention behind a shared prefix
 
 def _prefix(k_prefix, v_prefix, kv_heads: int, d: int, dev: int):
@@ -76,7 +115,6 @@ def sa_prefix_attn_decode_workspace_size(batch: int, prefix_tokens: int, heads: 
 
 
 _fwd_bytes = functools.lru_cache(maxsize=64)(sa_prefix_attn_fwd_workspace_size)
-_decode_bytes = functools.lru_cache(maxsize=64)(sa_prefix_attn_decode_workspace_size)
 
 
 def sa_prefix_attn_fwd(q, k_prefix, v_prefix, k, v, window: int, o, lse, workspace, softmax_scale: float | None = None,
@@ -113,39 +151,59 @@ def prefix_attn_fwd(q, k_prefix, v_prefix, k, v, window: int, softmax_scale: flo
     return o, lse
 
 
-def _decode_inputs(q, k_cache, v_cache, lengths, dev):
-    if len(k_cache.shape) != 4:
-        raise ValueError("k_cache: expected a bfloat16 [batch, capacity, kv_heads, head_dim] tensor")
-    b, cap, hk, d = k_cache.shape
-    qs = _s._token(q, b, d, dev)
-    return (b, cap, q.shape[2], hk, d), qs, _rows("k_cache", k_cache, dev), \
-        _rows("v_cache", v_cache, dev, k_cache.shape), _flat("lengths", lengths, _s.torch.int32, (b,), dev)
+def _one_token(shape, b: int, d: int) -> int:
+    if len(shape) != 4 or shape[0] != b or shape[1] != 1 or shape[3] != d:
+        raise ValueError("q: expected one token per sequence, [batch, 1, heads, head_dim]")
+    return shape[2]
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_plan(q, q_st, kp, kp_st, vp, vp_st, k, k_st, v, v_st):
+    """Sizes, the inputs' strides, o's where it is allocated here, and the workspace's bytes."""
+    b, cap, hk, d = _cache_dims("k_cache", k)
+    h = _one_token(q, b, d)
+    _expect("v_cache", v, k)
+    if len(kp) != 4 or kp[0] != 1 or kp[2:] != (hk, d):
+        raise ValueError(f"k_prefix: expected a [1, prefix tokens, {hk}, {d}] tensor, got {tuple(kp)}")
+    _expect("v_prefix", vp, kp)
+    qs, ks, vs = _layouts(q=(q, q_st), k_cache=(k, k_st), v_cache=(v, v_st))
+    # (an empty tensor's strides may be anything)
+    kps, vps = _layouts(k_prefix=(kp, kp_st), v_prefix=(vp, vp_st)) if kp[1] else (_NO_ROWS, _NO_ROWS)
+    return (b, kp[1], cap, h, hk, d), (qs, kps, vps, ks, vs), _dense(q), \
+        sa_prefix_attn_decode_workspace_size(b, kp[1], h, hk, d), (b,), d ** -0.5
+
+
+def _decode_call(q, k_prefix, v_prefix, k_cache, v_cache, lengths, dev):
+    if not (q.dtype is k_prefix.dtype is v_prefix.dtype is k_cache.dtype is v_cache.dtype is _s._BF16 and
+            q.get_device() == k_prefix.get_device() == v_prefix.get_device() == k_cache.get_device() ==
+            v_cache.get_device() == dev):
+        _blame(dev, q=q, k_prefix=k_prefix, v_prefix=v_prefix, k_cache=k_cache, v_cache=v_cache)
+    plan = _decode_plan(q.shape, q.stride(), k_prefix.shape, k_prefix.stride(), v_prefix.shape, v_prefix.stride(),
+                        k_cache.shape, k_cache.stride(), v_cache.shape, v_cache.stride())
+    return plan, (q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()), \
+        _flat("lengths", lengths, _s.torch.int32, plan[4], dev)
 
 
 def sa_prefix_attn_decode(q, k_prefix, v_prefix, k_cache, v_cache, lengths, window: int, o, lse, workspace,
                           softmax_scale: float | None = None, stream=None) -> None:
     """``lengths``: int32 [batch] on the device, own tokens in each cache with the query's own key."""
     dev = _device()
-    (b, cap, h, hk, d), qs, ks, vs, n = _decode_inputs(q, k_cache, v_cache, lengths, dev)
-    pre, pre_strides, p = _prefix(k_prefix, v_prefix, hk, d, dev)
+    (sizes, strides, _, _, _, scale), inputs, n = _decode_call(q, k_prefix, v_prefix, k_cache, v_cache, lengths, dev)
     _check("sa_prefix_attn_decode", _lib().sa_prefix_attn_decode(
-        q.data_ptr(), *pre, k_cache.data_ptr(), v_cache.data_ptr(), qs, *pre_strides, ks, vs, _rows("o", o, dev, q.shape), b,
-        p, cap, h, hk, d, n, _int(window), _scale(softmax_scale, d), o.data_ptr(),
-        _flat("lse", lse, _s.torch.float32, (b, h, 1), dev), *_workspace(workspace, dev), _stream(stream, dev)))
+        *inputs, *strides, _rows("o", o, dev, q.shape), *sizes, n, _int(window),
+        scale if softmax_scale is None else float(softmax_scale), o.data_ptr(),
+        _flat("lse", lse, _s.torch.float32, (sizes[0], sizes[3], 1), dev), *_workspace(workspace, dev), _stream(stream, dev)))
 
 
 def prefix_attn_decode(q, k_prefix, v_prefix, k_cache, v_cache, lengths, window: int, softmax_scale: float | None = None):
     """One token per sequence behind a shared prefix; returns (o [batch, 1, heads, head_dim], lse)."""
     dev = _device()
-    (b, cap, h, hk, d), qs, ks, vs, n = _decode_inputs(q, k_cache, v_cache, lengths, dev)
-    pre, pre_strides, p = _prefix(k_prefix, v_prefix, hk, d, dev)
-    size = _decode_bytes(b, p, h, hk, d)
+    (sizes, strides, os, size, _, scale), inputs, n = _decode_call(q, k_prefix, v_prefix, k_cache, v_cache, lengths, dev)
     o, lse = _s._token_outputs(q)
     ws = _bytes(size, q)
     _check("sa_prefix_attn_decode", _lib().sa_prefix_attn_decode(
-        q.data_ptr(), *pre, k_cache.data_ptr(), v_cache.data_ptr(), qs, *pre_strides, ks, vs, _dense(q.shape), b, p, cap, h,
-        hk, d, n, _int(window), _scale(softmax_scale, d), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), size,
-        _stream(None, dev)))
+        *inputs, *strides, os, *sizes, n, _int(window), scale if softmax_scale is None else float(softmax_scale),
+        o.data_ptr(), lse.data_ptr(), ws.data_ptr(), size, _stream(None, dev)))
     return o, lse
 
 
@@ -168,13 +226,22 @@ def scored_alloc(batch: int, capacity: int, kv_heads: int, head_dim: int, device
                        torch.zeros((batch, kv_heads, capacity), dtype=torch.int32, device=device))
 
 
+@functools.lru_cache(maxsize=256)
+def _cache_plan(k, k_st, v, v_st):
+    """Sizes and strides of a cache's rows, and its weights' shape."""
+    b, cap, hk, d = _cache_dims("k", k)
+    _expect("v", v, k)
+    return (b, hk, d, cap), tuple(_layouts(k=(k, k_st), v=(v, v_st))), (b, hk, cap), (b,)
+
+
 def _scored(cache, dev):
-    """Sizes, strides and addresses of a cache."""
+    """Plan and addresses of a cache."""
     k, v, w, pos = cache
-    strides = _rows("k", k, dev), _rows("v", v, dev, k.shape)
-    b, cap, hk, d = k.shape
-    return (b, hk, d, cap), (k.data_ptr(), v.data_ptr()), strides, \
-        _flat("weights", w, _s.torch.float32, (b, hk, cap), dev), _flat("positions", pos, _s.torch.int32, (b, hk, cap), dev)
+    if not (k.dtype is v.dtype is _s._BF16 and k.get_device() == v.get_device() == dev):
+        _blame(dev, k=k, v=v)
+    plan = _cache_plan(k.shape, k.stride(), v.shape, v.stride())
+    return plan, (k.data_ptr(), v.data_ptr()), _flat("weights", w, _s.torch.float32, plan[2], dev), \
+        _flat("positions", pos, _s.torch.int32, plan[2], dev)
 
 
 def sa_scored_append(cache: ScoredCache, k, v, start=None, tokens=None, stream=None) -> None:
@@ -182,15 +249,15 @@ def sa_scored_append(cache: ScoredCache, k, v, start=None, tokens=None, stream=N
     (``start``, ``tokens``: int32 [batch] on the device; None: slot 0, and the slots' own numbers; a
     sequence with a negative start is left out)."""
     dev = _device()
-    (b, hk, d, cap), rows, strides, w, pos = _scored(cache, dev)
-    ks = _rows("k", k, dev)
-    n = k.shape[1]
-    if k.shape != (b, n, hk, d):
-        raise ValueError(f"k: expected rows of the cache's shape {(b, n, hk, d)}, got {tuple(k.shape)}")
+    ((b, hk, d, cap), strides, _, batch), rows, w, pos = _scored(cache, dev)
+    shape = k.shape
+    ks, vs = _rows("k", k, dev), _rows("v", v, dev, shape)
+    if shape[0] != b or shape[2] != hk or shape[3] != d:
+        raise ValueError(f"k: expected rows of the cache's shape {(b, shape[1], hk, d)}, got {tuple(shape)}")
     i32 = _s.torch.int32
     _check("sa_scored_append", _lib().sa_scored_append(
-        k.data_ptr(), v.data_ptr(), ks, _rows("v", v, dev, k.shape), b, n, hk, d, cap, _flat("start", start, i32, (b,), dev),
-        _flat("tokens", tokens, i32, (b,), dev), *rows, *strides, w, pos, _stream(stream, dev)))
+        k.data_ptr(), v.data_ptr(), ks, vs, b, shape[1], hk, d, cap, _flat("start", start, i32, batch, dev),
+        _flat("tokens", tokens, i32, batch, dev), *rows, *strides, w, pos, _stream(stream, dev)))
 
 
 def scored_append(cache: ScoredCache, k, v, start=None, tokens=None) -> None:
@@ -201,24 +268,34 @@ def sa_scored_attn_decode_workspace_size(batch: int, capacity: int, heads: int, 
     return _size_of("sa_scored_attn_decode_workspace_size", batch, capacity, heads, kv_heads)
 
 
-_scored_bytes = functools.lru_cache(maxsize=64)(sa_scored_attn_decode_workspace_size)
+@functools.lru_cache(maxsize=256)
+def _scored_plan(q, q_st, k, k_st, v, v_st):
+    b, cap, hk, d = _cache_dims("k", k)
+    h = _one_token(q, b, d)
+    _expect("v", v, k)
+    return (b, cap, h, hk, d), tuple(_layouts(q=(q, q_st), k=(k, k_st), v=(v, v_st))), _dense(q), \
+        sa_scored_attn_decode_workspace_size(b, cap, h, hk), (b,), (b, hk, cap), d ** -0.5
 
 
-def _scored_decode(q, cache, lengths, decay, weights_out, dev):
-    (b, cap, h, hk, d), qs, ks, vs, n = _decode_inputs(q, cache[0], cache[1], lengths, dev)
-    f32, shape = _s.torch.float32, (b, hk, cap)
-    w = _flat("weights", cache[2], f32, shape, dev)
-    to = w if weights_out is None else _flat("weights_out", weights_out, f32, shape, dev)
-    return (b, cap, h, hk, d), (q.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(), qs, ks, vs), (n, float(decay), w, to)
+def _scored_call(q, cache, lengths, weights_out, dev):
+    k, v, w, _ = cache
+    if not (q.dtype is k.dtype is v.dtype is _s._BF16 and q.get_device() == k.get_device() == v.get_device() == dev):
+        _blame(dev, q=q, k=k, v=v)
+    plan = _scored_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride())
+    f32 = _s.torch.float32
+    at = _flat("weights", w, f32, plan[5], dev)
+    return plan, (q.data_ptr(), k.data_ptr(), v.data_ptr()), _flat("lengths", lengths, _s.torch.int32, plan[4], dev), \
+        (at, at if weights_out is None else _flat("weights_out", weights_out, f32, plan[5], dev))
 
 
 def sa_scored_attn_decode(q, cache: ScoredCache, lengths, o, lse, workspace, decay: float = 1.0, weights_out=None,
                           softmax_scale: float | None = None, stream=None) -> None:
     dev = _device()
-    (b, cap, h, hk, d), inputs, (n, decay, w, to) = _scored_decode(q, cache, lengths, decay, weights_out, dev)
+    (sizes, strides, _, _, _, _, scale), inputs, n, weights = _scored_call(q, cache, lengths, weights_out, dev)
     _check("sa_scored_attn_decode", _lib().sa_scored_attn_decode(
-        *inputs, _rows("o", o, dev, q.shape), b, cap, h, hk, d, n, _scale(softmax_scale, d), decay, w, to, o.data_ptr(),
-        _flat("lse", lse, _s.torch.float32, (b, h, 1), dev), *_workspace(workspace, dev), _stream(stream, dev)))
+        *inputs, *strides, _rows("o", o, dev, q.shape), *sizes, n, scale if softmax_scale is None else float(softmax_scale),
+        float(decay), *weights, o.data_ptr(), _flat("lse", lse, _s.torch.float32, (sizes[0], sizes[2], 1), dev),
+        *_workspace(workspace, dev), _stream(stream, dev)))
 
 
 def scored_attn_decode(q, cache: ScoredCache, lengths, decay: float = 1.0, weights_out=None,
@@ -227,26 +304,24 @@ def scored_attn_decode(q, cache: ScoredCache, lengths, decay: float = 1.0, weigh
     Every slot's weight becomes decay * weight + the sum of its probabilities over the query heads of its key
     head, in place or in ``weights_out``."""
     dev = _device()
-    (b, cap, h, hk, d), inputs, (n, decay, w, to) = _scored_decode(q, cache, lengths, decay, weights_out, dev)
-    size = _scored_bytes(b, cap, h, hk)
+    (sizes, strides, os, size, _, _, scale), inputs, n, weights = _scored_call(q, cache, lengths, weights_out, dev)
     o, lse = _s._token_outputs(q)
     ws = _bytes(size, q)
     _check("sa_scored_attn_decode", _lib().sa_scored_attn_decode(
-        *inputs, _dense(q.shape), b, cap, h, hk, d, n, _scale(softmax_scale, d), decay, w, to, o.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), size, _stream(None, dev)))
+        *inputs, *strides, os, *sizes, n, scale if softmax_scale is None else float(softmax_scale), float(decay), *weights,
+        o.data_ptr(), lse.data_ptr(), ws.data_ptr(), size, _stream(None, dev)))
     return o, lse
 
 
 def sa_scored_evict(cache: ScoredCache, lengths, keep: int, sinks: int, recent: int, weights_out, positions_out, lengths_out,
                     stream=None) -> None:
     dev = _device()
-    (b, hk, d, cap), rows, strides, w, pos = _scored(cache, dev)
+    ((b, hk, d, cap), strides, shape, batch), rows, w, pos = _scored(cache, dev)
     i32 = _s.torch.int32
     _check("sa_scored_evict", _lib().sa_scored_evict(
-        *rows, *strides, b, hk, d, cap, _int(keep), _int(sinks), _int(recent), w, pos, _flat("lengths", lengths, i32, (b,), dev),
-        _flat("weights_out", weights_out, _s.torch.float32, (b, hk, cap), dev),
-        _flat("positions_out", positions_out, i32, (b, hk, cap), dev), _flat("lengths_out", lengths_out, i32, (b,), dev),
-        _stream(stream, dev)))
+        *rows, *strides, b, hk, d, cap, _int(keep), _int(sinks), _int(recent), w, pos, _flat("lengths", lengths, i32, batch, dev),
+        _flat("weights_out", weights_out, _s.torch.float32, shape, dev), _flat("positions_out", positions_out, i32, shape, dev),
+        _flat("lengths_out", lengths_out, i32, batch, dev), _stream(stream, dev)))
 
 
 def scored_evict(cache: ScoredCache, lengths, keep: int, sinks: int, recent: int, weights_out=None, positions_out=None,

@@ -1466,6 +1466,7 @@ int sa_sink_attn_weights(const void* q, const void* k, const float* lse, const i
   int st = check_sink(batch, n_tokens, heads, kv_heads, head_dim, window, sinks);
   if (st != SA_OK) return st;
   if (first_query < 0 || first_query >= n_tokens) return SA_ERR_INVALID_ARG;
+  if (softmax_scale < 0x1p-100f) return SA_ERR_UNSUPPORTED;               // LSE is divided by it
   if (!aligned16(q) || !aligned16(k) || !strides_ok(q_strides) || !strides_ok(k_strides)) return SA_ERR_UNSUPPORTED;
   if ((st = check_workspace(workspace, workspace_bytes, sa::kWeightsWorkspace)) != SA_OK) return st;
   if (!device_ok()) return SA_ERR_CUDA;

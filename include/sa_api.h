@@ -569,7 +569,7 @@ int sa_scored_evict(void* k_cache, void* v_cache, const int64_t k_strides[3], co
  * sink-window graph, from the inputs and the LSE of sa_sink_attn_fwd (LSE of earlier queries is not used).
  *   d_weights : fp32 [batch][kv_heads][n_tokens], all written; the same bits on every run on one GPU.
  *   workspace : device memory, 256-byte aligned, of sa_sink_attn_weights_workspace_size bytes.
- * Limits as in sa_sink_attn_fwd. */
+ * Limits as in sa_sink_attn_fwd, and softmax_scale from 2^-100 on. */
 int sa_sink_attn_weights_workspace_size(size_t* h_bytes);
 int sa_sink_attn_weights(const void* q, const void* k, const float* lse, const int64_t q_strides[3],
                          const int64_t k_strides[3], int32_t batch, int32_t n_tokens, int32_t heads, int32_t kv_heads,
