@@ -45,12 +45,11 @@ struct Layout {
   int pre_tiles;                    // 128-key tiles of the prefix
   int tiles0, parts0, items0;       // class 0: row tiles of a key head, parts of their lists, items in all
   int tiles1, parts1, items1;       // class 1: row tiles of a sequence and key head, ...
-  int slots;                        // partial results of a row; 0: the items write O and LSE
-  // Item of part k of the list of row r of all sequences (class 0), or of row r of sequence s (class 1), of key head
-  // hk; the row's place in it is r % 128.
-  __host__ __device__ int item0(int hk, int r, int k) const { return (hk * tiles0 + r / kTile) * parts0 + k; }
-  __host__ __device__ int item1(int hk, int s, int r, int k) const {
-    return items0 + ((hk * batch + s) * tiles1 + r / kTile) * parts1 + k;
+  int row_tiles, slots;             // tiles of `rows`; partial results of a row (0: the items write O and LSE)
+  // Partial results lie in blocks of 128 rows of all sequences, `slots` blocks one behind the other: where the
+  // first of row r of key head hk has its m and l; the next is 128 places on.
+  __host__ __device__ int64_t place(int hk, int r) const {
+    return (int64_t)(hk * row_tiles + r / kTile) * slots * kTile + r % kTile;
   }
 };
 
@@ -59,8 +58,8 @@ struct PParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;                       // [batch][heads][n]
-  // Partial results by item, row tiles as the threads hold them: O [item][D / 4][128] of four columns each, m (log2
-  // units) and l [item][128]. A warp's 32 rows are neighbours: written row by row they took 2 us.
+  // O [block][D / 4][128] of four columns each, m (log2 units) and l [block][128]. A warp's 32 rows are neighbours:
+  // written row by row they took 2 us.
   float4* part_o;
   float2* part_ml;
   int64_t q_sb, q_sn, q_sh, o_sb, o_sn, o_sh;
@@ -74,6 +73,7 @@ struct Item {
   bool common;                      // class 0
   int s, hk, row0, rows;            // rows row0 .. row0 + rows - 1 of all sequences' (class 0) or of s's
   int pre, begin, steps, own;       // prefix tiles of the whole list; this part of it; first own tile
+  int slot;
   __device__ explicit Item(const PParams& p) : Item(p, (int)blockIdx.x) {}
   __host__ __device__ Item(const PParams& p, int first) : at(first) { set(p); }
   __device__ __forceinline__ bool more() const { return on; }
@@ -109,6 +109,7 @@ struct Item {
     }
     begin = (int)((int64_t)all * part / parts);
     steps = (int)((int64_t)all * (part + 1) / parts) - begin;
+    slot = common || l.items0 == 0 ? part : l.parts0;
   }
   __host__ __device__ bool is_prefix(int j) const { return begin + j < pre; }
   __host__ __device__ int key_tile(int j) const { return begin + j < pre ? begin + j : own + begin + j - pre; }
@@ -288,6 +289,7 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
     const float L = l0 * f0 + l1 * f1;
     const bool on = row < it.rows;
     const int r = it.row(p, on ? row : 0);
+    const int64_t at = p.l.place(it.hk, r) + (int64_t)it.slot * kTile;
     __nv_bfloat16* o = nullptr;
     if (p.l.slots == 0) {
       const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -297,13 +299,13 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
       o = p.o + s * p.o_sb + t * p.o_sn + (int64_t)h * p.o_sh;
       if (on)
         p.lse[((int64_t)s * p.l.heads + h) * p.l.n + t] = L == 0.f ? kNegInf : (m + __log2f(L)) * 0.69314718055994531f;
-    } else {
-      p.part_ml[(int64_t)it.at * kTile + row] = make_float2(m, L);
+    } else if (on) {
+      p.part_ml[at] = make_float2(m, L);
     }
     if (!__all_sync(0xffffffffu, wait_bar(&bars.o_full, (uint32_t)n & 1u, abort_flag))) return;
     tc_fence_after();
     const uint32_t t0 = base + C::COL_O, t1 = t0 + D;
-    float4* part = p.part_o + (int64_t)it.at * (D / 4) * kTile + row;
+    float4* part = p.part_o + at / kTile * (D / 4) * kTile + at % kTile;
 #pragma unroll 1
     for (int c = 0; c < D; c += 16) {
       uint32_t a[16], b[16];
@@ -314,7 +316,7 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(a[j]) * f0 + __uint_as_float(b[j]) * f1;
-      if (!on) continue;                               // (the places of rows past the last one are not read)
+      if (!on) continue;
       if (p.l.slots == 0) {
 #pragma unroll
         for (int j = 0; j < 16; j += 8)
@@ -424,31 +426,24 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hk = blockIdx.y;
   const int r = min((int)blockIdx.x * 32 + lane, p.l.rows - 1);
   const int tok = r / p.l.group, h = hk * p.l.group + r - tok * p.l.group, s = tok / p.l.n, t = tok - s * p.l.n;
-  const int seq_row = r - s * p.l.seq_rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // part k: of class 0 first, then of class 1
-  const auto place_of = [&](int k) {
-    const bool common = p.l.items0 > 0 && k < p.l.parts0;
-    const int item = common ? p.l.item0(hk, r, k) : p.l.item1(hk, s, seq_row, p.l.items0 > 0 ? k - p.l.parts0 : k);
-    return (int64_t)item * kTile + (common ? r : seq_row) % kTile;
-  };
+  const float2* ml = p.part_ml + p.l.place(hk, r);
+  const float4* part = p.part_o + (p.l.place(hk, r) / kTile * (D / 4)) * kTile + r % kTile;
   const int parts = p.l.slots;
   float M = kNegInf, L = 0.f;
 #pragma unroll 8
-  for (int k = 0; k < parts; ++k) M = fmaxf(M, p.part_ml[place_of(k)].x);
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, ml[k * kTile].x);
   float4 v[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int k = 0; k < parts; ++k) {
-    const int64_t at = place_of(k);
-    const float2 ml = p.part_ml[at];
-    const float a = M != kNegInf ? ex2_approx(ml.x - M) : 1.f;     // without a maximum the sums are zero, or NaN
-    L = fmaf(a, ml.y, L);
-    const float4* part = p.part_o + at / kTile * (D / 4) * kTile + at % kTile;
+    const float2 e = ml[k * kTile];
+    const float a = M != kNegInf ? ex2_approx(e.x - M) : 1.f;      // without a maximum the sums are zero, or NaN
+    L = fmaf(a, e.y, L);
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {
-      const float4 x = part[(warp + kWarps * c) * kTile];
+      const float4 x = part[((int64_t)k * (D / 4) + warp + kWarps * c) * kTile];
       v[c].x = fmaf(a, x.x, v[c].x);
       v[c].y = fmaf(a, x.y, v[c].y);
       v[c].z = fmaf(a, x.z, v[c].z);
@@ -510,7 +505,7 @@ Layout plan(int batch, int n, int prefix, int heads, int kv_heads, int window, b
   l.seq_rows = n * l.group;
   l.rows = batch * l.seq_rows;
   l.pre_tiles = ceil_div(prefix, kTile);
-  const int joint_tiles = ceil_div(l.rows, kTile), seq_tiles = ceil_div(l.seq_rows, kTile);
+  const int joint_tiles = l.row_tiles = ceil_div(l.rows, kTile), seq_tiles = ceil_div(l.seq_rows, kTile);
   const int64_t joint_lists = (int64_t)joint_tiles * kv_heads, seq_lists = (int64_t)batch * seq_tiles * kv_heads;
   // own tiles of a row tile, on average
   const double span = window + (double)kTile / l.group;
@@ -541,7 +536,7 @@ Layout plan(int batch, int n, int prefix, int heads, int kv_heads, int window, b
   return l;
 }
 
-size_t partial_rows(const Layout& l) { return l.slots > 0 ? (size_t)(l.items0 + l.items1) * kTile : 0; }
+size_t partial_rows(const Layout& l) { return (size_t)l.kv_heads * l.row_tiles * l.slots * kTile; }
 
 template <int D>
 int launch_d(const PrefixArgs& a, const Layout& l, cudaStream_t stream) {
@@ -604,8 +599,8 @@ PrefixWorkspace prefix_workspace(int batch, int n_tokens, int prefix, int heads,
                                  bool decode) {
   const Layout l = plan(batch, n_tokens, prefix, heads, kv_heads, window, decode);
   PrefixWorkspace w;
-  w.parts = l.parts0;
-  w.tiles = l.tiles0;
+  w.parts = l.slots;
+  w.tiles = l.row_tiles;
   w.part_o_off = partial_rows(l) * sizeof(float2);
   w.bytes = w.part_o_off + partial_rows(l) * head_dim * sizeof(float);
   if (w.bytes < 256) w.bytes = 256;

@@ -947,6 +947,7 @@ int check_prefix(int32_t batch, int32_t n_tokens, int32_t prefix, int32_t heads,
   const int64_t tiles = ((int64_t)n_tokens * (heads / kv_heads) + 127) / 128;
   if ((int64_t)batch * heads > (1 << 24) || (int64_t)batch * kv_heads * tiles > (1 << 24) || kv_heads > 65535)
     return SA_ERR_UNSUPPORTED;
+  if ((int64_t)batch * n_tokens * (heads / kv_heads) >= (int64_t)1 << 31) return SA_ERR_UNSUPPORTED;
   if (window > n_tokens - 1) window = n_tokens - 1;
   return SA_OK;
 }

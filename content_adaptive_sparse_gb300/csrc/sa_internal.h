@@ -241,7 +241,7 @@ struct PrefixArgs {
   void* workspace;
 };
 // Workspace: maxima and sums of the partial results, then their O. Decoding: `parts` partial results of every row
-// s * group + e of a key head, in items (hk * tiles + row / 128) * parts + part (prefix_attn.cu has their layout).
+// s * group + e of a key head, in blocks (hk * tiles + row / 128) * parts + part (prefix_attn.cu has their layout).
 struct PrefixWorkspace {
   int parts, tiles;
   size_t part_o_off, bytes;

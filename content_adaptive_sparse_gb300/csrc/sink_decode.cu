@@ -107,10 +107,10 @@ struct DParams {
   // 0x000f000f, not known to the compiler: (w & mask) | bits is one instruction, but only with one constant
   // in it (4 bits: 220 -> 158 ALU instructions per 16 rows, 86 -> 77 us)
   uint32_t code_mask;
-  // kBehindPrefix: n_parts partial results of row s group + e of a key head, in items (hk part_tiles + row / 128)
+  // kBehindPrefix: n_parts partial results of row s group + e of a key head, in blocks (hk part_tiles + row / 128)
   // n_parts + part
-  const float4* part_o;             // [item][D / 4][128]
-  const float2* part_ml;            // [item][128]: m (log2 units), l
+  const float4* part_o;             // [block][D / 4][128]
+  const float2* part_ml;            // [block][128]: m (log2 units), l
   int n_parts, part_tiles;
   // kScored
   float* scores;                    // [batch][kv_heads][head_groups][capacity][score_stride], log2 units
@@ -616,7 +616,7 @@ __device__ __forceinline__ void join_prefix(const DParams& p, cooperative_groups
   __shared__ float fm[kQ][kMaxCluster + kFactors];         // maxima, then factors: the ranks', then the parts'
   __shared__ float fl[kQ][kMaxCluster + kFactors];
   __shared__ float top[kQ], sum[kQ];
-  const auto item_of = [&](int q, int k) {                 // and the row's place in it
+  const auto block_of = [&](int q, int k) {                 // and the row's place in it
     const int row = s * p.group + hg * kQ + q;
     return make_int2((hk * p.part_tiles + row / 128) * p.n_parts + k, row % 128);
   };
@@ -642,7 +642,7 @@ __device__ __forceinline__ void join_prefix(const DParams& p, cooperative_groups
         fm[q][k] = *cluster.map_shared_rank(cm + q, k);
         fl[q][k] = *cluster.map_shared_rank(cl + q, k);
       } else {
-        const int2 at = item_of(q, k0 + k - own);
+        const int2 at = block_of(q, k0 + k - own);
         const float2 ml = p.part_ml[(int64_t)at.x * 128 + at.y];
         fm[q][k] = ml.x;
         fl[q][k] = ml.y;
@@ -694,7 +694,7 @@ __device__ __forceinline__ void join_prefix(const DParams& p, cooperative_groups
       };
       for (int k = 0; k < own; ++k)
         add(fm[q][k], *reinterpret_cast<const float4*>(cluster.map_shared_rank(wo + q * D + col, k)));
-      const int2 it = item_of(q, k0);
+      const int2 it = block_of(q, k0);
       const float4* at = p.part_o + ((int64_t)it.x * (D / 4) + col / 4) * 128 + it.y;
 #pragma unroll 8
       for (int k = 0; k < n; ++k) add(fm[q][own + k], at[(int64_t)k * (D / 4) * 128]);

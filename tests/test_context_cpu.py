@@ -119,13 +119,13 @@ def test_prefix_refusals(lib, decode):  # noqa: F811
 
 
 def test_prefix_workspace_sizes(lib):  # noqa: F811
-    """Nothing but a small block where the items write the result; else 128 rows of D + 2 floats for every item."""
+    """Nothing but a small block where the items write the result; else D + 2 floats for every row and part."""
     assert sa.sa_prefix_attn_fwd_workspace_size(4, 8192, 0, 16, 4, 128, 4095) == 256
     assert sa.sa_prefix_attn_fwd_workspace_size(1, 8192, 57344, 16, 4, 128, 4095) == 256
     assert sa.sa_prefix_attn_decode_workspace_size(64, 32768, 16, 4, 128) == 152 * 128 * (128 + 2) * 4
     assert sa.sa_prefix_attn_decode_workspace_size(64, 0, 16, 4, 128) == 256
     joint = sa.sa_prefix_attn_fwd_workspace_size(32, 37, 16384, 16, 4, 128, 36)
-    assert joint == (4 * 37 + 32 * 4 * 2) * 128 * (128 + 2) * 4
+    assert joint == 4 * 37 * 2 * 128 * (128 + 2) * 4
     for bad in ((0, 8, 8, 4, 2, 64, 3), (1, 0, 8, 4, 2, 64, 3), (1, 8, -1, 4, 2, 64, 3), (1, 8, 8, 3, 2, 64, 3), (1, 8, 8, 4, 2, 80, 3),
                 (1, 8, 8, 4, 2, 64, -1)):
         with pytest.raises(sa.SAError):
