@@ -27,7 +27,8 @@
 // is a kernel of its own (it may count the tokens itself).
 //
 // Measured, 4 x 8192 tokens, 12 + 12 heads of 64: forward 35.2 us (201 MB: 5.7 TB/s), backward with
-// the weights' gradients 55.9 us (302 MB: 5.4 TB/s), 0.84 and 0.80 of a plain copy's rate.
+// the weights' gradients 55.9 us (302 MB: 5.4 TB/s), 0.84 and 0.80 of a plain copy's rate; both directions
+// with three axes 95 us where one axis takes 91 to 99.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

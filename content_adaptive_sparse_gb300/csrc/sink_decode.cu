@@ -33,6 +33,10 @@
 // 46.5 M instructions, mostly to unpack codes (372 per 16 rows), that would take some 40 us at full issue;
 // the issue slots are 59 % busy, since the CTAs are unequal and come in 1.7 waves, each with its fill and
 // join. One sequence of 700 tokens, 12 heads of 64, window 511: 4.4 us, a launch, one load and the join.
+// With weights, 64 sequences of 2049 to 4096 slots, 16 / 4 heads of 128: 77 us, 5.3 TB/s; the CTAs of long sequences
+// outlast the others by some 10 us (a CTA's four warps take 64 rows in about half a microsecond, whatever the
+// memory could give), and their weights come after that, 4 us. Behind a prefix, 64 sequences of up to 1000 own tokens: 20 us of
+// that call's 42, the same end and the join of 19 parts.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -5,12 +5,22 @@
 // exchange. LSE belongs to the queries, the columns: it goes into the product as one more step of it, -LSE / scale in
 // three bf16 parts (24 bits) against ones, so that a thread only multiplies and takes 2^x. (Read from shared memory
 // instead, where 32 lanes get the same four bytes a cycle, it cost as much of its bandwidth as the products' operands
-// do: 259 us for two prompts of 8192 tokens where this takes NNN.) A list is 256 keys (two tiles: every tile of
+// do: 259 us for two prompts of 8192 tokens, 205 so.) A list is 256 keys (two tiles: every tile of
 // queries that comes through shared memory then serves twice, 4.7 instead of 9.4 TB/s from L2 at full
 // rate) of one (sequence, key head); its steps are the query tiles that see any of them, for every query head.
 // Lists are of unequal length (causal, windows, the sinks' keys), so all steps are laid end to end and cut
 // evenly between the CTAs; a list that is cut leaves sums in the workspace (at most two per CTA), which a second launch
 // adds in their order: the same bits on every run. Where a list begins on that line has a closed form (before()).
+//
+// Products: the keys are the A operand in TMEM, copied there by the summing warps once a list, so that shared memory is
+// read for the queries alone (with both operands in it, its bandwidth bound the products: 205 -> 188 us). Three
+// buffers of S^T take turns.
+//
+// Measured: two prompts of 8192 tokens, 16 heads of 128 over 4 key heads, all queries: 190 us, 1.46 PFLOP/s
+// (277 GFLOP of visible scores),
+// the tensor pipe 72 % busy, the exponentials' 64 %; a step's two products, its sums and the hand-overs between them
+// are each near its 1600 cycles. The last 64 queries of 32768: 19 us for 34 MB of keys: 4 us until the first
+// scores, 13.5 steps a CTA with a new list every fourth, and the joining launch.
 //
 // Sums: 64 queries a step in four fp32 sums, and the steps' totals with their rounding errors carried along
 // (two-term sums), since a key of a long prompt gathers from some 10^5 queries.

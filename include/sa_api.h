@@ -464,8 +464,8 @@ int sa_cache4_append(const void* k, const void* v, const int64_t k_strides[3], c
                      void* stream);
 
 /* The rows d_start[s] .. d_start[s] + n_tokens - 1 of the cache as bf16 (code * scale, rounded once) into
- * k and v. (sa_sink_attn_fwd takes as many keys as queries: a later chunk of a prompt attends to these
- * rows only in a call over the whole prompt.) Rows of a left-out sequence and rows at or past the
+ * k and v. (sa_sink_attn_fwd takes as many keys as queries; a later chunk of a prompt attends to these
+ * rows as the prefix of sa_prefix_attn_fwd.) Rows of a left-out sequence and rows at or past the
  * capacity (reported as by sa_cache4_append) come back as zeros. */
 int sa_cache4_read(const uint8_t* k_codes, const void* k_scales, const uint8_t* v_codes, const void* v_scales,
                    int32_t batch, int32_t n_tokens, int32_t kv_heads, int32_t head_dim, int32_t capacity,
