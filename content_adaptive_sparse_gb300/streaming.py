@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple
 
 import numpy as np
@@ -190,10 +191,9 @@ def _like(t):
 @functools.lru_cache(maxsize=64)
 def _axes(pair_axes: tuple):
     """A host array of the pairs' axes (kept by the caller, as `_frequencies`)."""
-    axes = [int(a) for a in pair_axes]
-    if any(not -_MAX <= a <= _MAX for a in axes):
+    if any(not -_MAX <= a <= _MAX for a in pair_axes):
         raise ValueError("pair_axes: expected axes of the positions")
-    return (ctypes.c_int32 * len(axes))(*axes) if axes else None
+    return (ctypes.c_int32 * len(pair_axes))(*pair_axes) if pair_axes else None
 
 
 def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, dev, pair_axes=None):
@@ -209,7 +209,10 @@ def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, 
     if pair_axes is None:
         places = (_flat("positions", positions, torch.int32, (b, n), dev),)
     else:
-        axes = tuple(pair_axes)
+        try:
+            axes = tuple(map(operator.index, pair_axes))
+        except TypeError:
+            raise ValueError("pair_axes: expected a sequence of whole numbers") from None
         if len(axes) != inv_freq.size:
             raise ValueError("pair_axes: expected one axis per frequency")
         if positions is None or len(positions.shape) != 3:

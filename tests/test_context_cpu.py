@@ -1,6 +1,7 @@
 """Shared contexts and bounded caches without a GPU: refusals of the C entry points and of the binding,
 and pins of the float64 oracles."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -55,6 +56,19 @@ def test_axes_binding_refuses(monkeypatch):
             sa.qk_norm_rope_axes_fwd(q, q, None, None, freq, pair, p)
         with pytest.raises(ValueError, match=what):
             sa.qk_norm_rope_axes_bwd(q, q, q, q, None, None, freq, pair, p)
+
+
+@pytest.mark.parametrize("pair", [[0.5] * 16, [1.0] * 16, [None] * 16, ["0"] * 16])
+def test_axes_binding_takes_whole_numbers(monkeypatch, pair):
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(1, 4, 3, dtype=torch.int32)
+    monkeypatch.setattr(sa.streaming, "_device", lambda: (sa.streaming._bind() if sa.streaming.torch is None else None, -1)[1])
+    with pytest.raises(sa.SAError):                       # the library's own answer, without a device
+        sa.sa_qk_norm_rope_axes_fwd(q, q, None, None, [0.5] * 16, np.ones(16, np.int64), pos, q, q,
+                                    stream=types.SimpleNamespace(cuda_stream=0))
+    with pytest.raises(ValueError, match="pair_axes"):
+        sa.qk_norm_rope_axes_fwd(q, q, None, None, [0.5] * 16, pair, pos)
 
 
 @pytest.mark.parametrize("inter", [False, True])
