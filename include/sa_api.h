@@ -493,7 +493,9 @@ int sa_sink_attn_decode_cache4(const void* q, const uint8_t* k_codes, const void
  * sa_prefix_attn_fwd: n_tokens own tokens of every sequence, 1 .. 2^24, whose keys and values k, v are
  * [batch, n_tokens, kv_heads, head_dim]. (With one sequence it is the later part of a prompt, over the rows
  * that its first part left.) SA_ERR_UNSUPPORTED past 2^24 query heads of all sequences, 2^24 tiles of 128
- * queries of a key head, or 2^31 queries of one key head. */
+ * queries of a key head, or 2^31 queries of one key head. As there, rows are expected to be finite: a value that is not
+ * reaches the queries whose tile meets it, in its own sequence alone where it is not the prefix's. (sa_prefix_attn_decode
+ * ignores whatever stands in the cache rows that its query does not see.) */
 int sa_prefix_attn_fwd_workspace_size(int32_t batch, int32_t n_tokens, int32_t prefix_tokens, int32_t heads,
                                       int32_t kv_heads, int32_t head_dim, int32_t window, size_t* h_bytes);
 int sa_prefix_attn_fwd(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
