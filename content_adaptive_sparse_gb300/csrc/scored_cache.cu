@@ -23,6 +23,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "key_range.h"
 #include "sa_internal.h"
 
 namespace sa {
@@ -155,7 +156,7 @@ template <int D, bool SMALL>
 __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) evict_kernel(const __grid_constant__ EvictParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) int hist[2048];
+  __shared__ __align__(16) int hist[KeyRange::kBins];
   __shared__ int warp_sums[kWarps];
   __shared__ uint32_t warp_low[kWarps], warp_high[kWarps];
   __shared__ int found[3];
@@ -301,17 +302,17 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) evict_kernel(const __
   if (equal < keep) {
     left = keep - equal;
     equal = len - equal;
+    KeyRange range{low, high};
     T = low;
 #pragma unroll 1
-    while (left < equal && low < high) {
-      const int shift = max(0, 21 - __clz(high - low));    // (high - low) >> shift < 2048
-      const uint32_t width = high - low;
+    while (left < equal && range.low < range.high) {
+      const int shift = range.shift();
       for_slots([&](int, uint32_t k, bool on) {
-        if (on && k - low <= width) atomicAdd(&hist[(k - low) >> shift], 1);
+        if (on && range.holds(k)) atomicAdd(&hist[range.bin(k, shift)], 1);
       });
       __syncthreads();
       // thread t: four bins from the 4 t-th from the top on
-      const int b0 = 2048 - 4 - 4 * (int)threadIdx.x;
+      const int b0 = KeyRange::kBins - 4 - 4 * (int)threadIdx.x;
       const int4 n = *reinterpret_cast<const int4*>(hist + b0);
       *reinterpret_cast<int4*>(hist + b0) = make_int4(0, 0, 0, 0);        // for the next round
       const int count[4] = {n.w, n.z, n.y, n.x};
@@ -326,11 +327,10 @@ __global__ void __launch_bounds__(kThreads, SMALL ? 2 : 1) evict_kernel(const __
         above += count[k];
       }
       __syncthreads();
-      low += (uint32_t)found[0] << shift;
-      high = min(high, low + ((1u << shift) - 1u));
+      range.take((uint32_t)found[0], shift);
       left -= found[1];
       equal = found[2];
-      T = low;
+      T = range.low;
     }
   }
   // ---- which slots stay. Of the keys equal to T the first `left`: their number before each word of 32 slots

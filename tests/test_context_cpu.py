@@ -1,6 +1,9 @@
 """Shared contexts and bounded caches without a GPU: refusals of the C entry points and of the binding,
 and pins of the float64 oracles."""
 import ctypes
+import os
+import shutil
+import subprocess
 import types
 
 import numpy as np
@@ -338,3 +341,18 @@ def test_eviction_oracle():
     assert oc.evict(k, k, w, pos, [6], 2, 0, 0)[3][0, 0, :2].tolist() == [0, 11]
     # a list that is short enough stays
     assert oc.evict(k, k, w, pos, [3], 4, 0, 1)[4] == [3]
+
+
+# ------------------------------------------------------------------ the selection of an eviction
+
+def test_the_border_of_an_eviction_is_found(tmp_path):
+    """key_range.h, as the kernel uses it, over random keys, many of them the largest (NaN), against sorted keys."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = tmp_path / "key_range"
+    subprocess.run([cxx, "-std=c++17", "-O1", "-I", os.path.join(os.path.dirname(here), "content_adaptive_sparse_gb300", "csrc"),
+                    os.path.join(here, "c", "key_range.cpp"), "-o", str(exe)], check=True, capture_output=True, text=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0, out.stdout

@@ -275,6 +275,40 @@ def test_evict_of_weights_that_are_not_numbers():
         check_evict(k, v, w, pos, [300, 299], keep, 0, 0)
 
 
+@pytest.mark.parametrize("cap,keep", [(40, 10), (300, 200), (1000, 480), (8192, 4096), (8193, 4000), (33000, 20000)])
+@pytest.mark.parametrize("low", [0.1234, 0.7, 3e-39])
+def test_evict_of_more_nan_than_there_is_room_for(cap, keep, low):
+    """NaN beside ordinary positive weights: the lowest slots among the NaN stay. Lists of every form."""
+    torch = torch_cuda()
+    k, v, w, pos = evict_inputs(2, cap, 1, 32)
+    w.clamp_(min=low)
+    assert (w > 0).all()
+    w[0, :, torch.randperm(cap, generator=torch.Generator().manual_seed(1))[:(cap + keep) // 2].cuda()] = float("nan")
+    w[1, :, cap // 8:] = float("nan")
+    check_evict(k, v, w, pos, [cap, cap - 1], keep, 0, 0)
+    check_evict(k, v, w, pos, [cap, cap - 1], keep, 2, keep // 4)
+
+
+def test_rows_after_a_nan_query_are_evicted_in_order():
+    """A NaN query makes every weight NaN; rows appended behind them gather numbers, and the eviction counts those as less."""
+    torch = torch_cuda()
+    b, cap, hk, h, d, n, more, keep = 2, 200, 2, 4, 64, 150, 40, 100
+    rows = [rand(i, b, n + more, hk, d)[0] for i in (1, 2)]
+    cache = sa.scored_alloc(b, cap, hk, d)
+    sa.scored_append(cache, *(x[:, :n] for x in rows))
+    q = rand(0, b, 1, h, d)[0]
+    lengths = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    bad = q.clone()
+    bad[0, 0, :, 3] = float("nan")
+    sa.scored_attn_decode(bad, cache, lengths)
+    sa.scored_append(cache, *(x[:, n:] for x in rows), lengths, lengths)
+    lengths += more
+    sa.scored_attn_decode(q, cache, lengths)
+    status_ok()
+    assert torch.isnan(cache.weights[0, :, :n]).all() and (cache.weights[0, :, n:n + more] > 0).all() and (cache.weights[1, :, :n + more] > 0).all()
+    check_evict(*cache, lengths.tolist(), keep, 4, 16)
+
+
 # ------------------------------------------------------------------ the weights of a prompt
 
 WEIGHTS_CASES = [
