@@ -946,8 +946,9 @@ __global__ void __launch_bounds__(kThreads, Q4 && NQ == 1 ? 4 : (MODE != kPlain 
         const float mk = *cluster.map_shared_rank(cm + q % kQ, q / kQ * ranks + k);
         L = fmaf(M != kNegInf ? ex2_approx(mk - M) : 1.f, *cluster.map_shared_rank(cl + q % kQ, q / kQ * ranks + k), L);
       }
-      hm[q] = M;
-      hi[q] = 1.f / L;
+      // a head without a finite score adds nothing, as its O is 0; L is NaN where a score is
+      hm[q] = M != kNegInf ? M : 0.f;
+      hi[q] = L == 0.f ? 0.f : 1.f / L;
     }
     __syncthreads();
     const int64_t list = (int64_t)s * p.kv_heads + hk;

@@ -543,7 +543,8 @@ int sa_scored_append(const void* k, const void* v, const int64_t k_strides[3], c
  *   decay : 0 .. 1; 0 does not read w_in.
  *   d_weights_out may be d_weights_in.
  *   workspace : device memory, 256-byte aligned, of sa_scored_attn_decode_workspace_size bytes (scores).
- * At most 128 query heads per key head. A score that is NaN makes its key head's weights NaN. */
+ * At most 128 query heads per key head. A score that is NaN makes its key head's weights NaN; a query head whose scores are
+ * all -inf (products past the fp32 range) adds nothing to them, as its o is 0 and its lse -inf. */
 int sa_scored_attn_decode_workspace_size(int32_t batch, int32_t capacity, int32_t heads, int32_t kv_heads,
                                          size_t* h_bytes);
 int sa_scored_attn_decode(const void* q, const void* k_cache, const void* v_cache, const int64_t q_strides[3],

@@ -482,6 +482,40 @@ def test_nan_of_what_is_seen(h, d):
     assert torch.equal(o[1, 0, :group], o1[1, 0, :group]) and torch.equal(lse[1, :group], lse1[1, :group])
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("h", [3, 20])
+def test_scores_that_are_all_minus_infinity_add_no_weight(h, d):
+    """Head 1's scores pass the fp32 range downwards, on every row or on some: rows without a finite score are as no rows (o 0, lse
+    -inf), and add nothing to the weights that the other heads give."""
+    torch = torch_cuda()
+    b, cap, lengths = 4, 600, [1, 600, 70, 600]
+    q, qf = rand(0, b, 1, h, d)
+    (k, kf), (v, vf) = rand(1, b, cap, 1, d), rand(2, b, cap, 1, d)
+    for t in (q, qf):
+        t[..., 0] = 0.0
+        t[:, :, 1] = 0.0
+    q[:, :, 1, 0] = 3e38
+    for t in (k, kf):
+        t[..., 0] = -4.0
+        t[3, ::7, :, 0] = 0.0                              # the last sequence has rows that head 1 sees, alike
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    old = torch.rand(b, 1, cap, device="cuda")
+    cache = sa.ScoredCache(k, v, old.clone(), torch.zeros(b, 1, cap, dtype=torch.int32, device="cuda"))
+    o, lse = sa.scored_attn_decode(q, cache, n, 0.5)
+    status_ok()
+    others = [e for e in range(h) if e != 1]
+    of, lf, ob, want, bound = oc.scored_decode(qf[:, :, others], kf, vf, lengths, old.double().cpu().numpy(), 0.5)
+    assert_close_attention(o[:, :, others], lse[:, others], (of, lf, ob))
+    assert not o[:3, 0, 1].any() and torch.isneginf(lse[:3, 1]).all()
+    rows = np.arange(0, cap, 7)
+    want[3, 0, rows] += 1 / len(rows)
+    bound[3, 0, rows] += oc.P_REL / len(rows)
+    close(cache.weights, want, bound + 1e-30, "weights")
+    mean = vf[3, rows, 0].mean(0)
+    close(o[3, 0, 1], mean, 1.02 * ref.U * (np.abs(mean) + np.abs(vf[3, rows, 0]).mean(0)) + 1e-6, "o")
+    assert abs(float(lse[3, 1]) - np.log(len(rows))) <= LSE_TOL
+
+
 @pytest.mark.parametrize("d", [32, 128])
 def test_prefix_attention_keeps_nan_queries(d):
     torch = torch_cuda()
