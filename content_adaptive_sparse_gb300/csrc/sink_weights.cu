@@ -505,9 +505,9 @@ __device__ void sums(const WParams& p, Walk w, Bars& bars, const uint8_t* sK, fl
         }
         float a, z;
         f2::unpack(f2::add(sum[0], sum[1]), a, z);
-        // total += a + z, with the rounding error of the sum carried on
+        // total += a + z, with the rounding error of the sum carried on (an infinite sum has none)
         const float y = (a + z) - lost, t = total + y;
-        lost = (t - total) - y;
+        lost = t < __int_as_float(0x7f800000) ? (t - total) - y : 0.f;
         total = t;
         tc_fence_before();
       }

@@ -388,6 +388,25 @@ def test_sink_weights_of_large_scores(d):
     close(got, want, LARGE_P * want + 1e-30, "weights")
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("value", [-200.0, -float("inf"), float("inf")])
+def test_sink_weights_past_the_fp32_range(d, value):
+    """LSE of some queries that is not the forward's: the keys that they see gather infinity (or nothing from them), however many
+    queries follow, and the others what they do without."""
+    torch = torch_cuda()
+    n, h, w, s = 2600, 16, 2000, 3                         # several steps a CTA
+    (q, qf), (k, kf) = rand(0, 1, n, h, d), rand(1, 1, n, 2, d)
+    _, lse = sa.sink_attn_fwd(q, k, k, w, s)
+    for e, i in ((0, 300), (1, 640), (1, 0), (11, 899), (15, 2599)):
+        lse[0, e, i] = value
+    got = sa.sink_attn_weights(q, k, lse, w, s).double().cpu().numpy()
+    status_ok()
+    want, bound = oc.sink_weights(qf, kf, lse.double().cpu().numpy(), w, s, 0)
+    over = want > np.finfo(np.float32).max
+    assert np.array_equal(np.isposinf(got), over) and over.any() == (value < 0) and not over.all()
+    close(got[~over], want[~over], bound[~over], "weights")
+
+
 def test_prefix_attention_strided_scaled_and_repeated():
     """Views of packed projections, one buffer of prefix keys and values, outputs with strides of their own."""
     torch = torch_cuda()
