@@ -389,7 +389,7 @@ __device__ void lse_rows(const WParams& p, Walk w, int which, Bars& bars, uint8_
       float part[3] = {y, 0.f, 0.f};
       const uint32_t top = __float_as_uint(y) & 0x7f800000u;
       if (top != 0x7f800000u) {                        // numbers: y = part 0 + part 1 + part 2
-        part[0] = __bfloat162float(__float2bfloat16_rn(y));
+        part[0] = __bfloat162float(__float2bfloat16_rz(y));    // towards 0: the largest numbers have to stay numbers
         part[1] = __bfloat162float(__float2bfloat16_rn(y - part[0]));
         part[2] = y - part[0] - part[1];
       }

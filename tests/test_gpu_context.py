@@ -407,6 +407,23 @@ def test_sink_weights_past_the_fp32_range(d, value):
     close(got[~over], want[~over], bound[~over], "weights")
 
 
+@pytest.mark.parametrize("value", [3.4e38, -3.4e38])
+def test_sink_weights_of_the_largest_lse(value):
+    """LSE next to the largest number, which rounds to infinity in bf16: its query gives nothing, or infinity."""
+    torch = torch_cuda()
+    n, w = 300, 299
+    (q, qf), (k, kf) = rand(0, 1, n, 2, 64, scale=0.3), rand(1, 1, n, 1, 64, scale=0.3)
+    _, lse = sa.sink_attn_fwd(q, k, k, w, 0, 1.0)
+    lse[0, 1, 170] = value
+    got = sa.sink_attn_weights(q, k, lse, w, 0, 0, 1.0).double().cpu().numpy()
+    status_ok()
+    with np.errstate(over="ignore"):
+        want, bound = oc.sink_weights(qf, kf, lse.double().cpu().numpy(), w, 0, 0, 1.0)
+    over = want > np.finfo(np.float32).max
+    assert np.array_equal(np.isposinf(got), over) and over.sum() == (171 if value < 0 else 0)
+    close(got[~over], want[~over], bound[~over], "weights")
+
+
 def test_prefix_attention_strided_scaled_and_repeated():
     """Views of packed projections, one buffer of prefix keys and values, outputs with strides of their own."""
     torch = torch_cuda()
