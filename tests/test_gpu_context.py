@@ -184,6 +184,22 @@ def test_scored_decode(h, hk, d, cap, decay, lengths):
     assert torch.equal(cache.weights, torch.where(unseen, w, out))
 
 
+@pytest.mark.parametrize("group", [33, 48, 66, 80, 96, 97, 112])
+@pytest.mark.parametrize("hk,d,cap,lengths", [(1, 64, 700, [700, 129, 3]), (2, 128, 65, [65]), (3, 32, 260, [0, 1, 260, 64, 63])])
+def test_scored_decode_of_many_head_groups(group, hk, d, cap, lengths):
+    """3, 5, 6 and 7 groups of 16 query heads of a key head, whose CTAs make clusters of sizes that are no powers of two."""
+    torch = torch_cuda()
+    b, h = len(lengths), group * hk
+    (q, qf), (k, kf), (v, vf) = rand(0, b, 1, h, d), rand(1, b, cap, hk, d), rand(2, b, cap, hk, d)
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    cache = sa.ScoredCache(k, v, torch.ones(b, hk, cap, device="cuda"), torch.zeros(b, hk, cap, dtype=torch.int32, device="cuda"))
+    o, lse = sa.scored_attn_decode(q, cache, n, 0.75)
+    status_ok()
+    of, lf, ob, w, wb = oc.scored_decode(qf, kf, vf, lengths, np.ones((b, hk, cap)), 0.75)
+    assert_close_attention(o, lse, (of, lf, ob))
+    close(cache.weights, w, wb + 1e-30, "weights")
+
+
 def test_scored_append():
     torch = torch_cuda()
     b, cap, hk, d, n = 3, 20, 2, 64, 5
