@@ -182,6 +182,10 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* v, uint64_t c2, uint64
   }
 }
 
+// Running maximum of a row without a finite score as yet (no key seen, or products past the fp32 range): 2^(s c - m) is 0 for s = -inf,
+// where -inf as the maximum would make it NaN.
+constexpr float kLowest = -0x1.fffffep127f;
+
 template <int D>
 struct Softmax {
   using C = Cfg<D>;
@@ -227,7 +231,7 @@ struct Softmax {
       const bool need = mx > m + 8.f;
       if (__any_sync(0xffffffffu, need)) {
         // the running maximum grows by more than 2^8: l and O_h follow
-        const float alpha = need ? ex2_approx(m - mx) : 1.f;              // 0 from -inf
+        const float alpha = need ? ex2_approx(m - mx) : 1.f;              // 0 from kLowest
         l *= alpha;
         if (need) m = mx;
         if (later) {
@@ -244,8 +248,7 @@ struct Softmax {
           }
         }
       }
-      const float ref = SEE == kSome && m == kNegInf ? 0.f : m;           // no key seen yet: all scores are -inf
-      const uint64_t c2 = f2::pack(c, c), r2 = f2::pack(-ref, -ref);
+      const uint64_t c2 = f2::pack(c, c), r2 = f2::pack(-m, -m);
       uint64_t rs[2] = {0ull, 0ull};
       if (on0) {
         exp_chunk(v, c2, r2, pk, rs);

@@ -195,7 +195,7 @@ __device__ void softmax(const PParams& p, Bars& bars, Handoff* hand, uint32_t tm
     const int last = it.rows - 1;
     const int t = (it.row0 + min(row, last)) / p.l.group;
     const int ta = __shfl_sync(0xffffffffu, t, 0), tb = __shfl_sync(0xffffffffu, t, 31);
-    W.m = __int_as_float(0xff800000);
+    W.m = kLowest;
     W.l = 0.f;
     bool later = false;
     for (int j = 0; j < it.steps; ++j, ++g) {
@@ -290,9 +290,8 @@ __device__ void epilogue(const PParams& p, Bars& bars, const Handoff* hand, uint
     const float m0 = hand[e].m[0][row], m1 = hand[e].m[1][row], l0 = hand[e].l[0][row], l1 = hand[e].l[1][row];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.epi_empty[e]);
-    // without a maximum the sums are zero, or NaN
     const float m = fmaxf(m0, m1);
-    float f0 = m == kNegInf ? 1.f : ex2_approx(m0 - m), f1 = m == kNegInf ? 1.f : ex2_approx(m1 - m);
+    float f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
     const float L = l0 * f0 + l1 * f1;
     const bool on = row < it.rows;
     const int r = it.row(p, on ? row : 0);
@@ -437,7 +436,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   const float2* ml = p.part_ml + p.l.place(hk, r);
   const float4* part = p.part_o + (p.l.place(hk, r) / kTile * (D / 4)) * kTile + r % kTile;
   const int parts = p.l.slots;
-  float M = kNegInf, L = 0.f;
+  float M = kLowest, L = 0.f;
 #pragma unroll 8
   for (int k = 0; k < parts; ++k) M = fmaxf(M, ml[k * kTile].x);
   float4 v[kCols];
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
 #pragma unroll 2
   for (int k = 0; k < parts; ++k) {
     const float2 e = ml[k * kTile];
-    const float a = M != kNegInf ? ex2_approx(e.x - M) : 1.f;      // without a maximum the sums are zero, or NaN
+    const float a = ex2_approx(e.x - M);
     L = fmaf(a, e.y, L);
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {

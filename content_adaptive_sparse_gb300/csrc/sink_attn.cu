@@ -185,7 +185,7 @@ __device__ void softmax(const FParams& p, Bars& bars, Handoff* hand, uint32_t tm
   int g = 0, n = 0;
   for (Item it(p); it.more(); it.next(p), ++n) {
     const int q0 = it.tile * kTile + 32 * quarter;
-    W.m = __int_as_float(0xff800000);
+    W.m = kLowest;
     W.l = 0.f;
     bool later = false;
     for (int j = 0; j < it.steps; ++j, ++g) {
@@ -226,7 +226,6 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;
   const int row = quarter * 32 + lane;
-  const float kNegInf = __int_as_float(0xff800000);
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
   uint8_t* stage = out + quarter * C::OUT;
   const uint32_t srow = smem_u32(stage) + 64u * lane;
@@ -238,9 +237,9 @@ __device__ void epilogue(const FParams& p, const CUtensorMap* to, Bars& bars, co
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.epi_empty[e]);
     const float m = fmaxf(m0, m1);
-    float f0 = m0 == kNegInf ? 0.f : ex2_approx(m0 - m), f1 = m1 == kNegInf ? 0.f : ex2_approx(m1 - m);
+    float f0 = ex2_approx(m0 - m), f1 = ex2_approx(m1 - m);
     const float L = l0 * f0 + l1 * f1;
-    const float inv = 1.f / L;                         // every query sees itself: L > 0, or NaN as its scores
+    const float inv = L == 0.f ? 0.f : 1.f / L;        // every query sees itself: 0 where its scores are all -inf
     f0 *= inv;
     f1 *= inv;
     const int q0 = it.tile * kTile + 32 * quarter, tok = q0 + lane;

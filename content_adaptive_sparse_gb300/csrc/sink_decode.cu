@@ -661,7 +661,7 @@ __device__ __forceinline__ void join_prefix(const DParams& p, cooperative_groups
       if (k0 > 0) {
         float M = top[q];
         for (int k = 0; k < all; ++k) M = fmaxf(M, fm[q][k]);
-        back[x] = M != kNegInf ? ex2_approx(top[q] - M) : 1.f;
+        back[x] = ex2_approx(top[q] - M);
       }
     }
     __syncthreads();
@@ -669,10 +669,10 @@ __device__ __forceinline__ void join_prefix(const DParams& p, cooperative_groups
       const int q = threadIdx.x;
       float M = top[q];
       for (int k = 0; k < all; ++k) M = fmaxf(M, fm[q][k]);
-      // without a maximum the sums are zero, or NaN
-      float L = sum[q] * (M != kNegInf ? ex2_approx(top[q] - M) : 1.f);
+      // M is a number, as the prefix's maxima are (half_softmax.cuh); the ranks' may be -inf
+      float L = sum[q] * ex2_approx(top[q] - M);
       for (int k = 0; k < all; ++k) {
-        const float a = M != kNegInf ? ex2_approx(fm[q][k] - M) : 1.f;
+        const float a = ex2_approx(fm[q][k] - M);
         fm[q][k] = a;
         L = fmaf(a, fl[q][k], L);
       }

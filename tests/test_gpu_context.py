@@ -568,6 +568,65 @@ def test_scores_that_are_all_minus_infinity_add_no_weight(h, d):
     assert abs(float(lse[3, 1]) - np.log(len(rows))) <= LSE_TOL
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("some", [False, True])
+def test_prefix_scores_that_are_minus_infinity(d, some):
+    """Head 1's scores pass the fp32 range downwards, on every key or on all but a few (whole tiles have no finite score): those few
+    are seen alike, and without one o is 0 and lse -inf. Prompts and single tokens, few rows and many."""
+    torch = torch_cuda()
+    for b, n, p, h in ((2, 150, 1500, 2), (3, 5, 700, 4)):
+        (q, qf), (k, kf), (v, vf) = (rand(i, b, n, x, d) for i, x in enumerate((h, 1, 1)))
+        (kp, kpf), (vp, vpf) = (rand(i, 1, p, 1, d) for i in (3, 4))
+        for t in (q, qf):
+            t[..., 0] = 0.0
+            t[:, :, 1] = 0.0
+        q[:, :, 1, 0] = 3e38
+        for t in (k, kf, kp, kpf):
+            t[..., 0] = -4.0
+        if some:
+            for t in (kp, kpf):
+                t[:, 130::400, :, 0] = 0.0
+        others, w = [e for e in range(h) if e != 1], 100
+        lengths = torch.full((b,), n, dtype=torch.int32, device="cuda")
+        seen = vpf[0, 130::400, 0]
+        mean, size = (seen.mean(0), np.abs(seen).mean(0)) if some else (0.0, 0.0)
+        want = oc.prefix_attention(qf[:, :, others], kpf, vpf, kf, vf, w)
+        for rows, (o, lse) in ((slice(0, n), sa.prefix_attn_fwd(q, kp, vp, k, v, w)),
+                               (slice(n - 1, n), sa.prefix_attn_decode(q[:, -1:], kp, vp, k, v, lengths, w))):
+            status_ok()
+            assert_close_attention(o[:, :, others], lse[:, others], (want[0][:, rows], want[1][:, :, rows], want[2][:, rows]))
+            mine = o[:, :, 1].double().cpu().numpy()
+            close(mine, np.broadcast_to(mean, mine.shape), 1.02 * ref.U * (np.abs(mean) + size) + 1e-6, "o")
+            assert ((lse[:, 1] - np.log(len(seen))).abs() <= LSE_TOL if some else torch.isneginf(lse[:, 1])).all()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sink_window_scores_that_are_minus_infinity(d):
+    """The same of the sink-window forward: head 1 has a finite score on the first token (a sink) and on every 400th alone."""
+    n, w, s = 1500, 300, 1
+    (q, qf), (k, kf), (v, vf) = (rand(i, 1, n, x, d) for i, x in enumerate((2, 1, 1)))
+    for t in (q, qf):
+        t[..., 0] = 0.0
+        t[:, :, 1] = 0.0
+    q[:, :, 1, 0] = 3e38
+    for t in (k, kf):
+        t[..., 0] = -4.0
+        t[:, ::400, :, 0] = 0.0
+    for sinks in (s, 0):
+        o, lse = sa.sink_attn_fwd(q, k, v, w, sinks)
+        status_ok()
+        want = ref.sink_attention(qf[:, :, :1], kf, vf, w, sinks)
+        assert_close_attention(o[:, :, :1], lse[:, :1], want)
+        mask = ref.sink_mask(n, w, sinks) & (np.arange(n) % 400 == 0)
+        count = mask.sum(1)
+        p = mask / np.maximum(count, 1)[:, None]
+        mean, size = p @ vf[0, :, 0], p @ np.abs(vf[0, :, 0])
+        close(o[0, :, 1], mean, 1.02 * ref.U * (np.abs(mean) + size) + 1e-6, "o")
+        assert (count == 0).any() == (sinks == 0)
+        got = lse[0, 1].double().cpu().numpy()
+        assert np.array_equal(np.isneginf(got), count == 0) and np.abs(got[count > 0] - np.log(count[count > 0])).max() <= LSE_TOL
+
+
 @pytest.mark.parametrize("d", [32, 128])
 def test_prefix_attention_keeps_nan_queries(d):
     torch = torch_cuda()
