@@ -55,7 +55,7 @@ struct Layout {
   int row_tiles, slots;             // tiles of `rows`; partial results of a row (0: the items write O and LSE)
   // Partial results lie in blocks of 128 rows of all sequences, `slots` blocks one behind the other: where the
   // first of row r of key head hk has its m and l; the next is 128 places on.
-  __host__ __device__ int64_t place(int hk, int r) const {
+  __device__ int64_t place(int hk, int r) const {
     return (int64_t)(hk * row_tiles + r / kTile) * slots * kTile + r % kTile;
   }
 };
@@ -81,15 +81,14 @@ struct Item {
   int s, hk, row0, rows;            // rows row0 .. row0 + rows - 1 of all sequences' (class 0) or of s's
   int pre, begin, steps, own;       // prefix tiles of the whole list; this part of it; first own tile
   int slot;
-  __device__ explicit Item(const PParams& p) : Item(p, (int)blockIdx.x) {}
-  __host__ __device__ Item(const PParams& p, int first) : at(first) { set(p); }
+  __device__ explicit Item(const PParams& p) : at((int)blockIdx.x) { set(p); }
   __device__ __forceinline__ bool more() const { return on; }
   __device__ __forceinline__ void next(const PParams& p) {
     at += (int)gridDim.x;
     set(p);
   }
   // The row tiles of a key head follow one another, so that CTAs at work share its prefix in L2.
-  __host__ __device__ void set(const PParams& p) {
+  __device__ void set(const PParams& p) {
     const Layout& l = p.l;
     on = at < l.items0 + l.items1;
     if (!on) return;
@@ -118,11 +117,11 @@ struct Item {
     steps = (int)((int64_t)all * (part + 1) / parts) - begin;
     slot = common || l.items0 == 0 ? part : l.parts0;
   }
-  __host__ __device__ bool is_prefix(int j) const { return begin + j < pre; }
-  __host__ __device__ int key_tile(int j) const { return begin + j < pre ? begin + j : own + begin + j - pre; }
+  __device__ bool is_prefix(int j) const { return begin + j < pre; }
+  __device__ int key_tile(int j) const { return begin + j < pre ? begin + j : own + begin + j - pre; }
   __device__ __forceinline__ bool one_half(const PParams&, int) const { return false; }
   // Row of a key head's matrix (all sequences) of the item's row r.
-  __host__ __device__ int row(const PParams& p, int r) const { return (common ? 0 : s * p.l.seq_rows) + row0 + r; }
+  __device__ int row(const PParams& p, int r) const { return (common ? 0 : s * p.l.seq_rows) + row0 + r; }
 };
 
 // ------------------------------------------------------------------ loader (warp 8, one lane)

@@ -124,24 +124,18 @@ __host__ __device__ inline int64_t before(const WParams& p, int t) {
 
 // The last list that begins at r or before, found by all lanes of a warp (one comparison after the other took 5 us of
 // 64-bit arithmetic).
-struct Search {
-  __host__ __device__ int operator()(const WParams& p, int64_t r) const {
-    int lo = 0, n = p.pairs;        // it is one of n lists from lo on
-#ifdef __CUDA_ARCH__
-    const int lane = threadIdx.x & 31;
-    while (n > 1) {
-      const int step = (n + 31) / 32;
-      const unsigned ok = __ballot_sync(0xffffffffu, lane * step < n && before(p, lo + lane * step) <= r);
-      const int last = 31 - __clz(ok);         // before(lo) <= r: bit 0 is set
-      n = n - last * step < step ? n - last * step : step;
-      lo += last * step;
-    }
-#else
-    for (; n > 1 && before(p, lo + 1) <= r; --n) ++lo;
-#endif
-    return lo;
+__device__ __forceinline__ int list_at(const WParams& p, int64_t r) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.pairs;          // it is one of n lists from lo on
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const unsigned ok = __ballot_sync(0xffffffffu, lane * step < n && before(p, lo + lane * step) <= r);
+    const int last = 31 - __clz(ok);           // before(lo) <= r: bit 0 is set
+    n = n - last * step < step ? n - last * step : step;
+    lo += last * step;
   }
-};
+  return lo;
+}
 
 // The pieces of lists of CTA c of `ctas`: steps [jb, je) of list t of (sequence, key head) sh.
 struct Walk {
@@ -149,10 +143,10 @@ struct Walk {
   int sh, t, i0, count;             // the list's first query tile and number of them
   int64_t list;                     // where it begins
   int jb, je;
-  __host__ __device__ static int64_t bound(const WParams& p, int c) { return p.quota * c + (c < p.rest ? c : p.rest); }
+  __device__ static int64_t bound(const WParams& p, int c) { return p.quota * c + (c < p.rest ? c : p.rest); }
   // (by all lanes of a warp)
-  __host__ __device__ Walk(const WParams& p, int c) : Walk(p, bound(p, c), bound(p, c + 1)) {}
-  __host__ __device__ Walk(const WParams& p, int64_t from, int64_t to) : at(from), end(to) {
+  __device__ Walk(const WParams& p, int c) : Walk(p, bound(p, c), bound(p, c + 1)) {}
+  __device__ Walk(const WParams& p, int64_t from, int64_t to) : at(from), end(to) {
     sh = t = i0 = count = jb = je = 0;
     list = 0;
     if (at >= end) return;
@@ -165,13 +159,13 @@ struct Walk {
       sh = (int)(at / per);
       r = (at - sh * per) / p.group;
     }
-    t = Search()(p, r);
+    t = list_at(p, r);
     list = sh * per + before(p, t) * p.group;
     set(p);
   }
-  __host__ __device__ bool more() const { return at < end; }
-  __host__ __device__ int length(const WParams& p) const { return count * p.group; }
-  __host__ __device__ void set(const WParams& p) {
+  __device__ bool more() const { return at < end; }
+  __device__ int length(const WParams& p) const { return count * p.group; }
+  __device__ void set(const WParams& p) {
     int i1;
     span(p, t, i0, i1);
     count = i1 - i0 + 1;
@@ -179,7 +173,7 @@ struct Walk {
     const int64_t rest = end - list;
     je = rest < length(p) ? (int)rest : length(p);
   }
-  __host__ __device__ void next(const WParams& p) {
+  __device__ void next(const WParams& p) {
     at = list + je;
     if (at >= end) return;
     list += length(p);              // the next list with steps
@@ -195,8 +189,8 @@ struct Walk {
 // Step j of a list: query head of the group and query tile.
 struct Step {
   int e, i;
-  __host__ __device__ Step(const Walk& w) : e(w.jb / w.count), i(w.i0 + w.jb % w.count) {}
-  __host__ __device__ void next(const Walk& w) {
+  __device__ Step(const Walk& w) : e(w.jb / w.count), i(w.i0 + w.jb % w.count) {}
+  __device__ void next(const Walk& w) {
     if (++i == w.i0 + w.count) {
       i = w.i0;
       ++e;
