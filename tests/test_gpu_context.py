@@ -325,6 +325,28 @@ def test_rows_after_a_nan_query_are_evicted_in_order():
     check_evict(*cache, lengths.tolist(), keep, 4, 16)
 
 
+@pytest.mark.parametrize("cap,keep", [(300, 299), (300, 100), (1500, 700), (9000, 8999), (9000, 4000)])
+@pytest.mark.parametrize("over", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (1, 0, 1), (0, 1, 1)])
+def test_evict_with_some_outputs_over_the_inputs(cap, keep, over):
+    """Weights, positions and lengths each in place or elsewhere."""
+    torch = torch_cuda()
+    lengths = [cap, keep - 1, keep + 1]
+    k, v, w, pos = evict_inputs(3, cap, 1, 32)
+    want = oc.evict(bits(k).cpu().numpy(), bits(v).cpu().numpy(), w.cpu().numpy(), pos.cpu().numpy(), lengths, keep, 1, keep // 3)
+    cache = sa.ScoredCache(k, v, w.clone(), pos.clone())
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    m = n.clone()
+    outs = [x if o else torch.full_like(x, -1) for x, o in zip((cache.weights, cache.positions, m), over)]
+    got = sa.scored_evict(cache, m, keep, 1, keep // 3, *outs)
+    status_ok()
+    assert np.array_equal(bits(k).cpu().numpy(), want[0]) and np.array_equal(bits(v).cpu().numpy(), want[1])
+    used = torch.arange(cap, device="cuda") < torch.tensor(want[4], device="cuda")[:, None, None]
+    for x, y, before, kept, o in ((got[0], want[2], w, cache.weights, over[0]), (got[1], want[3], pos, cache.positions, over[1])):
+        assert torch.equal(bits(x), bits(torch.where(used, torch.from_numpy(y).cuda(), before if o else torch.full_like(before, -1))))
+        assert o or torch.equal(kept, before)
+    assert got[2].tolist() == want[4] and (over[2] or m.tolist() == lengths)
+
+
 # ------------------------------------------------------------------ the weights of a prompt
 
 WEIGHTS_CASES = [
