@@ -17,12 +17,13 @@
 // has its own interval of visible keys. Warps whose 32 rows are all past the last one only pass
 // the barriers.
 //
-// Measured: the last 8192 tokens of a 64K prompt behind the other 57344, 16 heads of 128 over 4 key heads, window 4095: 2433 us,
-// 1.67 PFLOP/s, 0.86 of the library product's rate in a burst and 0.97 of its sustained one; the tensor pipe is two
-// thirds busy, as in the sink-window forward, with the handshakes of S, P and O between. 32 questions of 37 tokens to
-// 16384: 111 us of 82 (148 items of 128 steps on 152 SMs, 0.78 us a step; then one or two own items a CTA, and the
-// join, 5 us). 64 tokens behind 32768: 42 us with the decoding launch, of which 15 to 20 here: 2 until the first Q and
-// K are in (most of it a cold start of every role's code), 13.5 steps of 0.75 us, 1.5 for the results.
+// Measured: the last 8192 tokens of a 64K prompt behind the other 57344, 16 heads of 128 over 4 key heads, window 4095: 2400 to
+// 2430 us, 1.69 to 1.67 PFLOP/s, 0.87 of the library product's rate in a burst (2660 to 2730, 0.77, in a long loop, power-capped);
+// the tensor pipe is two thirds busy, as in the sink-window forward, with the handshakes of S, P and O between. 32 questions of
+// 37 tokens to 16384: 111 us of 82 (148 items of 128 steps on 152 SMs, 0.78 us a step; then one or two own items a CTA, and
+// the join, 5 us). 64 tokens behind 32768: 42 us with the decoding launch, of which 19 here, by a CTA's clock in calls that are
+// waited for: Q is in after 3.4, the first scores after 4.5 and the second after 6.6 (cold rows and a cold start of every role's
+// code), then 0.75 a step (13.5 steps), and 2.3 from the last scores to the results.
 //
 // Warp roles (512 threads): 0-7 softmax, 8 loader of K and V, 9 S = Q K^T, 10 and 11 O_h += P_h V_h, 12-15 load Q and
 // write the results.
@@ -475,7 +476,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
 
 constexpr int kPlanSms = 152;        // a plan must not depend on the device that asks for its workspace
 
-// Rounds of 152 CTAs times an item's steps; an item's start and end cost about three steps.
+// Rounds of 152 CTAs times an item's steps; an item's start and end cost about three steps (2.3 us). What a CTA's first item costs
+// besides, since everything is cold, comes once in every plan.
 double cost(int64_t items, double steps) {
   return (double)((items + kPlanSms - 1) / kPlanSms) * (steps + 3.0);
 }

@@ -17,9 +17,11 @@
 // buffers of S^T take turns.
 //
 // Measured: two prompts of 8192 tokens, 16 heads of 128 over 4 key heads, all queries: 190 us, 1.46 PFLOP/s
-// (277 GFLOP of visible scores),
+// (277 GFLOP of visible scores; 210 us in a long loop, power-capped),
 // the tensor pipe 72 % busy, the exponentials' 64 %; a step's two products, its sums and the hand-overs between them
-// are each near its 1600 cycles. The last 64 queries of 32768: 19 us for 34 MB of keys: 4 us until the first
+// are each near its 1600 cycles. With heads of 64 and 32, where LSE's step is a quarter and a half of the product, 167 and 162 us: there
+// the exponentials and hand-overs bound it, not the products. The last 64 queries of 32768: 19 us for 34 MB of keys (18 with
+// heads of 64 and 32): 4 us until the first
 // scores, 13.5 steps a CTA with a new list every fourth, and the joining launch.
 //
 // Sums: 64 queries a step in four fp32 sums, and the steps' totals with their rounding errors carried along
