@@ -786,6 +786,11 @@ __device__ __forceinline__ uint4 prep_row(const PrepTensor& t, int s, uint32_t i
   return *reinterpret_cast<const uint4*>(t.ptr + s * t.sb + i * t.sn + h * t.sh + 8 * part);
 }
 
+// -LSE in log2 units. A query without a finite score (LSE -inf) has no gradient: P is 0, as past the sequence.
+__device__ __forceinline__ float minus_lse(float lse) {
+  return lse == __int_as_float(0xff800000) ? lse : -lse * kLog2e;
+}
+
 // D / 8 consecutive threads per kPrepRows (token, head) rows of a sequence, 16 bytes of O and dO each;
 // tokens n .. pitch - 1 get D = 0 and -LSE = -inf, so that their P is 0. (16321 tokens of 16 heads of
 // 128: 28 us, 4.8 TB/s; one row a thread 32.)
@@ -815,7 +820,7 @@ __global__ void __launch_bounds__(256) sink_prep_kernel(const __grid_constant__ 
       if (part == 0 && r0 + u < rows) {
         const int64_t bh = (int64_t)s * heads + h;
         p.dvec[bh * p.pitch + i] = d;
-        p.nl2[bh * p.pitch + i] = i < n ? -p.lse[bh * n + i] * kLog2e : __int_as_float(0xff800000);
+        p.nl2[bh * p.pitch + i] = i < n ? minus_lse(p.lse[bh * n + i]) : __int_as_float(0xff800000);
       }
     }
   }
@@ -840,7 +845,7 @@ __global__ void __launch_bounds__(256) sink_few_kernel(const __grid_constant__ P
     const int64_t bh = (int64_t)s * heads + h;
     const uint4 q = keys > 0 ? prep_row(p.q, s, i, h, part) : zero;
     const uint4 g = keys > 0 ? prep_row(p.d_o, s, i, h, part) : zero;
-    const float nl2 = keys > 0 ? -p.lse[bh * n + i] * kLog2e : __int_as_float(0xff800000);
+    const float nl2 = keys > 0 ? minus_lse(p.lse[bh * n + i]) : __int_as_float(0xff800000);
     float d = 0.f;
 #pragma unroll 1
     for (int e0 = 0; __any_sync(0xffffffffu, e0 < keys); e0 += kFewStep) {

@@ -649,6 +649,26 @@ def test_sink_window_scores_that_are_minus_infinity(d):
         assert np.array_equal(np.isneginf(got), count == 0) and np.abs(got[count > 0] - np.log(count[count > 0])).max() <= LSE_TOL
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("n,w,s", [(600, 599, 0), (300, 70, 2), (40, 3, 0)])
+def test_sink_window_gradients_of_scores_that_are_minus_infinity(d, n, w, s):
+    """A head without a finite score has no gradient, and the others' are as without it."""
+    (q, qf), (k, kf), (v, vf), (g, gf) = (rand(i, 1, n, x, d) for i, x in enumerate((2, 1, 1, 2)))
+    for t in (q, qf):
+        t[..., 0] = 0.0
+        t[:, :, 1] = 0.0
+    q[:, :, 1, 0] = 3e38
+    for t in (k, kf):
+        t[..., 0] = -4.0
+    o, lse = sa.sink_attn_fwd(q, k, v, w, s)
+    dq, dk, dv = sa.sink_attn_bwd(q, k, v, o, lse, g, w, s)
+    status_ok()
+    (dqf, dkf, dvf), (bq, bk, bv) = ref.sink_attention_backward(qf[:, :, :1], kf, vf, gf[:, :, :1], w, s)
+    assert not dq[:, :, 1].any()
+    for x, y, bound in ((dq[:, :, :1], dqf, bq), (dk, dkf, bk), (dv, dvf, bv)):
+        close(x, y, bound, "gradient")
+
+
 @pytest.mark.parametrize("d", [32, 128])
 def test_prefix_attention_keeps_nan_queries(d):
     torch = torch_cuda()
