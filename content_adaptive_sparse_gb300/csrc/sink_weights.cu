@@ -381,7 +381,9 @@ __device__ void lse_rows(const WParams& p, Walk w, int which, Bars& bars, uint8_
     uint8_t* tile = sSide + side_slot(g);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const float y = v[x] * -p.inv_scale;
+      float y = v[x] * -p.inv_scale;
+      // for LSE = -inf the largest number: with it scores of -inf, the forward's reason for that LSE, stay so
+      if (y == __int_as_float(0x7f800000)) y = __int_as_float(0x7f7fffff);
       float part[3] = {y, 0.f, 0.f};
       const uint32_t top = __float_as_uint(y) & 0x7f800000u;
       if (top != 0x7f800000u) {                        // numbers: y = part 0 + part 1 + part 2

@@ -445,6 +445,26 @@ def test_sink_weights_past_the_fp32_range(d, value):
     close(got[~over], want[~over], bound[~over], "weights")
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_sink_weights_of_scores_that_are_minus_infinity(d):
+    """Queries without a finite score, whose LSE from the forward is -inf, add nothing."""
+    n, w, s = 700, 300, 4
+    (q, qf), (k, kf) = rand(0, 1, n, 2, d), rand(1, 1, n, 1, d)
+    for t in (q, qf):
+        t[..., 0] = 0.0
+        t[:, :, 1] = 0.0
+    q[:, 100:, 1, 0] = 3e38
+    for t in (k, kf):
+        t[..., 0] = -4.0
+    _, lse = sa.sink_attn_fwd(q, k, k, w, s)
+    got = sa.sink_attn_weights(q, k, lse, w, s)
+    status_ok()
+    finite = np.isfinite(lse.double().cpu().numpy())
+    assert finite[0, 0].all() and finite[0, 1].sum() == 100
+    want, bound = oc.sink_weights(qf, kf, np.where(finite, lse.double().cpu().numpy(), np.inf), w, s, 0)
+    close(got, want, bound, "weights")
+
+
 @pytest.mark.parametrize("value", [3.4e38, -3.4e38])
 def test_sink_weights_of_the_largest_lse(value):
     """LSE next to the largest number, which rounds to infinity in bf16: its query gives nothing, or infinity."""
